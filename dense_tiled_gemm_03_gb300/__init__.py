@@ -1,6 +1,8 @@
 """GB300-native tiled dense GEMM, C = A x B^T (A [M,K], B [N,K], K-major,
 fp16/bf16 in, fp32 accumulate, fp16/bf16 out), and the attention forward pass
-built on the same pipeline (``flash_attn``).
+built on the same pipeline (``flash_attn``), and a paged key/value cache with
+the attention of new tokens over it (``KVCache``, ``tree_attn``,
+``cache_append``, ``cache_weigh``, ``cache_evict``).
 
 The product is the C-ABI library ``libgemm_tn.so`` (hand-written sm_103a CUDA:
 TMA, mbarrier rings, tcgen05 tensor cores with TMEM accumulators); this
@@ -50,4 +52,12 @@ from ._native import (  # noqa: F401
     mm_tn_fused,
     mm_tn,
     mm_tn_host,
+)
+from ._cache import (  # noqa: F401
+    KVCache,
+    cache_append,
+    cache_evict,
+    cache_weigh,
+    tree_attn,
+    tree_mask,
 )

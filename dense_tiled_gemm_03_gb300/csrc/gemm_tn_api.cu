@@ -1063,6 +1063,70 @@ bool dependent_launch_enabled() {
 
 using namespace gemm_tn_impl;
 
+// ---------------------------------------------------------------- shared with kv_cache_api.cu
+
+namespace gemm_tn_impl {
+
+void api_begin() {
+  t_last_cuda_error = 0;
+  t_last_message[0] = '\0';
+}
+
+int api_fail(int status, const char* what) { return fail(status, what); }
+
+int api_fail_cuda(cudaError_t e, const char* what) { return fail_cuda(e, what); }
+
+cudaError_t api_counted(cudaError_t e) { return counted(e); }
+
+int api_device(int* num_sms) {
+  DeviceFacts* facts = nullptr;
+  const int st = current_device(&facts);
+  if (st == GEMM_TN_OK) *num_sms = facts->num_sms;
+  return st;
+}
+
+// Device memory from the workspace pool of the current device, in stream order.
+cudaError_t api_workspace(size_t bytes, cudaStream_t stream, void** out) {
+  int dev = -1;
+  cudaMemPool_t pool = nullptr;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e == cudaSuccess) e = dev >= 0 && dev < 64 ? workspace_pool(dev, &pool) : cudaErrorInvalidDevice;
+  return e == cudaSuccess ? cudaMallocFromPoolAsync(out, bytes, pool, stream) : e;
+}
+
+// A 4-D 16-bit map (dims innermost first, strides of dims 1 to 3 in elements),
+// moved in boxes of 128-byte rows with the 128-byte swizzle; elements outside
+// the dims read as zero.
+int api_encode_4d(CUtensorMap* map, bool bf16, const void* ptr, const int64_t dims[4], const int64_t strides[3],
+                  const int box[4]) {
+  auto encode = encode_fn();
+  if (encode == nullptr) return fail(GEMM_TN_ERR_CUDA, "cuTensorMapEncodeTiled is unavailable");
+  cuuint64_t d[4], s[3];
+  cuuint32_t b[4];
+  for (int i = 0; i < 4; ++i) {
+    d[i] = static_cast<cuuint64_t>(dims[i]);
+    b[i] = static_cast<cuuint32_t>(box[i]);
+  }
+  for (int i = 0; i < 3; ++i) s[i] = static_cast<cuuint64_t>(strides[i]) * 2;
+  const cuuint32_t elem_strides[4] = {1, 1, 1, 1};
+  const CUresult r = encode(map, bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 4,
+                            const_cast<void*>(ptr), d, s, b, elem_strides, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                            CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  if (r != CUDA_SUCCESS) {
+    char buf[96];
+    std::snprintf(buf, sizeof(buf), "cuTensorMapEncodeTiled failed (CUresult %d)", static_cast<int>(r));
+    return fail(GEMM_TN_ERR_CUDA, buf);
+  }
+  return GEMM_TN_OK;
+}
+
+uint64_t api_watchdog_ns() { return watchdog_ns(); }
+
+int api_drop_load() { return test_drop_load_kb(); }
+
+}  // namespace gemm_tn_impl
+
 extern "C" {
 
 int gemm_tn(int dtype, int64_t m, int64_t n, int64_t k, const void* a, const void* b, void* c,

@@ -1,0 +1,388 @@
+// kv_cache_api.cu -- the C ABI declared in include/kv_cache.h: argument checks,
+// tensor maps over the page pools, workspaces and the launches of
+// sm103_tree_attn.cu, sm103_cache_weigh.cu and kv_cache_ops.cu.
+#include <cuda.h>
+#include <cuda_runtime.h>
+
+#include <algorithm>
+#include <cmath>
+#include <cstdint>
+
+#include "gemm_tn_internal.h"
+#include "kv_cache.h"
+
+namespace gemm_tn_impl {
+
+namespace {
+
+constexpr int64_t kMax31 = (int64_t{1} << 31) - 1;
+constexpr int64_t kMaxStride = int64_t{1} << 39;   // elements: tensor-map strides stay under 2^40 bytes
+
+int invalid(const char* what) { return api_fail(GEMM_TN_ERR_INVALID_VALUE, what); }
+
+bool aligned(const void* p, uintptr_t n) { return reinterpret_cast<uintptr_t>(p) % n == 0; }
+
+int check_common(int dtype, int64_t batch, const kv_cache* c) {
+  if (dtype != GEMM_TN_F16 && dtype != GEMM_TN_BF16) return api_fail(GEMM_TN_ERR_UNSUPPORTED_DTYPE, "dtype");
+  if (c == nullptr) return invalid("cache is NULL");
+  if (batch < 0 || batch > kMax31) return invalid("batch must be in [0, 2^31)");
+  if (c->head_dim != 64 && c->head_dim != 128) return invalid("head_dim must be 64 or 128");
+  if (c->kv_heads < 1 || c->kv_heads > kMax31) return invalid("kv_heads must be in [1, 2^31)");
+  const int64_t ps = c->page_size;
+  if (!(ps == 8 || ps == 16 || ps == 32 || ps == 64 || (ps >= 128 && ps % 128 == 0 && ps <= (1 << 20))))
+    return invalid("page_size must be 8, 16, 32, 64 or a multiple of 128 up to 2^20");
+  if (c->num_pages < 1 || c->num_pages > kMax31 - 1) return invalid("num_pages must be in [1, 2^31 - 1)");
+  if (c->max_pages < 1 || c->max_pages > (kMax31 - 256) / ps) return invalid("max_pages * page_size must be in [1, 2^31 - 256]");
+  if (batch > 1 && c->table_stride < c->max_pages) return invalid("table_stride < max_pages");
+  if (batch > 0 && c->kv_heads > kMax31 / batch) return invalid("batch * kv_heads must be below 2^31");
+  for (const int64_t s : {c->page_stride, c->slot_stride, c->head_stride})
+    if (s < 0 || s >= kMaxStride || s % 8 != 0) return invalid("pool strides must be multiples of 8 elements in [0, 2^39)");
+  if ((c->num_pages > 1 && c->page_stride < c->head_dim) || c->slot_stride < c->head_dim ||
+      (c->kv_heads > 1 && c->head_stride < c->head_dim))
+    return invalid("pool strides must be at least head_dim");
+  if (batch == 0) return GEMM_TN_OK;
+  if (c->k == nullptr || c->v == nullptr || c->page_table == nullptr || c->lens == nullptr)
+    return invalid("the cache's k, v, page_table or lens is NULL");
+  if (!aligned(c->k, 16) || !aligned(c->v, 16)) return api_fail(GEMM_TN_ERR_MISALIGNED, "pool not 16-byte aligned");
+  for (const void* p : {static_cast<const void*>(c->page_table), static_cast<const void*>(c->lens),
+                        static_cast<const void*>(c->weight), static_cast<const void*>(c->pos),
+                        static_cast<const void*>(c->seen)})
+    if (!aligned(p, 4)) return api_fail(GEMM_TN_ERR_MISALIGNED, "cache array not 4-byte aligned");
+  return GEMM_TN_OK;
+}
+
+int check_rows(const kv_rows* r, int64_t batch, int64_t tokens, int64_t heads, int64_t dim) {
+  if (r == nullptr || r->data == nullptr) return invalid("q, k_new or v_new is NULL");
+  if (!aligned(r->data, 16)) return api_fail(GEMM_TN_ERR_MISALIGNED, "q, k_new or v_new not 16-byte aligned");
+  const int64_t strides[3] = {r->batch_stride, r->token_stride, r->head_stride}, sizes[3] = {batch, tokens, heads};
+  for (int i = 0; i < 3; ++i)
+    if (sizes[i] > 1 && (strides[i] < dim || strides[i] >= kMaxStride || strides[i] % 8 != 0))
+      return invalid("strides of q, k_new and v_new must be multiples of 8 elements, at least head_dim and below 2^39");
+  return GEMM_TN_OK;
+}
+
+struct Range {
+  uintptr_t begin, end;
+};
+bool overlap(const Range& a, const Range& b) { return a.begin < b.end && b.begin < a.end; }
+Range pool_range(const void* p, const kv_cache* c) {
+  const uintptr_t b = reinterpret_cast<uintptr_t>(p);
+  return {b, b + 2 * static_cast<uintptr_t>((c->num_pages - 1) * c->page_stride + (c->page_size - 1) * c->slot_stride +
+                                             (c->kv_heads - 1) * c->head_stride + c->head_dim)};
+}
+Range rows_range(const kv_rows* r, int64_t batch, int64_t tokens, int64_t heads, int64_t dim) {
+  const uintptr_t b = reinterpret_cast<uintptr_t>(r->data);
+  return {b, b + 2 * static_cast<uintptr_t>((batch - 1) * (batch > 1 ? r->batch_stride : 0) + (tokens - 1) * (tokens > 1 ? r->token_stride : 0) +
+                                             (heads - 1) * (heads > 1 ? r->head_stride : 0) + dim)};
+}
+
+// {dim, kv heads, page_size, num_pages}; moved in boxes of 64 elements of one
+// head by min(page_size, 128) rows of one page. Page num_pages reads as zeros.
+int encode_pool(CUtensorMap* map, bool bf16, const void* pool, const kv_cache* c) {
+  const int64_t dims[4] = {c->head_dim, c->kv_heads, c->page_size, c->num_pages};
+  const int64_t strides[3] = {c->kv_heads > 1 ? c->head_stride : c->head_dim, c->slot_stride,
+                              c->num_pages > 1 ? c->page_stride : c->head_dim};
+  const int box[4] = {64, 1, static_cast<int>(std::min<int64_t>(c->page_size, 128)), 1};
+  return api_encode_4d(map, bf16, pool, dims, strides, box);
+}
+
+// {dim, heads, tokens, batch}
+int encode_rows(CUtensorMap* map, bool bf16, const kv_rows* r, int64_t batch, int64_t tokens, int64_t heads, int64_t dim,
+                int box_heads, int box_tokens) {
+  const int64_t dims[4] = {dim, heads, tokens, batch};
+  const int64_t strides[3] = {heads > 1 ? r->head_stride : dim, tokens > 1 ? r->token_stride : dim,
+                              batch > 1 ? r->batch_stride : dim};
+  const int box[4] = {64, box_heads, box_tokens, 1};
+  return api_encode_4d(map, bf16, r->data, dims, strides, box);
+}
+
+// log2(e) times the softmax scale
+float scale_log2(float softmax_scale, int64_t dim) {
+  const double scale = softmax_scale > 0.0f ? static_cast<double>(softmax_scale) : 1.0 / std::sqrt(static_cast<double>(dim));
+  return static_cast<float>(scale * 1.4426950408889634);
+}
+
+int check_queries(const kv_cache* c, int64_t batch, int64_t tokens, int64_t heads, float softmax_scale) {
+  if (tokens < 0 || heads < 0 || tokens > kMax31 || heads > kMax31) return invalid("tokens and heads must be in [0, 2^31)");
+  if (heads % c->kv_heads != 0 || heads / c->kv_heads > 128)
+    return invalid("heads must be a multiple of kv_heads, at most 128 times it");
+  if (!(softmax_scale >= 0.0f) || !std::isfinite(softmax_scale))
+    return invalid("softmax_scale must be finite and non-negative");
+  if (batch > 0 && tokens > 0 && heads > 0 &&
+      (tokens > (int64_t{1} << 40) / batch || batch * tokens > (int64_t{1} << 40) / heads))
+    return invalid("batch * tokens * heads must be at most 2^40");
+  return GEMM_TN_OK;
+}
+
+gemm_tn_dev::CacheView view_of(const kv_cache* c, int64_t batch) {
+  gemm_tn_dev::CacheView v{};
+  v.k = static_cast<uint4*>(c->k);
+  v.v = static_cast<uint4*>(c->v);
+  v.page_stride = c->page_stride / 8;
+  v.slot_stride = c->slot_stride / 8;
+  v.head_stride = c->head_stride / 8;
+  v.page_table = c->page_table;
+  v.table_stride = c->table_stride;
+  v.batch = static_cast<int>(batch);
+  v.kv_heads = static_cast<int>(c->kv_heads);
+  v.vec = static_cast<int>(c->head_dim / 8);
+  v.page_size = static_cast<int>(c->page_size);
+  v.num_pages = static_cast<int>(c->num_pages);
+  v.capacity = static_cast<int>(c->max_pages * c->page_size);
+  return v;
+}
+
+// Least key tiles per CTA of the attention and of the weights.
+constexpr int kMinChunk = 2;
+
+}  // namespace
+
+}  // namespace gemm_tn_impl
+
+using namespace gemm_tn_impl;
+
+extern "C" {
+
+int tree_attn_fwd(int dtype, int64_t batch, int64_t tokens, int64_t heads, const kv_cache* cache, const kv_rows* q,
+                  const kv_rows* k_new, const kv_rows* v_new, const uint64_t* mask, const int32_t* token_lens, void* o,
+                  float* lse, float softmax_scale, int* d_status, gemm_tn_stream_t stream) {
+  api_begin();
+  int st = check_common(dtype, batch, cache);
+  if (st == GEMM_TN_OK) st = check_queries(cache, batch, tokens, heads, softmax_scale);
+  if (st != GEMM_TN_OK) return st;
+  if (batch == 0 || tokens == 0 || heads == 0) return GEMM_TN_OK;
+  const int64_t dim = cache->head_dim, kv_heads = cache->kv_heads;
+  if ((st = check_rows(q, batch, tokens, heads, dim)) != GEMM_TN_OK) return st;
+  if ((k_new == nullptr) != (v_new == nullptr)) return invalid("k_new and v_new come together");
+  const bool has_new = k_new != nullptr;
+  if (!has_new && mask != nullptr) return invalid("a mask needs k_new and v_new");
+  if (has_new) {
+    if ((st = check_rows(k_new, batch, tokens, kv_heads, dim)) != GEMM_TN_OK) return st;
+    if ((st = check_rows(v_new, batch, tokens, kv_heads, dim)) != GEMM_TN_OK) return st;
+  }
+  if (o == nullptr) return invalid("o is NULL");
+  if (!aligned(o, 16) || !aligned(lse, 4) || !aligned(mask, 8) || !aligned(token_lens, 4))
+    return api_fail(GEMM_TN_ERR_MISALIGNED, "o, lse, mask or token_lens is not aligned to its element (o: 16 bytes)");
+  const Range out = {reinterpret_cast<uintptr_t>(o), reinterpret_cast<uintptr_t>(o) + 2 * static_cast<uintptr_t>(batch * tokens * heads * dim)};
+  if (overlap(out, rows_range(q, batch, tokens, heads, dim)) || overlap(out, pool_range(cache->k, cache)) ||
+      overlap(out, pool_range(cache->v, cache)) ||
+      (has_new && (overlap(out, rows_range(k_new, batch, tokens, kv_heads, dim)) ||
+                   overlap(out, rows_range(v_new, batch, tokens, kv_heads, dim)))))
+    return invalid("o overlaps an input or the cache");
+  int sms = 0;
+  if ((st = api_device(&sms)) != GEMM_TN_OK) return st;
+
+  const bool bf16 = dtype == GEMM_TN_BF16;
+  alignas(64) gemm_tn_dev::TreeArgs args{};
+  args.group = static_cast<int>(heads / kv_heads);
+  args.tile_tokens = tree_attn_tile_rows() / args.group;
+  const int64_t row_tiles = (tokens + args.tile_tokens - 1) / args.tile_tokens;
+  args.units = row_tiles > 1 ? 2 : 1;
+  args.row_units = static_cast<int>((row_tiles + args.units - 1) / args.units);
+  if ((st = encode_rows(&args.tmap_q, bf16, q, batch, tokens, heads, dim, args.group, args.tile_tokens)) != GEMM_TN_OK ||
+      (st = encode_pool(&args.tmap_k, bf16, cache->k, cache)) != GEMM_TN_OK ||
+      (st = encode_pool(&args.tmap_v, bf16, cache->v, cache)) != GEMM_TN_OK)
+    return st;
+  if (has_new && ((st = encode_rows(&args.tmap_k_new, bf16, k_new, batch, tokens, kv_heads, dim, 1, 128)) != GEMM_TN_OK ||
+                  (st = encode_rows(&args.tmap_v_new, bf16, v_new, batch, tokens, kv_heads, dim, 1, 128)) != GEMM_TN_OK))
+    return st;
+  args.o = o;
+  args.lse = lse;
+  args.mask = mask;
+  args.lens = cache->lens;
+  args.token_lens = token_lens;
+  args.page_table = cache->page_table;
+  args.table_stride = cache->table_stride;
+  args.batch = static_cast<int>(batch);
+  args.tokens = static_cast<int>(tokens);
+  args.heads = static_cast<int>(heads);
+  args.kv_heads = static_cast<int>(kv_heads);
+  args.page_size = static_cast<int>(cache->page_size);
+  args.num_pages = static_cast<int>(cache->num_pages);
+  args.capacity = static_cast<int>(cache->max_pages * cache->page_size);
+  args.mask_words = static_cast<int>((tokens + 63) / 64);
+  args.has_new = has_new ? 1 : 0;
+  args.chunks = sms;
+  args.min_chunk = kMinChunk;
+  args.scale_log2 = scale_log2(softmax_scale, dim);
+  args.status = d_status;
+  args.timeout_ns = api_watchdog_ns();
+  args.drop_load_block = api_drop_load();
+
+  const size_t part_rows = static_cast<size_t>(2 * args.chunks) * static_cast<size_t>(args.units * tree_attn_tile_rows());
+  void* workspace = nullptr;
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  cudaError_t e = api_workspace(part_rows * static_cast<size_t>(dim * 4 + 8), s, &workspace);
+  if (e != cudaSuccess) return api_fail_cuda(e, "workspace");
+  args.part_o = static_cast<float*>(workspace);
+  args.part_ml = reinterpret_cast<float2*>(args.part_o + part_rows * static_cast<size_t>(dim));
+  e = api_counted(launch_tree_attn(static_cast<int>(dim), bf16, args, s));
+  if (e == cudaSuccess && args.chunks > 1) e = api_counted(launch_tree_attn_join(static_cast<int>(dim), bf16, args, s));
+  const cudaError_t freed = cudaFreeAsync(workspace, s);
+  if (e != cudaSuccess) return api_fail_cuda(e, "tree attention launch");
+  return freed == cudaSuccess ? GEMM_TN_OK : api_fail_cuda(freed, "cudaFreeAsync (workspace)");
+}
+
+int kv_cache_append(int dtype, int64_t batch, int64_t tokens, const kv_cache* cache, const kv_rows* k_new,
+                    const kv_rows* v_new, const int32_t* rows, const int32_t* counts, int64_t max_rows, int32_t* lens_out,
+                    int32_t* seen_out, int* d_status, gemm_tn_stream_t stream) {
+  api_begin();
+  int st = check_common(dtype, batch, cache);
+  if (st != GEMM_TN_OK) return st;
+  if (tokens < 0 || tokens > kMax31 || max_rows < 0 || max_rows > kMax31) return invalid("tokens and max_rows must be in [0, 2^31)");
+  if (rows == nullptr && max_rows > tokens) return invalid("max_rows > tokens without rows");
+  if (batch == 0) return GEMM_TN_OK;
+  if (lens_out == nullptr) return invalid("lens_out is NULL");
+  if ((seen_out != nullptr) && cache->seen == nullptr) return invalid("seen_out without seen");
+  if (!aligned(rows, 4) || !aligned(counts, 4) || !aligned(lens_out, 4) || !aligned(seen_out, 4))
+    return api_fail(GEMM_TN_ERR_MISALIGNED, "rows, counts, lens_out or seen_out not 4-byte aligned");
+  if (max_rows > 0 && tokens > 0) {
+    if ((st = check_rows(k_new, batch, tokens, cache->kv_heads, cache->head_dim)) != GEMM_TN_OK) return st;
+    if ((st = check_rows(v_new, batch, tokens, cache->kv_heads, cache->head_dim)) != GEMM_TN_OK) return st;
+    for (const kv_rows* r : {k_new, v_new})
+      for (const void* p : {cache->k, cache->v})
+        if (overlap(rows_range(r, batch, tokens, cache->kv_heads, cache->head_dim), pool_range(p, cache)))
+          return invalid("k_new or v_new overlaps the cache");
+    if (max_rows > (int64_t{1} << 36) / (batch * cache->kv_heads)) return invalid("batch * max_rows * kv_heads must be at most 2^36");
+  } else if (max_rows > 0) {
+    return invalid("max_rows > 0 without tokens");
+  }
+  int sms = 0;
+  if ((st = api_device(&sms)) != GEMM_TN_OK) return st;
+  gemm_tn_dev::AppendArgs args{};
+  args.c = view_of(cache, batch);
+  if (max_rows > 0) {
+    args.k_new = static_cast<const uint4*>(k_new->data);
+    args.v_new = static_cast<const uint4*>(v_new->data);
+    args.kn_batch = k_new->batch_stride / 8;
+    args.kn_token = k_new->token_stride / 8;
+    args.kn_head = k_new->head_stride / 8;
+    args.vn_batch = v_new->batch_stride / 8;
+    args.vn_token = v_new->token_stride / 8;
+    args.vn_head = v_new->head_stride / 8;
+  }
+  args.rows = rows;
+  args.counts = counts;
+  args.lens = cache->lens;
+  args.seen = cache->seen;
+  args.lens_out = lens_out;
+  args.seen_out = seen_out;
+  args.weight = cache->weight;
+  args.pos = cache->pos;
+  args.tokens = static_cast<int>(tokens);
+  args.max_rows = static_cast<int>(max_rows);
+  args.status = d_status;
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  const bool in_place = lens_out == cache->lens || (seen_out != nullptr && seen_out == cache->seen);
+  cudaError_t e = cudaSuccess;
+  if (max_rows > 0) e = api_counted(launch_cache_append(args, s));
+  if (e == cudaSuccess && (in_place || max_rows == 0)) e = api_counted(launch_cache_advance(args, s));
+  return e == cudaSuccess ? GEMM_TN_OK : api_fail_cuda(e, "cache append launch");
+}
+
+int kv_cache_weigh(int dtype, int64_t batch, int64_t tokens, int64_t heads, const kv_cache* cache, const kv_rows* q,
+                   const float* lse, const int32_t* rows, const int32_t* counts, int64_t max_rows, int causal,
+                   float softmax_scale, float* weight_out, int* d_status, gemm_tn_stream_t stream) {
+  api_begin();
+  int st = check_common(dtype, batch, cache);
+  if (st == GEMM_TN_OK) st = check_queries(cache, batch, tokens, heads, softmax_scale);
+  if (st != GEMM_TN_OK) return st;
+  if (max_rows < 0 || max_rows > kMax31 / 256) return invalid("max_rows must be in [0, 2^23)");
+  if (rows == nullptr && max_rows > tokens) return invalid("max_rows > tokens without rows");
+  if (batch == 0) return GEMM_TN_OK;
+  if (heads == 0) return invalid("heads must be positive");
+  if (cache->weight == nullptr || weight_out == nullptr) return invalid("weight or weight_out is NULL");
+  if (max_rows > 0) {
+    if (tokens == 0) return invalid("max_rows > 0 without tokens");
+    if ((st = check_rows(q, batch, tokens, heads, cache->head_dim)) != GEMM_TN_OK) return st;
+    if (lse == nullptr) return invalid("lse is NULL");
+  }
+  if (!aligned(rows, 4) || !aligned(counts, 4) || !aligned(lse, 4) || !aligned(weight_out, 4))
+    return api_fail(GEMM_TN_ERR_MISALIGNED, "rows, counts, lse or weight_out not 4-byte aligned");
+  int sms = 0;
+  if ((st = api_device(&sms)) != GEMM_TN_OK) return st;
+  const bool bf16 = dtype == GEMM_TN_BF16;
+  alignas(64) gemm_tn_dev::WeighArgs args{};
+  if ((st = encode_pool(&args.tmap_k, bf16, cache->k, cache)) != GEMM_TN_OK) return st;
+  if (max_rows > 0) {
+    args.q = q->data;
+    args.q_batch = q->batch_stride;
+    args.q_token = q->token_stride;
+    args.q_head = q->head_stride;
+  }
+  args.lse = lse;
+  args.rows = rows;
+  args.counts = counts;
+  args.lens = cache->lens;
+  args.page_table = cache->page_table;
+  args.weight = cache->weight;
+  args.weight_out = weight_out;
+  args.table_stride = cache->table_stride;
+  args.batch = static_cast<int>(batch);
+  args.tokens = static_cast<int>(tokens);
+  args.heads = static_cast<int>(heads);
+  args.kv_heads = static_cast<int>(cache->kv_heads);
+  args.group = static_cast<int>(heads / cache->kv_heads);
+  args.max_rows = static_cast<int>(max_rows);
+  args.page_size = static_cast<int>(cache->page_size);
+  args.num_pages = static_cast<int>(cache->num_pages);
+  args.capacity = static_cast<int>(cache->max_pages * cache->page_size);
+  args.block_tokens = 256 / args.group;
+  args.chunks = sms;
+  args.min_chunk = 1;
+  args.causal = causal != 0 ? 1 : 0;
+  args.scale_log2 = scale_log2(softmax_scale, cache->head_dim);
+  args.status = d_status;
+  args.timeout_ns = api_watchdog_ns();
+  args.drop_load_block = api_drop_load();
+  const cudaError_t e = api_counted(
+      launch_cache_weigh(static_cast<int>(cache->head_dim), bf16, args, reinterpret_cast<cudaStream_t>(stream)));
+  return e == cudaSuccess ? GEMM_TN_OK : api_fail_cuda(e, "cache weigh launch");
+}
+
+int kv_cache_evict(int dtype, int64_t batch, const kv_cache* cache, int64_t keep, int64_t recent, float* weight_out,
+                   int32_t* pos_out, int32_t* lens_out, int* d_status, gemm_tn_stream_t stream) {
+  api_begin();
+  int st = check_common(dtype, batch, cache);
+  if (st != GEMM_TN_OK) return st;
+  if (keep < 0 || keep > kMax31) return invalid("keep must be in [0, 2^31)");
+  if (recent < 0 || recent > keep) return invalid("recent must be in [0, keep]");
+  if (batch == 0) return GEMM_TN_OK;
+  if (cache->weight == nullptr || weight_out == nullptr || lens_out == nullptr)
+    return invalid("weight, weight_out or lens_out is NULL");
+  if (recent > 0 && (cache->pos == nullptr || cache->seen == nullptr)) return invalid("recent > 0 needs pos and seen");
+  if ((pos_out == nullptr) != (cache->pos == nullptr)) return invalid("pos_out goes with the cache's pos");
+  if (!aligned(weight_out, 4) || !aligned(pos_out, 4) || !aligned(lens_out, 4))
+    return api_fail(GEMM_TN_ERR_MISALIGNED, "weight_out, pos_out or lens_out not 4-byte aligned");
+  int sms = 0;
+  if ((st = api_device(&sms)) != GEMM_TN_OK) return st;
+  gemm_tn_dev::EvictArgs args{};
+  args.c = view_of(cache, batch);
+  args.weight = cache->weight;
+  args.weight_out = weight_out;
+  args.pos = cache->pos;
+  args.pos_out = pos_out;
+  args.seen = cache->seen;
+  args.lens = cache->lens;
+  args.lens_out = lens_out;
+  args.keep = static_cast<int>(keep);
+  args.recent = static_cast<int>(recent);
+  args.max_moves = static_cast<int>(std::max<int64_t>(0, std::min<int64_t>(keep, args.c.capacity - keep)));
+  args.smem_keys = evict_smem_keys(args.c.capacity);
+  args.status = d_status;
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  const size_t lists = static_cast<size_t>(batch * cache->kv_heads);
+  const size_t count_bytes = (lists * 4 + 15) / 16 * 16;
+  void* workspace = nullptr;
+  cudaError_t e = api_workspace(count_bytes + lists * static_cast<size_t>(args.max_moves) * 8, s, &workspace);
+  if (e != cudaSuccess) return api_fail_cuda(e, "workspace");
+  args.counts = static_cast<int32_t*>(workspace);
+  args.moves = reinterpret_cast<int2*>(static_cast<uint8_t*>(workspace) + count_bytes);
+  e = api_counted(launch_cache_select(args, s));
+  if (e == cudaSuccess) e = api_counted(launch_cache_move(args, sms, s));
+  const cudaError_t freed = cudaFreeAsync(workspace, s);
+  if (e != cudaSuccess) return api_fail_cuda(e, "cache evict launch");
+  return freed == cudaSuccess ? GEMM_TN_OK : api_fail_cuda(freed, "cudaFreeAsync (workspace)");
+}
+
+}  // extern "C"

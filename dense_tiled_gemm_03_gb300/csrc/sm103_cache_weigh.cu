@@ -1,0 +1,419 @@
+// sm103_cache_weigh.cu -- accumulated attention weight of cached keys
+// (include/kv_cache.h: kv_cache_weigh):
+//
+//   weight_out[b][h][s] = weight[b][h][s]
+//       + sum over counted tokens i and the query heads x of KV head h of
+//         exp(scale * q_(i,x) . k_s - lse_(i,x)),     s seen by i
+//
+// The transposed product S^T = K Q^T puts a key on each TMEM lane and the query
+// rows on its columns: a thread owns one key, sums its columns in registers and
+// is the only one that writes the key's weight. No maximum is needed (lse is
+// given), no reduction crosses threads, no atomics are used, and what lies
+// behind the last key stays on its own lanes.
+//
+// Keys are read once (dim * 2 bytes each) per 256 query rows against one
+// exponential per key and row: up to about 150 rows HBM bounds the kernel,
+// past that the exponentials do.
+//
+// Work: an item is (sequence, KV head); the items' 128-key tiles are cut into
+// equal contiguous chunks, one per CTA (sm103_cache.cuh). Per segment of an
+// item the query rows come in blocks of at most 256, each block walking the
+// segment's tiles.
+//   warp 0      TMA producer (lane l copies the tile's l-th page)
+//   warp 1      MMA issuer: S^T (128 x rows) into one of two TMEM buffers
+//   warps 2-9   two groups of four taking every other tile; all eight gather
+//               the block's query rows into shared memory first
+#include <cuda.h>
+#include <cuda_runtime.h>
+
+#include <atomic>
+#include <cstdint>
+
+#include "gemm_tn_internal.h"
+#include "sm103_cache.cuh"
+
+namespace gemm_tn_dev {
+
+namespace cw {
+
+using cache::kTileKeys;
+constexpr int kProducerWarp = 0;
+constexpr int kMmaWarp = 1;
+constexpr int kFirstSumWarp = 2;
+constexpr int kSumWarps = 8;
+constexpr int kMaxRows = 256;      // query rows per block (columns of one TMEM buffer)
+constexpr float kLog2e = 1.4426950408889634f;
+
+template <int kDim_, bool kBf16_>
+struct Cfg {
+  static constexpr int kDim = kDim_;
+  static constexpr bool kBf16 = kBf16_;
+  static constexpr int kNumThreads = 64 + 32 * kSumWarps;
+  static constexpr int kDimBoxes = kDim / 64;
+  static constexpr uint32_t kBoxBytes = 128u * 128u;        // 128 keys x 128 bytes
+  static constexpr uint32_t kTileBytes = kDimBoxes * kBoxBytes;
+  static constexpr uint32_t kQBoxBytes = kMaxRows * 128u;   // 256 query rows x 128 bytes
+  static constexpr int kStages = kDim == 64 ? 8 : 4;
+  static constexpr uint32_t kOffQ = 0;
+  static constexpr uint32_t kOffK = kOffQ + kDimBoxes * kQBoxBytes;
+  static constexpr uint32_t kOffLse = kOffK + kStages * kTileBytes;   // per row (-log2e lse rounded, 2^ what that left)
+  // q_full, q_free, k_full[S], k_empty[S], s_full[2], s_empty[2], drain
+  static constexpr int kNumBars = 2 + 2 * kStages + 4 + 1;
+  static constexpr uint32_t kOffBar = kOffLse + 8u * kMaxRows;
+  static constexpr uint32_t kOffTmemSlot = kOffBar + 8u * kNumBars;
+  static constexpr uint32_t kOffAbort = kOffTmemSlot + 4u;
+  static constexpr uint32_t kOffStart = (kOffAbort + 4u + 7u) / 8u * 8u;
+  static constexpr uint32_t kRaw = kOffStart + 24u + 1024u;
+  static constexpr uint32_t kSmemBytes = kRaw;
+  static constexpr uint32_t kTmemCols = 512;
+  static constexpr uint32_t kIdesc = mma_idesc_f16(kBf16, kTileKeys, 0, false);   // N is set per block
+  static_assert(kSmemBytes <= 227u * 1024u, "shared memory budget");
+  static_assert(kOffBar % 8u == 0 && kOffStart % 8u == 0, "64-bit shared words");
+};
+
+__device__ __forceinline__ int cached_len(const WeighArgs& a, int b) {
+  return min(max(__ldg(a.lens + b), 0), a.capacity);
+}
+__device__ __forceinline__ int row_count(const WeighArgs& a, int b) {
+  return a.counts == nullptr ? a.max_rows : min(max(__ldg(a.counts + b), 0), a.max_rows);
+}
+
+// Walks a chunk: runs of one (sequence, KV head)'s key tiles.
+struct Walk {
+  int b, h, j0, len, n, tiles, count;
+  int64_t left;
+
+  __device__ __forceinline__ void load(const WeighArgs& a) {
+    len = cached_len(a, b);
+    n = row_count(a, b);
+    tiles = (len + kTileKeys - 1) / kTileKeys;
+  }
+  __device__ __forceinline__ void start(const WeighArgs& a, int b_, int64_t off, int64_t left_) {
+    b = b_;
+    left = left_;
+    if (left <= 0) return;
+    load(a);
+    h = static_cast<int>(off / tiles);
+    j0 = static_cast<int>(off - static_cast<int64_t>(tiles) * h);
+    count = static_cast<int>(min(static_cast<int64_t>(tiles - j0), left));
+  }
+  __device__ __forceinline__ bool more() const { return left > 0; }
+  __device__ __forceinline__ void next(const WeighArgs& a) {
+    left -= count;
+    if (left <= 0) return;
+    j0 = 0;
+    if (++h == a.kv_heads) {
+      h = 0;
+      do {
+        ++b;
+        load(a);
+      } while (tiles == 0);
+    }
+    count = static_cast<int>(min(static_cast<int64_t>(tiles), left));
+  }
+  // blocks of query rows; one empty block where no token counts (the weights are still copied)
+  __device__ __forceinline__ int blocks(const WeighArgs& a) const {
+    return max(1, (n + a.block_tokens - 1) / a.block_tokens);
+  }
+  __device__ __forceinline__ int block_rows(const WeighArgs& a, int block) const {
+    return max(0, min(a.block_tokens, n - block * a.block_tokens)) * a.group;
+  }
+};
+
+}  // namespace cw
+
+template <class C>
+__global__ void __launch_bounds__(C::kNumThreads, 1) cache_weigh_kernel(const __grid_constant__ WeighArgs args) {
+  extern __shared__ uint8_t smem_raw[];
+  const uint32_t raw_addr = smem_addr(smem_raw);
+  uint8_t* smem = smem_raw + (((raw_addr + 1023u) & ~1023u) - raw_addr);
+  const uint32_t base = smem_addr(smem);
+  const uint32_t warp = threadIdx.x >> 5;
+  const uint32_t lane = lane_id();
+
+  auto k_tile = [&](int s) { return base + C::kOffK + s * C::kTileBytes; };
+  auto bar = [&](int i) { return base + C::kOffBar + 8u * i; };
+  const uint32_t q_full = bar(0), q_free = bar(1);
+  auto k_full = [&](int s) { return bar(2 + s); };
+  auto k_empty = [&](int s) { return bar(2 + C::kStages + s); };
+  auto s_full = [&](int g) { return bar(2 + 2 * C::kStages + g); };
+  auto s_empty = [&](int g) { return bar(4 + 2 * C::kStages + g); };
+  const uint32_t drain_bar = bar(6 + 2 * C::kStages);
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + C::kOffTmemSlot);
+  volatile uint32_t* abort_flag = reinterpret_cast<volatile uint32_t*>(smem + C::kOffAbort);
+  int64_t* start_slot = reinterpret_cast<int64_t*>(smem + C::kOffStart);
+  float2* row_lse = reinterpret_cast<float2*>(smem + C::kOffLse);
+
+  if (threadIdx.x == 0) {
+    mbar_init(q_full, cw::kSumWarps);
+    mbar_init(q_free, cw::kSumWarps);
+    for (int s = 0; s < C::kStages; ++s) {
+      mbar_init(k_full(s), 1);
+      mbar_init(k_empty(s), 1);
+    }
+    for (int g = 0; g < 2; ++g) {
+      mbar_init(s_full(g), 1);
+      mbar_init(s_empty(g), 4);
+    }
+    mbar_init(drain_bar, 1);
+    *abort_flag = 0u;
+    fence_barrier_init();
+  }
+  if (warp == cw::kProducerWarp && lane == 0) tma_prefetch_descriptor(&args.tmap_k);
+  if (warp == cw::kMmaWarp) {
+    tmem_alloc<1>(smem_addr(tmem_slot), C::kTmemCols);
+    tmem_relinquish<1>();
+  }
+  griddep_wait();
+  griddep_launch_dependents();
+  if (warp == cw::kProducerWarp) {
+    const cache::Start st =
+        cache::find_start(args.batch, args.chunks, args.min_chunk, static_cast<int>(blockIdx.x), lane, [&](int b) {
+          return static_cast<int64_t>((cw::cached_len(args, b) + cw::kTileKeys - 1) / cw::kTileKeys) * args.kv_heads;
+        });
+    if (lane == 0) {
+      start_slot[0] = st.b;
+      start_slot[1] = st.off;
+      start_slot[2] = min(st.chunk_tiles, st.total - st.chunk_tiles * static_cast<int64_t>(blockIdx.x));
+    }
+  }
+  tc_fence_before_sync();
+  __syncthreads();
+  tc_fence_after_sync();
+  const uint32_t tmem_base = *tmem_slot;
+  const cache::Watch wd{args.status, args.timeout_ns, abort_flag};
+  cw::Walk w;
+  w.start(args, static_cast<int>(start_slot[0]), start_slot[1], start_slot[2]);
+
+  if (warp == cw::kProducerWarp) {
+    // -------------------------------------------------------------- TMA producer
+    int issued[C::kStages];
+    for (int s = 0; s < C::kStages; ++s) issued[s] = -1;
+    const int box_rows = min(args.page_size, cw::kTileKeys);
+    const int tile_pages = cw::kTileKeys / box_rows;
+    int it = 0;
+    bool ok = true;
+    for (; ok && w.more(); w.next(args)) {
+      const int32_t* table = args.page_table + static_cast<int64_t>(w.b) * args.table_stride;
+      auto page_of = [&](int j) {   // the page that this lane copies of tile j
+        const int first = j * cw::kTileKeys + static_cast<int>(lane) * box_rows;
+        if (static_cast<int>(lane) >= tile_pages || first >= w.len) return 0;
+        int page = __ldg(table + first / args.page_size);
+        if (page < 0 || page >= args.num_pages) {   // not a page: the copy fills zeros, the caller is told
+          cache::report(args.status, cache::kStatusInvalid);
+          page = args.num_pages;
+        }
+        return page;
+      };
+      const int blocks = w.blocks(args);
+      for (int block = 0; ok && block < blocks; ++block) {
+        int page = page_of(w.j0);
+        for (int j = w.j0; j < w.j0 + w.count; ++j, ++it) {
+          const int valid = min(cw::kTileKeys, w.len - j * cw::kTileKeys);
+          const int boxes = (valid + box_rows - 1) / box_rows;
+          const int slot0 = tile_pages == 1 ? (j * cw::kTileKeys) % args.page_size : 0;
+          const int next_page = j + 1 < w.j0 + w.count ? page_of(j + 1) : 0;
+          const int s = it % C::kStages;
+          const uint32_t ph = static_cast<uint32_t>(it / C::kStages) & 1u;
+          if (!(ok = wd.warp_wait(k_empty(s), ph ^ 1u))) break;
+          if (lane == 0) mbar_arrive_expect_tx(k_full(s), static_cast<uint32_t>(boxes * box_rows) * 128u * C::kDimBoxes);
+          __syncwarp();
+          if (static_cast<int>(lane) < boxes && !(blockIdx.x == 0 && it == args.drop_load_block)) {
+            for (int c = 0; c < C::kDimBoxes; ++c)
+              tma_load_4d(&args.tmap_k, k_tile(s) + c * C::kBoxBytes + lane * box_rows * 128u, k_full(s), 64 * c, w.h,
+                          slot0, page);
+          }
+          issued[s] = static_cast<int>(ph);
+          page = next_page;
+        }
+      }
+    }
+    // wait (bounded) for every copy issued before the CTA may exit
+    for (int s = 0; s < C::kStages; ++s)
+      if (issued[s] >= 0) wd.drain(k_full(s), static_cast<uint32_t>(issued[s]));
+  } else if (warp == cw::kMmaWarp) {
+    if (lane == 0) {
+      // ------------------------------------------------------------ MMA issuer
+      int it = 0;       // tiles issued
+      int q_blocks = 0;
+      bool ok = true;
+      for (; ok && w.more(); w.next(args)) {
+        const int blocks = w.blocks(args);
+        for (int block = 0; ok && block < blocks; ++block, ++q_blocks) {
+          const int rows = w.block_rows(args, block);
+          const uint32_t n = static_cast<uint32_t>(max(1, (rows + 31) / 32)) * 32u;
+          const uint32_t idesc = C::kIdesc | ((n >> 3) << 17);
+          if (!(ok = wd.wait(q_full, static_cast<uint32_t>(q_blocks) & 1u))) break;
+          for (int j = 0; j < w.count; ++j, ++it) {
+            const int s = it % C::kStages, g = it & 1;
+            if (!(ok = wd.wait(s_empty(g), (static_cast<uint32_t>(it >> 1) & 1u) ^ 1u))) break;
+            if (!(ok = wd.wait(k_full(s), static_cast<uint32_t>(it / C::kStages) & 1u))) break;
+            tc_fence_after_sync();
+#pragma unroll
+            for (int c = 0; c < C::kDimBoxes; ++c) {
+              const uint64_t a_desc = sw128_kmajor_desc(k_tile(s) + c * C::kBoxBytes);
+              const uint64_t b_desc = sw128_kmajor_desc(base + C::kOffQ + c * C::kQBoxBytes);
+#pragma unroll
+              for (int kk = 0; kk < 4; ++kk)
+                mma_f16<1>(tmem_base + 256u * static_cast<uint32_t>(g), a_desc + 2u * kk, b_desc + 2u * kk, idesc,
+                           (c | kk) != 0 ? 1u : 0u);
+            }
+            mma_commit(s_full(g));
+            mma_commit(k_empty(s));
+          }
+        }
+      }
+      // every MMA issued here must finish before TMEM is freed
+      mma_commit(drain_bar);
+      wd.drain(drain_bar, 0);
+    }
+  } else {
+    // -------------------------------------------------------------- sums
+    const int g = (static_cast<int>(warp) - cw::kFirstSumWarp) >> 2;   // group: tiles it & 1 == g
+    const uint32_t quarter = warp & 3u;
+    const int key_lane = static_cast<int>(quarter * 32u + lane);
+    const uint32_t t_s = tmem_base + ((quarter * 32u) << 16) + 256u * static_cast<uint32_t>(g);
+    const float c_log2 = args.scale_log2;
+    const int sum_thread = static_cast<int>(threadIdx.x) - 64;
+    int it = 0, q_blocks = 0;
+    bool ok = true;
+    for (; ok && w.more(); w.next(args)) {
+      const int blocks = w.blocks(args);
+      const int64_t weight_row = (static_cast<int64_t>(w.b) * args.kv_heads + w.h) * args.capacity;
+      for (int block = 0; ok && block < blocks; ++block, ++q_blocks) {
+        const int rows = w.block_rows(args, block);
+        const int cols = max(1, (rows + 31) / 32) * 32;
+        const int first_row = block * args.block_tokens;   // of the counted tokens
+        // every sum warp is done with the block before: between them they have
+        // seen all its products complete, read its row_lse and written its weights
+        if (!(ok = wd.warp_wait(q_free, (static_cast<uint32_t>(q_blocks) & 1u) ^ 1u))) break;
+        // query rows -> shared memory, K-major with the 128-byte swizzle
+        constexpr int kPieces = C::kDim / 8;   // 16-byte pieces per row
+        for (int x = sum_thread; x < cols * kPieces; x += 32 * cw::kSumWarps) {
+          const int row = x / kPieces, piece = x % kPieces;
+          uint4 v = make_uint4(0u, 0u, 0u, 0u);
+          float lse = INFINITY;   // rows that do not count weigh nothing
+          if (row < rows) {
+            const int i = row / args.group, head = w.h * args.group + row - i * args.group;
+            int token = first_row + i;
+            if (args.rows != nullptr) token = __ldg(args.rows + static_cast<int64_t>(w.b) * args.max_rows + token);
+            if (token >= 0 && token < args.tokens) {
+              v = __ldg(reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(args.q) + w.b * args.q_batch +
+                                                       token * args.q_token + head * args.q_head) + piece);
+              if (piece == 0) lse = __ldg(args.lse + (static_cast<int64_t>(w.b) * args.tokens + token) * args.heads + head);
+              if (lse == -INFINITY) lse = INFINITY;
+            } else {
+              cache::report(args.status, cache::kStatusInvalid);
+            }
+          }
+          const int box = piece / 8;
+          st_shared_v4(base + C::kOffQ + box * C::kQBoxBytes + row * 128u + (((piece & 7) ^ (row & 7)) * 16u), v.x, v.y, v.z, v.w);
+          if (piece == 0) {
+            // lse * log2e as a rounded part and the factor that makes up for the rounding
+            const float hi = lse * cw::kLog2e;
+            const float lo = fmaf(lse, cw::kLog2e, -hi);
+            row_lse[row] = isinf(hi) ? make_float2(-INFINITY, 0.0f) : make_float2(-hi, ex2_approx(-lo));
+          }
+        }
+        fence_proxy_async_shared();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(q_full);
+        if (!(ok = wd.warp_wait(q_full, static_cast<uint32_t>(q_blocks) & 1u))) break;
+        for (int j = w.j0; ok && j < w.j0 + w.count; ++j, ++it) {
+          if ((it & 1) != g) continue;
+          const int key = j * cw::kTileKeys + key_lane;
+          const bool live = key < w.len;
+          float acc = 0.0f;
+          if (live) acc = block == 0 ? args.weight[weight_row + key] : args.weight_out[weight_row + key];
+          if (!(ok = wd.warp_wait(s_full(g), static_cast<uint32_t>(it >> 1) & 1u))) break;
+          tc_fence_after_sync();
+          // causal: counted token i is the key's own query or a later one from i = key - (len - n) on
+          const int low = args.causal ? (key - (w.len - w.n) - first_row) * args.group : 0;   // first column that sees the key
+          const bool masked = __any_sync(0xffffffffu, live && low > 0);
+          float sum0 = 0.0f, sum1 = 0.0f;
+          for (int c0 = 0; c0 < cols; c0 += 32) {
+            uint32_t raw[32];
+            tmem_load_32x32(t_s + static_cast<uint32_t>(c0), raw);
+            tmem_load_wait();
+            const float4* lse4 = reinterpret_cast<const float4*>(row_lse + c0);
+            if (!masked) {
+#pragma unroll
+              for (int e = 0; e < 32; e += 2) {
+                const float4 x = lse4[e / 2];
+                sum0 = fmaf(ex2_approx(fmaf(__uint_as_float(raw[e]), c_log2, x.x)), x.y, sum0);
+                sum1 = fmaf(ex2_approx(fmaf(__uint_as_float(raw[e + 1]), c_log2, x.z)), x.w, sum1);
+              }
+            } else {
+#pragma unroll
+              for (int e = 0; e < 32; e += 2) {
+                const float4 x = lse4[e / 2];
+                const float p0 = ex2_approx(fmaf(__uint_as_float(raw[e]), c_log2, x.x)) * x.y;
+                const float p1 = ex2_approx(fmaf(__uint_as_float(raw[e + 1]), c_log2, x.z)) * x.w;
+                if (c0 + e >= low) sum0 += p0;
+                if (c0 + e + 1 >= low) sum1 += p1;
+              }
+            }
+          }
+          tc_fence_before_sync();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(s_empty(g));
+          if (live) args.weight_out[weight_row + key] = acc + (sum0 + sum1);
+        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(q_free);
+      }
+    }
+  }
+
+  tc_fence_before_sync();
+  __syncthreads();
+  if (warp == cw::kMmaWarp) {
+    tc_fence_after_sync();
+    tmem_dealloc<1>(tmem_base, C::kTmemCols);
+  }
+}
+
+}  // namespace gemm_tn_dev
+
+namespace gemm_tn_impl {
+
+namespace {
+
+template <class C>
+cudaError_t launch_cfg(const gemm_tn_dev::WeighArgs& args, cudaStream_t stream) {
+  static std::atomic<uint64_t> done_mask{0};
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  const uint64_t bit = 1ull << (dev & 63);
+  if (!(done_mask.load(std::memory_order_acquire) & bit)) {
+    e = cudaFuncSetAttribute(gemm_tn_dev::cache_weigh_kernel<C>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             static_cast<int>(C::kSmemBytes));
+    if (e != cudaSuccess) return e;
+    done_mask.fetch_or(bit, std::memory_order_acq_rel);
+  }
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3(static_cast<unsigned>(args.chunks), 1, 1);
+  cfg.blockDim = dim3(C::kNumThreads, 1, 1);
+  cfg.dynamicSmemBytes = C::kSmemBytes;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = dependent_launch_enabled() ? 1 : 0;
+  return cudaLaunchKernelEx(&cfg, gemm_tn_dev::cache_weigh_kernel<C>, args);
+}
+
+}  // namespace
+
+cudaError_t launch_cache_weigh(int head_dim, bool bf16, const gemm_tn_dev::WeighArgs& args, cudaStream_t stream) {
+  using namespace gemm_tn_dev::cw;
+  if (head_dim == 64)
+    return bf16 ? launch_cfg<Cfg<64, true>>(args, stream) : launch_cfg<Cfg<64, false>>(args, stream);
+  if (head_dim == 128)
+    return bf16 ? launch_cfg<Cfg<128, true>>(args, stream) : launch_cfg<Cfg<128, false>>(args, stream);
+  return cudaErrorInvalidValue;
+}
+
+}  // namespace gemm_tn_impl

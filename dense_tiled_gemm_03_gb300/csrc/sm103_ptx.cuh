@@ -189,6 +189,16 @@ __device__ __forceinline__ void tma_load_3d(const void* tmap, uint32_t dst, uint
       : "memory");
 }
 
+// 4-D tile load global -> this CTA's shared memory (x innermost, in elements).
+__device__ __forceinline__ void tma_load_4d(const void* tmap, uint32_t dst, uint32_t bar, int32_t x, int32_t y,
+                                            int32_t z, int32_t w) {
+  asm volatile(
+      "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%2, %3, %4, %5}], [%6];"
+      :: "r"(dst), "l"(reinterpret_cast<uint64_t>(tmap)), "r"(x), "r"(y), "r"(z), "r"(w), "r"(bar)
+      : "memory");
+}
+
 // Multicast inside CTA pairs: the box lands at offset `dst` of every CTA in
 // `cta_mask`, and each destination pair's leader (even) CTA counts the bytes
 // on its barrier at the offset of `pair_bar` (a barrier address whose CTA

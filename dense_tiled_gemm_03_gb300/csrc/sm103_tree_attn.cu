@@ -1,0 +1,874 @@
+// sm103_tree_attn.cu -- attention of new (drafted) tokens over a paged
+// key/value cache and over one another (include/kv_cache.h: tree_attn_fwd).
+//
+//   s(i, k) = scale * q_i . k      k: the sequence's cached keys, then the new
+//   o_i     = sum_k softmax(s)_k v_k    tokens that i sees (bit mask or chain)
+//
+// The query rows of one KV head -- the new tokens times the query heads that
+// share it, token-major -- fill 128-row tiles, so one pass over the cache
+// serves the whole tree and the whole group: a tile's worth of keys is read
+// once for up to 128 rows (256 in pair mode). Per 128 cached keys of dim 128
+// that is 64 KB from memory against 8.4 MFLOP on the tensor cores, so up to
+// one row tile the kernel is bound by HBM, and past two by the tensor cores.
+//
+// Work: an item is (sequence, KV head, row unit) and walks its key tiles, the
+// cached ones and then the new tokens'. All items' key tiles are laid end to
+// end and cut into equal contiguous chunks, one per CTA, from the lengths as
+// they stand on the device: ragged batches balance to one tile, one long
+// sequence spreads over every SM, and a captured launch stays right when the
+// lengths change. An item that lies in one chunk is written by its CTA; one
+// that is cut leaves each part's unnormalised rows, maxima and sums in a
+// workspace and the second kernel joins them in order (repeatable to the bit).
+//
+// One CTA per SM:
+//   warp 0      TMA producer. Lane l copies the tile's l-th page (pages of 8 to
+//               64 rows; longer pages are copied 128 rows at a time), so page
+//               table look-ups and copies of a tile go out together.
+//   warp 1      MMA issuer (one thread): S_u = Q_u K_j^T, O_u += P_u V_j, with
+//               P_u in tensor memory over the scores it came from.
+//   warps 2-9   softmax, four warps per unit u, one thread per row.
+// The two units keep the tensor cores busy in turn. With at most 128 rows per
+// KV head (parity mode) both units hold the same rows and take every other key
+// tile, and their results are joined in tensor memory at the end of a chunk;
+// with more (pair mode) each has its own 128 rows and both read every tile.
+//
+// Rows behind the end of a sequence in its last page (or between its new
+// tokens' count and the array's end) may hold anything, NaN included: their
+// scores are replaced, not added to, the product P V stops at the 16-key step
+// that holds the last key, and the rows of V behind that key are zeroed in
+// shared memory.
+#include <cuda.h>
+#include <cuda_runtime.h>
+
+#include <atomic>
+#include <cstdint>
+
+#include "gemm_tn_internal.h"
+#include "sm103_cache.cuh"
+
+namespace gemm_tn_dev {
+
+namespace ta {
+
+constexpr int kProducerWarp = 0;
+constexpr int kMmaWarp = 1;
+constexpr int kFirstSoftmaxWarp = 2;
+constexpr int kTileRows = 128;     // query rows per tile (TMEM lanes)
+using cache::kTileKeys;
+using cache::pack2;
+constexpr float kLn2 = 0.69314718055994531f;
+
+template <int kDim_, bool kBf16_>
+struct Cfg {
+  static constexpr int kDim = kDim_;
+  static constexpr bool kBf16 = kBf16_;
+  static constexpr int kNumThreads = 64 + 256;
+  // registers per thread for one CTA per SM (16384 per sub-partition, three warps each)
+  static constexpr int kMaxRegs = 168;
+  static constexpr int kDimBoxes = kDim / 64;             // 64-element (128-byte) boxes across dim
+  static constexpr uint32_t kBoxBytes = 128u * 128u;      // 128 rows x 128 bytes
+  static constexpr uint32_t kTileBytes = kDimBoxes * kBoxBytes;
+  static constexpr int kKStages = kDim == 64 ? 6 : 3;
+  static constexpr int kVStages = kDim == 64 ? 5 : 2;
+  static constexpr uint32_t kOffQ = 0;                    // two slots of one row tile
+  static constexpr uint32_t kOffK = kOffQ + 2 * kTileBytes;
+  static constexpr uint32_t kOffV = kOffK + kKStages * kTileBytes;
+  static constexpr uint32_t kOffXch = kOffV + kVStages * kTileBytes;   // (max, sum) per row of unit 1
+  static constexpr uint32_t kOffBar = kOffXch + 8u * kTileRows;
+  // q_full[2], q_empty[2], k_full[KS], k_empty[KS], v_full[VS], v_empty[VS],
+  // s_full[2], p_full[2], o_done[2], xch_full, xch_empty, drain
+  static constexpr int kNumBars = 4 + 2 * kKStages + 2 * kVStages + 6 + 3;
+  static constexpr uint32_t kOffTmemSlot = kOffBar + 8u * kNumBars;
+  static constexpr uint32_t kOffAbort = kOffTmemSlot + 4u;
+  static constexpr uint32_t kOffStart = kOffAbort + 4u;   // chunk start (int64 x 3)
+  static constexpr uint32_t kSmemBytes = kOffStart + 24u + 1024u;   // + slack to align the base to 1024
+  static constexpr uint32_t kTmemCols = 512;
+  static constexpr uint32_t kColS = 0;      // S_u: 128 fp32 columns at 128 u (P_u over half of them)
+  static constexpr uint32_t kColO = 256;    // O_u: dim fp32 columns at 256 + dim u
+  static constexpr uint32_t kIdescS = mma_idesc_f16(kBf16, kTileRows, 0, false);   // N is set per tile
+  static constexpr uint32_t kIdescO = mma_idesc_f16(kBf16, kTileRows, kDim, true);
+  static_assert(kDim == 64 || kDim == 128, "head dim 64 or 128");
+  static_assert(kSmemBytes <= 227u * 1024u, "shared memory budget");
+  static_assert(kOffBar % 8u == 0 && kOffStart % 8u == 0, "64-bit shared words");
+};
+
+// ------------------------------------------------------------------ the schedule
+
+// Cached keys and new tokens of sequence b, as the kernels may use them: the
+// arrays on the device are clamped to what the cache and the inputs can hold.
+__device__ __forceinline__ int cached_len(const TreeArgs& a, int b) {
+  return min(max(__ldg(a.lens + b), 0), a.capacity);
+}
+__device__ __forceinline__ int new_len(const TreeArgs& a, int b) {
+  return a.token_lens == nullptr ? a.tokens : min(max(__ldg(a.token_lens + b), 0), a.tokens);
+}
+
+// Key tiles that unit `u` of row unit `ru` walks: all cached ones and the new
+// ones up to the last token it may see. At least one where the unit has rows
+// (an empty tile writes the empty softmax), none where it has not.
+__device__ __forceinline__ int unit_tiles(const TreeArgs& a, int len, int tl, int ru, int u) {
+  const int i0 = (ru * a.units + u) * a.tile_tokens;
+  if (i0 >= tl) return 0;
+  const int fresh = a.has_new == 0 ? 0 : (a.mask == nullptr ? min(tl, i0 + a.tile_tokens) : tl);
+  const int n = (len + kTileKeys - 1) / kTileKeys + (fresh + kTileKeys - 1) / kTileKeys;
+  return max(n, 1);
+}
+
+__device__ __forceinline__ int item_tiles(const TreeArgs& a, int len, int tl, int ru) {
+  const int n0 = unit_tiles(a, len, tl, ru, 0);
+  return a.units == 2 ? max(n0, unit_tiles(a, len, tl, ru, 1)) : n0;
+}
+
+// Key tiles of all row units of one KV head of a sequence.
+__device__ __forceinline__ int64_t head_tiles(const TreeArgs& a, int len, int tl) {
+  int64_t n = 0;
+  for (int ru = 0; ru < a.row_units; ++ru) n += item_tiles(a, len, tl, ru);
+  return n;
+}
+
+// Where chunk `chunk` starts (called by a whole warp).
+__device__ __forceinline__ cache::Start chunk_start(const TreeArgs& a, int chunk, uint32_t lane) {
+  return cache::find_start(a.batch, a.chunks, a.min_chunk, chunk, lane, [&](int b) {
+    return head_tiles(a, cached_len(a, b), new_len(a, b)) * a.kv_heads;
+  });
+}
+
+// Walks a chunk: one segment (a run of one item's key tiles) after another.
+struct Walk {
+  int b, h, ru, j0;      // item and its first tile in this segment
+  int len, tl;           // cached keys and new tokens of b
+  int tiles;             // tiles of the item
+  int count;             // tiles of the segment
+  int64_t left;          // tiles of the chunk from this segment on
+
+  __device__ __forceinline__ void load(const TreeArgs& a) {
+    len = cached_len(a, b);
+    tl = new_len(a, b);
+  }
+  __device__ __forceinline__ void start(const TreeArgs& a, int b_, int64_t off, int64_t left_) {
+    b = b_;
+    left = left_;
+    if (left <= 0) return;
+    load(a);
+    const int64_t per_head = head_tiles(a, len, tl);
+    h = static_cast<int>(off / per_head);
+    int rest = static_cast<int>(off - per_head * h);
+    ru = 0;
+    while ((tiles = item_tiles(a, len, tl, ru)) <= rest) {
+      rest -= tiles;
+      ++ru;
+    }
+    j0 = rest;
+    count = static_cast<int>(min(static_cast<int64_t>(tiles - j0), left));
+  }
+  __device__ __forceinline__ bool more() const { return left > 0; }
+  __device__ __forceinline__ void next(const TreeArgs& a) {
+    left -= count;
+    if (left <= 0) return;
+    j0 = 0;
+    do {
+      if (++ru == a.row_units) {
+        ru = 0;
+        if (++h == a.kv_heads) {
+          h = 0;
+          ++b;
+          load(a);
+        }
+      }
+      tiles = item_tiles(a, len, tl, ru);
+    } while (tiles == 0);
+    count = static_cast<int>(min(static_cast<int64_t>(tiles), left));
+  }
+  // Past the last tile of the segment that unit u walks.
+  __device__ __forceinline__ int unit_end(const TreeArgs& a, int u) const {
+    const int end = j0 + count;
+    return a.units == 2 ? max(j0, min(end, unit_tiles(a, len, tl, ru, u))) : end;
+  }
+};
+
+// Keys of tile j that exist: cached tiles first, then the new tokens'.
+struct Tile {
+  bool fresh;    // new tokens' keys
+  int index;     // tile number among its kind
+  int valid;     // keys of the tile that exist
+};
+__device__ __forceinline__ Tile tile_of(int len, int tl, bool has_new, int j) {
+  const int nc = (len + kTileKeys - 1) / kTileKeys;
+  Tile t;
+  t.fresh = j >= nc;
+  t.index = t.fresh ? j - nc : j;
+  t.valid = min(kTileKeys, max(0, (t.fresh ? (has_new ? tl : 0) : len) - t.index * kTileKeys));
+  return t;
+}
+
+}  // namespace ta
+
+template <class C>
+__global__ void __launch_bounds__(C::kNumThreads) __maxnreg__(C::kMaxRegs)
+    tree_attn_kernel(const __grid_constant__ TreeArgs args) {
+  extern __shared__ uint8_t smem_raw[];
+  const uint32_t raw_addr = smem_addr(smem_raw);
+  uint8_t* smem = smem_raw + (((raw_addr + 1023u) & ~1023u) - raw_addr);
+  const uint32_t base = smem_addr(smem);
+  const uint32_t warp = threadIdx.x >> 5;
+  const uint32_t lane = lane_id();
+
+  auto q_tile = [&](int s) { return base + C::kOffQ + s * C::kTileBytes; };
+  auto k_tile = [&](int s) { return base + C::kOffK + s * C::kTileBytes; };
+  auto v_tile = [&](int s) { return base + C::kOffV + s * C::kTileBytes; };
+  auto bar = [&](int i) { return base + C::kOffBar + 8u * i; };
+  constexpr int kKBar = 4, kVBar = kKBar + 2 * C::kKStages, kUBar = kVBar + 2 * C::kVStages;
+  auto q_full = [&](int s) { return bar(s); };
+  auto q_empty = [&](int s) { return bar(2 + s); };
+  auto k_full = [&](int s) { return bar(kKBar + s); };
+  auto k_empty = [&](int s) { return bar(kKBar + C::kKStages + s); };
+  auto v_full = [&](int s) { return bar(kVBar + s); };
+  auto v_empty = [&](int s) { return bar(kVBar + C::kVStages + s); };
+  auto s_full = [&](int u) { return bar(kUBar + u); };
+  auto p_full = [&](int u) { return bar(kUBar + 2 + u); };
+  auto o_done = [&](int u) { return bar(kUBar + 4 + u); };
+  const uint32_t xch_full = bar(kUBar + 6), xch_empty = bar(kUBar + 7), drain_bar = bar(kUBar + 8);
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + C::kOffTmemSlot);
+  volatile uint32_t* abort_flag = reinterpret_cast<volatile uint32_t*>(smem + C::kOffAbort);
+  int64_t* start_slot = reinterpret_cast<int64_t*>(smem + C::kOffStart);
+  float2* xch = reinterpret_cast<float2*>(smem + C::kOffXch);
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < 2; ++s) {
+      mbar_init(q_full(s), 1);
+      mbar_init(q_empty(s), 1);
+      mbar_init(s_full(s), 1);
+      mbar_init(p_full(s), 4);   // one arrival per softmax warp of the unit
+      mbar_init(o_done(s), 1);
+    }
+    for (int s = 0; s < C::kKStages; ++s) {
+      mbar_init(k_full(s), 1);
+      mbar_init(k_empty(s), 1);
+    }
+    for (int s = 0; s < C::kVStages; ++s) {
+      mbar_init(v_full(s), 1);
+      mbar_init(v_empty(s), 1);
+    }
+    mbar_init(xch_full, 4);
+    mbar_init(xch_empty, 4);
+    mbar_init(drain_bar, 1);
+    *abort_flag = 0u;
+    fence_barrier_init();
+  }
+  if (warp == ta::kProducerWarp && lane == 0) {
+    tma_prefetch_descriptor(&args.tmap_q);
+    tma_prefetch_descriptor(&args.tmap_k);
+    tma_prefetch_descriptor(&args.tmap_v);
+  }
+  if (warp == ta::kMmaWarp) {
+    tmem_alloc<1>(smem_addr(tmem_slot), C::kTmemCols);
+    tmem_relinquish<1>();
+  }
+  // The set-up above may overlap the end of the previous kernel in the
+  // stream; global memory is touched only once that kernel has completed.
+  griddep_wait();
+  griddep_launch_dependents();
+  if (warp == ta::kProducerWarp) {
+    const cache::Start st = ta::chunk_start(args, static_cast<int>(blockIdx.x), lane);
+    if (lane == 0) {
+      start_slot[0] = st.b;
+      start_slot[1] = st.off;
+      start_slot[2] = min(st.chunk_tiles, st.total - st.chunk_tiles * static_cast<int64_t>(blockIdx.x));
+    }
+  }
+  tc_fence_before_sync();
+  __syncthreads();
+  tc_fence_after_sync();
+  const uint32_t tmem_base = *tmem_slot;
+  const cache::Watch wd{args.status, args.timeout_ns, abort_flag};
+  const bool parity_mode = args.units == 1;
+  const bool has_new = args.has_new != 0;
+  ta::Walk w;
+  w.start(args, static_cast<int>(start_slot[0]), start_slot[1], start_slot[2]);
+
+  if (warp == ta::kProducerWarp) {
+    // -------------------------------------------------------------- TMA producer
+    int issued_k[C::kKStages], issued_v[C::kVStages], issued_q[2] = {-1, -1};
+    for (int s = 0; s < C::kKStages; ++s) issued_k[s] = -1;
+    for (int s = 0; s < C::kVStages; ++s) issued_v[s] = -1;
+    const int box_rows = min(args.page_size, ta::kTileKeys);
+    const int tile_pages = ta::kTileKeys / box_rows;   // pages (or parts of one) per tile
+    const uint32_t q_bytes = static_cast<uint32_t>(args.tile_tokens * args.group) * 128u * C::kDimBoxes;
+    int it = 0;     // tiles issued
+    int seg = 0;    // segments begun
+    bool ok = true;
+    for (; ok && w.more(); w.next(args), ++seg) {
+      for (int u = 0; u < args.units && ok; ++u) {
+        const int slot = parity_mode ? seg & 1 : u;
+        const uint32_t ph = static_cast<uint32_t>(parity_mode ? seg >> 1 : seg) & 1u;
+        ok = wd.warp_wait(q_empty(slot), ph ^ 1u);
+        if (ok && lane == 0) {
+          mbar_arrive_expect_tx(q_full(slot), q_bytes);
+          for (int c = 0; c < C::kDimBoxes; ++c)
+            tma_load_4d(&args.tmap_q, q_tile(slot) + c * C::kBoxBytes, q_full(slot), 64 * c, w.h * args.group,
+                        (w.ru * args.units + u) * args.tile_tokens, w.b);
+        }
+        if (ok) issued_q[slot] = static_cast<int>(ph);
+      }
+      const int32_t* table = args.page_table + static_cast<int64_t>(w.b) * args.table_stride;
+      // the page that this lane copies of cached tile j
+      auto page_of = [&](int j) {
+        const ta::Tile t = ta::tile_of(w.len, w.tl, has_new, j);
+        if (t.fresh || static_cast<int>(lane) * box_rows >= t.valid) return 0;
+        const int first = t.index * ta::kTileKeys + static_cast<int>(lane) * box_rows;
+        int page = __ldg(table + first / args.page_size);
+        if (page < 0 || page >= args.num_pages) {
+          // not a page: nothing is read (the copy fills zeros), and the caller is told
+          cache::report(args.status, cache::kStatusInvalid);
+          page = args.num_pages;
+        }
+        return page;
+      };
+      int page = page_of(w.j0);
+      for (int j = w.j0; j < w.j0 + w.count; ++j, ++it) {
+        const ta::Tile t = ta::tile_of(w.len, w.tl, has_new, j);
+        const int boxes = t.fresh ? (t.valid > 0 ? 1 : 0) : (t.valid + box_rows - 1) / box_rows;
+        const int rows = t.fresh ? ta::kTileKeys : box_rows;
+        const uint32_t bytes = static_cast<uint32_t>(boxes * rows) * 128u * C::kDimBoxes;
+        const int slot0 = t.fresh ? t.index * ta::kTileKeys
+                                  : (tile_pages == 1 ? (t.index * ta::kTileKeys) % args.page_size : 0);
+        const int next_page = j + 1 < w.j0 + w.count ? page_of(j + 1) : 0;
+        const bool mine = static_cast<int>(lane) < boxes;
+        const int s = it % C::kKStages;
+        const uint32_t ph = static_cast<uint32_t>(it / C::kKStages) & 1u;
+        if (!(ok = wd.warp_wait(k_empty(s), ph ^ 1u))) break;
+        if (lane == 0) mbar_arrive_expect_tx(k_full(s), bytes);
+        __syncwarp();
+        if (mine && !(blockIdx.x == 0 && it == args.drop_load_block)) {
+          for (int c = 0; c < C::kDimBoxes; ++c)
+            tma_load_4d(t.fresh ? &args.tmap_k_new : &args.tmap_k, k_tile(s) + c * C::kBoxBytes + lane * box_rows * 128u,
+                        k_full(s), 64 * c, w.h, slot0, t.fresh ? w.b : page);
+        }
+        issued_k[s] = static_cast<int>(ph);
+        const int sv = it % C::kVStages;
+        const uint32_t phv = static_cast<uint32_t>(it / C::kVStages) & 1u;
+        if (!(ok = wd.warp_wait(v_empty(sv), phv ^ 1u))) break;
+        if (lane == 0) mbar_arrive_expect_tx(v_full(sv), bytes);
+        __syncwarp();
+        if (mine) {
+          for (int c = 0; c < C::kDimBoxes; ++c)
+            tma_load_4d(t.fresh ? &args.tmap_v_new : &args.tmap_v, v_tile(sv) + c * C::kBoxBytes + lane * box_rows * 128u,
+                        v_full(sv), 64 * c, w.h, slot0, t.fresh ? w.b : page);
+        }
+        issued_v[sv] = static_cast<int>(phv);
+        page = next_page;
+      }
+    }
+    // Loads may still be landing if another role gave up: wait (bounded) for
+    // every phase issued before the CTA may exit.
+    for (int s = 0; s < 2; ++s)
+      if (issued_q[s] >= 0) wd.drain(q_full(s), static_cast<uint32_t>(issued_q[s]));
+    for (int s = 0; s < C::kKStages; ++s)
+      if (issued_k[s] >= 0) wd.drain(k_full(s), static_cast<uint32_t>(issued_k[s]));
+    for (int s = 0; s < C::kVStages; ++s)
+      if (issued_v[s] >= 0) wd.drain(v_full(s), static_cast<uint32_t>(issued_v[s]));
+  } else if (warp == ta::kMmaWarp) {
+    if (lane == 0) {
+      // ------------------------------------------------------------ MMA issuer
+      int it0 = 0;                    // ring number of the segment's first tile
+      int seg = 0;
+      int done[2] = {0, 0};           // tiles of each unit whose P has been asked for
+      bool ok = true;
+      for (; ok && w.more(); it0 += w.count, w.next(args), ++seg) {
+        const int end[2] = {w.unit_end(args, 0), w.unit_end(args, 1)};
+        const int step = parity_mode ? 2 : 1;
+        // the last unit that reads tile j (pair mode: both read it while both walk it)
+        auto last_reader = [&](int u, int j) { return parity_mode || u == 1 || j >= end[1]; };
+        auto wait_k = [&](int j) {
+          const int i = it0 + j - w.j0;
+          return wd.wait(k_full(i % C::kKStages), static_cast<uint32_t>(i / C::kKStages) & 1u);
+        };
+        auto issue_s = [&](int u, int j) {
+          const int s = (it0 + j - w.j0) % C::kKStages;
+          const int slot = parity_mode ? seg & 1 : u;
+          const int valid = ta::tile_of(w.len, w.tl, has_new, j).valid;
+          // N: the key columns that hold keys, in steps of 32
+          const uint32_t n = static_cast<uint32_t>(max(1, (valid + 31) / 32)) * 32u;
+          const uint32_t idesc = C::kIdescS | ((n >> 3) << 17);
+          const uint32_t t_s = tmem_base + C::kColS + 128u * static_cast<uint32_t>(u);
+#pragma unroll
+          for (int c = 0; c < C::kDimBoxes; ++c) {
+            const uint64_t a_desc = sw128_kmajor_desc(q_tile(slot) + c * C::kBoxBytes);
+            const uint64_t b_desc = sw128_kmajor_desc(k_tile(s) + c * C::kBoxBytes);
+#pragma unroll
+            for (int kk = 0; kk < 4; ++kk)   // 16 elements of dim = 32 bytes = 2 descriptor units
+              mma_f16<1>(t_s, a_desc + 2u * kk, b_desc + 2u * kk, idesc, (c | kk) != 0 ? 1u : 0u);
+          }
+          mma_commit(s_full(u));
+          if (last_reader(u, j)) mma_commit(k_empty(s));
+        };
+        auto issue_pv = [&](int u, int j, bool first) {
+          const int s = (it0 + j - w.j0) % C::kVStages;
+          const int steps = (ta::tile_of(w.len, w.tl, has_new, j).valid + 15) / 16;
+          const uint64_t v_desc = sw128_mnmajor_desc(v_tile(s), C::kBoxBytes);
+          const uint32_t t_p = tmem_base + C::kColS + 128u * static_cast<uint32_t>(u);
+          const uint32_t t_o = tmem_base + C::kColO + static_cast<uint32_t>(C::kDim * u);
+          auto pv = [&](int kk) {   // 16 keys: 8 columns of P; 16 rows of 128 bytes of V
+            mma_f16_tmem_a(t_o, t_p + 64u * static_cast<uint32_t>(kk >> 2) + 8u * static_cast<uint32_t>(kk & 3),
+                           v_desc + ((static_cast<uint32_t>(kk) * 2048u) >> 4), C::kIdescO,
+                           first && kk == 0 ? 0u : 1u);
+          };
+          if (steps == 8) {
+#pragma unroll
+            for (int kk = 0; kk < 8; ++kk) pv(kk);
+          } else {
+            for (int kk = 0; kk < steps; ++kk) pv(kk);
+          }
+          if (last_reader(u, j)) mma_commit(v_empty(s));
+        };
+        for (int u = 0; u < args.units && ok; ++u) {
+          const int slot = parity_mode ? seg & 1 : u;
+          ok = wd.wait(q_full(slot), static_cast<uint32_t>(parity_mode ? seg >> 1 : seg) & 1u);
+        }
+        for (int u = 0; u < 2 && ok; ++u) {
+          const int j = w.j0 + (parity_mode ? u : 0);
+          if (j >= end[u]) continue;
+          if (!(ok = wait_k(j))) break;
+          tc_fence_after_sync();
+          issue_s(u, j);
+        }
+        for (int j = w.j0; ok && j < w.j0 + w.count; ++j) {
+          const int i = it0 + j - w.j0;
+          if (!(ok = wd.wait(v_full(i % C::kVStages), static_cast<uint32_t>(i / C::kVStages) & 1u))) break;
+          for (int u = 0; u < 2; ++u) {
+            if (j >= end[u] || (parity_mode && ((j - w.j0) & 1) != u)) continue;
+            if (!(ok = wd.wait(p_full(u), static_cast<uint32_t>(done[u]) & 1u))) break;
+            ++done[u];
+            tc_fence_after_sync();
+            issue_pv(u, j, j - w.j0 < step);
+            if (j + step < end[u]) {
+              if (!(ok = wait_k(j + step))) break;
+              tc_fence_after_sync();
+              issue_s(u, j + step);
+            } else {
+              mma_commit(o_done(u));
+            }
+          }
+        }
+        for (int u = 0; u < args.units && ok; ++u) mma_commit(q_empty(parity_mode ? seg & 1 : u));
+      }
+      // every MMA issued here must finish before TMEM is freed
+      mma_commit(drain_bar);
+      wd.drain(drain_bar, 0);
+    }
+  } else {
+    // -------------------------------------------------------------- softmax
+    const int u = (static_cast<int>(warp) - ta::kFirstSoftmaxWarp) >> 2;   // unit
+    const uint32_t quarter = warp & 3u;                                    // TMEM lanes 32*quarter ..
+    const int r = static_cast<int>(quarter * 32u + lane);                  // row of the tile
+    const int r_token = r / args.group, r_head = r - r_token * args.group;
+    const uint32_t lane_off = (quarter * 32u) << 16;
+    const uint32_t t_s = tmem_base + lane_off + C::kColS + 128u * static_cast<uint32_t>(u);
+    auto p_col = [&](int key) { return t_s + static_cast<uint32_t>(64 * (key / 64) + (key % 64) / 2); };
+    const uint32_t t_o = tmem_base + lane_off + C::kColO + static_cast<uint32_t>(C::kDim * u);
+    const float c_log2 = args.scale_log2;
+    const int step = parity_mode ? 2 : 1;
+    int it0 = 0;                    // ring number of the segment's first tile
+    uint32_t tiles_done = 0;        // tiles of this unit so far
+    uint32_t ends[2] = {0, 0};      // o_done phases of the units so far
+    uint32_t joins = 0;             // exchanges so far (parity mode)
+    bool ok = true;
+    for (; ok && w.more(); it0 += w.count, w.next(args)) {
+      const int end[2] = {w.unit_end(args, 0), w.unit_end(args, 1)};
+      const int i0 = (w.ru * args.units + (parity_mode ? 0 : u)) * args.tile_tokens;   // first token of the tile
+      const int token = i0 + r_token;
+      const bool live = r_token < args.tile_tokens && token < w.tl;          // this row exists
+      const bool warp_live = __any_sync(0xffffffffu, live);
+      float m_ref = 0.0f;        // reference maximum, in units of scale * log2e
+      bool unset = live;         // no key seen yet: there is no reference
+      float l = 0.0f;            // row sum of probabilities, against m_ref
+      const int first = w.j0 + (parity_mode ? u : 0);
+      for (int j = first; j < end[u] && ok; j += step) {
+        // S_u for key tile j is complete, and with it P_u V of the tile before: O_u is stable
+        if (!wd.warp_wait(s_full(u), tiles_done & 1u)) {
+          ok = false;
+          break;
+        }
+        ++tiles_done;
+        tc_fence_after_sync();
+        const ta::Tile t = ta::tile_of(w.len, w.tl, has_new, j);
+        if (warp_live && t.valid > 0) {
+          float sv[128];
+          {
+            uint32_t raw[4][32];
+#pragma unroll
+            for (int c = 0; c < 4; ++c) tmem_load_32x32(t_s + 32u * c, raw[c]);
+            tmem_load_wait();
+#pragma unroll
+            for (int c = 0; c < 4; ++c)
+#pragma unroll
+              for (int e = 0; e < 32; ++e) sv[c * 32 + e] = __uint_as_float(raw[c][e]);
+          }
+          if (t.fresh || t.valid < ta::kTileKeys) {
+            uint32_t vis[4];
+            int limit = t.valid;   // keys of the tile that this row may see, but for the mask
+            if (t.fresh && args.mask == nullptr) limit = min(limit, token + 1 - t.index * ta::kTileKeys);
+#pragma unroll
+            for (int c = 0; c < 4; ++c) vis[c] = cache::low_bits(limit - 32 * c);
+            if (t.fresh && args.mask != nullptr && live) {
+              const uint64_t* words = args.mask + (static_cast<int64_t>(w.b) * args.tokens + token) * args.mask_words;
+#pragma unroll
+              for (int c = 0; c < 2; ++c) {
+                const uint64_t bits = 2 * t.index + c < args.mask_words ? __ldg(words + 2 * t.index + c) : 0ull;
+                vis[2 * c] &= static_cast<uint32_t>(bits);
+                vis[2 * c + 1] &= static_cast<uint32_t>(bits >> 32);
+              }
+            }
+#pragma unroll
+            for (int e = 0; e < 128; ++e)
+              if (!((vis[e / 32] >> (e % 32)) & 1u)) sv[e] = -INFINITY;
+          }
+          // probabilities against neg_m into the P columns; returns their sum
+          // (packed fp32 pairs: two values per instruction)
+          auto exp_pass = [&](float neg_m) {
+            const uint64_t cc = f32x2_pack(c_log2, c_log2), mm = f32x2_pack(neg_m, neg_m);
+            uint64_t s01 = f32x2_pack(0.0f, 0.0f), s23 = f32x2_pack(0.0f, 0.0f);
+#pragma unroll
+            for (int c = 0; c < 4; ++c) {
+              uint32_t pk[16];   // 32 scores -> 16 columns of P
+#pragma unroll
+              for (int e = 0; e < 32; e += 4) {
+                const float* x = sv + 32 * c + e;
+                float a0, a1, a2, a3;
+                f32x2_unpack(f32x2_fma(f32x2_pack(x[0], x[1]), cc, mm), a0, a1);
+                f32x2_unpack(f32x2_fma(f32x2_pack(x[2], x[3]), cc, mm), a2, a3);
+                const float p0 = ex2_approx(a0);
+                const float p1 = ex2_approx(a1);
+                const float p2 = ex2_approx(a2);
+                const float p3 = ex2_approx(a3);
+                s01 = f32x2_add(s01, f32x2_pack(p0, p1));
+                s23 = f32x2_add(s23, f32x2_pack(p2, p3));
+                pk[e / 2] = ta::pack2<C::kBf16>(p0, p1);
+                pk[e / 2 + 1] = ta::pack2<C::kBf16>(p2, p3);
+              }
+              tmem_store_32x16(p_col(32 * c), pk);
+            }
+            float sum0, sum1, sum2, sum3;
+            f32x2_unpack(s01, sum0, sum1);
+            f32x2_unpack(s23, sum2, sum3);
+            return (sum0 + sum1) + (sum2 + sum3);
+          };
+          auto row_max = [&]() {
+            float mx0 = sv[0], mx1 = sv[1], mx2 = sv[2], mx3 = sv[3];
+#pragma unroll
+            for (int e = 4; e < 128; e += 4) {
+              mx0 = fmaxf(mx0, sv[e]);
+              mx1 = fmaxf(mx1, sv[e + 1]);
+              mx2 = fmaxf(mx2, sv[e + 2]);
+              mx3 = fmaxf(mx3, sv[e + 3]);
+            }
+            return fmaxf(fmaxf(mx0, mx1), fmaxf(mx2, mx3));
+          };
+          // A row's reference is the maximum of the first tile in which it sees
+          // a key; later tiles are taken against it at once. No probability
+          // exceeds 2^8 unless the row sum does, so only then is the tile's
+          // maximum taken, and moved to where it is past that factor (the warp
+          // then computes the tile again and rescales O: the same softmax).
+          if (__any_sync(0xffffffffu, unset)) {
+            const float mx = row_max();
+            if (unset && mx != -INFINITY) {
+              m_ref = mx * c_log2;
+              unset = false;
+            }
+          }
+          float alpha = 1.0f;
+          float sum = exp_pass(-m_ref);
+          if (__any_sync(0xffffffffu, live && !(sum <= 256.0f))) {
+            const float m_tile = row_max() * c_log2;
+            const bool move = live && m_tile > m_ref + 8.0f;
+            if (__any_sync(0xffffffffu, move)) {
+              if (move) {
+                alpha = ex2_approx(m_ref - m_tile);
+                m_ref = m_tile;
+              }
+              tmem_store_wait();   // the first pass's stores land before they are overwritten
+              sum = exp_pass(-m_ref);
+            }
+          }
+          l = l * alpha + sum;
+          if (__any_sync(0xffffffffu, alpha != 1.0f)) {
+#pragma unroll
+            for (int c = 0; c < C::kDim / 32; ++c) {
+              uint32_t o[32];
+              tmem_load_32x32(t_o + 32u * c, o);
+              tmem_load_wait();
+#pragma unroll
+              for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * alpha);
+              tmem_store_32x32(t_o + 32u * c, o);
+            }
+          }
+          tmem_store_wait();
+        }
+        if (t.valid % 16 != 0) {
+          // zero the rows of V behind the last key, up to the end of its 16-key step
+          const int i = it0 + j - w.j0;
+          if (!wd.warp_wait(v_full(i % C::kVStages), static_cast<uint32_t>(i / C::kVStages) & 1u)) {
+            ok = false;
+            break;
+          }
+          const int row_end = (t.valid + 15) / 16 * 16;
+          const uint32_t tile = v_tile(i % C::kVStages);
+          for (int x = t.valid * 8 + r; x < row_end * 8; x += 128)
+#pragma unroll
+            for (int c = 0; c < C::kDimBoxes; ++c) st_shared_v4(tile + c * C::kBoxBytes + 16u * x, 0u, 0u, 0u, 0u);
+          fence_proxy_async_shared();
+        }
+        tc_fence_before_sync();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(p_full(u));
+      }
+      if (!ok) break;
+      // ---------------------------------------------------------- end of a segment
+      const bool mine = first < end[u];
+      if (mine) {
+        if (!(ok = wd.warp_wait(o_done(u), ends[u] & 1u))) break;
+        ++ends[u];
+      }
+      float other_m = 0.0f, other_l = 0.0f;   // the other unit's part of this row
+      if (parity_mode && end[0] - w.j0 > 1) {
+        if (u == 1) {
+          // unit 0 joins the rows: hand over maximum and sum, and leave O_1
+          // alone until they have been read
+          xch[r] = make_float2(m_ref, l);
+          tc_fence_before_sync();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(xch_full);
+          if (!(ok = wd.warp_wait(xch_empty, joins & 1u))) break;
+          tc_fence_after_sync();
+          ++joins;
+          continue;
+        }
+        if (!(ok = wd.warp_wait(o_done(1), ends[1] & 1u))) break;
+        ++ends[1];
+        if (!(ok = wd.warp_wait(xch_full, joins & 1u))) break;
+        const float2 x = xch[r];
+        other_m = x.x;
+        other_l = x.y;
+      } else if (!mine) {
+        continue;
+      }
+      tc_fence_after_sync();
+      if (warp_live) {
+        // a part with an empty sum has no reference and nothing in O
+        float m = l > 0.0f ? (other_l > 0.0f ? fmaxf(m_ref, other_m) : m_ref) : other_m;
+        const float w0 = l > 0.0f ? ex2_approx(m_ref - m) : 0.0f;
+        const float w1 = other_l > 0.0f ? ex2_approx(other_m - m) : 0.0f;
+        // NaN sums (NaN or infinite inputs) stay NaN
+        const float sum = !(l == 0.0f || other_l == 0.0f) ? l * w0 + other_l * w1 : (l == 0.0f ? other_l : l);
+        const bool join = __any_sync(0xffffffffu, other_l != 0.0f);
+        const bool whole = w.j0 == 0 && w.count == w.tiles;
+        const float f0 = l == 0.0f ? 0.0f : (l > 0.0f ? w0 : 1.0f);
+        const float f1 = other_l == 0.0f ? 0.0f : (other_l > 0.0f ? w1 : 1.0f);
+        const float inv = whole ? (sum == 0.0f ? 0.0f : 1.0f / sum) : 1.0f;
+        const int64_t out_row = (static_cast<int64_t>(w.b) * args.tokens + token) * args.heads + w.h * args.group + r_head;
+        const int slot = static_cast<int>(blockIdx.x) * 2 + (w.j0 == 0 ? 1 : 0);
+        const int64_t part_row = static_cast<int64_t>(slot) * (args.units * ta::kTileRows) + (parity_mode ? 0 : u) * ta::kTileRows + r;
+        if (live) {
+          if (whole) {
+            if (args.lse != nullptr)
+              args.lse[out_row] = sum == 0.0f ? -INFINITY : (m * ta::kLn2 + logf(sum));
+          } else {
+            args.part_ml[part_row] = make_float2(m, sum);
+          }
+        }
+        uint16_t* out = static_cast<uint16_t*>(args.o) + out_row * C::kDim;
+        float* part = args.part_o + part_row * C::kDim;
+#pragma unroll
+        for (int c = 0; c < C::kDim / 32; ++c) {
+          uint32_t o[32];
+          tmem_load_32x32(t_o + 32u * c, o);
+          tmem_load_wait();
+          float v[32];
+#pragma unroll
+          for (int e = 0; e < 32; ++e) v[e] = f0 != 0.0f ? __uint_as_float(o[e]) * f0 : 0.0f;
+          if (join) {
+            tmem_load_32x32(t_o + static_cast<uint32_t>(C::kDim) + 32u * c, o);
+            tmem_load_wait();
+#pragma unroll
+            for (int e = 0; e < 32; ++e) v[e] += f1 != 0.0f ? __uint_as_float(o[e]) * f1 : 0.0f;
+          }
+          if (live) {
+            if (whole) {
+              uint4* dst = reinterpret_cast<uint4*>(out + 32 * c);
+#pragma unroll
+              for (int x = 0; x < 4; ++x) {
+                const float* y = v + 8 * x;
+                dst[x] = make_uint4(ta::pack2<C::kBf16>(y[0] * inv, y[1] * inv), ta::pack2<C::kBf16>(y[2] * inv, y[3] * inv),
+                                    ta::pack2<C::kBf16>(y[4] * inv, y[5] * inv), ta::pack2<C::kBf16>(y[6] * inv, y[7] * inv));
+              }
+            } else {
+              float4* dst = reinterpret_cast<float4*>(part + 32 * c);
+#pragma unroll
+              for (int x = 0; x < 8; ++x) dst[x] = make_float4(v[4 * x], v[4 * x + 1], v[4 * x + 2], v[4 * x + 3]);
+            }
+          }
+        }
+      }
+      if (parity_mode && end[0] - w.j0 > 1) {
+        tc_fence_before_sync();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(xch_empty);
+        ++joins;
+      }
+    }
+  }
+
+  tc_fence_before_sync();
+  __syncthreads();
+  if (warp == ta::kMmaWarp) {
+    tc_fence_after_sync();
+    tmem_dealloc<1>(tmem_base, C::kTmemCols);
+  }
+}
+
+// Joins the parts of the items that a chunk boundary cut. Block x looks at the
+// boundary before chunk x + 1; the first boundary inside an item joins it:
+// part 0 lies in the chunk before, the others in the chunks after, in order.
+// One warp per row; the sums run over the parts in their order.
+template <int kDim, bool kBf16>
+__global__ void __launch_bounds__(256) tree_attn_join_kernel(const __grid_constant__ TreeArgs args) {
+  griddep_wait();
+  griddep_launch_dependents();
+  __shared__ int64_t found[4];
+  const uint32_t warp = threadIdx.x >> 5, lane = lane_id();
+  const int chunk = static_cast<int>(blockIdx.x) + 1;
+  if (warp == 0) {
+    const cache::Start st = ta::chunk_start(args, chunk, lane);
+    if (lane == 0) {
+      found[0] = st.b;
+      found[1] = st.off;
+      found[2] = st.chunk_tiles;
+      found[3] = st.total;
+    }
+  }
+  __syncthreads();
+  const int64_t per_chunk = found[2];
+  ta::Walk w;
+  w.start(args, static_cast<int>(found[0]), found[1], found[3] - per_chunk * chunk);
+  if (!w.more() || w.j0 == 0 || w.j0 > per_chunk) return;
+  const int parts = 1 + static_cast<int>((w.tiles - w.j0 + per_chunk - 1) / per_chunk);
+  const int rows_per_part = args.units * ta::kTileRows;
+  const int row = static_cast<int>(blockIdx.y) * 8 + static_cast<int>(warp);
+  const int unit = row / ta::kTileRows, r = row % ta::kTileRows;
+  const int r_token = r / args.group;
+  const int token = (w.ru * args.units + unit) * args.tile_tokens + r_token;
+  if (row >= rows_per_part || r_token >= args.tile_tokens || token >= w.tl) return;
+  // a unit whose rows end before the item's last parts left nothing there
+  auto at = [&](int p) {
+    const int slot = p == 0 ? (chunk - 1) * 2 + 1 : (chunk + p - 1) * 2;
+    return static_cast<int64_t>(slot) * rows_per_part + row;
+  };
+  const int own_tiles = ta::unit_tiles(args, w.len, w.tl, w.ru, unit);
+  auto has = [&](int p) {   // the part begins before the unit's last tile
+    return p == 0 || w.j0 + static_cast<int64_t>(p - 1) * per_chunk < own_tiles;
+  };
+  float m = -INFINITY;
+  for (int p = static_cast<int>(lane); p < parts; p += 32)
+    if (has(p)) {
+      const float2 ml = __ldg(args.part_ml + at(p));
+      if (ml.y > 0.0f) m = fmaxf(m, ml.x);
+    }
+#pragma unroll
+  for (int d = 16; d > 0; d /= 2) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, d));
+  float sum = 0.0f;
+  constexpr int kPer = kDim / 32;
+  float acc[kPer] = {};
+#pragma unroll 4
+  for (int p = 0; p < parts; ++p) {
+    if (!has(p)) continue;
+    const float2 ml = __ldg(args.part_ml + at(p));
+    const float f = ml.y == 0.0f ? 0.0f : (ml.y > 0.0f ? ex2_approx(ml.x - m) : 1.0f);
+    sum += f == 0.0f ? 0.0f : ml.y * f;
+    const float* src = args.part_o + at(p) * kDim + lane * kPer;
+    float x[kPer];
+    if constexpr (kPer == 4) {
+      const float4 y = __ldg(reinterpret_cast<const float4*>(src));
+      x[0] = y.x, x[1] = y.y, x[2] = y.z, x[3] = y.w;
+    } else {
+      const float2 y = __ldg(reinterpret_cast<const float2*>(src));
+      x[0] = y.x, x[1] = y.y;
+    }
+#pragma unroll
+    for (int e = 0; e < kPer; ++e) acc[e] += f == 0.0f ? 0.0f : x[e] * f;
+  }
+  const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
+  const int64_t out_row = (static_cast<int64_t>(w.b) * args.tokens + token) * args.heads + w.h * args.group + (r - r_token * args.group);
+  uint32_t* out = reinterpret_cast<uint32_t*>(static_cast<uint16_t*>(args.o) + out_row * kDim) + lane * (kPer / 2);
+#pragma unroll
+  for (int e = 0; e < kPer / 2; ++e) out[e] = ta::pack2<kBf16>(acc[2 * e] * inv, acc[2 * e + 1] * inv);
+  if (lane == 0 && args.lse != nullptr) args.lse[out_row] = sum == 0.0f ? -INFINITY : (m * ta::kLn2 + logf(sum));
+}
+
+}  // namespace gemm_tn_dev
+
+namespace gemm_tn_impl {
+
+namespace {
+
+template <class C>
+cudaError_t launch_cfg(const gemm_tn_dev::TreeArgs& args, cudaStream_t stream) {
+  static std::atomic<uint64_t> done_mask{0};
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  const uint64_t bit = 1ull << (dev & 63);
+  if (!(done_mask.load(std::memory_order_acquire) & bit)) {
+    e = cudaFuncSetAttribute(gemm_tn_dev::tree_attn_kernel<C>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             static_cast<int>(C::kSmemBytes));
+    if (e != cudaSuccess) return e;
+    done_mask.fetch_or(bit, std::memory_order_acq_rel);
+  }
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3(static_cast<unsigned>(args.chunks), 1, 1);
+  cfg.blockDim = dim3(C::kNumThreads, 1, 1);
+  cfg.dynamicSmemBytes = C::kSmemBytes;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = dependent_launch_enabled() ? 1 : 0;
+  return cudaLaunchKernelEx(&cfg, gemm_tn_dev::tree_attn_kernel<C>, args);
+}
+
+template <int kDim, bool kBf16>
+cudaError_t launch_join(const gemm_tn_dev::TreeArgs& args, cudaStream_t stream) {
+  cudaLaunchConfig_t cfg{};
+  const int rows = args.units == 2 ? 2 * gemm_tn_dev::ta::kTileRows
+                                   : (args.tokens < args.tile_tokens ? args.tokens : args.tile_tokens) * args.group;
+  cfg.gridDim = dim3(static_cast<unsigned>(args.chunks - 1), static_cast<unsigned>((rows + 7) / 8), 1);
+  cfg.blockDim = dim3(256, 1, 1);
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = dependent_launch_enabled() ? 1 : 0;
+  return cudaLaunchKernelEx(&cfg, gemm_tn_dev::tree_attn_join_kernel<kDim, kBf16>, args);
+}
+
+}  // namespace
+
+int tree_attn_tile_rows() { return gemm_tn_dev::ta::kTileRows; }
+
+cudaError_t launch_tree_attn(int head_dim, bool bf16, const gemm_tn_dev::TreeArgs& args, cudaStream_t stream) {
+  using namespace gemm_tn_dev::ta;
+  if (head_dim == 64)
+    return bf16 ? launch_cfg<Cfg<64, true>>(args, stream) : launch_cfg<Cfg<64, false>>(args, stream);
+  if (head_dim == 128)
+    return bf16 ? launch_cfg<Cfg<128, true>>(args, stream) : launch_cfg<Cfg<128, false>>(args, stream);
+  return cudaErrorInvalidValue;
+}
+
+cudaError_t launch_tree_attn_join(int head_dim, bool bf16, const gemm_tn_dev::TreeArgs& args, cudaStream_t stream) {
+  if (head_dim == 64) return bf16 ? launch_join<64, true>(args, stream) : launch_join<64, false>(args, stream);
+  if (head_dim == 128) return bf16 ? launch_join<128, true>(args, stream) : launch_join<128, false>(args, stream);
+  return cudaErrorInvalidValue;
+}
+
+}  // namespace gemm_tn_impl

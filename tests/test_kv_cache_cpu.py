@@ -1,0 +1,210 @@
+"""CPU tests of the paged cache's operators: the C ABI refuses bad arguments
+before it touches a device, the binding refuses tensors it cannot hand over, the
+tree masks, and the 64-bit reference of the GPU tests on closed forms."""
+from __future__ import annotations
+
+import ctypes
+import math
+
+import pytest
+import torch
+
+import dense_tiled_gemm_03_gb300 as gt
+from dense_tiled_gemm_03_gb300 import _cache
+import _cache_ref as ref
+
+
+@pytest.fixture(scope="module")
+def lib():
+    from dense_tiled_gemm_03_gb300 import build as native_build
+    native_build.build()
+    return gt.library()
+
+
+# Fake, well-separated addresses: validation never dereferences them.
+K, V, TABLE, LENS, Q, KN, VN, O, LSE, W, POS, SEEN, OUT = (0x100000000000 + 0x10000000000 * i for i in range(13))
+F16, BF16 = gt.GEMM_TN_F16, gt.GEMM_TN_BF16
+INVALID, MISALIGNED = gt.GEMM_TN_ERR_INVALID_VALUE, gt.GEMM_TN_ERR_MISALIGNED
+NO_DEVICE = (gt.GEMM_TN_ERR_UNSUPPORTED_DEVICE, gt.GEMM_TN_ERR_CUDA)
+
+
+def cache(**over):
+    """A valid cache: 100 pages of 16 rows of 2 heads of 64."""
+    f = dict(k=K, v=V, num_pages=100, page_size=16, kv_heads=2, head_dim=64, page_stride=2048, slot_stride=128,
+             head_stride=64, page_table=TABLE, table_stride=10, max_pages=10, lens=LENS, weight=W, pos=POS, seen=SEEN)
+    f.update(over)
+    return _cache.KvCacheStruct(**f)
+
+
+def rows(data=Q, b=4 * 8 * 64, t=8 * 64, h=64):
+    return _cache.KvRows(data, b, t, h)
+
+
+def ref_or_null(x):
+    return None if x is None else ctypes.byref(x)
+
+
+def attn(lib, dtype=BF16, batch=3, tokens=4, heads=8, c=cache(), q=rows(), kn=rows(KN, 512, 128), vn=rows(VN, 512, 128),
+         mask=None, token_lens=None, o=O, lse=LSE, scale=0.0):
+    return lib.tree_attn_fwd(dtype, batch, tokens, heads, ref_or_null(c), ref_or_null(q), ref_or_null(kn), ref_or_null(vn), mask,
+                             token_lens, o, lse, scale, None, None)
+
+
+def append(lib, dtype=BF16, batch=3, tokens=4, c=cache(), kn=rows(KN, 512, 128), vn=rows(VN, 512, 128), r=None, counts=None,
+           max_rows=4, lens_out=OUT, seen_out=None):
+    return lib.kv_cache_append(dtype, batch, tokens, ref_or_null(c), ref_or_null(kn), ref_or_null(vn), r, counts, max_rows,
+                               lens_out, seen_out, None, None)
+
+
+def weigh(lib, dtype=BF16, batch=3, tokens=4, heads=8, c=cache(), q=rows(), lse=LSE, r=None, counts=None, max_rows=4, causal=1,
+          scale=0.0, out=OUT):
+    return lib.kv_cache_weigh(dtype, batch, tokens, heads, ref_or_null(c), ref_or_null(q), lse, r, counts, max_rows, causal,
+                              scale, out, None, None)
+
+
+def evict(lib, dtype=BF16, batch=3, c=cache(), keep=50, recent=5, w=OUT, p=POS, lens_out=LENS):
+    return lib.kv_cache_evict(dtype, batch, ref_or_null(c), keep, recent, w, p, lens_out, None, None)
+
+
+def test_valid_calls_get_as_far_as_the_device(lib):
+    if torch.cuda.is_available():
+        pytest.skip("the addresses are not real")
+    for call in (attn, append, weigh, evict):
+        assert call(lib) in NO_DEVICE, call.__name__
+    assert attn(lib, kn=None, vn=None) in NO_DEVICE
+    assert attn(lib, lse=None, mask=0x1000, token_lens=0x2000) in NO_DEVICE
+    # a pool of [page][head][row] order, and one page, one head with strides nobody reads
+    assert attn(lib, c=cache(slot_stride=64, head_stride=1024)) in NO_DEVICE
+    assert attn(lib, c=cache(num_pages=1, page_stride=0, kv_heads=1, head_stride=0)) in NO_DEVICE
+    assert evict(lib, recent=0, p=None, c=cache(pos=None, seen=None)) in NO_DEVICE
+
+
+CACHE_FAULTS = [
+    (None, INVALID), (cache(k=None), INVALID), (cache(v=None), INVALID), (cache(page_table=None), INVALID),
+    (cache(lens=None), INVALID), (cache(head_dim=96), INVALID), (cache(kv_heads=0), INVALID), (cache(page_size=12), INVALID),
+    (cache(page_size=0), INVALID), (cache(page_size=200), INVALID), (cache(page_size=1 << 21), INVALID),
+    (cache(num_pages=0), INVALID), (cache(num_pages=2 ** 31), INVALID), (cache(max_pages=0), INVALID),
+    (cache(max_pages=2 ** 27), INVALID), (cache(table_stride=9), INVALID), (cache(page_stride=2047), INVALID),
+    (cache(slot_stride=-128), INVALID), (cache(slot_stride=0), INVALID), (cache(head_stride=0), INVALID),
+    (cache(head_stride=2 ** 39), INVALID), (cache(k=K + 2), MISALIGNED), (cache(v=V + 8), MISALIGNED),
+    (cache(lens=LENS + 2), MISALIGNED), (cache(page_table=TABLE + 1), MISALIGNED),
+]
+
+
+@pytest.mark.parametrize("fault,status", CACHE_FAULTS)
+@pytest.mark.parametrize("call", [attn, append, weigh, evict])
+def test_a_bad_cache_is_refused(lib, call, fault, status):
+    assert call(lib, c=fault) == status
+    assert gt.gemm_tn_last_error_message() != ""
+
+
+@pytest.mark.parametrize("call", [attn, append, weigh, evict])
+def test_types_and_sizes(lib, call):
+    assert call(lib, dtype=2) == gt.GEMM_TN_ERR_UNSUPPORTED_DTYPE
+    assert call(lib, batch=-1) == INVALID and call(lib, batch=2 ** 31) == INVALID
+    assert call(lib, batch=2 ** 31 - 1) == INVALID      # times kv_heads
+    assert call(lib, batch=0) == gt.GEMM_TN_OK
+
+
+@pytest.mark.parametrize("over,status", [
+    (dict(heads=7), INVALID), (dict(heads=2 * 129), INVALID), (dict(tokens=-1), INVALID), (dict(tokens=2 ** 31), INVALID),
+    (dict(scale=-1.0), INVALID), (dict(scale=float("nan")), INVALID), (dict(scale=float("inf")), INVALID),
+    (dict(q=None), INVALID), (dict(q=rows(None)), INVALID), (dict(q=rows(Q + 8)), MISALIGNED), (dict(q=rows(t=513)), INVALID),
+    (dict(q=rows(h=0)), INVALID), (dict(q=rows(b=-512)), INVALID), (dict(kn=None), INVALID), (dict(vn=None), INVALID),
+    (dict(kn=rows(KN, 512, 120)), gt.GEMM_TN_OK), (dict(vn=rows(VN, 512, 4)), INVALID), (dict(o=None), INVALID),
+    (dict(o=O + 8), MISALIGNED), (dict(lse=LSE + 2), MISALIGNED), (dict(mask=0x1004), MISALIGNED),
+    (dict(token_lens=0x1001), MISALIGNED), (dict(o=Q + 64), INVALID), (dict(o=K + 4096), INVALID), (dict(o=VN), INVALID),
+    (dict(kn=None, vn=None, mask=0x1000), INVALID)])
+def test_attention_refusals(lib, over, status):
+    rc = attn(lib, **over)
+    assert rc == status or (status == gt.GEMM_TN_OK and rc in NO_DEVICE)
+
+
+@pytest.mark.parametrize("over,status", [
+    (dict(tokens=-1), INVALID), (dict(max_rows=5), INVALID), (dict(max_rows=-1), INVALID), (dict(tokens=0, r=0x1000), INVALID),
+    (dict(lens_out=None), INVALID), (dict(c=cache(seen=None), seen_out=OUT), INVALID), (dict(r=0x1002), MISALIGNED),
+    (dict(counts=0x1001), MISALIGNED), (dict(kn=rows(K + 4096, 512, 128)), INVALID), (dict(vn=None), INVALID),
+    (dict(batch=2 ** 29, tokens=128, max_rows=128), INVALID)])
+def test_append_refusals(lib, over, status):
+    assert append(lib, **over) == status
+
+
+@pytest.mark.parametrize("over,status", [
+    (dict(heads=0), INVALID), (dict(heads=3), INVALID), (dict(max_rows=5), INVALID), (dict(tokens=0, r=0x1000), INVALID),
+    (dict(lse=None), INVALID), (dict(out=None), INVALID), (dict(c=cache(weight=None)), INVALID), (dict(out=OUT + 2), MISALIGNED),
+    (dict(r=0x1001), MISALIGNED), (dict(scale=-0.5), INVALID), (dict(max_rows=2 ** 23, r=0x1000), INVALID)])
+def test_weigh_refusals(lib, over, status):
+    assert weigh(lib, **over) == status
+
+
+@pytest.mark.parametrize("over,status", [
+    (dict(keep=-1), INVALID), (dict(keep=2 ** 31), INVALID), (dict(recent=-1), INVALID), (dict(recent=51), INVALID),
+    (dict(c=cache(pos=None), p=None), INVALID), (dict(c=cache(seen=None)), INVALID), (dict(p=None), INVALID),
+    (dict(c=cache(pos=None), recent=0), INVALID), (dict(c=cache(weight=None)), INVALID), (dict(w=None), INVALID),
+    (dict(lens_out=None), INVALID), (dict(lens_out=LENS + 1), MISALIGNED)])
+def test_evict_refusals(lib, over, status):
+    assert evict(lib, **over) == status
+
+
+def test_empty_calls_need_no_device(lib):
+    assert attn(lib, tokens=0) == gt.GEMM_TN_OK and attn(lib, heads=0) == gt.GEMM_TN_OK
+
+
+def test_the_binding_takes_cuda_tensors_only():
+    k = torch.zeros((2, 8, 1, 64), dtype=torch.float16)
+    with pytest.raises(ValueError, match="CUDA"):
+        gt.KVCache(k, k, torch.zeros((1, 2), dtype=torch.int32), torch.zeros(1, dtype=torch.int32))
+
+
+# ---------------------------------------------------------------- tree masks
+
+def test_tree_mask():
+    parents = torch.tensor([[-1, 0, 0, 1, 2, -1], [-1, 0, 1, 2, 3, 4]])
+    m = gt.tree_mask(parents)
+    assert m.shape == (2, 6, 1) and m.dtype == torch.int64
+    assert m[0, :, 0].tolist() == [0b1, 0b11, 0b101, 0b1011, 0b10101, 0b100000]
+    assert m[1, :, 0].tolist() == [2 ** (i + 1) - 1 for i in range(6)]
+    chain = torch.arange(-1, 129)[None]
+    see = ref.visible(130, gt.tree_mask(chain))
+    assert torch.equal(see, ref.visible(130)) and gt.tree_mask(chain).shape == (1, 130, 3)
+    assert gt.tree_mask(torch.zeros((2, 0), dtype=torch.int32)).shape == (2, 0, 0)
+
+
+@pytest.mark.parametrize("parents", [[[0]], [[-1, 1]], [[-2]], [[-1, 5]]])
+def test_tree_mask_refuses_parents_that_do_not_come_first(parents):
+    with pytest.raises(ValueError):
+        gt.tree_mask(torch.tensor(parents))
+
+
+def test_tree_mask_refuses_other_types():
+    for bad in (torch.zeros((1, 2)), torch.zeros(3, dtype=torch.int64), torch.zeros((1, 1), dtype=torch.bool)):
+        with pytest.raises(ValueError):
+            gt.tree_mask(bad)
+
+
+# ---------------------------------------------------------------- the reference
+
+def test_the_reference_on_closed_forms():
+    s = ref.make("bf16", 64, [20, 0], 3, 2, 2, 8, [3, 2], seed=1)
+    s.q.nan_to_num_(0.0)
+    s.q[:] = 0.0
+    o, lse, *_ = ref.attention(s)
+    assert abs(float(lse[0, 1, 0]) - math.log(22)) < 1e-12 and abs(float(lse[1, 0, 3])) < 1e-12
+    mean = torch.cat([s.rows_of(s.v, 0, 1, 20), s.v_new[0, :2, 1].double()]).mean(0)
+    assert torch.allclose(o[0, 1, 2], mean)
+    assert torch.isnan(lse[1, 2]).all() and not torch.isnan(o[0]).any()
+    w, _ = ref.weigh(s, torch.full((2, 3, 4), math.log(20.0)), None, [3, 0])
+    # three queries of two heads; the newest slot is seen by the last query alone
+    gain = (w - s.weight.double())[0, 0, :20]
+    assert torch.allclose(gain, torch.tensor([6.0] * 18 + [4.0, 2.0], dtype=torch.float64) / 20)
+
+
+def test_the_reference_evicts_the_lightest():
+    s = ref.make("bf16", 64, [6], 1, 1, 1, 8, seed=2)
+    s.weight[0, 0, :6] = torch.tensor([5.0, 1.0, 4.0, 1.0, 3.0, 0.0])
+    s.pos[0, 0] = torch.arange(8)
+    s.seen[0] = 6
+    k, v, weight, pos, lens = ref.evict(s, 4, 1)      # slot 5 is the newest; 0, 2, 4 the heaviest; 5, 4 fill 1, 3
+    assert lens.tolist() == [4] and pos[0, 0, :4].tolist() == [0, 4, 2, 5] and weight[0, 0, :4].tolist() == [5.0, 3.0, 4.0, 0.0]
+    page = int(s.table[0, 0])
+    assert torch.equal(k[page, 1], s.k[page, 4]) and torch.equal(v[page, 3], s.v[page, 5])

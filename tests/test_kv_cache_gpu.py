@@ -1,0 +1,615 @@
+"""GPU tests of the paged cache's operators (include/kv_cache.h) against a plain
+64-bit implementation: attention of new tokens over the cache, append,
+accumulated weights, eviction, and a run of them as a serving loop uses them.
+
+Whatever no result may depend on holds NaN: rows behind the last slot, unused
+pages, tokens behind the end of a sequence's own.
+"""
+from __future__ import annotations
+
+import math
+import time
+
+import pytest
+import torch
+
+import dense_tiled_gemm_03_gb300 as gt
+import _cache_ref as ref
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(autouse=True)
+def _gpu():
+    from _parity import require_gpu
+    require_gpu()
+
+
+DEV = "cuda:0"
+
+
+def on_gpu(s: ref.Setup, **over):
+    """The cache on the GPU (own copies of everything), and the status word."""
+    t = dict(k=s.k, v=s.v, page_table=s.table, lens=s.lens, weight=s.weight, pos=s.pos, seen=s.seen)
+    t.update(over)
+    t = {n: None if x is None else x.to(DEV).clone() for n, x in t.items()}
+    return gt.KVCache(**t), torch.zeros(1, dtype=torch.int32, device=DEV)
+
+
+def run_attn(s: ref.Setup, mask=None, use_new=True, scale=None, fill=7.0, cache=None):
+    status = torch.zeros(1, dtype=torch.int32, device=DEV)
+    if cache is None:
+        cache, status = on_gpu(s)
+    out = torch.full(s.q.shape, fill, dtype=s.dtype, device=DEV)
+    lse = torch.full(s.q.shape[:3], fill, device=DEV)
+    kn, vn = (s.k_new.to(DEV), s.v_new.to(DEV)) if use_new else (None, None)
+    gt.tree_attn(s.q.to(DEV), cache, kn, vn, mask=None if mask is None else mask.to(DEV),
+                 token_lens=s.token_lens.to(DEV), scale=scale, out=out, lse=lse, status=status)
+    torch.cuda.synchronize()
+    assert int(status.item()) == 0
+    return out.cpu(), lse.cpu()
+
+
+def random_mask(batch, tokens, seed, empty_row=False):
+    """Any mask: not a tree, some rows see nothing, bits behind the end set."""
+    g = torch.Generator().manual_seed(seed)
+    words = (tokens + 63) // 64
+    m = torch.randint(-2 ** 63, 2 ** 63 - 1, (batch, tokens, words), generator=g, dtype=torch.int64)
+    if empty_row:
+        m[:, tokens // 2] = 0
+    return m
+
+
+def random_tree(batch, tokens, seed):
+    g = torch.Generator().manual_seed(seed)
+    return torch.stack([torch.stack([torch.tensor(-1) if i == 0 else torch.randint(-1, i, (), generator=g)
+                                     for i in range(tokens)]) for _ in range(batch)])
+
+
+# lens, tokens, kv_heads, group, page, token_lens
+SHAPES = [
+    ([1], 1, 1, 1, 8, None),
+    ([0, 5], 1, 2, 1, 8, None),
+    ([127, 128, 129], 1, 2, 4, 16, None),
+    ([300, 0, 1, 640], 2, 1, 8, 64, [2, 1, 0, 2]),
+    ([255, 257], 7, 3, 3, 32, [7, 4]),
+    ([1000], 16, 2, 7, 128, None),
+    ([513, 90], 33, 1, 4, 256, [33, 17]),          # two row tiles: pair mode
+    ([40, 200], 65, 2, 2, 16, [64, 65]),           # 130 rows
+    ([70], 130, 1, 1, 8, None),
+    ([0, 0], 200, 2, 3, 32, [200, 129]),           # the new tokens alone
+    ([2500, 31], 3, 2, 128, 64, [3, 2]),           # one token per row tile
+]
+
+
+@pytest.mark.parametrize("dtype", ["fp16", "bf16"])
+@pytest.mark.parametrize("dim", [64, 128])
+@pytest.mark.parametrize("kind", ["chain", "mask", "cache_only"])
+@pytest.mark.parametrize("shape", SHAPES, ids=lambda s: "len{}_t{}_h{}x{}_p{}".format("-".join(map(str, s[0])), *s[1:5]))
+def test_attention(shape, kind, dim, dtype):
+    lens, tokens, kv_heads, group, page, token_lens = shape
+    s = ref.make(dtype, dim, lens, tokens, kv_heads, group, page, token_lens, seed=tokens + dim)
+    mask = random_mask(len(lens), tokens, seed=tokens, empty_row=True) if kind == "mask" else None
+    out, lse = run_attn(s, mask, use_new=kind != "cache_only")
+    ref.check_attention(out, lse, ref.attention(s, mask, use_new=kind != "cache_only"), s, 7.0)
+
+
+@pytest.mark.parametrize("tokens", [1, 26, 64, 97])
+def test_attention_of_drafted_trees(tokens):
+    s = ref.make("bf16", 128, [333, 1200, 64], tokens, 2, 4, 32, seed=tokens)
+    mask = gt.tree_mask(random_tree(3, tokens, seed=tokens))
+    out, lse = run_attn(s, mask)
+    ref.check_attention(out, lse, ref.attention(s, mask), s, 7.0)
+
+
+def test_many_short_sequences_and_one_long():
+    """Ragged lengths: chunks that hold many items, and an item cut many times."""
+    lens = [1 + 37 * i % 211 for i in range(70)] + [20000]
+    s = ref.make("bf16", 64, lens, 2, 1, 2, 16, [1 + i % 2 for i in range(71)], seed=3, max_pages=1250)
+    out, lse = run_attn(s)
+    ref.check_attention(out, lse, ref.attention(s), s, 7.0)
+
+
+def test_long_chunk_over_a_cache():
+    """The next tokens of a prompt: several row tiles and key tiles, the causal chain across them."""
+    s = ref.make("fp16", 64, [500, 77], 700, 1, 2, 64, [700, 389], seed=5)
+    out, lse = run_attn(s)
+    ref.check_attention(out, lse, ref.attention(s), s, 7.0)
+
+
+def test_scale_and_wide_scores():
+    """A given scale; scores that rise along the keys, so that references move many times."""
+    s = ref.make("fp16", 64, [900], 4, 2, 2, 64, seed=6, q_scale=4.0)
+    page = s.table[0].long()
+    ramp = torch.linspace(0.1, 3.0, 15 * 64).view(15, 64, 1, 1)
+    s.k[page] = (s.k[page].float() * ramp).to(s.dtype)
+    for scale in (None, 0.05, 0.4):
+        out, lse = run_attn(s, scale=scale)
+        ref.check_attention(out, lse, ref.attention(s, scale=scale), s, 7.0)
+
+
+def test_scores_far_below_the_first_tiles():
+    """Keys whose scores drop by hundreds behind the first tile, and the other way round."""
+    s = ref.make("bf16", 64, [400], 3, 1, 4, 16, seed=8, q_scale=0.25)
+    q = s.q.float()
+    q[..., 0] = 40.0
+    s.q = q.to(s.dtype)
+    for first, rest in ((8.0, -8.0), (-8.0, 8.0)):
+        k = s.k.float()
+        page = s.table[0].long()
+        k[page, :, :, 0] = rest
+        k[page[:8], :, :, 0] = first
+        s.k = k.to(s.dtype)
+        out, lse = run_attn(s)
+        ref.check_attention(out, lse, ref.attention(s), s, 7.0)
+
+
+def test_pool_and_input_layouts():
+    """[page][head][row] pools, K and V in one tensor, q, k, v side by side in one projection."""
+    s = ref.make("bf16", 128, [200, 131], 5, 4, 2, 16, [5, 3], seed=9)
+    want = ref.attention(s)
+    pools = torch.empty((s.k.shape[0], 2, 4, 16, 128), dtype=s.dtype, device=DEV)
+    pools[:, 0] = s.k.permute(0, 2, 1, 3).to(DEV)
+    pools[:, 1] = s.v.permute(0, 2, 1, 3).to(DEV)
+    cache = gt.KVCache(pools[:, 0].permute(0, 2, 1, 3), pools[:, 1].permute(0, 2, 1, 3), s.table.to(DEV), s.lens.to(DEV))
+    qkv = torch.cat([s.q, s.k_new, s.v_new], 2).to(DEV)
+    out = torch.full(s.q.shape, 7.0, dtype=s.dtype, device=DEV)
+    gt.tree_attn(qkv[:, :, :8], cache, qkv[:, :, 8:12], qkv[:, :, 12:], token_lens=s.token_lens.to(DEV), out=out)
+    ref.check_attention(out.cpu(), None, want, s, 7.0)
+
+
+def test_page_offsets_past_32_bits():
+    """A pool whose used pages lie more than 2^32 elements apart."""
+    s = ref.make("bf16", 128, [1000], 4, 8, 2, 128, seed=10)
+    far = 4300
+    pages = 33000
+    pool = torch.empty((2, pages, 128, 8, 128), dtype=s.dtype, device=DEV)   # 2 x 8.65 GB: 4.3e9 elements each
+    where = torch.tensor([0, far, 2 * far, 7 * far, 32999, 5, 32998, 32771])[:s.table.shape[1]]
+    for dst, src in ((pool[0], s.k), (pool[1], s.v)):
+        dst[where.to(DEV)] = src[s.table[0].long()].to(DEV)
+    cache = gt.KVCache(pool[0], pool[1], where[None].to(torch.int32).to(DEV), s.lens.to(DEV))
+    out, lse = run_attn(s, cache=cache)
+    ref.check_attention(out, lse, ref.attention(s), s, 7.0)
+    gt.cache_append(cache, s.k_new.to(DEV)[:, :1], s.v_new.to(DEV)[:, :1])
+    assert ref.same(pool[0, 32771, 1000 % 128].cpu(), s.k_new[0, 0])
+
+
+def test_repeated_calls_are_bit_identical():
+    s = ref.make("bf16", 128, [3000, 170, 901], 9, 2, 4, 32, seed=11)
+    a, b = run_attn(s), run_attn(s)
+    assert ref.same(a[0], b[0]) and ref.same(a[1], b[1])
+
+
+def test_lengths_on_the_device_are_clamped():
+    """Lengths and counts past what the arrays hold, and negative ones."""
+    s = ref.make("bf16", 64, [64, 32], 4, 1, 2, 16, [4, 3], seed=12, max_pages=4)
+    want = ref.attention(s)
+    cache, _ = on_gpu(s, lens=torch.tensor([1000, 32], dtype=torch.int32))
+    s.token_lens = torch.tensor([2 ** 31 - 1, 3], dtype=torch.int32)
+    out, _ = run_attn(s, cache=cache)
+    s.token_lens = torch.tensor([4, 3], dtype=torch.int32)
+    ref.check_attention(out, None, want, s, 7.0)
+    cache, _ = on_gpu(s, lens=torch.tensor([-5, -2 ** 31], dtype=torch.int32))
+    s.token_lens = torch.tensor([4, -1], dtype=torch.int32)
+    out, lse = run_attn(s, cache=cache)
+    s.lens, s.token_lens = torch.tensor([0, 0]), torch.tensor([4, 0])
+    ref.check_attention(out, lse, ref.attention(s), s, 7.0)
+
+
+def test_page_numbers_out_of_range_are_reported_and_not_followed():
+    s = ref.make("bf16", 64, [100, 100], 1, 1, 1, 16, seed=13)
+    for bad in (-1, s.k.shape[0], 2 ** 31 - 1):
+        s2 = ref.make("bf16", 64, [100, 100], 1, 1, 1, 16, seed=13)
+        s2.table[0, 3] = bad
+        cache, status = on_gpu(s2)
+        out = torch.zeros(s2.q.shape, dtype=s2.dtype, device=DEV)
+        lse = torch.zeros(s2.q.shape[:3], device=DEV)
+        gt.tree_attn(s2.q.to(DEV), cache, out=out, lse=lse, status=status)
+        torch.cuda.synchronize()
+        assert int(status.item()) == gt.GEMM_TN_ERR_INVALID_VALUE
+        want = ref.attention(s, use_new=False)
+        s_other = ref.Setup(**{**s.__dict__})
+        ref.check_attention(out.cpu()[1:], lse.cpu()[1:], tuple(t[1:] for t in want), s_other, 0.0)
+        for call in (lambda: gt.cache_weigh(cache, s2.q.to(DEV), lse, status=status),
+                     lambda: gt.cache_evict(cache, 40, status=status)):
+            status.zero_()
+            call()
+            torch.cuda.synchronize()
+            assert int(status.item()) == gt.GEMM_TN_ERR_INVALID_VALUE
+
+
+# ---------------------------------------------------------------- append
+
+@pytest.mark.parametrize("in_place", [False, True])
+@pytest.mark.parametrize("dim,kv_heads,page", [(64, 1, 8), (128, 3, 16), (64, 8, 128)])
+def test_append(dim, kv_heads, page, in_place):
+    tokens, lens, counts = 9, [0, 7, 16, 100, 33], [9, 0, 1, 5, 4]
+    s = ref.make("bf16", dim, lens, tokens, kv_heads, 2, page, seed=20, max_pages=-(-140 // page))
+    g = torch.Generator().manual_seed(1)
+    s.table = torch.randperm(s.k.shape[0], generator=g)[:s.table.numel()].view(s.table.shape).to(torch.int32)
+    rows = torch.stack([torch.randperm(tokens, generator=g) for _ in lens]).to(torch.int32)
+    rows[3, 1] = rows[3, 0]                      # the same token twice
+    s.seen = torch.tensor([50, 7, 99, 1000, 0], dtype=torch.int32)
+    k, v, weight, pos = s.k.clone(), s.v.clone(), s.weight.clone(), s.pos.clone()
+    for b, n in enumerate(counts):
+        for i in range(n):
+            slot = lens[b] + i
+            page_no = int(s.table[b, slot // page])
+            k[page_no, slot % page] = s.k_new[b, int(rows[b, i])]
+            v[page_no, slot % page] = s.v_new[b, int(rows[b, i])]
+            weight[b, :, slot] = 0
+            pos[b, :, slot] = s.seen[b] + i
+    cache, status = on_gpu(s)
+    new = torch.tensor(counts, dtype=torch.int32)
+    lens_out, seen_out = (None, None) if in_place else (torch.zeros(5, dtype=torch.int32, device=DEV) for _ in range(2))
+    gt.cache_append(cache, s.k_new.to(DEV), s.v_new.to(DEV), counts=new.to(DEV), rows=rows.to(DEV), lens_out=lens_out,
+                    seen_out=seen_out, status=status)
+    torch.cuda.synchronize()
+    assert int(status.item()) == 0
+    for got, want in ((cache.k, k), (cache.v, v), (cache.weight, weight), (cache.pos, pos),
+                      (cache.lens if in_place else lens_out, s.lens + new),
+                      (cache.seen if in_place else seen_out, s.seen + new)):
+        assert ref.same(got.cpu(), want)
+    if not in_place:
+        assert torch.equal(cache.lens.cpu(), s.lens) and torch.equal(cache.seen.cpu(), s.seen)
+
+
+def test_append_without_rows_and_statistics():
+    s = ref.make("fp16", 64, [3, 0], 40, 2, 1, 8, seed=21, max_pages=6)
+    s.table = torch.arange(12, dtype=torch.int32).view(2, 6)
+    cache, status = on_gpu(s, weight=None, pos=None, seen=None)
+    gt.cache_append(cache, s.k_new.to(DEV), s.v_new.to(DEV), status=status)
+    assert cache.lens.tolist() == [43, 40] and int(status.item()) == 0
+    s.lens = torch.tensor([43, 40])
+    for b, at in ((0, 3), (1, 0)):
+        for h in range(2):
+            assert torch.equal(s.rows_of(cache.k.cpu(), b, h, at + 40)[at:], s.k_new[b, :, h].double())
+            assert torch.equal(s.rows_of(cache.v.cpu(), b, h, at + 40)[at:], s.v_new[b, :, h].double())
+
+
+def test_append_past_the_capacity_and_from_rows_out_of_range():
+    s = ref.make("fp16", 64, [14, 2], 4, 1, 1, 8, seed=22, max_pages=2)
+    s.table = torch.tensor([[2, 1], [0, 4]], dtype=torch.int32)
+    cache, status = on_gpu(s)
+    before = cache.k.clone()
+    gt.cache_append(cache, s.k_new.to(DEV), s.v_new.to(DEV), status=status)
+    torch.cuda.synchronize()
+    assert int(status.item()) == gt.GEMM_TN_ERR_INVALID_VALUE and cache.lens.tolist() == [16, 6]
+    assert ref.same(cache.k[1, 6:8].cpu(), s.k_new[0, :2])          # the two that fit
+    assert ref.same(cache.k[0, 2:6].cpu(), s.k_new[1])
+    assert ref.same(cache.k[[3, 5]], before[[3, 5]])
+    status.zero_()
+    rows = torch.tensor([[0], [4]], dtype=torch.int32, device=DEV)
+    out = torch.zeros(2, dtype=torch.int32, device=DEV)
+    at = cache.k[0, 6].clone()
+    gt.cache_append(cache, s.k_new.to(DEV), s.v_new.to(DEV), rows=rows, lens_out=out,
+                    counts=torch.tensor([0, 1], dtype=torch.int32, device=DEV), status=status)
+    torch.cuda.synchronize()
+    assert int(status.item()) == gt.GEMM_TN_ERR_INVALID_VALUE and ref.same(cache.k[0, 6], at)
+
+
+# ---------------------------------------------------------------- accumulated weights
+
+# lens, tokens, kv_heads, group, page, counts
+WEIGH = [
+    ([1], 1, 1, 1, 8, None),
+    ([5, 0, 128], 1, 2, 4, 16, None),
+    ([300, 129], 9, 1, 8, 64, [9, 4]),
+    ([700, 64], 32, 2, 8, 32, [32, 7]),          # 256 rows: one full block
+    ([513, 900], 70, 1, 7, 128, [70, 33]),       # several blocks of rows
+    ([260], 3, 1, 128, 256, None),               # two tokens per block
+    ([90, 40], 5, 3, 3, 8, [0, 5]),              # no row counts: the weights come back
+]
+
+
+@pytest.mark.parametrize("dtype", ["fp16", "bf16"])
+@pytest.mark.parametrize("dim", [64, 128])
+@pytest.mark.parametrize("causal", [True, False])
+@pytest.mark.parametrize("shape", WEIGH, ids=lambda s: "len{}_t{}_h{}x{}_p{}".format("-".join(map(str, s[0])), *s[1:5]))
+def test_weigh(shape, causal, dim, dtype):
+    lens, tokens, kv_heads, group, page, counts = shape
+    counts = [min(tokens, n) for n in lens] if counts is None else counts
+    s = ref.make(dtype, dim, lens, tokens, kv_heads, group, page, seed=tokens + dim)
+    g = torch.Generator().manual_seed(2)
+    rows = torch.stack([torch.randperm(tokens, generator=g) for _ in lens]).to(torch.int32)
+    lse = torch.rand(s.q.shape[:3], generator=g) * 3 + math.log(max(max(lens), 2)) + 1.0
+    for b, n in enumerate(counts):               # tokens that do not count
+        for i in rows[b, n:].tolist():
+            s.q[b, i] = float("nan")
+            lse[b, i] = float("nan")
+    want, tol = ref.weigh(s, lse, rows, counts, causal)
+    cache, status = on_gpu(s)
+    out = torch.full_like(cache.weight, 5.0)
+    got = gt.cache_weigh(cache, s.q.to(DEV), lse.to(DEV), counts=torch.tensor(counts, dtype=torch.int32, device=DEV),
+                         rows=rows.to(DEV), causal=causal, out=out, status=status)
+    torch.cuda.synchronize()
+    assert got is out and int(status.item()) == 0
+    assert ref.same(cache.weight.cpu(), s.weight)
+    live = torch.arange(out.shape[2])[None, None, :] < s.lens[:, None, None]
+    live = live.expand(out.shape)
+    off = (out.cpu().double() - want).abs()
+    assert bool((off[live] <= tol[live]).all()), float((off - tol)[live].max())
+    assert (out.cpu()[~live] == 5.0).all()
+    gt.cache_weigh(cache, s.q.to(DEV), lse.to(DEV), counts=torch.tensor(counts, dtype=torch.int32, device=DEV),
+                   rows=rows.to(DEV), causal=causal, status=status)
+    assert ref.same(cache.weight.cpu()[live], out.cpu()[live]), "in place: the same sums"
+    assert ref.same(cache.weight.cpu()[~live], s.weight[~live])
+
+
+def test_weights_of_one_pass_sum_to_the_rows():
+    """With the attention's own lse every counted row's weights over the slots sum to one."""
+    s = ref.make("bf16", 128, [2000, 333], 6, 2, 4, 64, seed=30)
+    cache, status = on_gpu(s, weight=torch.zeros_like(s.weight))
+    q = s.q.to(DEV)
+    lse = torch.zeros(s.q.shape[:3], device=DEV)
+    gt.tree_attn(q, cache, lse=lse, status=status)
+    gt.cache_weigh(cache, q, lse, causal=False, status=status)
+    total = cache.weight.double().cpu()
+    for b in range(2):
+        got = total[b, :, :int(s.lens[b])].sum(1)
+        # 24 rows; each sum of probabilities is off by the scores' errors (amp < 40: 130 * 2^-23 * 40 < 1e-3)
+        assert (got - 24.0).abs().max().item() < 24 * 1e-3
+    assert int(status.item()) == 0
+
+
+# ---------------------------------------------------------------- evict
+
+@pytest.mark.parametrize("recent", [0, 5])
+@pytest.mark.parametrize("in_place", [False, True])
+@pytest.mark.parametrize("lens,keep,page,dim,kv_heads", [
+    ([1, 9], 8, 8, 64, 1), ([40, 41, 200, 0], 40, 16, 128, 3), ([300, 130], 129, 64, 64, 2),
+    ([2049, 1500], 1024, 128, 64, 1), ([33], 5, 8, 128, 2), ([1200], 1199, 32, 64, 1)])
+def test_evict(lens, keep, page, dim, kv_heads, in_place, recent):
+    s = ref.make("bf16", dim, lens, 1, kv_heads, 1, page, seed=keep)
+    check_evict(s, keep, recent, in_place)
+
+
+def check_evict(s, keep, recent, in_place):
+    k, v, weight, pos, lens = ref.evict(s, keep, recent)
+    cache, status = on_gpu(s)
+    outs = [None] * 3 if in_place else [torch.full_like(t, 3) for t in (cache.weight, cache.pos, cache.lens)]
+    gt.cache_evict(cache, keep, recent, *outs, status=status)
+    torch.cuda.synchronize()
+    assert int(status.item()) == 0
+    assert ref.same(cache.k.cpu(), k) and ref.same(cache.v.cpu(), v)
+    got = [cache.weight, cache.pos, cache.lens] if in_place else outs
+    assert torch.equal(got[2].cpu(), lens)
+    written = (torch.arange(weight.shape[2])[None, None, :] < lens[:, None, None]).expand(weight.shape)
+    for x, want, old in ((got[0].cpu(), weight, s.weight), (got[1].cpu(), pos, s.pos)):
+        assert ref.same(x[written], want[written])
+        assert ref.same(x[~written], old[~written] if in_place else torch.full_like(old, 3)[~written])
+    if not in_place:
+        assert ref.same(cache.weight.cpu(), s.weight) and ref.same(cache.pos.cpu(), s.pos)
+
+
+@pytest.mark.parametrize("keep", [0, 1, 63, 64])
+def test_evict_ties_and_odd_weights(keep):
+    """Equal weights keep the lowest slots; zeros of both signs are equal; infinities, NaN, negative and denormal values."""
+    s = ref.make("fp16", 64, [100, 97], 1, 1, 1, 16, seed=40)
+    odd = torch.tensor([0.0, -0.0, float("inf"), -float("inf"), float("nan"), 1.0, 1.0, -2.5, 1e-42, -1e-42, 3e38])
+    g = torch.Generator().manual_seed(3)
+    s.weight = odd[torch.randint(0, len(odd), s.weight.shape, generator=g)]
+    check_evict(s, keep, 0, False)
+    check_evict(s, keep, min(keep, 10), True)
+
+
+def test_evict_a_sequence_longer_than_shared_memory_holds():
+    s = ref.make("fp16", 64, [50000], 1, 1, 1, 128, seed=41)
+    check_evict(s, 20001, 100, False)
+
+
+def test_evict_without_positions():
+    s = ref.make("fp16", 64, [60], 1, 2, 1, 16, seed=42)
+    k, v, weight, _, lens = ref.evict(s, 30, 0)
+    cache, status = on_gpu(s, pos=None, seen=None)
+    gt.cache_evict(cache, 30, status=status)
+    assert ref.same(cache.k.cpu(), k) and ref.same(cache.v.cpu(), v) and cache.lens.tolist() == [30]
+    assert ref.same(cache.weight.cpu()[:, :, :30], weight[:, :, :30]) and int(status.item()) == 0
+
+
+# ---------------------------------------------------------------- together
+
+def serve(s: ref.Setup, steps, seed, capture=False):
+    """A serving loop: drafted trees attended, the accepted path appended, its
+    weights added, the cache cut to its budget; everything on the device."""
+    cache, status = on_gpu(s, weight=torch.zeros_like(s.weight))
+    g = torch.Generator().manual_seed(seed)
+    batch, tokens, heads, dim = s.q.shape
+    q, kn, vn = torch.empty_like(s.q, device=DEV), torch.empty_like(s.k_new, device=DEV), torch.empty_like(s.v_new, device=DEV)
+    mask = torch.zeros((batch, tokens, 1), dtype=torch.int64, device=DEV)
+    rows = torch.zeros((batch, tokens), dtype=torch.int32, device=DEV)
+    counts = torch.zeros(batch, dtype=torch.int32, device=DEV)
+    out, lse = torch.zeros_like(q), torch.zeros((batch, tokens, heads), device=DEV)
+
+    def step():
+        gt.tree_attn(q, cache, kn, vn, mask=mask, out=out, lse=lse, status=status)
+        gt.cache_append(cache, kn, vn, counts=counts, rows=rows, status=status)
+        gt.cache_weigh(cache, q, lse, counts=counts, rows=rows, status=status)
+        gt.cache_evict(cache, 150, 20, status=status)
+
+    graph = None
+    seen = []
+    for n in range(steps):
+        parents = random_tree(batch, tokens, seed=seed + n)
+        path = torch.zeros((batch, tokens), dtype=torch.int32)
+        length = torch.zeros(batch, dtype=torch.int32)
+        for b in range(batch):
+            at, line = int(torch.randint(0, tokens, (), generator=g)), []
+            while at >= 0:
+                line.append(at)
+                at = int(parents[b, at])
+            path[b, :len(line)] = torch.tensor(line[::-1], dtype=torch.int32)
+            length[b] = len(line)
+        inputs = [(q, torch.randn(q.shape, generator=g).to(s.dtype)), (kn, torch.randn(kn.shape, generator=g).to(s.dtype)),
+                  (vn, torch.randn(vn.shape, generator=g).to(s.dtype)), (mask, gt.tree_mask(parents)), (rows, path),
+                  (counts, length)]
+        for dst, src in inputs:
+            dst.copy_(src)
+        if capture and n == 1:
+            torch.cuda.synchronize()
+            graph = torch.cuda.CUDAGraph()
+            with torch.cuda.graph(graph):
+                step()
+        if graph is not None:
+            graph.replay()
+        else:
+            step()
+        torch.cuda.synchronize()
+        assert int(status.item()) == 0
+        seen.append([t.cpu().clone() for t in (out, lse, cache.k, cache.v, cache.weight, cache.pos, cache.lens, cache.seen)] +
+                    [x[1] for x in inputs])
+    return seen
+
+
+def serving_setup():
+    s = ref.make("bf16", 64, [140, 3, 90], 12, 2, 2, 16, seed=50, max_pages=14)
+    # every sequence gets all the pages it can grow into; what the slots in use held moves along
+    rows = [[s.rows_of(pool, b, h, int(s.lens[b])).to(s.dtype) for pool in (s.k, s.v)] for b in range(3) for h in range(2)]
+    s.table = torch.randperm(s.k.shape[0], generator=torch.Generator().manual_seed(51))[:42].view(3, 14).to(torch.int32)
+    s.k.fill_(float("nan"))
+    s.v.fill_(float("nan"))
+    for b in range(3):
+        for h in range(2):
+            at = torch.arange(int(s.lens[b]))
+            for pool, x in zip((s.k, s.v), rows[2 * b + h]):
+                pool[s.table[b].long()[at // 16], at % 16, h] = x
+    s.pos = torch.arange(s.pos.shape[2], dtype=torch.int32).expand(s.pos.shape).contiguous()
+    s.seen = s.lens.clone()
+    return s
+
+
+def test_a_serving_loop():
+    """Each step of the loop against the 64-bit operators run on the state that the step before left."""
+    s = serving_setup()
+    state = ref.Setup(**{**s.__dict__})
+    state.weight = torch.zeros_like(s.weight)
+    for out, lse, k, v, weight, pos, lens, seen, q, kn, vn, mask, rows, counts in serve(s, 6, seed=52):
+        state.q, state.k_new, state.v_new = q, kn, vn
+        state.token_lens = torch.full((3,), 12, dtype=torch.int32)
+        ref.check_attention(out, lse, ref.attention(state, mask), state, 0.0)
+        for b in range(3):
+            for i in range(int(counts[b])):
+                slot = int(state.lens[b]) + i
+                page = int(state.table[b, slot // 16])
+                state.k[page, slot % 16], state.v[page, slot % 16] = kn[b, rows[b, i]], vn[b, rows[b, i]]
+                state.weight[b, :, slot], state.pos[b, :, slot] = 0.0, state.seen[b] + i
+        state.lens, state.seen = state.lens + counts, state.seen + counts
+        want, tol = ref.weigh(state, lse, rows, counts)
+        # the sums differ by rounding, so which slots go is taken from the kernel's own weights
+        long = state.lens > 150
+        assert torch.equal(lens, torch.where(long, 150, state.lens).to(torch.int32)) and torch.equal(seen, state.seen)
+        for b in range(3):
+            for h in range(2):
+                n = int(lens[b])
+                where = {int(p): i for i, p in enumerate(state.pos[b, h, :int(state.lens[b])])}
+                at = torch.tensor([where[int(p)] for p in pos[b, h, :n]])
+                assert len(set(at.tolist())) == n
+                assert bool(((weight[b, h, :n].double() - want[b, h, at]).abs() <= tol[b, h, at]).all())
+                if bool(long[b]):
+                    gone = sorted(set(range(int(state.lens[b]))) - set(at.tolist()))
+                    newest = state.pos[b, h, gone] >= state.seen[b] - 20
+                    assert not newest.any()
+                    old = [i for i in at.tolist() if int(state.pos[b, h, i]) < int(state.seen[b]) - 20]
+                    assert float((want - tol)[b, h, gone].max()) <= float((want + tol)[b, h, old].min())
+                for pool, got in ((state.k, k), (state.v, v)):
+                    assert torch.equal(state.rows_of(got, b, h, n), state.rows_of(pool, b, h, int(state.lens[b]))[at])
+        state.k, state.v, state.weight, state.pos, state.lens, state.seen = k, v, weight, pos, lens, seen
+
+
+def test_a_serving_loop_in_a_graph():
+    """The same loop with the steps from the second on replayed from one capture, to the bit."""
+    a, b = serve(serving_setup(), 5, seed=53), serve(serving_setup(), 5, seed=53, capture=True)
+    for x, y in zip(a, b):
+        for p, q in zip(x, y):
+            assert ref.same(p, q)
+
+
+def test_two_streams_at_once_and_two_graphs_in_turn():
+    """Workspaces are each call's own: calls in flight on two streams, and two captures replayed over one another."""
+    s1 = ref.make("bf16", 128, [4000, 1500], 4, 2, 4, 64, seed=60)
+    s2 = ref.make("fp16", 64, [2500, 3, 700], 20, 1, 8, 16, seed=61)
+    want = [run_attn(s) for s in (s1, s2)]
+    args = []
+    for s in (s1, s2):
+        cache, status = on_gpu(s)
+        out, lse = torch.full(s.q.shape, 7.0, dtype=s.dtype, device=DEV), torch.full(s.q.shape[:3], 7.0, device=DEV)
+        args.append((s.q.to(DEV), cache, s.k_new.to(DEV), s.v_new.to(DEV), out, lse, status))
+
+    def call(a):
+        q, cache, kn, vn, out, lse, status = a
+        gt.tree_attn(q, cache, kn, vn, out=out, lse=lse, status=status)
+
+    def check():
+        torch.cuda.synchronize()
+        for a, w in zip(args, want):
+            assert ref.same(a[4].cpu(), w[0]) and ref.same(a[5].cpu(), w[1]) and int(a[6].item()) == 0
+            a[4].fill_(float("nan"))
+            a[5].fill_(float("nan"))
+        torch.cuda.synchronize()
+
+    streams = [torch.cuda.Stream() for _ in args]
+    torch.cuda.synchronize()
+    for _ in range(10):
+        for a, st in zip(args, streams):
+            with torch.cuda.stream(st):
+                call(a)
+    check()
+    graphs = []
+    for a in args:
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            call(a)
+        graphs.append(graph)
+    for _ in range(3):
+        for graph in graphs:
+            graph.replay()
+    check()
+    for graph, st in zip(graphs, streams):
+        with torch.cuda.stream(st):
+            graph.replay()
+    check()
+
+
+def test_watchdog_reports_a_timeout_and_the_context_survives():
+    """The first CTA's producer skips one copy (test hook), so a bounded wait expires."""
+    from _parity import env_var
+    s = ref.make("bf16", 128, [3000], 2, 2, 4, 64, seed=62)
+    cache, status = on_gpu(s)
+    q, lse = s.q.to(DEV), torch.zeros(s.q.shape[:3], device=DEV)
+    for call in (lambda: gt.tree_attn(q, cache, s.k_new.to(DEV), s.v_new.to(DEV), status=status),
+                 lambda: gt.cache_weigh(cache, q, lse, out=torch.zeros_like(cache.weight), status=status)):
+        status.zero_()
+        t0 = time.perf_counter()
+        with env_var("GEMM_TN_WATCHDOG_MS", "200"), env_var("GEMM_TN_TEST_DROP_LOAD", "0"):
+            call()
+            torch.cuda.synchronize()
+        assert int(status.item()) == gt.GEMM_TN_ERR_TIMEOUT and time.perf_counter() - t0 < 5.0
+    out, lse = run_attn(s)
+    ref.check_attention(out, lse, ref.attention(s), s, 7.0)
+
+
+def test_empty_calls():
+    s = ref.make("bf16", 64, [5], 2, 1, 1, 8, seed=63)
+    cache, status = on_gpu(s)
+    q = torch.zeros((1, 0, 1, 64), dtype=s.dtype, device=DEV)
+    assert gt.tree_attn(q, cache).shape == q.shape
+    gt.cache_append(cache, q, q, status=status)
+    assert cache.lens.tolist() == [5]
+    before = cache.weight.clone()
+    gt.cache_weigh(cache, q, torch.zeros((1, 0, 1), device=DEV), status=status)
+    gt.cache_evict(cache, 5, status=status)
+    assert ref.same(cache.weight, before) and cache.lens.tolist() == [5] and int(status.item()) == 0
+
+
+def test_the_cache_continues_a_prompts_attention():
+    """flash_attn over a prompt gives what tree_attn gives for its last tokens over a cache of the others."""
+    from dense_tiled_gemm_03_gb300.workloads import make_qkv
+    q, k, v = (t.to(DEV) for t in make_qkv(2, 300, 2, 64, "bf16", seed=64))
+    full = gt.flash_attn(q, k, v, causal=True)
+    pool_k = torch.zeros((2 * 16, 16, 2, 64), dtype=k.dtype, device=DEV)
+    cache = gt.KVCache(pool_k, torch.zeros_like(pool_k), torch.arange(32, dtype=torch.int32, device=DEV).view(2, 16),
+                       torch.zeros(2, dtype=torch.int32, device=DEV))
+    gt.cache_append(cache, k[:, :250].contiguous(), v[:, :250].contiguous())
+    part = gt.tree_attn(q[:, 250:], cache, k[:, 250:], v[:, 250:])
+    # both round their probabilities (2^-9 of the mean |v| <= 4) and their outputs
+    assert (part.float() - full[:, 250:].float()).abs().max().item() <= 2 * (2.0 ** -9 * 4 + 2.0 ** -9 * 4)
