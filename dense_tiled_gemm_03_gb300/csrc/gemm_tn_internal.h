@@ -39,8 +39,9 @@ struct TreeArgs {
   const int32_t* lens;      // [batch] cached keys
   const int32_t* token_lens;   // [batch] new tokens, or NULL: all
   const int32_t* page_table;   // [batch] rows of page numbers, table_stride apart
-  float* part_o;            // workspace: [2 chunks][units * 128][dim] unnormalised rows of cut items
-  float2* part_ml;          // and their (maximum, sum)
+  float* part_o;            // workspace: [2 chunks][dim / 4][units * 128][4] unnormalised rows of cut items
+  float2* part_ml;          // [2 chunks][units * 128]: their (maximum, sum)
+  int32_t* cuts;            // [chunks][8]: the item that each chunk begins inside of
   int64_t table_stride;
   int batch, tokens, heads, kv_heads, group;
   int page_size, num_pages, capacity;   // capacity: cached keys that a page table row can hold

@@ -132,8 +132,18 @@ gemm_tn_dev::CacheView view_of(const kv_cache* c, int64_t batch) {
   return v;
 }
 
-// Least key tiles per CTA of the attention and of the weights.
+// Least key tiles per CTA of the attention.
 constexpr int kMinChunk = 2;
+
+// The kernels count key tiles in 32 bits: an upper bound of their number, from
+// what the cache and the inputs can hold.
+int check_tiles(const kv_cache* c, int64_t batch, int64_t row_units, int64_t tokens) {
+  const int64_t per_item = (c->max_pages * c->page_size + 127) / 128 + (tokens + 127) / 128 + 1;
+  const int64_t items = batch * c->kv_heads;   // below 2^31
+  if (row_units > kMax31 / items || per_item > kMax31 / (items * row_units))
+    return invalid("too many key tiles: batch * kv_heads * tokens * capacity is too large");
+  return GEMM_TN_OK;
+}
 
 }  // namespace
 
@@ -169,16 +179,17 @@ int tree_attn_fwd(int dtype, int64_t batch, int64_t tokens, int64_t heads, const
       (has_new && (overlap(out, rows_range(k_new, batch, tokens, kv_heads, dim)) ||
                    overlap(out, rows_range(v_new, batch, tokens, kv_heads, dim)))))
     return invalid("o overlaps an input or the cache");
-  int sms = 0;
-  if ((st = api_device(&sms)) != GEMM_TN_OK) return st;
-
-  const bool bf16 = dtype == GEMM_TN_BF16;
   alignas(64) gemm_tn_dev::TreeArgs args{};
   args.group = static_cast<int>(heads / kv_heads);
   args.tile_tokens = tree_attn_tile_rows() / args.group;
   const int64_t row_tiles = (tokens + args.tile_tokens - 1) / args.tile_tokens;
   args.units = row_tiles > 1 ? 2 : 1;
   args.row_units = static_cast<int>((row_tiles + args.units - 1) / args.units);
+  if ((st = check_tiles(cache, batch, args.row_units, tokens)) != GEMM_TN_OK) return st;
+  int sms = 0;
+  if ((st = api_device(&sms)) != GEMM_TN_OK) return st;
+
+  const bool bf16 = dtype == GEMM_TN_BF16;
   if ((st = encode_rows(&args.tmap_q, bf16, q, batch, tokens, heads, dim, args.group, args.tile_tokens)) != GEMM_TN_OK ||
       (st = encode_pool(&args.tmap_k, bf16, cache->k, cache)) != GEMM_TN_OK ||
       (st = encode_pool(&args.tmap_v, bf16, cache->v, cache)) != GEMM_TN_OK)
@@ -212,10 +223,11 @@ int tree_attn_fwd(int dtype, int64_t batch, int64_t tokens, int64_t heads, const
   const size_t part_rows = static_cast<size_t>(2 * args.chunks) * static_cast<size_t>(args.units * tree_attn_tile_rows());
   void* workspace = nullptr;
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-  cudaError_t e = api_workspace(part_rows * static_cast<size_t>(dim * 4 + 8), s, &workspace);
+  cudaError_t e = api_workspace(part_rows * static_cast<size_t>(dim * 4 + 8) + static_cast<size_t>(args.chunks) * 32, s, &workspace);
   if (e != cudaSuccess) return api_fail_cuda(e, "workspace");
   args.part_o = static_cast<float*>(workspace);
   args.part_ml = reinterpret_cast<float2*>(args.part_o + part_rows * static_cast<size_t>(dim));
+  args.cuts = reinterpret_cast<int32_t*>(args.part_ml + part_rows);
   e = api_counted(launch_tree_attn(static_cast<int>(dim), bf16, args, s));
   if (e == cudaSuccess && args.chunks > 1) e = api_counted(launch_tree_attn_join(static_cast<int>(dim), bf16, args, s));
   const cudaError_t freed = cudaFreeAsync(workspace, s);
@@ -299,6 +311,7 @@ int kv_cache_weigh(int dtype, int64_t batch, int64_t tokens, int64_t heads, cons
   }
   if (!aligned(rows, 4) || !aligned(counts, 4) || !aligned(lse, 4) || !aligned(weight_out, 4))
     return api_fail(GEMM_TN_ERR_MISALIGNED, "rows, counts, lse or weight_out not 4-byte aligned");
+  if ((st = check_tiles(cache, batch, 1, 0)) != GEMM_TN_OK) return st;
   int sms = 0;
   if ((st = api_device(&sms)) != GEMM_TN_OK) return st;
   const bool bf16 = dtype == GEMM_TN_BF16;

@@ -72,52 +72,67 @@ __device__ __forceinline__ uint32_t pack2(float lo, float hi) {
   return out;
 }
 
-__device__ __forceinline__ int64_t warp_scan(int64_t x, uint32_t lane) {   // inclusive
+__device__ __forceinline__ int warp_scan(int x, uint32_t lane) {   // inclusive
 #pragma unroll
   for (int d = 1; d < 32; d *= 2) {
-    const int64_t y = __shfl_up_sync(0xffffffffu, x, d);
+    const int y = __shfl_up_sync(0xffffffffu, x, d);
     if (static_cast<int>(lane) >= d) x += y;
   }
   return x;
 }
 
-// Where chunk `chunk` of `chunks` starts. Called by a whole warp; every lane
-// gets the answer. seq_tiles(b): key tiles of sequence b, in all its items.
-struct Start {
-  int64_t chunk_tiles;   // tiles per chunk
-  int64_t total;         // tiles in all
-  int b;                 // sequence of the chunk's first tile (the batch size past the end) ...
-  int64_t off;           // ... and the tile's number in that sequence
-};
-template <class SeqTiles>
-__device__ __forceinline__ Start find_start(int batch, int chunks, int min_chunk, int chunk, uint32_t lane,
-                                            SeqTiles seq_tiles) {
-  auto tiles_of = [&](int b) { return b < batch ? seq_tiles(b) : int64_t{0}; };
-  const int64_t first = tiles_of(static_cast<int>(lane));   // a batch of up to 32 is read once
-  int64_t total = first;
-  for (int b0 = 32; b0 < batch; b0 += 32) total += tiles_of(b0 + static_cast<int>(lane));
-#pragma unroll
-  for (int d = 16; d > 0; d /= 2) total += __shfl_xor_sync(0xffffffffu, total, d);
-  Start s;
-  s.total = total;
-  s.chunk_tiles = max((total + chunks - 1) / chunks, static_cast<int64_t>(min_chunk));
-  const int64_t want = s.chunk_tiles * chunk;
-  s.b = batch;
-  s.off = 0;
-  int64_t before = 0;
-  for (int b0 = 0; b0 < batch && want < total; b0 += 32) {
-    const int64_t mine = b0 == 0 ? first : tiles_of(b0 + static_cast<int>(lane));
-    const int64_t upto = before + warp_scan(mine, lane);
-    const uint32_t past = __ballot_sync(0xffffffffu, upto > want);
-    if (past != 0) {
-      const int l = __ffs(past) - 1;
-      s.b = b0 + l;
-      s.off = want - __shfl_sync(0xffffffffu, upto - mine, l);
-      break;
+// Finds where chunk `chunk` of `chunks` starts, with one length per thread: a
+// batch of up to blockDim.x sequences costs one round of loads and one scan.
+// Called by the whole block (it synchronises); `sums` is 32 words of shared
+// memory. tiles_of(b): key tiles of sequence b in all its items; the host has
+// made sure that their sum stays below 2^31. found(b, off, left, chunk_tiles)
+// is called by the one thread whose sequence holds the chunk's first tile: the
+// tile's number in that sequence, the tiles of the chunk and of any chunk; no
+// thread calls it for a chunk past the end.
+template <class TilesOf, class Found>
+__device__ __forceinline__ void find_start(int batch, int chunks, int min_chunk, int chunk, int* sums,
+                                           TilesOf tiles_of, Found found) {
+  const int tid = static_cast<int>(threadIdx.x), threads = static_cast<int>(blockDim.x);
+  const uint32_t lane = lane_id();
+  const int warp = tid >> 5, warps = threads >> 5;
+  const int first = tid < batch ? tiles_of(tid) : 0;
+  int mine = first;
+  for (int b = tid + threads; b < batch; b += threads) mine += tiles_of(b);
+  // sums over warps: the total, and in one round the start of each warp's run
+  auto block_scan = [&](int x, int* total) {
+    const int upto = warp_scan(x, lane);
+    __syncthreads();
+    if (lane == 31) sums[warp] = upto;
+    __syncthreads();
+    int before = 0, all = 0;
+    for (int w = 0; w < warps; ++w) {
+      const int s = sums[w];
+      if (w < warp) before += s;
+      all += s;
     }
-    before = __shfl_sync(0xffffffffu, upto, 31);
+    *total = all;
+    return before + upto;
+  };
+  int total;
+  int upto = block_scan(mine, &total);
+  const int chunk_tiles = max((total + chunks - 1) / chunks, min_chunk);
+  const int64_t want64 = static_cast<int64_t>(chunk_tiles) * chunk;
+  if (want64 >= total) return;
+  const int want = static_cast<int>(want64), left = min(chunk_tiles, total - want);
+  if (batch <= threads) {
+    if (want >= upto - mine && want < upto) found(tid, want - (upto - mine), left, chunk_tiles);
+    return;
   }
-  return s;
+  int before = 0;
+  for (int b0 = 0; b0 < batch; b0 += threads) {
+    const int b = b0 + tid;
+    const int here = b0 == 0 ? first : (b < batch ? tiles_of(b) : 0);
+    int round;
+    upto = before + block_scan(here, &round);
+    if (want >= upto - here && want < upto) found(b, want - (upto - here), left, chunk_tiles);
+    before += round;
+    if (before > want) return;
+  }
 }
 
 // First `n` of 32 bits set (n may be negative or past 32).

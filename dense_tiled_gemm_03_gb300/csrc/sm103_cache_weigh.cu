@@ -62,13 +62,13 @@ struct Cfg {
   static constexpr uint32_t kOffBar = kOffLse + 8u * kMaxRows;
   static constexpr uint32_t kOffTmemSlot = kOffBar + 8u * kNumBars;
   static constexpr uint32_t kOffAbort = kOffTmemSlot + 4u;
-  static constexpr uint32_t kOffStart = (kOffAbort + 4u + 7u) / 8u * 8u;
-  static constexpr uint32_t kRaw = kOffStart + 24u + 1024u;
-  static constexpr uint32_t kSmemBytes = kRaw;
+  static constexpr uint32_t kOffStart = kOffAbort + 4u;   // the chunk's first Walk
+  static constexpr uint32_t kOffSums = kOffStart + 32u;   // 32 words of the search for it
+  static constexpr uint32_t kSmemBytes = kOffSums + 128u + 1024u;   // + slack to align the base to 1024
   static constexpr uint32_t kTmemCols = 512;
   static constexpr uint32_t kIdesc = mma_idesc_f16(kBf16, kTileKeys, 0, false);   // N is set per block
   static_assert(kSmemBytes <= 227u * 1024u, "shared memory budget");
-  static_assert(kOffBar % 8u == 0 && kOffStart % 8u == 0, "64-bit shared words");
+  static_assert(kOffBar % 8u == 0, "64-bit shared words");
 };
 
 __device__ __forceinline__ int cached_len(const WeighArgs& a, int b) {
@@ -80,22 +80,21 @@ __device__ __forceinline__ int row_count(const WeighArgs& a, int b) {
 
 // Walks a chunk: runs of one (sequence, KV head)'s key tiles.
 struct Walk {
-  int b, h, j0, len, n, tiles, count;
-  int64_t left;
+  int b, h, j0, len, n, tiles, left, count;
 
+  // The walk that begins at tile `off` of sequence b.
+  __device__ __forceinline__ void start(const WeighArgs& a, int b_, int off, int left_) {
+    b = b_;
+    load(a);
+    h = off / tiles;
+    j0 = off - tiles * h;
+    left = left_;
+    count = min(tiles - j0, left);
+  }
   __device__ __forceinline__ void load(const WeighArgs& a) {
     len = cached_len(a, b);
     n = row_count(a, b);
     tiles = (len + kTileKeys - 1) / kTileKeys;
-  }
-  __device__ __forceinline__ void start(const WeighArgs& a, int b_, int64_t off, int64_t left_) {
-    b = b_;
-    left = left_;
-    if (left <= 0) return;
-    load(a);
-    h = static_cast<int>(off / tiles);
-    j0 = static_cast<int>(off - static_cast<int64_t>(tiles) * h);
-    count = static_cast<int>(min(static_cast<int64_t>(tiles - j0), left));
   }
   __device__ __forceinline__ bool more() const { return left > 0; }
   __device__ __forceinline__ void next(const WeighArgs& a) {
@@ -109,7 +108,7 @@ struct Walk {
         load(a);
       } while (tiles == 0);
     }
-    count = static_cast<int>(min(static_cast<int64_t>(tiles), left));
+    count = min(tiles, left);
   }
   // blocks of query rows; one empty block where no token counts (the weights are still copied)
   __device__ __forceinline__ int blocks(const WeighArgs& a) const {
@@ -141,7 +140,8 @@ __global__ void __launch_bounds__(C::kNumThreads, 1) cache_weigh_kernel(const __
   const uint32_t drain_bar = bar(6 + 2 * C::kStages);
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + C::kOffTmemSlot);
   volatile uint32_t* abort_flag = reinterpret_cast<volatile uint32_t*>(smem + C::kOffAbort);
-  int64_t* start_slot = reinterpret_cast<int64_t*>(smem + C::kOffStart);
+  cw::Walk* start_walk = reinterpret_cast<cw::Walk*>(smem + C::kOffStart);
+  int* sums = reinterpret_cast<int*>(smem + C::kOffSums);
   float2* row_lse = reinterpret_cast<float2*>(smem + C::kOffLse);
 
   if (threadIdx.x == 0) {
@@ -157,6 +157,7 @@ __global__ void __launch_bounds__(C::kNumThreads, 1) cache_weigh_kernel(const __
     }
     mbar_init(drain_bar, 1);
     *abort_flag = 0u;
+    start_walk->left = 0;
     fence_barrier_init();
   }
   if (warp == cw::kProducerWarp && lane == 0) tma_prefetch_descriptor(&args.tmap_k);
@@ -166,24 +167,20 @@ __global__ void __launch_bounds__(C::kNumThreads, 1) cache_weigh_kernel(const __
   }
   griddep_wait();
   griddep_launch_dependents();
-  if (warp == cw::kProducerWarp) {
-    const cache::Start st =
-        cache::find_start(args.batch, args.chunks, args.min_chunk, static_cast<int>(blockIdx.x), lane, [&](int b) {
-          return static_cast<int64_t>((cw::cached_len(args, b) + cw::kTileKeys - 1) / cw::kTileKeys) * args.kv_heads;
-        });
-    if (lane == 0) {
-      start_slot[0] = st.b;
-      start_slot[1] = st.off;
-      start_slot[2] = min(st.chunk_tiles, st.total - st.chunk_tiles * static_cast<int64_t>(blockIdx.x));
-    }
-  }
+  cache::find_start(
+      args.batch, args.chunks, args.min_chunk, static_cast<int>(blockIdx.x), sums,
+      [&](int b) { return (cw::cached_len(args, b) + cw::kTileKeys - 1) / cw::kTileKeys * args.kv_heads; },
+      [&](int b, int off, int left, int) {
+        cw::Walk w;
+        w.start(args, b, off, left);
+        *start_walk = w;
+      });
   tc_fence_before_sync();
   __syncthreads();
   tc_fence_after_sync();
   const uint32_t tmem_base = *tmem_slot;
   const cache::Watch wd{args.status, args.timeout_ns, abort_flag};
-  cw::Walk w;
-  w.start(args, static_cast<int>(start_slot[0]), start_slot[1], start_slot[2]);
+  cw::Walk w = *start_walk;
 
   if (warp == cw::kProducerWarp) {
     // -------------------------------------------------------------- TMA producer

@@ -80,8 +80,9 @@ struct Cfg {
   static constexpr int kNumBars = 4 + 2 * kKStages + 2 * kVStages + 6 + 3;
   static constexpr uint32_t kOffTmemSlot = kOffBar + 8u * kNumBars;
   static constexpr uint32_t kOffAbort = kOffTmemSlot + 4u;
-  static constexpr uint32_t kOffStart = kOffAbort + 4u;   // chunk start (int64 x 3)
-  static constexpr uint32_t kSmemBytes = kOffStart + 24u + 1024u;   // + slack to align the base to 1024
+  static constexpr uint32_t kOffStart = kOffAbort + 4u;   // the chunk's first Walk
+  static constexpr uint32_t kOffSums = kOffStart + 36u;   // 32 words of the search for it
+  static constexpr uint32_t kSmemBytes = kOffSums + 128u + 1024u;   // + slack to align the base to 1024
   static constexpr uint32_t kTmemCols = 512;
   static constexpr uint32_t kColS = 0;      // S_u: 128 fp32 columns at 128 u (P_u over half of them)
   static constexpr uint32_t kColO = 256;    // O_u: dim fp32 columns at 256 + dim u
@@ -89,7 +90,7 @@ struct Cfg {
   static constexpr uint32_t kIdescO = mma_idesc_f16(kBf16, kTileRows, kDim, true);
   static_assert(kDim == 64 || kDim == 128, "head dim 64 or 128");
   static_assert(kSmemBytes <= 227u * 1024u, "shared memory budget");
-  static_assert(kOffBar % 8u == 0 && kOffStart % 8u == 0, "64-bit shared words");
+  static_assert(kOffBar % 8u == 0, "64-bit shared words");
 };
 
 // ------------------------------------------------------------------ the schedule
@@ -120,17 +121,10 @@ __device__ __forceinline__ int item_tiles(const TreeArgs& a, int len, int tl, in
 }
 
 // Key tiles of all row units of one KV head of a sequence.
-__device__ __forceinline__ int64_t head_tiles(const TreeArgs& a, int len, int tl) {
-  int64_t n = 0;
+__device__ __forceinline__ int head_tiles(const TreeArgs& a, int len, int tl) {
+  int n = 0;
   for (int ru = 0; ru < a.row_units; ++ru) n += item_tiles(a, len, tl, ru);
   return n;
-}
-
-// Where chunk `chunk` starts (called by a whole warp).
-__device__ __forceinline__ cache::Start chunk_start(const TreeArgs& a, int chunk, uint32_t lane) {
-  return cache::find_start(a.batch, a.chunks, a.min_chunk, chunk, lane, [&](int b) {
-    return head_tiles(a, cached_len(a, b), new_len(a, b)) * a.kv_heads;
-  });
 }
 
 // Walks a chunk: one segment (a run of one item's key tiles) after another.
@@ -138,28 +132,20 @@ struct Walk {
   int b, h, ru, j0;      // item and its first tile in this segment
   int len, tl;           // cached keys and new tokens of b
   int tiles;             // tiles of the item
+  int left;              // tiles of the chunk from this segment on
   int count;             // tiles of the segment
-  int64_t left;          // tiles of the chunk from this segment on
 
-  __device__ __forceinline__ void load(const TreeArgs& a) {
+  // The walk that begins at tile `off` of sequence b.
+  __device__ __forceinline__ void start(const TreeArgs& a, int b_, int off, int left_) {
+    b = b_;
     len = cached_len(a, b);
     tl = new_len(a, b);
-  }
-  __device__ __forceinline__ void start(const TreeArgs& a, int b_, int64_t off, int64_t left_) {
-    b = b_;
+    const int per_head = head_tiles(a, len, tl);
+    h = off / per_head;
+    j0 = off - per_head * h;
+    for (ru = 0; (tiles = item_tiles(a, len, tl, ru)) <= j0; ++ru) j0 -= tiles;
     left = left_;
-    if (left <= 0) return;
-    load(a);
-    const int64_t per_head = head_tiles(a, len, tl);
-    h = static_cast<int>(off / per_head);
-    int rest = static_cast<int>(off - per_head * h);
-    ru = 0;
-    while ((tiles = item_tiles(a, len, tl, ru)) <= rest) {
-      rest -= tiles;
-      ++ru;
-    }
-    j0 = rest;
-    count = static_cast<int>(min(static_cast<int64_t>(tiles - j0), left));
+    count = min(tiles - j0, left);
   }
   __device__ __forceinline__ bool more() const { return left > 0; }
   __device__ __forceinline__ void next(const TreeArgs& a) {
@@ -172,12 +158,13 @@ struct Walk {
         if (++h == a.kv_heads) {
           h = 0;
           ++b;
-          load(a);
+          len = cached_len(a, b);
+          tl = new_len(a, b);
         }
       }
       tiles = item_tiles(a, len, tl, ru);
     } while (tiles == 0);
-    count = static_cast<int>(min(static_cast<int64_t>(tiles), left));
+    count = min(tiles, left);
   }
   // Past the last tile of the segment that unit u walks.
   __device__ __forceinline__ int unit_end(const TreeArgs& a, int u) const {
@@ -230,7 +217,8 @@ __global__ void __launch_bounds__(C::kNumThreads) __maxnreg__(C::kMaxRegs)
   const uint32_t xch_full = bar(kUBar + 6), xch_empty = bar(kUBar + 7), drain_bar = bar(kUBar + 8);
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + C::kOffTmemSlot);
   volatile uint32_t* abort_flag = reinterpret_cast<volatile uint32_t*>(smem + C::kOffAbort);
-  int64_t* start_slot = reinterpret_cast<int64_t*>(smem + C::kOffStart);
+  ta::Walk* start_walk = reinterpret_cast<ta::Walk*>(smem + C::kOffStart);
+  int* sums = reinterpret_cast<int*>(smem + C::kOffSums);
   float2* xch = reinterpret_cast<float2*>(smem + C::kOffXch);
 
   if (threadIdx.x == 0) {
@@ -253,6 +241,7 @@ __global__ void __launch_bounds__(C::kNumThreads) __maxnreg__(C::kMaxRegs)
     mbar_init(xch_empty, 4);
     mbar_init(drain_bar, 1);
     *abort_flag = 0u;
+    start_walk->left = 0;
     fence_barrier_init();
   }
   if (warp == ta::kProducerWarp && lane == 0) {
@@ -268,14 +257,20 @@ __global__ void __launch_bounds__(C::kNumThreads) __maxnreg__(C::kMaxRegs)
   // stream; global memory is touched only once that kernel has completed.
   griddep_wait();
   griddep_launch_dependents();
-  if (warp == ta::kProducerWarp) {
-    const cache::Start st = ta::chunk_start(args, static_cast<int>(blockIdx.x), lane);
-    if (lane == 0) {
-      start_slot[0] = st.b;
-      start_slot[1] = st.off;
-      start_slot[2] = min(st.chunk_tiles, st.total - st.chunk_tiles * static_cast<int64_t>(blockIdx.x));
-    }
-  }
+  cache::find_start(
+      args.batch, args.chunks, args.min_chunk, static_cast<int>(blockIdx.x), sums,
+      [&](int b) { return ta::head_tiles(args, ta::cached_len(args, b), ta::new_len(args, b)) * args.kv_heads; },
+      [&](int b, int off, int left, int chunk_tiles) {
+        ta::Walk w;
+        w.start(args, b, off, left);
+        *start_walk = w;
+        // what the second kernel has to know about an item that this chunk begins inside of
+        if (w.j0 > 0) {
+          int4* to = reinterpret_cast<int4*>(args.cuts) + 2 * blockIdx.x;
+          to[0] = make_int4(w.b, w.h, w.ru, w.j0);
+          to[1] = make_int4(w.tiles, w.len, w.tl, chunk_tiles);
+        }
+      });
   tc_fence_before_sync();
   __syncthreads();
   tc_fence_after_sync();
@@ -283,8 +278,8 @@ __global__ void __launch_bounds__(C::kNumThreads) __maxnreg__(C::kMaxRegs)
   const cache::Watch wd{args.status, args.timeout_ns, abort_flag};
   const bool parity_mode = args.units == 1;
   const bool has_new = args.has_new != 0;
-  ta::Walk w;
-  w.start(args, static_cast<int>(start_slot[0]), start_slot[1], start_slot[2]);
+  ta::Walk w = *start_walk;
+  if (threadIdx.x == 0 && (!w.more() || w.j0 == 0)) reinterpret_cast<int4*>(args.cuts)[2 * blockIdx.x] = make_int4(-1, 0, 0, 0);
 
   if (warp == ta::kProducerWarp) {
     // -------------------------------------------------------------- TMA producer
@@ -377,6 +372,7 @@ __global__ void __launch_bounds__(C::kNumThreads) __maxnreg__(C::kMaxRegs)
       for (; ok && w.more(); it0 += w.count, w.next(args), ++seg) {
         const int end[2] = {w.unit_end(args, 0), w.unit_end(args, 1)};
         const int step = parity_mode ? 2 : 1;
+        int products = parity_mode ? w.count : end[0] + end[1] - 2 * w.j0;   // Q K^T still to issue
         // the last unit that reads tile j (pair mode: both read it while both walk it)
         auto last_reader = [&](int u, int j) { return parity_mode || u == 1 || j >= end[1]; };
         auto wait_k = [&](int j) {
@@ -401,6 +397,8 @@ __global__ void __launch_bounds__(C::kNumThreads) __maxnreg__(C::kMaxRegs)
           }
           mma_commit(s_full(u));
           if (last_reader(u, j)) mma_commit(k_empty(s));
+          if (--products == 0)   // Q has been read for the last time
+            for (int x = 0; x < args.units; ++x) mma_commit(q_empty(parity_mode ? seg & 1 : x));
         };
         auto issue_pv = [&](int u, int j, bool first) {
           const int s = (it0 + j - w.j0) % C::kVStages;
@@ -450,7 +448,6 @@ __global__ void __launch_bounds__(C::kNumThreads) __maxnreg__(C::kMaxRegs)
             }
           }
         }
-        for (int u = 0; u < args.units && ok; ++u) mma_commit(q_empty(parity_mode ? seg & 1 : u));
       }
       // every MMA issued here must finish before TMEM is freed
       mma_commit(drain_bar);
@@ -592,7 +589,7 @@ __global__ void __launch_bounds__(C::kNumThreads) __maxnreg__(C::kMaxRegs)
           }
           l = l * alpha + sum;
           if (__any_sync(0xffffffffu, alpha != 1.0f)) {
-#pragma unroll
+#pragma unroll 1
             for (int c = 0; c < C::kDim / 32; ++c) {
               uint32_t o[32];
               tmem_load_32x32(t_o + 32u * c, o);
@@ -667,7 +664,8 @@ __global__ void __launch_bounds__(C::kNumThreads) __maxnreg__(C::kMaxRegs)
         const float inv = whole ? (sum == 0.0f ? 0.0f : 1.0f / sum) : 1.0f;
         const int64_t out_row = (static_cast<int64_t>(w.b) * args.tokens + token) * args.heads + w.h * args.group + r_head;
         const int slot = static_cast<int>(blockIdx.x) * 2 + (w.j0 == 0 ? 1 : 0);
-        const int64_t part_row = static_cast<int64_t>(slot) * (args.units * ta::kTileRows) + (parity_mode ? 0 : u) * ta::kTileRows + r;
+        const int part_unit_row = (parity_mode ? 0 : u) * ta::kTileRows + r;
+        const int64_t part_row = static_cast<int64_t>(slot) * (args.units * ta::kTileRows) + part_unit_row;
         if (live) {
           if (whole) {
             if (args.lse != nullptr)
@@ -677,8 +675,11 @@ __global__ void __launch_bounds__(C::kNumThreads) __maxnreg__(C::kMaxRegs)
           }
         }
         uint16_t* out = static_cast<uint16_t*>(args.o) + out_row * C::kDim;
-        float* part = args.part_o + part_row * C::kDim;
-#pragma unroll
+        // [slot][dim / 4][row] pieces of four: a warp's 32 rows store 512 contiguous bytes at a time
+        float4* part = reinterpret_cast<float4*>(args.part_o) +
+                       static_cast<int64_t>(slot) * (args.units * ta::kTileRows) * (C::kDim / 4) + part_unit_row;
+        const int part_pitch = args.units * ta::kTileRows;
+#pragma unroll 1   // once per segment: short code, which is fetched cold, is faster than unrolled code
         for (int c = 0; c < C::kDim / 32; ++c) {
           uint32_t o[32];
           tmem_load_32x32(t_o + 32u * c, o);
@@ -702,9 +703,9 @@ __global__ void __launch_bounds__(C::kNumThreads) __maxnreg__(C::kMaxRegs)
                                     ta::pack2<C::kBf16>(y[4] * inv, y[5] * inv), ta::pack2<C::kBf16>(y[6] * inv, y[7] * inv));
               }
             } else {
-              float4* dst = reinterpret_cast<float4*>(part + 32 * c);
 #pragma unroll
-              for (int x = 0; x < 8; ++x) dst[x] = make_float4(v[4 * x], v[4 * x + 1], v[4 * x + 2], v[4 * x + 3]);
+              for (int x = 0; x < 8; ++x)
+                part[(8 * c + x) * part_pitch] = make_float4(v[4 * x], v[4 * x + 1], v[4 * x + 2], v[4 * x + 3]);
             }
           }
         }
@@ -729,79 +730,83 @@ __global__ void __launch_bounds__(C::kNumThreads) __maxnreg__(C::kMaxRegs)
 // Joins the parts of the items that a chunk boundary cut. Block x looks at the
 // boundary before chunk x + 1; the first boundary inside an item joins it:
 // part 0 lies in the chunk before, the others in the chunks after, in order.
-// One warp per row; the sums run over the parts in their order.
+// A warp has 32 rows and kPer four-column pieces of each: it reads 512
+// contiguous bytes of a part at a time and a thread writes whole sectors of o.
+// Two groups of eight warps take every other part, each as an online softmax;
+// the second hands its sums to the first in shared memory.
 template <int kDim, bool kBf16>
-__global__ void __launch_bounds__(256) tree_attn_join_kernel(const __grid_constant__ TreeArgs args) {
+__global__ void __launch_bounds__(512) tree_attn_join_kernel(const __grid_constant__ TreeArgs args) {
+  constexpr int kPieces = kDim / 4;            // four-column pieces of a row
+  constexpr int kPer = kPieces / 8;            // pieces per thread
+  __shared__ float4 other_o[kPer][256];
+  __shared__ float2 other_ml[256];
   griddep_wait();
   griddep_launch_dependents();
-  __shared__ int64_t found[4];
-  const uint32_t warp = threadIdx.x >> 5, lane = lane_id();
   const int chunk = static_cast<int>(blockIdx.x) + 1;
-  if (warp == 0) {
-    const cache::Start st = ta::chunk_start(args, chunk, lane);
-    if (lane == 0) {
-      found[0] = st.b;
-      found[1] = st.off;
-      found[2] = st.chunk_tiles;
-      found[3] = st.total;
-    }
-  }
-  __syncthreads();
-  const int64_t per_chunk = found[2];
-  ta::Walk w;
-  w.start(args, static_cast<int>(found[0]), found[1], found[3] - per_chunk * chunk);
-  if (!w.more() || w.j0 == 0 || w.j0 > per_chunk) return;
-  const int parts = 1 + static_cast<int>((w.tiles - w.j0 + per_chunk - 1) / per_chunk);
+  const int4* cuts = reinterpret_cast<const int4*>(args.cuts) + 2 * chunk;
+  const int4 c0 = __ldg(cuts), c1 = __ldg(cuts + 1);
+  const int b = c0.x, h = c0.y, ru = c0.z, j0 = c0.w, tiles = c1.x, len = c1.y, tl = c1.z, per_chunk = c1.w;
+  if (b < 0 || j0 > per_chunk) return;
+  const int parts = 2 + (tiles - j0 - 1) / per_chunk;
   const int rows_per_part = args.units * ta::kTileRows;
-  const int row = static_cast<int>(blockIdx.y) * 8 + static_cast<int>(warp);
+  const int group = static_cast<int>(threadIdx.x) >> 8, tid = static_cast<int>(threadIdx.x) & 255;
+  const int piece0 = (tid >> 5) * kPer;
+  const int row = static_cast<int>(blockIdx.y) * 32 + (tid & 31);
   const int unit = row / ta::kTileRows, r = row % ta::kTileRows;
   const int r_token = r / args.group;
-  const int token = (w.ru * args.units + unit) * args.tile_tokens + r_token;
-  if (row >= rows_per_part || r_token >= args.tile_tokens || token >= w.tl) return;
-  // a unit whose rows end before the item's last parts left nothing there
-  auto at = [&](int p) {
-    const int slot = p == 0 ? (chunk - 1) * 2 + 1 : (chunk + p - 1) * 2;
-    return static_cast<int64_t>(slot) * rows_per_part + row;
-  };
-  const int own_tiles = ta::unit_tiles(args, w.len, w.tl, w.ru, unit);
-  auto has = [&](int p) {   // the part begins before the unit's last tile
-    return p == 0 || w.j0 + static_cast<int64_t>(p - 1) * per_chunk < own_tiles;
-  };
-  float m = -INFINITY;
-  for (int p = static_cast<int>(lane); p < parts; p += 32)
-    if (has(p)) {
-      const float2 ml = __ldg(args.part_ml + at(p));
-      if (ml.y > 0.0f) m = fmaxf(m, ml.x);
-    }
+  const int token = (ru * args.units + unit) * args.tile_tokens + r_token;
+  const bool live = row < rows_per_part && r_token < args.tile_tokens && token < tl;
+  float m = -INFINITY, sum = 0.0f;
+  float4 acc[kPer];
 #pragma unroll
-  for (int d = 16; d > 0; d /= 2) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, d));
-  float sum = 0.0f;
-  constexpr int kPer = kDim / 32;
-  float acc[kPer] = {};
+  for (int x = 0; x < kPer; ++x) acc[x] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+  // adds a part; a sum of zero has no reference and nothing in its row
+  auto add = [&](float2 ml, const float4* y) {
+    if (ml.y == 0.0f) return;
+    const float m_new = fmaxf(m, ml.x);
+    const float f0 = sum == 0.0f ? 0.0f : ex2_approx(m - m_new), f1 = ex2_approx(ml.x - m_new);
+    m = m_new;
+    sum = sum * f0 + ml.y * f1;
+#pragma unroll
+    for (int x = 0; x < kPer; ++x)
+      acc[x] = make_float4(acc[x].x * f0 + y[x].x * f1, acc[x].y * f0 + y[x].y * f1, acc[x].z * f0 + y[x].z * f1,
+                           acc[x].w * f0 + y[x].w * f1);
+  };
+  if (live) {
+    // a unit whose keys end before the item's last parts left nothing there
+    const int own_tiles = ta::unit_tiles(args, len, tl, ru, unit);
+    const int own_parts = own_tiles > j0 ? min(parts, 2 + (own_tiles - j0 - 1) / per_chunk) : 1;
 #pragma unroll 4
-  for (int p = 0; p < parts; ++p) {
-    if (!has(p)) continue;
-    const float2 ml = __ldg(args.part_ml + at(p));
-    const float f = ml.y == 0.0f ? 0.0f : (ml.y > 0.0f ? ex2_approx(ml.x - m) : 1.0f);
-    sum += f == 0.0f ? 0.0f : ml.y * f;
-    const float* src = args.part_o + at(p) * kDim + lane * kPer;
-    float x[kPer];
-    if constexpr (kPer == 4) {
-      const float4 y = __ldg(reinterpret_cast<const float4*>(src));
-      x[0] = y.x, x[1] = y.y, x[2] = y.z, x[3] = y.w;
-    } else {
-      const float2 y = __ldg(reinterpret_cast<const float2*>(src));
-      x[0] = y.x, x[1] = y.y;
+    for (int p = group; p < own_parts; p += 2) {
+      const int64_t slot = p == 0 ? (chunk - 1) * 2 + 1 : (chunk + p - 1) * 2;
+      const float2 ml = __ldg(args.part_ml + slot * rows_per_part + row);
+      float4 y[kPer];
+#pragma unroll
+      for (int x = 0; x < kPer; ++x)
+        y[x] = __ldg(reinterpret_cast<const float4*>(args.part_o) + (slot * kPieces + piece0 + x) * rows_per_part + row);
+      add(ml, y);
     }
-#pragma unroll
-    for (int e = 0; e < kPer; ++e) acc[e] += f == 0.0f ? 0.0f : x[e] * f;
   }
-  const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
-  const int64_t out_row = (static_cast<int64_t>(w.b) * args.tokens + token) * args.heads + w.h * args.group + (r - r_token * args.group);
-  uint32_t* out = reinterpret_cast<uint32_t*>(static_cast<uint16_t*>(args.o) + out_row * kDim) + lane * (kPer / 2);
+  if (group == 1) {
 #pragma unroll
-  for (int e = 0; e < kPer / 2; ++e) out[e] = ta::pack2<kBf16>(acc[2 * e] * inv, acc[2 * e + 1] * inv);
-  if (lane == 0 && args.lse != nullptr) args.lse[out_row] = sum == 0.0f ? -INFINITY : (m * ta::kLn2 + logf(sum));
+    for (int x = 0; x < kPer; ++x) other_o[x][tid] = acc[x];
+    other_ml[tid] = make_float2(m, sum);
+  }
+  __syncthreads();
+  if (group == 1 || !live) return;
+  float4 y[kPer];
+#pragma unroll
+  for (int x = 0; x < kPer; ++x) y[x] = other_o[x][tid];
+  add(other_ml[tid], y);
+  const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
+  const int64_t out_row = (static_cast<int64_t>(b) * args.tokens + token) * args.heads + h * args.group + (r - r_token * args.group);
+  uint4* out = reinterpret_cast<uint4*>(static_cast<uint16_t*>(args.o) + out_row * kDim + piece0 * 4);
+#pragma unroll
+  for (int x = 0; x < kPer; x += 2)
+    out[x / 2] = make_uint4(ta::pack2<kBf16>(acc[x].x * inv, acc[x].y * inv), ta::pack2<kBf16>(acc[x].z * inv, acc[x].w * inv),
+                            ta::pack2<kBf16>(acc[x + 1].x * inv, acc[x + 1].y * inv),
+                            ta::pack2<kBf16>(acc[x + 1].z * inv, acc[x + 1].w * inv));
+  if (piece0 == 0 && args.lse != nullptr) args.lse[out_row] = sum == 0.0f ? -INFINITY : (m * ta::kLn2 + logf(sum));
 }
 
 }  // namespace gemm_tn_dev
@@ -841,8 +846,8 @@ cudaError_t launch_join(const gemm_tn_dev::TreeArgs& args, cudaStream_t stream) 
   cudaLaunchConfig_t cfg{};
   const int rows = args.units == 2 ? 2 * gemm_tn_dev::ta::kTileRows
                                    : (args.tokens < args.tile_tokens ? args.tokens : args.tile_tokens) * args.group;
-  cfg.gridDim = dim3(static_cast<unsigned>(args.chunks - 1), static_cast<unsigned>((rows + 7) / 8), 1);
-  cfg.blockDim = dim3(256, 1, 1);
+  cfg.gridDim = dim3(static_cast<unsigned>(args.chunks - 1), static_cast<unsigned>((rows + 31) / 32), 1);
+  cfg.blockDim = dim3(512, 1, 1);
   cfg.stream = stream;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
