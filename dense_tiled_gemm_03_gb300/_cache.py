@@ -8,9 +8,10 @@ CUDA kernels, on the current CUDA stream of the cache's device.
 from __future__ import annotations
 
 import ctypes
+import struct
 
 from . import _native
-from ._native import GEMM_TN_OK, GemmTnError, _dtype_code, _on_device, _status_ptr, library
+from ._native import GEMM_TN_BF16, GEMM_TN_F16, GEMM_TN_OK, GemmTnError, library
 
 _i64 = ctypes.c_int64
 _int = ctypes.c_int
@@ -30,23 +31,49 @@ class KvRows(ctypes.Structure):
     _fields_ = [("data", _ptr), ("batch_stride", _i64), ("token_stride", _i64), ("head_stride", _i64)]
 
 
-_cache_ptr = ctypes.POINTER(KvCacheStruct)
-_rows_ptr = ctypes.POINTER(KvRows)
-
+# struct kv_cache* and struct kv_rows* are passed as c_void_p: a ctypes.byref, or
+# the bytes that struct.pack makes (a small call's time is mostly the
+# binding's, and packing takes a fraction of filling a ctypes.Structure)
 _native._SIGNATURES.update({
-    "tree_attn_fwd": (_int, [_int, _i64, _i64, _i64, _cache_ptr, _rows_ptr, _rows_ptr, _rows_ptr, _ptr, _ptr, _ptr, _ptr,
-                             ctypes.c_float, _ptr, _ptr]),
-    "kv_cache_append": (_int, [_int, _i64, _i64, _cache_ptr, _rows_ptr, _rows_ptr, _ptr, _ptr, _i64, _ptr, _ptr, _ptr,
-                               _ptr]),
-    "kv_cache_weigh": (_int, [_int, _i64, _i64, _i64, _cache_ptr, _rows_ptr, _ptr, _ptr, _ptr, _i64, _int,
-                              ctypes.c_float, _ptr, _ptr, _ptr]),
-    "kv_cache_evict": (_int, [_int, _i64, _cache_ptr, _i64, _i64, _ptr, _ptr, _ptr, _ptr, _ptr]),
+    "tree_attn_fwd": (_int, [_int, _i64, _i64, _i64, _ptr, _ptr, _ptr, _ptr, _ptr, _ptr, _ptr, _ptr, ctypes.c_float, _ptr,
+                             _ptr]),
+    "kv_cache_append": (_int, [_int, _i64, _i64, _ptr, _ptr, _ptr, _ptr, _ptr, _i64, _ptr, _ptr, _ptr, _ptr]),
+    "kv_cache_weigh": (_int, [_int, _i64, _i64, _i64, _ptr, _ptr, _ptr, _ptr, _ptr, _i64, _int, ctypes.c_float, _ptr, _ptr,
+                              _ptr]),
+    "kv_cache_evict": (_int, [_int, _i64, _ptr, _i64, _i64, _ptr, _ptr, _ptr, _ptr, _ptr]),
 })
+_pack_cache = struct.Struct("16q").pack
+_pack_rows = struct.Struct("4q").pack
 
 
-def _torch():
-    import torch
-    return torch
+class _Torch:
+    """What the functions below use of torch, looked up once."""
+
+    def __getattr__(self, _):
+        import torch
+        self.int32, self.int64, self.float32 = torch.int32, torch.int64, torch.float32
+        self.codes = {torch.float16: GEMM_TN_F16, torch.bfloat16: GEMM_TN_BF16}
+        self.get_device, self.set_device = torch._C._cuda_getDevice, torch._C._cuda_setDevice
+        self.stream = torch._C._cuda_getCurrentRawStream
+        self.empty, self.zeros = torch.empty, torch.zeros
+        return self.__dict__[_]
+
+
+_t = _Torch()
+
+
+def _call(name: str, index: int, *args):
+    """One call of the library on device `index` and its current stream."""
+    current = _t.get_device()
+    if current != index:
+        _t.set_device(index)
+    try:
+        rc = getattr(_native._lib or library(), name)(*args, _t.stream(index))
+    finally:
+        if current != index:
+            _t.set_device(current)
+    if rc != GEMM_TN_OK:
+        raise GemmTnError(rc, name)
 
 
 class KVCache:
@@ -64,87 +91,99 @@ class KVCache:
     (capacity = max_pages * page_size).
     """
 
-    __slots__ = ("k", "v", "page_table", "lens", "weight", "pos", "seen", "batch", "capacity", "device", "dtype",
-                 "kv_heads", "head_dim", "struct", "_code", "_ref")
+    __slots__ = ("k", "v", "page_table", "lens", "weight", "pos", "seen", "batch", "capacity", "index", "dtype",
+                 "kv_heads", "head_dim", "_code", "_struct")
 
     def __init__(self, k, v, page_table, lens, weight=None, pos=None, seen=None):
-        torch = _torch()
-        dev = k.device
-        if dev.type != "cuda" or v.device != dev or page_table.device != dev or lens.device != dev:
+        index = k.get_device()
+        if index < 0 or v.get_device() != index or page_table.get_device() != index or lens.get_device() != index:
             raise ValueError("the cache's tensors must be CUDA tensors on one device")
-        if v.dtype != k.dtype:
+        dtype = k.dtype
+        if v.dtype is not dtype:
             raise TypeError("k and v must have the same dtype")
-        self._code = _dtype_code(k)
-        if k.dim() != 4 or v.shape != k.shape or k.stride() != v.stride():
+        code = _t.codes.get(dtype)
+        if code is None:
+            raise TypeError(f"unsupported dtype {dtype}: expected float16 or bfloat16")
+        shape, strides = k.shape, k.stride()
+        if len(shape) != 4 or v.shape != shape or v.stride() != strides:
             raise ValueError("k and v must be [num_pages, page_size, kv_heads, head_dim] with the same strides")
-        pages, page_size, heads, dim = k.shape
-        page_stride, slot_stride, head_stride, unit = k.stride()
+        pages, page_size, heads, dim = shape
+        page_stride, slot_stride, head_stride, unit = strides
         if unit != 1:
             raise ValueError("k and v must have unit stride along head_dim")
-        if page_table.dtype != torch.int32 or lens.dtype != torch.int32:
+        int32 = _t.int32
+        if page_table.dtype is not int32 or lens.dtype is not int32:
             raise TypeError("page_table and lens must be int32")
-        if page_table.dim() != 2 or (page_table.shape[1] > 1 and page_table.stride(1) != 1):
-            raise ValueError("page_table must be [batch, max_pages] with unit stride along max_pages")
+        if page_table.dim() != 2:
+            raise ValueError("page_table must be [batch, max_pages]")
         batch, max_pages = page_table.shape
+        table_stride, unit = page_table.stride()
+        if unit != 1 and max_pages > 1:
+            raise ValueError("page_table must have unit stride along max_pages")
         if lens.shape != (batch,) or not lens.is_contiguous():
             raise ValueError("lens must be a contiguous [batch] tensor")
-        capacity = max_pages * page_size
-        for name, t, dt in (("weight", weight, torch.float32), ("pos", pos, torch.int32)):
-            if t is not None and (t.dtype != dt or t.shape != (batch, heads, capacity) or t.device != dev or
-                                  not t.is_contiguous()):
-                raise ValueError(f"{name} must be a contiguous {dt} [batch, kv_heads, max_pages * page_size] tensor on {dev}")
-        if seen is not None and (seen.dtype != torch.int32 or seen.shape != (batch,) or seen.device != dev or
-                                 not seen.is_contiguous()):
-            raise ValueError(f"seen must be a contiguous int32 [batch] tensor on {dev}")
+        self.index, self.batch, self.kv_heads = index, batch, heads
+        self.capacity = capacity = max_pages * page_size
+        w = p = s = 0
+        if weight is not None:
+            w = _floats(weight, self, "weight", (batch, heads, capacity))
+        if pos is not None:
+            p = _ints(pos, self, "pos", (batch, heads, capacity))
+        if seen is not None:
+            s = _ints(seen, self, "seen", (batch,))
         self.k, self.v, self.page_table, self.lens = k, v, page_table, lens
         self.weight, self.pos, self.seen = weight, pos, seen
-        self.batch, self.capacity, self.device, self.dtype = batch, capacity, dev, k.dtype
-        self.kv_heads, self.head_dim = heads, dim
-        self.struct = KvCacheStruct(
+        self.dtype, self.head_dim, self._code = dtype, dim, code
+        self._struct = _pack_cache(
             k.data_ptr(), v.data_ptr(), pages, page_size, heads, dim, page_stride, slot_stride,
-            head_stride if heads > 1 else dim, page_table.data_ptr(),
-            page_table.stride(0) if batch > 1 else max_pages, max_pages, lens.data_ptr(),
-            weight.data_ptr() if weight is not None else None, pos.data_ptr() if pos is not None else None,
-            seen.data_ptr() if seen is not None else None)
-        self._ref = ctypes.byref(self.struct)
+            head_stride if heads > 1 else dim, page_table.data_ptr(), table_stride if batch > 1 else max_pages,
+            max_pages, lens.data_ptr(), w, p, s)
 
 
-def _rows(t, cache: KVCache, what: str, batch: int, tokens: int, heads: int):
-    """struct kv_rows of a [batch, tokens, heads, head_dim] tensor."""
-    if t.device != cache.device:
+def _rows(t, cache: KVCache, what: str, shape):
+    """struct kv_rows of a [batch, tokens, heads, head_dim] tensor of that shape."""
+    if t.get_device() != cache.index:
         raise ValueError(f"{what} must be on the cache's device")
-    if t.dtype != cache.dtype:
+    if t.dtype is not cache.dtype:
         raise TypeError(f"{what} must have the cache's dtype")
-    if t.shape != (batch, tokens, heads, cache.head_dim):
-        raise ValueError(f"{what} must be [batch, tokens, heads, head_dim] = {(batch, tokens, heads, cache.head_dim)}")
+    if t.shape != shape:
+        raise ValueError(f"{what} must be [batch, tokens, heads, head_dim] = {tuple(shape)}")
     sb, st, sh, unit = t.stride()
     if unit != 1:
         raise ValueError(f"{what} must have unit stride along head_dim")
-    return KvRows(t.data_ptr(), sb, st, sh)
+    return _pack_rows(t.data_ptr(), sb, st, sh)
 
 
 def _ints(t, cache: KVCache, what: str, shape):
     """Device pointer of a contiguous int32 tensor of that shape, or None."""
     if t is None:
         return None
-    if t.device != cache.device or t.dtype != _torch().int32 or t.shape != shape or not t.is_contiguous():
-        raise ValueError(f"{what} must be a contiguous int32 {tuple(shape)} tensor on {cache.device}")
+    if t.get_device() != cache.index or t.dtype is not _t.int32 or t.shape != shape or not t.is_contiguous():
+        raise ValueError(f"{what} must be a contiguous int32 {tuple(shape)} tensor on the cache's device")
     return t.data_ptr()
 
 
 def _floats(t, cache: KVCache, what: str, shape):
-    if t.device != cache.device or t.dtype != _torch().float32 or t.shape != shape or not t.is_contiguous():
-        raise ValueError(f"{what} must be a contiguous float32 {tuple(shape)} tensor on {cache.device}")
+    if t.get_device() != cache.index or t.dtype is not _t.float32 or t.shape != shape or not t.is_contiguous():
+        raise ValueError(f"{what} must be a contiguous float32 {tuple(shape)} tensor on the cache's device")
     return t.data_ptr()
 
 
-def _new_tokens(cache: KVCache, q):
-    if q.dim() != 4:
-        raise ValueError("q must be [batch, tokens, heads, head_dim]")
-    batch, tokens, heads, _ = q.shape
-    if batch != cache.batch:
-        raise ValueError("q must have the cache's batch size")
-    return batch, tokens, heads
+def _status(t, cache: KVCache):
+    """Device pointer of the optional status word."""
+    if t is None:
+        return None
+    if t.get_device() != cache.index or t.dtype is not _t.int32 or t.numel() < 1 or not t.is_contiguous():
+        raise ValueError("status must be a contiguous int32 tensor of at least one element on the cache's device")
+    return t.data_ptr()
+
+
+def _queries(q, cache: KVCache):
+    """q's shape and struct."""
+    shape = q.shape
+    if len(shape) != 4 or shape[0] != cache.batch or shape[3] != cache.head_dim:
+        raise ValueError("q must be [batch, tokens, heads, head_dim] with the cache's batch size and head_dim")
+    return shape, _rows(q, cache, "q", shape)
 
 
 def tree_attn(q, cache: KVCache, k_new=None, v_new=None, mask=None, token_lens=None, scale=None, out=None, lse=None,
@@ -159,46 +198,41 @@ def tree_attn(q, cache: KVCache, k_new=None, v_new=None, mask=None, token_lens=N
     1/sqrt(head_dim)); out: optional contiguous tensor of q's shape and dtype,
     whose rows from token_lens on are left as they are (without it they come
     back as zeros); lse: optional contiguous fp32 [batch, tokens, heads] that
-    receives the log of each row's sum of exponentials. Returns out."""
-    torch = _torch()
-    batch, tokens, heads = _new_tokens(cache, q)
-    rq = _rows(q, cache, "q", batch, tokens, heads)
-    rk = rv = None
-    if (k_new is None) != (v_new is None):
-        raise ValueError("k_new and v_new come together")
+    receives the log of each row's sum of exponentials; status: optional
+    one-element int32 CUDA tensor for device-side errors. Returns out."""
+    shape, rq = _queries(q, cache)
+    batch, tokens, heads, dim = shape
+    rk = rv = d_mask = None
     if k_new is not None:
-        rk = ctypes.byref(_rows(k_new, cache, "k_new", batch, tokens, cache.kv_heads))
-        rv = ctypes.byref(_rows(v_new, cache, "v_new", batch, tokens, cache.kv_heads))
-    d_mask = None
+        if v_new is None:
+            raise ValueError("k_new and v_new come together")
+        new_shape = (batch, tokens, cache.kv_heads, dim)
+        rk, rv = _rows(k_new, cache, "k_new", new_shape), _rows(v_new, cache, "v_new", new_shape)
+    elif v_new is not None:
+        raise ValueError("k_new and v_new come together")
     if mask is not None:
-        if mask.device != cache.device or mask.dtype != torch.int64 or not mask.is_contiguous() or \
-                mask.shape != (batch, tokens, (tokens + 63) // 64):
+        if mask.get_device() != cache.index or mask.dtype is not _t.int64 or \
+                mask.shape != (batch, tokens, (tokens + 63) // 64) or not mask.is_contiguous():
             raise ValueError("mask must be a contiguous int64 [batch, tokens, ceil(tokens / 64)] tensor on the cache's device")
         d_mask = mask.data_ptr()
     if out is None:
-        shape = (batch, tokens, heads, cache.head_dim)
-        out = (torch.empty if token_lens is None else torch.zeros)(shape, dtype=q.dtype, device=q.device)
-    elif out.shape != q.shape or out.dtype != q.dtype or out.device != q.device or not out.is_contiguous():
+        out = (_t.empty if token_lens is None else _t.zeros)(shape, dtype=cache.dtype, device=q.device)
+    elif out.shape != shape or out.dtype is not cache.dtype or out.get_device() != cache.index or not out.is_contiguous():
         raise ValueError("out must be a contiguous tensor with q's shape, dtype and device")
-    d_lse = _floats(lse, cache, "lse", (batch, tokens, heads)) if lse is not None else None
-    d_lens = _ints(token_lens, cache, "token_lens", (batch,))
-    d_status = _status_ptr(status, cache.device)
-    with _on_device(cache.device) as stream:
-        rc = library().tree_attn_fwd(cache._code, batch, tokens, heads, cache._ref, ctypes.byref(rq), rk, rv, d_mask, d_lens,
-                                     out.data_ptr(), d_lse, 0.0 if scale is None else float(scale), d_status, stream)
-    if rc != GEMM_TN_OK:
-        raise GemmTnError(rc, "tree_attn_fwd")
+    _call("tree_attn_fwd", cache.index, cache._code, batch, tokens, heads, cache._struct, rq, rk, rv, d_mask,
+          _ints(token_lens, cache, "token_lens", (batch,)), out.data_ptr(),
+          None if lse is None else _floats(lse, cache, "lse", (batch, tokens, heads)), 0.0 if scale is None else float(scale),
+          _status(status, cache))
     return out
 
 
 def _counted(cache: KVCache, rows, counts, batch: int, tokens: int):
     """(pointer of rows, pointer of counts, max_rows)"""
     if rows is None:
-        max_rows = tokens
-    else:
-        if rows.dim() != 2:
-            raise ValueError("rows must be [batch, max_rows]")
-        max_rows = rows.shape[1]
+        return None, _ints(counts, cache, "counts", (batch,)), tokens
+    if rows.dim() != 2:
+        raise ValueError("rows must be [batch, max_rows]")
+    max_rows = rows.shape[1]
     return _ints(rows, cache, "rows", (batch, max_rows)), _ints(counts, cache, "counts", (batch,)), max_rows
 
 
@@ -210,22 +244,18 @@ def cache_append(cache: KVCache, k_new, v_new, counts=None, rows=None, lens_out=
     and pos the token's position where the cache has them. lens_out, seen_out:
     int32 [batch] that receive the new lengths (None: the cache's own lens and
     seen are advanced)."""
-    if k_new.dim() != 4 or k_new.shape[0] != cache.batch:
-        raise ValueError("k_new must be [batch, tokens, kv_heads, head_dim] with the cache's batch size")
-    batch, tokens = k_new.shape[:2]
-    rk = _rows(k_new, cache, "k_new", batch, tokens, cache.kv_heads)
-    rv = _rows(v_new, cache, "v_new", batch, tokens, cache.kv_heads)
-    d_rows, d_counts, max_rows = _counted(cache, rows, counts, batch, tokens)
-    d_lens = _ints(cache.lens if lens_out is None else lens_out, cache, "lens_out", (batch,))
+    shape = k_new.shape
+    batch = cache.batch
+    if len(shape) != 4 or shape[0] != batch or shape[2] != cache.kv_heads or shape[3] != cache.head_dim:
+        raise ValueError("k_new must be [batch, tokens, kv_heads, head_dim] with the cache's sizes")
+    tokens = shape[1]
     if seen_out is not None and cache.seen is None:
         raise ValueError("seen_out needs a cache with seen")
-    d_seen = _ints(cache.seen if seen_out is None else seen_out, cache, "seen_out", (batch,))
-    d_status = _status_ptr(status, cache.device)
-    with _on_device(cache.device) as stream:
-        rc = library().kv_cache_append(cache._code, batch, tokens, cache._ref, ctypes.byref(rk), ctypes.byref(rv), d_rows,
-                                       d_counts, max_rows, d_lens, d_seen, d_status, stream)
-    if rc != GEMM_TN_OK:
-        raise GemmTnError(rc, "kv_cache_append")
+    d_rows, d_counts, max_rows = _counted(cache, rows, counts, batch, tokens)
+    _call("kv_cache_append", cache.index, cache._code, batch, tokens, cache._struct, _rows(k_new, cache, "k_new", shape),
+          _rows(v_new, cache, "v_new", shape), d_rows, d_counts, max_rows,
+          _ints(cache.lens if lens_out is None else lens_out, cache, "lens_out", (batch,)),
+          _ints(cache.seen if seen_out is None else seen_out, cache, "seen_out", (batch,)), _status(status, cache))
 
 
 def cache_weigh(cache: KVCache, q, lse, counts=None, rows=None, causal=True, scale=None, out=None, status=None):
@@ -236,22 +266,17 @@ def cache_weigh(cache: KVCache, q, lse, counts=None, rows=None, causal=True, sca
     slots' queries and see the slots up to their own; False: every one sees
     every slot. out: fp32 tensor of weight's shape that receives the sums
     (None: the cache's weight, in place). Returns out."""
-    batch, tokens, heads = _new_tokens(cache, q)
+    shape, rq = _queries(q, cache)
+    batch, tokens, heads, _ = shape
     if cache.weight is None:
         raise ValueError("the cache has no weight")
-    rq = _rows(q, cache, "q", batch, tokens, heads)
-    d_lse = _floats(lse, cache, "lse", (batch, tokens, heads))
-    d_rows, d_counts, max_rows = _counted(cache, rows, counts, batch, tokens)
     if out is None:
         out = cache.weight
-    d_out = _floats(out, cache, "out", cache.weight.shape)
-    d_status = _status_ptr(status, cache.device)
-    with _on_device(cache.device) as stream:
-        rc = library().kv_cache_weigh(cache._code, batch, tokens, heads, cache._ref, ctypes.byref(rq), d_lse, d_rows, d_counts,
-                                      max_rows, 1 if causal else 0, 0.0 if scale is None else float(scale), d_out,
-                                      d_status, stream)
-    if rc != GEMM_TN_OK:
-        raise GemmTnError(rc, "kv_cache_weigh")
+    d_rows, d_counts, max_rows = _counted(cache, rows, counts, batch, tokens)
+    _call("kv_cache_weigh", cache.index, cache._code, batch, tokens, heads, cache._struct, rq,
+          _floats(lse, cache, "lse", (batch, tokens, heads)), d_rows, d_counts, max_rows, 1 if causal else 0,
+          0.0 if scale is None else float(scale), _floats(out, cache, "out", (batch, cache.kv_heads, cache.capacity)),
+          _status(status, cache))
     return out
 
 
@@ -262,17 +287,19 @@ def cache_evict(cache: KVCache, keep: int, recent: int = 0, weight_out=None, pos
     that receive the results (None: the cache's own, in place)."""
     if cache.weight is None:
         raise ValueError("the cache has no weight")
-    d_weight = _floats(cache.weight if weight_out is None else weight_out, cache, "weight_out", cache.weight.shape)
     if pos_out is not None and cache.pos is None:
         raise ValueError("pos_out needs a cache with pos")
-    d_pos = _ints(cache.pos if pos_out is None else pos_out, cache, "pos_out", cache.weight.shape)
-    d_lens = _ints(cache.lens if lens_out is None else lens_out, cache, "lens_out", (cache.batch,))
-    d_status = _status_ptr(status, cache.device)
-    with _on_device(cache.device) as stream:
-        rc = library().kv_cache_evict(cache._code, cache.batch, cache._ref, int(keep), int(recent), d_weight, d_pos, d_lens,
-                                      d_status, stream)
-    if rc != GEMM_TN_OK:
-        raise GemmTnError(rc, "kv_cache_evict")
+    batch = cache.batch
+    shape = (batch, cache.kv_heads, cache.capacity)
+    _call("kv_cache_evict", cache.index, cache._code, batch, cache._struct, int(keep), int(recent),
+          _floats(cache.weight if weight_out is None else weight_out, cache, "weight_out", shape),
+          _ints(cache.pos if pos_out is None else pos_out, cache, "pos_out", shape),
+          _ints(cache.lens if lens_out is None else lens_out, cache, "lens_out", (batch,)), _status(status, cache))
+
+
+def _torch():
+    import torch
+    return torch
 
 
 def tree_mask(parents):
