@@ -25,7 +25,8 @@ BUILD_DIR = ROOT / "_build" / "gemm_tn"
 LIBRARY = PKG / "libgemm_tn.so"
 
 SOURCES = ["gemm_tn_api.cu", "sm103_gemm_1cta.cu", "sm103_gemm_2cta.cu", "sm103_gemm_nn.cu", "sm103_gemm_fused.cu",
-           "sm103_flash_attn.cu", "repack.cu", "sm103_gemm_splitk.cu", "sm103_tree_attn.cu", "sm103_cache_weigh.cu",
+           "sm103_flash_attn.cu", "repack.cu", "sm103_gemm_splitk.cu", "sm103_tree_attn.cu", "sm103_decode_attn.cu",
+           "sm103_cache_weigh.cu",
            "kv_cache_ops.cu", "kv_cache_api.cu"]
 GENCODE = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ["-O3", "-std=c++17", "-lineinfo", "--expt-relaxed-constexpr", "-Xcompiler", "-fPIC",

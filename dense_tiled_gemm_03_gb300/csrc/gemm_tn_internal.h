@@ -39,19 +39,21 @@ struct TreeArgs {
   const int32_t* lens;      // [batch] cached keys
   const int32_t* token_lens;   // [batch] new tokens, or NULL: all
   const int32_t* page_table;   // [batch] rows of page numbers, table_stride apart
-  float* part_o;            // workspace: [2 chunks][dim / 4][units * 128][4] unnormalised rows of cut items
-  float2* part_ml;          // [2 chunks][units * 128]: their (maximum, sum)
+  float* part_o;            // workspace: [2 chunks][dim / 4][part_rows][4] unnormalised rows of cut items
+  float2* part_ml;          // [2 chunks][part_rows]: their (maximum, sum)
   int32_t* cuts;            // [chunks][8]: the item that each chunk begins inside of
   int64_t table_stride;
   int batch, tokens, heads, kv_heads, group;
   int page_size, num_pages, capacity;   // capacity: cached keys that a page table row can hold
   int mask_words;
-  int tile_tokens;          // tokens per 128-row tile: floor(128 / group)
+  int part_rows;            // rows per item (units * 128; the decode kernel's 16 or 32)
+  int tile_tokens;          // tokens per row tile: floor(128 / group) (the decode kernel: all)
   int units;                // row tiles per item: 1 (both units share the rows) or 2
   int row_units;            // items per KV head of a sequence
   int has_new;
   int chunks;               // CTAs
   int min_chunk;            // least key tiles per CTA
+  int whole;                // 1: chunks take whole items (nothing is cut, part_o, part_ml and cuts are NULL)
   float scale_log2;         // softmax scale * log2(e), > 0
   int* status;
   uint64_t timeout_ns;
@@ -185,6 +187,11 @@ cudaError_t launch_flash_attn(int head_dim, bool bf16, const gemm_tn_dev::FlashA
 // kernel that joins the items its chunks cut.
 int tree_attn_tile_rows();
 cudaError_t launch_tree_attn(int head_dim, bool bf16, const gemm_tn_dev::TreeArgs& args, cudaStream_t stream);
+// The same for items of at most decode_attn_rows() query rows, with keys on the
+// tensor memory's lanes; args.part_rows is decode_attn_part_rows(rows).
+int decode_attn_rows();
+int decode_attn_part_rows(int rows);
+cudaError_t launch_decode_attn(int head_dim, bool bf16, const gemm_tn_dev::TreeArgs& args, cudaStream_t stream);
 cudaError_t launch_tree_attn_join(int head_dim, bool bf16, const gemm_tn_dev::TreeArgs& args, cudaStream_t stream);
 cudaError_t launch_cache_weigh(int head_dim, bool bf16, const gemm_tn_dev::WeighArgs& args, cudaStream_t stream);
 // Copies the rows; lens_out and seen_out are written by it, or (where one of

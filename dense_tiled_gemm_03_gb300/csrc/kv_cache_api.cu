@@ -7,6 +7,7 @@
 #include <algorithm>
 #include <cmath>
 #include <cstdint>
+#include <cstdlib>
 
 #include "gemm_tn_internal.h"
 #include "kv_cache.h"
@@ -135,6 +136,12 @@ gemm_tn_dev::CacheView view_of(const kv_cache* c, int64_t batch) {
 // Least key tiles per CTA of the attention.
 constexpr int kMinChunk = 2;
 
+// Most key tiles of an item (as far as the host can tell) that is not cut.
+int64_t whole_tiles() {
+  const char* s = std::getenv("WT");
+  return s ? atoi(s) : 8;
+}
+
 // The kernels count key tiles in 32 bits: an upper bound of their number, from
 // what the cache and the inputs can hold.
 int check_tiles(const kv_cache* c, int64_t batch, int64_t row_units, int64_t tokens) {
@@ -181,9 +188,11 @@ int tree_attn_fwd(int dtype, int64_t batch, int64_t tokens, int64_t heads, const
     return invalid("o overlaps an input or the cache");
   alignas(64) gemm_tn_dev::TreeArgs args{};
   args.group = static_cast<int>(heads / kv_heads);
-  args.tile_tokens = tree_attn_tile_rows() / args.group;
+  const bool decode = tokens * args.group <= decode_attn_rows() && !std::getenv("NODEC");
+  args.tile_tokens = decode ? static_cast<int>(tokens) : tree_attn_tile_rows() / args.group;
   const int64_t row_tiles = (tokens + args.tile_tokens - 1) / args.tile_tokens;
   args.units = row_tiles > 1 ? 2 : 1;
+  args.part_rows = decode ? decode_attn_part_rows(static_cast<int>(tokens) * args.group) : args.units * tree_attn_tile_rows();
   args.row_units = static_cast<int>((row_tiles + args.units - 1) / args.units);
   if ((st = check_tiles(cache, batch, args.row_units, tokens)) != GEMM_TN_OK) return st;
   int sms = 0;
@@ -214,22 +223,34 @@ int tree_attn_fwd(int dtype, int64_t batch, int64_t tokens, int64_t heads, const
   args.mask_words = static_cast<int>((tokens + 63) / 64);
   args.has_new = has_new ? 1 : 0;
   args.chunks = sms;
-  args.min_chunk = kMinChunk;
+  args.min_chunk = std::getenv("MC") ? atoi(std::getenv("MC")) : kMinChunk;
   args.scale_log2 = scale_log2(softmax_scale, dim);
   args.status = d_status;
   args.timeout_ns = api_watchdog_ns();
   args.drop_load_block = api_drop_load();
 
-  const size_t part_rows = static_cast<size_t>(2 * args.chunks) * static_cast<size_t>(args.units * tree_attn_tile_rows());
-  void* workspace = nullptr;
+  // items of few tiles are not cut
+  const int64_t item_tiles = (args.capacity + 127) / 128 + (has_new ? (tokens + 127) / 128 : 0);
+  args.whole = item_tiles <= whole_tiles() || sms == 1 ? 1 : 0;
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  auto launch = [&] {
+    return decode ? launch_decode_attn(static_cast<int>(dim), bf16, args, s)
+                  : launch_tree_attn(static_cast<int>(dim), bf16, args, s);
+  };
+  if (args.whole != 0) {
+    args.min_chunk = 1;
+    const cudaError_t e = api_counted(launch());
+    return e == cudaSuccess ? GEMM_TN_OK : api_fail_cuda(e, "tree attention launch");
+  }
+  const size_t part_rows = static_cast<size_t>(2 * args.chunks) * static_cast<size_t>(args.part_rows);
+  void* workspace = nullptr;
   cudaError_t e = api_workspace(part_rows * static_cast<size_t>(dim * 4 + 8) + static_cast<size_t>(args.chunks) * 32, s, &workspace);
   if (e != cudaSuccess) return api_fail_cuda(e, "workspace");
   args.part_o = static_cast<float*>(workspace);
   args.part_ml = reinterpret_cast<float2*>(args.part_o + part_rows * static_cast<size_t>(dim));
   args.cuts = reinterpret_cast<int32_t*>(args.part_ml + part_rows);
-  e = api_counted(launch_tree_attn(static_cast<int>(dim), bf16, args, s));
-  if (e == cudaSuccess && args.chunks > 1) e = api_counted(launch_tree_attn_join(static_cast<int>(dim), bf16, args, s));
+  e = api_counted(launch());
+  if (e == cudaSuccess) e = api_counted(launch_tree_attn_join(static_cast<int>(dim), bf16, args, s));
   const cudaError_t freed = cudaFreeAsync(workspace, s);
   if (e != cudaSuccess) return api_fail_cuda(e, "tree attention launch");
   return freed == cudaSuccess ? GEMM_TN_OK : api_fail_cuda(freed, "cudaFreeAsync (workspace)");

@@ -1,0 +1,638 @@
+// sm103_decode_attn.cu -- attention over a paged cache for few query rows: at
+// most 32 per KV head (one token of a group of 8, a small tree), the decode
+// step of tree_attn_fwd (include/kv_cache.h; the schedule, the parts of cut
+// items and their join are sm103_tree_attn.cu's).
+//
+// With rows on the tensor memory's lanes, as in sm103_tree_attn.cu, a tile of
+// 128 keys costs its one or two busy warps 128 exponentials however few rows
+// there are, all on one of the SM's four sub-partitions: 0.9 us a tile, with
+// 64 KB a tile due from memory every 1.5 us. Here both products are transposed:
+//   S^T = K Q^T   (M = 128 keys, N = 16 or 32 rows, K = dim)
+//   O^T += V^T P^T  (M = dim, N = rows, K = 128 keys; V's tile as it lies is an
+//                    MN-major A operand, P is the K-major B operand in shared memory)
+// A thread has one key: it computes one exponential per row, 16 or 32 a tile,
+// four warps a tile on four sub-partitions, and the tensor cores' work falls
+// with N as well. What the row-wise form gets for free has to cross threads:
+// a row's maximum (taken from the first tile, and again only when a probability
+// passes 2^8) and, once per segment, its sum. Every thread of a unit holds the
+// same row references; the four warps of a unit agree through an mbarrier once
+// a tile whether a reference has to move. The epilogue has dim on the lanes, so
+// rows go out in contiguous pieces.
+//
+// Roles: warp 0 TMA producer (lane l copies the tile's l-th page), warp 1 MMA
+// issuer, warps 2-5 and 6-9 two units that take every other key tile and are
+// joined at the end of a segment.
+#include <cuda.h>
+#include <cuda_runtime.h>
+
+#include <atomic>
+#include <cstdint>
+
+#include "gemm_tn_internal.h"
+#include "sm103_tree_attn.cuh"
+
+namespace gemm_tn_dev {
+
+namespace da {
+
+using cache::kTileKeys;
+constexpr int kProducerWarp = 0;
+constexpr int kMmaWarp = 1;
+constexpr int kFirstSoftmaxWarp = 2;
+constexpr int kMaxRows = 32;
+
+template <int kDim_, bool kBf16_, int kRows_>
+struct Cfg {
+  static constexpr int kDim = kDim_;
+  static constexpr bool kBf16 = kBf16_;
+  static constexpr int kRows = kRows_;                    // N of both products
+  static constexpr int kNumThreads = 64 + 256;
+  static constexpr int kDimBoxes = kDim / 64;
+  static constexpr uint32_t kBoxBytes = 128u * 128u;      // 128 keys x 128 bytes
+  static constexpr uint32_t kTileBytes = kDimBoxes * kBoxBytes;
+  static constexpr uint32_t kQBoxBytes = kRows * 128u;    // rows x 64 elements of dim
+  static constexpr uint32_t kQBytes = kDimBoxes * kQBoxBytes;
+  static constexpr uint32_t kPBoxBytes = kRows * 128u;    // rows x 64 keys
+  static constexpr uint32_t kPBytes = 2 * kPBoxBytes;
+  static constexpr int kStages = kDim == 64 ? 6 : 3;      // of K and of V
+  static constexpr uint32_t kOffK = 0;
+  static constexpr uint32_t kOffV = kOffK + kStages * kTileBytes;
+  static constexpr uint32_t kOffP = kOffV + kStages * kTileBytes;   // one per unit
+  static constexpr uint32_t kOffQ = kOffP + 2 * kPBytes;            // two slots
+  static constexpr uint32_t kOffWarps = kOffQ + 2 * kQBytes;          // [2 units][4 warps][32 rows]: a tile's maxima, a segment's sums
+  static constexpr uint32_t kOffRef = kOffWarps + 2u * 4u * 32u * 4u; // [2 units][32 rows]
+  static constexpr uint32_t kOffBar = kOffRef + 2u * 32u * 4u;
+  // q_full[2], q_empty[2], k_full[S], k_empty[S], v_full[S], v_empty[S],
+  // s_full[2], p_full[2], o_done[2], agree[2], xch_full, xch_empty, drain
+  static constexpr int kNumBars = 4 + 4 * kStages + 8 + 3;
+  static constexpr uint32_t kOffVote = kOffBar + 8u * kNumBars;     // [2 units][3]
+  static constexpr uint32_t kOffTmemSlot = kOffVote + 24u;
+  static constexpr uint32_t kOffAbort = kOffTmemSlot + 4u;
+  static constexpr uint32_t kOffStart = kOffAbort + 4u;   // the chunk's first Walk
+  static constexpr uint32_t kOffWalkSums = kOffStart + 36u;
+  static constexpr uint32_t kSmemBytes = kOffWalkSums + 128u + 1024u;   // + slack to align the base to 1024
+  static constexpr uint32_t kTmemCols = 4 * kRows;        // S_0, S_1, O_0, O_1
+  static constexpr uint32_t kIdescS = mma_idesc_f16(kBf16, kTileKeys, kRows, false);
+  // A is V^T, MN-major (bit 15). Dim 64 runs with M = 128: the lanes from 64 on
+  // multiply whatever lies 8 KB further on and are not looked at.
+  static constexpr uint32_t kIdescO = mma_idesc_f16(kBf16, 128, kRows, false) | (1u << 15);
+  static constexpr uint32_t kVBlockBytes = kDim == 128 ? kBoxBytes : 8192u;
+  static_assert(kRows == 16 || kRows == 32, "rows");
+  static_assert(kSmemBytes <= 227u * 1024u, "shared memory budget");
+  static_assert(kOffBar % 8u == 0, "64-bit shared words");
+};
+
+// The largest value of x over the warp (NaN is passed over).
+__device__ __forceinline__ float warp_max(float x) {
+  float y;
+  asm("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+// Sums kRows values over the 32 lanes: lane r (and r + 16 with 16 rows) gets row
+// r's. Halves the rows at every exchange.
+template <int kRows>
+__device__ __forceinline__ float warp_row_sums(float (&l)[kRows], uint32_t lane) {
+#pragma unroll
+  for (int half = kRows / 2; half >= 1; half /= 2) {
+    const bool upper = (lane & static_cast<uint32_t>(half)) != 0;
+#pragma unroll
+    for (int i = 0; i < half; ++i) {
+      const float keep = upper ? l[i + half] : l[i], give = upper ? l[i] : l[i + half];
+      l[i] = keep + __shfl_xor_sync(0xffffffffu, give, half);
+    }
+  }
+  if constexpr (kRows == 16) l[0] += __shfl_xor_sync(0xffffffffu, l[0], 16);
+  return l[0];
+}
+
+template <int kRows>
+__device__ __forceinline__ void tmem_load_rows(uint32_t taddr, float (&v)[kRows]) {
+  if constexpr (kRows == 32) {
+    uint32_t raw[32];
+    tmem_load_32x32(taddr, raw);
+    tmem_load_wait();
+#pragma unroll
+    for (int e = 0; e < 32; ++e) v[e] = __uint_as_float(raw[e]);
+  } else {
+    uint32_t raw[16];
+    tmem_load_32x16(taddr, raw);
+    tmem_load_wait();
+#pragma unroll
+    for (int e = 0; e < 16; ++e) v[e] = __uint_as_float(raw[e]);
+  }
+}
+
+template <int kRows>
+__device__ __forceinline__ void tmem_store_rows(uint32_t taddr, const float (&v)[kRows]) {
+  uint32_t raw[kRows];
+#pragma unroll
+  for (int e = 0; e < kRows; ++e) raw[e] = __float_as_uint(v[e]);
+  if constexpr (kRows == 32) tmem_store_32x32(taddr, raw);
+  else tmem_store_32x16(taddr, raw);
+}
+
+}  // namespace da
+
+template <class C>
+__global__ void __launch_bounds__(C::kNumThreads, 1) decode_attn_kernel(const __grid_constant__ TreeArgs args) {
+  extern __shared__ uint8_t smem_raw[];
+  const uint32_t raw_addr = smem_addr(smem_raw);
+  uint8_t* smem = smem_raw + (((raw_addr + 1023u) & ~1023u) - raw_addr);
+  const uint32_t base = smem_addr(smem);
+  const uint32_t warp = threadIdx.x >> 5;
+  const uint32_t lane = lane_id();
+
+  auto q_slot = [&](int s) { return base + C::kOffQ + s * C::kQBytes; };
+  auto k_tile = [&](int s) { return base + C::kOffK + s * C::kTileBytes; };
+  auto v_tile = [&](int s) { return base + C::kOffV + s * C::kTileBytes; };
+  auto p_tile = [&](int u) { return base + C::kOffP + u * C::kPBytes; };
+  auto bar = [&](int i) { return base + C::kOffBar + 8u * i; };
+  constexpr int kKBar = 4, kVBar = kKBar + 2 * C::kStages, kUBar = kVBar + 2 * C::kStages;
+  auto q_full = [&](int s) { return bar(s); };
+  auto q_empty = [&](int s) { return bar(2 + s); };
+  auto k_full = [&](int s) { return bar(kKBar + s); };
+  auto k_empty = [&](int s) { return bar(kKBar + C::kStages + s); };
+  auto v_full = [&](int s) { return bar(kVBar + s); };
+  auto v_empty = [&](int s) { return bar(kVBar + C::kStages + s); };
+  auto s_full = [&](int u) { return bar(kUBar + u); };
+  auto p_full = [&](int u) { return bar(kUBar + 2 + u); };
+  auto o_done = [&](int u) { return bar(kUBar + 4 + u); };
+  auto agree = [&](int u) { return bar(kUBar + 6 + u); };
+  const uint32_t xch_full = bar(kUBar + 8), xch_empty = bar(kUBar + 9), drain_bar = bar(kUBar + 10);
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + C::kOffTmemSlot);
+  volatile uint32_t* abort_flag = reinterpret_cast<volatile uint32_t*>(smem + C::kOffAbort);
+  ta::Walk* start_walk = reinterpret_cast<ta::Walk*>(smem + C::kOffStart);
+  int* sums = reinterpret_cast<int*>(smem + C::kOffWalkSums);
+  float* warp_maxima = reinterpret_cast<float*>(smem + C::kOffWarps);
+  float* warp_sums = warp_maxima;
+  float* unit_refs = reinterpret_cast<float*>(smem + C::kOffRef);
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < 2; ++s) {
+      mbar_init(q_full(s), 1);
+      mbar_init(q_empty(s), 1);
+      mbar_init(s_full(s), 1);
+      mbar_init(p_full(s), 4);   // one arrival per softmax warp of the unit
+      mbar_init(o_done(s), 1);
+      mbar_init(agree(s), 4);
+    }
+    for (int s = 0; s < C::kStages; ++s) {
+      mbar_init(k_full(s), 1);
+      mbar_init(k_empty(s), 1);
+      mbar_init(v_full(s), 1);
+      mbar_init(v_empty(s), 1);
+    }
+    mbar_init(xch_full, 8);
+    mbar_init(xch_empty, 4);
+    mbar_init(drain_bar, 1);
+    *abort_flag = 0u;
+    start_walk->left = 0;
+    fence_barrier_init();
+  }
+  if (warp == da::kProducerWarp && lane == 0) {
+    tma_prefetch_descriptor(&args.tmap_q);
+    tma_prefetch_descriptor(&args.tmap_k);
+    tma_prefetch_descriptor(&args.tmap_v);
+  }
+  if (warp == da::kMmaWarp) {
+    tmem_alloc<1>(smem_addr(tmem_slot), C::kTmemCols);
+    tmem_relinquish<1>();
+  }
+  // rows of Q past the item's stay zero
+  for (uint32_t x = threadIdx.x; x < 2 * C::kQBytes / 16; x += C::kNumThreads)
+    st_shared_v4(base + C::kOffQ + 16u * x, 0u, 0u, 0u, 0u);
+  if (threadIdx.x < 6) reinterpret_cast<uint32_t*>(smem + C::kOffVote)[threadIdx.x] = 0u;
+  fence_proxy_async_shared();
+  // The set-up above may overlap the end of the previous kernel in the
+  // stream; global memory is touched only once that kernel has completed.
+  griddep_wait();
+  griddep_launch_dependents();
+  ta::find_walk(args, start_walk, sums);
+  tc_fence_before_sync();
+  __syncthreads();
+  tc_fence_after_sync();
+  const uint32_t tmem_base = *tmem_slot;
+  const cache::Watch wd{args.status, args.timeout_ns, abort_flag};
+  const bool has_new = args.has_new != 0;
+  ta::Walk w = *start_walk;
+  if (threadIdx.x == 0) ta::note_no_cut(args, w);
+
+  if (warp == da::kProducerWarp) {
+    // -------------------------------------------------------------- TMA producer
+    int issued_k[C::kStages], issued_v[C::kStages], issued_q[2] = {-1, -1};
+#pragma unroll
+    for (int s = 0; s < C::kStages; ++s) issued_k[s] = issued_v[s] = -1;
+    const int box_rows = min(args.page_size, da::kTileKeys);
+    const int tile_pages = da::kTileKeys / box_rows;   // pages (or parts of one) per tile
+    const uint32_t q_bytes = static_cast<uint32_t>(args.tokens * args.group) * 128u * C::kDimBoxes;
+    int s = 0;             // ring stage and phase of the next tile
+    uint32_t ph = 0;
+    int it = 0, seg = 0;
+    bool ok = true;
+    for (; ok && w.more(); w.next(args), ++seg) {
+      const int32_t* table = args.page_table + static_cast<int64_t>(w.b) * args.table_stride;
+      auto page_of = [&](int j) {
+        return ta::page_of(args, table, ta::tile_of(w.len, w.tl, has_new, j), box_rows, static_cast<int>(lane));
+      };
+      int page = page_of(w.j0);
+      const int slot = seg & 1;
+      const uint32_t q_ph = static_cast<uint32_t>(seg >> 1) & 1u;
+      if (!(ok = wd.warp_wait(q_empty(slot), q_ph ^ 1u))) break;
+      if (lane == 0) {
+        mbar_arrive_expect_tx(q_full(slot), q_bytes);
+        for (int c = 0; c < C::kDimBoxes; ++c)
+          tma_load_4d(&args.tmap_q, q_slot(slot) + c * C::kQBoxBytes, q_full(slot), 64 * c, w.h * args.group, 0, w.b);
+      }
+      issued_q[slot] = static_cast<int>(q_ph);
+      for (int j = w.j0; j < w.j0 + w.count; ++j, ++it) {
+        const ta::Tile t = ta::tile_of(w.len, w.tl, has_new, j);
+        const int boxes = t.fresh ? (t.valid > 0 ? 1 : 0) : (t.valid + box_rows - 1) / box_rows;
+        const uint32_t bytes = static_cast<uint32_t>(boxes * (t.fresh ? da::kTileKeys : box_rows)) * 128u * C::kDimBoxes;
+        const int slot0 = t.fresh ? t.index * da::kTileKeys
+                                  : (tile_pages == 1 ? (t.index * da::kTileKeys) % args.page_size : 0);
+        const bool mine = static_cast<int>(lane) < boxes;
+        if (!(ok = wd.warp_wait(k_empty(s), ph ^ 1u))) break;
+        if (lane == 0) mbar_arrive_expect_tx(k_full(s), bytes);
+        __syncwarp();
+        if (mine && !(blockIdx.x == 0 && it == args.drop_load_block)) {
+          for (int c = 0; c < C::kDimBoxes; ++c)
+            tma_load_4d(t.fresh ? &args.tmap_k_new : &args.tmap_k, k_tile(s) + c * C::kBoxBytes + lane * box_rows * 128u,
+                        k_full(s), 64 * c, w.h, slot0, t.fresh ? w.b : page);
+        }
+#pragma unroll
+        for (int x = 0; x < C::kStages; ++x)
+          if (x == s) issued_k[x] = static_cast<int>(ph);
+        if (!(ok = wd.warp_wait(v_empty(s), ph ^ 1u))) break;
+        if (lane == 0) mbar_arrive_expect_tx(v_full(s), bytes);
+        __syncwarp();
+        if (mine) {
+          for (int c = 0; c < C::kDimBoxes; ++c)
+            tma_load_4d(t.fresh ? &args.tmap_v_new : &args.tmap_v, v_tile(s) + c * C::kBoxBytes + lane * box_rows * 128u,
+                        v_full(s), 64 * c, w.h, slot0, t.fresh ? w.b : page);
+        }
+#pragma unroll
+        for (int x = 0; x < C::kStages; ++x)
+          if (x == s) issued_v[x] = static_cast<int>(ph);
+        if (j + 1 < w.j0 + w.count) page = page_of(j + 1);
+        if (++s == C::kStages) {
+          s = 0;
+          ph ^= 1u;
+        }
+      }
+    }
+    // Loads may still be landing if another role gave up: wait (bounded) for
+    // every phase issued before the CTA may exit.
+    for (int x = 0; x < 2; ++x)
+      if (issued_q[x] >= 0) wd.drain(q_full(x), static_cast<uint32_t>(issued_q[x]));
+#pragma unroll
+    for (int x = 0; x < C::kStages; ++x) {
+      if (issued_k[x] >= 0) wd.drain(k_full(x), static_cast<uint32_t>(issued_k[x]));
+      if (issued_v[x] >= 0) wd.drain(v_full(x), static_cast<uint32_t>(issued_v[x]));
+    }
+  } else if (warp == da::kMmaWarp) {
+    if (lane == 0) {
+      // ------------------------------------------------------------ MMA issuer
+      int it0 = 0;                    // ring number of the segment's first tile
+      int seg = 0;
+      int done[2] = {0, 0};           // tiles of each unit whose P has been asked for
+      bool ok = true;
+      for (; ok && w.more(); it0 += w.count, w.next(args), ++seg) {
+        const int slot = seg & 1;
+        auto issue_s = [&](int u, int i) {   // i: tile of the segment
+          const int x = it0 + i, s = x % C::kStages;
+          if (!wd.wait(k_full(s), static_cast<uint32_t>(x / C::kStages) & 1u)) return false;
+          tc_fence_after_sync();
+#pragma unroll
+          for (int c = 0; c < C::kDimBoxes; ++c) {
+            const uint64_t a_desc = sw128_kmajor_desc(k_tile(s) + c * C::kBoxBytes);
+            const uint64_t b_desc = sw128_kmajor_desc(q_slot(slot) + c * C::kQBoxBytes);
+#pragma unroll
+            for (int kk = 0; kk < 4; ++kk)   // 16 elements of dim = 32 bytes = 2 descriptor units
+              mma_f16<1>(tmem_base + static_cast<uint32_t>(C::kRows * u), a_desc + 2u * kk, b_desc + 2u * kk, C::kIdescS,
+                         (c | kk) != 0 ? 1u : 0u);
+          }
+          mma_commit(s_full(u));
+          mma_commit(k_empty(s));
+          if (i == w.count - 1) mma_commit(q_empty(slot));   // Q has been read for the last time
+          return true;
+        };
+        if (!(ok = wd.wait(q_full(slot), static_cast<uint32_t>(seg >> 1) & 1u))) break;
+        ok = issue_s(0, 0) && (w.count < 2 || issue_s(1, 1));
+        for (int i = 0; ok && i < w.count; ++i) {
+          const int x = it0 + i, s = x % C::kStages, u = i & 1;
+          if (!(ok = wd.wait(v_full(s), static_cast<uint32_t>(x / C::kStages) & 1u))) break;
+          if (!(ok = wd.wait(p_full(u), static_cast<uint32_t>(done[u]) & 1u))) break;
+          ++done[u];
+          tc_fence_after_sync();
+          const int steps = (ta::tile_of(w.len, w.tl, has_new, w.j0 + i).valid + 15) / 16;
+          const uint64_t a_desc = sw128_mnmajor_desc(v_tile(s), C::kVBlockBytes);
+          const uint64_t b_desc = sw128_kmajor_desc(p_tile(u));
+          const uint32_t t_o = tmem_base + static_cast<uint32_t>(C::kRows * (2 + u));
+          auto pv = [&](int kk) {   // 16 keys: 16 rows of 128 bytes of V; 32 bytes of P's rows, 64 keys a box
+            mma_f16<1>(t_o, a_desc + ((static_cast<uint32_t>(kk) * 2048u) >> 4),
+                       b_desc + ((static_cast<uint32_t>(kk >> 2) * C::kPBoxBytes) >> 4) + 2u * static_cast<uint32_t>(kk & 3),
+                       C::kIdescO, i < 2 && kk == 0 ? 0u : 1u);
+          };
+          if (steps == 8) {
+#pragma unroll
+            for (int kk = 0; kk < 8; ++kk) pv(kk);
+          } else {
+            for (int kk = 0; kk < steps; ++kk) pv(kk);
+          }
+          mma_commit(v_empty(s));
+          if (i + 2 < w.count) ok = issue_s(u, i + 2);
+          else mma_commit(o_done(u));
+        }
+      }
+      // every MMA issued here must finish before TMEM is freed
+      mma_commit(drain_bar);
+      wd.drain(drain_bar, 0);
+    }
+  } else {
+    // -------------------------------------------------------------- softmax
+    const int u = (static_cast<int>(warp) - da::kFirstSoftmaxWarp) >> 2;   // unit
+    const uint32_t quarter = warp & 3u;                                    // TMEM lanes 32*quarter ..
+    const int key = static_cast<int>(quarter * 32u + lane);                // of the tile; column of O in the end
+    const uint32_t lane_off = (quarter * 32u) << 16;
+    const uint32_t t_s = tmem_base + lane_off + static_cast<uint32_t>(C::kRows * u);
+    const uint32_t t_o = tmem_base + lane_off + static_cast<uint32_t>(C::kRows * (2 + u));
+    const float c_log2 = args.scale_log2;
+    volatile uint32_t* votes = reinterpret_cast<volatile uint32_t*>(smem + C::kOffVote) + 3 * u;
+    float* my_maxima = warp_maxima + (u * 4 + static_cast<int>(quarter)) * 32;
+    uint32_t tiles_done = 0;        // tiles of this unit so far
+    uint32_t agreed = 0;            // phases of agree(u) so far
+    uint32_t voted = 0;             // votes so far
+    uint32_t ends[2] = {0, 0};      // o_done phases of the units so far
+    uint32_t segs = 0;
+    int it0 = 0;
+    bool ok = true;
+    // the unit's four warps meet (bounded)
+    auto meet = [&]() {
+      __syncwarp();
+      if (lane == 0) mbar_arrive(agree(u));
+      return wd.warp_wait(agree(u), agreed++ & 1u);
+    };
+    for (; ok && w.more(); it0 += w.count, w.next(args), ++segs) {
+      const int rows = w.tl * args.group;   // rows that exist, token-major
+      const uint32_t row_bits = cache::low_bits(rows);
+      uint32_t unset = row_bits;            // rows that have seen no key yet
+      float neg_m[C::kRows], l[C::kRows];   // minus the row's reference, in units of scale * log2e; this key lane's sum
+#pragma unroll
+      for (int r = 0; r < C::kRows; ++r) neg_m[r] = l[r] = 0.0f;
+      for (int i = u; i < w.count && ok; i += 2) {
+        // S_u for this tile is complete, and with it O_u += P_u V of the tile before
+        if (!(ok = wd.warp_wait(s_full(u), tiles_done & 1u))) break;
+        ++tiles_done;
+        tc_fence_after_sync();
+        const ta::Tile t = ta::tile_of(w.len, w.tl, has_new, w.j0 + i);
+        float s[C::kRows];
+        da::tmem_load_rows<C::kRows>(t_s, s);
+        uint32_t seen = key < t.valid ? 0xffffffffu : 0u;   // rows that see this thread's key
+        if (t.fresh && key < t.valid) {
+          // bit r / group of the word: whether that token sees this key
+          uint32_t tokens = 0;
+          if (args.mask == nullptr) {
+            tokens = ~cache::low_bits(key);
+          } else {
+            const uint64_t* words = args.mask + static_cast<int64_t>(w.b) * args.tokens;   // at most 32 tokens: one word each
+            for (int x = 0; x < w.tl; ++x) tokens |= static_cast<uint32_t>((__ldg(words + x) >> key) & 1ull) << x;
+          }
+          seen = 0;
+          for (int r = 0; r < rows; ++r) seen |= ((tokens >> (r / args.group)) & 1u) << r;
+        }
+        if (t.fresh || t.valid < da::kTileKeys) {
+#pragma unroll
+          for (int r = 0; r < C::kRows; ++r)
+            if (!((seen >> r) & 1u)) s[r] = -INFINITY;
+        }
+        float p[C::kRows];
+        bool over = unset != 0;
+        if (!over) {
+          // against the references at once; a probability past 2^8 calls for new ones
+          bool mine = false;
+#pragma unroll
+          for (int r = 0; r < C::kRows; ++r) {
+            p[r] = ex2_approx(fmaf(s[r], c_log2, neg_m[r]));
+            mine |= !(p[r] <= 256.0f) && ((row_bits >> r) & 1u);
+          }
+          // three words in turn: the next one is cleared before this meeting,
+          // after the meeting in which its last vote was read
+          const uint32_t word = voted % 3u;
+          if (quarter == 0 && lane == 0) votes[(word + 1u) % 3u] = 0u;
+          if (__any_sync(0xffffffffu, mine) && lane == 0) votes[word] = 1u;
+          if (!(ok = meet())) break;
+          over = votes[word] != 0u;
+          ++voted;
+        }
+        if (over) {
+          // the tile's row maxima over the unit's 128 keys
+#pragma unroll
+          for (int r = 0; r < C::kRows; ++r) {
+            const float mx = da::warp_max(s[r]);
+            if (lane == static_cast<uint32_t>(r)) my_maxima[r] = mx;
+          }
+          if (!(ok = meet())) break;
+          float alpha[C::kRows];
+          bool moved = false;
+#pragma unroll
+          for (int r = 0; r < C::kRows; ++r) {
+            const float* x = warp_maxima + u * 128 + r;
+            const float mx = fmaxf(fmaxf(x[0], x[32]), fmaxf(x[64], x[96])) * c_log2;
+            alpha[r] = 1.0f;
+            if ((unset >> r) & 1u) {
+              if (mx != -INFINITY) {
+                neg_m[r] = -mx;
+                unset &= ~(1u << r);
+              }
+            } else if (mx > 8.0f - neg_m[r] && ((row_bits >> r) & 1u)) {
+              alpha[r] = ex2_approx(-neg_m[r] - mx);
+              neg_m[r] = -mx;
+              l[r] *= alpha[r];
+              moved = true;
+            }
+            p[r] = ex2_approx(fmaf(s[r], c_log2, neg_m[r]));
+          }
+          if (moved) {   // the same in every thread of the unit
+            float o[C::kRows];
+            da::tmem_load_rows<C::kRows>(t_o, o);
+#pragma unroll
+            for (int r = 0; r < C::kRows; ++r) o[r] *= alpha[r];
+            da::tmem_store_rows<C::kRows>(t_o, o);
+            tmem_store_wait();
+          }
+          // the maxima are not written again before every warp has read them
+          if (!(ok = meet())) break;
+        }
+        // P: row r's 64-key boxes of 128 bytes, 16-byte pieces swizzled by the row
+        const uint32_t p_at = p_tile(u) + static_cast<uint32_t>(key >> 6) * C::kPBoxBytes + 2u * static_cast<uint32_t>(key & 7);
+        const uint32_t piece = static_cast<uint32_t>(key & 63) >> 3;
+#pragma unroll
+        for (int r = 0; r < C::kRows; ++r) {
+          l[r] += p[r];
+          st_shared_u16(p_at + 128u * r + 16u * (piece ^ (r & 7u)), static_cast<uint16_t>(cache::pack2<C::kBf16>(p[r], 0.0f)));
+        }
+        if (t.valid % 16 != 0) {
+          // zero the rows of V behind the last key, up to the end of its 16-key step
+          const int x = it0 + i, st = x % C::kStages;
+          if (!(ok = wd.warp_wait(v_full(st), static_cast<uint32_t>(x / C::kStages) & 1u))) break;
+          const int row_end = (t.valid + 15) / 16 * 16;
+          for (int y = t.valid * 8 + key; y < row_end * 8; y += 128)
+#pragma unroll
+            for (int c = 0; c < C::kDimBoxes; ++c) st_shared_v4(v_tile(st) + c * C::kBoxBytes + 16u * y, 0u, 0u, 0u, 0u);
+        }
+        fence_proxy_async_shared();
+        tc_fence_before_sync();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(p_full(u));
+      }
+      if (!ok) break;
+      // ---------------------------------------------------------- end of a segment
+      // references and sums to shared memory; unit 0 joins the two units' rows
+      {
+        const float sum = da::warp_row_sums<C::kRows>(l, lane);
+        if (lane < C::kRows) warp_sums[(u * 4 + static_cast<int>(quarter)) * 32 + static_cast<int>(lane)] = sum;
+        if (quarter == 0) {
+#pragma unroll
+          for (int r = 0; r < C::kRows; ++r)
+            if (lane == static_cast<uint32_t>(r)) unit_refs[u * 32 + r] = -neg_m[r];
+        }
+        const bool both = w.count > 1;
+        if (u < w.count) {
+          if (!(ok = wd.warp_wait(o_done(u), ends[u] & 1u))) break;
+          ++ends[u];
+        }
+        tc_fence_before_sync();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(xch_full);
+        if (u == 0) {
+          if (both) {
+            if (!(ok = wd.warp_wait(o_done(1), ends[1] & 1u))) break;
+            ++ends[1];
+          }
+          if (!(ok = wd.warp_wait(xch_full, segs & 1u))) break;
+          tc_fence_after_sync();
+          // lane r works out row r's factors
+          float f0 = 0.0f, f1 = 0.0f;
+          const bool whole = w.j0 == 0 && w.count == w.tiles;
+          const int slot = static_cast<int>(blockIdx.x) * 2 + (w.j0 == 0 ? 1 : 0);
+          if (static_cast<int>(lane) < rows) {
+            const float* x = warp_sums + lane;
+            const float l0 = (x[0] + x[32]) + (x[64] + x[96]);
+            const float l1 = both ? (x[128] + x[160]) + (x[192] + x[224]) : 0.0f;
+            const float m0 = unit_refs[lane], m1 = unit_refs[32 + lane];
+            // a part with an empty sum has no reference; NaN sums stay NaN
+            const float m = l0 == 0.0f ? m1 : (l1 == 0.0f ? m0 : fmaxf(m0, m1));
+            f0 = l0 == 0.0f ? 0.0f : ex2_approx(m0 - m);
+            f1 = l1 == 0.0f ? 0.0f : ex2_approx(m1 - m);
+            const float sum_all = (l0 == 0.0f ? 0.0f : l0 * f0) + (l1 == 0.0f ? 0.0f : l1 * f1);
+            if (whole) {
+              const float inv = sum_all == 0.0f ? 0.0f : 1.0f / sum_all;
+              f0 *= inv;
+              f1 *= inv;
+              if (quarter == 0 && args.lse != nullptr) {
+                const int token = static_cast<int>(lane) / args.group;
+                args.lse[(static_cast<int64_t>(w.b) * args.tokens + token) * args.heads + w.h * args.group +
+                         (static_cast<int>(lane) - token * args.group)] =
+                    sum_all == 0.0f ? -INFINITY : (m * ta::kLn2 + logf(sum_all));
+              }
+            } else if (quarter == 0) {
+              args.part_ml[static_cast<int64_t>(slot) * args.part_rows + lane] = make_float2(sum_all == 0.0f ? 0.0f : m, sum_all);
+            }
+          }
+          float o0[C::kRows], o1[C::kRows];
+          da::tmem_load_rows<C::kRows>(t_o, o0);
+          if (both) da::tmem_load_rows<C::kRows>(t_o + static_cast<uint32_t>(C::kRows), o1);
+          const bool column = key < C::kDim;   // this lane holds a column of O
+          uint16_t* out = static_cast<uint16_t*>(args.o) +
+                          (static_cast<int64_t>(w.b) * args.tokens * args.heads + w.h * args.group) * C::kDim + key;
+          float* part = args.part_o + (static_cast<int64_t>(slot) * (C::kDim / 4) + key / 4) * args.part_rows * 4 + key % 4;
+          int token = 0, head = 0;   // of row r
+#pragma unroll
+          for (int r = 0; r < C::kRows; ++r) {
+            const float a0 = __shfl_sync(0xffffffffu, f0, r), a1 = __shfl_sync(0xffffffffu, f1, r);
+            if (r < rows) {
+              float v = a0 == 0.0f ? 0.0f : o0[r] * a0;
+              if (both && a1 != 0.0f) v += o1[r] * a1;
+              if (column) {
+                if (whole) out[(static_cast<int64_t>(token) * args.heads + head) * C::kDim] = static_cast<uint16_t>(cache::pack2<C::kBf16>(v, 0.0f));
+                else part[4 * r] = v;
+              }
+              if (++head == args.group) {
+                head = 0;
+                ++token;
+              }
+            }
+          }
+          tc_fence_before_sync();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(xch_empty);
+        }
+        // shared sums and the O buffers are free again
+        if (!(ok = wd.warp_wait(xch_empty, segs & 1u))) break;
+        tc_fence_after_sync();
+      }
+    }
+  }
+
+  tc_fence_before_sync();
+  __syncthreads();
+  if (warp == da::kMmaWarp) {
+    tc_fence_after_sync();
+    tmem_dealloc<1>(tmem_base, C::kTmemCols);
+  }
+}
+
+}  // namespace gemm_tn_dev
+
+namespace gemm_tn_impl {
+
+namespace {
+
+template <class C>
+cudaError_t launch_cfg(const gemm_tn_dev::TreeArgs& args, cudaStream_t stream) {
+  static std::atomic<uint64_t> done_mask{0};
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  const uint64_t bit = 1ull << (dev & 63);
+  if (!(done_mask.load(std::memory_order_acquire) & bit)) {
+    e = cudaFuncSetAttribute(gemm_tn_dev::decode_attn_kernel<C>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             static_cast<int>(C::kSmemBytes));
+    if (e != cudaSuccess) return e;
+    done_mask.fetch_or(bit, std::memory_order_acq_rel);
+  }
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3(static_cast<unsigned>(args.chunks), 1, 1);
+  cfg.blockDim = dim3(C::kNumThreads, 1, 1);
+  cfg.dynamicSmemBytes = C::kSmemBytes;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = dependent_launch_enabled() ? 1 : 0;
+  return cudaLaunchKernelEx(&cfg, gemm_tn_dev::decode_attn_kernel<C>, args);
+}
+
+template <int kRows>
+cudaError_t launch_rows(int head_dim, bool bf16, const gemm_tn_dev::TreeArgs& args, cudaStream_t stream) {
+  using namespace gemm_tn_dev::da;
+  if (head_dim == 64)
+    return bf16 ? launch_cfg<Cfg<64, true, kRows>>(args, stream) : launch_cfg<Cfg<64, false, kRows>>(args, stream);
+  if (head_dim == 128)
+    return bf16 ? launch_cfg<Cfg<128, true, kRows>>(args, stream) : launch_cfg<Cfg<128, false, kRows>>(args, stream);
+  return cudaErrorInvalidValue;
+}
+
+}  // namespace
+
+int decode_attn_rows() { return gemm_tn_dev::da::kMaxRows; }
+
+int decode_attn_part_rows(int rows) { return rows <= 16 ? 16 : 32; }
+
+cudaError_t launch_decode_attn(int head_dim, bool bf16, const gemm_tn_dev::TreeArgs& args, cudaStream_t stream) {
+  return args.part_rows == 16 ? launch_rows<16>(head_dim, bf16, args, stream) : launch_rows<32>(head_dim, bf16, args, stream);
+}
+
+}  // namespace gemm_tn_impl

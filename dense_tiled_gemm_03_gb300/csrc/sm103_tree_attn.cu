@@ -19,6 +19,8 @@
 // lengths change. An item that lies in one chunk is written by its CTA; one
 // that is cut leaves each part's unnormalised rows, maxima and sums in a
 // workspace and the second kernel joins them in order (repeatable to the bit).
+// Where no item can be long, a chunk takes the items that begin in it whole, and
+// there is neither workspace nor second kernel.
 //
 // One CTA per SM:
 //   warp 0      TMA producer. Lane l copies the tile's l-th page (pages of 8 to
@@ -44,7 +46,7 @@
 #include <cstdint>
 
 #include "gemm_tn_internal.h"
-#include "sm103_cache.cuh"
+#include "sm103_tree_attn.cuh"
 
 namespace gemm_tn_dev {
 
@@ -54,9 +56,6 @@ constexpr int kProducerWarp = 0;
 constexpr int kMmaWarp = 1;
 constexpr int kFirstSoftmaxWarp = 2;
 constexpr int kTileRows = 128;     // query rows per tile (TMEM lanes)
-using cache::kTileKeys;
-using cache::pack2;
-constexpr float kLn2 = 0.69314718055994531f;
 
 template <int kDim_, bool kBf16_>
 struct Cfg {
@@ -92,101 +91,6 @@ struct Cfg {
   static_assert(kSmemBytes <= 227u * 1024u, "shared memory budget");
   static_assert(kOffBar % 8u == 0, "64-bit shared words");
 };
-
-// ------------------------------------------------------------------ the schedule
-
-// Cached keys and new tokens of sequence b, as the kernels may use them: the
-// arrays on the device are clamped to what the cache and the inputs can hold.
-__device__ __forceinline__ int cached_len(const TreeArgs& a, int b) {
-  return min(max(__ldg(a.lens + b), 0), a.capacity);
-}
-__device__ __forceinline__ int new_len(const TreeArgs& a, int b) {
-  return a.token_lens == nullptr ? a.tokens : min(max(__ldg(a.token_lens + b), 0), a.tokens);
-}
-
-// Key tiles that unit `u` of row unit `ru` walks: all cached ones and the new
-// ones up to the last token it may see. At least one where the unit has rows
-// (an empty tile writes the empty softmax), none where it has not.
-__device__ __forceinline__ int unit_tiles(const TreeArgs& a, int len, int tl, int ru, int u) {
-  const int i0 = (ru * a.units + u) * a.tile_tokens;
-  if (i0 >= tl) return 0;
-  const int fresh = a.has_new == 0 ? 0 : (a.mask == nullptr ? min(tl, i0 + a.tile_tokens) : tl);
-  const int n = (len + kTileKeys - 1) / kTileKeys + (fresh + kTileKeys - 1) / kTileKeys;
-  return max(n, 1);
-}
-
-__device__ __forceinline__ int item_tiles(const TreeArgs& a, int len, int tl, int ru) {
-  const int n0 = unit_tiles(a, len, tl, ru, 0);
-  return a.units == 2 ? max(n0, unit_tiles(a, len, tl, ru, 1)) : n0;
-}
-
-// Key tiles of all row units of one KV head of a sequence.
-__device__ __forceinline__ int head_tiles(const TreeArgs& a, int len, int tl) {
-  int n = 0;
-  for (int ru = 0; ru < a.row_units; ++ru) n += item_tiles(a, len, tl, ru);
-  return n;
-}
-
-// Walks a chunk: one segment (a run of one item's key tiles) after another.
-struct Walk {
-  int b, h, ru, j0;      // item and its first tile in this segment
-  int len, tl;           // cached keys and new tokens of b
-  int tiles;             // tiles of the item
-  int left;              // tiles of the chunk from this segment on
-  int count;             // tiles of the segment
-
-  // The walk that begins at tile `off` of sequence b.
-  __device__ __forceinline__ void start(const TreeArgs& a, int b_, int off, int left_) {
-    b = b_;
-    len = cached_len(a, b);
-    tl = new_len(a, b);
-    const int per_head = head_tiles(a, len, tl);
-    h = off / per_head;
-    j0 = off - per_head * h;
-    for (ru = 0; (tiles = item_tiles(a, len, tl, ru)) <= j0; ++ru) j0 -= tiles;
-    left = left_;
-    count = min(tiles - j0, left);
-  }
-  __device__ __forceinline__ bool more() const { return left > 0; }
-  __device__ __forceinline__ void next(const TreeArgs& a) {
-    left -= count;
-    if (left <= 0) return;
-    j0 = 0;
-    do {
-      if (++ru == a.row_units) {
-        ru = 0;
-        if (++h == a.kv_heads) {
-          h = 0;
-          ++b;
-          len = cached_len(a, b);
-          tl = new_len(a, b);
-        }
-      }
-      tiles = item_tiles(a, len, tl, ru);
-    } while (tiles == 0);
-    count = min(tiles, left);
-  }
-  // Past the last tile of the segment that unit u walks.
-  __device__ __forceinline__ int unit_end(const TreeArgs& a, int u) const {
-    const int end = j0 + count;
-    return a.units == 2 ? max(j0, min(end, unit_tiles(a, len, tl, ru, u))) : end;
-  }
-};
-
-// Keys of tile j that exist: cached tiles first, then the new tokens'.
-struct Tile {
-  bool fresh;    // new tokens' keys
-  int index;     // tile number among its kind
-  int valid;     // keys of the tile that exist
-};
-__device__ __forceinline__ Tile tile_of(int len, int tl, bool has_new, int j) {
-  const int nc = (len + kTileKeys - 1) / kTileKeys;
-  Tile t;
-  t.fresh = j >= nc;
-  t.index = t.fresh ? j - nc : j;
-  t.valid = min(kTileKeys, max(0, (t.fresh ? (has_new ? tl : 0) : len) - t.index * kTileKeys));
-  return t;
-}
 
 }  // namespace ta
 
@@ -257,20 +161,7 @@ __global__ void __launch_bounds__(C::kNumThreads) __maxnreg__(C::kMaxRegs)
   // stream; global memory is touched only once that kernel has completed.
   griddep_wait();
   griddep_launch_dependents();
-  cache::find_start(
-      args.batch, args.chunks, args.min_chunk, static_cast<int>(blockIdx.x), sums,
-      [&](int b) { return ta::head_tiles(args, ta::cached_len(args, b), ta::new_len(args, b)) * args.kv_heads; },
-      [&](int b, int off, int left, int chunk_tiles) {
-        ta::Walk w;
-        w.start(args, b, off, left);
-        *start_walk = w;
-        // what the second kernel has to know about an item that this chunk begins inside of
-        if (w.j0 > 0) {
-          int4* to = reinterpret_cast<int4*>(args.cuts) + 2 * blockIdx.x;
-          to[0] = make_int4(w.b, w.h, w.ru, w.j0);
-          to[1] = make_int4(w.tiles, w.len, w.tl, chunk_tiles);
-        }
-      });
+  ta::find_walk(args, start_walk, sums);
   tc_fence_before_sync();
   __syncthreads();
   tc_fence_after_sync();
@@ -279,7 +170,7 @@ __global__ void __launch_bounds__(C::kNumThreads) __maxnreg__(C::kMaxRegs)
   const bool parity_mode = args.units == 1;
   const bool has_new = args.has_new != 0;
   ta::Walk w = *start_walk;
-  if (threadIdx.x == 0 && (!w.more() || w.j0 == 0)) reinterpret_cast<int4*>(args.cuts)[2 * blockIdx.x] = make_int4(-1, 0, 0, 0);
+  if (threadIdx.x == 0) ta::note_no_cut(args, w);
 
   if (warp == ta::kProducerWarp) {
     // -------------------------------------------------------------- TMA producer
@@ -306,18 +197,8 @@ __global__ void __launch_bounds__(C::kNumThreads) __maxnreg__(C::kMaxRegs)
         if (ok) issued_q[slot] = static_cast<int>(ph);
       }
       const int32_t* table = args.page_table + static_cast<int64_t>(w.b) * args.table_stride;
-      // the page that this lane copies of cached tile j
       auto page_of = [&](int j) {
-        const ta::Tile t = ta::tile_of(w.len, w.tl, has_new, j);
-        if (t.fresh || static_cast<int>(lane) * box_rows >= t.valid) return 0;
-        const int first = t.index * ta::kTileKeys + static_cast<int>(lane) * box_rows;
-        int page = __ldg(table + first / args.page_size);
-        if (page < 0 || page >= args.num_pages) {
-          // not a page: nothing is read (the copy fills zeros), and the caller is told
-          cache::report(args.status, cache::kStatusInvalid);
-          page = args.num_pages;
-        }
-        return page;
+        return ta::page_of(args, table, ta::tile_of(w.len, w.tl, has_new, j), box_rows, static_cast<int>(lane));
       };
       int page = page_of(w.j0);
       for (int j = w.j0; j < w.j0 + w.count; ++j, ++it) {
@@ -665,7 +546,7 @@ __global__ void __launch_bounds__(C::kNumThreads) __maxnreg__(C::kMaxRegs)
         const int64_t out_row = (static_cast<int64_t>(w.b) * args.tokens + token) * args.heads + w.h * args.group + r_head;
         const int slot = static_cast<int>(blockIdx.x) * 2 + (w.j0 == 0 ? 1 : 0);
         const int part_unit_row = (parity_mode ? 0 : u) * ta::kTileRows + r;
-        const int64_t part_row = static_cast<int64_t>(slot) * (args.units * ta::kTileRows) + part_unit_row;
+        const int64_t part_row = static_cast<int64_t>(slot) * args.part_rows + part_unit_row;
         if (live) {
           if (whole) {
             if (args.lse != nullptr)
@@ -677,8 +558,8 @@ __global__ void __launch_bounds__(C::kNumThreads) __maxnreg__(C::kMaxRegs)
         uint16_t* out = static_cast<uint16_t*>(args.o) + out_row * C::kDim;
         // [slot][dim / 4][row] pieces of four: a warp's 32 rows store 512 contiguous bytes at a time
         float4* part = reinterpret_cast<float4*>(args.part_o) +
-                       static_cast<int64_t>(slot) * (args.units * ta::kTileRows) * (C::kDim / 4) + part_unit_row;
-        const int part_pitch = args.units * ta::kTileRows;
+                       static_cast<int64_t>(slot) * args.part_rows * (C::kDim / 4) + part_unit_row;
+        const int part_pitch = args.part_rows;
 #pragma unroll 1   // once per segment: short code, which is fetched cold, is faster than unrolled code
         for (int c = 0; c < C::kDim / 32; ++c) {
           uint32_t o[32];
@@ -748,7 +629,7 @@ __global__ void __launch_bounds__(512) tree_attn_join_kernel(const __grid_consta
   const int b = c0.x, h = c0.y, ru = c0.z, j0 = c0.w, tiles = c1.x, len = c1.y, tl = c1.z, per_chunk = c1.w;
   if (b < 0 || j0 > per_chunk) return;
   const int parts = 2 + (tiles - j0 - 1) / per_chunk;
-  const int rows_per_part = args.units * ta::kTileRows;
+  const int rows_per_part = args.part_rows;
   const int group = static_cast<int>(threadIdx.x) >> 8, tid = static_cast<int>(threadIdx.x) & 255;
   const int piece0 = (tid >> 5) * kPer;
   const int row = static_cast<int>(blockIdx.y) * 32 + (tid & 31);
@@ -844,7 +725,7 @@ cudaError_t launch_cfg(const gemm_tn_dev::TreeArgs& args, cudaStream_t stream) {
 template <int kDim, bool kBf16>
 cudaError_t launch_join(const gemm_tn_dev::TreeArgs& args, cudaStream_t stream) {
   cudaLaunchConfig_t cfg{};
-  const int rows = args.units == 2 ? 2 * gemm_tn_dev::ta::kTileRows
+  const int rows = args.units == 2 ? args.part_rows
                                    : (args.tokens < args.tile_tokens ? args.tokens : args.tile_tokens) * args.group;
   cfg.gridDim = dim3(static_cast<unsigned>(args.chunks - 1), static_cast<unsigned>((rows + 31) / 32), 1);
   cfg.blockDim = dim3(512, 1, 1);
