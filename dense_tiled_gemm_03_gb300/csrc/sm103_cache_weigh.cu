@@ -229,8 +229,10 @@ __global__ void __launch_bounds__(C::kNumThreads, 1) cache_weigh_kernel(const __
     for (int s = 0; s < C::kStages; ++s)
       if (issued[s] >= 0) wd.drain(k_full(s), static_cast<uint32_t>(issued[s]));
   } else if (warp == cw::kMmaWarp) {
-    if (lane == 0) {
+    {
       // ------------------------------------------------------------ MMA issuer
+      // (the whole warp runs this, one lane issues)
+      const uint32_t leader = elect_one();
       int it = 0;       // tiles issued
       int q_blocks = 0;
       bool ok = true;
@@ -240,11 +242,11 @@ __global__ void __launch_bounds__(C::kNumThreads, 1) cache_weigh_kernel(const __
           const int rows = w.block_rows(args, block);
           const uint32_t n = static_cast<uint32_t>(max(1, (rows + 31) / 32)) * 32u;
           const uint32_t idesc = C::kIdesc | ((n >> 3) << 17);
-          if (!(ok = wd.wait(q_full, static_cast<uint32_t>(q_blocks) & 1u))) break;
+          if (!(ok = wd.warp_wait(q_full, static_cast<uint32_t>(q_blocks) & 1u))) break;
           for (int j = 0; j < w.count; ++j, ++it) {
             const int s = it % C::kStages, g = it & 1;
-            if (!(ok = wd.wait(s_empty(g), (static_cast<uint32_t>(it >> 1) & 1u) ^ 1u))) break;
-            if (!(ok = wd.wait(k_full(s), static_cast<uint32_t>(it / C::kStages) & 1u))) break;
+            if (!(ok = wd.warp_wait(s_empty(g), (static_cast<uint32_t>(it >> 1) & 1u) ^ 1u))) break;
+            if (!(ok = wd.warp_wait(k_full(s), static_cast<uint32_t>(it / C::kStages) & 1u))) break;
             tc_fence_after_sync();
 #pragma unroll
             for (int c = 0; c < C::kDimBoxes; ++c) {
@@ -252,16 +254,16 @@ __global__ void __launch_bounds__(C::kNumThreads, 1) cache_weigh_kernel(const __
               const uint64_t b_desc = sw128_kmajor_desc(base + C::kOffQ + c * C::kQBoxBytes);
 #pragma unroll
               for (int kk = 0; kk < 4; ++kk)
-                mma_f16<1>(tmem_base + 256u * static_cast<uint32_t>(g), a_desc + 2u * kk, b_desc + 2u * kk, idesc,
+                mma_f16_warp(leader, tmem_base + 256u * static_cast<uint32_t>(g), a_desc + 2u * kk, b_desc + 2u * kk, idesc,
                            (c | kk) != 0 ? 1u : 0u);
             }
-            mma_commit(s_full(g));
-            mma_commit(k_empty(s));
+            mma_commit_warp(leader, s_full(g));
+            mma_commit_warp(leader, k_empty(s));
           }
         }
       }
       // every MMA issued here must finish before TMEM is freed
-      mma_commit(drain_bar);
+      mma_commit_warp(leader, drain_bar);
       wd.drain(drain_bar, 0);
     }
   } else {

@@ -291,8 +291,10 @@ __global__ void __launch_bounds__(C::kNumThreads, 1) decode_attn_kernel(const __
       if (issued_v[x] >= 0) wd.drain(v_full(x), static_cast<uint32_t>(issued_v[x]));
     }
   } else if (warp == da::kMmaWarp) {
-    if (lane == 0) {
+    {
       // ------------------------------------------------------------ MMA issuer
+      // (the whole warp runs this, one lane issues)
+      const uint32_t leader = elect_one();
       int it0 = 0;                    // ring number of the segment's first tile
       int seg = 0;
       int done[2] = {0, 0};           // tiles of each unit whose P has been asked for
@@ -301,7 +303,7 @@ __global__ void __launch_bounds__(C::kNumThreads, 1) decode_attn_kernel(const __
         const int slot = seg & 1;
         auto issue_s = [&](int u, int i) {   // i: tile of the segment
           const int x = it0 + i, s = x % C::kStages;
-          if (!wd.wait(k_full(s), static_cast<uint32_t>(x / C::kStages) & 1u)) return false;
+          if (!wd.warp_wait(k_full(s), static_cast<uint32_t>(x / C::kStages) & 1u)) return false;
           tc_fence_after_sync();
 #pragma unroll
           for (int c = 0; c < C::kDimBoxes; ++c) {
@@ -309,20 +311,20 @@ __global__ void __launch_bounds__(C::kNumThreads, 1) decode_attn_kernel(const __
             const uint64_t b_desc = sw128_kmajor_desc(q_slot(slot) + c * C::kQBoxBytes);
 #pragma unroll
             for (int kk = 0; kk < 4; ++kk)   // 16 elements of dim = 32 bytes = 2 descriptor units
-              mma_f16<1>(tmem_base + static_cast<uint32_t>(C::kRows * u), a_desc + 2u * kk, b_desc + 2u * kk, C::kIdescS,
+              mma_f16_warp(leader, tmem_base + static_cast<uint32_t>(C::kRows * u), a_desc + 2u * kk, b_desc + 2u * kk, C::kIdescS,
                          (c | kk) != 0 ? 1u : 0u);
           }
-          mma_commit(s_full(u));
-          mma_commit(k_empty(s));
-          if (i == w.count - 1) mma_commit(q_empty(slot));   // Q has been read for the last time
+          mma_commit_warp(leader, s_full(u));
+          mma_commit_warp(leader, k_empty(s));
+          if (i == w.count - 1) mma_commit_warp(leader, q_empty(slot));   // Q has been read for the last time
           return true;
         };
-        if (!(ok = wd.wait(q_full(slot), static_cast<uint32_t>(seg >> 1) & 1u))) break;
+        if (!(ok = wd.warp_wait(q_full(slot), static_cast<uint32_t>(seg >> 1) & 1u))) break;
         ok = issue_s(0, 0) && (w.count < 2 || issue_s(1, 1));
         for (int i = 0; ok && i < w.count; ++i) {
           const int x = it0 + i, s = x % C::kStages, u = i & 1;
-          if (!(ok = wd.wait(v_full(s), static_cast<uint32_t>(x / C::kStages) & 1u))) break;
-          if (!(ok = wd.wait(p_full(u), static_cast<uint32_t>(done[u]) & 1u))) break;
+          if (!(ok = wd.warp_wait(v_full(s), static_cast<uint32_t>(x / C::kStages) & 1u))) break;
+          if (!(ok = wd.warp_wait(p_full(u), static_cast<uint32_t>(done[u]) & 1u))) break;
           ++done[u];
           tc_fence_after_sync();
           const int steps = (ta::tile_of(w.len, w.tl, has_new, w.j0 + i).valid + 15) / 16;
@@ -330,7 +332,7 @@ __global__ void __launch_bounds__(C::kNumThreads, 1) decode_attn_kernel(const __
           const uint64_t b_desc = sw128_kmajor_desc(p_tile(u));
           const uint32_t t_o = tmem_base + static_cast<uint32_t>(C::kRows * (2 + u));
           auto pv = [&](int kk) {   // 16 keys: 16 rows of 128 bytes of V; 32 bytes of P's rows, 64 keys a box
-            mma_f16<1>(t_o, a_desc + ((static_cast<uint32_t>(kk) * 2048u) >> 4),
+            mma_f16_warp(leader, t_o, a_desc + ((static_cast<uint32_t>(kk) * 2048u) >> 4),
                        b_desc + ((static_cast<uint32_t>(kk >> 2) * C::kPBoxBytes) >> 4) + 2u * static_cast<uint32_t>(kk & 3),
                        C::kIdescO, i < 2 && kk == 0 ? 0u : 1u);
           };
@@ -340,13 +342,13 @@ __global__ void __launch_bounds__(C::kNumThreads, 1) decode_attn_kernel(const __
           } else {
             for (int kk = 0; kk < steps; ++kk) pv(kk);
           }
-          mma_commit(v_empty(s));
+          mma_commit_warp(leader, v_empty(s));
           if (i + 2 < w.count) ok = issue_s(u, i + 2);
-          else mma_commit(o_done(u));
+          else mma_commit_warp(leader, o_done(u));
         }
       }
       // every MMA issued here must finish before TMEM is freed
-      mma_commit(drain_bar);
+      mma_commit_warp(leader, drain_bar);
       wd.drain(drain_bar, 0);
     }
   } else {

@@ -244,8 +244,10 @@ __global__ void __launch_bounds__(C::kNumThreads) __maxnreg__(C::kMaxRegs)
     for (int s = 0; s < C::kVStages; ++s)
       if (issued_v[s] >= 0) wd.drain(v_full(s), static_cast<uint32_t>(issued_v[s]));
   } else if (warp == ta::kMmaWarp) {
-    if (lane == 0) {
+    {
       // ------------------------------------------------------------ MMA issuer
+      // (the whole warp runs this, one lane issues)
+      const uint32_t leader = elect_one();
       int it0 = 0;                    // ring number of the segment's first tile
       int seg = 0;
       int done[2] = {0, 0};           // tiles of each unit whose P has been asked for
@@ -258,7 +260,7 @@ __global__ void __launch_bounds__(C::kNumThreads) __maxnreg__(C::kMaxRegs)
         auto last_reader = [&](int u, int j) { return parity_mode || u == 1 || j >= end[1]; };
         auto wait_k = [&](int j) {
           const int i = it0 + j - w.j0;
-          return wd.wait(k_full(i % C::kKStages), static_cast<uint32_t>(i / C::kKStages) & 1u);
+          return wd.warp_wait(k_full(i % C::kKStages), static_cast<uint32_t>(i / C::kKStages) & 1u);
         };
         auto issue_s = [&](int u, int j) {
           const int s = (it0 + j - w.j0) % C::kKStages;
@@ -274,12 +276,12 @@ __global__ void __launch_bounds__(C::kNumThreads) __maxnreg__(C::kMaxRegs)
             const uint64_t b_desc = sw128_kmajor_desc(k_tile(s) + c * C::kBoxBytes);
 #pragma unroll
             for (int kk = 0; kk < 4; ++kk)   // 16 elements of dim = 32 bytes = 2 descriptor units
-              mma_f16<1>(t_s, a_desc + 2u * kk, b_desc + 2u * kk, idesc, (c | kk) != 0 ? 1u : 0u);
+              mma_f16_warp(leader, t_s, a_desc + 2u * kk, b_desc + 2u * kk, idesc, (c | kk) != 0 ? 1u : 0u);
           }
-          mma_commit(s_full(u));
-          if (last_reader(u, j)) mma_commit(k_empty(s));
+          mma_commit_warp(leader, s_full(u));
+          if (last_reader(u, j)) mma_commit_warp(leader, k_empty(s));
           if (--products == 0)   // Q has been read for the last time
-            for (int x = 0; x < args.units; ++x) mma_commit(q_empty(parity_mode ? seg & 1 : x));
+            for (int x = 0; x < args.units; ++x) mma_commit_warp(leader, q_empty(parity_mode ? seg & 1 : x));
         };
         auto issue_pv = [&](int u, int j, bool first) {
           const int s = (it0 + j - w.j0) % C::kVStages;
@@ -288,7 +290,7 @@ __global__ void __launch_bounds__(C::kNumThreads) __maxnreg__(C::kMaxRegs)
           const uint32_t t_p = tmem_base + C::kColS + 128u * static_cast<uint32_t>(u);
           const uint32_t t_o = tmem_base + C::kColO + static_cast<uint32_t>(C::kDim * u);
           auto pv = [&](int kk) {   // 16 keys: 8 columns of P; 16 rows of 128 bytes of V
-            mma_f16_tmem_a(t_o, t_p + 64u * static_cast<uint32_t>(kk >> 2) + 8u * static_cast<uint32_t>(kk & 3),
+            mma_f16_tmem_a_warp(leader, t_o, t_p + 64u * static_cast<uint32_t>(kk >> 2) + 8u * static_cast<uint32_t>(kk & 3),
                            v_desc + ((static_cast<uint32_t>(kk) * 2048u) >> 4), C::kIdescO,
                            first && kk == 0 ? 0u : 1u);
           };
@@ -298,11 +300,11 @@ __global__ void __launch_bounds__(C::kNumThreads) __maxnreg__(C::kMaxRegs)
           } else {
             for (int kk = 0; kk < steps; ++kk) pv(kk);
           }
-          if (last_reader(u, j)) mma_commit(v_empty(s));
+          if (last_reader(u, j)) mma_commit_warp(leader, v_empty(s));
         };
         for (int u = 0; u < args.units && ok; ++u) {
           const int slot = parity_mode ? seg & 1 : u;
-          ok = wd.wait(q_full(slot), static_cast<uint32_t>(parity_mode ? seg >> 1 : seg) & 1u);
+          ok = wd.warp_wait(q_full(slot), static_cast<uint32_t>(parity_mode ? seg >> 1 : seg) & 1u);
         }
         for (int u = 0; u < 2 && ok; ++u) {
           const int j = w.j0 + (parity_mode ? u : 0);
@@ -313,10 +315,10 @@ __global__ void __launch_bounds__(C::kNumThreads) __maxnreg__(C::kMaxRegs)
         }
         for (int j = w.j0; ok && j < w.j0 + w.count; ++j) {
           const int i = it0 + j - w.j0;
-          if (!(ok = wd.wait(v_full(i % C::kVStages), static_cast<uint32_t>(i / C::kVStages) & 1u))) break;
+          if (!(ok = wd.warp_wait(v_full(i % C::kVStages), static_cast<uint32_t>(i / C::kVStages) & 1u))) break;
           for (int u = 0; u < 2; ++u) {
             if (j >= end[u] || (parity_mode && ((j - w.j0) & 1) != u)) continue;
-            if (!(ok = wd.wait(p_full(u), static_cast<uint32_t>(done[u]) & 1u))) break;
+            if (!(ok = wd.warp_wait(p_full(u), static_cast<uint32_t>(done[u]) & 1u))) break;
             ++done[u];
             tc_fence_after_sync();
             issue_pv(u, j, j - w.j0 < step);
@@ -325,13 +327,13 @@ __global__ void __launch_bounds__(C::kNumThreads) __maxnreg__(C::kMaxRegs)
               tc_fence_after_sync();
               issue_s(u, j + step);
             } else {
-              mma_commit(o_done(u));
+              mma_commit_warp(leader, o_done(u));
             }
           }
         }
       }
       // every MMA issued here must finish before TMEM is freed
-      mma_commit(drain_bar);
+      mma_commit_warp(leader, drain_bar);
       wd.drain(drain_bar, 0);
     }
   } else {
