@@ -121,7 +121,8 @@ struct EvictArgs {
   const int32_t* lens;
   int32_t* lens_out;
   int32_t* counts;          // workspace: [batch * kv heads] rows to move
-  int2* moves;              // workspace: [batch * kv heads][max_moves] (from, to)
+  int2* moves;              // workspace: [batch * kv heads][max_moves] slots (from, to); NULL: the selecting blocks move
+  longlong2* places;        // workspace, the same moves: where the rows begin in the pools (16-byte units; -1: nowhere)
   int max_moves;
   int keep, recent;
   int smem_keys;            // slots whose keys fit in shared memory
@@ -200,6 +201,7 @@ cudaError_t launch_cache_append(const gemm_tn_dev::AppendArgs& args, cudaStream_
 cudaError_t launch_cache_advance(const gemm_tn_dev::AppendArgs& args, cudaStream_t stream);
 // Chooses the kept slots and lists the moves; then moves the rows.
 int evict_smem_keys(int capacity);
+int evict_fused_moves();   // most moves per list that the first kernel can make itself (moves NULL, lens_out not lens)
 cudaError_t launch_cache_select(const gemm_tn_dev::EvictArgs& args, cudaStream_t stream);
 cudaError_t launch_cache_move(const gemm_tn_dev::EvictArgs& args, int num_sms, cudaStream_t stream);
 

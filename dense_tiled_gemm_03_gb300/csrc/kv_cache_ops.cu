@@ -97,7 +97,9 @@ namespace ev {
 
 constexpr int kThreads = 1024;
 constexpr int kWarps = kThreads / 32;
-constexpr int kBins = 2048;        // digits of 11, 11 and 10 bits
+constexpr int kBins = 2048;
+constexpr int kSmemKeys = 40 * 1024;   // keys that a block holds in shared memory
+constexpr int kFusedMoves = 512;   // most moves of a list that the selecting block makes itself
 
 // An order-preserving whole number for a slot: the newest slots above
 // everything, then NaN, then the weights (-0 and +0 alike).
@@ -128,20 +130,31 @@ __device__ __forceinline__ int warp_base(int x, int* sums, int* total) {
 
 }  // namespace ev
 
-// One block per (sequence, KV head). The `keep` largest keys are found by a
-// radix selection from the top digit down (three counting passes); ties go to
-// the lowest slots. Then the holes before `keep` and the kept slots behind it
-// are numbered in ascending order by ballots and paired. Keys are held in
-// shared memory where they fit and recomputed from the arrays where they do not.
+// One block per (sequence, KV head). The `keep` largest keys are found by
+// counting: the range between the smallest and the largest key is cut into 2048
+// equal bins, then the bin that holds the keep-th largest, until a bin is one
+// key (three passes at most, usually two; bins of the keys' own range and not
+// of fixed leading bits, which weights share: counting those into a few bins of
+// shared memory one after the other took 20 us of 37 for 64 lists of 16384).
+// Ties go to the lowest slots. Then the holes before `keep` and the kept slots
+// behind it are numbered in ascending order by ballots and paired. Keys are
+// held in shared memory where they fit and recomputed from the arrays where
+// they do not. kFused: the block moves its rows itself, from a list in shared
+// memory, and writes lens_out.
+template <bool kFused>
 __global__ void __launch_bounds__(ev::kThreads) cache_select_kernel(const __grid_constant__ EvictArgs a) {
   extern __shared__ uint32_t smem_keys[];
   __shared__ int hist[ev::kBins];
   __shared__ int sums[ev::kWarps];
+  __shared__ uint32_t extremes[2][ev::kWarps];
   __shared__ int chosen[2];
+  __shared__ int2 list[kFused ? ev::kFusedMoves : 1];
+  __shared__ longlong2 places[kFused ? ev::kFusedMoves : 1];
+  __shared__ uint32_t kept_bits[ev::kSmemKeys / 32];
   griddep_wait();
   griddep_launch_dependents();
   const int bh = static_cast<int>(blockIdx.x);
-  const int b = bh / a.c.kv_heads;
+  const int b = bh / a.c.kv_heads, h = bh - b * a.c.kv_heads;
   const int tid = static_cast<int>(threadIdx.x);
   const int warp = tid >> 5, lane = tid & 31;
   const int len = cached_len(a.c, a.lens, b);
@@ -150,8 +163,9 @@ __global__ void __launch_bounds__(ev::kThreads) cache_select_kernel(const __grid
   const float* weight = a.weight + base;
   const int32_t* pos = a.pos != nullptr ? a.pos + base : nullptr;
   const int stay = min(len, keep);
+  if (kFused && h == 0 && tid == 0) a.lens_out[b] = stay;
   if (len <= keep) {
-    if (tid == 0) a.counts[bh] = 0;
+    if (!kFused && tid == 0) a.counts[bh] = 0;
     if (a.weight_out != a.weight)
       for (int s = tid; s < stay; s += ev::kThreads) a.weight_out[base + s] = weight[s];
     if (a.pos_out != nullptr && a.pos_out != a.pos)
@@ -161,25 +175,47 @@ __global__ void __launch_bounds__(ev::kThreads) cache_select_kernel(const __grid
   const int first_new = a.recent > 0 ? a.seen[b] - a.recent : 0;   // positions from here on are the newest
   auto load_key = [&](int s) { return ev::key_of(weight[s], a.recent > 0 && pos[s] >= first_new); };
   const bool in_smem = len <= a.smem_keys;
-  if (in_smem)
-    for (int s = tid; s < len; s += ev::kThreads) smem_keys[s] = load_key(s);
-  __syncthreads();
   auto key = [&](int s) { return in_smem ? smem_keys[s] : load_key(s); };
+  // the newest slots (key 0xffffffff) are counted, and left out of the range
+  uint32_t lowest = 0xffffffffu, highest = 0u;
+  int newest = 0;
+#pragma unroll 8
+  for (int s = tid; s < len; s += ev::kThreads) {
+    const uint32_t k = load_key(s);
+    if (in_smem) smem_keys[s] = k;
+    if (k == 0xffffffffu) {
+      ++newest;
+    } else {
+      lowest = min(lowest, k);
+      highest = max(highest, k);
+    }
+  }
+  lowest = __reduce_min_sync(0xffffffffu, lowest);
+  highest = __reduce_max_sync(0xffffffffu, highest);
+  if (lane == 0) {
+    extremes[0][warp] = lowest;
+    extremes[1][warp] = highest;
+  }
+  int total;
+  ev::warp_base(__reduce_add_sync(0xffffffffu, newest), sums, &total);
+  newest = total;
+  lowest = __reduce_min_sync(0xffffffffu, extremes[0][lane]);
+  highest = __reduce_max_sync(0xffffffffu, extremes[1][lane]);
 
   // the keep-th largest key, and how many slots that hold exactly it stay
-  uint32_t prefix = 0u;     // digits found so far
-  int need = keep;          // slots still to choose among those with that prefix
-  if (keep > 0) {
-    int low = 32;           // bits below the digits found
-    for (int digit = 0; digit < 3; ++digit) {
-      const int bits = digit == 2 ? 10 : 11;
-      const int high = low;
-      low -= bits;
+  uint32_t limit = 0xffffffffu;
+  int need = keep, ties = newest;
+  if (newest < keep) {
+    need = keep - newest;
+    limit = lowest;               // keys from here on, 2^bits of them, are looked at
+    int bits = 32 - __clz(highest - lowest);
+    while (true) {
+      const int shift = max(bits - 11, 0);
       for (int x = tid; x < ev::kBins; x += ev::kThreads) hist[x] = 0;
       __syncthreads();
       for (int s = tid; s < len; s += ev::kThreads) {
-        const uint32_t k = key(s);
-        if (high == 32 || (k >> high) == (prefix >> high)) atomicAdd(&hist[(k >> low) & ((1u << bits) - 1u)], 1);
+        const uint32_t k = key(s), d = k - limit;
+        if (k != 0xffffffffu && k >= limit && (bits == 32 || d < (1u << bits))) atomicAdd(&hist[d >> shift], 1);
       }
       __syncthreads();
       // from the top bin down: thread t looks at bins top - 2t and top - 2t - 1
@@ -191,7 +227,6 @@ __global__ void __launch_bounds__(ev::kThreads) cache_select_kernel(const __grid
         const int y = __shfl_up_sync(0xffffffffu, v, d);
         if (lane >= d) v += y;
       }
-      int total;
       const int before = ev::warp_base(__shfl_sync(0xffffffffu, v, 31), sums, &total) + v - n0 - n1;   // above this pair
       if (before < need && before + n0 >= need) {
         chosen[0] = top;
@@ -201,29 +236,49 @@ __global__ void __launch_bounds__(ev::kThreads) cache_select_kernel(const __grid
         chosen[1] = need - before - n0;
       }
       __syncthreads();
-      prefix |= static_cast<uint32_t>(chosen[0]) << low;
+      limit += static_cast<uint32_t>(chosen[0]) << shift;
       need = chosen[1];
+      ties = hist[chosen[0]];
       __syncthreads();
+      bits = shift;
+      if (shift == 0 || ties == 1) break;
+    }
+    if (bits > 0) {   // one key is left in the bin: it is the limit
+      for (int s = tid; s < len; s += ev::kThreads) {
+        const uint32_t k = key(s);
+        if (k != 0xffffffffu && k >= limit && k - limit < (1u << bits)) extremes[0][0] = k;
+      }
+      __syncthreads();
+      limit = extremes[0][0];
     }
   }
-  const uint32_t limit = prefix;
 
   // each warp has one contiguous run of slots; runs of 32 in ascending order
   const int per_warp = (len + 32 * ev::kWarps - 1) / (32 * ev::kWarps) * 32;
   const int s0 = min(len, warp * per_warp), s1 = min(len, s0 + per_warp);
-  int ties = 0;
-  for (int s = s0; s < s1; s += 32)
-    ties += __popc(__ballot_sync(0xffffffffu, s + lane < s1 && key(s + lane) == limit));
-  int total;
-  const int ties_before = ev::warp_base(ties, sums, &total);
+  const bool some_ties = ties != need;   // not all slots with the limit's key stay
+  int ties_before = 0;
+  if (some_ties) {
+    int mine = 0;
+    for (int s = s0; s < s1; s += 32)
+      mine += __popc(__ballot_sync(0xffffffffu, s + lane < s1 && key(s + lane) == limit));
+    ties_before = ev::warp_base(mine, sums, &total);
+  }
   // whether slot s stays; called by whole warps in ascending order from s0
   auto kept = [&](int s, int& tie_rank) {
     const uint32_t k = s + lane < s1 ? key(s + lane) : 0u;
+    const bool in = keep > 0 && s + lane < s1;
+    if (!some_ties) return in && k >= limit;
     const bool tie = s + lane < s1 && k == limit;
     const uint32_t tied = __ballot_sync(0xffffffffu, tie);
     const int rank = tie_rank + __popc(tied & ((1u << lane) - 1u));
     tie_rank += __popc(tied);
-    return keep > 0 && s + lane < s1 && (k > limit || (tie && rank < need));
+    return in && (k > limit || (tie && rank < need));
+  };
+  // a kept slot before `keep` stays where it is
+  auto copy = [&](int s) {
+    if (a.weight_out != a.weight) a.weight_out[base + s] = weight[s];
+    if (a.pos_out != nullptr && a.pos_out != a.pos) a.pos_out[base + s] = pos[s];
   };
   int holes = 0, movers = 0, tie_rank = ties_before;
   for (int s = s0; s < s1; s += 32) {
@@ -233,9 +288,9 @@ __global__ void __launch_bounds__(ev::kThreads) cache_select_kernel(const __grid
     movers += __popc(__ballot_sync(0xffffffffu, in && k && s + lane >= keep));
   }
   int hole_rank = ev::warp_base(holes, sums, &total);
-  int mover_rank = ev::warp_base(movers, sums, &total);
-  if (tid == 0) a.counts[bh] = total;   // as many movers as holes
-  int2* moves = a.moves + static_cast<int64_t>(bh) * a.max_moves;
+  int mover_rank = ev::warp_base(movers, sums, &total);   // as many movers as holes
+  if (!kFused && tid == 0) a.counts[bh] = total;
+  int2* moves = kFused ? list : a.moves + static_cast<int64_t>(bh) * a.max_moves;
   tie_rank = ties_before;
   for (int s = s0; s < s1; s += 32) {
     const bool k = kept(s, tie_rank);
@@ -247,17 +302,40 @@ __global__ void __launch_bounds__(ev::kThreads) cache_select_kernel(const __grid
     if (mover) moves[mover_rank + __popc(mb & below)].x = s + lane;
     hole_rank += __popc(hb);
     mover_rank += __popc(mb);
-    // kept slots before `keep` stay where they are
-    if (k && s + lane < keep) {
-      if (a.weight_out != a.weight) a.weight_out[base + s + lane] = weight[s + lane];
-      if (a.pos_out != nullptr && a.pos_out != a.pos) a.pos_out[base + s + lane] = pos[s + lane];
+    if (in_smem) {
+      const uint32_t bits = __ballot_sync(0xffffffffu, k);
+      if (lane == 0) kept_bits[s / 32] = bits;
+    } else if (k && s + lane < keep) {
+      copy(s + lane);
     }
   }
   __syncthreads();   // the list is complete, and every key has been read
+  if (in_smem && (a.weight_out != a.weight || (a.pos_out != nullptr && a.pos_out != a.pos))) {
+#pragma unroll 8
+    for (int s = tid; s < keep; s += ev::kThreads)
+      if ((kept_bits[s / 32] >> (s % 32)) & 1u) copy(s);
+  }
+#pragma unroll 4
   for (int x = tid; x < total; x += ev::kThreads) {
     const int2 m = moves[x];
     a.weight_out[base + m.y] = weight[m.x];
     if (a.pos_out != nullptr) a.pos_out[base + m.y] = pos[m.x];
+    // where the rows lie, worked out once and not by every thread that moves a piece
+    const longlong2 place = make_longlong2(slot_at(a.c, b, h, m.x), slot_at(a.c, b, h, m.y));
+    if (place.x < 0 || place.y < 0) cache::report(a.status, cache::kStatusInvalid);
+    if (kFused) places[x] = place;
+    else a.places[static_cast<int64_t>(bh) * a.max_moves + x] = place;
+  }
+  if (kFused) {
+    __syncthreads();
+    const int per_pass = ev::kThreads / a.c.vec, piece = tid % a.c.vec;
+    for (int x = tid / a.c.vec; x < total; x += per_pass) {
+      const longlong2 place = places[x];
+      if (place.x < 0 || place.y < 0) continue;
+      const uint4 k = a.c.k[place.x + piece], v = a.c.v[place.x + piece];
+      a.c.k[place.y + piece] = k;
+      a.c.v[place.y + piece] = v;
+    }
   }
 }
 
@@ -269,20 +347,30 @@ __global__ void __launch_bounds__(256) cache_move_kernel(const __grid_constant__
   const int piece = static_cast<int>(threadIdx.x) % a.c.vec;
   const int sub = static_cast<int>(threadIdx.x) / a.c.vec;
   for (int bh = static_cast<int>(blockIdx.y); bh < a.c.batch * a.c.kv_heads; bh += static_cast<int>(gridDim.y)) {
-    const int b = bh / a.c.kv_heads, h = bh - b * a.c.kv_heads;
-    if (h == 0 && blockIdx.x == 0 && threadIdx.x == 0)   // the only reader of lens in this kernel
+    const int b = bh / a.c.kv_heads;
+    if (bh == b * a.c.kv_heads && blockIdx.x == 0 && threadIdx.x == 0)   // the only reader of lens in this kernel
       a.lens_out[b] = min(min(max(a.lens[b], 0), a.c.capacity), a.keep);
     const int n = __ldg(a.counts + bh);
-    const int2* moves = a.moves + static_cast<int64_t>(bh) * a.max_moves;
-    for (int x = static_cast<int>(blockIdx.x) * per_block + sub; x < n; x += static_cast<int>(gridDim.x) * per_block) {
-      const int2 m = __ldg(moves + x);
-      const int64_t from = slot_at(a.c, b, h, m.x), to = slot_at(a.c, b, h, m.y);
-      if (from < 0 || to < 0) {
-        cache::report(a.status, cache::kStatusInvalid);
-        continue;
-      }
-      a.c.k[to + piece] = a.c.k[from + piece];
-      a.c.v[to + piece] = a.c.v[from + piece];
+    const longlong2* places = a.places + static_cast<int64_t>(bh) * a.max_moves;
+    // four rows a thread at a time, to have enough reads in flight
+    const int step = static_cast<int>(gridDim.x) * per_block;
+    for (int x0 = static_cast<int>(blockIdx.x) * per_block + sub; x0 < n; x0 += 4 * step) {
+      longlong2 place[4];
+      uint4 k[4], v[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) place[i] = x0 + i * step < n ? __ldg(places + x0 + i * step) : make_longlong2(-1, -1);
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        if (place[i].x >= 0 && place[i].y >= 0) {
+          k[i] = a.c.k[place[i].x + piece];
+          v[i] = a.c.v[place[i].x + piece];
+        }
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        if (place[i].x >= 0 && place[i].y >= 0) {
+          a.c.k[place[i].y + piece] = k[i];
+          a.c.v[place[i].y + piece] = v[i];
+        }
     }
   }
 }
@@ -292,9 +380,6 @@ __global__ void __launch_bounds__(256) cache_move_kernel(const __grid_constant__
 namespace gemm_tn_impl {
 
 namespace {
-
-// Keys in shared memory: what a block has beside the static histogram.
-constexpr int kMaxSmemKeys = 48 * 1024;
 
 template <class... Params, class... Args>
 cudaError_t launch(void (*kernel)(Params...), dim3 grid, int threads, size_t smem, cudaStream_t stream, Args... args) {
@@ -325,27 +410,35 @@ cudaError_t launch_cache_advance(const gemm_tn_dev::AppendArgs& a, cudaStream_t 
   return launch(gemm_tn_dev::cache_advance_kernel, dim3(static_cast<unsigned>((a.c.batch + 255) / 256), 1, 1), 256, 0, stream, a);
 }
 
-int evict_smem_keys(int capacity) { return std::min(capacity, kMaxSmemKeys); }
+int evict_smem_keys(int capacity) { return std::min(capacity, gemm_tn_dev::ev::kSmemKeys); }
 
-cudaError_t launch_cache_select(const gemm_tn_dev::EvictArgs& a, cudaStream_t stream) {
+int evict_fused_moves() { return gemm_tn_dev::ev::kFusedMoves; }
+
+template <bool kFused>
+static cudaError_t launch_select(const gemm_tn_dev::EvictArgs& a, cudaStream_t stream) {
   static std::atomic<uint64_t> done_mask{0};
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
   const uint64_t bit = 1ull << (dev & 63);
   if (!(done_mask.load(std::memory_order_acquire) & bit)) {
-    e = cudaFuncSetAttribute(gemm_tn_dev::cache_select_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxSmemKeys * 4);
+    e = cudaFuncSetAttribute(gemm_tn_dev::cache_select_kernel<kFused>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             gemm_tn_dev::ev::kSmemKeys * 4);
     if (e != cudaSuccess) return e;
     done_mask.fetch_or(bit, std::memory_order_acq_rel);
   }
-  return launch(gemm_tn_dev::cache_select_kernel, dim3(static_cast<unsigned>(a.c.batch * a.c.kv_heads), 1, 1),
+  return launch(gemm_tn_dev::cache_select_kernel<kFused>, dim3(static_cast<unsigned>(a.c.batch * a.c.kv_heads), 1, 1),
                 gemm_tn_dev::ev::kThreads, static_cast<size_t>(a.smem_keys) * 4, stream, a);
+}
+
+cudaError_t launch_cache_select(const gemm_tn_dev::EvictArgs& a, cudaStream_t stream) {
+  return a.moves == nullptr ? launch_select<true>(a, stream) : launch_select<false>(a, stream);
 }
 
 cudaError_t launch_cache_move(const gemm_tn_dev::EvictArgs& a, int num_sms, cudaStream_t stream) {
   const int lists = a.c.batch * a.c.kv_heads;
   const int rows_per_block = 256 / a.c.vec;
-  const int most = std::max(1, (a.max_moves + rows_per_block - 1) / rows_per_block);
+  const int most = std::max(1, (a.max_moves + 4 * rows_per_block - 1) / (4 * rows_per_block));
   const int per_list = std::min(most, std::max(1, (num_sms * 16 + lists - 1) / lists));
   return launch(gemm_tn_dev::cache_move_kernel,
                 dim3(static_cast<unsigned>(per_list), static_cast<unsigned>(std::min(lists, 65535)), 1), 256, 0, stream, a);

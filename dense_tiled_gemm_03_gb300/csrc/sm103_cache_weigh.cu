@@ -28,6 +28,7 @@
 
 #include <atomic>
 #include <cstdint>
+#include <type_traits>
 
 #include "gemm_tn_internal.h"
 #include "sm103_cache.cuh"
@@ -56,7 +57,7 @@ struct Cfg {
   static constexpr int kStages = kDim == 64 ? 8 : 4;
   static constexpr uint32_t kOffQ = 0;
   static constexpr uint32_t kOffK = kOffQ + kDimBoxes * kQBoxBytes;
-  static constexpr uint32_t kOffLse = kOffK + kStages * kTileBytes;   // per row (-log2e lse rounded, 2^ what that left)
+  static constexpr uint32_t kOffLse = kOffK + kStages * kTileBytes;   // [256] -log2e lse, rounded; [256] 2^ what that left
   // q_full, q_free, k_full[S], k_empty[S], s_full[2], s_empty[2], drain
   static constexpr int kNumBars = 2 + 2 * kStages + 4 + 1;
   static constexpr uint32_t kOffBar = kOffLse + 8u * kMaxRows;
@@ -142,7 +143,8 @@ __global__ void __launch_bounds__(C::kNumThreads, 1) cache_weigh_kernel(const __
   volatile uint32_t* abort_flag = reinterpret_cast<volatile uint32_t*>(smem + C::kOffAbort);
   cw::Walk* start_walk = reinterpret_cast<cw::Walk*>(smem + C::kOffStart);
   int* sums = reinterpret_cast<int*>(smem + C::kOffSums);
-  float2* row_lse = reinterpret_cast<float2*>(smem + C::kOffLse);
+  float* row_ref = reinterpret_cast<float*>(smem + C::kOffLse);
+  float* row_factor = row_ref + cw::kMaxRows;
 
   if (threadIdx.x == 0) {
     mbar_init(q_full, cw::kSumWarps);
@@ -284,7 +286,7 @@ __global__ void __launch_bounds__(C::kNumThreads, 1) cache_weigh_kernel(const __
         const int cols = max(1, (rows + 31) / 32) * 32;
         const int first_row = block * args.block_tokens;   // of the counted tokens
         // every sum warp is done with the block before: between them they have
-        // seen all its products complete, read its row_lse and written its weights
+        // seen all its products complete, read its rows' references and written its weights
         if (!(ok = wd.warp_wait(q_free, (static_cast<uint32_t>(q_blocks) & 1u) ^ 1u))) break;
         // query rows -> shared memory, K-major with the 128-byte swizzle
         constexpr int kPieces = C::kDim / 8;   // 16-byte pieces per row
@@ -311,7 +313,8 @@ __global__ void __launch_bounds__(C::kNumThreads, 1) cache_weigh_kernel(const __
             // lse * log2e as a rounded part and the factor that makes up for the rounding
             const float hi = lse * cw::kLog2e;
             const float lo = fmaf(lse, cw::kLog2e, -hi);
-            row_lse[row] = isinf(hi) ? make_float2(-INFINITY, 0.0f) : make_float2(-hi, ex2_approx(-lo));
+            row_ref[row] = isinf(hi) ? -INFINITY : -hi;
+            row_factor[row] = isinf(hi) ? 0.0f : ex2_approx(-lo);
           }
         }
         fence_proxy_async_shared();
@@ -329,34 +332,56 @@ __global__ void __launch_bounds__(C::kNumThreads, 1) cache_weigh_kernel(const __
           // causal: counted token i is the key's own query or a later one from i = key - (len - n) on
           const int low = args.causal ? (key - (w.len - w.n) - first_row) * args.group : 0;   // first column that sees the key
           const bool masked = __any_sync(0xffffffffu, live && low > 0);
-          float sum0 = 0.0f, sum1 = 0.0f;
-          for (int c0 = 0; c0 < cols; c0 += 32) {
-            uint32_t raw[32];
-            tmem_load_32x32(t_s + static_cast<uint32_t>(c0), raw);
-            tmem_load_wait();
-            const float4* lse4 = reinterpret_cast<const float4*>(row_lse + c0);
-            if (!masked) {
+          // two columns an instruction: p = 2^(s c - ref), sum += p factor. The next
+          // 32 columns come from tensor memory while these are worked on.
+          const uint64_t cc = f32x2_pack(c_log2, c_log2);
+          uint64_t sum01 = f32x2_pack(0.0f, 0.0f), sum23 = sum01;
+          uint32_t raw[2][32];
+          auto columns = [&](const uint32_t (&x)[32], int c0, auto mask) {
+            const ulonglong2* refs = reinterpret_cast<const ulonglong2*>(row_ref + c0);
+            const ulonglong2* factors = reinterpret_cast<const ulonglong2*>(row_factor + c0);
 #pragma unroll
-              for (int e = 0; e < 32; e += 2) {
-                const float4 x = lse4[e / 2];
-                sum0 = fmaf(ex2_approx(fmaf(__uint_as_float(raw[e]), c_log2, x.x)), x.y, sum0);
-                sum1 = fmaf(ex2_approx(fmaf(__uint_as_float(raw[e + 1]), c_log2, x.z)), x.w, sum1);
+            for (int e = 0; e < 32; e += 4) {
+              const ulonglong2 ref = refs[e / 4], f = factors[e / 4];
+              float p0, p1, p2, p3;
+              f32x2_unpack(f32x2_fma(f32x2_pack(__uint_as_float(x[e]), __uint_as_float(x[e + 1])), cc, ref.x), p0, p1);
+              f32x2_unpack(f32x2_fma(f32x2_pack(__uint_as_float(x[e + 2]), __uint_as_float(x[e + 3])), cc, ref.y), p2, p3);
+              p0 = ex2_approx(p0);
+              p1 = ex2_approx(p1);
+              p2 = ex2_approx(p2);
+              p3 = ex2_approx(p3);
+              if constexpr (mask.value) {
+                if (c0 + e < low) p0 = 0.0f;
+                if (c0 + e + 1 < low) p1 = 0.0f;
+                if (c0 + e + 2 < low) p2 = 0.0f;
+                if (c0 + e + 3 < low) p3 = 0.0f;
               }
-            } else {
-#pragma unroll
-              for (int e = 0; e < 32; e += 2) {
-                const float4 x = lse4[e / 2];
-                const float p0 = ex2_approx(fmaf(__uint_as_float(raw[e]), c_log2, x.x)) * x.y;
-                const float p1 = ex2_approx(fmaf(__uint_as_float(raw[e + 1]), c_log2, x.z)) * x.w;
-                if (c0 + e >= low) sum0 += p0;
-                if (c0 + e + 1 >= low) sum1 += p1;
+              sum01 = f32x2_fma(f32x2_pack(p0, p1), f.x, sum01);
+              sum23 = f32x2_fma(f32x2_pack(p2, p3), f.y, sum23);
+            }
+          };
+          auto all_columns = [&](auto mask) {
+            tmem_load_32x32(t_s, raw[0]);
+            for (int c0 = 0; c0 < cols; c0 += 64) {
+              tmem_load_wait();
+              if (c0 + 32 < cols) tmem_load_32x32(t_s + static_cast<uint32_t>(c0 + 32), raw[1]);
+              columns(raw[0], c0, mask);
+              if (c0 + 32 < cols) {
+                tmem_load_wait();
+                if (c0 + 64 < cols) tmem_load_32x32(t_s + static_cast<uint32_t>(c0 + 64), raw[0]);
+                columns(raw[1], c0 + 32, mask);
               }
             }
-          }
+          };
+          if (masked) all_columns(std::true_type{});
+          else all_columns(std::false_type{});
+          float sum0, sum1, sum2, sum3;
+          f32x2_unpack(sum01, sum0, sum1);
+          f32x2_unpack(sum23, sum2, sum3);
           tc_fence_before_sync();
           __syncwarp();
           if (lane == 0) mbar_arrive(s_empty(g));
-          if (live) args.weight_out[weight_row + key] = acc + (sum0 + sum1);
+          if (live) args.weight_out[weight_row + key] = acc + ((sum0 + sum1) + (sum2 + sum3));
         }
         __syncwarp();
         if (lane == 0) mbar_arrive(q_free);
