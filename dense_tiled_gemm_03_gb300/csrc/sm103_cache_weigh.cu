@@ -20,7 +20,9 @@
 // item the query rows come in blocks of at most 256, each block walking the
 // segment's tiles.
 //   warp 0      TMA producer (lane l copies the tile's l-th page)
-//   warp 1      MMA issuer: S^T (128 x rows) into one of two TMEM buffers
+//   warp 1      MMA issuer: S^T (128 keys x up to 128 rows) into one of the two
+//               TMEM buffers of the group that takes the tile, so that the next
+//               product runs while the group sums the one before
 //   warps 2-9   two groups of four taking every other tile; all eight gather
 //               the block's query rows into shared memory first
 #include <cuda.h>
@@ -42,7 +44,8 @@ constexpr int kProducerWarp = 0;
 constexpr int kMmaWarp = 1;
 constexpr int kFirstSumWarp = 2;
 constexpr int kSumWarps = 8;
-constexpr int kMaxRows = 256;      // query rows per block (columns of one TMEM buffer)
+constexpr int kMaxRows = 256;      // query rows per block
+constexpr int kHalf = 128;         // query rows per product (columns of one of the four TMEM buffers)
 constexpr float kLog2e = 1.4426950408889634f;
 
 template <int kDim_, bool kBf16_>
@@ -58,8 +61,8 @@ struct Cfg {
   static constexpr uint32_t kOffQ = 0;
   static constexpr uint32_t kOffK = kOffQ + kDimBoxes * kQBoxBytes;
   static constexpr uint32_t kOffLse = kOffK + kStages * kTileBytes;   // [256] -log2e lse, rounded; [256] 2^ what that left
-  // q_full, q_free, k_full[S], k_empty[S], s_full[2], s_empty[2], drain
-  static constexpr int kNumBars = 2 + 2 * kStages + 4 + 1;
+  // q_full, q_free, k_full[S], k_empty[S], s_full[2][2], s_empty[2][2], drain
+  static constexpr int kNumBars = 2 + 2 * kStages + 8 + 1;
   static constexpr uint32_t kOffBar = kOffLse + 8u * kMaxRows;
   static constexpr uint32_t kOffTmemSlot = kOffBar + 8u * kNumBars;
   static constexpr uint32_t kOffAbort = kOffTmemSlot + 4u;
@@ -136,9 +139,9 @@ __global__ void __launch_bounds__(C::kNumThreads, 1) cache_weigh_kernel(const __
   const uint32_t q_full = bar(0), q_free = bar(1);
   auto k_full = [&](int s) { return bar(2 + s); };
   auto k_empty = [&](int s) { return bar(2 + C::kStages + s); };
-  auto s_full = [&](int g) { return bar(2 + 2 * C::kStages + g); };
-  auto s_empty = [&](int g) { return bar(4 + 2 * C::kStages + g); };
-  const uint32_t drain_bar = bar(6 + 2 * C::kStages);
+  auto s_full = [&](int g, int buf) { return bar(2 + 2 * C::kStages + 2 * g + buf); };
+  auto s_empty = [&](int g, int buf) { return bar(6 + 2 * C::kStages + 2 * g + buf); };
+  const uint32_t drain_bar = bar(10 + 2 * C::kStages);
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + C::kOffTmemSlot);
   volatile uint32_t* abort_flag = reinterpret_cast<volatile uint32_t*>(smem + C::kOffAbort);
   cw::Walk* start_walk = reinterpret_cast<cw::Walk*>(smem + C::kOffStart);
@@ -153,9 +156,9 @@ __global__ void __launch_bounds__(C::kNumThreads, 1) cache_weigh_kernel(const __
       mbar_init(k_full(s), 1);
       mbar_init(k_empty(s), 1);
     }
-    for (int g = 0; g < 2; ++g) {
-      mbar_init(s_full(g), 1);
-      mbar_init(s_empty(g), 4);
+    for (int x = 0; x < 4; ++x) {
+      mbar_init(s_full(x >> 1, x & 1), 1);
+      mbar_init(s_empty(x >> 1, x & 1), 4);
     }
     mbar_init(drain_bar, 1);
     *abort_flag = 0u;
@@ -237,30 +240,34 @@ __global__ void __launch_bounds__(C::kNumThreads, 1) cache_weigh_kernel(const __
       const uint32_t leader = elect_one();
       int it = 0;       // tiles issued
       int q_blocks = 0;
+      int used[2] = {0, 0};   // products of each group so far
       bool ok = true;
       for (; ok && w.more(); w.next(args)) {
         const int blocks = w.blocks(args);
         for (int block = 0; ok && block < blocks; ++block, ++q_blocks) {
-          const int rows = w.block_rows(args, block);
-          const uint32_t n = static_cast<uint32_t>(max(1, (rows + 31) / 32)) * 32u;
-          const uint32_t idesc = C::kIdesc | ((n >> 3) << 17);
+          const int cols = max(1, (w.block_rows(args, block) + 31) / 32) * 32;
           if (!(ok = wd.warp_wait(q_full, static_cast<uint32_t>(q_blocks) & 1u))) break;
-          for (int j = 0; j < w.count; ++j, ++it) {
+          for (int j = 0; ok && j < w.count; ++j, ++it) {
             const int s = it % C::kStages, g = it & 1;
-            if (!(ok = wd.warp_wait(s_empty(g), (static_cast<uint32_t>(it >> 1) & 1u) ^ 1u))) break;
             if (!(ok = wd.warp_wait(k_full(s), static_cast<uint32_t>(it / C::kStages) & 1u))) break;
-            tc_fence_after_sync();
+            for (int c0 = 0; c0 < cols; c0 += cw::kHalf) {   // halves of the query rows
+              const int buf = used[g] & 1;
+              if (!(ok = wd.warp_wait(s_empty(g, buf), (static_cast<uint32_t>(used[g] >> 1) & 1u) ^ 1u))) break;
+              tc_fence_after_sync();
+              const uint32_t idesc = C::kIdesc | ((static_cast<uint32_t>(min(cols - c0, cw::kHalf)) >> 3) << 17);
+              const uint32_t t_s = tmem_base + 256u * static_cast<uint32_t>(g) + cw::kHalf * static_cast<uint32_t>(buf);
 #pragma unroll
-            for (int c = 0; c < C::kDimBoxes; ++c) {
-              const uint64_t a_desc = sw128_kmajor_desc(k_tile(s) + c * C::kBoxBytes);
-              const uint64_t b_desc = sw128_kmajor_desc(base + C::kOffQ + c * C::kQBoxBytes);
+              for (int c = 0; c < C::kDimBoxes; ++c) {
+                const uint64_t a_desc = sw128_kmajor_desc(k_tile(s) + c * C::kBoxBytes);
+                const uint64_t b_desc = sw128_kmajor_desc(base + C::kOffQ + c * C::kQBoxBytes + static_cast<uint32_t>(c0) * 128u);
 #pragma unroll
-              for (int kk = 0; kk < 4; ++kk)
-                mma_f16_warp(leader, tmem_base + 256u * static_cast<uint32_t>(g), a_desc + 2u * kk, b_desc + 2u * kk, idesc,
-                           (c | kk) != 0 ? 1u : 0u);
+                for (int kk = 0; kk < 4; ++kk)
+                  mma_f16_warp(leader, t_s, a_desc + 2u * kk, b_desc + 2u * kk, idesc, (c | kk) != 0 ? 1u : 0u);
+              }
+              mma_commit_warp(leader, s_full(g, buf));
+              ++used[g];
             }
-            mma_commit_warp(leader, s_full(g));
-            mma_commit_warp(leader, k_empty(s));
+            if (ok) mma_commit_warp(leader, k_empty(s));
           }
         }
       }
@@ -277,6 +284,7 @@ __global__ void __launch_bounds__(C::kNumThreads, 1) cache_weigh_kernel(const __
     const float c_log2 = args.scale_log2;
     const int sum_thread = static_cast<int>(threadIdx.x) - 64;
     int it = 0, q_blocks = 0;
+    int used = 0;   // products of this group so far
     bool ok = true;
     for (; ok && w.more(); w.next(args)) {
       const int blocks = w.blocks(args);
@@ -289,32 +297,52 @@ __global__ void __launch_bounds__(C::kNumThreads, 1) cache_weigh_kernel(const __
         // seen all its products complete, read its rows' references and written its weights
         if (!(ok = wd.warp_wait(q_free, (static_cast<uint32_t>(q_blocks) & 1u) ^ 1u))) break;
         // query rows -> shared memory, K-major with the 128-byte swizzle
+        // (four pieces a thread at a time: their loads are in flight together)
         constexpr int kPieces = C::kDim / 8;   // 16-byte pieces per row
-        for (int x = sum_thread; x < cols * kPieces; x += 32 * cw::kSumWarps) {
-          const int row = x / kPieces, piece = x % kPieces;
-          uint4 v = make_uint4(0u, 0u, 0u, 0u);
-          float lse = INFINITY;   // rows that do not count weigh nothing
-          if (row < rows) {
-            const int i = row / args.group, head = w.h * args.group + row - i * args.group;
-            int token = first_row + i;
-            if (args.rows != nullptr) token = __ldg(args.rows + static_cast<int64_t>(w.b) * args.max_rows + token);
-            if (token >= 0 && token < args.tokens) {
-              v = __ldg(reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(args.q) + w.b * args.q_batch +
-                                                       token * args.q_token + head * args.q_head) + piece);
-              if (piece == 0) lse = __ldg(args.lse + (static_cast<int64_t>(w.b) * args.tokens + token) * args.heads + head);
-              if (lse == -INFINITY) lse = INFINITY;
-            } else {
-              cache::report(args.status, cache::kStatusInvalid);
+        constexpr int kBatch = 4, kRowStep = 32 * cw::kSumWarps / kPieces;
+        const int piece = sum_thread % kPieces;
+        for (int row0 = sum_thread / kPieces; row0 < cols; row0 += kBatch * kRowStep) {
+          int token[kBatch], head[kBatch];
+          uint4 v[kBatch];
+          float lse[kBatch];
+#pragma unroll
+          for (int x = 0; x < kBatch; ++x) {
+            const int row = row0 + x * kRowStep, i = row / args.group;
+            head[x] = w.h * args.group + row - i * args.group;
+            token[x] = first_row + i;
+            if (row >= rows) token[x] = -1;
+            else if (args.rows != nullptr) {
+              token[x] = __ldg(args.rows + static_cast<int64_t>(w.b) * args.max_rows + token[x]);
+              if (token[x] < 0 || token[x] >= args.tokens) {
+                cache::report(args.status, cache::kStatusInvalid);
+                token[x] = -1;
+              }
             }
           }
-          const int box = piece / 8;
-          st_shared_v4(base + C::kOffQ + box * C::kQBoxBytes + row * 128u + (((piece & 7) ^ (row & 7)) * 16u), v.x, v.y, v.z, v.w);
-          if (piece == 0) {
-            // lse * log2e as a rounded part and the factor that makes up for the rounding
-            const float hi = lse * cw::kLog2e;
-            const float lo = fmaf(lse, cw::kLog2e, -hi);
-            row_ref[row] = isinf(hi) ? -INFINITY : -hi;
-            row_factor[row] = isinf(hi) ? 0.0f : ex2_approx(-lo);
+#pragma unroll
+          for (int x = 0; x < kBatch; ++x) {
+            v[x] = make_uint4(0u, 0u, 0u, 0u);
+            lse[x] = INFINITY;   // rows that do not count weigh nothing
+            if (token[x] >= 0) {
+              v[x] = __ldg(reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(args.q) + w.b * args.q_batch +
+                                                          token[x] * args.q_token + head[x] * args.q_head) + piece);
+              if (piece == 0)
+                lse[x] = __ldg(args.lse + (static_cast<int64_t>(w.b) * args.tokens + token[x]) * args.heads + head[x]);
+            }
+          }
+#pragma unroll
+          for (int x = 0; x < kBatch; ++x) {
+            const int row = row0 + x * kRowStep;
+            if (row >= cols) break;
+            st_shared_v4(base + C::kOffQ + (piece / 8) * C::kQBoxBytes + row * 128u + (((piece & 7) ^ (row & 7)) * 16u),
+                         v[x].x, v[x].y, v[x].z, v[x].w);
+            if (piece == 0) {
+              // lse * log2e as a rounded part and the factor that makes up for the rounding
+              const float hi = lse[x] * cw::kLog2e;
+              const float lo = fmaf(lse[x], cw::kLog2e, -hi);
+              row_ref[row] = isinf(hi) ? -INFINITY : -hi;
+              row_factor[row] = isinf(hi) ? 0.0f : ex2_approx(-lo);
+            }
           }
         }
         fence_proxy_async_shared();
@@ -327,8 +355,6 @@ __global__ void __launch_bounds__(C::kNumThreads, 1) cache_weigh_kernel(const __
           const bool live = key < w.len;
           float acc = 0.0f;
           if (live) acc = block == 0 ? args.weight[weight_row + key] : args.weight_out[weight_row + key];
-          if (!(ok = wd.warp_wait(s_full(g), static_cast<uint32_t>(it >> 1) & 1u))) break;
-          tc_fence_after_sync();
           // causal: counted token i is the key's own query or a later one from i = key - (len - n) on
           const int low = args.causal ? (key - (w.len - w.n) - first_row) * args.group : 0;   // first column that sees the key
           const bool masked = __any_sync(0xffffffffu, live && low > 0);
@@ -360,27 +386,35 @@ __global__ void __launch_bounds__(C::kNumThreads, 1) cache_weigh_kernel(const __
               sum23 = f32x2_fma(f32x2_pack(p2, p3), f.y, sum23);
             }
           };
-          auto all_columns = [&](auto mask) {
-            tmem_load_32x32(t_s, raw[0]);
-            for (int c0 = 0; c0 < cols; c0 += 64) {
+          // the columns c0 .. of a half, end - c0 of them
+          auto half = [&](uint32_t t_buf, int c0, int end, auto mask) {
+            tmem_load_32x32(t_buf, raw[0]);
+            for (; c0 < end; c0 += 64, t_buf += 64u) {
               tmem_load_wait();
-              if (c0 + 32 < cols) tmem_load_32x32(t_s + static_cast<uint32_t>(c0 + 32), raw[1]);
+              if (c0 + 32 < end) tmem_load_32x32(t_buf + 32u, raw[1]);
               columns(raw[0], c0, mask);
-              if (c0 + 32 < cols) {
+              if (c0 + 32 < end) {
                 tmem_load_wait();
-                if (c0 + 64 < cols) tmem_load_32x32(t_s + static_cast<uint32_t>(c0 + 64), raw[0]);
+                if (c0 + 64 < end) tmem_load_32x32(t_buf + 64u, raw[0]);
                 columns(raw[1], c0 + 32, mask);
               }
             }
           };
-          if (masked) all_columns(std::true_type{});
-          else all_columns(std::false_type{});
+          for (int c0 = 0; c0 < cols; c0 += cw::kHalf, ++used) {
+            const int buf = used & 1;
+            if (!(ok = wd.warp_wait(s_full(g, buf), static_cast<uint32_t>(used >> 1) & 1u))) break;
+            tc_fence_after_sync();
+            const uint32_t t_buf = t_s + cw::kHalf * static_cast<uint32_t>(buf);
+            if (masked) half(t_buf, c0, min(cols, c0 + cw::kHalf), std::true_type{});
+            else half(t_buf, c0, min(cols, c0 + cw::kHalf), std::false_type{});
+            tc_fence_before_sync();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(s_empty(g, buf));
+          }
+          if (!ok) break;
           float sum0, sum1, sum2, sum3;
           f32x2_unpack(sum01, sum0, sum1);
           f32x2_unpack(sum23, sum2, sum3);
-          tc_fence_before_sync();
-          __syncwarp();
-          if (lane == 0) mbar_arrive(s_empty(g));
           if (live) args.weight_out[weight_row + key] = acc + ((sum0 + sum1) + (sum2 + sum3));
         }
         __syncwarp();
