@@ -122,7 +122,7 @@ struct EvictArgs {
   int32_t* lens_out;
   int32_t* counts;          // workspace: [batch * kv heads] rows to move
   int2* moves;              // workspace: [batch * kv heads][max_moves] slots (from, to); NULL: the selecting blocks move
-  longlong2* places;        // workspace, the same moves: where the rows begin in the pools (16-byte units; -1: nowhere)
+  uint32_t* words;          // workspace: [batch * kv heads][3][ceil(capacity / 32)] where keys do not fit in shared memory
   int max_moves;
   int keep, recent;
   int smem_keys;            // slots whose keys fit in shared memory

@@ -406,18 +406,20 @@ int kv_cache_evict(int dtype, int64_t batch, const kv_cache* cache, int64_t keep
   args.status = d_status;
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   // few rows to move: one kernel (which must not write the lens that its other blocks read)
-  if (args.max_moves <= evict_fused_moves() && lens_out != cache->lens) {
+  if (args.max_moves <= evict_fused_moves() && args.smem_keys == args.c.capacity && lens_out != cache->lens) {
     const cudaError_t e = api_counted(launch_cache_select(args, s));
     return e == cudaSuccess ? GEMM_TN_OK : api_fail_cuda(e, "cache evict launch");
   }
   const size_t lists = static_cast<size_t>(batch * cache->kv_heads);
   const size_t count_bytes = (lists * 4 + 15) / 16 * 16;
+  const size_t move_bytes = lists * static_cast<size_t>(args.max_moves) * 8;
+  const size_t word_bytes = args.smem_keys == args.c.capacity ? 0 : lists * static_cast<size_t>((args.c.capacity + 31) / 32) * 12;
   void* workspace = nullptr;
-  cudaError_t e = api_workspace(count_bytes + lists * static_cast<size_t>(args.max_moves) * 24, s, &workspace);
+  cudaError_t e = api_workspace(count_bytes + move_bytes + word_bytes, s, &workspace);
   if (e != cudaSuccess) return api_fail_cuda(e, "workspace");
   args.counts = static_cast<int32_t*>(workspace);
-  args.places = reinterpret_cast<longlong2*>(static_cast<uint8_t*>(workspace) + count_bytes);
-  args.moves = reinterpret_cast<int2*>(args.places + lists * static_cast<size_t>(args.max_moves));
+  args.moves = reinterpret_cast<int2*>(static_cast<uint8_t*>(workspace) + count_bytes);
+  args.words = reinterpret_cast<uint32_t*>(static_cast<uint8_t*>(workspace) + count_bytes + move_bytes);
   e = api_counted(launch_cache_select(args, s));
   if (e == cudaSuccess) e = api_counted(launch_cache_move(args, sms, s));
   const cudaError_t freed = cudaFreeAsync(workspace, s);

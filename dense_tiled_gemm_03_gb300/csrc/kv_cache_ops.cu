@@ -130,6 +130,16 @@ __device__ __forceinline__ int warp_base(int x, int* sums, int* total) {
 
 }  // namespace ev
 
+// Where the rows of a move lie in the pools (16-byte units; -1 for a page that is none).
+__device__ __forceinline__ longlong2 places_of(const EvictArgs& a, int b, int h, int2 m) {
+  const longlong2 place = make_longlong2(slot_at(a.c, b, h, m.x), slot_at(a.c, b, h, m.y));
+  if (place.x < 0 || place.y < 0) {
+    cache::report(a.status, cache::kStatusInvalid);
+    return make_longlong2(-1, -1);
+  }
+  return place;
+}
+
 // One block per (sequence, KV head). The `keep` largest keys are found by
 // counting: the range between the smallest and the largest key is cut into 2048
 // equal bins, then the bin that holds the keep-th largest, until a bin is one
@@ -137,9 +147,8 @@ __device__ __forceinline__ int warp_base(int x, int* sums, int* total) {
 // of fixed leading bits, which weights share: counting those into a few bins of
 // shared memory one after the other took 20 us of 37 for 64 lists of 16384).
 // Ties go to the lowest slots. Then the holes before `keep` and the kept slots
-// behind it are numbered in ascending order by ballots and paired. Keys are
-// held in shared memory where they fit and recomputed from the arrays where
-// they do not. kFused: the block moves its rows itself, from a list in shared
+// behind it are numbered in ascending order and paired. Keys are held in shared
+// memory where they fit and recomputed from the arrays where they do not. kFused: the block moves its rows itself, from a list in shared
 // memory, and writes lens_out.
 template <bool kFused>
 __global__ void __launch_bounds__(ev::kThreads) cache_select_kernel(const __grid_constant__ EvictArgs a) {
@@ -150,7 +159,8 @@ __global__ void __launch_bounds__(ev::kThreads) cache_select_kernel(const __grid
   __shared__ int chosen[2];
   __shared__ int2 list[kFused ? ev::kFusedMoves : 1];
   __shared__ longlong2 places[kFused ? ev::kFusedMoves : 1];
-  __shared__ uint32_t kept_bits[ev::kSmemKeys / 32];
+  __shared__ uint32_t smem_words[ev::kSmemKeys / 32];
+  __shared__ int smem_ranks[2][ev::kSmemKeys / 32];
   griddep_wait();
   griddep_launch_dependents();
   const int bh = static_cast<int>(blockIdx.x);
@@ -176,18 +186,36 @@ __global__ void __launch_bounds__(ev::kThreads) cache_select_kernel(const __grid
   auto load_key = [&](int s) { return ev::key_of(weight[s], a.recent > 0 && pos[s] >= first_new); };
   const bool in_smem = len <= a.smem_keys;
   auto key = [&](int s) { return in_smem ? smem_keys[s] : load_key(s); };
+  const int word_pitch = (a.c.capacity + 31) / 32;
+  uint32_t* global_words = in_smem ? nullptr : a.words + static_cast<int64_t>(3 * bh) * word_pitch;
+  uint32_t* words = in_smem ? smem_words : global_words;
+  int* hole_ranks = in_smem ? smem_ranks[0] : reinterpret_cast<int*>(global_words + word_pitch);
+  int* mover_ranks = in_smem ? smem_ranks[1] : hole_ranks + word_pitch;
   // the newest slots (key 0xffffffff) are counted, and left out of the range
   uint32_t lowest = 0xffffffffu, highest = 0u;
   int newest = 0;
-#pragma unroll 8
-  for (int s = tid; s < len; s += ev::kThreads) {
-    const uint32_t k = load_key(s);
-    if (in_smem) smem_keys[s] = k;
-    if (k == 0xffffffffu) {
-      ++newest;
-    } else {
-      lowest = min(lowest, k);
-      highest = max(highest, k);
+  constexpr int kLoads = 8;   // slots a thread reads at a time
+  for (int x0 = tid; x0 < len; x0 += kLoads * ev::kThreads) {
+    float wt[kLoads];
+    int32_t ps[kLoads];
+#pragma unroll
+    for (int i = 0; i < kLoads; ++i) {
+      const int s = x0 + i * ev::kThreads;
+      wt[i] = s < len ? weight[s] : 0.0f;
+      ps[i] = s < len && a.recent > 0 ? pos[s] : 0;
+    }
+#pragma unroll
+    for (int i = 0; i < kLoads; ++i) {
+      const int s = x0 + i * ev::kThreads;
+      if (s >= len) break;
+      const uint32_t k = ev::key_of(wt[i], a.recent > 0 && ps[i] >= first_new);
+      if (in_smem) smem_keys[s] = k;
+      if (k == 0xffffffffu) {
+        ++newest;
+      } else {
+        lowest = min(lowest, k);
+        highest = max(highest, k);
+      }
     }
   }
   lowest = __reduce_min_sync(0xffffffffu, lowest);
@@ -253,85 +281,125 @@ __global__ void __launch_bounds__(ev::kThreads) cache_select_kernel(const __grid
     }
   }
 
-  // each warp has one contiguous run of slots; runs of 32 in ascending order
-  const int per_warp = (len + 32 * ev::kWarps - 1) / (32 * ev::kWarps) * 32;
-  const int s0 = min(len, warp * per_warp), s1 = min(len, s0 + per_warp);
-  const bool some_ties = ties != need;   // not all slots with the limit's key stay
-  int ties_before = 0;
-  if (some_ties) {
+  // Kept slots as words of 32 bits, and from here on a thread has a run of
+  // words: ranks come from one scan of their bit counts.
+  const int num_words = (len + 31) / 32;
+  for (int x = warp; x < num_words; x += ev::kWarps) {
+    const int s = 32 * x + lane;
+    const uint32_t k = s < len ? key(s) : 0u;
+    const uint32_t bits = __ballot_sync(0xffffffffu, s < len && k >= limit);
+    if (lane == 0) words[x] = bits;
+  }
+  __syncthreads();
+  const int run = (num_words + ev::kThreads - 1) / ev::kThreads;
+  const int w0 = min(num_words, tid * run), w1 = min(num_words, w0 + run);
+  // exclusive sum over the threads of the block
+  auto block_base = [&](int x) {
+    int v = x;
+#pragma unroll
+    for (int d = 1; d < 32; d *= 2) {
+      const int y = __shfl_up_sync(0xffffffffu, v, d);
+      if (lane >= d) v += y;
+    }
+    return ev::warp_base(__shfl_sync(0xffffffffu, v, 31), sums, &total) + v - x;
+  };
+  if (ties != need) {   // of the slots with the limit's key the lowest `need` stay
+    auto tied = [&](int x) {
+      uint32_t bits = 0;
+      for (uint32_t left = words[x]; left != 0u; left &= left - 1u) {
+        const int i = __ffs(left) - 1;
+        if (key(32 * x + i) == limit) bits |= 1u << i;
+      }
+      return bits;
+    };
     int mine = 0;
-    for (int s = s0; s < s1; s += 32)
-      mine += __popc(__ballot_sync(0xffffffffu, s + lane < s1 && key(s + lane) == limit));
-    ties_before = ev::warp_base(mine, sums, &total);
-  }
-  // whether slot s stays; called by whole warps in ascending order from s0
-  auto kept = [&](int s, int& tie_rank) {
-    const uint32_t k = s + lane < s1 ? key(s + lane) : 0u;
-    const bool in = keep > 0 && s + lane < s1;
-    if (!some_ties) return in && k >= limit;
-    const bool tie = s + lane < s1 && k == limit;
-    const uint32_t tied = __ballot_sync(0xffffffffu, tie);
-    const int rank = tie_rank + __popc(tied & ((1u << lane) - 1u));
-    tie_rank += __popc(tied);
-    return in && (k > limit || (tie && rank < need));
-  };
-  // a kept slot before `keep` stays where it is
-  auto copy = [&](int s) {
-    if (a.weight_out != a.weight) a.weight_out[base + s] = weight[s];
-    if (a.pos_out != nullptr && a.pos_out != a.pos) a.pos_out[base + s] = pos[s];
-  };
-  int holes = 0, movers = 0, tie_rank = ties_before;
-  for (int s = s0; s < s1; s += 32) {
-    const bool k = kept(s, tie_rank);
-    const bool in = s + lane < s1;
-    holes += __popc(__ballot_sync(0xffffffffu, in && !k && s + lane < keep));
-    movers += __popc(__ballot_sync(0xffffffffu, in && k && s + lane >= keep));
-  }
-  int hole_rank = ev::warp_base(holes, sums, &total);
-  int mover_rank = ev::warp_base(movers, sums, &total);   // as many movers as holes
-  if (!kFused && tid == 0) a.counts[bh] = total;
-  int2* moves = kFused ? list : a.moves + static_cast<int64_t>(bh) * a.max_moves;
-  tie_rank = ties_before;
-  for (int s = s0; s < s1; s += 32) {
-    const bool k = kept(s, tie_rank);
-    const bool in = s + lane < s1;
-    const bool hole = in && !k && s + lane < keep, mover = in && k && s + lane >= keep;
-    const uint32_t hb = __ballot_sync(0xffffffffu, hole), mb = __ballot_sync(0xffffffffu, mover);
-    const uint32_t below = (1u << lane) - 1u;
-    if (hole) moves[hole_rank + __popc(hb & below)].y = s + lane;
-    if (mover) moves[mover_rank + __popc(mb & below)].x = s + lane;
-    hole_rank += __popc(hb);
-    mover_rank += __popc(mb);
-    if (in_smem) {
-      const uint32_t bits = __ballot_sync(0xffffffffu, k);
-      if (lane == 0) kept_bits[s / 32] = bits;
-    } else if (k && s + lane < keep) {
-      copy(s + lane);
+    for (int x = w0; x < w1; ++x) mine += __popc(tied(x));
+    int stay_here = need - block_base(mine);   // of this thread's ties
+    for (int x = w0; x < w1; ++x) {
+      uint32_t drop = tied(x);
+      for (; drop != 0u && stay_here > 0; --stay_here) drop &= drop - 1u;
+      words[x] &= ~drop;
     }
   }
-  __syncthreads();   // the list is complete, and every key has been read
-  if (in_smem && (a.weight_out != a.weight || (a.pos_out != nullptr && a.pos_out != a.pos))) {
-#pragma unroll 8
-    for (int s = tid; s < keep; s += ev::kThreads)
-      if ((kept_bits[s / 32] >> (s % 32)) & 1u) copy(s);
+  // slots of word x before `keep`
+  auto before_keep = [&](int x) { return cache::low_bits(keep - 32 * x); };
+  auto holes_of = [&](int x) { return ~words[x] & before_keep(x); };
+  auto movers_of = [&](int x) { return words[x] & ~before_keep(x); };
+  int holes = 0, movers = 0;
+  for (int x = w0; x < w1; ++x) {
+    holes += __popc(holes_of(x));
+    movers += __popc(movers_of(x));
   }
-#pragma unroll 4
-  for (int x = tid; x < total; x += ev::kThreads) {
-    const int2 m = moves[x];
-    a.weight_out[base + m.y] = weight[m.x];
-    if (a.pos_out != nullptr) a.pos_out[base + m.y] = pos[m.x];
-    // where the rows lie, worked out once and not by every thread that moves a piece
-    const longlong2 place = make_longlong2(slot_at(a.c, b, h, m.x), slot_at(a.c, b, h, m.y));
-    if (place.x < 0 || place.y < 0) cache::report(a.status, cache::kStatusInvalid);
-    if (kFused) places[x] = place;
-    else a.places[static_cast<int64_t>(bh) * a.max_moves + x] = place;
+  int hole_rank = block_base(holes);
+  int mover_rank = block_base(movers);   // as many movers as holes: `total`
+  for (int x = w0; x < w1; ++x) {
+    hole_ranks[x] = hole_rank;
+    mover_ranks[x] = mover_rank;
+    hole_rank += __popc(holes_of(x));
+    mover_rank += __popc(movers_of(x));
+  }
+  __syncthreads();
+  int2* moves = kFused ? list : a.moves + static_cast<int64_t>(bh) * a.max_moves;
+  const uint32_t below = (1u << lane) - 1u;
+#pragma unroll 2
+  for (int x = warp; x < num_words; x += ev::kWarps) {
+    const uint32_t hole = holes_of(x), mover = movers_of(x);
+    if ((hole >> lane) & 1u) moves[hole_ranks[x] + __popc(hole & below)].y = 32 * x + lane;
+    if ((mover >> lane) & 1u) moves[mover_ranks[x] + __popc(mover & below)].x = 32 * x + lane;
+  }
+  if (!kFused && tid == 0) a.counts[bh] = total;
+  __syncthreads();   // the list is complete, and every key has been read
+  // Weights and positions: a kept slot before `keep` keeps its own (copied
+  // where they go elsewhere), a moved one takes them along. A thread's reads go
+  // out together, before its first write.
+  const bool copy_weight = a.weight_out != a.weight, copy_pos = a.pos_out != nullptr && a.pos_out != a.pos;
+  constexpr int kBatch = 4;
+  if (copy_weight || copy_pos) {
+    for (int x0 = tid; x0 < keep; x0 += kBatch * ev::kThreads) {
+      float wt[kBatch];
+      int32_t ps[kBatch];
+      bool on[kBatch];
+#pragma unroll
+      for (int i = 0; i < kBatch; ++i) {
+        const int s = x0 + i * ev::kThreads;
+        on[i] = s < keep && ((words[s / 32] >> (s % 32)) & 1u);
+        wt[i] = on[i] && copy_weight ? weight[s] : 0.0f;
+        ps[i] = on[i] && copy_pos ? pos[s] : 0;
+      }
+#pragma unroll
+      for (int i = 0; i < kBatch; ++i) {
+        const int s = x0 + i * ev::kThreads;
+        if (on[i] && copy_weight) a.weight_out[base + s] = wt[i];
+        if (on[i] && copy_pos) a.pos_out[base + s] = ps[i];
+      }
+    }
+  }
+  for (int x0 = tid; x0 < total; x0 += kBatch * ev::kThreads) {
+    int2 m[kBatch];
+    float wt[kBatch];
+    int32_t ps[kBatch];
+#pragma unroll
+    for (int i = 0; i < kBatch; ++i) m[i] = x0 + i * ev::kThreads < total ? moves[x0 + i * ev::kThreads] : make_int2(0, 0);
+#pragma unroll
+    for (int i = 0; i < kBatch; ++i) {
+      wt[i] = weight[m[i].x];
+      ps[i] = pos != nullptr ? pos[m[i].x] : 0;
+    }
+#pragma unroll
+    for (int i = 0; i < kBatch; ++i) {
+      const int x = x0 + i * ev::kThreads;
+      if (x >= total) break;
+      a.weight_out[base + m[i].y] = wt[i];
+      if (a.pos_out != nullptr) a.pos_out[base + m[i].y] = ps[i];
+      if (kFused) places[x] = places_of(a, b, h, m[i]);
+    }
   }
   if (kFused) {
     __syncthreads();
     const int per_pass = ev::kThreads / a.c.vec, piece = tid % a.c.vec;
     for (int x = tid / a.c.vec; x < total; x += per_pass) {
       const longlong2 place = places[x];
-      if (place.x < 0 || place.y < 0) continue;
+      if (place.x < 0) continue;
       const uint4 k = a.c.k[place.x + piece], v = a.c.v[place.x + piece];
       a.c.k[place.y + piece] = k;
       a.c.v[place.y + piece] = v;
@@ -339,37 +407,50 @@ __global__ void __launch_bounds__(ev::kThreads) cache_select_kernel(const __grid
   }
 }
 
-// Moves the listed rows: grid (blocks per list, lists).
-__global__ void __launch_bounds__(256) cache_move_kernel(const __grid_constant__ EvictArgs a) {
+// Moves the listed rows: grid (blocks per list, lists). A warp takes 8 moves (16 of dim 64); each of its
+// first lanes works out one move's places (page look-ups and divisions once a
+// row, not once a piece) and the warp then moves the rows, 16 bytes a lane,
+// eight reads a lane in flight.
+__global__ void __launch_bounds__(256, 4) cache_move_kernel(const __grid_constant__ EvictArgs a) {
   griddep_wait();
   griddep_launch_dependents();
-  const int per_block = 256 / a.c.vec;
-  const int piece = static_cast<int>(threadIdx.x) % a.c.vec;
-  const int sub = static_cast<int>(threadIdx.x) / a.c.vec;
+  const int lane = static_cast<int>(threadIdx.x) & 31;
+  const int piece = lane % a.c.vec, sub = lane / a.c.vec, rows = 32 / a.c.vec;   // rows a warp moves at a time
   for (int bh = static_cast<int>(blockIdx.y); bh < a.c.batch * a.c.kv_heads; bh += static_cast<int>(gridDim.y)) {
-    const int b = bh / a.c.kv_heads;
-    if (bh == b * a.c.kv_heads && blockIdx.x == 0 && threadIdx.x == 0)   // the only reader of lens in this kernel
+    const int b = bh / a.c.kv_heads, h = bh - b * a.c.kv_heads;
+    if (h == 0 && blockIdx.x == 0 && threadIdx.x == 0)   // the only reader of lens in this kernel
       a.lens_out[b] = min(min(max(a.lens[b], 0), a.c.capacity), a.keep);
     const int n = __ldg(a.counts + bh);
-    const longlong2* places = a.places + static_cast<int64_t>(bh) * a.max_moves;
-    // four rows a thread at a time, to have enough reads in flight
-    const int step = static_cast<int>(gridDim.x) * per_block;
-    for (int x0 = static_cast<int>(blockIdx.x) * per_block + sub; x0 < n; x0 += 4 * step) {
-      longlong2 place[4];
+    const int thread = static_cast<int>(blockIdx.x * 256 + threadIdx.x), threads = static_cast<int>(gridDim.x) * 256;
+    const int2* moves = a.moves + static_cast<int64_t>(bh) * a.max_moves;
+    const int batch = 4 * rows;   // moves of a warp at a time
+    auto place_of = [&](int x) {
+      if (lane >= batch || x >= n) return make_longlong2(-1, -1);
+      return places_of(a, b, h, __ldg(moves + x));
+    };
+    // lane l of the first `batch`: move l % rows of the l / rows-th run of `rows` of this warp
+    const int stride = threads / 32 * rows, step = 4 * stride;
+    int x0 = thread / 32 * rows;
+    const int ahead = lane / rows * stride + lane % rows;
+    longlong2 place = place_of(x0 + ahead);
+    for (; x0 < n; x0 += step) {
+      int64_t to[4];
       uint4 k[4], v[4];
 #pragma unroll
-      for (int i = 0; i < 4; ++i) place[i] = x0 + i * step < n ? __ldg(places + x0 + i * step) : make_longlong2(-1, -1);
-#pragma unroll
-      for (int i = 0; i < 4; ++i)
-        if (place[i].x >= 0 && place[i].y >= 0) {
-          k[i] = a.c.k[place[i].x + piece];
-          v[i] = a.c.v[place[i].x + piece];
+      for (int i = 0; i < 4; ++i) {
+        const int64_t from = __shfl_sync(0xffffffffu, place.x, i * rows + sub);
+        to[i] = __shfl_sync(0xffffffffu, place.y, i * rows + sub);
+        if (to[i] >= 0) {
+          k[i] = a.c.k[from + piece];
+          v[i] = a.c.v[from + piece];
         }
+      }
+      place = place_of(x0 + step + ahead);   // the next moves' look-ups, while the rows are on their way
 #pragma unroll
       for (int i = 0; i < 4; ++i)
-        if (place[i].x >= 0 && place[i].y >= 0) {
-          a.c.k[place[i].y + piece] = k[i];
-          a.c.v[place[i].y + piece] = v[i];
+        if (to[i] >= 0) {
+          a.c.k[to[i] + piece] = k[i];
+          a.c.v[to[i] + piece] = v[i];
         }
     }
   }
@@ -437,9 +518,9 @@ cudaError_t launch_cache_select(const gemm_tn_dev::EvictArgs& a, cudaStream_t st
 
 cudaError_t launch_cache_move(const gemm_tn_dev::EvictArgs& a, int num_sms, cudaStream_t stream) {
   const int lists = a.c.batch * a.c.kv_heads;
-  const int rows_per_block = 256 / a.c.vec;
-  const int most = std::max(1, (a.max_moves + 4 * rows_per_block - 1) / (4 * rows_per_block));
-  const int per_list = std::min(most, std::max(1, (num_sms * 16 + lists - 1) / lists));
+  const int per_block = 8 * 4 * (32 / a.c.vec);   // moves of a block at a time
+  const int most = std::max(1, (a.max_moves + per_block - 1) / per_block);
+  const int per_list = std::min(most, std::max(1, (num_sms * 8 + lists - 1) / lists));
   return launch(gemm_tn_dev::cache_move_kernel,
                 dim3(static_cast<unsigned>(per_list), static_cast<unsigned>(std::min(lists, 65535)), 1), 256, 0, stream, a);
 }
