@@ -81,7 +81,8 @@ struct Cfg {
   static constexpr uint32_t kOffAbort = kOffTmemSlot + 4u;
   static constexpr uint32_t kOffStart = kOffAbort + 4u;   // the chunk's first Walk
   static constexpr uint32_t kOffSums = kOffStart + 36u;   // 32 words of the search for it
-  static constexpr uint32_t kSmemBytes = kOffSums + 128u + 1024u;   // + slack to align the base to 1024
+  static constexpr uint32_t kOffNext = kOffSums + 128u;   // each softmax warp's next Walk
+  static constexpr uint32_t kSmemBytes = kOffNext + 8u * 36u + 1024u;   // + slack to align the base to 1024
   static constexpr uint32_t kTmemCols = 512;
   static constexpr uint32_t kColS = 0;      // S_u: 128 fp32 columns at 128 u (P_u over half of them)
   static constexpr uint32_t kColO = 256;    // O_u: dim fp32 columns at 256 + dim u
@@ -184,18 +185,6 @@ __global__ void __launch_bounds__(C::kNumThreads) __maxnreg__(C::kMaxRegs)
     int seg = 0;    // segments begun
     bool ok = true;
     for (; ok && w.more(); w.next(args), ++seg) {
-      for (int u = 0; u < args.units && ok; ++u) {
-        const int slot = parity_mode ? seg & 1 : u;
-        const uint32_t ph = static_cast<uint32_t>(parity_mode ? seg >> 1 : seg) & 1u;
-        ok = wd.warp_wait(q_empty(slot), ph ^ 1u);
-        if (ok && lane == 0) {
-          mbar_arrive_expect_tx(q_full(slot), q_bytes);
-          for (int c = 0; c < C::kDimBoxes; ++c)
-            tma_load_4d(&args.tmap_q, q_tile(slot) + c * C::kBoxBytes, q_full(slot), 64 * c, w.h * args.group,
-                        (w.ru * args.units + u) * args.tile_tokens, w.b);
-        }
-        if (ok) issued_q[slot] = static_cast<int>(ph);
-      }
       const int32_t* table = args.page_table + static_cast<int64_t>(w.b) * args.table_stride;
       auto page_of = [&](int j) {
         return ta::page_of(args, table, ta::tile_of(w.len, w.tl, has_new, j), box_rows, static_cast<int>(lane));
@@ -221,6 +210,23 @@ __global__ void __launch_bounds__(C::kNumThreads) __maxnreg__(C::kMaxRegs)
                         k_full(s), 64 * c, w.h, slot0, t.fresh ? w.b : page);
         }
         issued_k[s] = static_cast<int>(ph);
+        if (j == w.j0) {
+          // the segment's queries, behind its first keys: their slots are free
+          // only once the segment before has multiplied its last keys
+          for (int u = 0; u < args.units && ok; ++u) {
+            const int slot = parity_mode ? seg & 1 : u;
+            const uint32_t q_ph = static_cast<uint32_t>(parity_mode ? seg >> 1 : seg) & 1u;
+            ok = wd.warp_wait(q_empty(slot), q_ph ^ 1u);
+            if (ok && lane == 0) {
+              mbar_arrive_expect_tx(q_full(slot), q_bytes);
+              for (int c = 0; c < C::kDimBoxes; ++c)
+                tma_load_4d(&args.tmap_q, q_tile(slot) + c * C::kBoxBytes, q_full(slot), 64 * c, w.h * args.group,
+                            (w.ru * args.units + u) * args.tile_tokens, w.b);
+            }
+            if (ok) issued_q[slot] = static_cast<int>(q_ph);
+          }
+          if (!ok) break;
+        }
         const int sv = it % C::kVStages;
         const uint32_t phv = static_cast<uint32_t>(it / C::kVStages) & 1u;
         if (!(ok = wd.warp_wait(v_empty(sv), phv ^ 1u))) break;
@@ -348,12 +354,23 @@ __global__ void __launch_bounds__(C::kNumThreads) __maxnreg__(C::kMaxRegs)
     const uint32_t t_o = tmem_base + lane_off + C::kColO + static_cast<uint32_t>(C::kDim * u);
     const float c_log2 = args.scale_log2;
     const int step = parity_mode ? 2 : 1;
+    ta::Walk* next_walk = reinterpret_cast<ta::Walk*>(smem + C::kOffNext) + (warp - ta::kFirstSoftmaxWarp);
     int it0 = 0;                    // ring number of the segment's first tile
     uint32_t tiles_done = 0;        // tiles of this unit so far
     uint32_t ends[2] = {0, 0};      // o_done phases of the units so far
     uint32_t joins = 0;             // exchanges so far (parity mode)
     bool ok = true;
-    for (; ok && w.more(); it0 += w.count, w.next(args)) {
+    for (; ok && w.more(); it0 += w.count, w = *next_walk) {
+      {
+        // worked out now, while the first scores are awaited: at the end of the
+        // segment its reads of the lengths would queue behind the rows' writes
+        // (3 us after a part of 256 rows)
+        ta::Walk next = w;
+        next.next(args);
+        __syncwarp();
+        if (lane == 0) *next_walk = next;
+        __syncwarp();
+      }
       const int end[2] = {w.unit_end(args, 0), w.unit_end(args, 1)};
       const int i0 = (w.ru * args.units + (parity_mode ? 0 : u)) * args.tile_tokens;   // first token of the tile
       const int token = i0 + r_token;
@@ -449,26 +466,26 @@ __global__ void __launch_bounds__(C::kNumThreads) __maxnreg__(C::kMaxRegs)
           // exceeds 2^8 unless the row sum does, so only then is the tile's
           // maximum taken, and moved to where it is past that factor (the warp
           // then computes the tile again and rescales O: the same softmax).
-          if (__any_sync(0xffffffffu, unset)) {
-            const float mx = row_max();
-            if (unset && mx != -INFINITY) {
-              m_ref = mx * c_log2;
-              unset = false;
-            }
-          }
-          float alpha = 1.0f;
-          float sum = exp_pass(-m_ref);
-          if (__any_sync(0xffffffffu, live && !(sum <= 256.0f))) {
-            const float m_tile = row_max() * c_log2;
-            const bool move = live && m_tile > m_ref + 8.0f;
-            if (__any_sync(0xffffffffu, move)) {
-              if (move) {
+          // One copy of the code for both: it is long, and fetched cold.
+          float alpha = 1.0f, sum;
+          bool take_max = __any_sync(0xffffffffu, unset);
+          while (true) {
+            if (take_max) {
+              const float m_tile = row_max() * c_log2;
+              if (unset) {
+                if (m_tile != -INFINITY) {
+                  m_ref = m_tile;
+                  unset = false;
+                }
+              } else if (live && m_tile > m_ref + 8.0f) {
                 alpha = ex2_approx(m_ref - m_tile);
                 m_ref = m_tile;
               }
-              tmem_store_wait();   // the first pass's stores land before they are overwritten
-              sum = exp_pass(-m_ref);
             }
+            sum = exp_pass(-m_ref);
+            if (take_max || !__any_sync(0xffffffffu, live && !(sum <= 256.0f))) break;
+            take_max = true;
+            tmem_store_wait();   // the first pass's stores land before they are overwritten
           }
           l = l * alpha + sum;
           if (__any_sync(0xffffffffu, alpha != 1.0f)) {
@@ -613,16 +630,17 @@ __global__ void __launch_bounds__(C::kNumThreads) __maxnreg__(C::kMaxRegs)
 // Joins the parts of the items that a chunk boundary cut. Block x looks at the
 // boundary before chunk x + 1; the first boundary inside an item joins it:
 // part 0 lies in the chunk before, the others in the chunks after, in order.
-// A warp has 32 rows and kPer four-column pieces of each: it reads 512
-// contiguous bytes of a part at a time and a thread writes whole sectors of o.
-// Two groups of eight warps take every other part, each as an online softmax;
-// the second hands its sums to the first in shared memory.
-template <int kDim, bool kBf16>
-__global__ void __launch_bounds__(512) tree_attn_join_kernel(const __grid_constant__ TreeArgs args) {
+// A warp has 32 rows and two four-column pieces of each (blocks: 32 rows by 64
+// columns): it reads 512 contiguous bytes of a part at a time.
+// With two groups (few rows, perhaps many parts) each takes every other part,
+// as an online softmax, and the second hands its sums to the first in shared
+// memory.
+template <int kDim, bool kBf16, int kGroups>
+__global__ void __launch_bounds__(256 * kGroups) tree_attn_join_kernel(const __grid_constant__ TreeArgs args) {
   constexpr int kPieces = kDim / 4;            // four-column pieces of a row
-  constexpr int kPer = kPieces / 8;            // pieces per thread
-  __shared__ float4 other_o[kPer][256];
-  __shared__ float2 other_ml[256];
+  constexpr int kPer = 2;                      // pieces per thread
+  __shared__ float4 other_o[kGroups == 2 ? kPer : 1][kGroups == 2 ? 256 : 1];
+  __shared__ float2 other_ml[kGroups == 2 ? 256 : 1];
   griddep_wait();
   griddep_launch_dependents();
   const int chunk = static_cast<int>(blockIdx.x) + 1;
@@ -633,7 +651,7 @@ __global__ void __launch_bounds__(512) tree_attn_join_kernel(const __grid_consta
   const int parts = 2 + (tiles - j0 - 1) / per_chunk;
   const int rows_per_part = args.part_rows;
   const int group = static_cast<int>(threadIdx.x) >> 8, tid = static_cast<int>(threadIdx.x) & 255;
-  const int piece0 = (tid >> 5) * kPer;
+  const int piece0 = static_cast<int>(blockIdx.z) * 16 + (tid >> 5) * kPer;
   const int row = static_cast<int>(blockIdx.y) * 32 + (tid & 31);
   const int unit = row / ta::kTileRows, r = row % ta::kTileRows;
   const int r_token = r / args.group;
@@ -660,7 +678,7 @@ __global__ void __launch_bounds__(512) tree_attn_join_kernel(const __grid_consta
     const int own_tiles = ta::unit_tiles(args, len, tl, ru, unit);
     const int own_parts = own_tiles > j0 ? min(parts, 2 + (own_tiles - j0 - 1) / per_chunk) : 1;
 #pragma unroll 4
-    for (int p = group; p < own_parts; p += 2) {
+    for (int p = group; p < own_parts; p += kGroups) {
       const int64_t slot = p == 0 ? (chunk - 1) * 2 + 1 : (chunk + p - 1) * 2;
       const float2 ml = __ldg(args.part_ml + slot * rows_per_part + row);
       float4 y[kPer];
@@ -670,17 +688,20 @@ __global__ void __launch_bounds__(512) tree_attn_join_kernel(const __grid_consta
       add(ml, y);
     }
   }
-  if (group == 1) {
+  if constexpr (kGroups == 2) {
+    if (group == 1) {
 #pragma unroll
-    for (int x = 0; x < kPer; ++x) other_o[x][tid] = acc[x];
-    other_ml[tid] = make_float2(m, sum);
+      for (int x = 0; x < kPer; ++x) other_o[x][tid] = acc[x];
+      other_ml[tid] = make_float2(m, sum);
+    }
+    __syncthreads();
+    if (group == 1) return;
+    float4 y[kPer];
+#pragma unroll
+    for (int x = 0; x < kPer; ++x) y[x] = other_o[x][tid];
+    add(other_ml[tid], y);
   }
-  __syncthreads();
-  if (group == 1 || !live) return;
-  float4 y[kPer];
-#pragma unroll
-  for (int x = 0; x < kPer; ++x) y[x] = other_o[x][tid];
-  add(other_ml[tid], y);
+  if (!live) return;
   const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
   const int64_t out_row = (static_cast<int64_t>(b) * args.tokens + token) * args.heads + h * args.group + (r - r_token * args.group);
   uint4* out = reinterpret_cast<uint4*>(static_cast<uint16_t*>(args.o) + out_row * kDim + piece0 * 4);
@@ -724,20 +745,20 @@ cudaError_t launch_cfg(const gemm_tn_dev::TreeArgs& args, cudaStream_t stream) {
   return cudaLaunchKernelEx(&cfg, gemm_tn_dev::tree_attn_kernel<C>, args);
 }
 
-template <int kDim, bool kBf16>
+template <int kDim, bool kBf16, int kGroups>
 cudaError_t launch_join(const gemm_tn_dev::TreeArgs& args, cudaStream_t stream) {
   cudaLaunchConfig_t cfg{};
   const int rows = args.units == 2 ? args.part_rows
                                    : (args.tokens < args.tile_tokens ? args.tokens : args.tile_tokens) * args.group;
-  cfg.gridDim = dim3(static_cast<unsigned>(args.chunks - 1), static_cast<unsigned>((rows + 31) / 32), 1);
-  cfg.blockDim = dim3(512, 1, 1);
+  cfg.gridDim = dim3(static_cast<unsigned>(args.chunks - 1), static_cast<unsigned>((rows + 31) / 32), kDim / 64);
+  cfg.blockDim = dim3(256 * kGroups, 1, 1);
   cfg.stream = stream;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = dependent_launch_enabled() ? 1 : 0;
-  return cudaLaunchKernelEx(&cfg, gemm_tn_dev::tree_attn_join_kernel<kDim, kBf16>, args);
+  return cudaLaunchKernelEx(&cfg, gemm_tn_dev::tree_attn_join_kernel<kDim, kBf16, kGroups>, args);
 }
 
 }  // namespace
@@ -754,8 +775,13 @@ cudaError_t launch_tree_attn(int head_dim, bool bf16, const gemm_tn_dev::TreeArg
 }
 
 cudaError_t launch_tree_attn_join(int head_dim, bool bf16, const gemm_tn_dev::TreeArgs& args, cudaStream_t stream) {
-  if (head_dim == 64) return bf16 ? launch_join<64, true>(args, stream) : launch_join<64, false>(args, stream);
-  if (head_dim == 128) return bf16 ? launch_join<128, true>(args, stream) : launch_join<128, false>(args, stream);
+  if (args.part_rows <= 32) {   // the decode kernel's items
+    if (head_dim == 64) return bf16 ? launch_join<64, true, 2>(args, stream) : launch_join<64, false, 2>(args, stream);
+    if (head_dim == 128) return bf16 ? launch_join<128, true, 2>(args, stream) : launch_join<128, false, 2>(args, stream);
+  } else {
+    if (head_dim == 64) return bf16 ? launch_join<64, true, 1>(args, stream) : launch_join<64, false, 1>(args, stream);
+    if (head_dim == 128) return bf16 ? launch_join<128, true, 1>(args, stream) : launch_join<128, false, 1>(args, stream);
+  }
   return cudaErrorInvalidValue;
 }
 

@@ -36,15 +36,20 @@ __device__ __forceinline__ int unit_tiles(const TreeArgs& a, int len, int tl, in
   return max(n, 1);
 }
 
+// Key tiles of an item: what its last unit with rows walks.
 __device__ __forceinline__ int item_tiles(const TreeArgs& a, int len, int tl, int ru) {
-  const int n0 = unit_tiles(a, len, tl, ru, 0);
-  return a.units == 2 ? max(n0, unit_tiles(a, len, tl, ru, 1)) : n0;
+  const int per_item = a.units * a.tile_tokens, i0 = ru * per_item;
+  if (i0 >= tl) return 0;
+  const int fresh = a.has_new == 0 ? 0 : (a.mask == nullptr ? min(tl, i0 + per_item) : tl);
+  return max((len + kTileKeys - 1) / kTileKeys + (fresh + kTileKeys - 1) / kTileKeys, 1);
 }
 
 // Key tiles of all row units of one KV head of a sequence.
 __device__ __forceinline__ int head_tiles(const TreeArgs& a, int len, int tl) {
   int n = 0;
-  for (int ru = 0; ru < a.row_units; ++ru) n += item_tiles(a, len, tl, ru);
+  const int per_item = a.units * a.tile_tokens;
+#pragma unroll 4
+  for (int ru = 0; ru * per_item < tl; ++ru) n += item_tiles(a, len, tl, ru);
   return n;
 }
 
