@@ -7,7 +7,6 @@
 #include <algorithm>
 #include <cmath>
 #include <cstdint>
-#include <cstdlib>
 
 #include "gemm_tn_internal.h"
 #include "kv_cache.h"
@@ -136,10 +135,21 @@ gemm_tn_dev::CacheView view_of(const kv_cache* c, int64_t batch) {
 // Least key tiles per CTA of the attention.
 constexpr int kMinChunk = 2;
 
-// Most key tiles of an item (as far as the host can tell) that is not cut.
-int64_t whole_tiles() {
-  const char* s = std::getenv("WT");
-  return s ? atoi(s) : 8;
+// Whether the attention's items stay whole: each CTA then takes the items that
+// begin in its chunk, with no workspace and no second kernel. Cutting them
+// balances the CTAs to a tile and costs a second segment per CTA, the parts'
+// way through memory and the join: as much as walking 9 more tiles (5 where an
+// item is 256 rows wide). With items no more than SMs the longest item decides,
+// `tiles` against items * tiles / sms; with more, a chunk overruns by half an
+// item on average. Long items are always cut (the host knows what the page
+// table can hold, not how ragged the lengths are). GB300, us a call, one
+// token of 32 heads over 8 KV heads, cut and whole: 1 sequence of 512 slots 17.7
+// and 11.8, of 960 18.4 and 15.1, of 1408 14.9 and 17.9; 16 sequences of 960
+// slots 26.2 and 20.5, of 3008 45.2 and 39.4.
+bool keep_whole(int64_t items, int64_t tiles, int units, int sms) {
+  const int64_t allowance = units == 2 ? 5 : 9;
+  if (tiles > 32) return sms == 1;
+  return items <= sms ? tiles * (sms - items) <= allowance * sms : tiles <= 2 * allowance;
 }
 
 // The kernels count key tiles in 32 bits: an upper bound of their number, from
@@ -188,7 +198,7 @@ int tree_attn_fwd(int dtype, int64_t batch, int64_t tokens, int64_t heads, const
     return invalid("o overlaps an input or the cache");
   alignas(64) gemm_tn_dev::TreeArgs args{};
   args.group = static_cast<int>(heads / kv_heads);
-  const bool decode = tokens * args.group <= decode_attn_rows() && !std::getenv("NODEC");
+  const bool decode = tokens * args.group <= decode_attn_rows();
   args.tile_tokens = decode ? static_cast<int>(tokens) : tree_attn_tile_rows() / args.group;
   const int64_t row_tiles = (tokens + args.tile_tokens - 1) / args.tile_tokens;
   args.units = row_tiles > 1 ? 2 : 1;
@@ -223,15 +233,14 @@ int tree_attn_fwd(int dtype, int64_t batch, int64_t tokens, int64_t heads, const
   args.mask_words = static_cast<int>((tokens + 63) / 64);
   args.has_new = has_new ? 1 : 0;
   args.chunks = sms;
-  args.min_chunk = std::getenv("MC") ? atoi(std::getenv("MC")) : kMinChunk;
+  args.min_chunk = kMinChunk;
   args.scale_log2 = scale_log2(softmax_scale, dim);
   args.status = d_status;
   args.timeout_ns = api_watchdog_ns();
   args.drop_load_block = api_drop_load();
 
-  // items of few tiles are not cut
-  const int64_t item_tiles = (args.capacity + 127) / 128 + (has_new ? (tokens + 127) / 128 : 0);
-  args.whole = item_tiles <= whole_tiles() || sms == 1 ? 1 : 0;
+  const int64_t item_tiles = (static_cast<int64_t>(args.capacity) + 127) / 128 + (has_new ? (tokens + 127) / 128 : 0);
+  args.whole = keep_whole(batch * kv_heads * args.row_units, item_tiles, args.units, sms) ? 1 : 0;
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   auto launch = [&] {
     return decode ? launch_decode_attn(static_cast<int>(dim), bf16, args, s)
