@@ -285,7 +285,7 @@ int kv_cache_append(int dtype, int64_t batch, int64_t tokens, const kv_cache* ca
       for (const void* p : {cache->k, cache->v})
         if (overlap(rows_range(r, batch, tokens, cache->kv_heads, cache->head_dim), pool_range(p, cache)))
           return invalid("k_new or v_new overlaps the cache");
-    if (max_rows > (int64_t{1} << 36) / (batch * cache->kv_heads)) return invalid("batch * max_rows * kv_heads must be at most 2^36");
+    if (max_rows > (int64_t{1} << 34) / (batch * cache->kv_heads)) return invalid("batch * max_rows * kv_heads must be at most 2^34");
   } else if (max_rows > 0) {
     return invalid("max_rows > 0 without tokens");
   }

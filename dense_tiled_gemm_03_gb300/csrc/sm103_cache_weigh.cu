@@ -355,8 +355,10 @@ __global__ void __launch_bounds__(C::kNumThreads, 1) cache_weigh_kernel(const __
           const bool live = key < w.len;
           float acc = 0.0f;
           if (live) acc = block == 0 ? args.weight[weight_row + key] : args.weight_out[weight_row + key];
-          // causal: counted token i is the key's own query or a later one from i = key - (len - n) on
-          const int low = args.causal ? (key - (w.len - w.n) - first_row) * args.group : 0;   // first column that sees the key
+          // causal: counted token i sees the key from i = key - (len - n) on;
+          // low: the first column of this block that does
+          const int first_token = args.causal ? key - (w.len - w.n) - first_row : 0;
+          const int low = first_token > 0 ? min(first_token, args.block_tokens) * args.group : 0;
           const bool masked = __any_sync(0xffffffffu, live && low > 0);
           // two columns an instruction: p = 2^(s c - ref), sum += p factor. The next
           // 32 columns come from tensor memory while these are worked on.

@@ -110,6 +110,50 @@ def test_many_short_sequences_and_one_long():
     ref.check_attention(out, lse, ref.attention(s), s, 7.0)
 
 
+@pytest.mark.parametrize("tokens,group", [(1, 2), (3, 16)])
+def test_more_sequences_than_threads(tokens, group):
+    """The search for a CTA's first tile goes round more than once; some sequences have no work."""
+    lens = [(17 * i) % 150 if i % 5 else 0 for i in range(700)]
+    s = ref.make("bf16", 64, lens, tokens, 1, group, 16, [i % (tokens + 1) for i in range(700)], seed=7)
+    out, lse = run_attn(s)
+    ref.check_attention(out, lse, ref.attention(s), s, 7.0)
+    lse = torch.nan_to_num(lse, nan=5.0) + 1.0
+    counts = [min(n, int(m)) for n, m in zip(lens, s.token_lens)]
+    want, tol = ref.weigh(s, lse, None, counts)
+    cache, status = on_gpu(s)
+    gt.cache_weigh(cache, s.q.to(DEV), lse.to(DEV), counts=torch.tensor(counts, dtype=torch.int32, device=DEV), status=status)
+    assert int(status.item()) == 0
+    live = (torch.arange(want.shape[2])[None, None, :] < s.lens[:, None, None]).expand(want.shape)
+    assert bool(((cache.weight.cpu().double() - want).abs()[live] <= tol[live]).all())
+
+
+@pytest.mark.parametrize("page", [8, 128, 384, 1024])
+def test_page_sizes(page):
+    """Pages longer than a tile, and lengths that end everywhere in them."""
+    s = ref.make("fp16", 128, [page - 1, page + 1, 3 * page - 130 if page > 128 else 77, 900], 6, 1, 3, page, seed=page)
+    for use_new in (True, False):
+        out, lse = run_attn(s, use_new=use_new)
+        ref.check_attention(out, lse, ref.attention(s, use_new=use_new), s, 7.0)
+    check_evict(s, 64, 7, False)
+
+
+def test_a_bad_query_spoils_its_own_row_alone():
+    """NaN and infinite queries of one token beside finite ones, in each kernel's row layout."""
+    for tokens, group in ((4, 2), (9, 8), (70, 4)):
+        s = ref.make("bf16", 64, [300, 40], tokens, 1, group, 16, seed=tokens)
+        want = ref.attention(s)
+        s.q[0, 1, 0] = float("nan")
+        s.q[0, 2, 1] = float("inf")
+        out, lse = run_attn(s)
+        assert torch.isnan(out[0, 1, 0].float()).all() and torch.isnan(lse[0, 1, 0])
+        out[0, 1, 0], lse[0, 1, 0] = 7.0, 7.0
+        out[0, 2, 1], lse[0, 2, 1] = 7.0, 7.0
+        for t in want:
+            t[0, 1, 0] = float("nan")
+            t[0, 2, 1] = float("nan")
+        ref.check_attention(out, lse, want, s, 7.0)
+
+
 def test_long_chunk_over_a_cache():
     """The next tokens of a prompt: several row tiles and key tiles, the causal chain across them."""
     s = ref.make("fp16", 64, [500, 77], 700, 1, 2, 64, [700, 389], seed=5)
@@ -299,6 +343,7 @@ WEIGH = [
     ([513, 900], 70, 1, 7, 128, [70, 33]),       # several blocks of rows
     ([260], 3, 1, 128, 256, None),               # two tokens per block
     ([90, 40], 5, 3, 3, 8, [0, 5]),              # no row counts: the weights come back
+    ([3, 200], 9, 1, 40, 16, [9, 8]),            # more rows than slots; 360 columns in blocks of 240
 ]
 
 
@@ -380,6 +425,31 @@ def check_evict(s, keep, recent, in_place):
         assert ref.same(x[~written], old[~written] if in_place else torch.full_like(old, 3)[~written])
     if not in_place:
         assert ref.same(cache.weight.cpu(), s.weight) and ref.same(cache.pos.cpu(), s.pos)
+
+
+def test_evict_in_place_but_for_the_lengths():
+    """Weights and positions in place with lengths elsewhere (the form that moves its rows in one kernel), and the other way."""
+    s = ref.make("bf16", 64, [300, 90, 130], 1, 2, 1, 16, seed=44)
+    k, v, weight, pos, lens = ref.evict(s, 100, 9)
+    for lens_apart in (True, False):
+        cache, status = on_gpu(s)
+        outs = dict(lens_out=torch.zeros_like(cache.lens)) if lens_apart else \
+            dict(weight_out=torch.zeros_like(cache.weight), pos_out=torch.zeros_like(cache.pos))
+        gt.cache_evict(cache, 100, 9, **outs, status=status)
+        got = dict(weight_out=cache.weight, pos_out=cache.pos, lens_out=cache.lens) | outs
+        assert int(status.item()) == 0 and ref.same(cache.k.cpu(), k) and ref.same(cache.v.cpu(), v)
+        assert torch.equal(got["lens_out"].cpu(), lens)
+        live = (torch.arange(weight.shape[2])[None, None, :] < lens[:, None, None]).expand(weight.shape)
+        assert ref.same(got["weight_out"].cpu()[live], weight[live]) and ref.same(got["pos_out"].cpu()[live], pos[live])
+
+
+def test_evict_more_slots_than_the_newest_leave_room_for():
+    """Positions as an eviction leaves them twice over: more slots count as newest than are kept; the lowest stay."""
+    s = ref.make("bf16", 64, [200], 1, 1, 1, 8, seed=45)
+    s.pos = (s.pos % 40).contiguous()
+    s.seen[:] = 40
+    check_evict(s, 60, 30, False)
+    check_evict(s, 100, 30, True)
 
 
 @pytest.mark.parametrize("keep", [0, 1, 63, 64])
