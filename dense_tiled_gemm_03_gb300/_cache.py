@@ -11,7 +11,7 @@ import ctypes
 import struct
 
 from . import _native
-from ._native import GEMM_TN_BF16, GEMM_TN_F16, GEMM_TN_OK, GemmTnError, library
+from ._native import GEMM_TN_BF16, GEMM_TN_F16, GemmTnError, library
 
 _i64 = ctypes.c_int64
 _int = ctypes.c_int
@@ -46,33 +46,38 @@ _pack_cache = struct.Struct("16q").pack
 _pack_rows = struct.Struct("4q").pack
 
 
-class _Torch:
-    """What the functions below use of torch, looked up once."""
-
-    def __getattr__(self, _):
-        import torch
-        self.int32, self.int64, self.float32 = torch.int32, torch.int64, torch.float32
-        self.codes = {torch.float16: GEMM_TN_F16, torch.bfloat16: GEMM_TN_BF16}
-        self.get_device, self.set_device = torch._C._cuda_getDevice, torch._C._cuda_setDevice
-        self.stream = torch._C._cuda_getCurrentRawStream
-        self.empty, self.zeros = torch.empty, torch.zeros
-        return self.__dict__[_]
+# What the functions below use of torch and of the library, bound when the first
+# cache is made: looking them up costs a fifth of a small call.
+_int32 = _int64 = _float32 = _codes = _get_device = _set_device = _get_stream = None
+_tree_attn_fwd = _kv_cache_append = _kv_cache_weigh = _kv_cache_evict = None
 
 
-_t = _Torch()
+def _bind():
+    global _int32, _int64, _float32, _codes, _get_device, _set_device, _get_stream
+    global _tree_attn_fwd, _kv_cache_append, _kv_cache_weigh, _kv_cache_evict
+    import torch
+    lib = library()
+    _tree_attn_fwd, _kv_cache_append = lib.tree_attn_fwd, lib.kv_cache_append
+    _kv_cache_weigh, _kv_cache_evict = lib.kv_cache_weigh, lib.kv_cache_evict
+    _int64, _float32 = torch.int64, torch.float32
+    _codes = {torch.float16: GEMM_TN_F16, torch.bfloat16: GEMM_TN_BF16}
+    _get_device, _set_device = torch._C._cuda_getDevice, torch._C._cuda_setDevice
+    _get_stream = torch._C._cuda_getCurrentRawStream
+    _int32 = torch.int32
 
 
-def _call(name: str, index: int, *args):
+def _call(fn, name: str, index: int, *args):
     """One call of the library on device `index` and its current stream."""
-    current = _t.get_device()
-    if current != index:
-        _t.set_device(index)
-    try:
-        rc = getattr(_native._lib or library(), name)(*args, _t.stream(index))
-    finally:
-        if current != index:
-            _t.set_device(current)
-    if rc != GEMM_TN_OK:
+    current = _get_device()
+    if current == index:
+        rc = fn(*args, _get_stream(index))
+    else:
+        _set_device(index)
+        try:
+            rc = fn(*args, _get_stream(index))
+        finally:
+            _set_device(current)
+    if rc:
         raise GemmTnError(rc, name)
 
 
@@ -95,13 +100,15 @@ class KVCache:
                  "kv_heads", "head_dim", "_code", "_struct")
 
     def __init__(self, k, v, page_table, lens, weight=None, pos=None, seen=None):
+        if _int32 is None:
+            _bind()
         index = k.get_device()
         if index < 0 or v.get_device() != index or page_table.get_device() != index or lens.get_device() != index:
             raise ValueError("the cache's tensors must be CUDA tensors on one device")
         dtype = k.dtype
         if v.dtype is not dtype:
             raise TypeError("k and v must have the same dtype")
-        code = _t.codes.get(dtype)
+        code = _codes.get(dtype)
         if code is None:
             raise TypeError(f"unsupported dtype {dtype}: expected float16 or bfloat16")
         shape, strides = k.shape, k.stride()
@@ -111,7 +118,7 @@ class KVCache:
         page_stride, slot_stride, head_stride, unit = strides
         if unit != 1:
             raise ValueError("k and v must have unit stride along head_dim")
-        int32 = _t.int32
+        int32 = _int32
         if page_table.dtype is not int32 or lens.dtype is not int32:
             raise TypeError("page_table and lens must be int32")
         if page_table.dim() != 2:
@@ -158,13 +165,13 @@ def _ints(t, cache: KVCache, what: str, shape):
     """Device pointer of a contiguous int32 tensor of that shape, or None."""
     if t is None:
         return None
-    if t.get_device() != cache.index or t.dtype is not _t.int32 or t.shape != shape or not t.is_contiguous():
+    if t.get_device() != cache.index or t.dtype is not _int32 or t.shape != shape or not t.is_contiguous():
         raise ValueError(f"{what} must be a contiguous int32 {tuple(shape)} tensor on the cache's device")
     return t.data_ptr()
 
 
 def _floats(t, cache: KVCache, what: str, shape):
-    if t.get_device() != cache.index or t.dtype is not _t.float32 or t.shape != shape or not t.is_contiguous():
+    if t.get_device() != cache.index or t.dtype is not _float32 or t.shape != shape or not t.is_contiguous():
         raise ValueError(f"{what} must be a contiguous float32 {tuple(shape)} tensor on the cache's device")
     return t.data_ptr()
 
@@ -173,7 +180,7 @@ def _status(t, cache: KVCache):
     """Device pointer of the optional status word."""
     if t is None:
         return None
-    if t.get_device() != cache.index or t.dtype is not _t.int32 or t.numel() < 1 or not t.is_contiguous():
+    if t.get_device() != cache.index or t.dtype is not _int32 or t.numel() < 1 or not t.is_contiguous():
         raise ValueError("status must be a contiguous int32 tensor of at least one element on the cache's device")
     return t.data_ptr()
 
@@ -211,15 +218,15 @@ def tree_attn(q, cache: KVCache, k_new=None, v_new=None, mask=None, token_lens=N
     elif v_new is not None:
         raise ValueError("k_new and v_new come together")
     if mask is not None:
-        if mask.get_device() != cache.index or mask.dtype is not _t.int64 or \
+        if mask.get_device() != cache.index or mask.dtype is not _int64 or \
                 mask.shape != (batch, tokens, (tokens + 63) // 64) or not mask.is_contiguous():
             raise ValueError("mask must be a contiguous int64 [batch, tokens, ceil(tokens / 64)] tensor on the cache's device")
         d_mask = mask.data_ptr()
     if out is None:
-        out = (_t.empty if token_lens is None else _t.zeros)(shape, dtype=cache.dtype, device=q.device)
+        out = q.new_empty(shape) if token_lens is None else q.new_zeros(shape)
     elif out.shape != shape or out.dtype is not cache.dtype or out.get_device() != cache.index or not out.is_contiguous():
         raise ValueError("out must be a contiguous tensor with q's shape, dtype and device")
-    _call("tree_attn_fwd", cache.index, cache._code, batch, tokens, heads, cache._struct, rq, rk, rv, d_mask,
+    _call(_tree_attn_fwd, "tree_attn_fwd", cache.index, cache._code, batch, tokens, heads, cache._struct, rq, rk, rv, d_mask,
           _ints(token_lens, cache, "token_lens", (batch,)), out.data_ptr(),
           None if lse is None else _floats(lse, cache, "lse", (batch, tokens, heads)), 0.0 if scale is None else float(scale),
           _status(status, cache))
@@ -252,7 +259,7 @@ def cache_append(cache: KVCache, k_new, v_new, counts=None, rows=None, lens_out=
     if seen_out is not None and cache.seen is None:
         raise ValueError("seen_out needs a cache with seen")
     d_rows, d_counts, max_rows = _counted(cache, rows, counts, batch, tokens)
-    _call("kv_cache_append", cache.index, cache._code, batch, tokens, cache._struct, _rows(k_new, cache, "k_new", shape),
+    _call(_kv_cache_append, "kv_cache_append", cache.index, cache._code, batch, tokens, cache._struct, _rows(k_new, cache, "k_new", shape),
           _rows(v_new, cache, "v_new", shape), d_rows, d_counts, max_rows,
           _ints(cache.lens if lens_out is None else lens_out, cache, "lens_out", (batch,)),
           _ints(cache.seen if seen_out is None else seen_out, cache, "seen_out", (batch,)), _status(status, cache))
@@ -273,7 +280,7 @@ def cache_weigh(cache: KVCache, q, lse, counts=None, rows=None, causal=True, sca
     if out is None:
         out = cache.weight
     d_rows, d_counts, max_rows = _counted(cache, rows, counts, batch, tokens)
-    _call("kv_cache_weigh", cache.index, cache._code, batch, tokens, heads, cache._struct, rq,
+    _call(_kv_cache_weigh, "kv_cache_weigh", cache.index, cache._code, batch, tokens, heads, cache._struct, rq,
           _floats(lse, cache, "lse", (batch, tokens, heads)), d_rows, d_counts, max_rows, 1 if causal else 0,
           0.0 if scale is None else float(scale), _floats(out, cache, "out", (batch, cache.kv_heads, cache.capacity)),
           _status(status, cache))
@@ -291,7 +298,7 @@ def cache_evict(cache: KVCache, keep: int, recent: int = 0, weight_out=None, pos
         raise ValueError("pos_out needs a cache with pos")
     batch = cache.batch
     shape = (batch, cache.kv_heads, cache.capacity)
-    _call("kv_cache_evict", cache.index, cache._code, batch, cache._struct, int(keep), int(recent),
+    _call(_kv_cache_evict, "kv_cache_evict", cache.index, cache._code, batch, cache._struct, int(keep), int(recent),
           _floats(cache.weight if weight_out is None else weight_out, cache, "weight_out", shape),
           _ints(cache.pos if pos_out is None else pos_out, cache, "pos_out", shape),
           _ints(cache.lens if lens_out is None else lens_out, cache, "lens_out", (batch,)), _status(status, cache))
