@@ -175,7 +175,7 @@ __global__ void __launch_bounds__(C::kNumThreads, 1) cache_weigh_kernel(const __
   cache::find_start(
       args.batch, args.chunks, args.min_chunk, static_cast<int>(blockIdx.x), sums,
       [&](int b) { return (cw::cached_len(args, b) + cw::kTileKeys - 1) / cw::kTileKeys * args.kv_heads; },
-      [&](int b, int off, int left, int) {
+      [&](int b, int, int off, int left, int) {
         cw::Walk w;
         w.start(args, b, off, left);
         *start_walk = w;
@@ -184,13 +184,12 @@ __global__ void __launch_bounds__(C::kNumThreads, 1) cache_weigh_kernel(const __
   __syncthreads();
   tc_fence_after_sync();
   const uint32_t tmem_base = *tmem_slot;
-  const cache::Watch wd{args.status, args.timeout_ns, abort_flag};
+  const cache::Watch<false> wd{args.status, args.timeout_ns, abort_flag};
   cw::Walk w = *start_walk;
 
   if (warp == cw::kProducerWarp) {
     // -------------------------------------------------------------- TMA producer
-    int issued[C::kStages];
-    for (int s = 0; s < C::kStages; ++s) issued[s] = -1;
+    cache::Issued issued;
     const int box_rows = min(args.page_size, cw::kTileKeys);
     const int tile_pages = cw::kTileKeys / box_rows;
     int it = 0;
@@ -225,14 +224,13 @@ __global__ void __launch_bounds__(C::kNumThreads, 1) cache_weigh_kernel(const __
               tma_load_4d(&args.tmap_k, k_tile(s) + c * C::kBoxBytes + lane * box_rows * 128u, k_full(s), 64 * c, w.h,
                           slot0, page);
           }
-          issued[s] = static_cast<int>(ph);
+          issued.note(s, ph);
           page = next_page;
         }
       }
     }
     // wait (bounded) for every copy issued before the CTA may exit
-    for (int s = 0; s < C::kStages; ++s)
-      if (issued[s] >= 0) wd.drain(k_full(s), static_cast<uint32_t>(issued[s]));
+    issued.drain(wd, C::kStages, k_full);
   } else if (warp == cw::kMmaWarp) {
     {
       // ------------------------------------------------------------ MMA issuer

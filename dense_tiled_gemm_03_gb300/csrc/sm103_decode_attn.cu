@@ -213,16 +213,14 @@ __global__ void __launch_bounds__(C::kNumThreads, 1) decode_attn_kernel(const __
   __syncthreads();
   tc_fence_after_sync();
   const uint32_t tmem_base = *tmem_slot;
-  const cache::Watch wd{args.status, args.timeout_ns, abort_flag};
+  const cache::Watch<false> wd{args.status, args.timeout_ns, abort_flag};
   const bool has_new = args.has_new != 0;
   ta::Walk w = *start_walk;
   if (threadIdx.x == 0) ta::note_no_cut(args, w);
 
   if (warp == da::kProducerWarp) {
     // -------------------------------------------------------------- TMA producer
-    int issued_k[C::kStages], issued_v[C::kStages], issued_q[2] = {-1, -1};
-#pragma unroll
-    for (int s = 0; s < C::kStages; ++s) issued_k[s] = issued_v[s] = -1;
+    cache::Issued issued_q, issued_k, issued_v;
     const int box_rows = min(args.page_size, da::kTileKeys);
     const int tile_pages = da::kTileKeys / box_rows;   // pages (or parts of one) per tile
     const uint32_t q_bytes = static_cast<uint32_t>(args.tokens * args.group) * 128u * C::kDimBoxes;
@@ -244,7 +242,7 @@ __global__ void __launch_bounds__(C::kNumThreads, 1) decode_attn_kernel(const __
         for (int c = 0; c < C::kDimBoxes; ++c)
           tma_load_4d(&args.tmap_q, q_slot(slot) + c * C::kQBoxBytes, q_full(slot), 64 * c, w.h * args.group, 0, w.b);
       }
-      issued_q[slot] = static_cast<int>(q_ph);
+      issued_q.note(slot, q_ph);
       for (int j = w.j0; j < w.j0 + w.count; ++j, ++it) {
         const ta::Tile t = ta::tile_of(w.len, w.tl, has_new, j);
         const int boxes = t.fresh ? (t.valid > 0 ? 1 : 0) : (t.valid + box_rows - 1) / box_rows;
@@ -260,9 +258,7 @@ __global__ void __launch_bounds__(C::kNumThreads, 1) decode_attn_kernel(const __
             tma_load_4d(t.fresh ? &args.tmap_k_new : &args.tmap_k, k_tile(s) + c * C::kBoxBytes + lane * box_rows * 128u,
                         k_full(s), 64 * c, w.h, slot0, t.fresh ? w.b : page);
         }
-#pragma unroll
-        for (int x = 0; x < C::kStages; ++x)
-          if (x == s) issued_k[x] = static_cast<int>(ph);
+        issued_k.note(s, ph);
         if (!(ok = wd.warp_wait(v_empty(s), ph ^ 1u))) break;
         if (lane == 0) mbar_arrive_expect_tx(v_full(s), bytes);
         __syncwarp();
@@ -271,9 +267,7 @@ __global__ void __launch_bounds__(C::kNumThreads, 1) decode_attn_kernel(const __
             tma_load_4d(t.fresh ? &args.tmap_v_new : &args.tmap_v, v_tile(s) + c * C::kBoxBytes + lane * box_rows * 128u,
                         v_full(s), 64 * c, w.h, slot0, t.fresh ? w.b : page);
         }
-#pragma unroll
-        for (int x = 0; x < C::kStages; ++x)
-          if (x == s) issued_v[x] = static_cast<int>(ph);
+        issued_v.note(s, ph);
         if (j + 1 < w.j0 + w.count) page = page_of(j + 1);
         if (++s == C::kStages) {
           s = 0;
@@ -283,13 +277,9 @@ __global__ void __launch_bounds__(C::kNumThreads, 1) decode_attn_kernel(const __
     }
     // Loads may still be landing if another role gave up: wait (bounded) for
     // every phase issued before the CTA may exit.
-    for (int x = 0; x < 2; ++x)
-      if (issued_q[x] >= 0) wd.drain(q_full(x), static_cast<uint32_t>(issued_q[x]));
-#pragma unroll
-    for (int x = 0; x < C::kStages; ++x) {
-      if (issued_k[x] >= 0) wd.drain(k_full(x), static_cast<uint32_t>(issued_k[x]));
-      if (issued_v[x] >= 0) wd.drain(v_full(x), static_cast<uint32_t>(issued_v[x]));
-    }
+    issued_q.drain(wd, 2, q_full);
+    issued_k.drain(wd, C::kStages, k_full);
+    issued_v.drain(wd, C::kStages, v_full);
   } else if (warp == da::kMmaWarp) {
     {
       // ------------------------------------------------------------ MMA issuer
@@ -549,21 +539,21 @@ __global__ void __launch_bounds__(C::kNumThreads, 1) decode_attn_kernel(const __
           uint16_t* out = static_cast<uint16_t*>(args.o) +
                           (static_cast<int64_t>(w.b) * args.tokens * args.heads + w.h * args.group) * C::kDim + key;
           float* part = args.part_o + (static_cast<int64_t>(slot) * (C::kDim / 4) + key / 4) * args.part_rows * 4 + key % 4;
-          int token = 0, head = 0;   // of row r
+          const int next_token = (args.heads - args.group) * C::kDim;   // from a token's last row to the next one's first
+          int head = 0;
 #pragma unroll
           for (int r = 0; r < C::kRows; ++r) {
             const float a0 = __shfl_sync(0xffffffffu, f0, r), a1 = __shfl_sync(0xffffffffu, f1, r);
-            if (r < rows) {
-              float v = a0 == 0.0f ? 0.0f : o0[r] * a0;
-              if (both && a1 != 0.0f) v += o1[r] * a1;
-              if (column) {
-                if (whole) out[(static_cast<int64_t>(token) * args.heads + head) * C::kDim] = static_cast<uint16_t>(cache::pack2<C::kBf16>(v, 0.0f));
-                else part[4 * r] = v;
-              }
-              if (++head == args.group) {
-                head = 0;
-                ++token;
-              }
+            float v = a0 == 0.0f ? 0.0f : o0[r] * a0;
+            if (both && a1 != 0.0f) v += o1[r] * a1;
+            if (column && r < rows) {
+              if (whole) *out = static_cast<uint16_t>(cache::pack2<C::kBf16>(v, 0.0f));
+              else part[4 * r] = v;
+            }
+            out += C::kDim;
+            if (++head == args.group) {
+              head = 0;
+              out += next_token;
             }
           }
           tc_fence_before_sync();

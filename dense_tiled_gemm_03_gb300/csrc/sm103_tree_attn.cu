@@ -167,7 +167,7 @@ __global__ void __launch_bounds__(C::kNumThreads) __maxnreg__(C::kMaxRegs)
   __syncthreads();
   tc_fence_after_sync();
   const uint32_t tmem_base = *tmem_slot;
-  const cache::Watch wd{args.status, args.timeout_ns, abort_flag};
+  const cache::Watch<true> wd{args.status, args.timeout_ns, abort_flag};
   const bool parity_mode = args.units == 1;
   const bool has_new = args.has_new != 0;
   ta::Walk w = *start_walk;
@@ -175,9 +175,7 @@ __global__ void __launch_bounds__(C::kNumThreads) __maxnreg__(C::kMaxRegs)
 
   if (warp == ta::kProducerWarp) {
     // -------------------------------------------------------------- TMA producer
-    int issued_k[C::kKStages], issued_v[C::kVStages], issued_q[2] = {-1, -1};
-    for (int s = 0; s < C::kKStages; ++s) issued_k[s] = -1;
-    for (int s = 0; s < C::kVStages; ++s) issued_v[s] = -1;
+    cache::Issued issued_q, issued_k, issued_v;
     const int box_rows = min(args.page_size, ta::kTileKeys);
     const int tile_pages = ta::kTileKeys / box_rows;   // pages (or parts of one) per tile
     const uint32_t q_bytes = static_cast<uint32_t>(args.tile_tokens * args.group) * 128u * C::kDimBoxes;
@@ -209,7 +207,7 @@ __global__ void __launch_bounds__(C::kNumThreads) __maxnreg__(C::kMaxRegs)
             tma_load_4d(t.fresh ? &args.tmap_k_new : &args.tmap_k, k_tile(s) + c * C::kBoxBytes + lane * box_rows * 128u,
                         k_full(s), 64 * c, w.h, slot0, t.fresh ? w.b : page);
         }
-        issued_k[s] = static_cast<int>(ph);
+        issued_k.note(s, ph);
         if (j == w.j0) {
           // the segment's queries, behind its first keys: their slots are free
           // only once the segment before has multiplied its last keys
@@ -223,7 +221,7 @@ __global__ void __launch_bounds__(C::kNumThreads) __maxnreg__(C::kMaxRegs)
                 tma_load_4d(&args.tmap_q, q_tile(slot) + c * C::kBoxBytes, q_full(slot), 64 * c, w.h * args.group,
                             (w.ru * args.units + u) * args.tile_tokens, w.b);
             }
-            if (ok) issued_q[slot] = static_cast<int>(q_ph);
+            if (ok) issued_q.note(slot, q_ph);
           }
           if (!ok) break;
         }
@@ -237,18 +235,15 @@ __global__ void __launch_bounds__(C::kNumThreads) __maxnreg__(C::kMaxRegs)
             tma_load_4d(t.fresh ? &args.tmap_v_new : &args.tmap_v, v_tile(sv) + c * C::kBoxBytes + lane * box_rows * 128u,
                         v_full(sv), 64 * c, w.h, slot0, t.fresh ? w.b : page);
         }
-        issued_v[sv] = static_cast<int>(phv);
+        issued_v.note(sv, phv);
         page = next_page;
       }
     }
     // Loads may still be landing if another role gave up: wait (bounded) for
     // every phase issued before the CTA may exit.
-    for (int s = 0; s < 2; ++s)
-      if (issued_q[s] >= 0) wd.drain(q_full(s), static_cast<uint32_t>(issued_q[s]));
-    for (int s = 0; s < C::kKStages; ++s)
-      if (issued_k[s] >= 0) wd.drain(k_full(s), static_cast<uint32_t>(issued_k[s]));
-    for (int s = 0; s < C::kVStages; ++s)
-      if (issued_v[s] >= 0) wd.drain(v_full(s), static_cast<uint32_t>(issued_v[s]));
+    issued_q.drain(wd, 2, q_full);
+    issued_k.drain(wd, C::kKStages, k_full);
+    issued_v.drain(wd, C::kVStages, v_full);
   } else if (warp == ta::kMmaWarp) {
     {
       // ------------------------------------------------------------ MMA issuer

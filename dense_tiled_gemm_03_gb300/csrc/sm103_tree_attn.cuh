@@ -48,7 +48,7 @@ __device__ __forceinline__ int item_tiles(const TreeArgs& a, int len, int tl, in
 __device__ __forceinline__ int head_tiles(const TreeArgs& a, int len, int tl) {
   int n = 0;
   const int per_item = a.units * a.tile_tokens;
-#pragma unroll 4
+#pragma unroll 1
   for (int ru = 0; ru * per_item < tl; ++ru) n += item_tiles(a, len, tl, ru);
   return n;
 }
@@ -61,14 +61,15 @@ struct Walk {
   int left;              // tiles of the chunk from this segment on
   int count;             // tiles of the segment
 
-  // The walk that begins at tile `off` of sequence b.
-  __device__ __forceinline__ void start(const TreeArgs& a, int b_, int off, int left_) {
+  // The walk that begins at tile `off` of the `all` tiles of sequence b.
+  __device__ __forceinline__ void start(const TreeArgs& a, int b_, int all, int off, int left_) {
     b = b_;
     len = cached_len(a, b);
     tl = new_len(a, b);
-    const int per_head = head_tiles(a, len, tl);
+    const int per_head = all / a.kv_heads;
     h = off / per_head;
     j0 = off - per_head * h;
+#pragma unroll 1
     for (ru = 0; (tiles = item_tiles(a, len, tl, ru)) <= j0; ++ru) j0 -= tiles;
     left = left_;
     count = tiles - j0;
@@ -128,9 +129,9 @@ __device__ __forceinline__ void find_walk(const TreeArgs& a, Walk* start, int* s
   cache::find_start(
       a.batch, a.chunks, a.min_chunk, static_cast<int>(blockIdx.x), sums,
       [&](int b) { return head_tiles(a, cached_len(a, b), new_len(a, b)) * a.kv_heads; },
-      [&](int b, int off, int left, int chunk_tiles) {
+      [&](int b, int all, int off, int left, int chunk_tiles) {
         Walk w;
-        w.start(a, b, off, left);
+        w.start(a, b, all, off, left);
         *start = w;
         if (w.j0 > 0 && w.more()) {
           int4* to = reinterpret_cast<int4*>(a.cuts) + 2 * blockIdx.x;
