@@ -393,20 +393,22 @@ __global__ void __launch_bounds__(C::kNumThreads, 1) decode_attn_kernel(const __
           seen = 0;
           for (int r = 0; r < rows; ++r) seen |= ((tokens >> (r / args.group)) & 1u) << r;
         }
-        if (t.fresh || t.valid < da::kTileKeys) {
+        const bool partial = t.fresh || t.valid < da::kTileKeys;
+        auto hide = [&]() {   // scores that their rows do not see
 #pragma unroll
           for (int r = 0; r < C::kRows; ++r)
             if (!((seen >> r) & 1u)) s[r] = -INFINITY;
-        }
-        float p[C::kRows];
+        };
+        if (partial) hide();
         bool over = unset != 0;
         if (!over) {
-          // against the references at once; a probability past 2^8 calls for new ones
+          // probabilities, in the scores' registers, against the references at
+          // once; one past 2^8 calls for new references
           bool mine = false;
 #pragma unroll
           for (int r = 0; r < C::kRows; ++r) {
-            p[r] = ex2_approx(fmaf(s[r], c_log2, neg_m[r]));
-            mine |= !(p[r] <= 256.0f) && ((row_bits >> r) & 1u);
+            s[r] = ex2_approx(fmaf(s[r], c_log2, neg_m[r]));
+            mine |= !(s[r] <= 256.0f) && ((row_bits >> r) & 1u);
           }
           // three words in turn: the next one is cleared before this meeting,
           // after the meeting in which its last vote was read
@@ -416,6 +418,10 @@ __global__ void __launch_bounds__(C::kNumThreads, 1) decode_attn_kernel(const __
           if (!(ok = meet())) break;
           over = votes[word] != 0u;
           ++voted;
+          if (over) {   // the scores are still in tensor memory
+            da::tmem_load_rows<C::kRows>(t_s, s);
+            if (partial) hide();
+          }
         }
         if (over) {
           // the tile's row maxima over the unit's 128 keys
@@ -443,14 +449,17 @@ __global__ void __launch_bounds__(C::kNumThreads, 1) decode_attn_kernel(const __
               l[r] *= alpha[r];
               moved = true;
             }
-            p[r] = ex2_approx(fmaf(s[r], c_log2, neg_m[r]));
+            s[r] = ex2_approx(fmaf(s[r], c_log2, neg_m[r]));
           }
           if (moved) {   // the same in every thread of the unit
-            float o[C::kRows];
-            da::tmem_load_rows<C::kRows>(t_o, o);
 #pragma unroll
-            for (int r = 0; r < C::kRows; ++r) o[r] *= alpha[r];
-            da::tmem_store_rows<C::kRows>(t_o, o);
+            for (int c = 0; c < C::kRows; c += 16) {
+              float o[16];
+              da::tmem_load_rows<16>(t_o + static_cast<uint32_t>(c), o);
+#pragma unroll
+              for (int r = 0; r < 16; ++r) o[r] *= alpha[c + r];
+              da::tmem_store_rows<16>(t_o + static_cast<uint32_t>(c), o);
+            }
             tmem_store_wait();
           }
           // the maxima are not written again before every warp has read them
@@ -461,8 +470,8 @@ __global__ void __launch_bounds__(C::kNumThreads, 1) decode_attn_kernel(const __
         const uint32_t piece = static_cast<uint32_t>(key & 63) >> 3;
 #pragma unroll
         for (int r = 0; r < C::kRows; ++r) {
-          l[r] += p[r];
-          st_shared_u16(p_at + 128u * r + 16u * (piece ^ (r & 7u)), static_cast<uint16_t>(cache::pack2<C::kBf16>(p[r], 0.0f)));
+          l[r] += s[r];
+          st_shared_u16(p_at + 128u * r + 16u * (piece ^ (r & 7u)), static_cast<uint16_t>(cache::pack2<C::kBf16>(s[r], 0.0f)));
         }
         if (t.valid % 16 != 0) {
           // zero the rows of V behind the last key, up to the end of its 16-key step
