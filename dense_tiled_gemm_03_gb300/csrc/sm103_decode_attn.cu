@@ -82,28 +82,21 @@ struct Cfg {
   static_assert(kOffBar % 8u == 0, "64-bit shared words");
 };
 
-// The largest value of x over the warp (NaN is passed over).
-__device__ __forceinline__ float warp_max(float x) {
-  float y;
-  asm("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(y) : "f"(x));
-  return y;
-}
-
-// Sums kRows values over the 32 lanes: lane r (and r + 16 with 16 rows) gets row
-// r's. Halves the rows at every exchange.
-template <int kRows>
-__device__ __forceinline__ float warp_row_sums(float (&l)[kRows], uint32_t lane) {
+// Reduces kRows values over the 32 lanes: lane r (and r + 16 with 16 rows) gets
+// row r's. Halves the rows at every exchange: 31 shuffles for 32 rows.
+template <int kRows, class Op>
+__device__ __forceinline__ float warp_rows(float (&x)[kRows], uint32_t lane, Op op) {
 #pragma unroll
   for (int half = kRows / 2; half >= 1; half /= 2) {
     const bool upper = (lane & static_cast<uint32_t>(half)) != 0;
 #pragma unroll
     for (int i = 0; i < half; ++i) {
-      const float keep = upper ? l[i + half] : l[i], give = upper ? l[i] : l[i + half];
-      l[i] = keep + __shfl_xor_sync(0xffffffffu, give, half);
+      const float keep = upper ? x[i + half] : x[i], give = upper ? x[i] : x[i + half];
+      x[i] = op(keep, __shfl_xor_sync(0xffffffffu, give, half));
     }
   }
-  if constexpr (kRows == 16) l[0] += __shfl_xor_sync(0xffffffffu, l[0], 16);
-  return l[0];
+  if constexpr (kRows == 16) x[0] = op(x[0], __shfl_xor_sync(0xffffffffu, x[0], 16));
+  return x[0];
 }
 
 template <int kRows>
@@ -381,17 +374,18 @@ __global__ void __launch_bounds__(C::kNumThreads, 1) decode_attn_kernel(const __
         float s[C::kRows];
         da::tmem_load_rows<C::kRows>(t_s, s);
         uint32_t seen = key < t.valid ? 0xffffffffu : 0u;   // rows that see this thread's key
-        if (t.fresh && key < t.valid) {
-          // bit r / group of the word: whether that token sees this key
-          uint32_t tokens = 0;
-          if (args.mask == nullptr) {
-            tokens = ~cache::low_bits(key);
-          } else {
-            const uint64_t* words = args.mask + static_cast<int64_t>(w.b) * args.tokens;   // at most 32 tokens: one word each
-            for (int x = 0; x < w.tl; ++x) tokens |= static_cast<uint32_t>((__ldg(words + x) >> key) & 1ull) << x;
+        if (t.fresh) {
+          // new token x's rows are bits x * group .. of the word; x sees this key or does not
+          const uint64_t* words = args.mask + static_cast<int64_t>(w.b) * args.tokens;   // at most 32 tokens: one word each
+          uint32_t word = cache::low_bits(static_cast<int>(lane) + 1);   // lane x: the keys that token x sees
+          if (args.mask != nullptr) word = static_cast<int>(lane) < w.tl ? static_cast<uint32_t>(__ldg(words + lane)) : 0u;
+          const uint32_t token_rows = cache::low_bits(args.group);
+          uint32_t rows_seen = 0;
+          for (int x = 0; x < w.tl; ++x) {
+            const uint32_t sees = __shfl_sync(0xffffffffu, word, x);
+            if ((sees >> (key & 31)) & 1u) rows_seen |= token_rows << (x * args.group);
           }
-          seen = 0;
-          for (int r = 0; r < rows; ++r) seen |= ((tokens >> (r / args.group)) & 1u) << r;
+          if (key < t.valid) seen = rows_seen;
         }
         const bool partial = t.fresh || t.valid < da::kTileKeys;
         auto hide = [&]() {   // scores that their rows do not see
@@ -403,13 +397,15 @@ __global__ void __launch_bounds__(C::kNumThreads, 1) decode_attn_kernel(const __
         bool over = unset != 0;
         if (!over) {
           // probabilities, in the scores' registers, against the references at
-          // once; one past 2^8 calls for new references
-          bool mine = false;
+          // once; one past 2^8 calls for new references (a NaN does not: its
+          // row is lost either way)
+          float most = 0.0f;
 #pragma unroll
           for (int r = 0; r < C::kRows; ++r) {
             s[r] = ex2_approx(fmaf(s[r], c_log2, neg_m[r]));
-            mine |= !(s[r] <= 256.0f) && ((row_bits >> r) & 1u);
+            most = fmaxf(most, s[r]);
           }
+          const bool mine = most > 256.0f;
           // three words in turn: the next one is cleared before this meeting,
           // after the meeting in which its last vote was read
           const uint32_t word = voted % 3u;
@@ -424,40 +420,43 @@ __global__ void __launch_bounds__(C::kNumThreads, 1) decode_attn_kernel(const __
           }
         }
         if (over) {
-          // the tile's row maxima over the unit's 128 keys
+          // the tile's row maxima over the unit's 128 keys: over the warp, then
+          // over the four warps; from there on lane r decides for row r
+          float x[C::kRows];
 #pragma unroll
-          for (int r = 0; r < C::kRows; ++r) {
-            const float mx = da::warp_max(s[r]);
-            if (lane == static_cast<uint32_t>(r)) my_maxima[r] = mx;
-          }
+          for (int r = 0; r < C::kRows; ++r) x[r] = s[r];
+          const float warp_max = da::warp_rows<C::kRows>(x, lane, [](float p, float q) { return fmaxf(p, q); });
+          if (lane < C::kRows) my_maxima[lane] = warp_max;
           if (!(ok = meet())) break;
-          float alpha[C::kRows];
-          bool moved = false;
+          const uint32_t row = lane % C::kRows;
+          const float* all = warp_maxima + u * 128 + row;
+          const float mx = fmaxf(fmaxf(all[0], all[32]), fmaxf(all[64], all[96])) * c_log2;
+          float neg = 0.0f, alpha = 1.0f;   // the row's reference so far, and O's and l's factor
+#pragma unroll
+          for (int r = 0; r < C::kRows; ++r)
+            if (row == static_cast<uint32_t>(r)) neg = neg_m[r];
+          const bool fresh_row = ((unset >> row) & 1u) != 0u && mx != -INFINITY;
+          const bool move = ((row_bits & ~unset) >> row & 1u) != 0u && mx > 8.0f - neg;
+          if (move) alpha = ex2_approx(-neg - mx);
+          if (fresh_row || move) neg = -mx;
+          unset &= ~(__ballot_sync(0xffffffffu, fresh_row) & cache::low_bits(C::kRows));
+          const bool moved = __any_sync(0xffffffffu, move);   // the same in every warp of the unit
 #pragma unroll
           for (int r = 0; r < C::kRows; ++r) {
-            const float* x = warp_maxima + u * 128 + r;
-            const float mx = fmaxf(fmaxf(x[0], x[32]), fmaxf(x[64], x[96])) * c_log2;
-            alpha[r] = 1.0f;
-            if ((unset >> r) & 1u) {
-              if (mx != -INFINITY) {
-                neg_m[r] = -mx;
-                unset &= ~(1u << r);
-              }
-            } else if (mx > 8.0f - neg_m[r] && ((row_bits >> r) & 1u)) {
-              alpha[r] = ex2_approx(-neg_m[r] - mx);
-              neg_m[r] = -mx;
-              l[r] *= alpha[r];
-              moved = true;
-            }
+            neg_m[r] = __shfl_sync(0xffffffffu, neg, r);
             s[r] = ex2_approx(fmaf(s[r], c_log2, neg_m[r]));
           }
-          if (moved) {   // the same in every thread of the unit
+          if (moved) {
 #pragma unroll
             for (int c = 0; c < C::kRows; c += 16) {
               float o[16];
               da::tmem_load_rows<16>(t_o + static_cast<uint32_t>(c), o);
 #pragma unroll
-              for (int r = 0; r < 16; ++r) o[r] *= alpha[c + r];
+              for (int r = 0; r < 16; ++r) {
+                const float f = __shfl_sync(0xffffffffu, alpha, c + r);
+                o[r] *= f;
+                l[c + r] *= f;
+              }
               da::tmem_store_rows<16>(t_o + static_cast<uint32_t>(c), o);
             }
             tmem_store_wait();
@@ -491,7 +490,7 @@ __global__ void __launch_bounds__(C::kNumThreads, 1) decode_attn_kernel(const __
       // ---------------------------------------------------------- end of a segment
       // references and sums to shared memory; unit 0 joins the two units' rows
       {
-        const float sum = da::warp_row_sums<C::kRows>(l, lane);
+        const float sum = da::warp_rows<C::kRows>(l, lane, [](float p, float q) { return p + q; });
         if (lane < C::kRows) warp_sums[(u * 4 + static_cast<int>(quarter)) * 32 + static_cast<int>(lane)] = sum;
         if (quarter == 0) {
 #pragma unroll
@@ -551,18 +550,22 @@ __global__ void __launch_bounds__(C::kNumThreads, 1) decode_attn_kernel(const __
           const int next_token = (args.heads - args.group) * C::kDim;   // from a token's last row to the next one's first
           int head = 0;
 #pragma unroll
-          for (int r = 0; r < C::kRows; ++r) {
-            const float a0 = __shfl_sync(0xffffffffu, f0, r), a1 = __shfl_sync(0xffffffffu, f1, r);
-            float v = a0 == 0.0f ? 0.0f : o0[r] * a0;
-            if (both && a1 != 0.0f) v += o1[r] * a1;
-            if (column && r < rows) {
-              if (whole) *out = static_cast<uint16_t>(cache::pack2<C::kBf16>(v, 0.0f));
-              else part[4 * r] = v;
-            }
-            out += C::kDim;
-            if (++head == args.group) {
-              head = 0;
-              out += next_token;
+          for (int r0 = 0; r0 < C::kRows; r0 += 8) {
+            if (r0 >= rows) break;
+#pragma unroll
+            for (int r = r0; r < r0 + 8; ++r) {
+              const float a0 = __shfl_sync(0xffffffffu, f0, r), a1 = __shfl_sync(0xffffffffu, f1, r);
+              float v = a0 == 0.0f ? 0.0f : o0[r] * a0;
+              if (both && a1 != 0.0f) v += o1[r] * a1;
+              if (column && r < rows) {
+                if (whole) *out = static_cast<uint16_t>(cache::pack2<C::kBf16>(v, 0.0f));
+                else part[4 * r] = v;
+              }
+              out += C::kDim;
+              if (++head == args.group) {
+                head = 0;
+                out += next_token;
+              }
             }
           }
           tc_fence_before_sync();
