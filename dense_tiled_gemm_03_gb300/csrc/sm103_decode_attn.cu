@@ -540,23 +540,24 @@ __global__ void __launch_bounds__(C::kNumThreads, 1) decode_attn_kernel(const __
               args.part_ml[static_cast<int64_t>(slot) * args.part_rows + lane] = make_float2(sum_all == 0.0f ? 0.0f : m, sum_all);
             }
           }
-          float o0[C::kRows], o1[C::kRows];
-          da::tmem_load_rows<C::kRows>(t_o, o0);
-          if (both) da::tmem_load_rows<C::kRows>(t_o + static_cast<uint32_t>(C::kRows), o1);
           const bool column = key < C::kDim;   // this lane holds a column of O
           uint16_t* out = static_cast<uint16_t*>(args.o) +
                           (static_cast<int64_t>(w.b) * args.tokens * args.heads + w.h * args.group) * C::kDim + key;
           float* part = args.part_o + (static_cast<int64_t>(slot) * (C::kDim / 4) + key / 4) * args.part_rows * 4 + key % 4;
           const int next_token = (args.heads - args.group) * C::kDim;   // from a token's last row to the next one's first
           int head = 0;
+#pragma unroll 1   // once per segment: a loop's instructions are fetched once
+          for (int r0 = 0; r0 < rows; r0 += 8) {
+            uint32_t o0[8], o1[8];
+            tmem_load_32x8(t_o + static_cast<uint32_t>(r0), o0);
+            if (both) tmem_load_32x8(t_o + static_cast<uint32_t>(C::kRows + r0), o1);
+            tmem_load_wait();
 #pragma unroll
-          for (int r0 = 0; r0 < C::kRows; r0 += 8) {
-            if (r0 >= rows) break;
-#pragma unroll
-            for (int r = r0; r < r0 + 8; ++r) {
+            for (int i = 0; i < 8; ++i) {
+              const int r = r0 + i;
               const float a0 = __shfl_sync(0xffffffffu, f0, r), a1 = __shfl_sync(0xffffffffu, f1, r);
-              float v = a0 == 0.0f ? 0.0f : o0[r] * a0;
-              if (both && a1 != 0.0f) v += o1[r] * a1;
+              float v = a0 == 0.0f ? 0.0f : __uint_as_float(o0[i]) * a0;
+              if (both && a1 != 0.0f) v += __uint_as_float(o1[i]) * a1;
               if (column && r < rows) {
                 if (whole) *out = static_cast<uint16_t>(cache::pack2<C::kBf16>(v, 0.0f));
                 else part[4 * r] = v;
