@@ -162,7 +162,9 @@ def load_peaks():
 # translation unit, the PTX helpers and the host side that encodes its maps;
 # the GEMM kernels are built from every other file but the repack kernel's
 ATTN_SOURCES = ("sm103_flash_attn.cu", "sm103_ptx.cuh", "gemm_tn_internal.h", "gemm_tn_api.cu")
-NOT_GEMM_SOURCES = ("sm103_flash_attn.cu", "repack.cu")
+NOT_GEMM_SOURCES = ("sm103_flash_attn.cu", "repack.cu", "kv_cache_api.cu", "kv_cache_internal.h", "kv_cache_ops.cu",
+                    "sm103_cache.cuh", "sm103_cache_ptx.cuh", "sm103_cache_weigh.cu", "sm103_decode_attn.cu",
+                    "sm103_tree_attn.cu", "sm103_tree_attn.cuh")
 
 
 def source_digest(kind: str = "gemm") -> str:

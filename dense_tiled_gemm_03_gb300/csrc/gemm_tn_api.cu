@@ -25,6 +25,7 @@
 #include "flash_attn.h"
 #include "gemm_tn.h"
 #include "gemm_tn_internal.h"
+#include "kv_cache_internal.h"
 #include "sm103_gemm_kernel.cuh"
 
 namespace gemm_tn_impl {

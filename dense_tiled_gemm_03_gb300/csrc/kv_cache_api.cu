@@ -8,8 +8,8 @@
 #include <cmath>
 #include <cstdint>
 
-#include "gemm_tn_internal.h"
 #include "kv_cache.h"
+#include "kv_cache_internal.h"
 
 namespace gemm_tn_impl {
 

@@ -8,7 +8,7 @@
 
 #include <cstdint>
 
-#include "sm103_ptx.cuh"
+#include "sm103_cache_ptx.cuh"
 
 namespace gemm_tn_dev {
 

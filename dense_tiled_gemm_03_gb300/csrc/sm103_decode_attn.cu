@@ -28,7 +28,7 @@
 #include <atomic>
 #include <cstdint>
 
-#include "gemm_tn_internal.h"
+#include "kv_cache_internal.h"
 #include "sm103_tree_attn.cuh"
 
 namespace gemm_tn_dev {

@@ -5,7 +5,7 @@
 
 #include <cstdint>
 
-#include "gemm_tn_internal.h"
+#include "kv_cache_internal.h"
 #include "sm103_cache.cuh"
 
 namespace gemm_tn_dev {
