@@ -135,27 +135,40 @@ gemm_tn_dev::CacheView view_of(const kv_cache* c, int64_t batch) {
 // Least key tiles per CTA of the attention.
 constexpr int kMinChunk = 2;
 
-// Whether the attention's items stay whole: each CTA then takes the items that
-// begin in its chunk, with no workspace and no second kernel. Cutting them
-// balances the CTAs to a tile and costs a second segment per CTA, the parts'
-// way through memory and the join: as much as walking 9 more tiles (5 where an
-// item is 256 rows wide). With items no more than SMs the longest item decides,
-// `tiles` against items * tiles / sms; with more, a chunk overruns by half an
-// item on average. Long items are always cut (the host knows what the page
-// table can hold, not how ragged the lengths are). GB300, us a call, one
-// token of 32 heads over 8 KV heads, cut and whole: 1 sequence of 512 slots 17.7
-// and 11.8, of 960 18.4 and 15.1, of 1408 14.9 and 17.9; 16 sequences of 960
-// slots 26.2 and 20.5, of 3008 45.2 and 39.4.
-bool keep_whole(int64_t items, int64_t tiles, int units, int sms) {
-  const int64_t allowance = units == 2 ? 5 : 9;
-  if (tiles > 32) return sms == 1;
-  return items <= sms ? tiles * (sms - items) <= allowance * sms : tiles <= 2 * allowance;
+// Key tiles that a CTA could walk in the time that it takes to finish one item
+// and begin another: items are laid out that far apart before they are cut into
+// chunks. GB300, us a call with no gap and with 2 (3 where an item is 256 rows
+// wide): 63 tokens of 16 heads over 2 KV heads, 4 sequences of up to 32768
+// slots 65.8 and 62.7; 26 tokens of 32 heads over 8, 8 sequences of up to 4096
+// 35.0 and 34.2; one token, 2 sequences of 8192 24.2 and 22.5, 64 of up to 8192
+// 190.5 and 190.0.
+int change_tiles(int units) { return units + 1; }
+
+// Whether the attention's items stay whole, with no workspace and no second
+// kernel: one item per CTA where there are no more than SMs (2), else each CTA
+// takes the items that begin in its chunk (1). Cutting them balances the CTAs
+// to a tile and costs a second segment per CTA, the parts' way through memory
+// and the join: as much as walking 6 more tiles (5 where an item is 256 rows
+// wide). With items no more than SMs the longest item decides, `tiles` against
+// items * tiles / sms; with more, a chunk overruns by half an item on average.
+// Long items are always cut (the host knows what the page table can hold, not
+// how ragged the lengths are). GB300, us a call, one token of 32 heads over 8
+// KV heads, lengths from three quarters of the stated slots, cut and whole: 1
+// sequence of 512 slots 11.9 and 10.6, of 768 12.3 and 12.5, of 1024 12.5 and
+// 14.2; 16 of 1024 22.8 and 18.1, of 3008 39.5 and 35.8; 24 of 500 23.6 and
+// 20.5, of 1000 28.8 and 29.1, of 1500 33.2 and 38.6. 60 tokens: 1 of 512 16.6
+// and 16.1, of 768 17.0 and 19.2; 32 of 256 35.6 and 29.6, of 1000 56.8 and 58.5.
+int keep_whole(int64_t items, int64_t tiles, int units, int sms) {
+  const int64_t allowance = units == 2 ? 5 : 6;
+  if (tiles > 32) return sms == 1 ? 1 : 0;
+  if (items <= sms) return tiles * (sms - items) <= allowance * sms ? 2 : 0;
+  return tiles <= allowance ? 1 : 0;
 }
 
 // The kernels count key tiles in 32 bits: an upper bound of their number, from
 // what the cache and the inputs can hold.
 int check_tiles(const kv_cache* c, int64_t batch, int64_t row_units, int64_t tokens) {
-  const int64_t per_item = (c->max_pages * c->page_size + 127) / 128 + (tokens + 127) / 128 + 1;
+  const int64_t per_item = (c->max_pages * c->page_size + 127) / 128 + (tokens + 127) / 128 + 1 + change_tiles(2);
   const int64_t items = batch * c->kv_heads;   // below 2^31
   if (row_units > kMax31 / items || per_item > kMax31 / (items * row_units))
     return invalid("too many key tiles: batch * kv_heads * tokens * capacity is too large");
@@ -234,13 +247,14 @@ int tree_attn_fwd(int dtype, int64_t batch, int64_t tokens, int64_t heads, const
   args.has_new = has_new ? 1 : 0;
   args.chunks = sms;
   args.min_chunk = kMinChunk;
+  args.gap = change_tiles(args.units);
   args.scale_log2 = scale_log2(softmax_scale, dim);
   args.status = d_status;
   args.timeout_ns = api_watchdog_ns();
   args.drop_load_block = api_drop_load();
 
   const int64_t item_tiles = (static_cast<int64_t>(args.capacity) + 127) / 128 + (has_new ? (tokens + 127) / 128 : 0);
-  args.whole = keep_whole(batch * kv_heads * args.row_units, item_tiles, args.units, sms) ? 1 : 0;
+  args.whole = keep_whole(batch * kv_heads * args.row_units, item_tiles, args.units, sms);
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   auto launch = [&] {
     return decode ? launch_decode_attn(static_cast<int>(dim), bf16, args, s)
@@ -248,6 +262,7 @@ int tree_attn_fwd(int dtype, int64_t batch, int64_t tokens, int64_t heads, const
   };
   if (args.whole != 0) {
     args.min_chunk = 1;
+    args.gap = 0;
     const cudaError_t e = api_counted(launch());
     return e == cudaSuccess ? GEMM_TN_OK : api_fail_cuda(e, "tree attention launch");
   }

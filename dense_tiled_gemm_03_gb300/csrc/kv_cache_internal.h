@@ -40,7 +40,10 @@ struct TreeArgs {
   int has_new;
   int chunks;               // CTAs
   int min_chunk;            // least key tiles per CTA
-  int whole;                // 1: chunks take whole items (nothing is cut, part_o, part_ml and cuts are NULL)
+  int gap;                  // key tiles that the change to another item costs a CTA
+  // 1: a chunk takes the items that begin in it whole; 2: it takes one item
+  // (at most `chunks` of them); part_o, part_ml and cuts are NULL in both
+  int whole;
   float scale_log2;         // softmax scale * log2(e), > 0
   int* status;
   uint64_t timeout_ns;

@@ -118,13 +118,14 @@ __device__ __forceinline__ int warp_scan(int x, uint32_t lane) {   // inclusive
 // batch of up to blockDim.x sequences costs one round of loads and one scan.
 // Called by the whole block (it synchronises); `sums` is 32 words of shared
 // memory. tiles_of(b): key tiles of sequence b in all its items; the host has
-// made sure that their sum stays below 2^31. found(b, tiles, off, left,
+// made sure that their sum stays below 2^31. The first `skip` tiles belong to
+// no chunk. found(b, tiles, off, left,
 // chunk_tiles) is called by the one thread whose sequence holds the chunk's
 // first tile: the sequence's tiles, the number of the tile among them, the
 // tiles of the chunk and of any chunk; no thread calls it for a chunk past the
 // end.
 template <class TilesOf, class Found>
-__device__ __forceinline__ void find_start(int batch, int chunks, int min_chunk, int chunk, int* sums,
+__device__ __forceinline__ void find_start(int batch, int chunks, int min_chunk, int skip, int chunk, int* sums,
                                            TilesOf tiles_of, Found found) {
   const int tid = static_cast<int>(threadIdx.x), threads = static_cast<int>(blockDim.x);
   const uint32_t lane = lane_id();
@@ -156,8 +157,8 @@ __device__ __forceinline__ void find_start(int batch, int chunks, int min_chunk,
     }
     if (pass == 0) total += round;
     if (b0 + threads >= batch && pass == 0) {
-      chunk_tiles = max((total + chunks - 1) / chunks, min_chunk);
-      const int64_t first = static_cast<int64_t>(chunk_tiles) * chunk;
+      chunk_tiles = max((total - skip + chunks - 1) / chunks, min_chunk);
+      const int64_t first = static_cast<int64_t>(chunk_tiles) * chunk + skip;
       if (first >= total) return;
       want = static_cast<int>(first);
       left = min(chunk_tiles, total - want);

@@ -10,6 +10,12 @@
 // once for up to 128 rows (256 in pair mode). Per 128 cached keys of dim 128
 // that is 64 KB from memory against 8.4 MFLOP on the tensor cores, so up to
 // one row tile the kernel is bound by HBM, and past two by the tensor cores.
+// GB300, in a replayed graph, second kernel included: trees of 26 tokens, 32
+// heads over 8, 8 sequences of 1000 to 4096 slots 36.6 us (2.7 TB/s: few tiles
+// a CTA, the start and the join are half of it); trees of 63 tokens, 16 heads
+// over 2, 4 sequences of 20011 to 32768 slots 69.5 us (724 TFLOP/s); 1024
+// tokens, 32 heads over 8, after 2 contexts of about 8000 slots 229 us
+// (1275 TFLOP/s).
 //
 // Work: an item is (sequence, KV head, row unit) and walks its key tiles, the
 // cached ones and then the new tokens'. All items' key tiles are laid end to
@@ -81,8 +87,8 @@ struct Cfg {
   static constexpr uint32_t kOffAbort = kOffTmemSlot + 4u;
   static constexpr uint32_t kOffStart = kOffAbort + 4u;   // the chunk's first Walk
   static constexpr uint32_t kOffSums = kOffStart + 36u;   // 32 words of the search for it
-  static constexpr uint32_t kOffNext = kOffSums + 128u;   // each softmax warp's next Walk
-  static constexpr uint32_t kSmemBytes = kOffNext + 8u * 36u + 1024u;   // + slack to align the base to 1024
+  static constexpr uint32_t kOffWalks = kOffSums + 128u;   // each softmax warp's Walk, of this segment and the next
+  static constexpr uint32_t kSmemBytes = kOffWalks + 16u * 36u + 1024u;   // + slack to align the base to 1024
   static constexpr uint32_t kTmemCols = 512;
   static constexpr uint32_t kColS = 0;      // S_u: 128 fp32 columns at 128 u (P_u over half of them)
   static constexpr uint32_t kColO = 256;    // O_u: dim fp32 columns at 256 + dim u
@@ -349,13 +355,20 @@ __global__ void __launch_bounds__(C::kNumThreads) __maxnreg__(C::kMaxRegs)
     const uint32_t t_o = tmem_base + lane_off + C::kColO + static_cast<uint32_t>(C::kDim * u);
     const float c_log2 = args.scale_log2;
     const int step = parity_mode ? 2 : 1;
-    ta::Walk* next_walk = reinterpret_cast<ta::Walk*>(smem + C::kOffNext) + (warp - ta::kFirstSoftmaxWarp);
+    ta::Walk* walks = reinterpret_cast<ta::Walk*>(smem + C::kOffWalks) + 2 * (warp - ta::kFirstSoftmaxWarp);
+    if (lane == 0) walks[0] = w;
+    __syncwarp();
     int it0 = 0;                    // ring number of the segment's first tile
     uint32_t tiles_done = 0;        // tiles of this unit so far
     uint32_t ends[2] = {0, 0};      // o_done phases of the units so far
     uint32_t joins = 0;             // exchanges so far (parity mode)
     bool ok = true;
-    for (; ok && w.more(); it0 += w.count, w = *next_walk) {
+    int seg = 0;
+    // A segment's Walk lies in shared memory: its end reads again what the key
+    // tiles do not need, which then takes no registers there.
+    for (; ok; it0 += w.count, ++seg) {
+      w = walks[seg & 1];
+      if (!w.more()) break;
       {
         // worked out now, while the first scores are awaited: at the end of the
         // segment its reads of the lengths would queue behind the rows' writes
@@ -363,7 +376,7 @@ __global__ void __launch_bounds__(C::kNumThreads) __maxnreg__(C::kMaxRegs)
         ta::Walk next = w;
         next.next(args);
         __syncwarp();
-        if (lane == 0) *next_walk = next;
+        if (lane == 0) walks[(seg + 1) & 1] = next;
         __syncwarp();
       }
       const int end[2] = {w.unit_end(args, 0), w.unit_end(args, 1)};
@@ -516,6 +529,8 @@ __global__ void __launch_bounds__(C::kNumThreads) __maxnreg__(C::kMaxRegs)
       }
       if (!ok) break;
       // ---------------------------------------------------------- end of a segment
+      asm volatile("" ::: "memory");
+      w = walks[seg & 1];
       const bool mine = first < end[u];
       if (mine) {
         if (!(ok = wd.warp_wait(o_done(u), ends[u] & 1u))) break;
@@ -631,7 +646,7 @@ __global__ void __launch_bounds__(C::kNumThreads) __maxnreg__(C::kMaxRegs)
 // as an online softmax, and the second hands its sums to the first in shared
 // memory.
 template <int kDim, bool kBf16, int kGroups>
-__global__ void __launch_bounds__(256 * kGroups) tree_attn_join_kernel(const __grid_constant__ TreeArgs args) {
+__global__ void __launch_bounds__(256 * kGroups, 4 / kGroups) tree_attn_join_kernel(const __grid_constant__ TreeArgs args) {
   constexpr int kPieces = kDim / 4;            // four-column pieces of a row
   constexpr int kPer = 2;                      // pieces per thread
   __shared__ float4 other_o[kGroups == 2 ? kPer : 1][kGroups == 2 ? 256 : 1];
@@ -672,15 +687,24 @@ __global__ void __launch_bounds__(256 * kGroups) tree_attn_join_kernel(const __g
     // a unit whose keys end before the item's last parts left nothing there
     const int own_tiles = ta::unit_tiles(args, len, tl, ru, unit);
     const int own_parts = own_tiles > j0 ? min(parts, 2 + (own_tiles - j0 - 1) / per_chunk) : 1;
-#pragma unroll 4
-    for (int p = group; p < own_parts; p += kGroups) {
-      const int64_t slot = p == 0 ? (chunk - 1) * 2 + 1 : (chunk + p - 1) * 2;
-      const float2 ml = __ldg(args.part_ml + slot * rows_per_part + row);
-      float4 y[kPer];
+    constexpr int kBatch = 4;   // parts read at a time
+#pragma unroll 1
+    for (int p0 = group; p0 < own_parts; p0 += kBatch * kGroups) {
+      float2 ml[kBatch];
+      float4 y[kBatch][kPer];
 #pragma unroll
-      for (int x = 0; x < kPer; ++x)
-        y[x] = __ldg(reinterpret_cast<const float4*>(args.part_o) + (slot * kPieces + piece0 + x) * rows_per_part + row);
-      add(ml, y);
+      for (int i = 0; i < kBatch; ++i) {
+        const int p = p0 + i * kGroups;
+        ml[i] = make_float2(0.0f, 0.0f);
+        if (p >= own_parts) continue;
+        const int64_t slot = p == 0 ? (chunk - 1) * 2 + 1 : (chunk + p - 1) * 2;
+        ml[i] = __ldg(args.part_ml + slot * rows_per_part + row);
+#pragma unroll
+        for (int x = 0; x < kPer; ++x)
+          y[i][x] = __ldg(reinterpret_cast<const float4*>(args.part_o) + (slot * kPieces + piece0 + x) * rows_per_part + row);
+      }
+#pragma unroll
+      for (int i = 0; i < kBatch; ++i) add(ml[i], y[i]);
     }
   }
   if constexpr (kGroups == 2) {

@@ -44,12 +44,15 @@ __device__ __forceinline__ int item_tiles(const TreeArgs& a, int len, int tl, in
   return max((len + kTileKeys - 1) / kTileKeys + (fresh + kTileKeys - 1) / kTileKeys, 1);
 }
 
-// Key tiles of all row units of one KV head of a sequence.
-__device__ __forceinline__ int head_tiles(const TreeArgs& a, int len, int tl) {
+// Places of all row units of one KV head of a sequence: its items' key tiles,
+// each item's behind `gap` places that stand for the time a change of items
+// costs. With an item per chunk (whole == 2) every item is one place.
+__device__ __forceinline__ int head_places(const TreeArgs& a, int len, int tl) {
   int n = 0;
   const int per_item = a.units * a.tile_tokens;
+  if (a.whole == 2) return (tl + per_item - 1) / per_item;
 #pragma unroll 1
-  for (int ru = 0; ru * per_item < tl; ++ru) n += item_tiles(a, len, tl, ru);
+  for (int ru = 0; ru * per_item < tl; ++ru) n += item_tiles(a, len, tl, ru) + a.gap;
   return n;
 }
 
@@ -58,10 +61,10 @@ struct Walk {
   int b, h, ru, j0;      // item and its first tile in this segment
   int len, tl;           // cached keys and new tokens of b
   int tiles;             // tiles of the item
-  int left;              // tiles of the chunk from this segment on
+  int left;              // places of the chunk from this segment's first tile on
   int count;             // tiles of the segment
 
-  // The walk that begins at tile `off` of the `all` tiles of sequence b.
+  // The walk that begins at place `off` of the `all` places of sequence b.
   __device__ __forceinline__ void start(const TreeArgs& a, int b_, int all, int off, int left_) {
     b = b_;
     len = cached_len(a, b);
@@ -69,9 +72,18 @@ struct Walk {
     const int per_head = all / a.kv_heads;
     h = off / per_head;
     j0 = off - per_head * h;
-#pragma unroll 1
-    for (ru = 0; (tiles = item_tiles(a, len, tl, ru)) <= j0; ++ru) j0 -= tiles;
     left = left_;
+    if (a.whole == 2) {
+      ru = j0;
+      j0 = 0;
+      count = tiles = item_tiles(a, len, tl, ru);
+      return;
+    }
+#pragma unroll 1
+    for (ru = 0; (tiles = item_tiles(a, len, tl, ru)) + a.gap <= j0; ++ru) j0 -= tiles + a.gap;
+    j0 -= a.gap;
+    left += min(j0, 0);
+    j0 = max(j0, 0);
     count = tiles - j0;
     if (a.whole == 0) {
       count = min(count, left);
@@ -96,6 +108,7 @@ struct Walk {
       }
       tiles = item_tiles(a, len, tl, ru);
     } while (tiles == 0);
+    left -= a.gap;
     count = a.whole != 0 ? tiles : min(tiles, left);
   }
   // Past the last tile of the segment that unit u walks.
@@ -127,16 +140,16 @@ __device__ __forceinline__ Tile tile_of(int len, int tl, bool has_new, int j) {
 // before it reads *start.
 __device__ __forceinline__ void find_walk(const TreeArgs& a, Walk* start, int* sums) {
   cache::find_start(
-      a.batch, a.chunks, a.min_chunk, static_cast<int>(blockIdx.x), sums,
-      [&](int b) { return head_tiles(a, cached_len(a, b), new_len(a, b)) * a.kv_heads; },
-      [&](int b, int all, int off, int left, int chunk_tiles) {
+      a.batch, a.chunks, a.min_chunk, a.gap, static_cast<int>(blockIdx.x), sums,   // nothing comes before the first item
+      [&](int b) { return head_places(a, cached_len(a, b), new_len(a, b)) * a.kv_heads; },
+      [&](int b, int all, int off, int left, int chunk_places) {
         Walk w;
         w.start(a, b, all, off, left);
         *start = w;
         if (w.j0 > 0 && w.more()) {
           int4* to = reinterpret_cast<int4*>(a.cuts) + 2 * blockIdx.x;
           to[0] = make_int4(w.b, w.h, w.ru, w.j0);
-          to[1] = make_int4(w.tiles, w.len, w.tl, chunk_tiles);
+          to[1] = make_int4(w.tiles, w.len, w.tl, chunk_places);
         }
       });
 }

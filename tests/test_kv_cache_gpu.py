@@ -127,6 +127,18 @@ def test_more_sequences_than_threads(tokens, group):
     assert bool(((cache.weight.cpu().double() - want).abs()[live] <= tol[live]).all())
 
 
+@pytest.mark.parametrize("tokens", [1, 30, 70, 200])
+@pytest.mark.parametrize("batch,max_pages", [(19, 6), (19, 70), (5, 6), (5, 70), (45, 3)])
+def test_ragged_items_over_the_ctas(batch, max_pages, tokens):
+    """Items whole or cut (70 pages are more tiles than stay whole), with sequences and new tokens missing among them."""
+    lens = [(97 * b * b + 41 * b) % (64 * min(max_pages, 6) + 1) if b % 4 else 0 for b in range(batch)]
+    counts = [0 if b % 5 == 2 else 1 + (7 * b + tokens - 1) % tokens for b in range(batch)]
+    s = ref.make("bf16", 64, lens, tokens, 8, 4, 64, token_lens=counts, seed=tokens + batch, max_pages=max_pages)
+    mask = random_mask(batch, tokens, 8, empty_row=True) if batch % 2 and tokens < 100 else None
+    out, lse = run_attn(s, mask)
+    ref.check_attention(out, lse, ref.attention(s, mask), s, 7.0)
+
+
 @pytest.mark.parametrize("page", [8, 128, 384, 1024])
 def test_page_sizes(page):
     """Pages longer than a tile, and lengths that end everywhere in them."""
