@@ -143,6 +143,18 @@ constexpr int kMinChunk = 2;
 // 35.0 and 34.2; one token, 2 sequences of 8192 24.2 and 22.5, 64 of up to 8192
 // 190.5 and 190.0.
 int change_tiles(int units) { return units + 1; }
+constexpr int kMaxChange = 7;   // of this and of weigh_change_tiles
+
+// The same for the accumulated weights, where a change of items ends with the
+// gathering of `rows` query rows (past 256 a tile is walked once per 256, and the
+// change is worth fewer of them). GB300, us a call with gaps of 0, 3, 6 and 10: 1
+// row per KV head, 32 sequences of up to 2048 slots 24.2, 22.9, 23.5 and 25.2; 64
+// rows, 8 of up to 8192 23.6, 22.8, 22.4 and 22.9; 128 rows, 8 of up to 16384
+// 46.1, 45.0, 43.9 and 43.5; 700 rows, 2 of up to 4000 38.1, 37.9, 37.9 and 40.8.
+int weigh_change_tiles(int64_t rows) {
+  if (rows > 256) return 4;
+  return 3 + static_cast<int>((std::min<int64_t>(std::max<int64_t>(rows, 1), 160) - 1) / 32);
+}
 
 // Whether the attention's items stay whole, with no workspace and no second
 // kernel: one item per CTA where there are no more than SMs (2), else each CTA
@@ -168,7 +180,7 @@ int keep_whole(int64_t items, int64_t tiles, int units, int sms) {
 // The kernels count key tiles in 32 bits: an upper bound of their number, from
 // what the cache and the inputs can hold.
 int check_tiles(const kv_cache* c, int64_t batch, int64_t row_units, int64_t tokens) {
-  const int64_t per_item = (c->max_pages * c->page_size + 127) / 128 + (tokens + 127) / 128 + 1 + change_tiles(2);
+  const int64_t per_item = (c->max_pages * c->page_size + 127) / 128 + (tokens + 127) / 128 + 1 + kMaxChange;
   const int64_t items = batch * c->kv_heads;   // below 2^31
   if (row_units > kMax31 / items || per_item > kMax31 / (items * row_units))
     return invalid("too many key tiles: batch * kv_heads * tokens * capacity is too large");
@@ -388,6 +400,7 @@ int kv_cache_weigh(int dtype, int64_t batch, int64_t tokens, int64_t heads, cons
   args.block_tokens = 256 / args.group;
   args.chunks = sms;
   args.min_chunk = 1;
+  args.gap = weigh_change_tiles(max_rows * args.group);
   args.causal = causal != 0 ? 1 : 0;
   args.scale_log2 = scale_log2(softmax_scale, cache->head_dim);
   args.status = d_status;

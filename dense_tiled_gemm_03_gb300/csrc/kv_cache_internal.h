@@ -66,7 +66,7 @@ struct WeighArgs {
   int batch, tokens, heads, kv_heads, group, max_rows;
   int page_size, num_pages, capacity;
   int block_tokens;         // tokens per pass: floor(256 / group)
-  int chunks, min_chunk;
+  int chunks, min_chunk, gap;   // as in TreeArgs
   int causal;
   float scale_log2;
   int* status;

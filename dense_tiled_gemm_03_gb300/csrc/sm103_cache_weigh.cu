@@ -14,11 +14,12 @@
 // Keys are read once (dim * 2 bytes each) per 256 query rows against one
 // exponential per key and row: up to about 150 rows HBM bounds the kernel,
 // past that the exponentials do. GB300: 32 tokens of 32 heads over 8 KV heads
-// (128 rows), dim 128, 8 sequences of 9001 to 16384 slots, 231 MB: 46.9 us, 4.9
+// (128 rows), dim 128, 8 sequences of 9001 to 16384 slots, 231 MB: 44.5 us, 5.2
 // TB/s; one token of 16 heads of dim 64, 4 sequences of 300 to 1024 slots: 6.9.
 //
-// Work: an item is (sequence, KV head); the items' 128-key tiles are cut into
-// equal contiguous chunks, one per CTA (sm103_cache.cuh). Per segment of an
+// Work: an item is (sequence, KV head); the items' 128-key tiles, laid end to end
+// a change of items apart, are cut into equal contiguous chunks, one per CTA
+// (sm103_cache.cuh). Per segment of an
 // item the query rows come in blocks of at most 256, each block walking the
 // segment's tiles.
 //   warp 0      TMA producer (lane l copies the tile's l-th page)
@@ -88,13 +89,15 @@ __device__ __forceinline__ int row_count(const WeighArgs& a, int b) {
 struct Walk {
   int b, h, j0, len, n, tiles, left, count;
 
-  // The walk that begins at tile `off` of sequence b.
+  // The walk that begins at place `off` of sequence b: each of its items' tiles
+  // lie behind `gap` places that stand for the time a change of items costs.
   __device__ __forceinline__ void start(const WeighArgs& a, int b_, int off, int left_) {
     b = b_;
     load(a);
-    h = off / tiles;
-    j0 = off - tiles * h;
-    left = left_;
+    h = off / (tiles + a.gap);
+    j0 = off - (tiles + a.gap) * h - a.gap;
+    left = left_ + min(j0, 0);
+    j0 = max(j0, 0);
     count = min(tiles - j0, left);
   }
   __device__ __forceinline__ void load(const WeighArgs& a) {
@@ -114,6 +117,7 @@ struct Walk {
         load(a);
       } while (tiles == 0);
     }
+    left -= a.gap;
     count = min(tiles, left);
   }
   // blocks of query rows; one empty block where no token counts (the weights are still copied)
@@ -175,8 +179,11 @@ __global__ void __launch_bounds__(C::kNumThreads, 1) cache_weigh_kernel(const __
   griddep_wait();
   griddep_launch_dependents();
   cache::find_start(
-      args.batch, args.chunks, args.min_chunk, 0, static_cast<int>(blockIdx.x), sums,
-      [&](int b) { return (cw::cached_len(args, b) + cw::kTileKeys - 1) / cw::kTileKeys * args.kv_heads; },
+      args.batch, args.chunks, args.min_chunk, args.gap, static_cast<int>(blockIdx.x), sums,
+      [&](int b) {
+        const int tiles = (cw::cached_len(args, b) + cw::kTileKeys - 1) / cw::kTileKeys;
+        return tiles > 0 ? (tiles + args.gap) * args.kv_heads : 0;
+      },
       [&](int b, int, int off, int left, int) {
         cw::Walk w;
         w.start(args, b, off, left);

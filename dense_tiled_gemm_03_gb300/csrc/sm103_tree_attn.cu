@@ -11,15 +11,15 @@
 // that is 64 KB from memory against 8.4 MFLOP on the tensor cores, so up to
 // one row tile the kernel is bound by HBM, and past two by the tensor cores.
 // GB300, in a replayed graph, second kernel included: trees of 26 tokens, 32
-// heads over 8, 8 sequences of 1000 to 4096 slots 36.6 us (2.7 TB/s: few tiles
+// heads over 8, 8 sequences of 1000 to 4096 slots 33.5 us (2.9 TB/s: few tiles
 // a CTA, the start and the join are half of it); trees of 63 tokens, 16 heads
-// over 2, 4 sequences of 20011 to 32768 slots 69.5 us (724 TFLOP/s); 1024
-// tokens, 32 heads over 8, after 2 contexts of about 8000 slots 229 us
-// (1275 TFLOP/s).
+// over 2, 4 sequences of 20011 to 32768 slots 61.2 us (822 TFLOP/s); 1024
+// tokens, 32 heads over 8, after 2 contexts of about 8000 slots 222 us
+// (1315 TFLOP/s).
 //
 // Work: an item is (sequence, KV head, row unit) and walks its key tiles, the
 // cached ones and then the new tokens'. All items' key tiles are laid end to
-// end and cut into equal contiguous chunks, one per CTA, from the lengths as
+// end (a change of items apart) and cut into equal contiguous chunks, one per CTA, from the lengths as
 // they stand on the device: ragged batches balance to one tile, one long
 // sequence spreads over every SM, and a captured launch stays right when the
 // lengths change. An item that lies in one chunk is written by its CTA; one

@@ -393,6 +393,26 @@ def test_weigh(shape, causal, dim, dtype):
     assert ref.same(cache.weight.cpu()[~live], s.weight[~live])
 
 
+@pytest.mark.parametrize("tokens", [1, 20, 40, 130])
+@pytest.mark.parametrize("batch,longest", [(3, 4500), (19, 700), (45, 130)])
+def test_weights_of_ragged_items_over_the_ctas(batch, longest, tokens):
+    """Few long and many short items, empty sequences and sequences without counted tokens among them."""
+    lens = [(97 * b * b + longest) % (longest + 1) if b % 4 != 1 else 0 for b in range(batch)]
+    counts = [0 if b % 5 == 2 else min(n, 1 + (7 * b + tokens - 1) % tokens) for b, n in enumerate(lens)]
+    s = ref.make("fp16", 64, lens, tokens, 4, 4, 32, seed=tokens + batch)
+    rows = torch.arange(tokens, dtype=torch.int32).repeat(batch, 1)
+    lse = torch.full(s.q.shape[:3], math.log(longest) + 2.0)
+    want, tol = ref.weigh(s, lse, rows, counts, True)
+    cache, status = on_gpu(s)
+    gt.cache_weigh(cache, s.q.to(DEV), lse.to(DEV), counts=torch.tensor(counts, dtype=torch.int32, device=DEV),
+                   status=status)
+    out = cache.weight.cpu()
+    live = (torch.arange(out.shape[2])[None, None, :] < s.lens[:, None, None]).expand(out.shape)
+    off = (out.double() - want).abs()
+    assert bool((off[live] <= tol[live]).all()), float((off - tol)[live].max())
+    assert ref.same(out[~live], s.weight[~live]) and int(status.item()) == 0
+
+
 def test_weights_of_one_pass_sum_to_the_rows():
     """With the attention's own lse every counted row's weights over the slots sum to one."""
     s = ref.make("bf16", 128, [2000, 333], 6, 2, 4, 64, seed=30)
