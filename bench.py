@@ -67,32 +67,32 @@ CSRC = ROOT / "dense_tiled_gemm_03_gb300" / "csrc"
 # are unchanged (a changed kernel makes it stale). Keyed by (workload, kernel
 # configuration) or, for the fused kernels, (workload, configuration, epilogue).
 NCU_TRAFFIC: dict[tuple, dict] = {
-    ("bf16_8192x8192x8192", "2cta_n256"): {  # 546.8 us
-        "bytes": 1082566400 + 136527872, "when": "2026-12-02", "source": "c6c6d69fc4ea",
+    ("bf16_8192x8192x8192", "2cta_n256"): {  # 550.8 us
+        "bytes": 1108863744 + 133212672, "when": "2026-12-06", "source": "b8d49b2cccdf",
         "kernel": "gemm_tn_sm103_kernel<GemmConfig<2, 256, 6, 1, 1, 0, 0, 0, 0>>"},
-    ("fp16_4096x4096x4096", "2cta_n256_mc"): {  # 81.9 us
-        "bytes": 106305536 + 33761792, "when": "2026-12-02", "source": "c6c6d69fc4ea",
+    ("fp16_4096x4096x4096", "2cta_n256_mc"): {  # 81.1 us
+        "bytes": 106874112 + 30655232, "when": "2026-12-06", "source": "b8d49b2cccdf",
         "kernel": "gemm_tn_sm103_kernel<GemmConfig<2, 256, 6, 0, 2, 0, 0, 0, 0>>"},
-    ("fp16_3001x5003x4097", "2cta_n256_mc"): {  # 83.9 us
-        "bytes": 96957440 + 27212800, "when": "2026-12-02", "source": "c6c6d69fc4ea",
+    ("fp16_3001x5003x4097", "2cta_n256_mc"): {  # 84.2 us
+        "bytes": 97274112 + 24135680, "when": "2026-12-06", "source": "b8d49b2cccdf",
         "kernel": "gemm_tn_sm103_kernel<GemmConfig<2, 256, 6, 0, 2, 0, 0, 0, 0>>"},
-    ("bf16_128x16384x16384", "1cta_n128"): {  # 92.0 us
-        "bytes": 542159872 + 3272960, "when": "2026-12-02", "source": "c6c6d69fc4ea",
+    ("bf16_128x16384x16384", "1cta_n128"): {  # 91.3 us
+        "bytes": 542150656 + 390144, "when": "2026-12-06", "source": "b8d49b2cccdf",
         "kernel": "gemm_tn_sm103_kernel<GemmConfig<1, 128, 6, 1, 1, 0, 0, 0, 0>>"},
     ("fp16_256x256x256", "1cta_n64"): {  # 6.8 us
-        "bytes": 305920 + 0, "when": "2026-12-02", "source": "c6c6d69fc4ea",
+        "bytes": 305408 + 0, "when": "2026-12-06", "source": "b8d49b2cccdf",
         "kernel": "gemm_tn_sm103_kernel<GemmConfig<1, 64, 4, 0, 1, 0, 0, 0, 1>>"},
-    ("bf16_8x4096x4096", "1cta_decode_splitk"): {  # 11.9 us
-        "bytes": 33637632 + 0, "when": "2026-12-02", "source": "c6c6d69fc4ea",
+    ("bf16_8x4096x4096", "1cta_decode_splitk"): {  # 11.3 us
+        "bytes": 33637632 + 0, "when": "2026-12-06", "source": "b8d49b2cccdf",
         "kernel": "gemm_tn_decode_kernel<4, 16, 1, 2>"},
-    ("bf16_8192x8192x8192", "2cta_n256", "bias_gelu"): {  # 555.5 us
-        "bytes": 1072375040 + 135900416, "when": "2026-12-02", "source": "c6c6d69fc4ea",
+    ("bf16_8192x8192x8192", "2cta_n256", "bias_gelu"): {  # 556.9 us
+        "bytes": 1092319232 + 132353280, "when": "2026-12-06", "source": "b8d49b2cccdf",
         "kernel": "gemm_tn_sm103_kernel<GemmConfig<2, 256, 6, 1, 1, 0, 1, 0, 0>>"},
 }
 # the same for the attention kernel, keyed by workload
 NCU_TRAFFIC_ATTN: dict[str, dict] = {
-    "attn_bf16_b2_s8192_h32_d128_causal": {  # 754.8 us
-        "bytes": 454553088 + 117239552, "when": "2026-12-02", "source": "b1f83bdde46d",
+    "attn_bf16_b2_s8192_h32_d128_causal": {  # 751.3 us
+        "bytes": 457214976 + 113783808, "when": "2026-12-06", "source": "dba3b08885ae",
         "kernel": "flash_attn_fwd_kernel<Cfg<128, 1>>"},
 }
 
