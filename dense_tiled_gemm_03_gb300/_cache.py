@@ -185,6 +185,13 @@ def _status(t, cache: KVCache):
     return t.data_ptr()
 
 
+def _factor(scale):
+    scale = float(scale)
+    if scale == 0.0:   # the C ABI's word for the default
+        raise ValueError("scale must be positive")
+    return scale
+
+
 def _queries(q, cache: KVCache):
     """q's shape and struct."""
     shape = q.shape
@@ -228,7 +235,7 @@ def tree_attn(q, cache: KVCache, k_new=None, v_new=None, mask=None, token_lens=N
         raise ValueError("out must be a contiguous tensor with q's shape, dtype and device")
     _call(_tree_attn_fwd, "tree_attn_fwd", cache.index, cache._code, batch, tokens, heads, cache._struct, rq, rk, rv, d_mask,
           _ints(token_lens, cache, "token_lens", (batch,)), out.data_ptr(),
-          None if lse is None else _floats(lse, cache, "lse", (batch, tokens, heads)), 0.0 if scale is None else float(scale),
+          None if lse is None else _floats(lse, cache, "lse", (batch, tokens, heads)), 0.0 if scale is None else _factor(scale),
           _status(status, cache))
     return out
 
@@ -282,7 +289,7 @@ def cache_weigh(cache: KVCache, q, lse, counts=None, rows=None, causal=True, sca
     d_rows, d_counts, max_rows = _counted(cache, rows, counts, batch, tokens)
     _call(_kv_cache_weigh, "kv_cache_weigh", cache.index, cache._code, batch, tokens, heads, cache._struct, rq,
           _floats(lse, cache, "lse", (batch, tokens, heads)), d_rows, d_counts, max_rows, 1 if causal else 0,
-          0.0 if scale is None else float(scale), _floats(out, cache, "out", (batch, cache.kv_heads, cache.capacity)),
+          0.0 if scale is None else _factor(scale), _floats(out, cache, "out", (batch, cache.kv_heads, cache.capacity)),
           _status(status, cache))
     return out
 

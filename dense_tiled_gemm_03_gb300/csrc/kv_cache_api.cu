@@ -76,6 +76,23 @@ Range rows_range(const kv_rows* r, int64_t batch, int64_t tokens, int64_t heads,
                                              (heads - 1) * (heads > 1 ? r->head_stride : 0) + dim)};
 }
 
+Range words_range(const void* p, int64_t count) {   // of 4 bytes; empty for NULL
+  const uintptr_t b = reinterpret_cast<uintptr_t>(p);
+  return {b, p != nullptr ? b + 4 * static_cast<uintptr_t>(count) : b};
+}
+Range table_range(const kv_cache* c, int64_t batch) {
+  return words_range(c->page_table, (batch - 1) * (batch > 1 ? c->table_stride : 0) + c->max_pages);
+}
+// Whether an output lies in one of the inputs, which other blocks may still read
+// when it is written; `own` is the input that it may replace, exactly.
+template <size_t kInputs>
+bool lies_in(const Range& out, const Range& own, const Range (&inputs)[kInputs]) {
+  if (out.begin != own.begin && overlap(out, own)) return true;
+  for (const Range& in : inputs)
+    if (overlap(out, in)) return true;
+  return false;
+}
+
 // {dim, kv heads, page_size, num_pages}; moved in boxes of 64 elements of one
 // head by min(page_size, 128) rows of one page. Page num_pages reads as zeros.
 int encode_pool(CUtensorMap* map, bool bf16, const void* pool, const kv_cache* c) {
@@ -215,12 +232,15 @@ int tree_attn_fwd(int dtype, int64_t batch, int64_t tokens, int64_t heads, const
   if (o == nullptr) return invalid("o is NULL");
   if (!aligned(o, 16) || !aligned(lse, 4) || !aligned(mask, 8) || !aligned(token_lens, 4))
     return api_fail(GEMM_TN_ERR_MISALIGNED, "o, lse, mask or token_lens is not aligned to its element (o: 16 bytes)");
-  const Range out = {reinterpret_cast<uintptr_t>(o), reinterpret_cast<uintptr_t>(o) + 2 * static_cast<uintptr_t>(batch * tokens * heads * dim)};
-  if (overlap(out, rows_range(q, batch, tokens, heads, dim)) || overlap(out, pool_range(cache->k, cache)) ||
-      overlap(out, pool_range(cache->v, cache)) ||
-      (has_new && (overlap(out, rows_range(k_new, batch, tokens, kv_heads, dim)) ||
-                   overlap(out, rows_range(v_new, batch, tokens, kv_heads, dim)))))
-    return invalid("o overlaps an input or the cache");
+  const Range out = words_range(o, batch * tokens * heads * (dim / 2)), none = {0, 0};
+  const Range ins[] = {rows_range(q, batch, tokens, heads, dim), pool_range(cache->k, cache), pool_range(cache->v, cache),
+                       has_new ? rows_range(k_new, batch, tokens, kv_heads, dim) : none,
+                       has_new ? rows_range(v_new, batch, tokens, kv_heads, dim) : none,
+                       words_range(mask, 2 * batch * tokens * ((tokens + 63) / 64)), words_range(token_lens, batch),
+                       words_range(cache->lens, batch), table_range(cache, batch)};
+  if (lies_in(out, none, ins)) return invalid("o overlaps an input or the cache");
+  const Range sums = words_range(lse, batch * tokens * heads);
+  if (overlap(sums, out) || lies_in(sums, none, ins)) return invalid("lse overlaps o, an input or the cache");
   alignas(64) gemm_tn_dev::TreeArgs args{};
   args.group = static_cast<int>(heads / kv_heads);
   const bool decode = tokens * args.group <= decode_attn_rows();
@@ -316,6 +336,12 @@ int kv_cache_append(int dtype, int64_t batch, int64_t tokens, const kv_cache* ca
   } else if (max_rows > 0) {
     return invalid("max_rows > 0 without tokens");
   }
+  const Range lens = words_range(cache->lens, batch), seen = words_range(cache->seen, batch);
+  const Range new_lens = words_range(lens_out, batch), new_seen = words_range(seen_out, batch);
+  const Range ins[] = {words_range(rows, batch * max_rows), words_range(counts, batch), table_range(cache, batch)};
+  if (overlap(new_lens, new_seen) || overlap(new_lens, seen) || overlap(new_seen, lens) || lies_in(new_lens, lens, ins) ||
+      lies_in(new_seen, seen, ins))
+    return invalid("lens_out or seen_out overlaps another array of the call");
   int sms = 0;
   if ((st = api_device(&sms)) != GEMM_TN_OK) return st;
   gemm_tn_dev::AppendArgs args{};
@@ -368,6 +394,13 @@ int kv_cache_weigh(int dtype, int64_t batch, int64_t tokens, int64_t heads, cons
   }
   if (!aligned(rows, 4) || !aligned(counts, 4) || !aligned(lse, 4) || !aligned(weight_out, 4))
     return api_fail(GEMM_TN_ERR_MISALIGNED, "rows, counts, lse or weight_out not 4-byte aligned");
+  const int64_t slots = batch * cache->kv_heads * cache->max_pages * cache->page_size;
+  const Range ins[] = {max_rows > 0 ? rows_range(q, batch, tokens, heads, cache->head_dim) : Range{0, 0},
+                       words_range(lse, max_rows > 0 ? batch * tokens * heads : 0), words_range(rows, batch * max_rows),
+                       words_range(counts, batch), words_range(cache->lens, batch), table_range(cache, batch),
+                       pool_range(cache->k, cache)};
+  if (lies_in(words_range(weight_out, slots), words_range(cache->weight, slots), ins))
+    return invalid("weight_out overlaps another array of the call");
   if ((st = check_tiles(cache, batch, 1, 0)) != GEMM_TN_OK) return st;
   int sms = 0;
   if ((st = api_device(&sms)) != GEMM_TN_OK) return st;
@@ -425,6 +458,15 @@ int kv_cache_evict(int dtype, int64_t batch, const kv_cache* cache, int64_t keep
   if ((pos_out == nullptr) != (cache->pos == nullptr)) return invalid("pos_out goes with the cache's pos");
   if (!aligned(weight_out, 4) || !aligned(pos_out, 4) || !aligned(lens_out, 4))
     return api_fail(GEMM_TN_ERR_MISALIGNED, "weight_out, pos_out or lens_out not 4-byte aligned");
+  const int64_t slots = batch * cache->kv_heads * cache->max_pages * cache->page_size;
+  const Range weight = words_range(cache->weight, slots), pos = words_range(cache->pos, slots);
+  const Range lens = words_range(cache->lens, batch), new_weight = words_range(weight_out, slots);
+  const Range new_pos = words_range(pos_out, slots), new_lens = words_range(lens_out, batch);
+  const Range ins[] = {words_range(cache->seen, batch), table_range(cache, batch)};
+  if (overlap(new_weight, pos) || overlap(new_weight, lens) || overlap(new_weight, new_pos) || overlap(new_weight, new_lens) ||
+      overlap(new_pos, weight) || overlap(new_pos, lens) || overlap(new_pos, new_lens) || overlap(new_lens, weight) ||
+      overlap(new_lens, pos) || lies_in(new_weight, weight, ins) || lies_in(new_pos, pos, ins) || lies_in(new_lens, lens, ins))
+    return invalid("weight_out, pos_out or lens_out overlaps another array of the call");
   int sms = 0;
   if ((st = api_device(&sms)) != GEMM_TN_OK) return st;
   gemm_tn_dev::EvictArgs args{};

@@ -34,6 +34,8 @@
  *     test hook: the first CTA skips the K load of its tile of that number.
  *   - Pages that a call writes (append, evict) belong to one sequence only;
  *     pages that are only read may be shared.
+ *   - An output overlaps no other array of the call (INVALID_VALUE), except
+ *     that it may be, exactly, the cache's array that it replaces.
  *   - Results are repeatable to the bit: no atomics touch them.
  *   - Serving only: there are no gradients.
  */

@@ -146,6 +146,36 @@ def test_evict_refusals(lib, over, status):
     assert evict(lib, **over) == status
 
 
+@pytest.mark.parametrize("call,over", [
+    (attn, dict(lse=O)), (attn, dict(lse=O + 3 * 4 * 8 * 64 * 2 - 4)), (attn, dict(lse=Q + 64)), (attn, dict(lse=LENS)),
+    (attn, dict(lse=TABLE + 96)), (attn, dict(o=TABLE)), (attn, dict(o=0x1000, token_lens=0x1000)), (attn, dict(o=0x1000, mask=0x1010)),
+    (append, dict(lens_out=LENS + 4)), (append, dict(lens_out=SEEN)), (append, dict(lens_out=OUT, seen_out=OUT + 8)),
+    (append, dict(lens_out=OUT, counts=OUT)), (append, dict(lens_out=OUT, r=OUT - 40)), (append, dict(seen_out=LENS)),
+    (append, dict(seen_out=SEEN + 4)), (append, dict(lens_out=TABLE + 116)), (weigh, dict(out=W + 4)), (weigh, dict(out=LSE)),
+    (weigh, dict(out=LENS - 8)), (weigh, dict(out=K)), (weigh, dict(out=0x1000, counts=0x1100)), (evict, dict(w=W + 64)),
+    (evict, dict(w=POS)), (evict, dict(p=W)), (evict, dict(p=POS - 4)), (evict, dict(w=OUT, p=OUT + 3 * 2 * 160 * 4 - 4)),
+    (evict, dict(lens_out=LENS - 4)), (evict, dict(lens_out=SEEN)), (evict, dict(lens_out=TABLE)), (evict, dict(lens_out=W))])
+def test_outputs_that_lie_in_other_arrays_are_refused(lib, call, over):
+    assert call(lib, **over) == INVALID
+    assert "overlap" in gt.gemm_tn_last_error_message()
+
+
+def test_outputs_that_replace_the_caches_own_arrays_are_not(lib):
+    if torch.cuda.is_available():
+        pytest.skip("the addresses are not real")
+    for rc in (append(lib, lens_out=LENS, seen_out=SEEN), append(lib, lens_out=LENS), append(lib, lens_out=OUT, seen_out=OUT + 12),
+               weigh(lib, out=W), evict(lib, w=W, p=POS, lens_out=LENS), evict(lib, w=OUT, p=OUT + 3 * 2 * 160 * 4),
+               attn(lib, lse=O + 3 * 4 * 8 * 64 * 2)):
+        assert rc in NO_DEVICE
+
+
+def test_a_scale_of_zero_is_refused():
+    """The C call takes 0 for the default; in Python that is None."""
+    with pytest.raises(ValueError, match="scale"):
+        _cache._factor(0.0)
+    assert _cache._factor(0.5) == 0.5
+
+
 def test_empty_calls_need_no_device(lib):
     assert attn(lib, tokens=0) == gt.GEMM_TN_OK and attn(lib, heads=0) == gt.GEMM_TN_OK
 
