@@ -6,7 +6,8 @@ the attention of new tokens over it (``KVCache``, ``tree_attn``,
 
 The product is the C-ABI library ``libgemm_tn.so`` (hand-written sm_103a CUDA:
 TMA, mbarrier rings, tcgen05 tensor cores with TMEM accumulators); this
-package is its ctypes binding plus the seeded workload generator. Build the
+package is its binding (ctypes; the paged cache's is an extension module) plus
+the seeded workload generator. Build the
 library with ``python -m dense_tiled_gemm_03_gb300.build``.
 """
 from ._native import (  # noqa: F401
@@ -53,11 +54,17 @@ from ._native import (  # noqa: F401
     mm_tn,
     mm_tn_host,
 )
-from ._cache import (  # noqa: F401
-    KVCache,
-    cache_append,
-    cache_evict,
-    cache_weigh,
-    tree_attn,
-    tree_mask,
-)
+from . import _cache
+from ._cache import tree_mask  # noqa: F401
+
+
+def __getattr__(name):
+    """The paged cache's names, which load its extension module at their first use."""
+    if name not in _cache.BOUND:
+        raise AttributeError(f"module {__name__!r} has no attribute {name!r}")
+    globals().update({n: getattr(_cache, n) for n in _cache.BOUND})
+    return globals()[name]
+
+
+def __dir__():
+    return sorted({*globals(), *_cache.BOUND})

@@ -1,19 +1,24 @@
-"""Build step for the CUDA library ``libgemm_tn.so`` (sm_103a only).
+"""Build step for the CUDA library ``libgemm_tn.so`` (sm_103a only) and the
+paged cache's extension module ``_kv_cache``.
 
 Each translation unit under ``csrc/`` is compiled by nvcc in parallel with one
 ``-gencode arch=compute_103a,code=sm_103a`` and linked into a shared object in
 this package directory. Objects go to ``_build/`` at the repository root.
 The CUDA runtime is linked statically, so the library only needs the driver.
+The extension module is one C++ file over torch's headers (g++), compiled at
+the same time.
 
     python -m dense_tiled_gemm_03_gb300.build [--force] [--ptxas-verbose]
 """
 from __future__ import annotations
 
 import argparse
+import importlib.util
 import os
 import shutil
 import subprocess
 import sys
+import sysconfig
 from concurrent.futures import ThreadPoolExecutor
 from pathlib import Path
 
@@ -23,6 +28,8 @@ CSRC = PKG / "csrc"
 INCLUDE = ROOT / "include"
 BUILD_DIR = ROOT / "_build" / "gemm_tn"
 LIBRARY = PKG / "libgemm_tn.so"
+BINDING_SOURCE = CSRC / "kv_cache_py.cpp"
+BINDING = PKG / ("_kv_cache" + sysconfig.get_config_var("EXT_SUFFIX"))
 
 SOURCES = ["gemm_tn_api.cu", "sm103_gemm_1cta.cu", "sm103_gemm_2cta.cu", "sm103_gemm_nn.cu", "sm103_gemm_fused.cu",
            "sm103_flash_attn.cu", "repack.cu", "sm103_gemm_splitk.cu", "sm103_tree_attn.cu", "sm103_decode_attn.cu",
@@ -53,6 +60,31 @@ def is_stale() -> bool:
     return any(p.stat().st_mtime > built for p in _inputs())
 
 
+def binding_is_stale() -> bool:
+    if not BINDING.exists():
+        return True
+    inputs = [BINDING_SOURCE, Path(__file__), *INCLUDE.glob("*.h")]
+    return any(p.stat().st_mtime > BINDING.stat().st_mtime for p in inputs)
+
+
+def build_binding() -> Path:
+    """Compile the extension module against the installed torch (found, not imported)."""
+    spec = importlib.util.find_spec("torch")
+    if spec is None:
+        raise RuntimeError("torch not found: the paged cache's binding is built against its headers")
+    torch_dir = Path(spec.submodule_search_locations[0])
+    cuda = Path(nvcc()).resolve().parent.parent
+    tmp = BINDING.with_name(f".{BINDING.name}.{os.getpid()}")
+    cmd = ["g++", "-O2", "-std=c++17", "-fPIC", "-shared", "-fvisibility=hidden", str(BINDING_SOURCE), "-o", str(tmp),
+           "-I", str(INCLUDE), "-I", str(torch_dir / "include"), "-I", sysconfig.get_paths()["include"],
+           "-I", str(cuda / "include"), "-L", str(torch_dir / "lib"), "-lc10", "-lc10_cuda", "-ltorch_cpu", "-ltorch_python"]
+    res = subprocess.run(cmd, capture_output=True, text=True)
+    if res.returncode != 0:
+        raise RuntimeError(f"g++ failed for {BINDING_SOURCE.name}:\n{res.stdout}\n{res.stderr}")
+    os.replace(tmp, BINDING)
+    return BINDING
+
+
 def _compile(src: Path, obj: Path, verbose_ptxas: bool) -> None:
     cmd = [nvcc(), *GENCODE, *NVCC_FLAGS, "-c", str(src), "-o", str(obj)]
     if verbose_ptxas:
@@ -65,13 +97,19 @@ def _compile(src: Path, obj: Path, verbose_ptxas: bool) -> None:
 
 
 def build(force: bool = False, verbose_ptxas: bool = False) -> Path:
-    """Compile and link libgemm_tn.so if any source changed (or if forced)."""
-    if not force and not verbose_ptxas and not is_stale():
+    """Compile and link libgemm_tn.so and the binding if a source changed (or if forced). Returns the library's path."""
+    all_of_it = force or verbose_ptxas
+    if not all_of_it and not is_stale():
+        if binding_is_stale():
+            build_binding()
         return LIBRARY
     BUILD_DIR.mkdir(parents=True, exist_ok=True)
     objs = [BUILD_DIR / (Path(s).stem + ".o") for s in SOURCES]
-    with ThreadPoolExecutor(max_workers=len(SOURCES)) as pool:
+    with ThreadPoolExecutor(max_workers=len(SOURCES) + 1) as pool:
+        binding = pool.submit(build_binding) if all_of_it or binding_is_stale() else None
         list(pool.map(lambda so: _compile(CSRC / so[0], so[1], verbose_ptxas), zip(SOURCES, objs)))
+        if binding is not None:
+            binding.result()
     tmp = LIBRARY.with_name(f".libgemm_tn.{os.getpid()}.so")
     cmd = [nvcc(), *GENCODE, "-shared", "-Xcompiler", "-fPIC", *map(str, objs), "-o", str(tmp)]
     res = subprocess.run(cmd, capture_output=True, text=True)

@@ -169,21 +169,46 @@ def test_outputs_that_replace_the_caches_own_arrays_are_not(lib):
         assert rc in NO_DEVICE
 
 
-def test_a_scale_of_zero_is_refused():
-    """The C call takes 0 for the default; in Python that is None."""
-    with pytest.raises(ValueError, match="scale"):
-        _cache._factor(0.0)
-    assert _cache._factor(0.5) == 0.5
-
-
 def test_empty_calls_need_no_device(lib):
     assert attn(lib, tokens=0) == gt.GEMM_TN_OK and attn(lib, heads=0) == gt.GEMM_TN_OK
 
 
-def test_the_binding_takes_cuda_tensors_only():
+def test_the_binding_takes_cuda_tensors_only(lib):
     k = torch.zeros((2, 8, 1, 64), dtype=torch.float16)
     with pytest.raises(ValueError, match="CUDA"):
         gt.KVCache(k, k, torch.zeros((1, 2), dtype=torch.int32), torch.zeros(1, dtype=torch.int32))
+
+
+@pytest.mark.parametrize("call,what", [
+    (lambda: gt.KVCache(), "missing required argument 'k'"), (lambda: gt.KVCache(1, 2, 3, 4), "k must be a tensor"),
+    (lambda: gt.KVCache(None, None, None, None), "k must be a tensor"),
+    (lambda: gt.KVCache(1, 2, 3, 4, k=1), "multiple values for argument 'k'"),
+    (lambda: gt.KVCache(1, 2, 3, 4, table=1), "unexpected keyword argument 'table'"),
+    (lambda: gt.KVCache(*range(8)), "at most 7 arguments"), (lambda: gt.tree_attn(torch.zeros(1), None), "must be a KVCache"),
+    (lambda: gt.tree_attn(torch.zeros(1), torch.zeros(1)), "must be a KVCache"),
+    (lambda: gt.cache_append(3, 4), "missing required argument 'v_new'"), (lambda: gt.cache_weigh(3, 4, 5), "must be a KVCache"),
+    (lambda: gt.cache_evict(cache=3, keep=4), "must be a KVCache"), (lambda: gt.cache_evict(), "missing required argument 'cache'")])
+def test_the_binding_refuses_what_is_no_call(lib, call, what):
+    with pytest.raises(TypeError, match=what):
+        call()
+
+
+def test_the_bindings_names_and_documentation(lib):
+    import inspect
+    assert set(_cache.BOUND) <= set(dir(gt)) and not hasattr(gt, "no_such_name")
+    for name in _cache.BOUND:
+        assert getattr(gt, name).__doc__
+    names = list(inspect.signature(gt.tree_attn).parameters)
+    assert names == ["q", "cache", "k_new", "v_new", "mask", "token_lens", "scale", "out", "lse", "status"]
+    assert inspect.signature(gt.cache_weigh).parameters["causal"].default is True
+
+
+def test_a_missing_binding_fails_loudly(lib, monkeypatch):
+    import sys
+    monkeypatch.setitem(sys.modules, "dense_tiled_gemm_03_gb300._kv_cache", None)
+    monkeypatch.delattr(gt, "_kv_cache", raising=False)
+    with pytest.raises(RuntimeError, match="build it"):
+        _cache.binding()
 
 
 # ---------------------------------------------------------------- tree masks

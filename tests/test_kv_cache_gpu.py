@@ -7,7 +7,9 @@ pages, tokens behind the end of a sequence's own.
 """
 from __future__ import annotations
 
+import gc
 import math
+import sys
 import time
 
 import pytest
@@ -688,6 +690,74 @@ def test_watchdog_reports_a_timeout_and_the_context_survives():
         assert int(status.item()) == gt.GEMM_TN_ERR_TIMEOUT and time.perf_counter() - t0 < 5.0
     out, lse = run_attn(s)
     ref.check_attention(out, lse, ref.attention(s), s, 7.0)
+
+
+def test_the_binding_refuses_tensors_that_do_not_fit():
+    s = ref.make("bf16", 64, [30, 40], 3, 2, 2, 16, seed=66)
+    cache, _ = on_gpu(s)
+    q, kn, vn = s.q.to(DEV), s.k_new.to(DEV), s.v_new.to(DEV)
+    lse = torch.zeros(s.q.shape[:3], device=DEV)
+    whole = dict(k=cache.k, v=cache.v, page_table=cache.page_table, lens=cache.lens, weight=cache.weight, pos=cache.pos,
+                 seen=cache.seen)
+    i32 = torch.int32
+
+    def other(**over):
+        return lambda: gt.KVCache(**{**whole, **over})
+
+    refused = [
+        (other(v=cache.v.cpu()), ValueError), (other(lens=cache.lens.cpu()), ValueError), (other(v=cache.v.half()), TypeError),
+        (other(k=cache.k.float(), v=cache.v.float()), TypeError), (other(k=cache.k[0], v=cache.v[0]), ValueError),
+        (other(v=cache.v[:-1]), ValueError), (other(v=cache.v.transpose(1, 2).contiguous().transpose(1, 2)), ValueError),
+        (other(k=cache.k.transpose(0, 3), v=cache.v.transpose(0, 3)), ValueError), (other(lens=cache.lens.long()), TypeError),
+        (other(page_table=cache.page_table[0]), ValueError), (other(page_table=cache.page_table.t().contiguous().t()), ValueError),
+        (other(lens=cache.lens[:1]), ValueError), (other(lens=torch.zeros(4, dtype=i32, device=DEV)[::2]), ValueError),
+        (other(weight=cache.weight[:, :1]), ValueError), (other(weight=cache.weight.double()), ValueError),
+        (other(pos=cache.pos.long()), ValueError), (other(seen=cache.seen[:1]), ValueError),
+        (lambda: gt.tree_attn(q[0], cache), ValueError), (lambda: gt.tree_attn(q[:1], cache), ValueError),
+        (lambda: gt.tree_attn(q.half(), cache), TypeError), (lambda: gt.tree_attn(s.q, cache), ValueError),
+        (lambda: gt.tree_attn(q.transpose(1, 3), cache), ValueError), (lambda: gt.tree_attn(q, cache, kn), ValueError),
+        (lambda: gt.tree_attn(q, cache, None, vn), ValueError), (lambda: gt.tree_attn(q, cache, kn[:, :2], vn), ValueError),
+        (lambda: gt.tree_attn(q, cache, kn, vn, mask=torch.zeros((2, 3, 1), dtype=i32, device=DEV)), ValueError),
+        (lambda: gt.tree_attn(q, cache, kn, vn, mask=torch.zeros((2, 3, 2), dtype=torch.int64, device=DEV)), ValueError),
+        (lambda: gt.tree_attn(q, cache, token_lens=torch.zeros(3, dtype=i32, device=DEV)), ValueError),
+        (lambda: gt.tree_attn(q, cache, out=q.transpose(1, 2)), ValueError), (lambda: gt.tree_attn(q, cache, out=q.half()), ValueError),
+        (lambda: gt.tree_attn(q, cache, lse=lse[:1]), ValueError), (lambda: gt.tree_attn(q, cache, scale=0.0), ValueError),
+        (lambda: gt.tree_attn(q, cache, scale="x"), TypeError), (lambda: gt.tree_attn(q, cache, status=lse), ValueError),
+        (lambda: gt.tree_attn(q, cache, out=q), gt.GemmTnError), (lambda: gt.tree_attn(q, cache, scale=-1.0), gt.GemmTnError),
+        (lambda: gt.cache_append(cache, kn[:, :, :1], vn), ValueError), (lambda: gt.cache_append(cache, kn, vn[:, :2]), ValueError),
+        (lambda: gt.cache_append(cache, kn, vn, rows=torch.zeros(2, dtype=i32, device=DEV)), ValueError),
+        (lambda: gt.cache_append(other(seen=None)(), kn, vn, seen_out=cache.seen), ValueError),
+        (lambda: gt.cache_append(cache, kn, vn, lens_out=cache.seen), gt.GemmTnError),
+        (lambda: gt.cache_weigh(other(weight=None)(), q, lse), ValueError), (lambda: gt.cache_weigh(cache, q, lse[0]), ValueError),
+        (lambda: gt.cache_weigh(cache, q, lse, out=cache.weight[:1]), ValueError), (lambda: gt.cache_weigh(cache, q, None), TypeError),
+        (lambda: gt.cache_evict(other(weight=None)(), 8), ValueError), (lambda: gt.cache_evict(cache, 8.5), TypeError),
+        (lambda: gt.cache_evict(other(pos=None)(), 8, pos_out=cache.pos), ValueError), (lambda: gt.cache_evict(cache, -1), gt.GemmTnError),
+        (lambda: gt.cache_evict(cache, 8, 9), gt.GemmTnError)]
+    before = {n: sys.getrefcount(t) for n, t in [*whole.items(), ("q", q), ("lse", lse)]}
+    for i, (call, error) in enumerate(refused):
+        with pytest.raises(error) as caught:
+            call()
+        assert str(caught.value), i
+        del caught
+    gc.collect()
+    assert before == {n: sys.getrefcount(t) for n, t in [*whole.items(), ("q", q), ("lse", lse)]}
+
+
+def test_a_cache_keeps_its_tensors_and_shows_them():
+    s = ref.make("fp16", 128, [9], 1, 2, 1, 8, seed=67)
+    cache, _ = on_gpu(s)
+    lens = torch.tensor([5], dtype=torch.int32, device=DEV)
+    count = sys.getrefcount(lens)
+    other = gt.KVCache(cache.k, cache.v, cache.page_table, lens)
+    assert sys.getrefcount(lens) == count + 1 and other.lens is lens and other.weight is None and other.seen is None
+    assert (other.batch, other.capacity, other.index, other.kv_heads, other.head_dim) == (1, 16, 0, 2, 128)
+    assert other.dtype is torch.float16
+    with pytest.raises(AttributeError):
+        other.lens = cache.lens      # the description was made of the tensor
+    del other
+    assert sys.getrefcount(lens) == count
+    out = gt.tree_attn(s.q.to(DEV), cache)
+    assert sys.getrefcount(out) == 2 and gt.tree_attn(s.q.to(DEV), cache, out=out) is out
 
 
 def test_empty_calls():
