@@ -38,12 +38,13 @@ struct TreeArgs {
   int units;                // row tiles per item: 1 (both units share the rows) or 2
   int row_units;            // items per KV head of a sequence
   int has_new;
-  int chunks;               // CTAs
+  int chunks;               // CTAs (clusters of `spread` CTAs)
   int min_chunk;            // least key tiles per CTA
   int gap;                  // key tiles that the change to another item costs a CTA
   // 1: a chunk takes the items that begin in it whole; 2: it takes one item
   // (at most `chunks` of them); part_o, part_ml and cuts are NULL in both
   int whole;
+  int spread;               // CTAs of a cluster that share an item's key tiles (whole == 2 in the decode kernel; else 1)
   float scale_log2;         // softmax scale * log2(e), > 0
   int* status;
   uint64_t timeout_ns;

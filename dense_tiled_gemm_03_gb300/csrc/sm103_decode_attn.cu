@@ -22,9 +22,11 @@
 // Bound by HBM once a CTA has some ten tiles: one token of 32 heads over 8 KV
 // heads of dim 128 for 64 sequences of 900 to 8192 slots reads 1.2 GB in 190 us
 // (6.3 TB/s, 0.93 of the measured copy bandwidth; this change of layout alone
-// took 223 us to 202). One sequence of 517 slots takes 12.6 us: the start, one
-// round trip to memory for a table entry, another for its page, the products
-// and the way out.
+// took 223 us to 202). A few short sequences are bound by latency: the start, one
+// round trip to memory for a table entry, another for its page, the tiles one
+// after another (0.9 us each) and the way out. There the CTAs of a cluster share
+// an item's tiles and join their results through shared memory: one sequence of
+// 517 slots, 8 heads of dim 64, takes 8.9 us (12.6 on one CTA per head).
 //
 // Roles: warp 0 TMA producer (lane l copies the tile's l-th page), warp 1 MMA
 // issuer, warps 2-5 and 6-9 two units that take every other key tile and are
@@ -68,7 +70,8 @@ struct Cfg {
   static constexpr uint32_t kOffQ = kOffP + 2 * kPBytes;            // two slots
   static constexpr uint32_t kOffWarps = kOffQ + 2 * kQBytes;          // [2 units][4 warps][32 rows]: a tile's maxima, a segment's sums
   static constexpr uint32_t kOffRef = kOffWarps + 2u * 4u * 32u * 4u; // [2 units][32 rows]
-  static constexpr uint32_t kOffBar = kOffRef + 2u * 32u * 4u;
+  static constexpr uint32_t kOffShare = kOffRef + 2u * 32u * 4u;      // [32 rows] (max, sum) of this CTA's share of an item
+  static constexpr uint32_t kOffBar = kOffShare + 32u * 8u;
   // q_full[2], q_empty[2], k_full[S], k_empty[S], v_full[S], v_empty[S],
   // s_full[2], p_full[2], o_done[2], agree[2], xch_full, xch_empty, drain
   static constexpr int kNumBars = 4 + 4 * kStages + 8 + 3;
@@ -132,6 +135,52 @@ __device__ __forceinline__ void tmem_store_rows(uint32_t taddr, const float (&v)
   else tmem_store_32x16(taddr, raw);
 }
 
+// Joins the shares of an item that the CTAs of a cluster have in shared memory,
+// in the order of their tiles: each CTA joins and writes a part of the rows'
+// 4-column pieces.
+template <class C>
+__device__ __forceinline__ void join_shares(const TreeArgs& args, const ta::Walk& w, uint32_t base) {
+  constexpr int kPieces = C::kDim / 4, kMost = 8;   // CTAs of a cluster
+  const int rows = w.tl * args.group;
+  const uint32_t rank = cluster_ctarank();
+#pragma unroll 1
+  for (int x = static_cast<int>(rank) * C::kNumThreads + static_cast<int>(threadIdx.x); x < rows * kPieces;
+       x += args.spread * C::kNumThreads) {
+    const int r = x / kPieces, piece = x - r * kPieces;
+    float2 ml[kMost];
+    float4 y[kMost];
+#pragma unroll
+    for (int i = 0; i < kMost; ++i) {
+      ml[i] = make_float2(0.0f, 0.0f);
+      if (i >= args.spread) continue;
+      const uint32_t at = map_to_cta(base, static_cast<uint32_t>(i));
+      ml[i] = ld_cluster_f2(at + C::kOffShare + 8u * r);
+      y[i] = ld_cluster_f4(at + C::kOffK + 16u * x);
+    }
+    // a sum of zero has no maximum and nothing in its row
+    float m = -INFINITY;
+#pragma unroll
+    for (int i = 0; i < kMost; ++i) m = ml[i].y != 0.0f ? fmaxf(m, ml[i].x) : m;
+    float sum = 0.0f, o0 = 0.0f, o1 = 0.0f, o2 = 0.0f, o3 = 0.0f;
+#pragma unroll
+    for (int i = 0; i < kMost; ++i) {
+      if (ml[i].y == 0.0f) continue;
+      const float f = ex2_approx(ml[i].x - m);
+      sum += ml[i].y * f;
+      o0 += y[i].x * f;
+      o1 += y[i].y * f;
+      o2 += y[i].z * f;
+      o3 += y[i].w * f;
+    }
+    const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
+    const int token = r / args.group;
+    const int64_t out_row = (static_cast<int64_t>(w.b) * args.tokens + token) * args.heads + w.h * args.group + (r - token * args.group);
+    *reinterpret_cast<uint2*>(static_cast<uint16_t*>(args.o) + out_row * C::kDim + 4 * piece) =
+        make_uint2(cache::pack2<C::kBf16>(o0 * inv, o1 * inv), cache::pack2<C::kBf16>(o2 * inv, o3 * inv));
+    if (piece == 0 && args.lse != nullptr) args.lse[out_row] = sum == 0.0f ? -INFINITY : (m * ta::kLn2 + logf(sum));
+  }
+}
+
 }  // namespace da
 
 template <class C>
@@ -188,6 +237,7 @@ __global__ void __launch_bounds__(C::kNumThreads, 1) decode_attn_kernel(const __
     mbar_init(drain_bar, 1);
     *abort_flag = 0u;
     start_walk->left = 0;
+    start_walk->b = -1;
     fence_barrier_init();
   }
   if (warp == da::kProducerWarp && lane == 0) {
@@ -203,6 +253,7 @@ __global__ void __launch_bounds__(C::kNumThreads, 1) decode_attn_kernel(const __
   for (uint32_t x = threadIdx.x; x < 2 * C::kQBytes / 16; x += C::kNumThreads)
     st_shared_v4(base + C::kOffQ + 16u * x, 0u, 0u, 0u, 0u);
   if (threadIdx.x < 6) reinterpret_cast<uint32_t*>(smem + C::kOffVote)[threadIdx.x] = 0u;
+  if (threadIdx.x < 32) reinterpret_cast<float2*>(smem + C::kOffShare)[threadIdx.x] = make_float2(0.0f, 0.0f);
   fence_proxy_async_shared();
   // The set-up above may overlap the end of the previous kernel in the
   // stream; global memory is touched only once that kernel has completed.
@@ -521,8 +572,10 @@ __global__ void __launch_bounds__(C::kNumThreads, 1) decode_attn_kernel(const __
           tc_fence_after_sync();
           // lane r works out row r's factors
           float f0 = 0.0f, f1 = 0.0f;
-          const bool whole = w.j0 == 0 && w.count == w.tiles;
-          const int slot = static_cast<int>(blockIdx.x) * 2 + (w.j0 == 0 ? 1 : 0);
+          const bool shared = args.spread > 1;   // the cluster's CTAs join their shares, once all are there
+          const bool whole = w.j0 == 0 && w.count == w.tiles && !shared;
+          const int64_t slot = static_cast<int>(blockIdx.x) * 2 + (w.j0 == 0 ? 1 : 0);
+          float2* part_ml = shared ? reinterpret_cast<float2*>(smem + C::kOffShare) : args.part_ml + slot * args.part_rows;
           if (static_cast<int>(lane) < rows) {
             const float* x = warp_sums + lane;
             const float l0 = (x[0] + x[32]) + (x[64] + x[96]);
@@ -544,13 +597,16 @@ __global__ void __launch_bounds__(C::kNumThreads, 1) decode_attn_kernel(const __
                     sum_all == 0.0f ? -INFINITY : (m * ta::kLn2 + logf(sum_all));
               }
             } else if (quarter == 0) {
-              args.part_ml[static_cast<int64_t>(slot) * args.part_rows + lane] = make_float2(sum_all == 0.0f ? 0.0f : m, sum_all);
+              part_ml[lane] = make_float2(sum_all == 0.0f ? 0.0f : m, sum_all);
             }
           }
           const bool column = key < C::kDim;   // this lane holds a column of O
           uint16_t* out = static_cast<uint16_t*>(args.o) +
                           (static_cast<int64_t>(w.b) * args.tokens * args.heads + w.h * args.group) * C::kDim + key;
-          float* part = args.part_o + (static_cast<int64_t>(slot) * (C::kDim / 4) + key / 4) * args.part_rows * 4 + key % 4;
+          // a share lies over the K ring, which has been read for the last time: row after row
+          float* part = shared ? reinterpret_cast<float*>(smem + C::kOffK) + key
+                               : args.part_o + (slot * (C::kDim / 4) + key / 4) * args.part_rows * 4 + key % 4;
+          const int part_step = shared ? C::kDim : 4;
           const int next_token = (args.heads - args.group) * C::kDim;   // from a token's last row to the next one's first
           int head = 0;
 #pragma unroll 1   // once per segment: a loop's instructions are fetched once
@@ -567,7 +623,7 @@ __global__ void __launch_bounds__(C::kNumThreads, 1) decode_attn_kernel(const __
               if (both && a1 != 0.0f) v += __uint_as_float(o1[i]) * a1;
               if (column && r < rows) {
                 if (whole) *out = static_cast<uint16_t>(cache::pack2<C::kBf16>(v, 0.0f));
-                else part[4 * r] = v;
+                else part[part_step * r] = v;
               }
               out += C::kDim;
               if (++head == args.group) {
@@ -593,6 +649,13 @@ __global__ void __launch_bounds__(C::kNumThreads, 1) decode_attn_kernel(const __
     tc_fence_after_sync();
     tmem_dealloc<1>(tmem_base, C::kTmemCols);
   }
+  if (args.spread > 1) {
+    // every CTA of the cluster comes here, also one that has given up (its
+    // waits are bounded) or had no tiles
+    cluster_sync_all();
+    if (start_walk->b >= 0) da::join_shares<C>(args, *start_walk, base);
+    cluster_sync_all();   // no CTA leaves while its shared memory is read
+  }
 }
 
 }  // namespace gemm_tn_dev
@@ -615,15 +678,26 @@ cudaError_t launch_cfg(const gemm_tn_dev::TreeArgs& args, cudaStream_t stream) {
     done_mask.fetch_or(bit, std::memory_order_acq_rel);
   }
   cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3(static_cast<unsigned>(args.chunks), 1, 1);
+  cfg.gridDim = dim3(static_cast<unsigned>(args.chunks * args.spread), 1, 1);
   cfg.blockDim = dim3(C::kNumThreads, 1, 1);
   cfg.dynamicSmemBytes = C::kSmemBytes;
   cfg.stream = stream;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchAttribute attr[2];
+  int attrs = 0;
+  if (args.spread > 1) {
+    attr[attrs].id = cudaLaunchAttributeClusterDimension;
+    attr[attrs].val.clusterDim.x = static_cast<unsigned>(args.spread);
+    attr[attrs].val.clusterDim.y = 1;
+    attr[attrs].val.clusterDim.z = 1;
+    ++attrs;
+  }
+  if (dependent_launch_enabled()) {
+    attr[attrs].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[attrs].val.programmaticStreamSerializationAllowed = 1;
+    ++attrs;
+  }
   cfg.attrs = attr;
-  cfg.numAttrs = dependent_launch_enabled() ? 1 : 0;
+  cfg.numAttrs = static_cast<unsigned>(attrs);
   return cudaLaunchKernelEx(&cfg, gemm_tn_dev::decode_attn_kernel<C>, args);
 }
 

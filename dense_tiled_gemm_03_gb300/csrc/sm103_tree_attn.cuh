@@ -75,8 +75,12 @@ struct Walk {
     left = left_;
     if (a.whole == 2) {
       ru = j0;
-      j0 = 0;
-      count = tiles = item_tiles(a, len, tl, ru);
+      tiles = item_tiles(a, len, tl, ru);
+      // the tiles of the cluster's rank-th CTA (perhaps none)
+      const int rank = static_cast<int>(blockIdx.x) % a.spread;
+      j0 = (rank * tiles + a.spread - 1) / a.spread;
+      count = ((rank + 1) * tiles + a.spread - 1) / a.spread - j0;
+      left = count;
       return;
     }
 #pragma unroll 1
@@ -134,19 +138,19 @@ __device__ __forceinline__ Tile tile_of(int len, int tl, bool has_new, int j) {
 }
 
 
-// Finds this CTA's chunk and notes, for the kernel that joins parts, the item
+// Finds this CTA's chunk (its share of it) and notes, for the kernel that joins parts, the item
 // that the chunk begins inside of. Called by the whole block; *start and sums
 // (32 words) are shared, start->left is 0 before. The block has to synchronise
 // before it reads *start.
 __device__ __forceinline__ void find_walk(const TreeArgs& a, Walk* start, int* sums) {
   cache::find_start(
-      a.batch, a.chunks, a.min_chunk, a.gap, static_cast<int>(blockIdx.x), sums,   // nothing comes before the first item
+      a.batch, a.chunks, a.min_chunk, a.gap, static_cast<int>(blockIdx.x) / a.spread, sums,   // nothing comes before the first item
       [&](int b) { return head_places(a, cached_len(a, b), new_len(a, b)) * a.kv_heads; },
       [&](int b, int all, int off, int left, int chunk_places) {
         Walk w;
         w.start(a, b, all, off, left);
         *start = w;
-        if (w.j0 > 0 && w.more()) {
+        if (a.whole == 0 && w.j0 > 0 && w.more()) {
           int4* to = reinterpret_cast<int4*>(a.cuts) + 2 * blockIdx.x;
           to[0] = make_int4(w.b, w.h, w.ru, w.j0);
           to[1] = make_int4(w.tiles, w.len, w.tl, chunk_places);
