@@ -173,18 +173,20 @@ int weigh_change_tiles(int64_t rows) {
   return 3 + static_cast<int>((std::min<int64_t>(std::max<int64_t>(rows, 1), 160) - 1) / 32);
 }
 
-// CTAs of a cluster that share each of `items` items of `tiles` key tiles in the
-// decode kernel: as many as the tiles keep busy and as find room at once (15
+// CTAs of a cluster that share each of `items` items of `tiles` key tiles, one
+// row tile wide: as many as the tiles keep busy and as find room at once (15
 // clusters of 8, 36 of 4 or 76 of 2 on a GB300; 16 of 8 took two rounds, 17.3 us
-// for 9.0). GB300, us a call with clusters of 1, 2, 4 and 8, one token of 32
-// heads over 8 KV heads: 1 sequence of 100 slots 8.3, 8.9, 8.8 and 9.1, of 512
-// 10.8, 10.4, 9.4 and 9.2, of 2048 21.7, 15.9, 12.1 and 10.5; 4 of 1024 14.7,
-// 12.3 and 11.1; 7 of 1024 15.1 and 12.7.
-int spread_of(int64_t items, int64_t tiles, int sms) {
-  if (tiles < 4) return 1;
+// for 9.0). GB300, us a call with clusters of 1, 2, 4 and 8, 32 heads over 8 KV
+// heads: one token, 1 sequence of 100 slots 8.3, 8.9, 8.8 and 9.1, of 512 10.8,
+// 10.4, 9.4 and 9.2, of 2048 21.7, 15.9, 12.1 and 10.5; 4 of 1024 14.7, 12.3 and
+// 11.1; 7 of 1024 15.1 and 12.7. 26 tokens, whose joins are larger: 1 of 256
+// 10.8, 14.4, 11.4 and 11.3, of 1024 18.3, 18.3, 14.2 and 12.8; 4 of 1024 18.7,
+// 18.6 and 15.0 (16.6 cut); 8 of 1024 20.0 and 19.9.
+int spread_of(bool decode, int64_t items, int64_t tiles, int sms) {
+  if (tiles < (decode ? 4 : 5)) return 1;
   if (tiles > 4 && items * 8 <= sms * 4 / 5) return 8;
   if (items * 4 <= sms * 7 / 8) return 4;
-  return items * 2 <= sms * 15 / 16 ? 2 : 1;
+  return decode && items * 2 <= sms * 15 / 16 ? 2 : 1;
 }
 
 // Whether the attention's items stay whole, with no workspace and no second
@@ -201,7 +203,8 @@ int spread_of(int64_t items, int64_t tiles, int sms) {
 // sequence of 1024 slots 12.7 and 9.6, of 4096 14.4 and 12.3, of 8192 17.1 and
 // 16.7; 2 of 2048 14.0 and 12.2, of 4096 16.0 and 16.9; 16 of 1024 22.8 and
 // 18.1, of 3008 39.5 and 35.8; 24 of 500 23.6 and 20.5, of 1000 28.8 and 29.1,
-// of 1500 33.2 and 38.6. 60 tokens: 1 of 512 16.6 and 16.1, of 768 17.0 and
+// of 1500 33.2 and 38.6. 26 tokens: 1 of 1024 15.0 and 12.8, of 4096 18.3 and
+// 16.7, of 8192 21.9 and 22.9; 4 of 2048 19.5 and 18.4. 60 tokens: 1 of 512 16.6 and 16.1, of 768 17.0 and
 // 19.2; 32 of 256 35.6 and 29.6, of 1000 56.8 and 58.5.
 int keep_whole(int64_t items, int64_t tiles, int units, int spread, int sms) {
   const int64_t allowance = spread > 1 ? 4 : (units == 2 ? 5 : 6);
@@ -303,7 +306,7 @@ int tree_attn_fwd(int dtype, int64_t batch, int64_t tokens, int64_t heads, const
 
   const int64_t item_tiles = (static_cast<int64_t>(args.capacity) + 127) / 128 + (has_new ? (tokens + 127) / 128 : 0);
   const int64_t items = batch * kv_heads * args.row_units;
-  const int spread = decode ? spread_of(items, item_tiles, sms) : 1;
+  const int spread = args.units == 1 ? spread_of(decode, items, item_tiles, sms) : 1;
   args.whole = keep_whole(items, item_tiles, args.units, spread, sms);
   args.spread = args.whole == 2 ? spread : 1;
   if (args.whole == 2) args.chunks = static_cast<int>(items);

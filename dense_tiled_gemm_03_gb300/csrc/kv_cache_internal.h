@@ -44,7 +44,7 @@ struct TreeArgs {
   // 1: a chunk takes the items that begin in it whole; 2: it takes one item
   // (at most `chunks` of them); part_o, part_ml and cuts are NULL in both
   int whole;
-  int spread;               // CTAs of a cluster that share an item's key tiles (whole == 2 in the decode kernel; else 1)
+  int spread;               // CTAs of a cluster that share an item's key tiles (whole == 2 and units == 1; else 1)
   float scale_log2;         // softmax scale * log2(e), > 0
   int* status;
   uint64_t timeout_ns;
@@ -123,6 +123,25 @@ struct EvictArgs {
 }  // namespace gemm_tn_dev
 
 namespace gemm_tn_impl {
+
+// Launch attributes of the attention's kernels: clusters of `spread` CTAs,
+// programmatic dependent launch. Returns their number.
+inline unsigned attn_launch_attributes(cudaLaunchAttribute (&attr)[2], int spread) {
+  unsigned n = 0;
+  if (spread > 1) {
+    attr[n].id = cudaLaunchAttributeClusterDimension;
+    attr[n].val.clusterDim.x = static_cast<unsigned>(spread);
+    attr[n].val.clusterDim.y = 1;
+    attr[n].val.clusterDim.z = 1;
+    ++n;
+  }
+  if (dependent_launch_enabled()) {
+    attr[n].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[n].val.programmaticStreamSerializationAllowed = 1;
+    ++n;
+  }
+  return n;
+}
 
 // Attention over a paged cache: rows of queries per tile, the kernel, and the
 // kernel that joins the items its chunks cut.

@@ -683,21 +683,8 @@ cudaError_t launch_cfg(const gemm_tn_dev::TreeArgs& args, cudaStream_t stream) {
   cfg.dynamicSmemBytes = C::kSmemBytes;
   cfg.stream = stream;
   cudaLaunchAttribute attr[2];
-  int attrs = 0;
-  if (args.spread > 1) {
-    attr[attrs].id = cudaLaunchAttributeClusterDimension;
-    attr[attrs].val.clusterDim.x = static_cast<unsigned>(args.spread);
-    attr[attrs].val.clusterDim.y = 1;
-    attr[attrs].val.clusterDim.z = 1;
-    ++attrs;
-  }
-  if (dependent_launch_enabled()) {
-    attr[attrs].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[attrs].val.programmaticStreamSerializationAllowed = 1;
-    ++attrs;
-  }
   cfg.attrs = attr;
-  cfg.numAttrs = static_cast<unsigned>(attrs);
+  cfg.numAttrs = attn_launch_attributes(attr, args.spread);
   return cudaLaunchKernelEx(&cfg, gemm_tn_dev::decode_attn_kernel<C>, args);
 }
 

@@ -14,8 +14,8 @@
 // heads over 8, 8 sequences of 1000 to 4096 slots 33.5 us (2.9 TB/s: few tiles
 // a CTA, the start and the join are half of it); trees of 63 tokens, 16 heads
 // over 2, 4 sequences of 20011 to 32768 slots 61.2 us (822 TFLOP/s); 1024
-// tokens, 32 heads over 8, after 2 contexts of about 8000 slots 222 us
-// (1315 TFLOP/s).
+// tokens, 32 heads over 8, after 2 contexts of about 8000 slots 220 us
+// (1325 TFLOP/s).
 //
 // Work: an item is (sequence, KV head, row unit) and walks its key tiles, the
 // cached ones and then the new tokens'. All items' key tiles are laid end to
@@ -25,8 +25,9 @@
 // lengths change. An item that lies in one chunk is written by its CTA; one
 // that is cut leaves each part's unnormalised rows, maxima and sums in a
 // workspace and the second kernel joins them in order (repeatable to the bit).
-// Where no item can be long, a chunk takes the items that begin in it whole, and
-// there is neither workspace nor second kernel.
+// Where no item can be long, a chunk takes the items that begin in it whole, or a
+// cluster's CTAs share one and join its parts through shared memory, and there is
+// neither workspace nor second kernel.
 //
 // One CTA per SM:
 //   warp 0      TMA producer. Lane l copies the tile's l-th page (pages of 8 to
@@ -99,6 +100,59 @@ struct Cfg {
   static_assert(kOffBar % 8u == 0, "64-bit shared words");
 };
 
+// Joins the shares of an item that the CTAs of a cluster have in shared memory,
+// in the order of their tiles: each CTA joins and writes a part of the rows'
+// 8-column pieces. A function of its own, to leave the kernel's registers alone.
+template <class C>
+static __device__ __noinline__ void join_shares(const TreeArgs& args, const Walk& w, uint32_t base) {
+  constexpr int kPieces = C::kDim / 8, kMost = 8;   // CTAs of a cluster
+  const uint32_t rank = cluster_ctarank();
+#pragma unroll 1
+  for (int x = static_cast<int>(rank) * C::kNumThreads + static_cast<int>(threadIdx.x); x < kTileRows * kPieces;
+       x += args.spread * C::kNumThreads) {
+    const int r = x % kTileRows, piece = x / kTileRows;
+    const int r_token = r / args.group, token = w.ru * args.tile_tokens + r_token;
+    if (r_token >= args.tile_tokens || token >= w.tl) continue;
+    float2 ml[kMost];
+    float m = -INFINITY;   // a sum of zero has no maximum and nothing in its row
+#pragma unroll
+    for (int i = 0; i < kMost; ++i) {
+      ml[i] = make_float2(0.0f, 0.0f);
+      if (i < args.spread) ml[i] = ld_cluster_f2(map_to_cta(base, static_cast<uint32_t>(i)) + C::kOffXch + 8u * r);
+    }
+#pragma unroll
+    for (int i = 0; i < kMost; ++i) m = ml[i].y != 0.0f ? fmaxf(m, ml[i].x) : m;
+    float sum = 0.0f, o[8] = {};
+#pragma unroll
+    for (int i0 = 0; i0 < kMost; i0 += 4) {
+      float4 y[4][2];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        if (i0 + i >= args.spread) continue;
+        const uint32_t at = map_to_cta(base, static_cast<uint32_t>(i0 + i)) + C::kOffK + 16u * (2 * piece * kTileRows + r);
+        y[i][0] = ld_cluster_f4(at);
+        y[i][1] = ld_cluster_f4(at + 16u * kTileRows);
+      }
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const float2 part = ml[i0 + i];
+        if (part.y == 0.0f) continue;
+        const float f = ex2_approx(part.x - m);
+        sum += part.y * f;
+        const float v[8] = {y[i][0].x, y[i][0].y, y[i][0].z, y[i][0].w, y[i][1].x, y[i][1].y, y[i][1].z, y[i][1].w};
+#pragma unroll
+        for (int e = 0; e < 8; ++e) o[e] += v[e] * f;
+      }
+    }
+    const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
+    const int64_t out_row = (static_cast<int64_t>(w.b) * args.tokens + token) * args.heads + w.h * args.group + (r - r_token * args.group);
+    *reinterpret_cast<uint4*>(static_cast<uint16_t*>(args.o) + out_row * C::kDim + 8 * piece) =
+        make_uint4(pack2<C::kBf16>(o[0] * inv, o[1] * inv), pack2<C::kBf16>(o[2] * inv, o[3] * inv),
+                   pack2<C::kBf16>(o[4] * inv, o[5] * inv), pack2<C::kBf16>(o[6] * inv, o[7] * inv));
+    if (piece == 0 && args.lse != nullptr) args.lse[out_row] = sum == 0.0f ? -INFINITY : (m * kLn2 + logf(sum));
+  }
+}
+
 }  // namespace ta
 
 template <class C>
@@ -153,6 +207,7 @@ __global__ void __launch_bounds__(C::kNumThreads) __maxnreg__(C::kMaxRegs)
     mbar_init(drain_bar, 1);
     *abort_flag = 0u;
     start_walk->left = 0;
+    start_walk->b = -1;
     fence_barrier_init();
   }
   if (warp == ta::kProducerWarp && lane == 0) {
@@ -164,6 +219,7 @@ __global__ void __launch_bounds__(C::kNumThreads) __maxnreg__(C::kMaxRegs)
     tmem_alloc<1>(smem_addr(tmem_slot), C::kTmemCols);
     tmem_relinquish<1>();
   }
+  if (threadIdx.x < ta::kTileRows) xch[threadIdx.x] = make_float2(0.0f, 0.0f);   // a share without tiles stays so
   // The set-up above may overlap the end of the previous kernel in the
   // stream; global memory is touched only once that kernel has completed.
   griddep_wait();
@@ -568,7 +624,8 @@ __global__ void __launch_bounds__(C::kNumThreads) __maxnreg__(C::kMaxRegs)
         // NaN sums (NaN or infinite inputs) stay NaN
         const float sum = !(l == 0.0f || other_l == 0.0f) ? l * w0 + other_l * w1 : (l == 0.0f ? other_l : l);
         const bool join = __any_sync(0xffffffffu, other_l != 0.0f);
-        const bool whole = w.j0 == 0 && w.count == w.tiles;
+        const bool shared = args.spread > 1;   // the cluster's CTAs join their shares, once all are there
+        const bool whole = w.j0 == 0 && w.count == w.tiles && !shared;
         const float f0 = l == 0.0f ? 0.0f : (l > 0.0f ? w0 : 1.0f);
         const float f1 = other_l == 0.0f ? 0.0f : (other_l > 0.0f ? w1 : 1.0f);
         const float inv = whole ? (sum == 0.0f ? 0.0f : 1.0f / sum) : 1.0f;
@@ -581,13 +638,16 @@ __global__ void __launch_bounds__(C::kNumThreads) __maxnreg__(C::kMaxRegs)
             if (args.lse != nullptr)
               args.lse[out_row] = sum == 0.0f ? -INFINITY : (m * ta::kLn2 + logf(sum));
           } else {
-            args.part_ml[part_row] = make_float2(m, sum);
+            // (this thread has read the other unit's maximum and sum from there)
+            *(shared ? xch + r : args.part_ml + part_row) = make_float2(m, sum);
           }
         }
         uint16_t* out = static_cast<uint16_t*>(args.o) + out_row * C::kDim;
         // [slot][dim / 4][row] pieces of four: a warp's 32 rows store 512 contiguous bytes at a time
-        float4* part = reinterpret_cast<float4*>(args.part_o) +
-                       static_cast<int64_t>(slot) * args.part_rows * (C::kDim / 4) + part_unit_row;
+        // (a share over the K ring, which has been read for the last time)
+        float4* part = shared ? reinterpret_cast<float4*>(smem + C::kOffK) + r
+                              : reinterpret_cast<float4*>(args.part_o) +
+                                    static_cast<int64_t>(slot) * args.part_rows * (C::kDim / 4) + part_unit_row;
         const int part_pitch = args.part_rows;
 #pragma unroll 1   // once per segment: short code, which is fetched cold, is faster than unrolled code
         for (int c = 0; c < C::kDim / 32; ++c) {
@@ -634,6 +694,13 @@ __global__ void __launch_bounds__(C::kNumThreads) __maxnreg__(C::kMaxRegs)
   if (warp == ta::kMmaWarp) {
     tc_fence_after_sync();
     tmem_dealloc<1>(tmem_base, C::kTmemCols);
+  }
+  if (args.spread > 1) {
+    // every CTA of the cluster comes here, also one that has given up (its
+    // waits are bounded) or had no tiles
+    cluster_sync_all();
+    if (start_walk->b >= 0) ta::join_shares<C>(args, *start_walk, base);
+    cluster_sync_all();   // no CTA leaves while its shared memory is read
   }
 }
 
@@ -752,15 +819,13 @@ cudaError_t launch_cfg(const gemm_tn_dev::TreeArgs& args, cudaStream_t stream) {
     done_mask.fetch_or(bit, std::memory_order_acq_rel);
   }
   cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3(static_cast<unsigned>(args.chunks), 1, 1);
+  cfg.gridDim = dim3(static_cast<unsigned>(args.chunks * args.spread), 1, 1);
   cfg.blockDim = dim3(C::kNumThreads, 1, 1);
   cfg.dynamicSmemBytes = C::kSmemBytes;
   cfg.stream = stream;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchAttribute attr[2];
   cfg.attrs = attr;
-  cfg.numAttrs = dependent_launch_enabled() ? 1 : 0;
+  cfg.numAttrs = attn_launch_attributes(attr, args.spread);
   return cudaLaunchKernelEx(&cfg, gemm_tn_dev::tree_attn_kernel<C>, args);
 }
 

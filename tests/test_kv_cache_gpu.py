@@ -141,6 +141,20 @@ def test_ragged_items_over_the_ctas(batch, max_pages, tokens):
     ref.check_attention(out, lse, ref.attention(s, mask), s, 7.0)
 
 
+@pytest.mark.parametrize("dim", [64, 128])
+@pytest.mark.parametrize("tokens", [1, 4, 30])
+@pytest.mark.parametrize("batch,kv_heads,longest", [(1, 1, 640), (3, 5, 700), (1, 2, 4000), (8, 4, 1500), (13, 5, 900)])
+def test_items_shared_by_a_cluster(batch, kv_heads, longest, tokens, dim):
+    """Clusters of 8, 4 and 2; lengths far below the capacity leave CTAs of a cluster without tiles, or all of them."""
+    lens = [longest] + [(211 * b * b + 3) % longest if b % 3 else 0 for b in range(1, batch)]
+    counts = [tokens] + [(5 * b) % (tokens + 1) for b in range(1, batch)]
+    s = ref.make("fp16" if dim == 64 else "bf16", dim, lens, tokens, kv_heads, 4, 32, token_lens=counts, seed=batch + tokens)
+    out, lse = run_attn(s)
+    ref.check_attention(out, lse, ref.attention(s), s, 7.0)
+    out, lse = run_attn(s, use_new=False)      # rows that see no key at all
+    ref.check_attention(out, lse, ref.attention(s, use_new=False), s, 7.0)
+
+
 @pytest.mark.parametrize("page", [8, 128, 384, 1024])
 def test_page_sizes(page):
     """Pages longer than a tile, and lengths that end everywhere in them."""
