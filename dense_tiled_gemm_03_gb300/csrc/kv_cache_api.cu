@@ -189,6 +189,19 @@ int spread_of(bool decode, int64_t items, int64_t tiles, int sms) {
   return decode && items * 2 <= sms * 15 / 16 ? 2 : 1;
 }
 
+// Blocks of a cluster that select from one of `lists` lists of at most `slots`
+// slots: as many as find room at once, where the lists are long enough for their
+// half a dozen meetings. GB300, us a call (with the moves) with clusters of 1, 2,
+// 4 and 8, 8 lists a sequence, cut to half: 1 sequence of 8192 slots 17.6, 19.5,
+// 19.7 and 22.8, of 32768 50.4, 42.2, 35.9 and 36.7; 2 of 16384 36.9, 34.9 and
+// 33.8; 8 of 16384 66.3 and 65.5. Past 40960 slots the keys of a list lie in the
+// shared memory of several blocks, of one they do not: 2 of 60000 180, 87 and 75.
+int evict_spread(int64_t lists, int64_t slots, int sms) {
+  if (slots < 16384) return 1;
+  if (lists * 4 <= sms * 7 / 8) return 4;
+  return lists * 2 <= sms * 15 / 16 || slots > evict_smem_keys(1 << 30) ? 2 : 1;
+}
+
 // Whether the attention's items stay whole, with no workspace and no second
 // kernel: one item per CTA, or per cluster of `spread`, where there are no more
 // of those than SMs (2), else each CTA takes the items that begin in its chunk
@@ -505,6 +518,7 @@ int kv_cache_evict(int dtype, int64_t batch, const kv_cache* cache, int64_t keep
   args.recent = static_cast<int>(recent);
   args.max_moves = static_cast<int>(std::max<int64_t>(0, std::min<int64_t>(keep, args.c.capacity - keep)));
   args.smem_keys = evict_smem_keys(args.c.capacity);
+  args.spread = 1;
   args.status = d_status;
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   // few rows to move: one kernel (which must not write the lens that its other blocks read)
@@ -513,9 +527,12 @@ int kv_cache_evict(int dtype, int64_t batch, const kv_cache* cache, int64_t keep
     return e == cudaSuccess ? GEMM_TN_OK : api_fail_cuda(e, "cache evict launch");
   }
   const size_t lists = static_cast<size_t>(batch * cache->kv_heads);
+  args.spread = evict_spread(static_cast<int64_t>(lists), args.c.capacity, sms);
+  const int per_block = ((args.c.capacity + args.spread - 1) / args.spread + 31) / 32 * 32;
+  args.smem_keys = evict_smem_keys(per_block);
   const size_t count_bytes = (lists * 4 + 15) / 16 * 16;
   const size_t move_bytes = lists * static_cast<size_t>(args.max_moves) * 8;
-  const size_t word_bytes = args.smem_keys == args.c.capacity ? 0 : lists * static_cast<size_t>((args.c.capacity + 31) / 32) * 12;
+  const size_t word_bytes = args.smem_keys == per_block ? 0 : lists * static_cast<size_t>((args.c.capacity + 31) / 32) * 12;
   void* workspace = nullptr;
   cudaError_t e = api_workspace(count_bytes + move_bytes + word_bytes, s, &workspace);
   if (e != cudaSuccess) return api_fail_cuda(e, "workspace");

@@ -116,7 +116,8 @@ struct EvictArgs {
   uint32_t* words;          // workspace: [batch * kv heads][3][ceil(capacity / 32)] where keys do not fit in shared memory
   int max_moves;
   int keep, recent;
-  int smem_keys;            // slots whose keys fit in shared memory
+  int smem_keys;            // keys that a block holds in shared memory (none where it has more slots)
+  int spread;               // blocks of a cluster that share a list
   int* status;
 };
 
@@ -124,9 +125,9 @@ struct EvictArgs {
 
 namespace gemm_tn_impl {
 
-// Launch attributes of the attention's kernels: clusters of `spread` CTAs,
+// Launch attributes of the cache's kernels: clusters of `spread` CTAs,
 // programmatic dependent launch. Returns their number.
-inline unsigned attn_launch_attributes(cudaLaunchAttribute (&attr)[2], int spread) {
+inline unsigned cache_launch_attributes(cudaLaunchAttribute (&attr)[2], int spread) {
   unsigned n = 0;
   if (spread > 1) {
     attr[n].id = cudaLaunchAttributeClusterDimension;

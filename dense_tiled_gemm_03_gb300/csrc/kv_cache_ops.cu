@@ -147,7 +147,9 @@ __device__ __forceinline__ longlong2 places_of(const EvictArgs& a, int b, int h,
   return place;
 }
 
-// One block per (sequence, KV head). The `keep` largest keys are found by
+// One block per (sequence, KV head), or for few long lists a cluster of `spread`
+// blocks that each hold a run of the slots and add up their counts through shared
+// memory. The `keep` largest keys are found by
 // counting: the range between the smallest and the largest key is cut into 2048
 // equal bins, then the bin that holds the keep-th largest, until a bin is one
 // key (three passes at most, usually two; bins of the keys' own range and not
@@ -161,17 +163,19 @@ __device__ __forceinline__ longlong2 places_of(const EvictArgs& a, int b, int h,
 template <bool kFused>
 __global__ void __launch_bounds__(ev::kThreads) cache_select_kernel(const __grid_constant__ EvictArgs a) {
   extern __shared__ uint32_t smem_keys[];
-  __shared__ int hist[ev::kBins];
+  __shared__ __align__(8) int hist[2][ev::kBins];   // a round's, and the one before's while other blocks read it
   __shared__ int sums[ev::kWarps];
   __shared__ uint32_t extremes[2][ev::kWarps];
-  __shared__ int chosen[2];
+  __shared__ uint32_t shared_words[8];   // what the cluster's other blocks read of this one, each word once
+  __shared__ int chosen[3];
   __shared__ int2 list[kFused ? ev::kFusedMoves : 1];
   __shared__ longlong2 places[kFused ? ev::kFusedMoves : 1];
   __shared__ uint32_t smem_words[ev::kSmemKeys / 32];
   __shared__ int smem_ranks[2][ev::kSmemKeys / 32];
   griddep_wait();
   griddep_launch_dependents();
-  const int bh = static_cast<int>(blockIdx.x);
+  const int spread = kFused ? 1 : a.spread;
+  const int bh = static_cast<int>(blockIdx.x) / spread, rank = static_cast<int>(blockIdx.x) - bh * spread;
   const int b = bh / a.c.kv_heads, h = bh - b * a.c.kv_heads;
   const int tid = static_cast<int>(threadIdx.x);
   const int warp = tid >> 5, lane = tid & 31;
@@ -182,20 +186,42 @@ __global__ void __launch_bounds__(ev::kThreads) cache_select_kernel(const __grid
   const int32_t* pos = a.pos != nullptr ? a.pos + base : nullptr;
   const int stay = min(len, keep);
   if (kFused && h == 0 && tid == 0) a.lens_out[b] = stay;
+  const int thread = rank * ev::kThreads + tid, threads = spread * ev::kThreads;   // of the list
   if (len <= keep) {
-    if (!kFused && tid == 0) a.counts[bh] = 0;
+    if (!kFused && thread == 0) a.counts[bh] = 0;
     if (a.weight_out != a.weight)
-      for (int s = tid; s < stay; s += ev::kThreads) a.weight_out[base + s] = weight[s];
+      for (int s = thread; s < stay; s += threads) a.weight_out[base + s] = weight[s];
     if (a.pos_out != nullptr && a.pos_out != a.pos)
-      for (int s = tid; s < stay; s += ev::kThreads) a.pos_out[base + s] = pos[s];
+      for (int s = thread; s < stay; s += threads) a.pos_out[base + s] = pos[s];
     return;
   }
+  // this block's run of slots: whole words of 32
+  const int per_block = ((len + spread - 1) / spread + 31) / 32 * 32;
+  const int s0 = min(len, rank * per_block), s1 = min(len, s0 + per_block);
+  auto sync = [&] {
+    if (spread > 1) cluster_sync_all();
+    else __syncthreads();
+  };
+  // word `at` of the cluster's block i, after a sync
+  auto word_of = [&](int i, int at) {
+    return spread > 1 ? ld_cluster_u32(map_to_cta(smem_addr(shared_words + at), static_cast<uint32_t>(i))) : shared_words[at];
+  };
+  // the blocks' values of word `at` before this one's, and of all of them
+  auto before_and_all = [&](int at, int* all) {
+    int before = 0;
+    *all = 0;
+    for (int i = 0; i < spread; ++i) {
+      if (i == rank) before = *all;
+      *all += static_cast<int>(word_of(i, at));
+    }
+    return before;
+  };
   const int first_new = a.recent > 0 ? a.seen[b] - a.recent : 0;   // positions from here on are the newest
   auto load_key = [&](int s) { return ev::key_of(weight[s], a.recent > 0 && pos[s] >= first_new); };
-  const bool in_smem = len <= a.smem_keys;
-  auto key = [&](int s) { return in_smem ? smem_keys[s] : load_key(s); };
+  const bool in_smem = s1 - s0 <= a.smem_keys;
+  auto key = [&](int s) { return in_smem ? smem_keys[s - s0] : load_key(s); };
   const int word_pitch = (a.c.capacity + 31) / 32;
-  uint32_t* global_words = in_smem ? nullptr : a.words + static_cast<int64_t>(3 * bh) * word_pitch;
+  uint32_t* global_words = in_smem ? nullptr : a.words + static_cast<int64_t>(3 * bh) * word_pitch + s0 / 32;
   uint32_t* words = in_smem ? smem_words : global_words;
   int* hole_ranks = in_smem ? smem_ranks[0] : reinterpret_cast<int*>(global_words + word_pitch);
   int* mover_ranks = in_smem ? smem_ranks[1] : hole_ranks + word_pitch;
@@ -203,21 +229,21 @@ __global__ void __launch_bounds__(ev::kThreads) cache_select_kernel(const __grid
   uint32_t lowest = 0xffffffffu, highest = 0u;
   int newest = 0;
   constexpr int kLoads = 8;   // slots a thread reads at a time
-  for (int x0 = tid; x0 < len; x0 += kLoads * ev::kThreads) {
+  for (int x0 = s0 + tid; x0 < s1; x0 += kLoads * ev::kThreads) {
     float wt[kLoads];
     int32_t ps[kLoads];
 #pragma unroll
     for (int i = 0; i < kLoads; ++i) {
       const int s = x0 + i * ev::kThreads;
-      wt[i] = s < len ? weight[s] : 0.0f;
-      ps[i] = s < len && a.recent > 0 ? pos[s] : 0;
+      wt[i] = s < s1 ? weight[s] : 0.0f;
+      ps[i] = s < s1 && a.recent > 0 ? pos[s] : 0;
     }
 #pragma unroll
     for (int i = 0; i < kLoads; ++i) {
       const int s = x0 + i * ev::kThreads;
-      if (s >= len) break;
+      if (s >= s1) break;
       const uint32_t k = ev::key_of(wt[i], a.recent > 0 && ps[i] >= first_new);
-      if (in_smem) smem_keys[s] = k;
+      if (in_smem) smem_keys[s - s0] = k;
       if (k == 0xffffffffu) {
         ++newest;
       } else {
@@ -237,6 +263,19 @@ __global__ void __launch_bounds__(ev::kThreads) cache_select_kernel(const __grid
   newest = total;
   lowest = __reduce_min_sync(0xffffffffu, extremes[0][lane]);
   highest = __reduce_max_sync(0xffffffffu, extremes[1][lane]);
+  if (spread > 1) {
+    if (tid == 0) {
+      shared_words[0] = lowest;
+      shared_words[1] = highest;
+      shared_words[2] = static_cast<uint32_t>(newest);
+    }
+    sync();
+    for (int i = 0; i < spread; ++i) {
+      lowest = min(lowest, word_of(i, 0));
+      highest = max(highest, word_of(i, 1));
+    }
+    before_and_all(2, &newest);
+  }
 
   // the keep-th largest key, and how many slots that hold exactly it stay
   uint32_t limit = 0xffffffffu;
@@ -245,18 +284,29 @@ __global__ void __launch_bounds__(ev::kThreads) cache_select_kernel(const __grid
     need = keep - newest;
     limit = lowest;               // keys from here on, 2^bits of them, are looked at
     int bits = 32 - __clz(highest - lowest);
-    while (true) {
+    for (int round = 0;; ++round) {
       const int shift = max(bits - 11, 0);
-      for (int x = tid; x < ev::kBins; x += ev::kThreads) hist[x] = 0;
+      int* bins = hist[round & 1];
+      for (int x = tid; x < ev::kBins; x += ev::kThreads) bins[x] = 0;
       __syncthreads();
-      for (int s = tid; s < len; s += ev::kThreads) {
+      for (int s = s0 + tid; s < s1; s += ev::kThreads) {
         const uint32_t k = key(s), d = k - limit;
-        if (k != 0xffffffffu && k >= limit && (bits == 32 || d < (1u << bits))) atomicAdd(&hist[d >> shift], 1);
+        if (k != 0xffffffffu && k >= limit && (bits == 32 || d < (1u << bits))) atomicAdd(&bins[d >> shift], 1);
       }
-      __syncthreads();
+      sync();
       // from the top bin down: thread t looks at bins top - 2t and top - 2t - 1
       const int top = ev::kBins - 1 - 2 * tid;
-      const int n0 = hist[top], n1 = hist[top - 1];
+      int n0 = bins[top], n1 = bins[top - 1];
+      if (spread > 1) {
+        n0 = n1 = 0;
+        const uint32_t at = smem_addr(bins + top - 1);
+#pragma unroll 8
+        for (int i = 0; i < spread; ++i) {
+          const int2 n = ld_cluster_s2(map_to_cta(at, static_cast<uint32_t>(i)));
+          n0 += n.y;
+          n1 += n.x;
+        }
+      }
       int v = n0 + n1;
 #pragma unroll
       for (int d = 1; d < 32; d *= 2) {
@@ -267,35 +317,40 @@ __global__ void __launch_bounds__(ev::kThreads) cache_select_kernel(const __grid
       if (before < need && before + n0 >= need) {
         chosen[0] = top;
         chosen[1] = need - before;
+        chosen[2] = n0;
       } else if (before + n0 < need && before + n0 + n1 >= need) {
         chosen[0] = top - 1;
         chosen[1] = need - before - n0;
+        chosen[2] = n1;
       }
       __syncthreads();
       limit += static_cast<uint32_t>(chosen[0]) << shift;
       need = chosen[1];
-      ties = hist[chosen[0]];
+      ties = chosen[2];
       __syncthreads();
       bits = shift;
       if (shift == 0 || ties == 1) break;
     }
-    if (bits > 0) {   // one key is left in the bin: it is the limit
-      for (int s = tid; s < len; s += ev::kThreads) {
-        const uint32_t k = key(s);
-        if (k != 0xffffffffu && k >= limit && k - limit < (1u << bits)) extremes[0][0] = k;
-      }
+    if (bits > 0) {   // one key is left in the bin: it is the limit (no key is 0)
+      if (tid == 0) shared_words[3] = 0u;
       __syncthreads();
-      limit = extremes[0][0];
+      for (int s = s0 + tid; s < s1; s += ev::kThreads) {
+        const uint32_t k = key(s);
+        if (k != 0xffffffffu && k >= limit && k - limit < (1u << bits)) shared_words[3] = k;
+      }
+      sync();
+      limit = 0u;
+      for (int i = 0; i < spread; ++i) limit = max(limit, word_of(i, 3));
     }
   }
 
   // Kept slots as words of 32 bits, and from here on a thread has a run of
   // words: ranks come from one scan of their bit counts.
-  const int num_words = (len + 31) / 32;
+  const int num_words = (s1 - s0 + 31) / 32;   // word x: slots from s0 + 32 x
   for (int x = warp; x < num_words; x += ev::kWarps) {
-    const int s = 32 * x + lane;
-    const uint32_t k = s < len ? key(s) : 0u;
-    const uint32_t bits = __ballot_sync(0xffffffffu, s < len && k >= limit);
+    const int s = s0 + 32 * x + lane;
+    const uint32_t k = s < s1 ? key(s) : 0u;
+    const uint32_t bits = __ballot_sync(0xffffffffu, s < s1 && k >= limit);
     if (lane == 0) words[x] = bits;
   }
   __syncthreads();
@@ -316,13 +371,19 @@ __global__ void __launch_bounds__(ev::kThreads) cache_select_kernel(const __grid
       uint32_t bits = 0;
       for (uint32_t left = words[x]; left != 0u; left &= left - 1u) {
         const int i = __ffs(left) - 1;
-        if (key(32 * x + i) == limit) bits |= 1u << i;
+        if (key(s0 + 32 * x + i) == limit) bits |= 1u << i;
       }
       return bits;
     };
     int mine = 0;
     for (int x = w0; x < w1; ++x) mine += __popc(tied(x));
     int stay_here = need - block_base(mine);   // of this thread's ties
+    if (spread > 1) {
+      if (tid == 0) shared_words[4] = static_cast<uint32_t>(total);
+      sync();
+      int all;
+      stay_here -= before_and_all(4, &all);
+    }
     for (int x = w0; x < w1; ++x) {
       uint32_t drop = tied(x);
       for (; drop != 0u && stay_here > 0; --stay_here) drop &= drop - 1u;
@@ -330,7 +391,7 @@ __global__ void __launch_bounds__(ev::kThreads) cache_select_kernel(const __grid
     }
   }
   // slots of word x before `keep`
-  auto before_keep = [&](int x) { return cache::low_bits(keep - 32 * x); };
+  auto before_keep = [&](int x) { return cache::low_bits(keep - s0 - 32 * x); };
   auto holes_of = [&](int x) { return ~words[x] & before_keep(x); };
   auto movers_of = [&](int x) { return words[x] & ~before_keep(x); };
   int holes = 0, movers = 0;
@@ -339,7 +400,18 @@ __global__ void __launch_bounds__(ev::kThreads) cache_select_kernel(const __grid
     movers += __popc(movers_of(x));
   }
   int hole_rank = block_base(holes);
-  int mover_rank = block_base(movers);   // as many movers as holes: `total`
+  const int block_holes = total;
+  int mover_rank = block_base(movers);
+  if (spread > 1) {
+    if (tid == 0) {
+      shared_words[5] = static_cast<uint32_t>(block_holes);
+      shared_words[6] = static_cast<uint32_t>(total);
+    }
+    sync();
+    hole_rank += before_and_all(5, &total);
+    mover_rank += before_and_all(6, &total);
+  }
+  // as many movers as holes: `total`
   for (int x = w0; x < w1; ++x) {
     hole_ranks[x] = hole_rank;
     mover_ranks[x] = mover_rank;
@@ -352,25 +424,26 @@ __global__ void __launch_bounds__(ev::kThreads) cache_select_kernel(const __grid
 #pragma unroll 2
   for (int x = warp; x < num_words; x += ev::kWarps) {
     const uint32_t hole = holes_of(x), mover = movers_of(x);
-    if ((hole >> lane) & 1u) moves[hole_ranks[x] + __popc(hole & below)].y = 32 * x + lane;
-    if ((mover >> lane) & 1u) moves[mover_ranks[x] + __popc(mover & below)].x = 32 * x + lane;
+    if ((hole >> lane) & 1u) moves[hole_ranks[x] + __popc(hole & below)].y = s0 + 32 * x + lane;
+    if ((mover >> lane) & 1u) moves[mover_ranks[x] + __popc(mover & below)].x = s0 + 32 * x + lane;
   }
-  if (!kFused && tid == 0) a.counts[bh] = total;
-  __syncthreads();   // the list is complete, and every key has been read
+  if (!kFused && thread == 0) a.counts[bh] = total;
+  sync();   // the list is complete, every key has been read, and so has every block's shared memory by the others
   // Weights and positions: a kept slot before `keep` keeps its own (copied
   // where they go elsewhere), a moved one takes them along. A thread's reads go
   // out together, before its first write.
   const bool copy_weight = a.weight_out != a.weight, copy_pos = a.pos_out != nullptr && a.pos_out != a.pos;
   constexpr int kBatch = 4;
   if (copy_weight || copy_pos) {
-    for (int x0 = tid; x0 < keep; x0 += kBatch * ev::kThreads) {
+    const int end = min(s1, keep);
+    for (int x0 = s0 + tid; x0 < end; x0 += kBatch * ev::kThreads) {
       float wt[kBatch];
       int32_t ps[kBatch];
       bool on[kBatch];
 #pragma unroll
       for (int i = 0; i < kBatch; ++i) {
         const int s = x0 + i * ev::kThreads;
-        on[i] = s < keep && ((words[s / 32] >> (s % 32)) & 1u);
+        on[i] = s < end && ((words[(s - s0) / 32] >> (s % 32)) & 1u);
         wt[i] = on[i] && copy_weight ? weight[s] : 0.0f;
         ps[i] = on[i] && copy_pos ? pos[s] : 0;
       }
@@ -382,12 +455,12 @@ __global__ void __launch_bounds__(ev::kThreads) cache_select_kernel(const __grid
       }
     }
   }
-  for (int x0 = tid; x0 < total; x0 += kBatch * ev::kThreads) {
+  for (int x0 = thread; x0 < total; x0 += kBatch * threads) {
     int2 m[kBatch];
     float wt[kBatch];
     int32_t ps[kBatch];
 #pragma unroll
-    for (int i = 0; i < kBatch; ++i) m[i] = x0 + i * ev::kThreads < total ? moves[x0 + i * ev::kThreads] : make_int2(0, 0);
+    for (int i = 0; i < kBatch; ++i) m[i] = x0 + i * threads < total ? moves[x0 + i * threads] : make_int2(0, 0);
 #pragma unroll
     for (int i = 0; i < kBatch; ++i) {
       wt[i] = weight[m[i].x];
@@ -395,7 +468,7 @@ __global__ void __launch_bounds__(ev::kThreads) cache_select_kernel(const __grid
     }
 #pragma unroll
     for (int i = 0; i < kBatch; ++i) {
-      const int x = x0 + i * ev::kThreads;
+      const int x = x0 + i * threads;
       if (x >= total) break;
       a.weight_out[base + m[i].y] = wt[i];
       if (a.pos_out != nullptr) a.pos_out[base + m[i].y] = ps[i];
@@ -471,17 +544,16 @@ namespace gemm_tn_impl {
 namespace {
 
 template <class... Params, class... Args>
-cudaError_t launch(void (*kernel)(Params...), dim3 grid, int threads, size_t smem, cudaStream_t stream, Args... args) {
+cudaError_t launch(void (*kernel)(Params...), dim3 grid, int threads, size_t smem, int cluster, cudaStream_t stream,
+                   Args... args) {
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = grid;
   cfg.blockDim = dim3(static_cast<unsigned>(threads), 1, 1);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = stream;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchAttribute attr[2];
   cfg.attrs = attr;
-  cfg.numAttrs = dependent_launch_enabled() ? 1 : 0;
+  cfg.numAttrs = cache_launch_attributes(attr, cluster);
   return cudaLaunchKernelEx(&cfg, kernel, args...);
 }
 
@@ -491,15 +563,15 @@ cudaError_t launch_cache_append(const gemm_tn_dev::AppendArgs& a, cudaStream_t s
   const int64_t threads = static_cast<int64_t>(a.c.batch) * a.max_rows * a.c.kv_heads * a.c.vec;
   // lens_out and seen_out may be written here only if no block reads them
   const int write_lens = a.lens_out != a.lens && (a.seen_out == nullptr || a.seen_out != a.seen) ? 1 : 0;
-  return launch(gemm_tn_dev::cache_append_kernel, dim3(static_cast<unsigned>((threads + 255) / 256), 1, 1), 256, 0, stream,
+  return launch(gemm_tn_dev::cache_append_kernel, dim3(static_cast<unsigned>((threads + 255) / 256), 1, 1), 256, 0, 1, stream,
                 a, write_lens);
 }
 
 cudaError_t launch_cache_advance(const gemm_tn_dev::AppendArgs& a, cudaStream_t stream) {
-  return launch(gemm_tn_dev::cache_advance_kernel, dim3(static_cast<unsigned>((a.c.batch + 255) / 256), 1, 1), 256, 0, stream, a);
+  return launch(gemm_tn_dev::cache_advance_kernel, dim3(static_cast<unsigned>((a.c.batch + 255) / 256), 1, 1), 256, 0, 1, stream, a);
 }
 
-int evict_smem_keys(int capacity) { return std::min(capacity, gemm_tn_dev::ev::kSmemKeys); }
+int evict_smem_keys(int slots) { return std::min(slots, gemm_tn_dev::ev::kSmemKeys); }
 
 int evict_fused_moves() { return gemm_tn_dev::ev::kFusedMoves; }
 
@@ -516,8 +588,8 @@ static cudaError_t launch_select(const gemm_tn_dev::EvictArgs& a, cudaStream_t s
     if (e != cudaSuccess) return e;
     done_mask.fetch_or(bit, std::memory_order_acq_rel);
   }
-  return launch(gemm_tn_dev::cache_select_kernel<kFused>, dim3(static_cast<unsigned>(a.c.batch * a.c.kv_heads), 1, 1),
-                gemm_tn_dev::ev::kThreads, static_cast<size_t>(a.smem_keys) * 4, stream, a);
+  return launch(gemm_tn_dev::cache_select_kernel<kFused>, dim3(static_cast<unsigned>(a.c.batch * a.c.kv_heads * a.spread), 1, 1),
+                gemm_tn_dev::ev::kThreads, static_cast<size_t>(a.smem_keys) * 4, a.spread, stream, a);
 }
 
 cudaError_t launch_cache_select(const gemm_tn_dev::EvictArgs& a, cudaStream_t stream) {
@@ -530,7 +602,7 @@ cudaError_t launch_cache_move(const gemm_tn_dev::EvictArgs& a, int num_sms, cuda
   const int most = std::max(1, (a.max_moves + per_block - 1) / per_block);
   const int per_list = std::min(most, std::max(1, (num_sms * 8 + lists - 1) / lists));
   return launch(gemm_tn_dev::cache_move_kernel,
-                dim3(static_cast<unsigned>(per_list), static_cast<unsigned>(std::min(lists, 65535)), 1), 256, 0, stream, a);
+                dim3(static_cast<unsigned>(per_list), static_cast<unsigned>(std::min(lists, 65535)), 1), 256, 0, 1, stream, a);
 }
 
 }  // namespace gemm_tn_impl

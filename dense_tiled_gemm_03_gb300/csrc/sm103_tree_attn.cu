@@ -825,7 +825,7 @@ cudaError_t launch_cfg(const gemm_tn_dev::TreeArgs& args, cudaStream_t stream) {
   cfg.stream = stream;
   cudaLaunchAttribute attr[2];
   cfg.attrs = attr;
-  cfg.numAttrs = attn_launch_attributes(attr, args.spread);
+  cfg.numAttrs = cache_launch_attributes(attr, args.spread);
   return cudaLaunchKernelEx(&cfg, gemm_tn_dev::tree_attn_kernel<C>, args);
 }
 

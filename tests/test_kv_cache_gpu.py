@@ -516,6 +516,18 @@ def test_evict_a_sequence_longer_than_shared_memory_holds():
     check_evict(s, 20001, 100, False)
 
 
+@pytest.mark.parametrize("lens,kv_heads,keep,recent,odd", [
+    ([17000, 30, 9000], 2, 5000, 64, True), ([17000, 16300], 1, 8191, 0, True), ([16500, 40, 5001], 1, 5000, 100, False),
+    ([17000] + [90, 0, 200] * 8, 3, 77, 5, True), ([70001], 1, 40000, 33, False), ([170000], 1, 90001, 64, True)])
+def test_evict_lists_shared_by_a_cluster(lens, kv_heads, keep, recent, odd):
+    """Ties and the newest slots spread over several blocks, blocks without slots, and more slots a block than its shared memory holds."""
+    s = ref.make("bf16", 64, lens, 1, kv_heads, 1, 128, seed=keep)
+    if odd:
+        few = torch.tensor([0.0, -0.0, 0.5, 0.25, 2.0, float("nan"), -1.0, float("inf")])
+        s.weight = few[torch.randint(0, len(few), s.weight.shape, generator=torch.Generator().manual_seed(4))]
+    check_evict(s, keep, recent, keep % 2 == 0)
+
+
 def test_evict_without_positions():
     s = ref.make("fp16", 64, [60], 1, 2, 1, 16, seed=42)
     k, v, weight, _, lens = ref.evict(s, 30, 0)
