@@ -550,11 +550,10 @@ __global__ void __launch_bounds__(C::kNumThreads, 1) decode_attn_kernel(const __
       {
         const float sum = da::warp_rows<C::kRows>(l, lane, [](float p, float q) { return p + q; });
         if (lane < C::kRows) warp_sums[(u * 4 + static_cast<int>(quarter)) * 32 + static_cast<int>(lane)] = sum;
-        if (quarter == 0) {
+        float neg = 0.0f;   // lane r: row r's (selected, not stored under a branch a row: those took 1 us)
 #pragma unroll
-          for (int r = 0; r < C::kRows; ++r)
-            if (lane == static_cast<uint32_t>(r)) unit_refs[u * 32 + r] = -neg_m[r];
-        }
+        for (int r = 0; r < C::kRows; ++r) neg = lane == static_cast<uint32_t>(r) ? neg_m[r] : neg;
+        if (quarter == 0 && lane < C::kRows) unit_refs[u * 32 + static_cast<int>(lane)] = -neg;
         const bool both = w.count > 1;
         if (u < w.count) {
           if (!(ok = wd.warp_wait(o_done(u), ends[u] & 1u))) break;
