@@ -78,8 +78,8 @@ struct Cfg {
   static constexpr uint32_t kOffVote = kOffBar + 8u * kNumBars;     // [2 units][3]
   static constexpr uint32_t kOffTmemSlot = kOffVote + 24u;
   static constexpr uint32_t kOffAbort = kOffTmemSlot + 4u;
-  static constexpr uint32_t kOffStart = kOffAbort + 4u;   // the chunk's first Walk
-  static constexpr uint32_t kOffWalkSums = kOffStart + 36u;
+  static constexpr uint32_t kOffStart = kOffAbort + 4u;   // the chunk's first Walk, the second; then the segments' in turn
+  static constexpr uint32_t kOffWalkSums = kOffStart + 72u;
   static constexpr uint32_t kSmemBytes = kOffWalkSums + 128u + 1024u;   // + slack to align the base to 1024
   static constexpr uint32_t kTmemCols = 4 * kRows;        // S_0, S_1, O_0, O_1
   static constexpr uint32_t kIdescS = mma_idesc_f16(kBf16, kTileKeys, kRows, false);
@@ -416,7 +416,14 @@ __global__ void __launch_bounds__(C::kNumThreads, 1) decode_attn_kernel(const __
       if (lane == 0) mbar_arrive(agree(u));
       return wd.warp_wait(agree(u), agreed++ & 1u);
     };
-    for (; ok && w.more(); it0 += w.count, w.next(args), ++segs) {
+    for (; ok && w.more(); it0 += w.count, ++segs, w = start_walk[segs & 1u]) {
+      if (u == 0 && quarter == 0) {
+        // the next segment's, worked out by one warp while the first scores are
+        // awaited; the exchange at the end of the segment hands it to the others
+        ta::Walk next = w;
+        next.next(args);
+        if (lane == 0) start_walk[(segs + 1u) & 1u] = next;
+      }
       const int rows = w.tl * args.group;   // rows that exist, token-major
       const uint32_t row_bits = cache::low_bits(rows);
       uint32_t unset = row_bits;            // rows that have seen no key yet
