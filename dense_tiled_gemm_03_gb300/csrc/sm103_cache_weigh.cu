@@ -303,55 +303,63 @@ __global__ void __launch_bounds__(C::kNumThreads, 1) cache_weigh_kernel(const __
         // every sum warp is done with the block before: between them they have
         // seen all its products complete, read its rows' references and written its weights
         if (!(ok = wd.warp_wait(q_free, (static_cast<uint32_t>(q_blocks) & 1u) ^ 1u))) break;
-        // query rows -> shared memory, K-major with the 128-byte swizzle
-        // (four pieces a thread at a time: their loads are in flight together)
+        // query rows -> shared memory, K-major with the 128-byte swizzle, four or
+        // eight pieces a thread at a time: their loads are in flight together
+        // (eight where four would take two rounds: 128 rows of dim 128 over 8
+        // sequences of up to 16384 slots 44.5 -> 44.0 us; eight always makes 32
+        // rows 1 to 12% slower, whose code it lengthens)
         constexpr int kPieces = C::kDim / 8;   // 16-byte pieces per row
-        constexpr int kBatch = 4, kRowStep = 32 * cw::kSumWarps / kPieces;
+        constexpr int kRowStep = 32 * cw::kSumWarps / kPieces;
         const int piece = sum_thread % kPieces;
-        for (int row0 = sum_thread / kPieces; row0 < cols; row0 += kBatch * kRowStep) {
-          int token[kBatch], head[kBatch];
-          uint4 v[kBatch];
-          float lse[kBatch];
+        auto gather = [&](auto batch) {
+          constexpr int kBatch = batch.value;
+          for (int row0 = sum_thread / kPieces; row0 < cols; row0 += kBatch * kRowStep) {
+            int token[kBatch], head[kBatch];
+            uint4 v[kBatch];
+            float lse[kBatch];
 #pragma unroll
-          for (int x = 0; x < kBatch; ++x) {
-            const int row = row0 + x * kRowStep, i = row / args.group;
-            head[x] = w.h * args.group + row - i * args.group;
-            token[x] = first_row + i;
-            if (row >= rows) token[x] = -1;
-            else if (args.rows != nullptr) {
-              token[x] = __ldg(args.rows + static_cast<int64_t>(w.b) * args.max_rows + token[x]);
-              if (token[x] < 0 || token[x] >= args.tokens) {
-                cache::report(args.status, cache::kStatusInvalid);
-                token[x] = -1;
+            for (int x = 0; x < kBatch; ++x) {
+              const int row = row0 + x * kRowStep, i = row / args.group;
+              head[x] = w.h * args.group + row - i * args.group;
+              token[x] = first_row + i;
+              if (row >= rows) token[x] = -1;
+              else if (args.rows != nullptr) {
+                token[x] = __ldg(args.rows + static_cast<int64_t>(w.b) * args.max_rows + token[x]);
+                if (token[x] < 0 || token[x] >= args.tokens) {
+                  cache::report(args.status, cache::kStatusInvalid);
+                  token[x] = -1;
+                }
+              }
+            }
+#pragma unroll
+            for (int x = 0; x < kBatch; ++x) {
+              v[x] = make_uint4(0u, 0u, 0u, 0u);
+              lse[x] = INFINITY;   // rows that do not count weigh nothing
+              if (token[x] >= 0) {
+                v[x] = __ldg(reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(args.q) + w.b * args.q_batch +
+                                                            token[x] * args.q_token + head[x] * args.q_head) + piece);
+                if (piece == 0)
+                  lse[x] = __ldg(args.lse + (static_cast<int64_t>(w.b) * args.tokens + token[x]) * args.heads + head[x]);
+              }
+            }
+#pragma unroll
+            for (int x = 0; x < kBatch; ++x) {
+              const int row = row0 + x * kRowStep;
+              if (row >= cols) break;
+              st_shared_v4(base + C::kOffQ + (piece / 8) * C::kQBoxBytes + row * 128u + (((piece & 7) ^ (row & 7)) * 16u),
+                           v[x].x, v[x].y, v[x].z, v[x].w);
+              if (piece == 0) {
+                // lse * log2e as a rounded part and the factor that makes up for the rounding
+                const float hi = lse[x] * cw::kLog2e;
+                const float lo = fmaf(lse[x], cw::kLog2e, -hi);
+                row_ref[row] = isinf(hi) ? -INFINITY : -hi;
+                row_factor[row] = isinf(hi) ? 0.0f : ex2_approx(-lo);
               }
             }
           }
-#pragma unroll
-          for (int x = 0; x < kBatch; ++x) {
-            v[x] = make_uint4(0u, 0u, 0u, 0u);
-            lse[x] = INFINITY;   // rows that do not count weigh nothing
-            if (token[x] >= 0) {
-              v[x] = __ldg(reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(args.q) + w.b * args.q_batch +
-                                                          token[x] * args.q_token + head[x] * args.q_head) + piece);
-              if (piece == 0)
-                lse[x] = __ldg(args.lse + (static_cast<int64_t>(w.b) * args.tokens + token[x]) * args.heads + head[x]);
-            }
-          }
-#pragma unroll
-          for (int x = 0; x < kBatch; ++x) {
-            const int row = row0 + x * kRowStep;
-            if (row >= cols) break;
-            st_shared_v4(base + C::kOffQ + (piece / 8) * C::kQBoxBytes + row * 128u + (((piece & 7) ^ (row & 7)) * 16u),
-                         v[x].x, v[x].y, v[x].z, v[x].w);
-            if (piece == 0) {
-              // lse * log2e as a rounded part and the factor that makes up for the rounding
-              const float hi = lse[x] * cw::kLog2e;
-              const float lo = fmaf(lse[x], cw::kLog2e, -hi);
-              row_ref[row] = isinf(hi) ? -INFINITY : -hi;
-              row_factor[row] = isinf(hi) ? 0.0f : ex2_approx(-lo);
-            }
-          }
-        }
+        };
+        if (cols > 4 * kRowStep) gather(std::integral_constant<int, 8>{});
+        else gather(std::integral_constant<int, 4>{});
         fence_proxy_async_shared();
         __syncwarp();
         if (lane == 0) mbar_arrive(q_full);
