@@ -160,18 +160,16 @@ constexpr int kMinChunk = 2;
 // 35.0 and 34.2; one token, 2 sequences of 8192 24.2 and 22.5, 64 of up to 8192
 // 190.5 and 190.0.
 int change_tiles(int units) { return units + 1; }
-constexpr int kMaxChange = 7;   // of this and of weigh_change_tiles
+constexpr int kMaxChange = 8;   // of this and of weigh_change_tiles
 
-// The same for the accumulated weights, where a change of items ends with the
-// gathering of `rows` query rows (past 256 a tile is walked once per 256, and the
-// change is worth fewer of them). GB300, us a call with gaps of 0, 3, 6 and 10: 1
-// row per KV head, 32 sequences of up to 2048 slots 24.2, 22.9, 23.5 and 25.2; 64
-// rows, 8 of up to 8192 23.6, 22.8, 22.4 and 22.9; 128 rows, 8 of up to 16384
-// 46.1, 45.0, 43.9 and 43.5; 700 rows, 2 of up to 4000 38.1, 37.9, 37.9 and 40.8.
-int weigh_change_tiles(int64_t rows) {
-  if (rows > 256) return 4;
-  return 3 + static_cast<int>((std::min<int64_t>(std::max<int64_t>(rows, 1), 160) - 1) / 32);
-}
+// The same for the accumulated weights. Up to 128 query rows are gathered ahead;
+// more of them between the items (past 256 a tile is walked once per 256, and the
+// change is worth fewer of them). GB300, us a call with gaps of 0, 2, 4 and 8: 1
+// row per KV head, 32 sequences of up to 2048 slots 23.4, 23.0, 23.5 and 24.4; 128
+// rows, 8 of up to 16384 43.9, 43.6, 43.9 and 44.6, 2 of 8192 14.4, 13.3, 13.8 and
+// 13.9; 256 rows, 8 of up to 8192 46.1, 45.2, 43.8 and 40.8; 700 rows, 2 of up to
+// 4000 38.6, 38.4, 38.5 and 41.0.
+int weigh_change_tiles(int64_t rows) { return rows <= 128 ? 2 : (rows <= 256 ? 8 : 4); }
 
 // CTAs of a cluster that share each of `items` items of `tiles` key tiles, one
 // row tile wide: as many as the tiles keep busy and as find room at once (15

@@ -65,6 +65,24 @@ struct Watch {
     return __all_sync(0xffffffffu, wait(bar, parity));
   }
 
+  // The same where nothing is late for a while: asks every half a microsecond, and
+  // leaves the issue slots to the warps that share them.
+  __device__ __forceinline__ bool patient_wait(uint32_t bar, uint32_t parity) const {
+    const uint64_t deadline = globaltimer_ns() + timeout_ns;
+    bool ok = true;
+    while (ok && !mbar_try_wait<false, false>(bar, parity)) {
+      __nanosleep(500);
+      if (*abort_flag) {
+        ok = false;
+      } else if (globaltimer_ns() > deadline) {
+        report(status, kStatusTimeout);
+        *abort_flag = 1u;
+        ok = false;
+      }
+    }
+    return __all_sync(0xffffffffu, ok);
+  }
+
   // Bounded wait while draining after a failure; never raises the flag.
   __device__ __forceinline__ bool drain(uint32_t bar, uint32_t parity) const {
     const uint64_t deadline = globaltimer_ns() + timeout_ns;

@@ -43,6 +43,14 @@ __device__ __forceinline__ int2 ld_cluster_s2(uint32_t cluster_addr) {
   return v;
 }
 
+// A copy of 16 bytes to this CTA's shared memory, which runs on while the thread
+// does other things.
+__device__ __forceinline__ void cp_async_16(uint32_t dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" :: "r"(dst), "l"(src) : "memory");
+}
+// Waits for this thread's copies.
+__device__ __forceinline__ void cp_async_wait_all() { asm volatile("cp.async.wait_all;" ::: "memory"); }
+
 __device__ __forceinline__ void st_shared_u16(uint32_t addr, uint16_t v) {
   asm volatile("st.shared.u16 [%0], %1;" :: "r"(addr), "h"(v) : "memory");
 }

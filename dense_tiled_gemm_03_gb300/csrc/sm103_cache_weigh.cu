@@ -14,20 +14,23 @@
 // Keys are read once (dim * 2 bytes each) per 256 query rows against one
 // exponential per key and row: up to about 150 rows HBM bounds the kernel,
 // past that the exponentials do. GB300: 32 tokens of 32 heads over 8 KV heads
-// (128 rows), dim 128, 8 sequences of 9001 to 16384 slots, 231 MB: 44.5 us, 5.2
-// TB/s; one token of 16 heads of dim 64, 4 sequences of 300 to 1024 slots: 6.9.
+// (128 rows), dim 128, 8 sequences of 9001 to 16384 slots, 231 MB: 43.6 us, 5.3
+// TB/s; one token of 16 heads of dim 64, 4 sequences of 300 to 1024 slots: 7.2.
 //
 // Work: an item is (sequence, KV head); the items' 128-key tiles, laid end to end
 // a change of items apart, are cut into equal contiguous chunks, one per CTA
-// (sm103_cache.cuh). Per segment of an
-// item the query rows come in blocks of at most 256, each block walking the
-// segment's tiles.
+// (sm103_cache.cuh). Per segment of an item the query rows come in blocks of at
+// most 256, each block walking the segment's tiles.
 //   warp 0      TMA producer (lane l copies the tile's l-th page)
 //   warp 1      MMA issuer: S^T (128 keys x up to 128 rows) into one of the two
 //               TMEM buffers of the group that takes the tile, so that the next
 //               product runs while the group sums the one before
-//   warps 2-9   two groups of four taking every other tile; all eight gather
-//               the block's query rows into shared memory first
+//   warps 2-9   two groups of four taking every other tile; all eight gather a
+//               block's query rows into shared memory first, but
+//   warp 10     gathers those of blocks of up to 128 rows behind another such: these
+//               lie in the buffer's halves in turn, and are there when the block
+//               before ends (in between, the gathering's two round trips to memory
+//               stand still for 4 us: 40 sequences of up to 1000 slots 29.5 -> 23.5)
 #include <cuda.h>
 #include <cuda_runtime.h>
 
@@ -47,6 +50,7 @@ constexpr int kProducerWarp = 0;
 constexpr int kMmaWarp = 1;
 constexpr int kFirstSumWarp = 2;
 constexpr int kSumWarps = 8;
+constexpr int kGatherWarp = kFirstSumWarp + kSumWarps;
 constexpr int kMaxRows = 256;      // query rows per block
 constexpr int kHalf = 128;         // query rows per product (columns of one of the four TMEM buffers)
 constexpr float kLog2e = 1.4426950408889634f;
@@ -55,7 +59,7 @@ template <int kDim_, bool kBf16_>
 struct Cfg {
   static constexpr int kDim = kDim_;
   static constexpr bool kBf16 = kBf16_;
-  static constexpr int kNumThreads = 64 + 32 * kSumWarps;
+  static constexpr int kNumThreads = 32 * (kGatherWarp + 1);
   static constexpr int kDimBoxes = kDim / 64;
   static constexpr uint32_t kBoxBytes = 128u * 128u;        // 128 keys x 128 bytes
   static constexpr uint32_t kTileBytes = kDimBoxes * kBoxBytes;
@@ -64,8 +68,8 @@ struct Cfg {
   static constexpr uint32_t kOffQ = 0;
   static constexpr uint32_t kOffK = kOffQ + kDimBoxes * kQBoxBytes;
   static constexpr uint32_t kOffLse = kOffK + kStages * kTileBytes;   // [256] -log2e lse, rounded; [256] 2^ what that left
-  // q_full, q_free, k_full[S], k_empty[S], s_full[2][2], s_empty[2][2], drain
-  static constexpr int kNumBars = 2 + 2 * kStages + 8 + 1;
+  // q_full[2], q_free[2], k_full[S], k_empty[S], s_full[2][2], s_empty[2][2], drain
+  static constexpr int kNumBars = 4 + 2 * kStages + 8 + 1;
   static constexpr uint32_t kOffBar = kOffLse + 8u * kMaxRows;
   static constexpr uint32_t kOffTmemSlot = kOffBar + 8u * kNumBars;
   static constexpr uint32_t kOffAbort = kOffTmemSlot + 4u;
@@ -84,6 +88,27 @@ __device__ __forceinline__ int cached_len(const WeighArgs& a, int b) {
 __device__ __forceinline__ int row_count(const WeighArgs& a, int b) {
   return a.counts == nullptr ? a.max_rows : min(max(__ldg(a.counts + b), 0), a.max_rows);
 }
+
+// Which of the query buffer's halves the blocks take: those of up to 128 rows one
+// in turn, wider ones both. Every role that uses the buffer keeps one of these.
+// (One word: it lives across the tile loop, which has no registers to spare.)
+struct Halves {
+  // bits 0, 1: parity of the blocks that have taken each half; 2: whose turn it
+  // is; 3: the block at hand is wide (as none is before the first); 4: the one before was
+  uint32_t state = 8u;
+
+  __device__ __forceinline__ void take(int cols) {
+    state = (state & 7u) | (cols > kHalf ? 8u : 0u) | ((state & 8u) << 1);
+  }
+  __device__ __forceinline__ bool wide() const { return (state & 8u) != 0; }
+  __device__ __forceinline__ int turn() const { return static_cast<int>(state >> 2) & 1; }
+  __device__ __forceinline__ int first() const { return wide() ? 0 : turn() * kHalf; }   // buffer row
+  __device__ __forceinline__ bool has(int half) const { return wide() || half == turn(); }
+  __device__ __forceinline__ uint32_t phase(int half) const { return (state >> half) & 1u; }
+  // Whether the block's half is free while the block before is used.
+  __device__ __forceinline__ bool ahead() const { return (state & 24u) == 0; }
+  __device__ __forceinline__ void leave() { state ^= wide() ? 3u : 4u | (1u << turn()); }
+};
 
 // Walks a chunk: runs of one (sequence, KV head)'s key tiles.
 struct Walk {
@@ -142,12 +167,13 @@ __global__ void __launch_bounds__(C::kNumThreads, 1) cache_weigh_kernel(const __
 
   auto k_tile = [&](int s) { return base + C::kOffK + s * C::kTileBytes; };
   auto bar = [&](int i) { return base + C::kOffBar + 8u * i; };
-  const uint32_t q_full = bar(0), q_free = bar(1);
-  auto k_full = [&](int s) { return bar(2 + s); };
-  auto k_empty = [&](int s) { return bar(2 + C::kStages + s); };
-  auto s_full = [&](int g, int buf) { return bar(2 + 2 * C::kStages + 2 * g + buf); };
-  auto s_empty = [&](int g, int buf) { return bar(6 + 2 * C::kStages + 2 * g + buf); };
-  const uint32_t drain_bar = bar(10 + 2 * C::kStages);
+  auto q_full = [&](int half) { return bar(half); };
+  auto q_free = [&](int half) { return bar(2 + half); };
+  auto k_full = [&](int s) { return bar(4 + s); };
+  auto k_empty = [&](int s) { return bar(4 + C::kStages + s); };
+  auto s_full = [&](int g, int buf) { return bar(4 + 2 * C::kStages + 2 * g + buf); };
+  auto s_empty = [&](int g, int buf) { return bar(8 + 2 * C::kStages + 2 * g + buf); };
+  const uint32_t drain_bar = bar(12 + 2 * C::kStages);
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + C::kOffTmemSlot);
   volatile uint32_t* abort_flag = reinterpret_cast<volatile uint32_t*>(smem + C::kOffAbort);
   cw::Walk* start_walk = reinterpret_cast<cw::Walk*>(smem + C::kOffStart);
@@ -156,8 +182,10 @@ __global__ void __launch_bounds__(C::kNumThreads, 1) cache_weigh_kernel(const __
   float* row_factor = row_ref + cw::kMaxRows;
 
   if (threadIdx.x == 0) {
-    mbar_init(q_full, cw::kSumWarps);
-    mbar_init(q_free, cw::kSumWarps);
+    for (int half = 0; half < 2; ++half) {
+      mbar_init(q_full(half), cw::kSumWarps + 1);   // whoever gathers, all of them arrive
+      mbar_init(q_free(half), cw::kSumWarps);
+    }
     for (int s = 0; s < C::kStages; ++s) {
       mbar_init(k_full(s), 1);
       mbar_init(k_empty(s), 1);
@@ -246,14 +274,16 @@ __global__ void __launch_bounds__(C::kNumThreads, 1) cache_weigh_kernel(const __
       // (the whole warp runs this, one lane issues)
       const uint32_t leader = elect_one();
       int it = 0;       // tiles issued
-      int q_blocks = 0;
+      cw::Halves halves;
       int used[2] = {0, 0};   // products of each group so far
       bool ok = true;
       for (; ok && w.more(); w.next(args)) {
         const int blocks = w.blocks(args);
-        for (int block = 0; ok && block < blocks; ++block, ++q_blocks) {
+        for (int block = 0; ok && block < blocks; ++block, halves.leave()) {
           const int cols = max(1, (w.block_rows(args, block) + 31) / 32) * 32;
-          if (!(ok = wd.warp_wait(q_full, static_cast<uint32_t>(q_blocks) & 1u))) break;
+          halves.take(cols);
+          for (int half = 0; half < 2 && ok; ++half)
+            if (halves.has(half)) ok = wd.warp_wait(q_full(half), halves.phase(half));
           for (int j = 0; ok && j < w.count; ++j, ++it) {
             const int s = it % C::kStages, g = it & 1;
             if (!(ok = wd.warp_wait(k_full(s), static_cast<uint32_t>(it / C::kStages) & 1u))) break;
@@ -266,7 +296,7 @@ __global__ void __launch_bounds__(C::kNumThreads, 1) cache_weigh_kernel(const __
 #pragma unroll
               for (int c = 0; c < C::kDimBoxes; ++c) {
                 const uint64_t a_desc = sw128_kmajor_desc(k_tile(s) + c * C::kBoxBytes);
-                const uint64_t b_desc = sw128_kmajor_desc(base + C::kOffQ + c * C::kQBoxBytes + static_cast<uint32_t>(c0) * 128u);
+                const uint64_t b_desc = sw128_kmajor_desc(base + C::kOffQ + c * C::kQBoxBytes + static_cast<uint32_t>(halves.first() + c0) * 128u);
 #pragma unroll
                 for (int kk = 0; kk < 4; ++kk)
                   mma_f16_warp(leader, t_s, a_desc + 2u * kk, b_desc + 2u * kk, idesc, (c | kk) != 0 ? 1u : 0u);
@@ -282,6 +312,83 @@ __global__ void __launch_bounds__(C::kNumThreads, 1) cache_weigh_kernel(const __
       mma_commit_warp(leader, drain_bar);
       wd.drain(drain_bar, 0);
     }
+  } else if (warp == cw::kGatherWarp) {
+    // -------------------------------------------------------------- query rows
+    // K-major with the 128-byte swizzle. A lane looks up the rows of its number,
+    // four at a time; the warp then copies them, 16 bytes a lane.
+    constexpr int kPieces = C::kDim / 8;   // 16-byte pieces per row
+    constexpr int kAtOnce = 32 / kPieces;  // rows that the warp copies at a time
+    const int piece = static_cast<int>(lane) % kPieces, sub = static_cast<int>(lane) / kPieces;
+    cw::Halves halves;
+    bool ok = true;
+    for (; ok && w.more(); w.next(args)) {
+      const int blocks = w.blocks(args);
+      const uint16_t* q = static_cast<const uint16_t*>(args.q) + w.b * args.q_batch + w.h * args.group * args.q_head + 8 * piece;
+      for (int block = 0; ok && block < blocks; ++block, halves.leave()) {
+        const int rows = w.block_rows(args, block);
+        const int cols = max(1, (rows + 31) / 32) * 32;
+        halves.take(cols);
+        for (int half = 0; half < 2 && ok; ++half)   // every sum warp is done with the block that was there
+          if (halves.has(half)) ok = wd.patient_wait(q_free(half), halves.phase(half) ^ 1u);
+        if (!ok) break;
+        if (halves.ahead()) {   // at most 128 rows
+          int token[4];
+          int64_t from[4];   // where the row begins, in elements; -1: a row that does not count
+          float lse[4];
+#pragma unroll
+          for (int x = 0; x < 4; ++x) {
+            const int row = 32 * x + static_cast<int>(lane);
+            token[x] = -1;
+            if (row < rows) {
+              token[x] = block * args.block_tokens + row / args.group;   // of the counted tokens
+              if (args.rows != nullptr) token[x] = __ldg(args.rows + static_cast<int64_t>(w.b) * args.max_rows + token[x]);
+            }
+          }
+#pragma unroll
+          for (int x = 0; x < 4; ++x) {
+            const int row = 32 * x + static_cast<int>(lane), head = row % args.group;
+            from[x] = -1;
+            lse[x] = INFINITY;   // rows that do not count weigh nothing
+            if (row < rows) {
+              if (token[x] < 0 || token[x] >= args.tokens) {
+                cache::report(args.status, cache::kStatusInvalid);
+              } else {
+                from[x] = token[x] * args.q_token + head * args.q_head;
+                lse[x] = __ldg(args.lse + (static_cast<int64_t>(w.b) * args.tokens + token[x]) * args.heads + w.h * args.group + head);
+              }
+            }
+          }
+#pragma unroll
+          for (int x = 0; x < 4; ++x) {
+            if (32 * x >= cols) break;
+#pragma unroll 4
+            for (int r = sub; r < 32; r += kAtOnce) {
+              const int64_t at = __shfl_sync(0xffffffffu, from[x], r);
+              const int row = halves.first() + 32 * x + r;
+              const uint32_t to = base + C::kOffQ + (piece / 8) * C::kQBoxBytes + row * 128u + (((piece & 7) ^ (row & 7)) * 16u);
+              if (at >= 0) cp_async_16(to, q + at);
+              else st_shared_v4(to, 0u, 0u, 0u, 0u);
+            }
+          }
+#pragma unroll
+          for (int x = 0; x < 4; ++x) {
+            if (32 * x >= cols) break;
+            // lse * log2e as a rounded part and the factor that makes up for the rounding
+            const int row = halves.first() + 32 * x + static_cast<int>(lane);
+            const float hi = lse[x] * cw::kLog2e;
+            const float lo = fmaf(lse[x], cw::kLog2e, -hi);
+            row_ref[row] = isinf(hi) ? -INFINITY : -hi;
+            row_factor[row] = isinf(hi) ? 0.0f : ex2_approx(-lo);
+          }
+        }
+        cp_async_wait_all();
+        fence_proxy_async_shared();
+        __syncwarp();
+        if (lane == 0)
+          for (int half = 0; half < 2; ++half)
+            if (halves.has(half)) mbar_arrive(q_full(half));
+      }
+    }
   } else {
     // -------------------------------------------------------------- sums
     const int g = (static_cast<int>(warp) - cw::kFirstSumWarp) >> 2;   // group: tiles it & 1 == g
@@ -290,80 +397,92 @@ __global__ void __launch_bounds__(C::kNumThreads, 1) cache_weigh_kernel(const __
     const uint32_t t_s = tmem_base + ((quarter * 32u) << 16) + 256u * static_cast<uint32_t>(g);
     const float c_log2 = args.scale_log2;
     const int sum_thread = static_cast<int>(threadIdx.x) - 64;
-    int it = 0, q_blocks = 0;
+    cw::Halves halves;
+    int it = 0;
     int used = 0;   // products of this group so far
     bool ok = true;
     for (; ok && w.more(); w.next(args)) {
       const int blocks = w.blocks(args);
       const int64_t weight_row = (static_cast<int64_t>(w.b) * args.kv_heads + w.h) * args.capacity;
-      for (int block = 0; ok && block < blocks; ++block, ++q_blocks) {
-        const int rows = w.block_rows(args, block);
-        const int cols = max(1, (rows + 31) / 32) * 32;
+      for (int block = 0; ok && block < blocks; ++block, halves.leave()) {
+        const int cols = max(1, (w.block_rows(args, block) + 31) / 32) * 32;
         const int first_row = block * args.block_tokens;   // of the counted tokens
-        // every sum warp is done with the block before: between them they have
-        // seen all its products complete, read its rows' references and written its weights
-        if (!(ok = wd.warp_wait(q_free, (static_cast<uint32_t>(q_blocks) & 1u) ^ 1u))) break;
-        // query rows -> shared memory, K-major with the 128-byte swizzle, four or
-        // eight pieces a thread at a time: their loads are in flight together
-        // (eight where four would take two rounds: 128 rows of dim 128 over 8
-        // sequences of up to 16384 slots 44.5 -> 44.0 us; eight always makes 32
-        // rows 1 to 12% slower, whose code it lengthens)
-        constexpr int kPieces = C::kDim / 8;   // 16-byte pieces per row
-        constexpr int kRowStep = 32 * cw::kSumWarps / kPieces;
-        const int piece = sum_thread % kPieces;
-        auto gather = [&](auto batch) {
-          constexpr int kBatch = batch.value;
-          for (int row0 = sum_thread / kPieces; row0 < cols; row0 += kBatch * kRowStep) {
-            int token[kBatch], head[kBatch];
-            uint4 v[kBatch];
-            float lse[kBatch];
+        halves.take(cols);
+        const bool ahead = halves.ahead();
+        if (!ahead) {
+          // every sum warp is done with the block that was there: between them they
+          // have seen all its products complete and read its rows' references
+          for (int half = 0; half < 2 && ok; ++half)
+            if (halves.has(half)) ok = wd.warp_wait(q_free(half), halves.phase(half) ^ 1u);
+          if (!ok) break;
+          const int rows = w.block_rows(args, block);
+          // query rows -> shared memory, K-major with the 128-byte swizzle, four or
+          // eight pieces a thread at a time: their loads are in flight together
+          // (eight where four would take two rounds: 128 rows of dim 128 over 8
+          // sequences of up to 16384 slots 44.5 -> 44.0 us; eight always makes 32
+          // rows 1 to 12% slower, whose code it lengthens)
+          constexpr int kPieces = C::kDim / 8;   // 16-byte pieces per row
+          constexpr int kRowStep = 32 * cw::kSumWarps / kPieces;
+          const int piece = sum_thread % kPieces;
+          auto gather = [&](auto batch) {
+            constexpr int kBatch = batch.value;
+            for (int row0 = sum_thread / kPieces; row0 < cols; row0 += kBatch * kRowStep) {
+              int token[kBatch], head[kBatch];
+              uint4 v[kBatch];
+              float lse[kBatch];
 #pragma unroll
-            for (int x = 0; x < kBatch; ++x) {
-              const int row = row0 + x * kRowStep, i = row / args.group;
-              head[x] = w.h * args.group + row - i * args.group;
-              token[x] = first_row + i;
-              if (row >= rows) token[x] = -1;
-              else if (args.rows != nullptr) {
-                token[x] = __ldg(args.rows + static_cast<int64_t>(w.b) * args.max_rows + token[x]);
-                if (token[x] < 0 || token[x] >= args.tokens) {
-                  cache::report(args.status, cache::kStatusInvalid);
-                  token[x] = -1;
+              for (int x = 0; x < kBatch; ++x) {
+                const int row = row0 + x * kRowStep, i = row / args.group;
+                head[x] = w.h * args.group + row - i * args.group;
+                token[x] = first_row + i;
+                if (row >= rows) token[x] = -1;
+                else if (args.rows != nullptr) {
+                  token[x] = __ldg(args.rows + static_cast<int64_t>(w.b) * args.max_rows + token[x]);
+                  if (token[x] < 0 || token[x] >= args.tokens) {
+                    cache::report(args.status, cache::kStatusInvalid);
+                    token[x] = -1;
+                  }
+                }
+              }
+#pragma unroll
+              for (int x = 0; x < kBatch; ++x) {
+                v[x] = make_uint4(0u, 0u, 0u, 0u);
+                lse[x] = INFINITY;   // rows that do not count weigh nothing
+                if (token[x] >= 0) {
+                  v[x] = __ldg(reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(args.q) + w.b * args.q_batch +
+                                                              token[x] * args.q_token + head[x] * args.q_head) + piece);
+                  if (piece == 0)
+                    lse[x] = __ldg(args.lse + (static_cast<int64_t>(w.b) * args.tokens + token[x]) * args.heads + head[x]);
+                }
+              }
+#pragma unroll
+              for (int x = 0; x < kBatch; ++x) {
+                const int row = row0 + x * kRowStep;
+                if (row >= cols) break;
+                st_shared_v4(base + C::kOffQ + (piece / 8) * C::kQBoxBytes + (halves.first() + row) * 128u + (((piece & 7) ^ (row & 7)) * 16u),
+                             v[x].x, v[x].y, v[x].z, v[x].w);
+                if (piece == 0) {
+                  // lse * log2e as a rounded part and the factor that makes up for the rounding
+                  const float hi = lse[x] * cw::kLog2e;
+                  const float lo = fmaf(lse[x], cw::kLog2e, -hi);
+                  row_ref[halves.first() + row] = isinf(hi) ? -INFINITY : -hi;
+                  row_factor[halves.first() + row] = isinf(hi) ? 0.0f : ex2_approx(-lo);
                 }
               }
             }
-#pragma unroll
-            for (int x = 0; x < kBatch; ++x) {
-              v[x] = make_uint4(0u, 0u, 0u, 0u);
-              lse[x] = INFINITY;   // rows that do not count weigh nothing
-              if (token[x] >= 0) {
-                v[x] = __ldg(reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(args.q) + w.b * args.q_batch +
-                                                            token[x] * args.q_token + head[x] * args.q_head) + piece);
-                if (piece == 0)
-                  lse[x] = __ldg(args.lse + (static_cast<int64_t>(w.b) * args.tokens + token[x]) * args.heads + head[x]);
-              }
-            }
-#pragma unroll
-            for (int x = 0; x < kBatch; ++x) {
-              const int row = row0 + x * kRowStep;
-              if (row >= cols) break;
-              st_shared_v4(base + C::kOffQ + (piece / 8) * C::kQBoxBytes + row * 128u + (((piece & 7) ^ (row & 7)) * 16u),
-                           v[x].x, v[x].y, v[x].z, v[x].w);
-              if (piece == 0) {
-                // lse * log2e as a rounded part and the factor that makes up for the rounding
-                const float hi = lse[x] * cw::kLog2e;
-                const float lo = fmaf(lse[x], cw::kLog2e, -hi);
-                row_ref[row] = isinf(hi) ? -INFINITY : -hi;
-                row_factor[row] = isinf(hi) ? 0.0f : ex2_approx(-lo);
-              }
-            }
-          }
-        };
-        if (cols > 4 * kRowStep) gather(std::integral_constant<int, 8>{});
-        else gather(std::integral_constant<int, 4>{});
-        fence_proxy_async_shared();
+          };
+          if (cols > 4 * kRowStep) gather(std::integral_constant<int, 8>{});
+          else gather(std::integral_constant<int, 4>{});
+          fence_proxy_async_shared();
+        }
         __syncwarp();
-        if (lane == 0) mbar_arrive(q_full);
-        if (!(ok = wd.warp_wait(q_full, static_cast<uint32_t>(q_blocks) & 1u))) break;
+        if (lane == 0)
+          for (int half = 0; half < 2; ++half)
+            if (halves.has(half)) mbar_arrive(q_full(half));
+        for (int half = 0; half < 2 && ok; ++half)
+          if (halves.has(half)) ok = wd.warp_wait(q_full(half), halves.phase(half));
+        if (!ok) break;
+        const float* block_ref = row_ref + halves.first();   // and as far behind it as row_factor is
         for (int j = w.j0; ok && j < w.j0 + w.count; ++j, ++it) {
           if ((it & 1) != g) continue;
           const int key = j * cw::kTileKeys + key_lane;
@@ -381,8 +500,8 @@ __global__ void __launch_bounds__(C::kNumThreads, 1) cache_weigh_kernel(const __
           uint64_t sum01 = f32x2_pack(0.0f, 0.0f), sum23 = sum01;
           uint32_t raw[2][32];
           auto columns = [&](const uint32_t (&x)[32], int c0, auto mask) {
-            const ulonglong2* refs = reinterpret_cast<const ulonglong2*>(row_ref + c0);
-            const ulonglong2* factors = reinterpret_cast<const ulonglong2*>(row_factor + c0);
+            const ulonglong2* refs = reinterpret_cast<const ulonglong2*>(block_ref + c0);
+            const ulonglong2* factors = reinterpret_cast<const ulonglong2*>(block_ref + cw::kMaxRows + c0);
 #pragma unroll
             for (int e = 0; e < 32; e += 4) {
               const ulonglong2 ref = refs[e / 4], f = factors[e / 4];
@@ -435,7 +554,10 @@ __global__ void __launch_bounds__(C::kNumThreads, 1) cache_weigh_kernel(const __
           if (live) args.weight_out[weight_row + key] = acc + ((sum0 + sum1) + (sum2 + sum3));
         }
         __syncwarp();
-        if (lane == 0) mbar_arrive(q_free);
+        if (lane == 0)
+          for (int half = 0; half < 2; ++half)
+            if (halves.has(half)) mbar_arrive(q_free(half));
+        __syncwarp();
       }
     }
   }
