@@ -37,10 +37,13 @@ __device__ __forceinline__ int new_count(const AppendArgs& a, int b) {
   return a.counts == nullptr ? a.max_rows : min(max(__ldg(a.counts + b), 0), a.max_rows);
 }
 
+// The length after n more tokens: n may be any count, so the room is compared and not the sum.
+__device__ __forceinline__ int longer(const CacheView& c, int len, int n) { return len + min(n, c.capacity - len); }
+
 __device__ __forceinline__ void advance(const AppendArgs& a, int b) {
   const int n = new_count(a, b);
   const int seen = a.seen_out != nullptr ? a.seen[b] : 0;
-  a.lens_out[b] = min(cached_len(a.c, a.lens, b) + n, a.c.capacity);
+  a.lens_out[b] = longer(a.c, cached_len(a.c, a.lens, b), n);
   if (a.seen_out != nullptr) a.seen_out[b] = seen + n;
 }
 
@@ -61,11 +64,12 @@ __global__ void __launch_bounds__(256) cache_append_kernel(const __grid_constant
   const int b = static_cast<int>(b64);
   if (write_lens != 0 && i == 0 && h == 0 && piece == 0) advance(a, b);
   if (i >= new_count(a, b)) return;
-  const int slot = cached_len(a.c, a.lens, b) + i;
-  if (slot >= a.c.capacity) {   // the sequence's pages are full
-    cache::report(a.status, cache::kStatusInvalid);
+  const int len = cached_len(a.c, a.lens, b), room = a.c.capacity - len;
+  if (i >= room) {   // the sequence's pages are full: one thread says so
+    if (i == room && h == 0 && piece == 0) cache::report(a.status, cache::kStatusInvalid);
     return;
   }
+  const int slot = len + i;
   const int token = a.rows == nullptr ? i : __ldg(a.rows + static_cast<int64_t>(b) * a.max_rows + i);
   const int64_t to = slot_at(a.c, b, h, slot);
   if (token < 0 || token >= a.tokens || to < 0) {
@@ -77,7 +81,7 @@ __global__ void __launch_bounds__(256) cache_append_kernel(const __grid_constant
   if (piece == 0) {
     const int64_t at = (static_cast<int64_t>(b) * a.c.kv_heads + h) * a.c.capacity + slot;
     if (a.weight != nullptr) a.weight[at] = 0.0f;
-    if (a.pos != nullptr) a.pos[at] = (a.seen != nullptr ? __ldg(a.seen + b) : cached_len(a.c, a.lens, b)) + i;
+    if (a.pos != nullptr) a.pos[at] = (a.seen != nullptr ? __ldg(a.seen + b) : len) + i;
   }
 }
 
@@ -90,7 +94,7 @@ __global__ void __launch_bounds__(256) cache_advance_kernel(const __grid_constan
     const int len = min(max(a.lens[b], 0), a.c.capacity);
     const int n = new_count(a, b);
     if (a.seen_out != nullptr) a.seen_out[b] = a.seen[b] + n;
-    a.lens_out[b] = min(len + n, a.c.capacity);
+    a.lens_out[b] = longer(a.c, len, n);
   }
 }
 

@@ -360,6 +360,30 @@ def test_append_past_the_capacity_and_from_rows_out_of_range():
     assert int(status.item()) == gt.GEMM_TN_ERR_INVALID_VALUE and ref.same(cache.k[0, 6], at)
 
 
+@pytest.mark.parametrize("in_place", [False, True])
+def test_append_more_rows_than_any_cache_has_slots(in_place):
+    """max_rows at its limit, the one token over and over: len + max_rows is past 32 bits, and the slots end at the capacity."""
+    if torch.cuda.mem_get_info()[0] < 12 * 2 ** 30:
+        pytest.skip("the list of rows takes 8.6 GB")
+    s = ref.make("bf16", 64, [13], 1, 1, 1, 8, seed=24, max_pages=4)
+    s.table = torch.tensor([[4, 1, 5, 2]], dtype=torch.int32)
+    k, v, weight, pos = s.k.clone(), s.v.clone(), s.weight.clone(), s.pos.clone()
+    for slot in range(13, 32):
+        k[s.table[0, slot // 8], slot % 8], v[s.table[0, slot // 8], slot % 8] = s.k_new[0, 0], s.v_new[0, 0]
+        weight[0, 0, slot], pos[0, 0, slot] = 0.0, int(s.seen[0]) + slot - 13
+    cache, status = on_gpu(s)
+    out = cache.lens if in_place else torch.zeros(1, dtype=torch.int32, device=DEV)
+    rows = torch.zeros((1, 2 ** 31 - 1), dtype=torch.int32, device=DEV)
+    gt.cache_append(cache, s.k_new.to(DEV), s.v_new.to(DEV), rows=rows, lens_out=out,
+                    seen_out=torch.zeros(1, dtype=torch.int32, device=DEV), status=status)
+    torch.cuda.synchronize()
+    del rows
+    torch.cuda.empty_cache()
+    assert out.tolist() == [32] and int(status.item()) == gt.GEMM_TN_ERR_INVALID_VALUE
+    for got, want in ((cache.k, k), (cache.v, v), (cache.weight, weight), (cache.pos, pos)):
+        assert ref.same(got.cpu(), want)
+
+
 # ---------------------------------------------------------------- accumulated weights
 
 # lens, tokens, kv_heads, group, page, counts
