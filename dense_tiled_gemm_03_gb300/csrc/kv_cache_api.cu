@@ -485,6 +485,10 @@ int kv_cache_evict(int dtype, int64_t batch, const kv_cache* cache, int64_t keep
   if (st != GEMM_TN_OK) return st;
   if (keep < 0 || keep > kMax31) return invalid("keep must be in [0, 2^31)");
   if (recent < 0 || recent > keep) return invalid("recent must be in [0, keep]");
+  // the kernels walk slots and lists in 32 bits, by up to 2^16 at a time
+  if (cache->max_pages * cache->page_size > kMax31 + 1 - (1 << 16))
+    return invalid("max_pages * page_size must be at most 2^31 - 2^16");
+  if (batch > 0 && cache->kv_heads > (int64_t{1} << 30) / batch) return invalid("batch * kv_heads must be at most 2^30");
   if (batch == 0) return GEMM_TN_OK;
   if (cache->weight == nullptr || weight_out == nullptr || lens_out == nullptr)
     return invalid("weight, weight_out or lens_out is NULL");

@@ -225,7 +225,7 @@ __global__ void __launch_bounds__(ev::kThreads) cache_select_kernel(const __grid
   const bool in_smem = s1 - s0 <= a.smem_keys;
   auto key = [&](int s) { return in_smem ? smem_keys[s - s0] : load_key(s); };
   const int word_pitch = (a.c.capacity + 31) / 32;
-  uint32_t* global_words = in_smem ? nullptr : a.words + static_cast<int64_t>(3 * bh) * word_pitch + s0 / 32;
+  uint32_t* global_words = in_smem ? nullptr : a.words + 3 * static_cast<int64_t>(bh) * word_pitch + s0 / 32;
   uint32_t* words = in_smem ? smem_words : global_words;
   int* hole_ranks = in_smem ? smem_ranks[0] : reinterpret_cast<int*>(global_words + word_pitch);
   int* mover_ranks = in_smem ? smem_ranks[1] : hole_ranks + word_pitch;

@@ -161,6 +161,7 @@ GEMM_TN_API int kv_cache_weigh(int dtype, int64_t batch, int64_t tokens, int64_t
  * min(lens[b], keep)) may be the cache's own weight, pos and lens. pos and
  * seen may be NULL when recent is 0; pos_out is NULL exactly when pos is.
  * 0 <= recent <= keep. K and V behind the new length keep their old contents.
+ * Limits: capacity <= 2^31 - 2^16, batch * kv_heads <= 2^30.
  * The list of moves is a workspace from the library's pool.
  */
 GEMM_TN_API int kv_cache_evict(int dtype, int64_t batch, const kv_cache* cache, int64_t keep, int64_t recent,

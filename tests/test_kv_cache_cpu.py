@@ -169,6 +169,15 @@ def test_outputs_that_replace_the_caches_own_arrays_are_not(lib):
         assert rc in NO_DEVICE
 
 
+def test_evict_refuses_sizes_that_its_32_bit_walks_cannot_hold(lib):
+    """The walk over slots steps up to 2^16 past the last one, the walk over lists by up to 65535."""
+    wide = cache(page_size=128, max_pages=(2 ** 31 - 257) // 128, table_stride=2 ** 24)
+    assert evict(lib, c=wide) == INVALID and "2^31 - 2^16" in gt.gemm_tn_last_error_message()
+    many = cache(kv_heads=1, table_stride=10)
+    for batch in (2 ** 31 - 1, 2 ** 30 + 1):
+        assert evict(lib, batch=batch, c=many) == INVALID and "2^30" in gt.gemm_tn_last_error_message()
+
+
 def test_empty_calls_need_no_device(lib):
     assert attn(lib, tokens=0) == gt.GEMM_TN_OK and attn(lib, heads=0) == gt.GEMM_TN_OK
 
