@@ -224,12 +224,13 @@ int keep_whole(int64_t items, int64_t tiles, int units, int spread, int sms) {
   return tiles <= allowance ? 1 : 0;
 }
 
-// The kernels count key tiles in 32 bits: an upper bound of their number, from
-// what the cache and the inputs can hold.
+// The kernels count key tiles in 32 bits, rounded up to whole chunks (one per SM):
+// an upper bound of their number, from what the cache and the inputs can hold.
 int check_tiles(const kv_cache* c, int64_t batch, int64_t row_units, int64_t tokens) {
   const int64_t per_item = (c->max_pages * c->page_size + 127) / 128 + (tokens + 127) / 128 + 1 + kMaxChange;
   const int64_t items = batch * c->kv_heads;   // below 2^31
-  if (row_units > kMax31 / items || per_item > kMax31 / (items * row_units))
+  constexpr int64_t kMost = kMax31 - (1 << 16);
+  if (row_units > kMost / items || per_item > kMost / (items * row_units))
     return invalid("too many key tiles: batch * kv_heads * tokens * capacity is too large");
   return GEMM_TN_OK;
 }

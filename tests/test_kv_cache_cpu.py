@@ -178,6 +178,13 @@ def test_evict_refuses_sizes_that_its_32_bit_walks_cannot_hold(lib):
         assert evict(lib, batch=batch, c=many) == INVALID and "2^30" in gt.gemm_tn_last_error_message()
 
 
+def test_as_many_key_tiles_as_32_bits_hold_leave_room_for_whole_chunks(lib):
+    """192 lists of 11184810 tiles and places between them: 2^31 - 128, which rounding up to chunks would carry past 2^31."""
+    c = cache(page_size=128, max_pages=11184810 - 9, table_stride=2 ** 24)
+    assert 192 * 11184810 == 2 ** 31 - 128
+    assert weigh(lib, batch=96, c=c) == INVALID and "key tiles" in gt.gemm_tn_last_error_message()
+
+
 def test_empty_calls_need_no_device(lib):
     assert attn(lib, tokens=0) == gt.GEMM_TN_OK and attn(lib, heads=0) == gt.GEMM_TN_OK
 
