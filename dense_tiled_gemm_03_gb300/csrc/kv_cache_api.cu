@@ -7,6 +7,7 @@
 #include <algorithm>
 #include <cmath>
 #include <cstdint>
+#include <initializer_list>
 
 #include "kv_cache.h"
 #include "kv_cache_internal.h"
@@ -64,14 +65,17 @@ int check_rows(const kv_rows* r, int64_t batch, int64_t tokens, int64_t heads, i
 struct Range {
   uintptr_t begin, end;
 };
-bool overlap(const Range& a, const Range& b) { return a.begin < b.end && b.begin < a.end; }
+bool overlap(const Range& a, const Range& b) {
+  return a.begin < a.end && b.begin < b.end && a.begin < b.end && b.begin < a.end;
+}
 Range pool_range(const void* p, const kv_cache* c) {
   const uintptr_t b = reinterpret_cast<uintptr_t>(p);
   return {b, b + 2 * static_cast<uintptr_t>((c->num_pages - 1) * c->page_stride + (c->page_size - 1) * c->slot_stride +
                                              (c->kv_heads - 1) * c->head_stride + c->head_dim)};
 }
-Range rows_range(const kv_rows* r, int64_t batch, int64_t tokens, int64_t heads, int64_t dim) {
-  const uintptr_t b = reinterpret_cast<uintptr_t>(r->data);
+Range rows_range(const kv_rows* r, int64_t batch, int64_t tokens, int64_t heads, int64_t dim) {   // empty for NULL
+  const uintptr_t b = r != nullptr ? reinterpret_cast<uintptr_t>(r->data) : 0;
+  if (b == 0) return {0, 0};
   return {b, b + 2 * static_cast<uintptr_t>((batch - 1) * (batch > 1 ? r->batch_stride : 0) + (tokens - 1) * (tokens > 1 ? r->token_stride : 0) +
                                              (heads - 1) * (heads > 1 ? r->head_stride : 0) + dim)};
 }
@@ -83,14 +87,72 @@ Range words_range(const void* p, int64_t count) {   // of 4 bytes; empty for NUL
 Range table_range(const kv_cache* c, int64_t batch) {
   return words_range(c->page_table, (batch - 1) * (batch > 1 ? c->table_stride : 0) + c->max_pages);
 }
-// Whether an output lies in one of the inputs, which other blocks may still read
-// when it is written; `own` is the input that it may replace, exactly.
-template <size_t kInputs>
-bool lies_in(const Range& out, const Range& own, const Range (&inputs)[kInputs]) {
-  if (out.begin != own.begin && overlap(out, own)) return true;
-  for (const Range& in : inputs)
-    if (overlap(out, in)) return true;
-  return false;
+
+// The cache's arrays, also those that the call at hand does not use.
+struct CacheRanges {
+  Range k, v, table, lens, weight, pos, seen;
+};
+CacheRanges cache_ranges(const kv_cache* c, int64_t batch) {
+  const int64_t slots = batch * c->kv_heads * c->max_pages * c->page_size;
+  return {pool_range(c->k, c),         pool_range(c->v, c),           table_range(c, batch),     words_range(c->lens, batch),
+          words_range(c->weight, slots), words_range(c->pos, slots), words_range(c->seen, batch)};
+}
+
+// An array that a call writes, and the input that it replaces and may be, exactly.
+struct Output {
+  Range at, own;
+};
+using Outputs = std::initializer_list<Output>;
+using Inputs = std::initializer_list<Range>;   // but for those that outputs replace
+// Whether an array lies in one of these, in what they replace, or in an input.
+bool meets(const Range& a, Outputs outs, Inputs ins, const Output* but = nullptr) {
+  for (const Output& x : outs)
+    if (&x != but && (overlap(a, x.at) || overlap(a, x.own))) return true;
+  return std::any_of(ins.begin(), ins.end(), [&](const Range& in) { return overlap(a, in); });
+}
+// Whether an output lies in another array, which other blocks may still read or
+// write when it is written.
+bool clash(Outputs outs, Inputs ins) {
+  return std::any_of(outs.begin(), outs.end(), [&](const Output& o) {
+    return meets(o.at, outs, ins, &o) || (o.at.begin != o.own.begin && overlap(o.at, o.own));
+  });
+}
+
+// Whether a row of the K pool and a row of the V pool share elements; the pools'
+// address ranges may interleave (K and V of a page, or of a slot, side by side). The
+// rows are `apart` elements plus multiples of the three strides apart: one stride
+// after the other, the longest first, only the two multiples next to what is left can
+// bring it within the shorter strides' reach. Where a stride is shorter than that
+// reach (rows that share elements within one pool) any touching of the ranges counts.
+bool pools_overlap(const kv_cache* c) {
+  if (!overlap(pool_range(c->k, c), pool_range(c->v, c))) return false;
+  struct Dim {
+    int64_t stride, count;
+  };
+  Dim dims[3] = {{c->page_stride, c->num_pages}, {c->slot_stride, c->page_size}, {c->head_stride, c->kv_heads}};
+  std::sort(dims, dims + 3, [](const Dim& a, const Dim& b) { return (a.count > 1 ? a.stride : 0) > (b.count > 1 ? b.stride : 0); });
+  int64_t reach = c->head_dim;   // elements from the first to past the last of the dims after the one at hand
+  for (int i = 2; i >= 0; --i) {
+    if (dims[i].count == 1) continue;
+    if (dims[i].stride < reach) return true;
+    reach += dims[i].stride * (dims[i].count - 1);
+  }
+  const int64_t bytes = static_cast<int64_t>(reinterpret_cast<uintptr_t>(c->v) - reinterpret_cast<uintptr_t>(c->k));
+  int64_t left[8] = {bytes / 2};   // the pools start on 16-byte boundaries
+  int n = 1;
+  for (const Dim& d : dims) {
+    if (d.count == 1) continue;
+    int64_t next[8];
+    int m = 0;
+    for (int i = 0; i < n; ++i) {
+      const int64_t down = left[i] / d.stride - (left[i] % d.stride < 0 ? 1 : 0);
+      for (int64_t q = down; q <= down + 1; ++q)
+        if (q > -d.count && q < d.count) next[m++] = left[i] - q * d.stride;
+    }
+    n = m;
+    std::copy(next, next + m, left);
+  }
+  return std::any_of(left, left + n, [&](int64_t x) { return x > -c->head_dim && x < c->head_dim; });
 }
 
 // {dim, kv heads, page_size, num_pages}; moved in boxes of 64 elements of one
@@ -263,15 +325,15 @@ int tree_attn_fwd(int dtype, int64_t batch, int64_t tokens, int64_t heads, const
   if (o == nullptr) return invalid("o is NULL");
   if (!aligned(o, 16) || !aligned(lse, 4) || !aligned(mask, 8) || !aligned(token_lens, 4))
     return api_fail(GEMM_TN_ERR_MISALIGNED, "o, lse, mask or token_lens is not aligned to its element (o: 16 bytes)");
-  const Range out = words_range(o, batch * tokens * heads * (dim / 2)), none = {0, 0};
-  const Range ins[] = {rows_range(q, batch, tokens, heads, dim), pool_range(cache->k, cache), pool_range(cache->v, cache),
-                       has_new ? rows_range(k_new, batch, tokens, kv_heads, dim) : none,
-                       has_new ? rows_range(v_new, batch, tokens, kv_heads, dim) : none,
-                       words_range(mask, 2 * batch * tokens * ((tokens + 63) / 64)), words_range(token_lens, batch),
-                       words_range(cache->lens, batch), table_range(cache, batch)};
-  if (lies_in(out, none, ins)) return invalid("o overlaps an input or the cache");
-  const Range sums = words_range(lse, batch * tokens * heads);
-  if (overlap(sums, out) || lies_in(sums, none, ins)) return invalid("lse overlaps o, an input or the cache");
+  const CacheRanges r = cache_ranges(cache, batch);
+  const Range none = {0, 0};
+  if (clash({{words_range(o, batch * tokens * heads * (dim / 2)), none},
+             {words_range(lse, batch * tokens * heads), none},
+             {words_range(d_status, 1), none}},
+            {rows_range(q, batch, tokens, heads, dim), rows_range(k_new, batch, tokens, kv_heads, dim),
+             rows_range(v_new, batch, tokens, kv_heads, dim), words_range(mask, 2 * batch * tokens * ((tokens + 63) / 64)),
+             words_range(token_lens, batch), r.k, r.v, r.table, r.lens, r.weight, r.pos, r.seen}))
+    return invalid("o, lse or the status word overlaps another array of the call");
   alignas(64) gemm_tn_dev::TreeArgs args{};
   args.group = static_cast<int>(heads / kv_heads);
   const bool decode = tokens * args.group <= decode_attn_rows();
@@ -363,20 +425,24 @@ int kv_cache_append(int dtype, int64_t batch, int64_t tokens, const kv_cache* ca
   if (max_rows > 0 && tokens > 0) {
     if ((st = check_rows(k_new, batch, tokens, cache->kv_heads, cache->head_dim)) != GEMM_TN_OK) return st;
     if ((st = check_rows(v_new, batch, tokens, cache->kv_heads, cache->head_dim)) != GEMM_TN_OK) return st;
-    for (const kv_rows* r : {k_new, v_new})
-      for (const void* p : {cache->k, cache->v})
-        if (overlap(rows_range(r, batch, tokens, cache->kv_heads, cache->head_dim), pool_range(p, cache)))
-          return invalid("k_new or v_new overlaps the cache");
     if (max_rows > (int64_t{1} << 34) / (batch * cache->kv_heads)) return invalid("batch * max_rows * kv_heads must be at most 2^34");
   } else if (max_rows > 0) {
     return invalid("max_rows > 0 without tokens");
   }
-  const Range lens = words_range(cache->lens, batch), seen = words_range(cache->seen, batch);
-  const Range new_lens = words_range(lens_out, batch), new_seen = words_range(seen_out, batch);
-  const Range ins[] = {words_range(rows, batch * max_rows), words_range(counts, batch), table_range(cache, batch)};
-  if (overlap(new_lens, new_seen) || overlap(new_lens, seen) || overlap(new_seen, lens) || lies_in(new_lens, lens, ins) ||
-      lies_in(new_seen, seen, ins))
-    return invalid("lens_out or seen_out overlaps another array of the call");
+  const CacheRanges r = cache_ranges(cache, batch);
+  const Range none = {0, 0};
+  const bool copies = max_rows > 0;
+  if (pools_overlap(cache)) return invalid("the K and V pools overlap");
+  const Outputs outs = {{r.weight, none},
+                        {r.pos, none},
+                        {words_range(lens_out, batch), r.lens},
+                        {words_range(seen_out, batch), r.seen},
+                        {words_range(d_status, 1), none}};
+  const Inputs ins = {copies ? rows_range(k_new, batch, tokens, cache->kv_heads, cache->head_dim) : none,
+                      copies ? rows_range(v_new, batch, tokens, cache->kv_heads, cache->head_dim) : none,
+                      words_range(rows, batch * max_rows), words_range(counts, batch), r.table};
+  if (clash(outs, ins) || meets(r.k, outs, ins) || meets(r.v, outs, ins))
+    return invalid("a pool, weight, pos, lens_out, seen_out or the status word overlaps another array of the call");
   int sms = 0;
   if ((st = api_device(&sms)) != GEMM_TN_OK) return st;
   gemm_tn_dev::AppendArgs args{};
@@ -429,13 +495,14 @@ int kv_cache_weigh(int dtype, int64_t batch, int64_t tokens, int64_t heads, cons
   }
   if (!aligned(rows, 4) || !aligned(counts, 4) || !aligned(lse, 4) || !aligned(weight_out, 4))
     return api_fail(GEMM_TN_ERR_MISALIGNED, "rows, counts, lse or weight_out not 4-byte aligned");
+  const CacheRanges r = cache_ranges(cache, batch);
+  const Range none = {0, 0};
   const int64_t slots = batch * cache->kv_heads * cache->max_pages * cache->page_size;
-  const Range ins[] = {max_rows > 0 ? rows_range(q, batch, tokens, heads, cache->head_dim) : Range{0, 0},
-                       words_range(lse, max_rows > 0 ? batch * tokens * heads : 0), words_range(rows, batch * max_rows),
-                       words_range(counts, batch), words_range(cache->lens, batch), table_range(cache, batch),
-                       pool_range(cache->k, cache)};
-  if (lies_in(words_range(weight_out, slots), words_range(cache->weight, slots), ins))
-    return invalid("weight_out overlaps another array of the call");
+  if (clash({{words_range(weight_out, slots), r.weight}, {words_range(d_status, 1), none}},
+            {max_rows > 0 ? rows_range(q, batch, tokens, heads, cache->head_dim) : none,
+             words_range(lse, max_rows > 0 ? batch * tokens * heads : 0), words_range(rows, batch * max_rows),
+             words_range(counts, batch), r.k, r.v, r.table, r.lens, r.pos, r.seen}))
+    return invalid("weight_out or the status word overlaps another array of the call");
   if ((st = check_tiles(cache, batch, 1, 0)) != GEMM_TN_OK) return st;
   int sms = 0;
   if ((st = api_device(&sms)) != GEMM_TN_OK) return st;
@@ -497,15 +564,17 @@ int kv_cache_evict(int dtype, int64_t batch, const kv_cache* cache, int64_t keep
   if ((pos_out == nullptr) != (cache->pos == nullptr)) return invalid("pos_out goes with the cache's pos");
   if (!aligned(weight_out, 4) || !aligned(pos_out, 4) || !aligned(lens_out, 4))
     return api_fail(GEMM_TN_ERR_MISALIGNED, "weight_out, pos_out or lens_out not 4-byte aligned");
+  const CacheRanges r = cache_ranges(cache, batch);
+  const Range none = {0, 0};
   const int64_t slots = batch * cache->kv_heads * cache->max_pages * cache->page_size;
-  const Range weight = words_range(cache->weight, slots), pos = words_range(cache->pos, slots);
-  const Range lens = words_range(cache->lens, batch), new_weight = words_range(weight_out, slots);
-  const Range new_pos = words_range(pos_out, slots), new_lens = words_range(lens_out, batch);
-  const Range ins[] = {words_range(cache->seen, batch), table_range(cache, batch)};
-  if (overlap(new_weight, pos) || overlap(new_weight, lens) || overlap(new_weight, new_pos) || overlap(new_weight, new_lens) ||
-      overlap(new_pos, weight) || overlap(new_pos, lens) || overlap(new_pos, new_lens) || overlap(new_lens, weight) ||
-      overlap(new_lens, pos) || lies_in(new_weight, weight, ins) || lies_in(new_pos, pos, ins) || lies_in(new_lens, lens, ins))
-    return invalid("weight_out, pos_out or lens_out overlaps another array of the call");
+  if (pools_overlap(cache)) return invalid("the K and V pools overlap");
+  const Outputs outs = {{words_range(weight_out, slots), r.weight},
+                        {words_range(pos_out, slots), r.pos},
+                        {words_range(lens_out, batch), r.lens},
+                        {words_range(d_status, 1), none}};
+  const Inputs ins = {r.table, r.seen};
+  if (clash(outs, ins) || meets(r.k, outs, ins) || meets(r.v, outs, ins))
+    return invalid("a pool, weight_out, pos_out, lens_out or the status word overlaps another array of the call");
   int sms = 0;
   if ((st = api_device(&sms)) != GEMM_TN_OK) return st;
   gemm_tn_dev::EvictArgs args{};

@@ -34,8 +34,11 @@
  *     test hook: the first CTA skips the K load of its tile of that number.
  *   - Pages that a call writes (append, evict) belong to one sequence only;
  *     pages that are only read may be shared.
- *   - An output overlaps no other array of the call (INVALID_VALUE), except
- *     that it may be, exactly, the cache's array that it replaces.
+ *   - An output (the pools, weight and pos too where they are written, and the
+ *     status word) overlaps no other array of the call, used by it or not
+ *     (INVALID_VALUE), except that it may be, exactly, the cache's array that it
+ *     replaces. The K and V pools of append and evict may lie between one
+ *     another's rows (K and V of a page or of a slot side by side) but share none.
  *   - Results are repeatable to the bit: no atomics touch them.
  *   - Serving only: there are no gradients.
  */

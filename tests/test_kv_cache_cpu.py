@@ -160,6 +160,83 @@ def test_outputs_that_lie_in_other_arrays_are_refused(lib, call, over):
     assert "overlap" in gt.gemm_tn_last_error_message()
 
 
+def with_status(lib, name, at):
+    """A call of the C function with a status word at that address."""
+    c, q, kn, vn = cache(), rows(), rows(KN, 512, 128), rows(VN, 512, 128)
+    r = ctypes.byref
+    return {"attn": lambda: lib.tree_attn_fwd(BF16, 3, 4, 8, r(c), r(q), r(kn), r(vn), None, None, O, LSE, 0.0, at, None),
+            "append": lambda: lib.kv_cache_append(BF16, 3, 4, r(c), r(kn), r(vn), None, None, 4, OUT, None, at, None),
+            "weigh": lambda: lib.kv_cache_weigh(BF16, 3, 4, 8, r(c), r(q), LSE, None, None, 4, 1, 0.0, OUT, at, None),
+            "evict": lambda: lib.kv_cache_evict(BF16, 3, r(c), 50, 5, W, POS, LENS, at, None)}[name]()
+
+
+@pytest.mark.parametrize("call,over", [
+    (append, dict(lens_out=KN)), (append, dict(lens_out=VN + 64)), (append, dict(lens_out=K + 4096)), (append, dict(lens_out=V)),
+    (append, dict(lens_out=W + 8)), (append, dict(lens_out=POS)), (append, dict(seen_out=K)), (append, dict(seen_out=W)),
+    (append, dict(c=cache(weight=KN))), (append, dict(c=cache(pos=LENS))), (append, dict(c=cache(pos=SEEN))),
+    (append, dict(c=cache(pos=W))), (append, dict(c=cache(pos=W + 3 * 2 * 160 * 4 - 4))), (append, dict(c=cache(weight=K))),
+    (append, dict(c=cache(lens=K))), (append, dict(c=cache(page_table=V))), (append, dict(c=cache(v=K))),
+    (append, dict(c=cache(v=K + 128))), (append, dict(counts=K)), (append, dict(r=W)),
+    (evict, dict(w=K)), (evict, dict(p=V)), (evict, dict(lens_out=K)), (evict, dict(lens_out=V + 8)), (evict, dict(c=cache(v=K))),
+    (evict, dict(c=cache(seen=K))), (evict, dict(c=cache(page_table=K))), (evict, dict(c=cache(weight=K))),
+    (evict, dict(c=cache(weight=POS), w=POS, p=OUT)), (weigh, dict(out=V)), (weigh, dict(out=POS)), (weigh, dict(out=SEEN)),
+    (attn, dict(o=W)), (attn, dict(lse=POS)), (attn, dict(o=SEEN))])
+def test_what_a_call_writes_lies_apart_from_all_its_arrays(lib, call, over):
+    assert call(lib, **over) == INVALID
+    assert "overlap" in gt.gemm_tn_last_error_message()
+
+
+@pytest.mark.parametrize("name,places", [
+    ("attn", [O, LSE, Q, KN, VN, K, V, LENS, TABLE, W]), ("append", [OUT, K, V, W, POS, LENS, SEEN, TABLE, KN]),
+    ("weigh", [OUT, W, Q, LSE, K, LENS, TABLE]), ("evict", [W, POS, LENS, SEEN, TABLE, K, V])])
+def test_the_status_word_lies_apart_too(lib, name, places):
+    for at in places:
+        assert with_status(lib, name, at) == INVALID and "overlap" in gt.gemm_tn_last_error_message()
+    if not torch.cuda.is_available():
+        assert with_status(lib, name, 0x1000) in NO_DEVICE
+
+
+def test_pools_may_lie_between_one_another(lib):
+    """K and V of a page, of a slot, of a head or of all heads side by side; reading may share them outright."""
+    if torch.cuda.is_available():
+        pytest.skip("the addresses are not real")
+    for over in (dict(page_stride=4096, v=K + 2048 * 2), dict(page_stride=4096, slot_stride=256, v=K + 128 * 2),
+                 dict(page_stride=4096, slot_stride=256, head_stride=128, v=K + 64 * 2), dict(v=K + 100 * 2048 * 2),
+                 dict(k=K + 2048 * 2, v=K, page_stride=4096), dict(num_pages=1, page_stride=0, v=K + 2048 * 2)):
+        for call in (append, evict):
+            assert call(lib, c=cache(**over)) in NO_DEVICE, over
+    for call in (attn, weigh):
+        assert call(lib, c=cache(v=K)) in NO_DEVICE
+    assert append(lib, max_rows=0, kn=None, vn=None) in NO_DEVICE
+
+
+def test_whether_pools_share_rows_is_found_for_any_strides(lib):
+    """Random strides and distances against the rows listed one by one; 8-element steps are what 16-byte rows allow."""
+    if torch.cuda.is_available():
+        pytest.skip("the addresses are not real")
+    import random
+    rng = random.Random(7)
+    shared = apart = 0
+    for _ in range(1500):
+        heads, pages = rng.randint(1, 3), rng.randint(1, 4)
+        inner, n_inner, outer, n_outer = rng.choice([("head", heads, "slot", 8), ("slot", 8, "head", heads)])
+        s = {inner: 64 + 8 * rng.choice([0, 0, 1, 8, 9])}
+        s[outer] = s[inner] * (n_inner - 1) + 64 + 8 * rng.choice([0, 0, 3, 8, 16])
+        s["page"] = s[outer] * (n_outer - 1) + s[inner] * (n_inner - 1) + 64 + 8 * rng.choice([0, 0, 8, 40, 80])
+        reach = s["page"] * pages
+        d = 8 * rng.randint(-reach // 8 - 4, reach // 8 + 4) if rng.random() < 0.5 else \
+            64 * rng.randint(-3, 3) + rng.choice([0, s["slot"], s["head"], s["page"]]) * rng.randint(-9, 9)
+        at = {p * s["page"] + r * s["slot"] + h * s["head"] for p in range(pages) for r in range(8) for h in range(heads)}
+        spans = {x // 8 + e for x in at for e in range(8)}                     # in steps of 8 elements
+        want = any((x + d) // 8 + e in spans for x in at for e in range(8))
+        c = cache(kv_heads=heads, num_pages=pages, page_size=8, page_stride=s["page"], slot_stride=s["slot"],
+                  head_stride=s["head"], v=K + 2 * d)
+        rc = evict(lib, c=c)
+        assert (rc == INVALID) == want and (want or rc in NO_DEVICE), (s, d, heads, pages)
+        shared, apart = shared + want, apart + (not want)
+    assert shared > 200 and apart > 200
+
+
 def test_outputs_that_replace_the_caches_own_arrays_are_not(lib):
     if torch.cuda.is_available():
         pytest.skip("the addresses are not real")
