@@ -98,15 +98,34 @@ std::string shape_text(at::IntArrayRef shape) {
 
 // ---------------------------------------------------------------- KVCache
 
-struct Cache {
-  PyObject_HEAD
-  PyObject *k, *v, *page_table, *lens, *weight, *pos, *seen;   // None where there is none
-  PyObject* dtype;
+// What seven tensors make up, as they are when it is read: a tensor may be given
+// other storage later (set_, resize_, an assignment to .data), so every call
+// describes the tensors anew.
+struct Description {
   long long batch, capacity, index, kv_heads, head_dim;
   int code;
   at::ScalarType type;
   kv_cache c;
+  PyObject *lens, *weight, *pos, *seen;   // borrowed; nullptr where there is none
 };
+
+struct Cache {
+  PyObject_HEAD
+  PyObject *k, *v, *page_table, *lens, *weight, *pos, *seen;   // None where there is none
+  PyObject* dtype;
+  Description made;   // as it was made; its pointers are not used again
+};
+
+// Whether the tensor's storage holds it (it may have been made smaller, or been freed).
+bool stored(const Tensor& t, const char* what) {
+  if (t.numel() == 0) return true;
+  int64_t extent = 1;
+  for (int64_t i = 0; i < t.dim(); ++i) extent += (t.size(i) - 1) * t.stride(i);
+  const uint64_t bytes = static_cast<uint64_t>(t.storage_offset() + extent) * t.element_size();
+  if (t.storage().nbytes() >= bytes) return true;
+  PyErr_Format(PyExc_ValueError, "the storage of %s is smaller than the tensor", what);
+  return false;
+}
 
 // The pointer of a contiguous tensor of 32-bit numbers of that shape, nullptr for no tensor; false with an exception set.
 bool numbers(PyObject* o, at::ScalarType type, int64_t index, const char* what, at::IntArrayRef shape, void** to) {
@@ -120,22 +139,22 @@ bool numbers(PyObject* o, at::ScalarType type, int64_t index, const char* what, 
     return false;
   }
   *to = t->data_ptr();
-  return true;
+  return stored(*t, what);
 }
-bool ints(PyObject* o, const Cache* c, const char* what, at::IntArrayRef shape, int32_t** to) {
+bool ints(PyObject* o, const Description* c, const char* what, at::IntArrayRef shape, int32_t** to) {
   void* p = nullptr;
   const bool ok = numbers(o, at::kInt, c->index, what, shape, &p);
   *to = static_cast<int32_t*>(p);
   return ok;
 }
-bool floats(PyObject* o, const Cache* c, const char* what, at::IntArrayRef shape, float** to) {
+bool floats(PyObject* o, const Description* c, const char* what, at::IntArrayRef shape, float** to) {
   void* p = nullptr;
   const bool ok = numbers(o, at::kFloat, c->index, what, shape, &p);
   *to = static_cast<float*>(p);
   return ok;
 }
 
-bool status_word(PyObject* o, const Cache* c, int** to) {
+bool status_word(PyObject* o, const Description* c, int** to) {
   *to = nullptr;
   if (o == nullptr) return true;
   const Tensor* t = tensor(o, "status");
@@ -149,7 +168,7 @@ bool status_word(PyObject* o, const Cache* c, int** to) {
 }
 
 // A [batch, tokens, heads, head_dim] tensor of that shape.
-bool rows_of(PyObject* o, const Cache* c, const char* what, at::IntArrayRef shape, kv_rows* to) {
+bool rows_of(PyObject* o, const Description* c, const char* what, at::IntArrayRef shape, kv_rows* to) {
   const Tensor* t = tensor(o, what);
   if (t == nullptr) return false;
   if (cuda_index(*t) != c->index) {
@@ -198,11 +217,11 @@ PyMemberDef cache_members[] = {
     {"pos", T_OBJECT, offsetof(Cache, pos), READONLY, nullptr},
     {"seen", T_OBJECT, offsetof(Cache, seen), READONLY, nullptr},
     {"dtype", T_OBJECT, offsetof(Cache, dtype), READONLY, nullptr},
-    {"batch", T_LONGLONG, offsetof(Cache, batch), READONLY, nullptr},
-    {"capacity", T_LONGLONG, offsetof(Cache, capacity), READONLY, "max_pages * page_size"},
-    {"index", T_LONGLONG, offsetof(Cache, index), READONLY, "the device's"},
-    {"kv_heads", T_LONGLONG, offsetof(Cache, kv_heads), READONLY, nullptr},
-    {"head_dim", T_LONGLONG, offsetof(Cache, head_dim), READONLY, nullptr},
+    {"batch", T_LONGLONG, offsetof(Cache, made.batch), READONLY, nullptr},
+    {"capacity", T_LONGLONG, offsetof(Cache, made.capacity), READONLY, "max_pages * page_size"},
+    {"index", T_LONGLONG, offsetof(Cache, made.index), READONLY, "the device's"},
+    {"kv_heads", T_LONGLONG, offsetof(Cache, made.kv_heads), READONLY, nullptr},
+    {"head_dim", T_LONGLONG, offsetof(Cache, made.head_dim), READONLY, nullptr},
     {nullptr, 0, 0, 0, nullptr},
 };
 
@@ -217,7 +236,8 @@ PyTypeObject* cache_type() {
     t.tp_doc =
         "KVCache(k, v, page_table, lens, weight=None, pos=None, seen=None)\n--\n\n"
         "A paged key/value cache in the caller's tensors (nothing is copied; the\n"
-        "tensors are kept alive).\n\n"
+        "tensors are kept alive, and each call finds their storage where it then\n"
+        "is; tensors whose sizes, strides or types have changed are refused).\n\n"
         "k, v: [num_pages, page_size, kv_heads, head_dim] CUDA fp16/bf16 views with\n"
         "unit stride along head_dim and the same strides; permute a\n"
         "[num_pages, kv_heads, page_size, head_dim] pool into this order. page_size 8,\n"
@@ -237,18 +257,16 @@ PyTypeObject* cache_type() {
   return &type;
 }
 
-PyObject* cache_new(PyObject* type, PyObject* const* args, size_t nargsf, PyObject* kwnames) {
-  HANDLE_TH_ERRORS
-  static const char* const names[] = {"k", "v", "page_table", "lens", "weight", "pos", "seen"};
-  PyObject* in[7];
-  if (!place("KVCache", names, 4, args, PyVectorcall_NARGS(nargsf), kwnames, in)) return nullptr;
+// Describes the cache of k, v, page_table, lens, weight, pos and seen (nullptr for
+// the last three: none); false with an exception set.
+bool describe(PyObject* const (&in)[7], Description* to) {
   const Tensor *k = tensor(in[0], "k"), *v = k != nullptr ? tensor(in[1], "v") : nullptr;
   const Tensor* table = v != nullptr ? tensor(in[2], "page_table") : nullptr;
   const Tensor* lens = table != nullptr ? tensor(in[3], "lens") : nullptr;
-  if (lens == nullptr) return nullptr;
-  auto refuse = [](PyObject* kind, const char* what) -> PyObject* {
+  if (lens == nullptr) return false;
+  auto refuse = [](PyObject* kind, const char* what) {
     PyErr_SetString(kind, what);
-    return nullptr;
+    return false;
   };
   const int64_t index = cuda_index(*k);
   if (index < 0 || cuda_index(*v) != index || cuda_index(*table) != index || cuda_index(*lens) != index)
@@ -271,10 +289,48 @@ PyObject* cache_new(PyObject* type, PyObject* const* args, size_t nargsf, PyObje
     return refuse(PyExc_ValueError, "lens must be a contiguous [batch] tensor");
   const int64_t capacity = max_pages * shape[1];
   void *weight = nullptr, *pos = nullptr, *seen = nullptr;
-  if (!numbers(in[4], at::kFloat, index, "weight", {batch, heads, capacity}, &weight) ||
+  if (!stored(*k, "k") || !stored(*v, "v") || !stored(*table, "page_table") || !stored(*lens, "lens") ||
+      !numbers(in[4], at::kFloat, index, "weight", {batch, heads, capacity}, &weight) ||
       !numbers(in[5], at::kInt, index, "pos", {batch, heads, capacity}, &pos) ||
       !numbers(in[6], at::kInt, index, "seen", {batch}, &seen))
-    return nullptr;
+    return false;
+  to->lens = in[3];
+  to->weight = in[4];
+  to->pos = in[5];
+  to->seen = in[6];
+  to->batch = batch;
+  to->capacity = capacity;
+  to->index = index;
+  to->kv_heads = heads;
+  to->head_dim = dim;
+  to->code = dtype == at::kHalf ? GEMM_TN_F16 : GEMM_TN_BF16;
+  to->type = dtype;
+  to->c = kv_cache{};
+  to->c.k = k->data_ptr();
+  to->c.v = v->data_ptr();
+  to->c.num_pages = shape[0];
+  to->c.page_size = shape[1];
+  to->c.kv_heads = heads;
+  to->c.head_dim = dim;
+  to->c.page_stride = strides[0];
+  to->c.slot_stride = strides[1];
+  to->c.head_stride = heads > 1 ? strides[2] : dim;
+  to->c.page_table = static_cast<const int32_t*>(table->data_ptr());
+  to->c.table_stride = batch > 1 ? table->stride(0) : max_pages;
+  to->c.max_pages = max_pages;
+  to->c.lens = static_cast<int32_t*>(lens->data_ptr());
+  to->c.weight = static_cast<float*>(weight);
+  to->c.pos = static_cast<int32_t*>(pos);
+  to->c.seen = static_cast<int32_t*>(seen);
+  return true;
+}
+
+PyObject* cache_new(PyObject* type, PyObject* const* args, size_t nargsf, PyObject* kwnames) {
+  HANDLE_TH_ERRORS
+  static const char* const names[] = {"k", "v", "page_table", "lens", "weight", "pos", "seen"};
+  PyObject* in[7];
+  Description made;
+  if (!place("KVCache", names, 4, args, PyVectorcall_NARGS(nargsf), kwnames, in) || !describe(in, &made)) return nullptr;
   PyObject* torch_type = PyObject_GetAttrString(in[0], "dtype");
   if (torch_type == nullptr) return nullptr;
   Cache* c = PyObject_GC_New(Cache, reinterpret_cast<PyTypeObject*>(type));
@@ -288,38 +344,29 @@ PyObject* cache_new(PyObject* type, PyObject* const* args, size_t nargsf, PyObje
     Py_INCREF(*to[i]);
   }
   c->dtype = torch_type;
-  c->batch = batch;
-  c->capacity = capacity;
-  c->index = index;
-  c->kv_heads = heads;
-  c->head_dim = dim;
-  c->code = dtype == at::kHalf ? GEMM_TN_F16 : GEMM_TN_BF16;
-  c->type = dtype;
-  c->c = kv_cache{};
-  c->c.k = k->data_ptr();
-  c->c.v = v->data_ptr();
-  c->c.num_pages = shape[0];
-  c->c.page_size = shape[1];
-  c->c.kv_heads = heads;
-  c->c.head_dim = dim;
-  c->c.page_stride = strides[0];
-  c->c.slot_stride = strides[1];
-  c->c.head_stride = heads > 1 ? strides[2] : dim;
-  c->c.page_table = static_cast<const int32_t*>(table->data_ptr());
-  c->c.table_stride = batch > 1 ? table->stride(0) : max_pages;
-  c->c.max_pages = max_pages;
-  c->c.lens = static_cast<int32_t*>(lens->data_ptr());
-  c->c.weight = static_cast<float*>(weight);
-  c->c.pos = static_cast<int32_t*>(pos);
-  c->c.seen = static_cast<int32_t*>(seen);
+  c->made = made;
   PyObject_GC_Track(reinterpret_cast<PyObject*>(c));
   return reinterpret_cast<PyObject*>(c);
   END_HANDLE_TH_ERRORS
 }
 
-const Cache* cache_of(PyObject* o) {
-  if (o != nullptr && Py_TYPE(o) == cache_type()) return reinterpret_cast<const Cache*>(o);
-  PyErr_SetString(PyExc_TypeError, "cache must be a KVCache");
+// The cache's tensors as they are now, in *now.
+const Description* cache_of(PyObject* o, Description* now) {
+  if (o == nullptr || Py_TYPE(o) != cache_type()) {
+    PyErr_SetString(PyExc_TypeError, "cache must be a KVCache");
+    return nullptr;
+  }
+  const Cache* c = reinterpret_cast<const Cache*>(o);
+  auto held = [](PyObject* x) { return x != Py_None ? x : nullptr; };
+  PyObject* const in[7] = {c->k, c->v, c->page_table, c->lens, held(c->weight), held(c->pos), held(c->seen)};
+  if (!describe(in, now)) return nullptr;
+  const kv_cache &x = now->c, &y = c->made.c;
+  if (now->batch == c->made.batch && now->index == c->made.index && now->type == c->made.type && x.num_pages == y.num_pages &&
+      x.page_size == y.page_size && x.kv_heads == y.kv_heads && x.head_dim == y.head_dim && x.max_pages == y.max_pages &&
+      x.page_stride == y.page_stride && x.slot_stride == y.slot_stride && x.head_stride == y.head_stride &&
+      x.table_stride == y.table_stride)
+    return now;
+  PyErr_SetString(PyExc_ValueError, "the cache's tensors have changed their sizes, strides or types since it was made");
   return nullptr;
 }
 
@@ -328,7 +375,7 @@ const Cache* cache_of(PyObject* o) {
 // One call of the library on the cache's device and its current stream; false
 // with GemmTnError set. The call itself throws nothing.
 template <class Call>
-bool run(const Cache* c, const char* name, Call call) {
+bool run(const Description* c, const char* name, Call call) {
   int rc;
   {
     const c10::cuda::CUDAGuard device(static_cast<c10::DeviceIndex>(c->index));
@@ -360,7 +407,7 @@ bool factor(PyObject* o, float* to) {
   return true;
 }
 
-bool queries(PyObject* o, const Cache* c, at::IntArrayRef* shape, kv_rows* to) {
+bool queries(PyObject* o, const Description* c, at::IntArrayRef* shape, kv_rows* to) {
   const Tensor* q = tensor(o, "q");
   if (q == nullptr) return false;
   *shape = q->sizes();
@@ -373,7 +420,7 @@ bool queries(PyObject* o, const Cache* c, at::IntArrayRef* shape, kv_rows* to) {
 }
 
 // rows and counts; max_rows is rows' width, `tokens` without rows.
-bool counted(const Cache* c, PyObject* rows, PyObject* counts, int64_t tokens, int32_t** d_rows, int32_t** d_counts,
+bool counted(const Description* c, PyObject* rows, PyObject* counts, int64_t tokens, int32_t** d_rows, int32_t** d_counts,
              int64_t* max_rows) {
   *max_rows = tokens;
   if (rows != nullptr) {
@@ -388,14 +435,15 @@ bool counted(const Cache* c, PyObject* rows, PyObject* counts, int64_t tokens, i
   return ints(rows, c, "rows", {c->batch, *max_rows}, d_rows) && ints(counts, c, "counts", {c->batch}, d_counts);
 }
 
-PyObject* or_own(PyObject* out, PyObject* own) { return out != nullptr ? out : (own != Py_None ? own : nullptr); }
+PyObject* or_own(PyObject* out, PyObject* own) { return out != nullptr ? out : own; }
 
 PyObject* tree_attn(PyObject*, PyObject* const* args, Py_ssize_t nargs, PyObject* kwnames) {
   HANDLE_TH_ERRORS
   static const char* const names[] = {"q", "cache", "k_new", "v_new", "mask", "token_lens", "scale", "out", "lse", "status"};
   PyObject* in[10];
   if (!place("tree_attn", names, 2, args, nargs, kwnames, in)) return nullptr;
-  const Cache* c = cache_of(in[1]);
+  Description now;
+  const Description* c = cache_of(in[1], &now);
   at::IntArrayRef shape;
   kv_rows q, k_new, v_new;
   if (c == nullptr || !queries(in[0], c, &shape, &q)) return nullptr;
@@ -458,7 +506,8 @@ PyObject* cache_append(PyObject*, PyObject* const* args, Py_ssize_t nargs, PyObj
   static const char* const names[] = {"cache", "k_new", "v_new", "counts", "rows", "lens_out", "seen_out", "status"};
   PyObject* in[8];
   if (!place("cache_append", names, 3, args, nargs, kwnames, in)) return nullptr;
-  const Cache* c = cache_of(in[0]);
+  Description now;
+  const Description* c = cache_of(in[0], &now);
   const Tensor* t = c != nullptr ? tensor(in[1], "k_new") : nullptr;
   if (t == nullptr) return nullptr;
   const at::IntArrayRef shape = t->sizes();
@@ -466,7 +515,7 @@ PyObject* cache_append(PyObject*, PyObject* const* args, Py_ssize_t nargs, PyObj
     PyErr_SetString(PyExc_ValueError, "k_new must be [batch, tokens, kv_heads, head_dim] with the cache's sizes");
     return nullptr;
   }
-  if (in[6] != nullptr && c->seen == Py_None) {
+  if (in[6] != nullptr && c->seen == nullptr) {
     PyErr_SetString(PyExc_ValueError, "seen_out needs a cache with seen");
     return nullptr;
   }
@@ -493,11 +542,12 @@ PyObject* cache_weigh(PyObject*, PyObject* const* args, Py_ssize_t nargs, PyObje
   static const char* const names[] = {"cache", "q", "lse", "counts", "rows", "causal", "scale", "out", "status"};
   PyObject* in[9];
   if (!place("cache_weigh", names, 3, args, nargs, kwnames, in)) return nullptr;
-  const Cache* c = cache_of(in[0]);
+  Description now;
+  const Description* c = cache_of(in[0], &now);
   at::IntArrayRef shape;
   kv_rows q;
   if (c == nullptr || !queries(in[1], c, &shape, &q)) return nullptr;
-  if (c->weight == Py_None) {
+  if (c->weight == nullptr) {
     PyErr_SetString(PyExc_ValueError, "the cache has no weight");
     return nullptr;
   }
@@ -532,7 +582,8 @@ PyObject* cache_evict(PyObject*, PyObject* const* args, Py_ssize_t nargs, PyObje
   static const char* const names[] = {"cache", "keep", "recent", "weight_out", "pos_out", "lens_out", "status"};
   PyObject* in[7];
   if (!place("cache_evict", names, 2, args, nargs, kwnames, in)) return nullptr;
-  const Cache* c = cache_of(in[0]);
+  Description now;
+  const Description* c = cache_of(in[0], &now);
   if (c == nullptr) return nullptr;
   if (in[1] == nullptr) {
     PyErr_SetString(PyExc_TypeError, "keep must be a whole number");
@@ -542,11 +593,11 @@ PyObject* cache_evict(PyObject*, PyObject* const* args, Py_ssize_t nargs, PyObje
   if (keep == -1 && PyErr_Occurred()) return nullptr;
   const long long recent = in[2] != nullptr ? PyLong_AsLongLong(in[2]) : 0;
   if (recent == -1 && PyErr_Occurred()) return nullptr;
-  if (c->weight == Py_None) {
+  if (c->weight == nullptr) {
     PyErr_SetString(PyExc_ValueError, "the cache has no weight");
     return nullptr;
   }
-  if (in[4] != nullptr && c->pos == Py_None) {
+  if (in[4] != nullptr && c->pos == nullptr) {
     PyErr_SetString(PyExc_ValueError, "pos_out needs a cache with pos");
     return nullptr;
   }

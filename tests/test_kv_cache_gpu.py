@@ -810,6 +810,62 @@ def test_a_cache_keeps_its_tensors_and_shows_them():
     assert sys.getrefcount(out) == 2 and gt.tree_attn(s.q.to(DEV), cache, out=out) is out
 
 
+def test_a_cache_follows_its_tensors_to_other_storage():
+    """Tensors given other storage after the cache was made: .data, set_ and resize_ to the same sizes; every call goes there."""
+    s = ref.make("bf16", 64, [30, 41], 3, 2, 2, 16, seed=68)
+    want = ref.attention(s)
+    for move in ("data", "set_", "resize_"):
+        wrong = ref.make("bf16", 64, [9, 5], 3, 2, 2, 16, seed=69, max_pages=s.table.shape[1])
+        cache, status = on_gpu(wrong)
+        for name in ("k", "v", "page_table", "lens", "weight", "pos", "seen"):
+            held, now = getattr(cache, name), {"page_table": s.table}.get(name, getattr(s, name, None)).to(DEV)
+            if move == "data":
+                held.data = now
+            elif move == "set_":
+                held.set_(now)
+            else:
+                shape = held.shape
+                held.resize_(4 * held.numel()).resize_(shape)      # the storage moves as it grows
+                held.copy_(now)
+        out, lse = run_attn(s, cache=cache)
+        ref.check_attention(out, lse, want, s, 7.0)
+        pool = cache.k
+        gt.cache_append(cache, s.k_new[:, :1].to(DEV), s.v_new[:, :1].to(DEV), status=status)
+        assert cache.lens.tolist() == [31, 42] and int(status.item()) == 0
+        assert ref.same(pool[int(s.table[1, 2]), 41 % 16].cpu(), s.k_new[1, 0])
+        kept = cache.weight.clone()
+        gt.cache_weigh(cache, s.q.to(DEV), lse.to(DEV), counts=torch.zeros(2, dtype=torch.int32, device=DEV))
+        assert ref.same(cache.weight, kept)
+        gt.cache_evict(cache, 20)
+        assert cache.lens.tolist() == [20, 20]
+
+
+def test_a_cache_refuses_tensors_that_no_longer_fit():
+    """Other sizes, types or a freed storage behind a cache's tensors: every call refuses, and touches nothing."""
+    s = ref.make("bf16", 64, [30, 40], 3, 2, 2, 16, seed=70)
+    q, kn, vn, lse = s.q.to(DEV), s.k_new.to(DEV), s.v_new.to(DEV), torch.zeros(s.q.shape[:3], device=DEV)
+
+    def freed(c):
+        c.v.untyped_storage().resize_(0)
+
+    def shorter(c):
+        c.weight.untyped_storage().resize_(c.weight.numel() * 4 - 4)
+
+    for spoil, what in [(lambda c: c.k.resize_(c.k.shape[0] - 1, *c.k.shape[1:]), "same strides"), (freed, "smaller than"),
+                        (shorter, "smaller than"), (lambda c: c.lens.resize_(1), "contiguous \\[batch\\]"),
+                        (lambda c: c.pos.resize_(3), "pos must be"),
+                        (lambda c: [c.k.resize_(1, *c.k.shape[1:]), c.v.resize_(1, *c.v.shape[1:])], "have changed"),
+                        (lambda c: [t.resize_(1, *t.shape[1:]) for t in (c.page_table, c.weight, c.pos)] +
+                         [t.resize_(1) for t in (c.lens, c.seen)], "have changed")]:
+        cache, _ = on_gpu(s)
+        spoil(cache)
+        for call in (lambda: gt.tree_attn(q, cache, kn, vn), lambda: gt.cache_append(cache, kn, vn),
+                     lambda: gt.cache_weigh(cache, q, lse), lambda: gt.cache_evict(cache, 8)):
+            with pytest.raises(ValueError, match=what):
+                call()
+    torch.cuda.synchronize()
+
+
 def test_empty_calls():
     s = ref.make("bf16", 64, [5], 2, 1, 1, 8, seed=63)
     cache, status = on_gpu(s)
