@@ -14,8 +14,8 @@
 // Keys are read once (dim * 2 bytes each) per 256 query rows against one
 // exponential per key and row: up to about 150 rows HBM bounds the kernel,
 // past that the exponentials do. GB300: 32 tokens of 32 heads over 8 KV heads
-// (128 rows), dim 128, 8 sequences of 9001 to 16384 slots, 231 MB: 43.6 us, 5.3
-// TB/s; one token of 16 heads of dim 64, 4 sequences of 300 to 1024 slots: 7.2.
+// (128 rows), dim 128, 8 sequences of 9001 to 16384 slots, 231 MB: 43.7 us, 5.3
+// TB/s; one token of 16 heads of dim 64, 4 sequences of 300 to 1024 slots: 7.3.
 //
 // Work: an item is (sequence, KV head); the items' 128-key tiles, laid end to end
 // a change of items apart, are cut into equal contiguous chunks, one per CTA
@@ -497,9 +497,12 @@ __global__ void __launch_bounds__(C::kNumThreads, 1) cache_weigh_kernel(const __
           // two columns an instruction: p = 2^(s c - ref), sum += p factor. The next
           // 32 columns come from tensor memory while these are worked on.
           const uint64_t cc = f32x2_pack(c_log2, c_log2);
-          uint64_t sum01 = f32x2_pack(0.0f, 0.0f), sum23 = sum01;
+          uint64_t sum01, sum23;
           uint32_t raw[2][32];
           auto columns = [&](const uint32_t (&x)[32], int c0, auto mask) {
+            uint32_t hidden = 0;   // columns that weigh nothing (factor 0), and that do not see the key
+            if constexpr (mask.value)
+              hidden = __ballot_sync(0xffffffffu, block_ref[cw::kMaxRows + c0 + static_cast<int>(lane)] == 0.0f) | cache::low_bits(low - c0);
             const ulonglong2* refs = reinterpret_cast<const ulonglong2*>(block_ref + c0);
             const ulonglong2* factors = reinterpret_cast<const ulonglong2*>(block_ref + cw::kMaxRows + c0);
 #pragma unroll
@@ -513,17 +516,18 @@ __global__ void __launch_bounds__(C::kNumThreads, 1) cache_weigh_kernel(const __
               p2 = ex2_approx(p2);
               p3 = ex2_approx(p3);
               if constexpr (mask.value) {
-                if (c0 + e < low) p0 = 0.0f;
-                if (c0 + e + 1 < low) p1 = 0.0f;
-                if (c0 + e + 2 < low) p2 = 0.0f;
-                if (c0 + e + 3 < low) p3 = 0.0f;
+                if ((hidden >> e) & 1u) p0 = 0.0f;
+                if ((hidden >> (e + 1)) & 1u) p1 = 0.0f;
+                if ((hidden >> (e + 2)) & 1u) p2 = 0.0f;
+                if ((hidden >> (e + 3)) & 1u) p3 = 0.0f;
               }
               sum01 = f32x2_fma(f32x2_pack(p0, p1), f.x, sum01);
               sum23 = f32x2_fma(f32x2_pack(p2, p3), f.y, sum23);
             }
           };
-          // the columns c0 .. of a half, end - c0 of them
+          // this key's sum over the columns c0 .. of a half, end - c0 of them
           auto half = [&](uint32_t t_buf, int c0, int end, auto mask) {
+            sum01 = sum23 = f32x2_pack(0.0f, 0.0f);
             tmem_load_32x32(t_buf, raw[0]);
             for (; c0 < end; c0 += 64, t_buf += 64u) {
               tmem_load_wait();
@@ -535,23 +539,37 @@ __global__ void __launch_bounds__(C::kNumThreads, 1) cache_weigh_kernel(const __
                 columns(raw[1], c0 + 32, mask);
               }
             }
+            float sum0, sum1, sum2, sum3;
+            f32x2_unpack(sum01, sum0, sum1);
+            f32x2_unpack(sum23, sum2, sum3);
+            return (sum0 + sum1) + (sum2 + sum3);
           };
+          float total = 0.0f;
           for (int c0 = 0; c0 < cols; c0 += cw::kHalf, ++used) {
             const int buf = used & 1;
             if (!(ok = wd.warp_wait(s_full(g, buf), static_cast<uint32_t>(used >> 1) & 1u))) break;
             tc_fence_after_sync();
             const uint32_t t_buf = t_s + cw::kHalf * static_cast<uint32_t>(buf);
-            if (masked) half(t_buf, c0, min(cols, c0 + cw::kHalf), std::true_type{});
-            else half(t_buf, c0, min(cols, c0 + cw::kHalf), std::false_type{});
+            // Rows that weigh nothing (the padding, queries that are none) are zeros with
+            // a factor of 0, which is enough but for a key with an infinity or a NaN:
+            // where a sum is none, it is taken again without them. (Leaving them out at
+            // once, by a bit a column wherever there are some, took 256 rows over 8
+            // sequences of up to 8192 slots from 42.8 us to 43.9, one row of 4 heads over
+            // 40 of up to 1000 from 16.1 to 16.5; this way takes 44.4 and 16.1.)
+            float sum = 0.0f;
+            bool again = masked;
+            if (!masked) {
+              sum = half(t_buf, c0, min(cols, c0 + cw::kHalf), std::false_type{});
+              again = __any_sync(0xffffffffu, sum != sum);
+            }
+            if (again) sum = half(t_buf, c0, min(cols, c0 + cw::kHalf), std::true_type{});
+            total += sum;
             tc_fence_before_sync();
             __syncwarp();
             if (lane == 0) mbar_arrive(s_empty(g, buf));
           }
           if (!ok) break;
-          float sum0, sum1, sum2, sum3;
-          f32x2_unpack(sum01, sum0, sum1);
-          f32x2_unpack(sum23, sum2, sum3);
-          if (live) args.weight_out[weight_row + key] = acc + ((sum0 + sum1) + (sum2 + sum3));
+          if (live) args.weight_out[weight_row + key] = acc + total;
         }
         __syncwarp();
         if (lane == 0)

@@ -143,6 +143,9 @@ GEMM_TN_API int kv_cache_append(int dtype, int64_t batch, int64_t tokens, const 
  * tree_attn_fwd writes it). causal non-zero: the counted rows are the queries of
  * the newest counts[b] slots, in order, and row i counts for slots s <
  * lens[b] - counts[b] + i + 1 only; zero: every row counts for every slot.
+ * A counted row adds nothing where its lse is infinite (-inf: it saw no key) or
+ * its entry of rows is out of range, whatever the keys hold; neither does a row
+ * to a slot that it does not count for.
  * weight_out may be cache->weight; entries from lens[b] on are left as they
  * were. Sums are fp32. The same limits and errors as tree_attn_fwd.
  */

@@ -453,6 +453,42 @@ def test_weights_of_ragged_items_over_the_ctas(batch, longest, tokens):
     assert ref.same(out[~live], s.weight[~live]) and int(status.item()) == 0
 
 
+@pytest.mark.parametrize("causal", [True, False])
+@pytest.mark.parametrize("batch,tokens,kv_heads,group", [(1, 3, 1, 2), (3, 9, 2, 8), (2, 70, 1, 7), (3, 32, 1, 8), (40, 1, 8, 4), (40, 5, 8, 3)])
+def test_keys_that_weigh_nothing_keep_their_weight_whatever_they_hold(batch, tokens, kv_heads, group, causal):
+    """Infinities and NaN in keys that no query counts for, and infinite keys whose scores are all -inf: no row that the
+    kernel pads with, and no row that is none, may bring them in."""
+    lens = [200 + 37 * b % 190 for b in range(batch)]
+    counts = [0 if b % 3 == 2 else 1 + (5 * b + tokens - 1) % tokens for b in range(batch)]
+    s = ref.make("bf16", 64, lens, tokens, kv_heads, group, 16, seed=31 + tokens)
+    s.q[..., 5] = -s.q[..., 5].abs() - 0.5
+    g = torch.Generator().manual_seed(32)
+    rows = torch.stack([torch.randperm(tokens, generator=g) for _ in lens]).to(torch.int32)
+    lse = torch.full(s.q.shape[:3], 7.0)
+    want, tol = ref.weigh(s, lse, rows, counts, causal)
+    bad = torch.zeros(want.shape, dtype=torch.bool)
+    for b, n in enumerate(lens):
+        at = torch.arange(b % 7, n, 7)
+        bad[b, :, at] = True
+        s.k[s.table[b].long()[at // 16], at % 16, :, 5] = float("nan") if counts[b] == 0 and b % 2 else float("inf")
+    live = (torch.arange(want.shape[2])[None, None, :] < s.lens[:, None, None]).expand(want.shape)
+    for none in (None, -1, tokens):              # a counted row of sequence 0 that is no token weighs nothing
+        if none is not None:
+            if counts[0] > 1:
+                continue
+            rows[0, 0] = none
+            want[0] = s.weight[0].double()
+        cache, status = on_gpu(s)
+        gt.cache_weigh(cache, s.q.to(DEV), lse.to(DEV), counts=torch.tensor(counts, dtype=torch.int32, device=DEV),
+                       rows=rows.to(DEV), causal=causal, status=status)
+        torch.cuda.synchronize()
+        assert int(status.item()) == (0 if none is None else gt.GEMM_TN_ERR_INVALID_VALUE)
+        out = cache.weight.cpu()
+        assert ref.same(out[bad | ~live], s.weight[bad | ~live])
+        off = (out.double() - want).abs()
+        assert bool((off[live & ~bad] <= tol[live & ~bad]).all()), float((off - tol)[live & ~bad].max())
+
+
 def test_weights_of_one_pass_sum_to_the_rows():
     """With the attention's own lse every counted row's weights over the slots sum to one."""
     s = ref.make("bf16", 128, [2000, 333], 6, 2, 4, 64, seed=30)
