@@ -6,7 +6,8 @@ Each translation unit under ``csrc/`` is compiled by nvcc in parallel with one
 this package directory. Objects go to ``_build/`` at the repository root.
 The CUDA runtime is linked statically, so the library only needs the driver.
 The extension module is one C++ file over torch's headers (g++), compiled at
-the same time.
+the same time. The library needs none of it: without a torch that has CUDA, or
+where the module does not compile, it is there all the same.
 
     python -m dense_tiled_gemm_03_gb300.build [--force] [--ptxas-verbose]
 """
@@ -67,12 +68,15 @@ def binding_is_stale() -> bool:
     return any(p.stat().st_mtime > BINDING.stat().st_mtime for p in inputs)
 
 
-def build_binding() -> Path:
-    """Compile the extension module against the installed torch (found, not imported)."""
+def torch_dir() -> Path | None:
+    """Where the installed torch lies (found, not imported); None for no torch, or one without CUDA."""
     spec = importlib.util.find_spec("torch")
-    if spec is None:
-        raise RuntimeError("torch not found: the paged cache's binding is built against its headers")
-    torch_dir = Path(spec.submodule_search_locations[0])
+    found = Path(spec.submodule_search_locations[0]) if spec is not None and spec.submodule_search_locations else None
+    return found if found is not None and (found / "lib" / "libc10_cuda.so").exists() else None
+
+
+def build_binding(torch_dir: Path) -> Path:
+    """Compile the extension module against that torch."""
     cuda = Path(nvcc()).resolve().parent.parent
     tmp = BINDING.with_name(f".{BINDING.name}.{os.getpid()}")
     cmd = ["g++", "-O2", "-std=c++17", "-fPIC", "-shared", "-fvisibility=hidden", str(BINDING_SOURCE), "-o", str(tmp),
@@ -96,26 +100,30 @@ def _compile(src: Path, obj: Path, verbose_ptxas: bool) -> None:
         sys.stderr.write(res.stdout + res.stderr)
 
 
-def build(force: bool = False, verbose_ptxas: bool = False) -> Path:
-    """Compile and link libgemm_tn.so and the binding if a source changed (or if forced). Returns the library's path."""
-    all_of_it = force or verbose_ptxas
-    if not all_of_it and not is_stale():
-        if binding_is_stale():
-            build_binding()
-        return LIBRARY
-    BUILD_DIR.mkdir(parents=True, exist_ok=True)
-    objs = [BUILD_DIR / (Path(s).stem + ".o") for s in SOURCES]
-    with ThreadPoolExecutor(max_workers=len(SOURCES) + 1) as pool:
-        binding = pool.submit(build_binding) if all_of_it or binding_is_stale() else None
-        list(pool.map(lambda so: _compile(CSRC / so[0], so[1], verbose_ptxas), zip(SOURCES, objs)))
-        if binding is not None:
-            binding.result()
+def _link(objs: list[Path]) -> None:
     tmp = LIBRARY.with_name(f".libgemm_tn.{os.getpid()}.so")
     cmd = [nvcc(), *GENCODE, "-shared", "-Xcompiler", "-fPIC", *map(str, objs), "-o", str(tmp)]
     res = subprocess.run(cmd, capture_output=True, text=True)
     if res.returncode != 0:
         raise RuntimeError(f"link failed:\n{res.stdout}\n{res.stderr}")
     os.replace(tmp, LIBRARY)
+
+
+def build(force: bool = False, verbose_ptxas: bool = False) -> Path:
+    """Compile and link libgemm_tn.so and the binding if a source changed (or if forced). Returns the library's path."""
+    all_of_it = force or verbose_ptxas
+    torch = torch_dir()
+    if torch is None:
+        sys.stderr.write("no torch with CUDA found: the paged cache's Python binding is not built\n")
+    with ThreadPoolExecutor(max_workers=len(SOURCES) + 1) as pool:
+        binding = pool.submit(build_binding, torch) if torch is not None and (all_of_it or binding_is_stale()) else None
+        if all_of_it or is_stale():
+            BUILD_DIR.mkdir(parents=True, exist_ok=True)
+            objs = [BUILD_DIR / (Path(s).stem + ".o") for s in SOURCES]
+            list(pool.map(lambda so: _compile(CSRC / so[0], so[1], verbose_ptxas), zip(SOURCES, objs)))
+            _link(objs)
+        if binding is not None:
+            binding.result()
     return LIBRARY
 
 

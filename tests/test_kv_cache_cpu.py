@@ -304,6 +304,48 @@ def test_a_missing_binding_fails_loudly(lib, monkeypatch):
         _cache.binding()
 
 
+# ---------------------------------------------------------------- the build
+
+@pytest.fixture
+def small_build(monkeypatch, tmp_path):
+    """The build step with one source, and everything that it makes elsewhere."""
+    from dense_tiled_gemm_03_gb300 import build as b
+    for name, value in (("SOURCES", ["repack.cu"]), ("BUILD_DIR", tmp_path / "objects"), ("LIBRARY", tmp_path / "lib.so"),
+                        ("BINDING", tmp_path / "binding.so")):
+        monkeypatch.setattr(b, name, value)
+    return b
+
+
+@pytest.mark.parametrize("torch_is", ["missing", "without CUDA"])
+def test_the_library_builds_without_torch(small_build, monkeypatch, tmp_path, torch_is, capsys):
+    import importlib.util
+    from types import SimpleNamespace
+    find = importlib.util.find_spec
+    spec = None if torch_is == "missing" else SimpleNamespace(submodule_search_locations=[str(tmp_path)])
+    monkeypatch.setattr(importlib.util, "find_spec", lambda name, *a: spec if name == "torch" else find(name, *a))
+    assert small_build.build() == small_build.LIBRARY and small_build.LIBRARY.exists()
+    assert not small_build.BINDING.exists() and "no torch" in capsys.readouterr().err
+
+
+def test_a_binding_that_does_not_compile_leaves_the_library(small_build, monkeypatch, tmp_path):
+    broken = tmp_path / "broken.cpp"
+    broken.write_text("#error no binding\n")
+    monkeypatch.setattr(small_build, "BINDING_SOURCE", broken)
+    with pytest.raises(RuntimeError, match="no binding"):
+        small_build.build()
+    assert small_build.LIBRARY.exists() and not small_build.BINDING.exists()
+
+
+def test_the_package_loads_its_library_without_torch(lib):
+    import subprocess
+    import sys
+    from pathlib import Path
+    code = ("import sys; sys.modules['torch'] = None\n"
+            "import dense_tiled_gemm_03_gb300 as gt\n"
+            "assert gt.gemm_tn_version() > 0 and gt.gemm_tn_select_config(0, 256, 256, 256) >= 0\n")
+    subprocess.run([sys.executable, "-c", code], check=True, cwd=Path(__file__).resolve().parents[1])
+
+
 # ---------------------------------------------------------------- tree masks
 
 def test_tree_mask():
