@@ -46,11 +46,14 @@ BOUND = ("KVCache", "tree_attn", "cache_append", "cache_weigh", "cache_evict")
 
 
 def binding():
-    """The extension module, bound to the loaded library; raises if either has not been built."""
-    import torch  # noqa: F401  (loads the libraries that the module is linked to)
+    """The extension module, bound to the loaded library; raises if either has not been built, or the module against
+    another torch (whose objects it reads in place)."""
+    import torch  # loads the libraries that the module is linked to
     lib = library()
     try:
         from . import _kv_cache
+        if _kv_cache.built_against != torch.__version__:
+            raise ImportError(f"built against torch {_kv_cache.built_against}, not {torch.__version__}")
     except ImportError as e:
         raise RuntimeError("the paged cache's binding is missing or does not fit the installed torch: build it with "
                            "`python -m dense_tiled_gemm_03_gb300.build --force`") from e

@@ -16,6 +16,7 @@ from __future__ import annotations
 import argparse
 import importlib.util
 import os
+import re
 import shutil
 import subprocess
 import sys
@@ -61,8 +62,20 @@ def is_stale() -> bool:
     return any(p.stat().st_mtime > built for p in _inputs())
 
 
-def binding_is_stale() -> bool:
-    if not BINDING.exists():
+def torch_version(torch_dir: Path) -> str:
+    """The version that the torch there states of itself (torch.__version__)."""
+    return re.search(r"""^__version__\s*=\s*['"]([^'"]+)""", (torch_dir / "version.py").read_text(), re.MULTILINE).group(1)
+
+
+def _binding_stamp() -> Path:
+    return BUILD_DIR / "binding_torch.txt"
+
+
+def binding_is_stale(torch_dir: Path) -> bool:
+    """Whether the module is missing, older than its sources, or built against another torch."""
+    if not BINDING.exists() or not _binding_stamp().exists():
+        return True
+    if _binding_stamp().read_text() != f"{torch_dir} {torch_version(torch_dir)}":
         return True
     inputs = [BINDING_SOURCE, Path(__file__), *INCLUDE.glob("*.h")]
     return any(p.stat().st_mtime > BINDING.stat().st_mtime for p in inputs)
@@ -79,13 +92,17 @@ def build_binding(torch_dir: Path) -> Path:
     """Compile the extension module against that torch."""
     cuda = Path(nvcc()).resolve().parent.parent
     tmp = BINDING.with_name(f".{BINDING.name}.{os.getpid()}")
+    version = torch_version(torch_dir)
     cmd = ["g++", "-O2", "-std=c++17", "-fPIC", "-shared", "-fvisibility=hidden", str(BINDING_SOURCE), "-o", str(tmp),
+           f'-DKV_CACHE_TORCH="{version}"',
            "-I", str(INCLUDE), "-I", str(torch_dir / "include"), "-I", sysconfig.get_paths()["include"],
            "-I", str(cuda / "include"), "-L", str(torch_dir / "lib"), "-lc10", "-lc10_cuda", "-ltorch_cpu", "-ltorch_python"]
     res = subprocess.run(cmd, capture_output=True, text=True)
     if res.returncode != 0:
         raise RuntimeError(f"g++ failed for {BINDING_SOURCE.name}:\n{res.stdout}\n{res.stderr}")
     os.replace(tmp, BINDING)
+    BUILD_DIR.mkdir(parents=True, exist_ok=True)
+    _binding_stamp().write_text(f"{torch_dir} {version}")
     return BINDING
 
 
@@ -116,7 +133,7 @@ def build(force: bool = False, verbose_ptxas: bool = False) -> Path:
     if torch is None:
         sys.stderr.write("no torch with CUDA found: the paged cache's Python binding is not built\n")
     with ThreadPoolExecutor(max_workers=len(SOURCES) + 1) as pool:
-        binding = pool.submit(build_binding, torch) if torch is not None and (all_of_it or binding_is_stale()) else None
+        binding = pool.submit(build_binding, torch) if torch is not None and (all_of_it or binding_is_stale(torch)) else None
         if all_of_it or is_stale():
             BUILD_DIR.mkdir(parents=True, exist_ok=True)
             objs = [BUILD_DIR / (Path(s).stem + ".o") for s in SOURCES]

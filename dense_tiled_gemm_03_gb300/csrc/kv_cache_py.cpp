@@ -702,5 +702,10 @@ PyMODINIT_FUNC PyInit__kv_cache() {
     Py_DECREF(m);
     return nullptr;
   }
+  // the torch whose headers this was compiled with
+  if (PyModule_AddStringConstant(m, "built_against", KV_CACHE_TORCH) < 0) {
+    Py_DECREF(m);
+    return nullptr;
+  }
   return m;
 }

@@ -336,6 +336,25 @@ def test_a_binding_that_does_not_compile_leaves_the_library(small_build, monkeyp
     assert small_build.LIBRARY.exists() and not small_build.BINDING.exists()
 
 
+def test_a_binding_built_against_another_torch_is_stale(lib, monkeypatch, tmp_path):
+    from dense_tiled_gemm_03_gb300 import build as b
+    here = b.torch_dir()
+    assert b.torch_version(here) == torch.__version__ and not b.binding_is_stale(here)
+    other = tmp_path / "torch"
+    other.mkdir()
+    (other / "version.py").write_text((here / "version.py").read_text())
+    assert b.binding_is_stale(other)                       # elsewhere
+    monkeypatch.setattr(b, "torch_version", lambda d: "0.0.1+cu1")
+    assert b.binding_is_stale(here)                        # there, another version
+
+
+def test_a_binding_built_against_another_torch_is_not_used(lib, monkeypatch):
+    assert _cache.binding().built_against == torch.__version__
+    monkeypatch.setattr(torch, "__version__", "0.0.1+cu1")
+    with pytest.raises(RuntimeError, match="build it"):
+        _cache.binding()
+
+
 def test_the_package_loads_its_library_without_torch(lib):
     import subprocess
     import sys
