@@ -20,3 +20,18 @@ def pytest_configure(config):
 def oracle_lib():
     import oracle
     return oracle.load_library()
+
+
+#: files whose tests hand the C ABI made-up addresses, some of them in calls that are
+#: valid but for the device: where a GPU is visible a kernel would follow them
+MADE_UP_ADDRESSES = ("test_abi_cpu.py", "test_kv_cache_cpu.py")
+
+
+def pytest_collection_modifyitems(items):
+    mine = [item for item in items if item.path.name in MADE_UP_ADDRESSES]
+    if not mine:
+        return
+    import torch
+    if torch.cuda.is_available():
+        for item in mine:
+            item.add_marker(pytest.mark.skip(reason="made-up addresses: run where no GPU is visible (CUDA_VISIBLE_DEVICES=)"))
