@@ -527,11 +527,15 @@ __global__ void __launch_bounds__(C::kNumThreads) __maxnreg__(C::kMaxRegs)
           };
           // A row's reference is the maximum of the first tile in which it sees
           // a key; later tiles are taken against it at once. No probability
-          // exceeds 2^8 unless the row sum does, so only then is the tile's
-          // maximum taken, and moved to where it is past that factor (the warp
-          // then computes the tile again and rescales O: the same softmax).
+          // exceeds 2^8 unless the row's sum over the tile does, so only then is
+          // the tile's maximum taken, and the reference moved there (the warp
+          // then computes the tile again and rescales O: the same softmax). It
+          // moves for the sum, not for a probability past 2^8: keys that all lie
+          // a little above the first tile's would else be computed twice, tile
+          // after tile (256 tokens over 8192 keys 1 to 7 powers of two above the
+          // first tile's: 84 us, and 66 where nothing moves).
           // One copy of the code for both: it is long, and fetched cold.
-          float alpha = 1.0f, sum;
+          float alpha = 1.0f, sum = 0.0f;
           bool take_max = __any_sync(0xffffffffu, unset);
           while (true) {
             if (take_max) {
@@ -541,13 +545,13 @@ __global__ void __launch_bounds__(C::kNumThreads) __maxnreg__(C::kMaxRegs)
                   m_ref = m_tile;
                   unset = false;
                 }
-              } else if (live && m_tile > m_ref + 8.0f) {
+              } else if (live && (m_tile > m_ref + 8.0f || (sum > 256.0f && m_tile > m_ref))) {
                 alpha = ex2_approx(m_ref - m_tile);
                 m_ref = m_tile;
               }
             }
             sum = exp_pass(-m_ref);
-            if (take_max || !__any_sync(0xffffffffu, live && !(sum <= 256.0f))) break;
+            if (take_max || !__any_sync(0xffffffffu, live && sum > 256.0f)) break;   // (a NaN's row is lost either way)
             take_max = true;
             tmem_store_wait();   // the first pass's stores land before they are overwritten
           }

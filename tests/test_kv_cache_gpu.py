@@ -216,6 +216,58 @@ def test_scores_far_below_the_first_tiles():
         ref.check_attention(out, lse, ref.attention(s), s, 7.0)
 
 
+def replayed_us(call, calls=8, replays=9):
+    """Shortest time of a call in a replayed graph of several."""
+    stream = torch.cuda.Stream()
+    with torch.cuda.stream(stream):
+        call()
+        stream.synchronize()
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph, stream=stream):
+            for _ in range(calls):
+                call()
+        best = float("inf")
+        for _ in range(replays):
+            start, end = (torch.cuda.Event(enable_timing=True) for _ in range(2))
+            start.record()
+            graph.replay()
+            end.record()
+            stream.synchronize()
+            best = min(best, start.elapsed_time(end) * 1e3 / calls)
+    return best
+
+
+def risen(tokens, lens, heads, group, dim, rise, dtype=torch.bfloat16):
+    """Queries and keys whose scores lie `rise` powers of two above the first 128 keys' from there on."""
+    s = ref.make("bf16", dim, lens, tokens, heads, group, 64, seed=13, q_scale=0.05)
+    q, k = s.q.float(), s.k.float() * 0.05
+    q[..., 0], k[..., 0] = 10.0, 1.0 + rise * math.log(2) * math.sqrt(dim) / 10.0
+    for b in range(len(lens)):
+        k[s.table[b, :2].long(), :, :, 0] = 1.0
+    s.q, s.k = q.to(s.dtype), k.to(s.dtype)
+    return s
+
+
+@pytest.mark.parametrize("tokens,group", [(1, 4), (20, 4), (70, 4)])
+@pytest.mark.parametrize("rise", [1.5, 3.0, 7.0, 9.0])
+def test_scores_a_little_above_the_first_tiles(rise, tokens, group):
+    s = risen(tokens, [900, 333], 2, group, 64, rise)
+    out, lse = run_attn(s, use_new=False)
+    ref.check_attention(out, lse, ref.attention(s, use_new=False), s, 7.0)
+
+
+def test_scores_a_little_above_the_first_tiles_take_no_longer():
+    """Their exponentials once a tile, as where no reference moves. (Twice, they are over half of a tile's time: 1.28 of it.)"""
+    times = []
+    for rise in (0.0, 3.0):
+        s = risen(256, [8192, 8192], 8, 4, 128, rise)
+        s.k.nan_to_num_(0.0)
+        cache, _ = on_gpu(s)
+        q, out = s.q.to(DEV), torch.zeros(s.q.shape, dtype=s.dtype, device=DEV)
+        times.append(replayed_us(lambda: gt.tree_attn(q, cache, out=out)))
+    assert times[1] <= 1.1 * times[0], times
+
+
 def test_pool_and_input_layouts():
     """[page][head][row] pools, K and V in one tensor, q, k, v side by side in one projection."""
     s = ref.make("bf16", 128, [200, 131], 5, 4, 2, 16, [5, 3], seed=9)
