@@ -428,8 +428,13 @@ __global__ void __launch_bounds__(C::kNumThreads, 1) decode_attn_kernel(const __
       const uint32_t row_bits = cache::low_bits(rows);
       uint32_t unset = row_bits;            // rows that have seen no key yet
       float neg_m[C::kRows], l[C::kRows];   // minus the row's reference, in units of scale * log2e; this key lane's sum
+      // Rows that do not exist, whose queries may be anything: a reference of infinity
+      // makes their probabilities 0 (or NaN), which call for no new references.
 #pragma unroll
-      for (int r = 0; r < C::kRows; ++r) neg_m[r] = l[r] = 0.0f;
+      for (int r = 0; r < C::kRows; ++r) {
+        neg_m[r] = (row_bits >> r) & 1u ? 0.0f : -INFINITY;
+        l[r] = 0.0f;
+      }
       for (int i = u; i < w.count && ok; i += 2) {
         // S_u for this tile is complete, and with it O_u += P_u V of the tile before
         if (!(ok = wd.warp_wait(s_full(u), tiles_done & 1u))) break;
