@@ -536,6 +536,43 @@ def test_weights_of_ragged_items_over_the_ctas(batch, longest, tokens):
     assert ref.same(out[~live], s.weight[~live]) and int(status.item()) == 0
 
 
+@pytest.mark.parametrize("none", [False, True])
+@pytest.mark.parametrize("tokens,group", [(1, 4), (20, 4), (32, 4), (40, 4), (70, 7)])
+@pytest.mark.parametrize("batch,longest", [(19, 700), (45, 130)])
+def test_weights_of_chosen_rows_over_the_ctas(batch, longest, tokens, group, none):
+    """Listed rows where a CTA has several items, so that each way of gathering queries looks them up (up to 128 rows ahead of
+    the item, more between items); uncounted tokens hold NaN; rows that are no token are reported and weigh nothing."""
+    lens = [(97 * b * b + longest) % (longest + 1) if b % 4 != 1 else 0 for b in range(batch)]
+    counts = [0 if b % 5 == 2 else min(n, 1 + (7 * b + tokens - 1) % tokens) for b, n in enumerate(lens)]
+    s = ref.make("fp16", 64, lens, tokens, 8, group, 32, seed=tokens + batch)
+    g = torch.Generator().manual_seed(33)
+    rows = torch.stack([torch.randperm(tokens, generator=g) for _ in lens]).to(torch.int32)
+    lse = math.log(longest) + 2.0 + torch.rand(s.q.shape[:3], generator=g)
+    for b, n in enumerate(counts):
+        s.q[b, rows[b, n:].long()] = float("nan")
+        lse[b, rows[b, n:].long()] = float("nan")
+    clean_lse = lse.clone()
+    if none:
+        hit = [b for b, n in enumerate(counts) if n > 0 and b % 3 == 0]
+        assert hit
+        for b in hit:                    # for the reference: a token whose lse leaves it no weight
+            clean_lse[b, int(rows[b, counts[b] // 2])] = 1e30
+    want, tol = ref.weigh(s, clean_lse, rows, counts, True)
+    if none:
+        for x, b in enumerate(hit):
+            rows[b, counts[b] // 2] = (-1, tokens, 2 ** 31 - 1, -2 ** 31)[x % 4]
+    cache, status = on_gpu(s)
+    gt.cache_weigh(cache, s.q.to(DEV), lse.to(DEV), counts=torch.tensor(counts, dtype=torch.int32, device=DEV),
+                   rows=rows.to(DEV), status=status)
+    torch.cuda.synchronize()
+    assert int(status.item()) == (gt.GEMM_TN_ERR_INVALID_VALUE if none else 0)
+    out = cache.weight.cpu()
+    live = (torch.arange(out.shape[2])[None, None, :] < s.lens[:, None, None]).expand(out.shape)
+    off = (out.double() - want).abs()
+    assert bool((off[live] <= tol[live]).all()), float((off - tol)[live].max())
+    assert ref.same(out[~live], s.weight[~live])
+
+
 @pytest.mark.parametrize("causal", [True, False])
 @pytest.mark.parametrize("batch,tokens,kv_heads,group", [(1, 3, 1, 2), (3, 9, 2, 8), (2, 70, 1, 7), (3, 32, 1, 8), (40, 1, 8, 4), (40, 5, 8, 3)])
 def test_keys_that_weigh_nothing_keep_their_weight_whatever_they_hold(batch, tokens, kv_heads, group, causal):
