@@ -76,8 +76,9 @@ def tree_mask(parents):
     [batch, tokens]; parents[b][i] < i is the token that i was drafted after, -1
     for one drafted right after the cached ones. Token i sees itself and its
     ancestors. Returns int64 [batch, tokens, ceil(tokens / 64)] on parents'
-    device (bit j % 64 of word j / 64: i sees j). Plain torch operations; a tree
-    shape is made once and reused."""
+    device (bit j % 64 of word j / 64: i sees j). Host code, a loop over the tokens:
+    it waits for a CUDA tensor and cannot be captured, so make the mask of a tree
+    shape once and reuse it."""
     import torch
     if parents.dim() != 2 or parents.is_floating_point() or parents.dtype == torch.bool:
         raise ValueError("parents must be an integer [batch, tokens] tensor")

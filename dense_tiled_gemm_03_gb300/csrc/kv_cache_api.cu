@@ -226,11 +226,11 @@ constexpr int kMaxChange = 8;   // of this and of weigh_change_tiles
 
 // The same for the accumulated weights. Up to 128 query rows are gathered ahead;
 // more of them between the items (past 256 a tile is walked once per 256, and the
-// change is worth fewer of them). GB300, us a call with gaps of 0, 2, 4 and 8: 1
-// row per KV head, 32 sequences of up to 2048 slots 23.4, 23.0, 23.5 and 24.4; 128
-// rows, 8 of up to 16384 43.9, 43.6, 43.9 and 44.6, 2 of 8192 14.4, 13.3, 13.8 and
-// 13.9; 256 rows, 8 of up to 8192 46.1, 45.2, 43.8 and 40.8; 700 rows, 2 of up to
-// 4000 38.6, 38.4, 38.5 and 41.0.
+// change is worth fewer of them: 2 and 4 do the same there). GB300, us a call with
+// gaps of 0, 2, 4 and 8: 1 token of 4 heads per KV head, 32 sequences of up to
+// 2048 slots 23.4, 22.9, 23.4 and 24.4; 128 rows, 8 of up to 16384 44.3, 43.8, 44.0
+// and 44.8, 2 of 8192 14.5, 13.5, 13.9 and 13.9; 256 rows, 8 of up to 8192 47.2,
+// 46.2, 44.8 and 41.8; 700 rows, 2 of up to 4000 39.2, 39.1, 39.1 and 41.4.
 int weigh_change_tiles(int64_t rows) { return rows <= 128 ? 2 : (rows <= 256 ? 8 : 4); }
 
 // CTAs of a cluster that share each of `items` items of `tiles` key tiles, one

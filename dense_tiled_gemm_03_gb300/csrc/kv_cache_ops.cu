@@ -5,9 +5,9 @@
 //
 // Both are bound by the bytes they move. Rows go 16 bytes a thread, a row of
 // one head on 8 or 16 neighbouring threads. GB300: 2 x 8192 tokens of 8 KV
-// heads of dim 128 appended (135 MB) in 25.3 us, 5.3 TB/s; 8 sequences of 12001
-// to 16384 slots cut to 8192 (250 MB with the weights) in 65.5 us, about a
-// third of them the selection.
+// heads of dim 128 appended (135 MB) in 25.4 us, 5.3 TB/s; 8 sequences of 12001
+// to 16384 slots cut to 8192 (250 MB with the weights) in 65.7 us, 19 of them
+// the selection.
 #include <cuda_runtime.h>
 
 #include <algorithm>

@@ -7,8 +7,8 @@
 // tensors with their sizes and strides: read one attribute at a time from
 // Python, that took 6 to 8 us of calls whose kernels run for 3 to 10.
 // Measured on a GB300's Arm cores, from Python and here, the cache's description
-// included: tree_attn 10.6 and 3.7 us, cache_append 10.7 and 3.3, cache_weigh
-// 10.7 and 3.4, cache_evict 8.5 and 3.1 (2 to 2.5 of them the launch).
+// included: tree_attn 10.6 and 4.1 us, cache_append 10.7 and 3.6, cache_weigh
+// 10.7 and 3.6, cache_evict 8.5 and 3.5 (2 to 2.5 of them the launch).
 //
 // bind() hands over the C functions' addresses, so that the one loaded
 // libgemm_tn.so is called, and the exception type of its errors.

@@ -13,9 +13,9 @@
 // GB300, in a replayed graph, second kernel included: trees of 26 tokens, 32
 // heads over 8, 8 sequences of 1000 to 4096 slots 33.5 us (2.9 TB/s: few tiles
 // a CTA, the start and the join are half of it); trees of 63 tokens, 16 heads
-// over 2, 4 sequences of 20011 to 32768 slots 61.2 us (822 TFLOP/s); 1024
-// tokens, 32 heads over 8, after 2 contexts of about 8000 slots 220 us
-// (1325 TFLOP/s).
+// over 2, 4 sequences of 20011 to 32768 slots 61 us (825 TFLOP/s); 1024
+// tokens, 32 heads over 8, after 2 contexts of about 8000 slots 221 us
+// (1320 TFLOP/s; 225 to 234 in calls in a row, at the board's power limit).
 //
 // Work: an item is (sequence, KV head, row unit) and walks its key tiles, the
 // cached ones and then the new tokens'. All items' key tiles are laid end to
