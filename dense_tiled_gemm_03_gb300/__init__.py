@@ -2,7 +2,9 @@
 fp16/bf16 in, fp32 accumulate, fp16/bf16 out), and the attention forward pass
 built on the same pipeline (``flash_attn``), and a paged key/value cache with
 the attention of new tokens over it (``KVCache``, ``tree_attn``,
-``cache_append``, ``cache_weigh``, ``cache_evict``).
+``cache_append``, ``cache_weigh``, ``cache_evict``), and a feed-forward block's
+gated projection with its backward pass (``mm_tn_gated``, ``gated_grad``,
+``mm_nt``) and 8-bit products (``quantize_e4m3``, ``mm_tn_e4m3``).
 
 The product is the C-ABI library ``libgemm_tn.so`` (hand-written sm_103a CUDA:
 TMA, mbarrier rings, tcgen05 tensor cores with TMEM accumulators); this
@@ -56,6 +58,17 @@ from ._native import (  # noqa: F401
 )
 from . import _cache
 from ._cache import tree_mask  # noqa: F401
+from ._feed_forward import (  # noqa: F401
+    GEMM_TN_ACT_SILU,
+    GEMM_TN_ELEM_BF16,
+    GEMM_TN_ELEM_F16,
+    GEMM_TN_ELEM_F32,
+    gated_grad,
+    mm_nt,
+    mm_tn_e4m3,
+    mm_tn_gated,
+    quantize_e4m3,
+)
 
 
 def __getattr__(name):

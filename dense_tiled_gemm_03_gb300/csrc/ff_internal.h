@@ -1,0 +1,85 @@
+// ff_internal.h -- host-side interface of the feed-forward operators: kernel
+// arguments, launches, and the tile shapes ff_api.cu chooses from.
+#pragma once
+
+#include <cuda.h>
+#include <cuda_runtime.h>
+
+#include <cstdint>
+
+#include "kv_cache_internal.h"   // api_*: what the C ABI's translation units share
+
+namespace gemm_tn_dev {
+
+// Kernel arguments of the products with whole tiles (sm103_ff_gemm.cuh) and of
+// those with few rows of A (sm103_ff_skinny.cu).
+struct FfArgs {
+  CUtensorMap tmap_a;   // 128-byte-swizzled boxes, 128 bytes along the contiguous dimension
+  CUtensorMap tmap_b;
+  void* c;              // [m, n], element type out_kind
+  int64_t ldc;
+  void* pre;            // gated: [m, 2n] the two projections, or NULL
+  int64_t ldp;
+  const float* a_scale;   // e4m3: [m, k blocks], strides in elements
+  const float* b_scale;   // [n or ceil(n / 128), k blocks]
+  int64_t as_row, as_blk, bs_row, bs_blk;
+  int32_t b_block_rows;   // rows of B that share a scale: 1 or 128
+  int32_t m, n;         // of C
+  int32_t num_k_blocks;
+  int32_t num_m_tiles, num_n_tiles, num_tiles;
+  int32_t group_m;      // tile rows that run together (whole tiles)
+  int32_t activation;   // 1 relu, 2 gelu, 3 silu
+  int32_t out_kind;     // 0 fp16, 1 bf16, 2 fp32
+  int32_t accumulate;   // fp32: C's contents are added to
+  int* status;
+  uint64_t timeout_ns;
+  int32_t drop_load_kb; // test hook: k-block of the first tile whose loads are skipped (-1: none)
+};
+
+struct GatedGradArgs {
+  const void* grad;     // [m, n]
+  const void* pre;      // [m, 2n]
+  void* out;            // [m, 2n]
+  int64_t ldg, ldp, ldo;
+  int64_t m, n;
+  int32_t activation;
+};
+
+struct QuantizeArgs {
+  const void* x;        // [rows, cols]
+  int64_t ldx;
+  uint8_t* q;           // [rows, cols], or [cols, rows] transposed
+  int64_t ldq;
+  float* scale;
+  int64_t s_line, s_blk;   // strides of the scales: lines (or blocks of 128 lines) of q, and blocks along a line
+  int64_t rows, cols;
+};
+
+}  // namespace gemm_tn_dev
+
+namespace gemm_tn_impl {
+
+enum FfKind : int { kFfGated = 0, kFfNt = 1, kFfE4m3 = 2, kFfE4m3Rows = 3 };
+// Whole-tile shapes: rows x columns of the MMA, and the CTAs that share it.
+enum FfTile : int { kFfPair256 = 0, kFfPair128 = 1, kFfSingle128 = 2, kNumFfTiles = 3 };
+struct FfTileInfo {
+  int cta_group, tile_m, block_n;
+};
+constexpr FfTileInfo kFfTiles[kNumFfTiles] = {{2, 256, 256}, {2, 256, 128}, {1, 128, 128}};
+
+cudaError_t launch_ff_gated(int tile, bool bf16, const gemm_tn_dev::FfArgs& args, int grid, cudaStream_t stream);
+cudaError_t launch_ff_nt(int tile, bool bf16, const gemm_tn_dev::FfArgs& args, int grid, cudaStream_t stream);
+cudaError_t launch_ff_e4m3(int tile, bool b_rows, const gemm_tn_dev::FfArgs& args, int grid, cudaStream_t stream);
+// CTA pairs that run at once on the current device (0 on error): every form of
+// a tile takes an SM's shared memory whole.
+int ff_resident_pairs(int sms);
+
+// Few rows of A: `rows` (16, 32, 64 or 128) of them against 128 rows of B a CTA, K split over clusters of `splits`.
+cudaError_t launch_ff_skinny(int kind, bool bf16, int rows, int splits, const gemm_tn_dev::FfArgs& args, int grid,
+                             cudaStream_t stream);
+
+cudaError_t launch_gated_grad(bool bf16, const gemm_tn_dev::GatedGradArgs& args, int num_sms, cudaStream_t stream);
+cudaError_t launch_quantize(int src_kind, int block_rows, bool transpose, const gemm_tn_dev::QuantizeArgs& args,
+                            cudaStream_t stream);
+
+}  // namespace gemm_tn_impl

@@ -1,0 +1,507 @@
+// sm103_ff_gemm.cuh -- the feed-forward products in whole tiles, one kernel in
+// three forms:
+//  * gated: H = act(A Bg^T) * (A Bu^T), with B's rows [0, n) the gate's and
+//    [n, 2n) the other projection's. A tile multiplies the same rows of A by
+//    as many rows of either, side by side as one N of the tensor core's
+//    instruction, so that an epilogue thread finds both values of an output
+//    in its own row of tensor memory and the two projections never leave the
+//    chip (unless `pre` asks for them).
+//  * nt: C = A^T B, both operands stored with the summed dimension outermost
+//    (a weight's gradient, summed over tokens): read in place through
+//    MN-major descriptors, no transposed copies.
+//  * e4m3: C[i][j] = sum over blocks of 128 of sa[i][b] sb[j][b] (A_b B_b^T)[i][j].
+//    The scales differ from block to block, so the tensor core's sum ends at
+//    each block of 128: the block's product lands in one of the tensor
+//    memory's buffers, and the epilogue warps fold it, scaled, into fp32 sums
+//    in registers while the next block multiplies.
+//
+// One persistent CTA (or pair: cta_group::2, 256 rows) per SM: warp 0 moves
+// tiles with the TMA into a ring, one thread of warp 1 issues the MMAs, warps
+// 4 to 11 are the epilogue, two for each quarter of tensor memory.
+//
+// What bounds them is the tensor core: see the figures at the instantiations.
+#pragma once
+
+#include <atomic>
+
+#include "sm103_ff.cuh"
+
+namespace gemm_tn_dev {
+namespace ff {
+
+constexpr int kThreads = 384;
+constexpr int kFirstEpilogueWarp = 4;
+constexpr int kEpilogueWarps = 8;
+// e4m3: an epilogue thread holds 128 sums and the block being added; the first
+// warpgroup gives up registers for it (128 x 72 + 256 x 216 = 384 x 168, what
+// the block is launched with)
+constexpr uint32_t kFewRegisters = 72, kManyRegisters = 216;
+static_assert(128 * kFewRegisters + 256 * kManyRegisters <= 384 * 168, "register split");
+constexpr int kGated = 0, kNt = 1, kE4m3 = 2, kE4m3Rows = 3;   // kE4m3Rows: a scale for each row of B, else for 128 rows
+
+template <int kForm_, int kCtaGroup_, int kBlockN_, int kStages_, bool kBf16_>
+struct Tile {
+  static constexpr int kForm = kForm_;
+  static constexpr int kCtaGroup = kCtaGroup_;
+  static constexpr int kBlockN = kBlockN_;               // MMA N
+  static constexpr int kStages = kStages_;
+  static constexpr bool kBf16 = kBf16_;
+  static constexpr bool kScaled = kForm == kE4m3 || kForm == kE4m3Rows;
+  static constexpr int kBlockM = 128;                    // rows per CTA
+  static constexpr int kTileM = kBlockM * kCtaGroup;     // MMA M
+  static constexpr int kOutN = kForm == kGated ? kBlockN / 2 : kBlockN;   // columns of C
+  static constexpr int kBlockK = kScaled ? 128 : 64;     // 128 bytes
+  static constexpr int kBRows = kBlockN / kCtaGroup;     // rows of B this CTA loads
+  static constexpr uint32_t kStageA = kBlockM * 128;
+  static constexpr uint32_t kStageB = kBRows * 128;
+  static constexpr uint32_t kBoxBytes = 64 * 64 * 2;     // nt: 64 x 64 boxes
+  static constexpr int kBuffers = kScaled ? 512 / kBlockN : 2;   // of tensor memory
+  static constexpr uint32_t kTmemCols = kBuffers * kBlockN;
+  static constexpr uint32_t kStagingBytes = 4096;        // per epilogue warp
+  static constexpr uint32_t kOffA = 0;
+  static constexpr uint32_t kOffB = kOffA + kStages * kStageA;
+  static constexpr uint32_t kOffStaging = kOffB + kStages * kStageB;
+  static constexpr uint32_t kOffBar = kOffStaging + kEpilogueWarps * kStagingBytes;
+  static constexpr int kNumBars = 2 * kStages + 2 * kBuffers + 1;   // full, empty, sum full, sum empty, drain
+  static constexpr uint32_t kOffTmemSlot = kOffBar + kNumBars * 8;
+  static constexpr uint32_t kOffAbort = kOffTmemSlot + 4;
+  static constexpr uint32_t kSmemBytes = kOffAbort + 4 + 1024;
+  static constexpr uint32_t kIdesc = mma_idesc_f16(!kScaled && kBf16, kTileM, kBlockN, kForm == kNt) |
+                                     (kForm == kNt ? 1u << 15 : 0u);
+  static_assert(kStages <= 32, "issued phases fit a 32-bit mask");
+  static_assert(kTmemCols <= 512 && (kTmemCols & (kTmemCols - 1)) == 0, "TMEM columns");
+  static_assert(kStageB % 1024 == 0 && kOffStaging % 1024 == 0, "swizzle atoms stay 1024-aligned");
+  static_assert(kForm != kNt || kBRows % 64 == 0, "boxes of 64 columns");
+  static_assert(kSmemBytes <= 232448, "fits the opt-in shared memory of one CTA");
+};
+
+// Tiles in groups of group_m tile rows, so that those running together share
+// rows of A and of B in L2.
+__device__ __forceinline__ void tile_at(const FfArgs& a, int tile, int& tm, int& tn) {
+  const int per_group = a.group_m * a.num_n_tiles;
+  const int first = tile / per_group * a.group_m;
+  const int in = tile - first * a.num_n_tiles;
+  const int rows = min(a.group_m, a.num_m_tiles - first);
+  tn = in / rows;
+  tm = first + in - tn * rows;
+}
+
+// H of a chunk of 32 columns from its two projections (32 fp32 values a lane).
+template <int kAct>
+__device__ __forceinline__ void gate(const uint32_t (&g)[32], const uint32_t (&u)[32], float (&h)[32]) {
+#pragma unroll
+  for (int j = 0; j < 32; ++j) h[j] = act<kAct>(__uint_as_float(g[j])) * __uint_as_float(u[j]);
+}
+
+template <class T>
+__global__ void __launch_bounds__(kThreads, 1) ff_gemm_kernel(const __grid_constant__ FfArgs args) {
+  extern __shared__ uint8_t smem_raw[];
+  const uint32_t raw = smem_addr(smem_raw);
+  uint8_t* smem = smem_raw + (((raw + 1023u) & ~1023u) - raw);
+  const uint32_t base = smem_addr(smem);
+
+  const uint32_t warp = threadIdx.x >> 5, lane = lane_id();
+  const uint32_t rank = T::kCtaGroup == 2 ? cluster_ctarank() : 0u;
+  const bool leader = rank == 0;
+  auto a_tile = [&](int s) { return base + T::kOffA + s * T::kStageA; };
+  auto b_tile = [&](int s) { return base + T::kOffB + s * T::kStageB; };
+  auto full_bar = [&](int s) { return base + T::kOffBar + 8u * s; };
+  auto empty_bar = [&](int s) { return base + T::kOffBar + 8u * (T::kStages + s); };
+  auto sum_full = [&](int b) { return base + T::kOffBar + 8u * (2 * T::kStages + b); };
+  auto sum_empty = [&](int b) { return base + T::kOffBar + 8u * (2 * T::kStages + T::kBuffers + b); };
+  const uint32_t drain_bar = base + T::kOffBar + 8u * (2 * T::kStages + 2 * T::kBuffers);
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + T::kOffTmemSlot);
+  volatile uint32_t* abort_flag = reinterpret_cast<volatile uint32_t*>(smem + T::kOffAbort);
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < T::kStages; ++s) {
+      mbar_init(full_bar(s), 1);
+      mbar_init(empty_bar(s), 1);
+    }
+    for (int b = 0; b < T::kBuffers; ++b) {
+      mbar_init(sum_full(b), 1);
+      mbar_init(sum_empty(b), T::kCtaGroup * kEpilogueWarps);
+    }
+    mbar_init(drain_bar, 1);
+    *abort_flag = 0u;
+    fence_barrier_init();
+    tma_prefetch_descriptor(&args.tmap_a);
+    tma_prefetch_descriptor(&args.tmap_b);
+  }
+  if (warp == 1) {
+    tmem_alloc<T::kCtaGroup>(smem_addr(tmem_slot), T::kTmemCols);
+    tmem_relinquish<T::kCtaGroup>();
+  }
+  tc_fence_before_sync();
+  if constexpr (T::kCtaGroup == 2) {
+    cluster_sync_all();
+  } else {
+    __syncthreads();
+  }
+  tc_fence_after_sync();
+  const uint32_t tmem_base = *tmem_slot;
+  // set-up may overlap the previous kernel in the stream; memory waits for it
+  griddep_wait();
+  griddep_launch_dependents();
+
+  const Waiter<T::kCtaGroup> wd{args.status, args.timeout_ns, abort_flag};
+  const int first_tile = static_cast<int>(blockIdx.x) / T::kCtaGroup;
+  const int tile_step = static_cast<int>(gridDim.x) / T::kCtaGroup;
+
+  if (warp < static_cast<uint32_t>(kFirstEpilogueWarp)) {
+    if constexpr (T::kScaled) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" :: "n"(kFewRegisters));
+    if (warp == 0 && lane == 0) {
+      // ---------------------------------------------------------------- TMA producer
+      int stage = 0;
+      uint32_t phase = 0;
+      Issued issued;
+      bool ok = true;
+      for (int tile = first_tile; ok && tile < args.num_tiles; tile += tile_step) {
+        int tm, tn;
+        tile_at(args, tile, tm, tn);
+        const int a_row = tm * T::kTileM + static_cast<int>(rank) * T::kBlockM;
+        const int b_row = tn * T::kOutN + static_cast<int>(rank) * T::kBRows;
+        for (int kb = 0; kb < args.num_k_blocks; ++kb) {
+          if (!wd.wait(empty_bar(stage), phase ^ 1u)) {
+            ok = false;
+            break;
+          }
+          const uint32_t bar = T::kCtaGroup == 2 ? map_to_cta(full_bar(stage), 0u) : full_bar(stage);
+          if (leader) mbar_arrive_expect_tx(full_bar(stage), T::kCtaGroup * (T::kStageA + T::kStageB));
+          auto load = [&](const CUtensorMap* map, uint32_t dst, int x, int y) {
+            if constexpr (T::kCtaGroup == 2) {
+              tma_load_2d_pair(map, dst, bar, x, y);
+            } else {
+              tma_load_2d(map, dst, bar, x, y);
+            }
+          };
+          const int k0 = kb * T::kBlockK;
+          if (kb != args.drop_load_kb || tile != first_tile) {
+            if constexpr (T::kForm == kNt) {
+#pragma unroll
+              for (int j = 0; j < T::kBlockM / 64; ++j)
+                load(&args.tmap_a, a_tile(stage) + j * T::kBoxBytes, a_row + 64 * j, k0);
+#pragma unroll
+              for (int j = 0; j < T::kBRows / 64; ++j)
+                load(&args.tmap_b, b_tile(stage) + j * T::kBoxBytes, b_row + 64 * j, k0);
+            } else {
+              load(&args.tmap_a, a_tile(stage), k0, a_row);
+              if constexpr (T::kForm != kGated) {
+                load(&args.tmap_b, b_tile(stage), k0, b_row);
+              } else if constexpr (T::kCtaGroup == 2) {
+                // the pair's halves of N: the gate's rows, the other projection's
+                load(&args.tmap_b, b_tile(stage), k0, tn * T::kOutN + static_cast<int>(rank) * args.n);
+              } else {
+                load(&args.tmap_b, b_tile(stage), k0, b_row);
+                load(&args.tmap_b, b_tile(stage) + T::kStageB / 2, k0, b_row + args.n);
+              }
+            }
+          }
+          issued.record(stage, phase);
+          if (++stage == T::kStages) {
+            stage = 0;
+            phase ^= 1u;
+          }
+        }
+      }
+      // loads may still be landing if another role gave up
+      for (int s = 0; s < T::kStages; ++s)
+        if (leader && ((issued.issued >> s) & 1u)) wd.drain(full_bar(s), (issued.parity >> s) & 1u);
+    } else if (warp == 1 && leader && lane == 0) {
+      // ---------------------------------------------------------------- MMA issuer
+      int stage = 0, buf = 0;
+      uint32_t phase = 0, buf_phase = 0;
+      bool ok = true;
+      auto done = [&](uint32_t bar, uint16_t mask) {
+        if constexpr (T::kCtaGroup == 2) {
+          mma_commit_pair(bar, mask);
+        } else {
+          mma_commit(bar);
+        }
+      };
+      for (int tile = first_tile; ok && tile < args.num_tiles; tile += tile_step) {
+        for (int kb = 0; kb < args.num_k_blocks; ++kb) {
+          if ((T::kScaled || kb == 0) && !wd.wait(sum_empty(buf), buf_phase ^ 1u)) ok = false;
+          if (!ok || !wd.wait(full_bar(stage), phase)) {
+            ok = false;
+            break;
+          }
+          tc_fence_after_sync();
+          const uint32_t d = tmem_base + static_cast<uint32_t>(buf * T::kBlockN);
+          // a step along K: 32 bytes of a K-major row, or two 8-row groups of an MN-major tile
+          constexpr uint32_t kStep = T::kForm == kNt ? 2048u >> 4 : 2u;
+          const uint64_t a_desc = T::kForm == kNt ? sw128_mnmajor_desc(a_tile(stage), T::kBoxBytes)
+                                                  : sw128_kmajor_desc(a_tile(stage));
+          const uint64_t b_desc = T::kForm == kNt ? sw128_mnmajor_desc(b_tile(stage), T::kBoxBytes)
+                                                  : sw128_kmajor_desc(b_tile(stage));
+#pragma unroll
+          for (int kk = 0; kk < 4; ++kk) {
+            const uint32_t add = kk > 0 || (!T::kScaled && kb > 0) ? 1u : 0u;
+            if constexpr (T::kScaled) {
+              mma_f8<T::kCtaGroup>(d, a_desc + kStep * kk, b_desc + kStep * kk, T::kIdesc, add);
+            } else {
+              mma_f16<T::kCtaGroup>(d, a_desc + kStep * kk, b_desc + kStep * kk, T::kIdesc, add);
+            }
+          }
+          done(empty_bar(stage), 0x3);
+          if (++stage == T::kStages) {
+            stage = 0;
+            phase ^= 1u;
+          }
+          if (T::kScaled || kb == args.num_k_blocks - 1) {
+            done(sum_full(buf), 0x3);
+            if (++buf == T::kBuffers) {
+              buf = 0;
+              buf_phase ^= 1u;
+            }
+          }
+        }
+      }
+      // all MMAs of this thread finish before tensor memory is freed
+      done(drain_bar, 0x1);
+      wd.drain(drain_bar, 0);
+    }
+  } else {
+    if constexpr (T::kScaled) asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" :: "n"(kManyRegisters));
+    // ------------------------------------------------------------------ epilogue
+    const uint32_t quarter = warp & 3u;
+    const int epilogue_warp = static_cast<int>(warp) - kFirstEpilogueWarp;
+    const int half = epilogue_warp >> 2;
+    uint8_t* staging = smem + T::kOffStaging + static_cast<uint32_t>(epilogue_warp) * T::kStagingBytes;
+    const uint32_t sum_empty0 = T::kCtaGroup == 2 ? map_to_cta(sum_empty(0), 0u) : sum_empty(0);
+    int buf = 0;
+    uint32_t buf_phase = 0;
+    bool ok = true;
+    auto hand_back = [&]() {   // the buffer is in registers: the MMA warp may write it again
+      tc_fence_before_sync();
+      __syncwarp();
+      if (lane == 0) {
+        if constexpr (T::kCtaGroup == 2) {
+          mbar_arrive_cluster(sum_empty0 + 8u * buf);
+        } else {
+          mbar_arrive(sum_empty(buf));
+        }
+      }
+      if (++buf == T::kBuffers) {
+        buf = 0;
+        buf_phase ^= 1u;
+      }
+    };
+    for (int tile = first_tile; ok && tile < args.num_tiles; tile += tile_step) {
+      int tm, tn;
+      tile_at(args, tile, tm, tn);
+      const int row0 = tm * T::kTileM + static_cast<int>(rank) * T::kBlockM + static_cast<int>(quarter) * 32;
+      const int col0 = tn * T::kOutN;
+      const uint32_t t_quarter = tmem_base + ((quarter * 32u) << 16);
+
+      if constexpr (T::kScaled) {
+        // this warp's half of the columns; a thread's sums: its row's, two to a register pair
+        constexpr int kCols = T::kBlockN / 2;
+        const int my_col = col0 + half * kCols;
+        const int row = row0 + static_cast<int>(lane);
+        uint64_t sum[kCols / 2];
+#pragma unroll
+        for (int j = 0; j < kCols / 2; ++j) sum[j] = 0;
+        const float* sa = args.a_scale + static_cast<int64_t>(min(row, args.m - 1)) * args.as_row;
+        float* vec = reinterpret_cast<float*>(staging);   // kE4m3Rows: [2][kCols] scales of this warp's columns
+        const float* sb;
+        if constexpr (T::kForm == kE4m3) {
+          sb = args.b_scale + static_cast<int64_t>(min(my_col, args.n - 1) / 128) * args.bs_row;
+        } else {
+          sb = args.b_scale;
+        }
+        // the scales of a block are loaded a block ahead
+        float a_next = __ldg(sa), b_next[T::kForm == kE4m3 ? 1 : kCols / 32];
+        auto load_b = [&](int kb) {
+          if constexpr (T::kForm == kE4m3) {
+            b_next[0] = __ldg(sb + kb * args.bs_blk);
+          } else {
+#pragma unroll
+            for (int i = 0; i < kCols / 32; ++i)
+              b_next[i] = __ldg(sb + static_cast<int64_t>(min(my_col + i * 32 + static_cast<int>(lane), args.n - 1)) *
+                                         args.bs_row + kb * args.bs_blk);
+          }
+        };
+        load_b(0);
+        for (int kb = 0; kb < args.num_k_blocks; ++kb) {
+          float scale = a_next;
+          if constexpr (T::kForm == kE4m3) {
+            scale *= b_next[0];
+          } else {
+            // two buffers: the other warps' lanes never see this one, so a
+            // warp's own order is all that is needed
+#pragma unroll
+            for (int i = 0; i < kCols / 32; ++i) vec[(kb & 1) * kCols + i * 32 + lane] = b_next[i];
+            __syncwarp();
+          }
+          if (kb + 1 < args.num_k_blocks) {
+            a_next = __ldg(sa + (kb + 1) * args.as_blk);
+            load_b(kb + 1);
+          }
+          if (!__all_sync(0xffffffffu, wd.wait(sum_full(buf), buf_phase))) {
+            ok = false;
+            break;
+          }
+          tc_fence_after_sync();
+          const uint32_t t = t_quarter + static_cast<uint32_t>(buf * T::kBlockN + half * kCols);
+          const uint64_t scale2 = f32x2_pack(scale, scale);
+          uint32_t v[2][16];
+          tmem_load_32x16(t, v[0]);
+#pragma unroll
+          for (int c = 0; c < kCols / 16; ++c) {
+            tmem_loaded(v[c & 1]);
+            if (c + 1 < kCols / 16) {
+              tmem_load_32x16(t + 16u * (c + 1), v[(c + 1) & 1]);
+            } else {
+              hand_back();
+            }
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+              const uint64_t p = f32x2_pack(__uint_as_float(v[c & 1][2 * j]), __uint_as_float(v[c & 1][2 * j + 1]));
+              uint64_t& s = sum[c * 8 + j];
+              if constexpr (T::kForm == kE4m3) {
+                s = f32x2_fma(p, scale2, s);
+              } else {
+                const uint64_t b2 = *reinterpret_cast<const uint64_t*>(vec + (kb & 1) * kCols + c * 16 + 2 * j);
+                s = f32x2_fma(f32x2_mul(p, scale2), b2, s);
+              }
+            }
+          }
+        }
+        if (!ok) break;
+        if constexpr (T::kForm == kE4m3Rows) __syncwarp();   // the scales' memory is the staging's
+#pragma unroll
+        for (int c = 0; c < kCols / 32; ++c) {
+          float out[32];
+#pragma unroll
+          for (int j = 0; j < 16; ++j) f32x2_unpack(sum[c * 16 + j], out[2 * j], out[2 * j + 1]);
+          if (my_col + c * 32 < args.n) store_block(args, row0, my_col + c * 32, out, staging);
+        }
+      } else {
+        // chunks of 32 columns of C, alternately this warp's and its partner's
+        constexpr int kChunks = T::kOutN / 32;
+        if (!__all_sync(0xffffffffu, wd.wait(sum_full(buf), buf_phase))) break;
+        tc_fence_after_sync();
+        const uint32_t t = t_quarter + static_cast<uint32_t>(buf * T::kBlockN);
+#pragma unroll 1
+        for (int c = half; c < kChunks; c += 2) {
+          const int col = col0 + c * 32;
+          uint32_t v[32];
+          tmem_load_32x32(t + 32u * c, v);
+          if constexpr (T::kForm == kGated) {
+            uint32_t u[32];
+            tmem_load_32x32(t + T::kOutN + 32u * c, u);
+            tmem_loaded(v);
+            tmem_loaded(u);
+            if (c + 2 >= kChunks) hand_back();
+            if (col >= args.n) continue;
+            if (args.pre != nullptr) {
+              uint32_t p[16];
+              uint16_t* pre = static_cast<uint16_t*>(args.pre) + static_cast<int64_t>(row0) * args.ldp + col;
+#pragma unroll
+              for (int j = 0; j < 16; ++j)
+                p[j] = pack16<T::kBf16>(__uint_as_float(v[2 * j]), __uint_as_float(v[2 * j + 1]));
+              store_block16(pre, args.ldp, args.m - row0, args.n - col, p, staging);
+#pragma unroll
+              for (int j = 0; j < 16; ++j)
+                p[j] = pack16<T::kBf16>(__uint_as_float(u[2 * j]), __uint_as_float(u[2 * j + 1]));
+              store_block16(pre + args.n, args.ldp, args.m - row0, args.n - col, p, staging);
+            }
+            float h[32];
+            if (args.activation == kSilu) {
+              gate<kSilu>(v, u, h);
+            } else if (args.activation == kGelu) {
+              gate<kGelu>(v, u, h);
+            } else {
+              gate<kRelu>(v, u, h);
+            }
+            store_block(args, row0, col, h, staging);
+          } else {
+            tmem_loaded(v);
+            if (c + 2 >= kChunks) hand_back();
+            if (col >= args.n) continue;
+            float out[32];
+#pragma unroll
+            for (int j = 0; j < 32; ++j) out[j] = __uint_as_float(v[j]);
+            store_block(args, row0, col, out, staging);
+          }
+        }
+      }
+    }
+    __syncwarp();
+  }
+
+  // ------------------------------------------------------------------ teardown
+  tc_fence_before_sync();
+  if constexpr (T::kCtaGroup == 2) {
+    cluster_sync_all();
+  } else {
+    __syncthreads();
+  }
+  if (warp == 1) {
+    tc_fence_after_sync();
+    tmem_dealloc<T::kCtaGroup>(tmem_base, T::kTmemCols);
+  }
+}
+
+}  // namespace ff
+}  // namespace gemm_tn_dev
+
+namespace gemm_tn_impl {
+
+template <class T>
+struct FfLauncher {
+  static cudaError_t fill(cudaLaunchConfig_t& cfg, cudaLaunchAttribute* attr, int grid, cudaStream_t stream) {
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    static std::atomic<uint64_t> done_mask{0};
+    const uint64_t bit = 1ull << (dev & 63);
+    if (!(done_mask.load(std::memory_order_acquire) & bit)) {
+      e = cudaFuncSetAttribute(gemm_tn_dev::ff::ff_gemm_kernel<T>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                               static_cast<int>(T::kSmemBytes));
+      if (e != cudaSuccess) return e;
+      done_mask.fetch_or(bit, std::memory_order_acq_rel);
+    }
+    cfg = cudaLaunchConfig_t{};
+    cfg.gridDim = dim3(static_cast<unsigned>(grid));
+    cfg.blockDim = dim3(gemm_tn_dev::ff::kThreads);
+    cfg.dynamicSmemBytes = T::kSmemBytes;
+    cfg.stream = stream;
+    cfg.attrs = attr;
+    if (T::kCtaGroup == 2) {
+      attr[cfg.numAttrs].id = cudaLaunchAttributeClusterDimension;
+      attr[cfg.numAttrs].val.clusterDim.x = 2;
+      attr[cfg.numAttrs].val.clusterDim.y = 1;
+      attr[cfg.numAttrs++].val.clusterDim.z = 1;
+    }
+    return cudaSuccess;
+  }
+
+  static cudaError_t launch(const gemm_tn_dev::FfArgs& args, int grid, cudaStream_t stream) {
+    cudaLaunchConfig_t cfg;
+    cudaLaunchAttribute attr[2];
+    cudaError_t e = fill(cfg, attr, grid, stream);
+    if (e != cudaSuccess) return e;
+    if (dependent_launch_enabled()) {
+      attr[cfg.numAttrs].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+      attr[cfg.numAttrs++].val.programmaticStreamSerializationAllowed = 1;
+    }
+    return cudaLaunchKernelEx(&cfg, gemm_tn_dev::ff::ff_gemm_kernel<T>, args);
+  }
+
+  static int resident(int sms) {
+    cudaLaunchConfig_t cfg;
+    cudaLaunchAttribute attr[2];
+    if (fill(cfg, attr, sms - sms % T::kCtaGroup, nullptr) != cudaSuccess) return 0;
+    if (T::kCtaGroup == 1) return sms;
+    int clusters = 0;
+    if (cudaOccupancyMaxActiveClusters(&clusters, gemm_tn_dev::ff::ff_gemm_kernel<T>, &cfg) != cudaSuccess) {
+      cudaGetLastError();
+      return 0;
+    }
+    return clusters;
+  }
+};
+
+}  // namespace gemm_tn_impl
