@@ -16,11 +16,13 @@ namespace gemm_tn_dev {
 struct FfArgs {
   CUtensorMap tmap_a;   // 128-byte-swizzled boxes, 128 bytes along the contiguous dimension
   CUtensorMap tmap_b;
+  CUtensorMap tmap_as;  // e4m3 in whole tiles: A's scales {m, k blocks}, boxes {128, 1}
+  CUtensorMap tmap_bs;  // B's {n, k blocks}, boxes {MMA N, 1}; or, of 128 rows, {k blocks, n / 128}, boxes {4, MMA N / 128}
   void* c;              // [m, n], element type out_kind
   int64_t ldc;
   void* pre;            // gated: [m, 2n] the two projections, or NULL
   int64_t ldp;
-  const float* a_scale;   // e4m3: [m, k blocks], strides in elements
+  const float* a_scale;   // e4m3 with few rows: [m, k blocks], strides in elements
   const float* b_scale;   // [n or ceil(n / 128), k blocks]
   int64_t as_row, as_blk, bs_row, bs_blk;
   int32_t b_block_rows;   // rows of B that share a scale: 1 or 128
@@ -77,6 +79,14 @@ int ff_resident_pairs(int sms);
 // Few rows of A: `rows` (16, 32, 64 or 128) of them against 128 rows of B a CTA, K split over clusters of `splits`.
 cudaError_t launch_ff_skinny(int kind, bool bf16, int rows, int splits, const gemm_tn_dev::FfArgs& args, int grid,
                              cudaStream_t stream);
+
+// dst[i * pitch + j] = src[i * s_i + j * s_j] for i < rows, j < cols; up to two at once (rows 0: none).
+struct PackRequest {
+  const float* src;
+  float* dst;
+  int64_t rows, cols, s_i, s_j, pitch;
+};
+cudaError_t launch_pack_scales(const PackRequest (&req)[2], cudaStream_t stream);
 
 cudaError_t launch_gated_grad(bool bf16, const gemm_tn_dev::GatedGradArgs& args, int num_sms, cudaStream_t stream);
 cudaError_t launch_quantize(int src_kind, int block_rows, bool transpose, const gemm_tn_dev::QuantizeArgs& args,

@@ -89,6 +89,32 @@ __global__ void __launch_bounds__(kGradThreads) gated_grad_kernel(const GatedGra
   }
 }
 
+// ------------------------------------------------------------------ scales laid out for the product
+// 32 x 32 tiles through shared memory, lanes along the source's shorter stride.
+struct PackArgs {
+  gemm_tn_impl::PackRequest req[2];
+  int64_t tiles0;   // of the first request
+};
+
+__global__ void __launch_bounds__(256) pack_scales_kernel(const PackArgs a) {
+  __shared__ float tile[32][33];
+  griddep_wait();
+  griddep_launch_dependents();
+  const bool second = blockIdx.x >= a.tiles0;
+  const gemm_tn_impl::PackRequest& q = second ? a.req[1] : a.req[0];
+  const int64_t at = static_cast<int64_t>(blockIdx.x) - (second ? a.tiles0 : 0), across = (q.cols + 31) / 32;
+  const int64_t i0 = at / across * 32, j0 = at % across * 32;
+  const int lane = static_cast<int>(threadIdx.x) & 31, group = static_cast<int>(threadIdx.x) >> 5;
+  const bool along_j = q.s_j <= q.s_i;
+  for (int g = group; g < 32; g += 8) {
+    const int i = along_j ? g : lane, j = along_j ? lane : g;
+    if (i0 + i < q.rows && j0 + j < q.cols) tile[i][j] = q.src[(i0 + i) * q.s_i + (j0 + j) * q.s_j];
+  }
+  __syncthreads();
+  for (int i = group; i < 32; i += 8)
+    if (i0 + i < q.rows && j0 + lane < q.cols) q.dst[(i0 + i) * q.pitch + j0 + lane] = tile[i][lane];
+}
+
 // ------------------------------------------------------------------ e4m3 in blocks of 128
 // A block's scale is the least power of two that brings its largest finite
 // magnitude to 448 at most (1 for a block of zeros; no less than 2^-126):
@@ -355,6 +381,15 @@ cudaError_t launch_gated_grad(bool bf16, const GatedGradArgs& a, int num_sms, cu
   const dim3 grid(static_cast<unsigned>(units < most ? units : most));
   if (bf16) return vec ? launch_grad<true, true>(a, grid, stream) : launch_grad<true, false>(a, grid, stream);
   return vec ? launch_grad<false, true>(a, grid, stream) : launch_grad<false, false>(a, grid, stream);
+}
+
+cudaError_t launch_pack_scales(const PackRequest (&req)[2], cudaStream_t stream) {
+  ff::PackArgs args{{req[0], req[1]}, 0};
+  int64_t tiles[2];
+  for (int x = 0; x < 2; ++x) tiles[x] = (req[x].rows + 31) / 32 * ((req[x].cols + 31) / 32);
+  args.tiles0 = tiles[0];
+  return launch_dependent<ff::PackArgs>(ff::pack_scales_kernel, dim3(static_cast<unsigned>(tiles[0] + tiles[1])), 256, stream,
+                                        args);
 }
 
 cudaError_t launch_quantize(int src_kind, int block_rows, bool transpose, const QuantizeArgs& a, cudaStream_t stream) {

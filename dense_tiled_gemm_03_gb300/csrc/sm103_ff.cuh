@@ -8,6 +8,7 @@
 #include <cstdint>
 
 #include "ff_internal.h"
+#include "sm103_cache_ptx.cuh"   // elect_one
 #include "sm103_ptx.cuh"
 
 namespace gemm_tn_dev {
@@ -18,7 +19,9 @@ constexpr int kRelu = 1, kGelu = 2, kSilu = 3;
 constexpr int kOutF16 = 0, kOutBf16 = 1, kOutF32 = 2;
 
 // Bounded waits: past the deadline the kernel records the error, tells every
-// role of the cluster to stop, and returns.
+// role of the cluster to stop, and returns. They acquire at CTA scope: what the
+// barriers guard is in shared and tensor memory (an acquire at cluster scope
+// also gives up the SM's cached lines, at every block).
 template <int kClusterSize>
 struct Waiter {
   int* status;
@@ -27,10 +30,10 @@ struct Waiter {
   static constexpr bool kCluster = kClusterSize > 1;
 
   __device__ __forceinline__ bool wait(uint32_t bar, uint32_t parity) const {
-    if (mbar_try_wait<kCluster>(bar, parity)) return true;
+    if (mbar_try_wait<false>(bar, parity)) return true;
     const uint64_t deadline = globaltimer_ns() + timeout_ns;
     while (true) {
-      if (mbar_try_wait<kCluster>(bar, parity)) return true;
+      if (mbar_try_wait<false>(bar, parity)) return true;
       if (*abort_flag) return false;
       if (globaltimer_ns() > deadline) {
         if (status != nullptr) atomicCAS(status, 0, kStatusExpired);
@@ -45,10 +48,15 @@ struct Waiter {
     }
   }
 
+  // The same for a whole warp, with one outcome.
+  __device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity) const {
+    return __all_sync(0xffffffffu, wait(bar, parity));
+  }
+
   // For what is in flight once another role has given up: never sets the flag.
   __device__ __forceinline__ void drain(uint32_t bar, uint32_t parity) const {
     const uint64_t deadline = globaltimer_ns() + timeout_ns;
-    while (!mbar_try_wait<kCluster>(bar, parity))
+    while (!mbar_try_wait<false>(bar, parity))
       if (globaltimer_ns() > deadline) return;
   }
 };
@@ -62,25 +70,94 @@ struct Issued {
   }
 };
 
-// D[tmem] (+)= A[smem] x B[smem]^T, e4m3 operands, fp32 accumulator; one
-// instruction takes 32 elements of K. Its instruction descriptor is that of
-// kind::f16 with the formats' fields zero (e4m3).
+// Arrive on a barrier of any CTA of the cluster to hand back tensor memory: what
+// it orders is this thread's tcgen05 loads (complete, and fenced before it), no
+// data in memory. A release at cluster scope would wait for the warp's loads and
+// stores in flight each time: measured at a block of 128 a time, e4m3 4096^3
+// took 232 us with it.
+__device__ __forceinline__ void arrive_remote(uint32_t cluster_bar) {
+  asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" :: "r"(cluster_bar) : "memory");
+}
+
+// ------------------------------------------------------------------ warps that issue as a whole
+// Every lane of the producer and MMA warps runs the same code with the same
+// operands, and the one lane with leader != 0 (elect_one) issues: the operands
+// of tcgen05 and TMA instructions are uniform registers, and where one lane runs
+// alone each is moved there for every instruction. An e4m3 block of 128 lasts
+// 545 clocks on the tensor core; issued by single threads it took some 700.
+
+// D[tmem] (+)= A[smem] x B[smem]^T: fp16/bf16 (16 elements of K), or e4m3 (32),
+// whose instruction descriptor is that of kind::f16 with the formats' fields zero.
+template <int kCtaGroup, bool kF8>
+__device__ __forceinline__ void mma_warp(uint32_t leader, uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc,
+                                         uint32_t accumulate) {
+#define FF_MMA(GROUP, KIND)                                                                                       \
+  asm volatile(                                                                                                   \
+      "{\n\t.reg .pred p, q;\n\t"                                                                                 \
+      "setp.ne.b32 p, %4, 0;\n\t"                                                                                 \
+      "setp.ne.b32 q, %5, 0;\n\t"                                                                                 \
+      "@q tcgen05.mma.cta_group::" GROUP ".kind::" KIND " [%0], %1, %2, %3, p;\n\t}"                              \
+      :: "r"(d_tmem), "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate), "r"(leader) : "memory")
+  if constexpr (kCtaGroup == 1 && kF8) {
+    FF_MMA("1", "f8f6f4");
+  } else if constexpr (kCtaGroup == 1) {
+    FF_MMA("1", "f16");
+  } else if constexpr (kF8) {
+    FF_MMA("2", "f8f6f4");
+  } else {
+    FF_MMA("2", "f16");
+  }
+#undef FF_MMA
+}
+
+// Arrive on `bar` (kCtaGroup 2: at its offset in every CTA of the mask) when
+// what the leader issued so far has completed.
 template <int kCtaGroup>
-__device__ __forceinline__ void mma_f8(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc,
-                                       uint32_t accumulate) {
+__device__ __forceinline__ void commit_warp(uint32_t leader, uint32_t bar, uint16_t mask) {
   if constexpr (kCtaGroup == 1) {
     asm volatile(
-        "{\n\t.reg .pred p;\n\t"
-        "setp.ne.b32 p, %4, 0;\n\t"
-        "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}"
-        :: "r"(d_tmem), "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate) : "memory");
+        "{\n\t.reg .pred q;\n\t"
+        "setp.ne.b32 q, %1, 0;\n\t"
+        "@q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}"
+        :: "r"(bar), "r"(leader) : "memory");
   } else {
     asm volatile(
-        "{\n\t.reg .pred p;\n\t"
-        "setp.ne.b32 p, %4, 0;\n\t"
-        "tcgen05.mma.cta_group::2.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}"
-        :: "r"(d_tmem), "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate) : "memory");
+        "{\n\t.reg .pred q;\n\t"
+        "setp.ne.b32 q, %2, 0;\n\t"
+        "@q tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;\n\t}"
+        :: "r"(bar), "h"(mask), "r"(leader) : "memory");
   }
+}
+
+// 2-D tile load; kCtaGroup 2: the barrier may be the pair's other CTA's.
+template <int kCtaGroup>
+__device__ __forceinline__ void load_warp(uint32_t leader, const void* tmap, uint32_t dst, uint32_t bar, int32_t x, int32_t y) {
+  if constexpr (kCtaGroup == 1) {
+    asm volatile(
+        "{\n\t.reg .pred q;\n\t"
+        "setp.ne.b32 q, %5, 0;\n\t"
+        "@q cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+        " [%0], [%1, {%2, %3}], [%4];\n\t}"
+        :: "r"(dst), "l"(reinterpret_cast<uint64_t>(tmap)), "r"(x), "r"(y), "r"(bar), "r"(leader) : "memory");
+  } else {
+    asm volatile(
+        "{\n\t.reg .pred q;\n\t"
+        "setp.ne.b32 q, %5, 0;\n\t"
+        "@q cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+        " [%0], [%1, {%2, %3}], [%4];\n\t}"
+        :: "r"(dst), "l"(reinterpret_cast<uint64_t>(tmap)), "r"(x), "r"(y), "r"(bar), "r"(leader) : "memory");
+  }
+}
+
+// The same with an L2 cache policy.
+__device__ __forceinline__ void load_warp_hint(uint32_t leader, const void* tmap, uint32_t dst, uint32_t bar, int32_t x,
+                                               int32_t y, uint64_t policy) {
+  asm volatile(
+      "{\n\t.reg .pred q;\n\t"
+      "setp.ne.b32 q, %6, 0;\n\t"
+      "@q cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.L2::cache_hint"
+      " [%0], [%1, {%2, %3}], [%4], %5;\n\t}"
+      :: "r"(dst), "l"(reinterpret_cast<uint64_t>(tmap)), "r"(x), "r"(y), "r"(bar), "l"(policy), "r"(leader) : "memory");
 }
 
 // tcgen05.wait::ld as the point where loaded values come to be: an operation on
@@ -161,97 +238,91 @@ __device__ __forceinline__ float widen16(uint32_t bits) {
   }
 }
 
-// ------------------------------------------------------------------ a warp's 32 x 32 block of C
-// Lane l holds row l. The block goes through the warp's staging memory so that
-// each store writes whole stretches of rows: 16 bytes a lane where the rows are
-// aligned so, else one row's 32 elements an instruction. rows, cols: how many
-// of the 32 exist (<= 0: none).
+// ------------------------------------------------------------------ a warp's rows of C
+// 64 bytes of each of 32 rows: lane l holds row l's, 16 words. They go through
+// the warp's 2 KiB of staging so that each store writes whole stretches of rows:
+// 16 bytes a lane where the rows are aligned so, else one element a lane along
+// the rows. rows, cols: how many of the 32 rows and 64 / kSize columns exist
+// (<= 0: none). add (4-byte elements): to what is there.
+constexpr uint32_t kStagingBytes = 2048;
 
-__device__ __forceinline__ void store_block16(uint16_t* c, int64_t ldc, int rows, int cols, const uint32_t (&v)[16],
-                                              uint8_t* stage) {
+template <int kSize>
+__device__ __forceinline__ void store_rows(void* to, int64_t ldc, int rows, int cols, const uint32_t (&v)[16], bool add,
+                                           uint8_t* stage) {
+  constexpr int kCols = 64 / kSize;
   const uint32_t lane = lane_id();
   const uint32_t s = smem_addr(stage);
+  // 16-byte unit u of row r lies at u ^ ((r >> 1) & 3): all banks in every access
 #pragma unroll
-  for (int j = 0; j < 4; ++j)
-    st_shared_v4(s + lane * 64u + ((static_cast<uint32_t>(j) ^ ((lane >> 1) & 3u)) * 16u), v[4 * j], v[4 * j + 1],
-                 v[4 * j + 2], v[4 * j + 3]);
+  for (uint32_t u = 0; u < 4; ++u)
+    st_shared_v4(s + lane * 64u + ((u ^ ((lane >> 1) & 3u)) * 16u), v[4 * u], v[4 * u + 1], v[4 * u + 2], v[4 * u + 3]);
   __syncwarp();
-  if (cols >= 32 && ((reinterpret_cast<uintptr_t>(c) | static_cast<uintptr_t>(ldc * 2)) & 15u) == 0) {
+  uint8_t* c = static_cast<uint8_t*>(to);
+  const int64_t pitch = ldc * kSize;
+  if (cols >= kCols && ((reinterpret_cast<uintptr_t>(c) | static_cast<uintptr_t>(pitch)) & 15u) == 0) {
     const uint32_t unit = lane & 3u;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const uint32_t r = static_cast<uint32_t>(i) * 8u + (lane >> 2);
-      const uint4 w = *reinterpret_cast<const uint4*>(stage + r * 64u + ((unit ^ ((r >> 1) & 3u)) * 16u));
-      if (static_cast<int>(r) < rows) *reinterpret_cast<uint4*>(c + static_cast<int64_t>(r) * ldc + unit * 8u) = w;
-    }
-  } else {
-    const bool mine = static_cast<int>(lane) < cols;
-    uint16_t* p = c + lane;
-#pragma unroll 8
-    for (int r = 0; r < 32; ++r) {
-      const uint32_t unit = (lane >> 3) ^ ((static_cast<uint32_t>(r) >> 1) & 3u);
-      const uint16_t w = *reinterpret_cast<const uint16_t*>(stage + r * 64 + unit * 16u + (lane & 7u) * 2u);
-      if (mine && r < rows) *p = w;
-      p += ldc;
-    }
-  }
-  __syncwarp();
-}
-
-__device__ __forceinline__ void store_block32(float* c, int64_t ldc, int rows, int cols, const float (&v)[32],
-                                              bool add, uint8_t* stage) {
-  const uint32_t lane = lane_id();
-  const uint32_t s = smem_addr(stage);
-#pragma unroll
-  for (int u = 0; u < 8; ++u)
-    st_shared_v4(s + lane * 128u + ((static_cast<uint32_t>(u) ^ (lane & 7u)) * 16u), __float_as_uint(v[4 * u]),
-                 __float_as_uint(v[4 * u + 1]), __float_as_uint(v[4 * u + 2]), __float_as_uint(v[4 * u + 3]));
-  __syncwarp();
-  if (cols >= 32 && ((reinterpret_cast<uintptr_t>(c) | static_cast<uintptr_t>(ldc * 4)) & 15u) == 0) {
-    const uint32_t unit = lane & 7u;
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const uint32_t r = static_cast<uint32_t>(i) * 4u + (lane >> 3);
-      float4 w = *reinterpret_cast<const float4*>(stage + r * 128u + ((unit ^ (r & 7u)) * 16u));
-      float4* p = reinterpret_cast<float4*>(c + static_cast<int64_t>(r) * ldc + unit * 4u);
-      if (static_cast<int>(r) < rows) {
-        if (add) {
-          const float4 o = *p;
-          w = make_float4(o.x + w.x, o.y + w.y, o.z + w.z, o.w + w.w);
-        }
-        *p = w;
+    for (uint32_t i = 0; i < 4; ++i) {
+      const uint32_t r = i * 8u + (lane >> 2);
+      uint4 w = *reinterpret_cast<const uint4*>(stage + r * 64u + ((unit ^ ((r >> 1) & 3u)) * 16u));
+      if (static_cast<int>(r) >= rows) continue;
+      uint4* p = reinterpret_cast<uint4*>(c + r * pitch) + unit;
+      if (kSize == 4 && add) {
+        const uint4 o = *p;
+        w.x = __float_as_uint(__uint_as_float(o.x) + __uint_as_float(w.x));
+        w.y = __float_as_uint(__uint_as_float(o.y) + __uint_as_float(w.y));
+        w.z = __float_as_uint(__uint_as_float(o.z) + __uint_as_float(w.z));
+        w.w = __float_as_uint(__uint_as_float(o.w) + __uint_as_float(w.w));
       }
+      *p = w;
     }
   } else {
-    const bool mine = static_cast<int>(lane) < cols;
-    float* p = c + lane;
+    constexpr uint32_t kPer = 16 / kSize;      // elements of a unit
+    constexpr int kStep = 32 / kCols;          // rows an access covers: 1, or 2 (fp32)
+    const uint32_t col = lane % kCols, sub = lane / kCols;
+    const bool mine = static_cast<int>(col) < cols;
+    uint8_t* p = c + static_cast<int64_t>(sub) * pitch + col * kSize;
 #pragma unroll 8
-    for (int r = 0; r < 32; ++r) {
-      const uint32_t unit = (lane >> 2) ^ (static_cast<uint32_t>(r) & 7u);
-      const float w = *reinterpret_cast<const float*>(stage + r * 128 + unit * 16u + (lane & 3u) * 4u);
-      if (mine && r < rows) *p = add ? *p + w : w;
-      p += ldc;
+    for (int i = 0; i < 32; i += kStep) {
+      const uint32_t r = static_cast<uint32_t>(i) + sub;
+      const uint8_t* from = stage + r * 64u + (((col / kPer) ^ ((r >> 1) & 3u)) * 16u) + (col % kPer) * kSize;
+      if (mine && static_cast<int>(r) < rows) {
+        if constexpr (kSize == 2) {
+          *reinterpret_cast<uint16_t*>(p) = *reinterpret_cast<const uint16_t*>(from);
+        } else {
+          const float w = *reinterpret_cast<const float*>(from);
+          float* q = reinterpret_cast<float*>(p);
+          *q = add ? *q + w : w;
+        }
+      }
+      p += kStep * pitch;
     }
   }
   __syncwarp();
 }
 
-// 32 fp32 values a lane as C's element type.
+// 32 fp32 values a lane, from column col0 of row row0 + lane, as C's element type.
 __device__ __forceinline__ void store_block(const FfArgs& a, int row0, int col0, const float (&v)[32], uint8_t* stage) {
   const int64_t at = static_cast<int64_t>(row0) * a.ldc + col0;
+  uint32_t w[16];
   if (a.out_kind == kOutF32) {
-    store_block32(static_cast<float*>(a.c) + at, a.ldc, a.m - row0, a.n - col0, v, a.accumulate != 0, stage);
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+#pragma unroll
+      for (int j = 0; j < 16; ++j) w[j] = __float_as_uint(v[16 * h + j]);
+      store_rows<4>(static_cast<float*>(a.c) + at + 16 * h, a.ldc, a.m - row0, a.n - col0 - 16 * h, w, a.accumulate != 0,
+                    stage);
+    }
     return;
   }
-  uint32_t p[16];
   if (a.out_kind == kOutBf16) {
 #pragma unroll
-    for (int j = 0; j < 16; ++j) p[j] = pack16<true>(v[2 * j], v[2 * j + 1]);
+    for (int j = 0; j < 16; ++j) w[j] = pack16<true>(v[2 * j], v[2 * j + 1]);
   } else {
 #pragma unroll
-    for (int j = 0; j < 16; ++j) p[j] = pack16<false>(v[2 * j], v[2 * j + 1]);
+    for (int j = 0; j < 16; ++j) w[j] = pack16<false>(v[2 * j], v[2 * j + 1]);
   }
-  store_block16(static_cast<uint16_t*>(a.c) + at, a.ldc, a.m - row0, a.n - col0, p, stage);
+  store_rows<2>(static_cast<uint16_t*>(a.c) + at, a.ldc, a.m - row0, a.n - col0, w, false, stage);
 }
 
 }  // namespace ff

@@ -15,8 +15,8 @@
 //    memory's buffers, and the epilogue warps fold it, scaled, into fp32 sums
 //    in registers while the next block multiplies.
 //
-// One persistent CTA (or pair: cta_group::2, 256 rows) per SM: warp 0 moves
-// tiles with the TMA into a ring, one thread of warp 1 issues the MMAs, warps
+// One persistent CTA (or pair: cta_group::2, 256 rows) per SM: warps 0 and 2
+// move A's and B's tiles with the TMA into a ring, warp 1 issues the MMAs, warps
 // 4 to 11 are the epilogue, two for each quarter of tensor memory.
 //
 // What bounds them is the tensor core: see the figures at the instantiations.
@@ -29,14 +29,15 @@
 namespace gemm_tn_dev {
 namespace ff {
 
-constexpr int kThreads = 384;
+constexpr uint32_t kLoadA = 0, kMultiply = 1, kLoadB = 2;   // warps
 constexpr int kFirstEpilogueWarp = 4;
-constexpr int kEpilogueWarps = 8;
-// e4m3: an epilogue thread holds 128 sums and the block being added; the first
+// e4m3: an epilogue thread holds 128 sums and the values being added; the first
 // warpgroup gives up registers for it (128 x 72 + 256 x 216 = 384 x 168, what
 // the block is launched with)
+constexpr int kEpilogueWarps = 8;
+constexpr int kThreads = 32 * (kFirstEpilogueWarp + kEpilogueWarps);
 constexpr uint32_t kFewRegisters = 72, kManyRegisters = 216;
-static_assert(128 * kFewRegisters + 256 * kManyRegisters <= 384 * 168, "register split");
+static_assert(128 * kFewRegisters + 256 * kManyRegisters <= kThreads * 168, "register split");
 constexpr int kGated = 0, kNt = 1, kE4m3 = 2, kE4m3Rows = 3;   // kE4m3Rows: a scale for each row of B, else for 128 rows
 
 template <int kForm_, int kCtaGroup_, int kBlockN_, int kStages_, bool kBf16_>
@@ -57,11 +58,23 @@ struct Tile {
   static constexpr uint32_t kBoxBytes = 64 * 64 * 2;     // nt: 64 x 64 boxes
   static constexpr int kBuffers = kScaled ? 512 / kBlockN : 2;   // of tensor memory
   static constexpr uint32_t kTmemCols = kBuffers * kBlockN;
-  static constexpr uint32_t kStagingBytes = 4096;        // per epilogue warp
+  // e4m3: warps 1 and 3 multiply, every other block each
+  static constexpr int kMultiplyWarps = kScaled ? 2 : 1;
+  // e4m3: a ring of the blocks' scales. A block's are loaded with its operands.
+  // Its slot is free once its sums are made; when the stage of block i is
+  // loaded anew (with block i + kStages), block i has been multiplied, so the
+  // one kBuffers before it has left tensor memory and the one before that has
+  // been added: at most kStages + kBuffers + 1 blocks' scales are alive.
+  static constexpr int kScaleSlots = kStages + kBuffers + 1;
+  static constexpr uint32_t kAScaleBytes = kBlockM * 4;
+  static constexpr uint32_t kBScaleBytes = kForm == kE4m3Rows ? kBlockN * 4 : (kBlockN + 127) / 128 * 16;
+  static constexpr uint32_t kScaleStride = kForm == kE4m3Rows ? kAScaleBytes + kBScaleBytes : kAScaleBytes + 128;
+  static constexpr uint32_t kStageScales = kScaled ? kAScaleBytes + kBScaleBytes : 0;
   static constexpr uint32_t kOffA = 0;
   static constexpr uint32_t kOffB = kOffA + kStages * kStageA;
   static constexpr uint32_t kOffStaging = kOffB + kStages * kStageB;
-  static constexpr uint32_t kOffBar = kOffStaging + kEpilogueWarps * kStagingBytes;
+  static constexpr uint32_t kOffScale = kOffStaging + kEpilogueWarps * kStagingBytes;
+  static constexpr uint32_t kOffBar = kOffScale + (kScaled ? kScaleSlots * kScaleStride : 0);
   static constexpr int kNumBars = 2 * kStages + 2 * kBuffers + 1;   // full, empty, sum full, sum empty, drain
   static constexpr uint32_t kOffTmemSlot = kOffBar + kNumBars * 8;
   static constexpr uint32_t kOffAbort = kOffTmemSlot + 4;
@@ -105,6 +118,7 @@ __global__ void __launch_bounds__(kThreads, 1) ff_gemm_kernel(const __grid_const
   const bool leader = rank == 0;
   auto a_tile = [&](int s) { return base + T::kOffA + s * T::kStageA; };
   auto b_tile = [&](int s) { return base + T::kOffB + s * T::kStageB; };
+  auto scales_at = [&](int s) { return base + T::kOffScale + static_cast<uint32_t>(s) * T::kScaleStride; };
   auto full_bar = [&](int s) { return base + T::kOffBar + 8u * s; };
   auto empty_bar = [&](int s) { return base + T::kOffBar + 8u * (T::kStages + s); };
   auto sum_full = [&](int b) { return base + T::kOffBar + 8u * (2 * T::kStages + b); };
@@ -122,13 +136,17 @@ __global__ void __launch_bounds__(kThreads, 1) ff_gemm_kernel(const __grid_const
       mbar_init(sum_full(b), 1);
       mbar_init(sum_empty(b), T::kCtaGroup * kEpilogueWarps);
     }
-    mbar_init(drain_bar, 1);
+    mbar_init(drain_bar, T::kMultiplyWarps);
     *abort_flag = 0u;
     fence_barrier_init();
     tma_prefetch_descriptor(&args.tmap_a);
     tma_prefetch_descriptor(&args.tmap_b);
+    if constexpr (T::kScaled) {
+      tma_prefetch_descriptor(&args.tmap_as);
+      tma_prefetch_descriptor(&args.tmap_bs);
+    }
   }
-  if (warp == 1) {
+  if (warp == kMultiply) {
     tmem_alloc<T::kCtaGroup>(smem_addr(tmem_slot), T::kTmemCols);
     tmem_relinquish<T::kCtaGroup>();
   }
@@ -150,9 +168,10 @@ __global__ void __launch_bounds__(kThreads, 1) ff_gemm_kernel(const __grid_const
 
   if (warp < static_cast<uint32_t>(kFirstEpilogueWarp)) {
     if constexpr (T::kScaled) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" :: "n"(kFewRegisters));
-    if (warp == 0 && lane == 0) {
-      // ---------------------------------------------------------------- TMA producer
-      int stage = 0;
+    const uint32_t elected = elect_one();
+    if (warp == kLoadA || warp == kLoadB) {
+      // ---------------------------------------------------------------- TMA producers, one for each operand
+      int stage = 0, slot = 0;
       uint32_t phase = 0;
       Issued issued;
       bool ok = true;
@@ -162,39 +181,49 @@ __global__ void __launch_bounds__(kThreads, 1) ff_gemm_kernel(const __grid_const
         const int a_row = tm * T::kTileM + static_cast<int>(rank) * T::kBlockM;
         const int b_row = tn * T::kOutN + static_cast<int>(rank) * T::kBRows;
         for (int kb = 0; kb < args.num_k_blocks; ++kb) {
-          if (!wd.wait(empty_bar(stage), phase ^ 1u)) {
+          if (!wd.warp_wait(empty_bar(stage), phase ^ 1u)) {
             ok = false;
             break;
           }
           const uint32_t bar = T::kCtaGroup == 2 ? map_to_cta(full_bar(stage), 0u) : full_bar(stage);
-          if (leader) mbar_arrive_expect_tx(full_bar(stage), T::kCtaGroup * (T::kStageA + T::kStageB));
           auto load = [&](const CUtensorMap* map, uint32_t dst, int x, int y) {
-            if constexpr (T::kCtaGroup == 2) {
-              tma_load_2d_pair(map, dst, bar, x, y);
-            } else {
-              tma_load_2d(map, dst, bar, x, y);
-            }
+            load_warp<T::kCtaGroup>(elected, map, dst, bar, x, y);
           };
           const int k0 = kb * T::kBlockK;
-          if (kb != args.drop_load_kb || tile != first_tile) {
-            if constexpr (T::kForm == kNt) {
+          const bool skip = kb == args.drop_load_kb && tile == first_tile;
+          if (warp == kLoadA) {
+            // the bytes of both operands, and of both CTAs of a pair
+            if (leader && elected != 0) mbar_arrive_expect_tx(full_bar(stage), T::kCtaGroup * (T::kStageA + T::kStageB + T::kStageScales));
+            __syncwarp();
+            if (!skip) {
+              if constexpr (T::kForm == kNt) {
 #pragma unroll
-              for (int j = 0; j < T::kBlockM / 64; ++j)
-                load(&args.tmap_a, a_tile(stage) + j * T::kBoxBytes, a_row + 64 * j, k0);
+                for (int j = 0; j < T::kBlockM / 64; ++j)
+                  load(&args.tmap_a, a_tile(stage) + j * T::kBoxBytes, a_row + 64 * j, k0);
+              } else {
+                load(&args.tmap_a, a_tile(stage), k0, a_row);
+                if constexpr (T::kScaled) load(&args.tmap_as, scales_at(slot), a_row, kb);
+              }
+            }
+          } else if (!skip) {
+            if constexpr (T::kForm == kNt) {
 #pragma unroll
               for (int j = 0; j < T::kBRows / 64; ++j)
                 load(&args.tmap_b, b_tile(stage) + j * T::kBoxBytes, b_row + 64 * j, k0);
-            } else {
-              load(&args.tmap_a, a_tile(stage), k0, a_row);
-              if constexpr (T::kForm != kGated) {
-                load(&args.tmap_b, b_tile(stage), k0, b_row);
-              } else if constexpr (T::kCtaGroup == 2) {
-                // the pair's halves of N: the gate's rows, the other projection's
-                load(&args.tmap_b, b_tile(stage), k0, tn * T::kOutN + static_cast<int>(rank) * args.n);
+            } else if constexpr (T::kForm != kGated) {
+              load(&args.tmap_b, b_tile(stage), k0, b_row);
+              // every CTA takes the scales of all the tile's columns
+              if constexpr (T::kForm == kE4m3Rows) {
+                load(&args.tmap_bs, scales_at(slot) + T::kAScaleBytes, tn * T::kOutN, kb);
               } else {
-                load(&args.tmap_b, b_tile(stage), k0, b_row);
-                load(&args.tmap_b, b_tile(stage) + T::kStageB / 2, k0, b_row + args.n);
+                load(&args.tmap_bs, scales_at(slot) + T::kAScaleBytes, kb & ~3, tn * (T::kBlockN / 128));
               }
+            } else if constexpr (T::kCtaGroup == 2) {
+              // the pair's halves of N: the gate's rows, the other projection's
+              load(&args.tmap_b, b_tile(stage), k0, tn * T::kOutN + static_cast<int>(rank) * args.n);
+            } else {
+              load(&args.tmap_b, b_tile(stage), k0, b_row);
+              load(&args.tmap_b, b_tile(stage) + T::kStageB / 2, k0, b_row + args.n);
             }
           }
           issued.record(stage, phase);
@@ -202,27 +231,25 @@ __global__ void __launch_bounds__(kThreads, 1) ff_gemm_kernel(const __grid_const
             stage = 0;
             phase ^= 1u;
           }
+          if (T::kScaled && ++slot == T::kScaleSlots) slot = 0;
         }
       }
       // loads may still be landing if another role gave up
       for (int s = 0; s < T::kStages; ++s)
         if (leader && ((issued.issued >> s) & 1u)) wd.drain(full_bar(s), (issued.parity >> s) & 1u);
-    } else if (warp == 1 && leader && lane == 0) {
-      // ---------------------------------------------------------------- MMA issuer
-      int stage = 0, buf = 0;
+    } else if (leader && (warp == kMultiply || T::kMultiplyWarps == 2)) {
+      // ---------------------------------------------------------------- MMA issuers
+      // with two, each takes every other block (of all the CTA's tiles), and
+      // the waits of one run beside the other's
+      int stage = static_cast<int>(warp) >> 1, buf = static_cast<int>(warp) >> 1;   // warp 1: 0, warp 3: 1
       uint32_t phase = 0, buf_phase = 0;
       bool ok = true;
-      auto done = [&](uint32_t bar, uint16_t mask) {
-        if constexpr (T::kCtaGroup == 2) {
-          mma_commit_pair(bar, mask);
-        } else {
-          mma_commit(bar);
-        }
-      };
+      int first_kb = stage;
       for (int tile = first_tile; ok && tile < args.num_tiles; tile += tile_step) {
-        for (int kb = 0; kb < args.num_k_blocks; ++kb) {
-          if ((T::kScaled || kb == 0) && !wd.wait(sum_empty(buf), buf_phase ^ 1u)) ok = false;
-          if (!ok || !wd.wait(full_bar(stage), phase)) {
+        int kb = first_kb;
+        for (; kb < args.num_k_blocks; kb += T::kMultiplyWarps) {
+          if ((T::kScaled || kb == 0) && !wd.warp_wait(sum_empty(buf), buf_phase ^ 1u)) ok = false;
+          if (!ok || !wd.warp_wait(full_bar(stage), phase)) {
             ok = false;
             break;
           }
@@ -235,41 +262,40 @@ __global__ void __launch_bounds__(kThreads, 1) ff_gemm_kernel(const __grid_const
           const uint64_t b_desc = T::kForm == kNt ? sw128_mnmajor_desc(b_tile(stage), T::kBoxBytes)
                                                   : sw128_kmajor_desc(b_tile(stage));
 #pragma unroll
-          for (int kk = 0; kk < 4; ++kk) {
-            const uint32_t add = kk > 0 || (!T::kScaled && kb > 0) ? 1u : 0u;
-            if constexpr (T::kScaled) {
-              mma_f8<T::kCtaGroup>(d, a_desc + kStep * kk, b_desc + kStep * kk, T::kIdesc, add);
-            } else {
-              mma_f16<T::kCtaGroup>(d, a_desc + kStep * kk, b_desc + kStep * kk, T::kIdesc, add);
-            }
-          }
-          done(empty_bar(stage), 0x3);
-          if (++stage == T::kStages) {
-            stage = 0;
+          for (int kk = 0; kk < 4; ++kk)
+            mma_warp<T::kCtaGroup, T::kScaled>(elected, d, a_desc + kStep * kk, b_desc + kStep * kk, T::kIdesc,
+                                               kk > 0 || (!T::kScaled && kb > 0) ? 1u : 0u);
+          commit_warp<T::kCtaGroup>(elected, empty_bar(stage), 0x3);
+          stage += T::kMultiplyWarps;
+          if (stage >= T::kStages) {
+            stage -= T::kStages;
             phase ^= 1u;
           }
           if (T::kScaled || kb == args.num_k_blocks - 1) {
-            done(sum_full(buf), 0x3);
-            if (++buf == T::kBuffers) {
-              buf = 0;
+            commit_warp<T::kCtaGroup>(elected, sum_full(buf), 0x3);
+            buf += T::kMultiplyWarps;
+            if (buf >= T::kBuffers) {
+              buf -= T::kBuffers;
               buf_phase ^= 1u;
             }
           }
         }
+        first_kb = kb - args.num_k_blocks;
       }
-      // all MMAs of this thread finish before tensor memory is freed
-      done(drain_bar, 0x1);
+      // what was issued here finishes before tensor memory is freed
+      commit_warp<T::kCtaGroup>(elected, drain_bar, 0x1);
       wd.drain(drain_bar, 0);
     }
+    __syncwarp();
   } else {
     if constexpr (T::kScaled) asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" :: "n"(kManyRegisters));
     // ------------------------------------------------------------------ epilogue
     const uint32_t quarter = warp & 3u;
     const int epilogue_warp = static_cast<int>(warp) - kFirstEpilogueWarp;
     const int half = epilogue_warp >> 2;
-    uint8_t* staging = smem + T::kOffStaging + static_cast<uint32_t>(epilogue_warp) * T::kStagingBytes;
+    uint8_t* staging = smem + T::kOffStaging + static_cast<uint32_t>(epilogue_warp) * kStagingBytes;
     const uint32_t sum_empty0 = T::kCtaGroup == 2 ? map_to_cta(sum_empty(0), 0u) : sum_empty(0);
-    int buf = 0;
+    int buf = 0, slot = 0;
     uint32_t buf_phase = 0;
     bool ok = true;
     auto hand_back = [&]() {   // the buffer is in registers: the MMA warp may write it again
@@ -277,7 +303,7 @@ __global__ void __launch_bounds__(kThreads, 1) ff_gemm_kernel(const __grid_const
       __syncwarp();
       if (lane == 0) {
         if constexpr (T::kCtaGroup == 2) {
-          mbar_arrive_cluster(sum_empty0 + 8u * buf);
+          arrive_remote(sum_empty0 + 8u * buf);
         } else {
           mbar_arrive(sum_empty(buf));
         }
@@ -298,78 +324,51 @@ __global__ void __launch_bounds__(kThreads, 1) ff_gemm_kernel(const __grid_const
         // this warp's half of the columns; a thread's sums: its row's, two to a register pair
         constexpr int kCols = T::kBlockN / 2;
         const int my_col = col0 + half * kCols;
-        const int row = row0 + static_cast<int>(lane);
+        const uint32_t t_mine = t_quarter + static_cast<uint32_t>(half * kCols);
         uint64_t sum[kCols / 2];
 #pragma unroll
         for (int j = 0; j < kCols / 2; ++j) sum[j] = 0;
-        const float* sa = args.a_scale + static_cast<int64_t>(min(row, args.m - 1)) * args.as_row;
-        float* vec = reinterpret_cast<float*>(staging);   // kE4m3Rows: [2][kCols] scales of this warp's columns
-        const float* sb;
-        if constexpr (T::kForm == kE4m3) {
-          sb = args.b_scale + static_cast<int64_t>(min(my_col, args.n - 1) / 128) * args.bs_row;
-        } else {
-          sb = args.b_scale;
-        }
-        // the scales of a block are loaded a block ahead
-        float a_next = __ldg(sa), b_next[T::kForm == kE4m3 ? 1 : kCols / 32];
-        auto load_b = [&](int kb) {
-          if constexpr (T::kForm == kE4m3) {
-            b_next[0] = __ldg(sb + kb * args.bs_blk);
-          } else {
-#pragma unroll
-            for (int i = 0; i < kCols / 32; ++i)
-              b_next[i] = __ldg(sb + static_cast<int64_t>(min(my_col + i * 32 + static_cast<int>(lane), args.n - 1)) *
-                                         args.bs_row + kb * args.bs_blk);
-          }
-        };
-        load_b(0);
+#pragma unroll 1
         for (int kb = 0; kb < args.num_k_blocks; ++kb) {
-          float scale = a_next;
-          if constexpr (T::kForm == kE4m3) {
-            scale *= b_next[0];
-          } else {
-            // two buffers: the other warps' lanes never see this one, so a
-            // warp's own order is all that is needed
-#pragma unroll
-            for (int i = 0; i < kCols / 32; ++i) vec[(kb & 1) * kCols + i * 32 + lane] = b_next[i];
-            __syncwarp();
-          }
-          if (kb + 1 < args.num_k_blocks) {
-            a_next = __ldg(sa + (kb + 1) * args.as_blk);
-            load_b(kb + 1);
-          }
-          if (!__all_sync(0xffffffffu, wd.wait(sum_full(buf), buf_phase))) {
+          if (!wd.warp_wait(sum_full(buf), buf_phase)) {
             ok = false;
             break;
           }
           tc_fence_after_sync();
-          const uint32_t t = t_quarter + static_cast<uint32_t>(buf * T::kBlockN + half * kCols);
-          const uint64_t scale2 = f32x2_pack(scale, scale);
-          uint32_t v[2][16];
-          tmem_load_32x16(t, v[0]);
+          const uint32_t t = t_mine + static_cast<uint32_t>(buf * T::kBlockN);
+          // (the block has been multiplied, so its scales have landed too)
+          const float* scales = reinterpret_cast<const float*>(smem + T::kOffScale + static_cast<uint32_t>(slot) * T::kScaleStride);
+          const float* cols = scales + T::kBlockM + half * kCols;
+          if (++slot == T::kScaleSlots) slot = 0;
+          uint64_t scale2 = 0;
 #pragma unroll
           for (int c = 0; c < kCols / 16; ++c) {
-            tmem_loaded(v[c & 1]);
-            if (c + 1 < kCols / 16) {
-              tmem_load_32x16(t + 16u * (c + 1), v[(c + 1) & 1]);
-            } else {
-              hand_back();
+            uint32_t v[16];
+            tmem_load_32x16(t + 16u * c, v);
+            if (c == 0) {
+              float scale = scales[quarter * 32u + lane];
+              if constexpr (T::kForm == kE4m3) scale *= scales[T::kBlockM + (half * kCols / 128) * 4 + (kb & 3)];
+              scale2 = f32x2_pack(scale, scale);
             }
+            tmem_loaded(v);
+            if (c == kCols / 16 - 1) hand_back();
 #pragma unroll
-            for (int j = 0; j < 8; ++j) {
-              const uint64_t p = f32x2_pack(__uint_as_float(v[c & 1][2 * j]), __uint_as_float(v[c & 1][2 * j + 1]));
-              uint64_t& s = sum[c * 8 + j];
+            for (int j = 0; j < 8; j += 2) {
+              const uint64_t p0 = f32x2_pack(__uint_as_float(v[2 * j]), __uint_as_float(v[2 * j + 1]));
+              const uint64_t p1 = f32x2_pack(__uint_as_float(v[2 * j + 2]), __uint_as_float(v[2 * j + 3]));
+              uint64_t &s0 = sum[c * 8 + j], &s1 = sum[c * 8 + j + 1];
               if constexpr (T::kForm == kE4m3) {
-                s = f32x2_fma(p, scale2, s);
+                s0 = f32x2_fma(p0, scale2, s0);
+                s1 = f32x2_fma(p1, scale2, s1);
               } else {
-                const uint64_t b2 = *reinterpret_cast<const uint64_t*>(vec + (kb & 1) * kCols + c * 16 + 2 * j);
-                s = f32x2_fma(f32x2_mul(p, scale2), b2, s);
+                const ulonglong2 b = *reinterpret_cast<const ulonglong2*>(cols + c * 16 + 2 * j);
+                s0 = f32x2_fma(f32x2_mul(p0, scale2), b.x, s0);
+                s1 = f32x2_fma(f32x2_mul(p1, scale2), b.y, s1);
               }
             }
           }
         }
         if (!ok) break;
-        if constexpr (T::kForm == kE4m3Rows) __syncwarp();   // the scales' memory is the staging's
 #pragma unroll
         for (int c = 0; c < kCols / 32; ++c) {
           float out[32];
@@ -401,11 +400,11 @@ __global__ void __launch_bounds__(kThreads, 1) ff_gemm_kernel(const __grid_const
 #pragma unroll
               for (int j = 0; j < 16; ++j)
                 p[j] = pack16<T::kBf16>(__uint_as_float(v[2 * j]), __uint_as_float(v[2 * j + 1]));
-              store_block16(pre, args.ldp, args.m - row0, args.n - col, p, staging);
+              store_rows<2>(pre, args.ldp, args.m - row0, args.n - col, p, false, staging);
 #pragma unroll
               for (int j = 0; j < 16; ++j)
                 p[j] = pack16<T::kBf16>(__uint_as_float(u[2 * j]), __uint_as_float(u[2 * j + 1]));
-              store_block16(pre + args.n, args.ldp, args.m - row0, args.n - col, p, staging);
+              store_rows<2>(pre + args.n, args.ldp, args.m - row0, args.n - col, p, false, staging);
             }
             float h[32];
             if (args.activation == kSilu) {
@@ -438,7 +437,7 @@ __global__ void __launch_bounds__(kThreads, 1) ff_gemm_kernel(const __grid_const
   } else {
     __syncthreads();
   }
-  if (warp == 1) {
+  if (warp == kMultiply) {
     tc_fence_after_sync();
     tmem_dealloc<T::kCtaGroup>(tmem_base, T::kTmemCols);
   }

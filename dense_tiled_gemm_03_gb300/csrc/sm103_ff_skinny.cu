@@ -110,70 +110,65 @@ __global__ void __launch_bounds__(kThreads, 2) ff_skinny_kernel(const __grid_con
   const Waiter<1> wd{args.status, args.timeout_ns, abort_flag};
 
   if (warp == 0) {
-    if (lane == 0) {
-      // ------------------------------------------------------------ TMA producer
-      const uint64_t once = l2_policy_evict_first();
-      int stage = 0;
-      uint32_t phase = 0;
-      Issued issued;
-      for (int kb = kb0; kb < kb1; ++kb) {
-        if (!wd.wait(empty_bar(stage), phase ^ 1u)) break;
-        const uint32_t bar = full_bar(stage);
-        mbar_arrive_expect_tx(bar, kStageB + C::kStageA);
-        if (kb - kb0 != args.drop_load_kb) {
-          const int k0 = kb * C::kBlockK;
-          if constexpr (C::kGatedForm) {
-            tma_load_2d_hint(&args.tmap_b, b_tile(stage), bar, k0, tn * 64, once);
-            tma_load_2d_hint(&args.tmap_b, b_tile(stage) + kStageB / 2, bar, k0, tn * 64 + args.n, once);
-          } else {
-            tma_load_2d_hint(&args.tmap_b, b_tile(stage), bar, k0, tn * 128, once);
-          }
-          tma_load_2d(&args.tmap_a, a_tile(stage), bar, k0, 0);
+    // -------------------------------------------------------------- TMA producer (the whole warp, one lane issues)
+    const uint32_t elected = elect_one();
+    const uint64_t once = l2_policy_evict_first();
+    int stage = 0;
+    uint32_t phase = 0;
+    Issued issued;
+    for (int kb = kb0; kb < kb1; ++kb) {
+      if (!wd.warp_wait(empty_bar(stage), phase ^ 1u)) break;
+      const uint32_t bar = full_bar(stage);
+      if (elected != 0) mbar_arrive_expect_tx(bar, kStageB + C::kStageA);
+      __syncwarp();
+      if (kb - kb0 != args.drop_load_kb) {
+        const int k0 = kb * C::kBlockK;
+        if constexpr (C::kGatedForm) {
+          load_warp_hint(elected, &args.tmap_b, b_tile(stage), bar, k0, tn * 64, once);
+          load_warp_hint(elected, &args.tmap_b, b_tile(stage) + kStageB / 2, bar, k0, tn * 64 + args.n, once);
+        } else {
+          load_warp_hint(elected, &args.tmap_b, b_tile(stage), bar, k0, tn * 128, once);
         }
-        issued.record(stage, phase);
-        if (++stage == C::kStages) {
-          stage = 0;
-          phase ^= 1u;
-        }
+        load_warp<1>(elected, &args.tmap_a, a_tile(stage), bar, k0, 0);
       }
-      for (int s = 0; s < C::kStages; ++s)
-        if ((issued.issued >> s) & 1u) wd.drain(full_bar(s), (issued.parity >> s) & 1u);
+      issued.record(stage, phase);
+      if (++stage == C::kStages) {
+        stage = 0;
+        phase ^= 1u;
+      }
     }
+    for (int s = 0; s < C::kStages; ++s)
+      if ((issued.issued >> s) & 1u) wd.drain(full_bar(s), (issued.parity >> s) & 1u);
   } else if (warp == 1) {
-    if (lane == 0) {
-      // ------------------------------------------------------------ MMA issuer: D[j][i] += B[j] A[i]
-      int stage = 0, buf = 0;
-      uint32_t phase = 0, buf_phase = 0;
-      for (int kb = kb0; kb < kb1; ++kb) {
-        if (C::kScaled && !wd.wait(sum_empty(buf), buf_phase ^ 1u)) break;
-        if (!wd.wait(full_bar(stage), phase)) break;
-        tc_fence_after_sync();
-        const uint32_t d = tmem_base + static_cast<uint32_t>(buf * C::kN);
-        const uint64_t a_desc = sw128_kmajor_desc(a_tile(stage)), b_desc = sw128_kmajor_desc(b_tile(stage));
+    // -------------------------------------------------------------- MMA issuer: D[j][i] += B[j] A[i]
+    const uint32_t elected = elect_one();
+    int stage = 0, buf = 0;
+    uint32_t phase = 0, buf_phase = 0;
+    for (int kb = kb0; kb < kb1; ++kb) {
+      if (C::kScaled && !wd.warp_wait(sum_empty(buf), buf_phase ^ 1u)) break;
+      if (!wd.warp_wait(full_bar(stage), phase)) break;
+      tc_fence_after_sync();
+      const uint32_t d = tmem_base + static_cast<uint32_t>(buf * C::kN);
+      const uint64_t a_desc = sw128_kmajor_desc(a_tile(stage)), b_desc = sw128_kmajor_desc(b_tile(stage));
 #pragma unroll
-        for (int kk = 0; kk < 4; ++kk) {
-          if constexpr (C::kScaled) {
-            mma_f8<1>(d, b_desc + 2u * kk, a_desc + 2u * kk, C::kIdesc, kk > 0 ? 1u : 0u);
-          } else {
-            mma_f16<1>(d, b_desc + 2u * kk, a_desc + 2u * kk, C::kIdesc, kk > 0 || kb > kb0 ? 1u : 0u);
-          }
-        }
-        mma_commit(empty_bar(stage));
-        if (++stage == C::kStages) {
-          stage = 0;
-          phase ^= 1u;
-        }
-        if (C::kScaled || kb == kb1 - 1) {
-          mma_commit(sum_full(buf));
-          if (++buf == C::kBuffers) {
-            buf = 0;
-            buf_phase ^= 1u;
-          }
+      for (int kk = 0; kk < 4; ++kk)
+        mma_warp<1, C::kScaled>(elected, d, b_desc + 2u * kk, a_desc + 2u * kk, C::kIdesc,
+                                kk > 0 || (!C::kScaled && kb > kb0) ? 1u : 0u);
+      commit_warp<1>(elected, empty_bar(stage), 0);
+      if (++stage == C::kStages) {
+        stage = 0;
+        phase ^= 1u;
+      }
+      if (C::kScaled || kb == kb1 - 1) {
+        commit_warp<1>(elected, sum_full(buf), 0);
+        if (++buf == C::kBuffers) {
+          buf = 0;
+          buf_phase ^= 1u;
         }
       }
-      mma_commit(drain_bar);
-      wd.drain(drain_bar, 0);
     }
+    commit_warp<1>(elected, drain_bar, 0);
+    wd.drain(drain_bar, 0);
   } else {
     // -------------------------------------------------------------- a lane's sums -> own shared memory
     const uint32_t quarter = warp & 3u;
