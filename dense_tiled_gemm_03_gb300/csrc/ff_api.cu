@@ -92,13 +92,16 @@ bool scales_addressable(const float* p, int64_t rows, int64_t cols, int64_t s_i,
 
 // ---------------------------------------------------------------- the choice of a kernel
 
-// Time of a tile of each shape, relative to the first's, where tiles abound.
-// e4m3 8192^3: 397, 446 and 450 us; with a scale for every row of B 588, 567 and 559.
+// Time of a tile of each shape, relative to the first's, where tiles abound
+// (smaller tiles read more from L2 for their work). Measured, us: gated 8192 x
+// 16384 x 4096 1061, 1512 and 1790; nt 16384 x 4096 x 8192 638, 771 and 900;
+// e4m3 8192^3 397, 446 and 450, with a scale for every row of B 588, 567 and 559.
 constexpr double kTileTime[4][kNumFfTiles] = {
-    {1.0, 0.54, 0.58}, {1.0, 0.54, 0.58}, {1.0, 0.56, 0.57}, {1.0, 0.48, 0.475}};
+    {1.0, 0.71, 0.84}, {1.0, 0.60, 0.70}, {1.0, 0.56, 0.57}, {1.0, 0.48, 0.475}};
 
-// Rows of A up to which the skinny kernel runs.
-constexpr int64_t kMostSkinny = 64;
+// Rows of A up to which the skinny kernel runs whatever the number of tiles, and
+// up to which it can run.
+constexpr int64_t kFew = 32, kMostFew = 128;
 
 struct Choice {
   int rows = 0, splits = 0;   // skinny (rows != 0)
@@ -137,9 +140,9 @@ Forced forced() {
 int choose(int kind, FfArgs& a, int sms, Choice* to) {
   const int64_t out_n = kind == kFfGated ? 2 : 1;   // columns of the product for one of C
   const Forced force = forced();
-  const bool force_skinny = a.m <= 128 && a.num_k_blocks >= force.splits &&
+  const bool force_skinny = a.m <= kMostFew && a.num_k_blocks >= force.splits &&
                             (force.splits == 1 || force.splits == 2 || force.splits == 4 || force.splits == 8);
-  if (kind != kFfNt && (force_skinny || (force.tile < 0 && a.m <= kMostSkinny))) {
+  if (kind != kFfNt && (force_skinny || (force.tile < 0 && a.m <= kFew))) {
     to->rows = a.m <= 16 ? 16 : a.m <= 32 ? 32 : a.m <= 64 ? 64 : 128;
     const int64_t tiles = (static_cast<int64_t>(a.n) * out_n + 127) / 128;
     int splits = 1;

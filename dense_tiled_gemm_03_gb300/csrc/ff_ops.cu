@@ -1,6 +1,8 @@
 // ff_ops.cu -- the feed-forward operators that only move and scale: the gated
 // projection's elementwise gradient and quantising to e4m3 in blocks of 128.
 // Both are bound by memory: each element is read once and written once.
+#include <type_traits>
+
 #include "sm103_ff.cuh"
 
 namespace gemm_tn_dev {
@@ -10,81 +12,77 @@ namespace ff {
 // h = act(g) u: dg = dh u act'(g), du = dh act(g), in 32 bits from 16-bit
 // values, rounded once to 16.
 constexpr int kGradThreads = 256;
-constexpr int kGradPer = 2;   // 8-element pieces a thread loads before it computes
 
-template <bool kBf16, int kAct>
-__device__ __forceinline__ void grad_piece(const uint4& d4, const uint4& g4, const uint4& u4, uint4& dg4, uint4& du4) {
-  const uint32_t d[4] = {d4.x, d4.y, d4.z, d4.w}, g[4] = {g4.x, g4.y, g4.z, g4.w}, u[4] = {u4.x, u4.y, u4.z, u4.w};
-  uint32_t og[4], ou[4];
-#pragma unroll
-  for (int j = 0; j < 4; ++j) {
-    const float d0 = widen16<kBf16>(d[j] & 0xFFFFu), d1 = widen16<kBf16>(d[j] >> 16);
-    const float2 a0 = act_slope<kAct>(widen16<kBf16>(g[j] & 0xFFFFu)), a1 = act_slope<kAct>(widen16<kBf16>(g[j] >> 16));
-    og[j] = pack16<kBf16>(d0 * widen16<kBf16>(u[j] & 0xFFFFu) * a0.y, d1 * widen16<kBf16>(u[j] >> 16) * a1.y);
-    ou[j] = pack16<kBf16>(d0 * a0.x, d1 * a1.x);
-  }
-  dg4 = make_uint4(og[0], og[1], og[2], og[3]);
-  du4 = make_uint4(ou[0], ou[1], ou[2], ou[3]);
-}
-
-// 16-byte pieces are counted in 32 bits (2^32 of them would be 64 GiB an
-// operand), single elements in 64.
-template <bool kVec>
-struct IndexOf {
-  using type = uint32_t;
+// A piece of kWidth 16-bit elements (8, 4 or 1), as a thread loads it.
+template <int kWidth>
+struct Piece;
+template <>
+struct Piece<8> {
+  using type = uint4;
+  static constexpr int kPer = 2;   // pieces that a thread loads before it computes
 };
 template <>
-struct IndexOf<false> {
-  using type = uint64_t;
+struct Piece<4> {
+  using type = uint2;
+  static constexpr int kPer = 4;
+};
+template <>
+struct Piece<1> {
+  using type = uint16_t;
+  static constexpr int kPer = 8;
 };
 
-// kVec: 16-byte pieces (n, the pitches and the pointers allow them); else
-// element by element.
-template <bool kBf16, int kAct, bool kVec>
+// Pieces of 8 or 4 are counted in 32 bits, single elements in 64.
+template <bool kBf16, int kAct, int kWidth>
 __global__ void __launch_bounds__(kGradThreads) gated_grad_kernel(const GatedGradArgs a) {
+  using P = typename Piece<kWidth>::type;
+  using Index = typename std::conditional<kWidth == 1, uint64_t, uint32_t>::type;
+  constexpr int kPer = Piece<kWidth>::kPer;
   griddep_wait();
   griddep_launch_dependents();
   const uint16_t *grad = static_cast<const uint16_t*>(a.grad), *pre = static_cast<const uint16_t*>(a.pre);
   uint16_t* out = static_cast<uint16_t*>(a.out);
-  constexpr int kWidth = kVec ? 8 : 1;
-  using Index = typename IndexOf<kVec>::type;
   const Index pieces = static_cast<Index>(a.n / kWidth), total = static_cast<Index>(a.m) * pieces;
-  const Index step = static_cast<Index>(gridDim.x) * (kGradThreads * kGradPer);
-  for (Index at = static_cast<Index>(blockIdx.x) * (kGradThreads * kGradPer) + threadIdx.x; at < total; at += step) {
-    if constexpr (kVec) {
-      uint4 dv[kGradPer], gv[kGradPer], uv[kGradPer];
-      uint4* to[kGradPer];
+  const Index step = static_cast<Index>(gridDim.x) * (kGradThreads * kPer);
+  for (Index at = static_cast<Index>(blockIdx.x) * (kGradThreads * kPer) + threadIdx.x; at < total; at += step) {
+    P dv[kPer], gv[kPer], uv[kPer];
+    uint16_t* to[kPer];
 #pragma unroll
-      for (int i = 0; i < kGradPer; ++i) {
-        const Index x = at + i * kGradThreads;
-        if (x >= total) continue;
-        const Index row = x / pieces, p = x - row * pieces;
-        const int64_t r = static_cast<int64_t>(row);
-        dv[i] = __ldcs(reinterpret_cast<const uint4*>(grad + r * a.ldg) + p);
-        gv[i] = __ldcs(reinterpret_cast<const uint4*>(pre + r * a.ldp) + p);
-        uv[i] = __ldcs(reinterpret_cast<const uint4*>(pre + r * a.ldp + a.n) + p);
-        to[i] = reinterpret_cast<uint4*>(out + r * a.ldo) + p;
-      }
+    for (int i = 0; i < kPer; ++i) {
+      const Index x = at + i * kGradThreads;
+      if (x >= total) continue;
+      const Index row = x / pieces;
+      const int64_t r = static_cast<int64_t>(row), j = static_cast<int64_t>(x - row * pieces) * kWidth;
+      dv[i] = __ldcs(reinterpret_cast<const P*>(grad + r * a.ldg + j));
+      gv[i] = __ldcs(reinterpret_cast<const P*>(pre + r * a.ldp + j));
+      uv[i] = __ldcs(reinterpret_cast<const P*>(pre + r * a.ldp + a.n + j));
+      to[i] = out + r * a.ldo + j;
+    }
 #pragma unroll
-      for (int i = 0; i < kGradPer; ++i) {
-        if (at + i * kGradThreads >= total) continue;
-        uint4 x, y;
-        grad_piece<kBf16, kAct>(dv[i], gv[i], uv[i], x, y);
-        to[i][0] = x;
-        to[i][pieces] = y;
-      }
-    } else {
+    for (int i = 0; i < kPer; ++i) {
+      if (at + i * kGradThreads >= total) continue;
+      P dg, du;
+      if constexpr (kWidth == 1) {
+        const float d = widen16<kBf16>(dv[i]);
+        const float2 s = act_slope<kAct>(widen16<kBf16>(gv[i]));
+        const uint32_t both = pack16<kBf16>(d * widen16<kBf16>(uv[i]) * s.y, d * s.x);
+        dg = static_cast<uint16_t>(both);
+        du = static_cast<uint16_t>(both >> 16);
+      } else {
+        const uint32_t *d = reinterpret_cast<const uint32_t*>(&dv[i]), *g = reinterpret_cast<const uint32_t*>(&gv[i]),
+                       *u = reinterpret_cast<const uint32_t*>(&uv[i]);
+        uint32_t *og = reinterpret_cast<uint32_t*>(&dg), *ou = reinterpret_cast<uint32_t*>(&du);
 #pragma unroll
-      for (int i = 0; i < kGradPer; ++i) {
-        const Index x = at + i * kGradThreads;
-        if (x >= total) continue;
-        const int64_t row = static_cast<int64_t>(x / pieces), j = static_cast<int64_t>(x) - row * a.n;
-        const float d = widen16<kBf16>(grad[row * a.ldg + j]), u = widen16<kBf16>(pre[row * a.ldp + a.n + j]);
-        const float2 s = act_slope<kAct>(widen16<kBf16>(pre[row * a.ldp + j]));
-        const uint32_t both = pack16<kBf16>(d * u * s.y, d * s.x);
-        out[row * a.ldo + j] = static_cast<uint16_t>(both);
-        out[row * a.ldo + a.n + j] = static_cast<uint16_t>(both >> 16);
+        for (int w = 0; w < kWidth / 2; ++w) {
+          const float d0 = widen16<kBf16>(d[w] & 0xFFFFu), d1 = widen16<kBf16>(d[w] >> 16);
+          const float2 s0 = act_slope<kAct>(widen16<kBf16>(g[w] & 0xFFFFu));
+          const float2 s1 = act_slope<kAct>(widen16<kBf16>(g[w] >> 16));
+          og[w] = pack16<kBf16>(d0 * widen16<kBf16>(u[w] & 0xFFFFu) * s0.y, d1 * widen16<kBf16>(u[w] >> 16) * s1.y);
+          ou[w] = pack16<kBf16>(d0 * s0.x, d1 * s1.x);
+        }
       }
+      *reinterpret_cast<P*>(to[i]) = dg;
+      *reinterpret_cast<P*>(to[i] + a.n) = du;
     }
   }
 }
@@ -125,13 +123,47 @@ __global__ void __launch_bounds__(256) pack_scales_kernel(const PackArgs a) {
 // A CTA takes a tile of 128 x 128 elements, each thread holding its part in
 // registers: 16 bytes a load, all of them issued before the first is used. A
 // block of the scales is a row of the tile, the tile, or (transposed) a column.
+// Magnitudes are compared as the integers that their bits are (two 16-bit ones
+// at a time), infinities and NaN on top: a block whose largest magnitude is one
+// of these is looked through again without them.
 
 constexpr int kQuantThreads = 256;
 
-__device__ __forceinline__ float finite_magnitude(float x) {
-  const float m = fabsf(x);
-  return m <= 3.402823466e38f ? m : 0.0f;
-}
+// kSrc: 0 fp16, 1 bf16, 2 fp32.
+template <int kSrc>
+struct Source {
+  static constexpr int kWidth = kSrc == 2 ? 4 : 8;          // elements of a 16-byte load
+  static constexpr int kLanes = 128 / kWidth;               // threads along a row
+  static constexpr int kRows = 128 / (kQuantThreads / kLanes);   // consecutive rows a thread holds: 8, or 16 (fp32)
+  static constexpr uint32_t kLargest = kSrc == 0 ? 0x7BFFu : kSrc == 1 ? 0x7F7Fu : 0x7F7FFFFFu;   // finite magnitude
+
+  // Element j of a load, and its magnitude's bits.
+  static __device__ __forceinline__ uint32_t bits(const uint32_t (&w)[4], int j) {
+    if constexpr (kSrc == 2) return w[j] & 0x7FFFFFFFu;
+    return (w[j >> 1] >> ((j & 1) * 16)) & 0x7FFFu;
+  }
+  static __device__ __forceinline__ float value(const uint32_t (&w)[4], int j) {
+    if constexpr (kSrc == 2) return __uint_as_float(w[j]);
+    return widen16<kSrc == 1>((j & 1) ? w[j >> 1] >> 16 : w[j >> 1] & 0xFFFFu);
+  }
+  static __device__ __forceinline__ float of_bits(uint32_t magnitude) {
+    if constexpr (kSrc == 2) return __uint_as_float(magnitude);
+    return widen16<kSrc == 1>(magnitude);
+  }
+  // The larger magnitudes of two words of magnitudes, element by element.
+  static __device__ __forceinline__ uint32_t larger(uint32_t a, uint32_t b) { return kSrc == 2 ? max(a, b) : __vmaxu2(a, b); }
+  static __device__ __forceinline__ uint32_t magnitudes(uint32_t w) { return w & (kSrc == 2 ? 0x7FFFFFFFu : 0x7FFF7FFFu); }
+  // The largest of a word's.
+  static __device__ __forceinline__ uint32_t largest(uint32_t w) { return kSrc == 2 ? w : max(w >> 16, w & 0xFFFFu); }
+  static __device__ __forceinline__ uint32_t largest_finite(uint32_t so_far, const uint32_t (&w)[4]) {
+#pragma unroll
+    for (int j = 0; j < kWidth; ++j) {
+      const uint32_t m = bits(w, j);
+      if (m <= kLargest) so_far = max(so_far, m);
+    }
+    return so_far;
+  }
+};
 
 // The exponent t of the scale of a block whose largest magnitude is `top`.
 __device__ __forceinline__ int scale_exponent(float top) {
@@ -141,152 +173,222 @@ __device__ __forceinline__ int scale_exponent(float top) {
   return t < -126 ? -126 : t;   // (t <= 120)
 }
 __device__ __forceinline__ float power_of_two(int t) { return __uint_as_float(static_cast<uint32_t>(t + 127) << 23); }
+// The reciprocal of a power of two from its exponent field, exactly.
+__device__ __forceinline__ float inverse(float s) { return __uint_as_float((254u << 23) - __float_as_uint(s)); }
 
-__device__ __forceinline__ uint32_t quantize4(float a, float b, float c, float d, float inv) {
-  auto scaled = [&](float x) { return fabsf(x) <= 3.402823466e38f ? x * inv : __uint_as_float(0x7FC00000u); };
-  return cvt_e4m3x2(scaled(a), scaled(b)) | (cvt_e4m3x2(scaled(c), scaled(d)) << 16);
+__device__ __forceinline__ float nan_unless_finite(float x) {
+  return fabsf(x) <= 3.402823466e38f ? x : __uint_as_float(0x7FC00000u);
+}
+__device__ __forceinline__ uint32_t quantize4(float a, float b, float c, float d) {
+  return cvt_e4m3x2(a, b) | (cvt_e4m3x2(c, d) << 16);
 }
 
-// kSrc: 0 fp16, 1 bf16, 2 fp32.
-template <int kSrc>
-__device__ __forceinline__ float element(const void* x, int64_t at) {
-  if constexpr (kSrc == 2) {
-    return static_cast<const float*>(x)[at];
-  } else {
-    return widen16<kSrc == 1>(static_cast<const uint16_t*>(x)[at]);
+// The largest over kLanes lanes of each of kCount values a lane: lane l gets value
+// (l * kCount / kLanes)'s. Each step halves the values that a lane holds and
+// leaves the halves with the partner that keeps them.
+template <int kCount, int kLanes>
+__device__ __forceinline__ uint32_t largest_of_lanes(uint32_t (&v)[kCount], int lane) {
+  int n = kCount;
+#pragma unroll
+  for (int o = kLanes / 2; o > 0; o >>= 1) {
+    if (n > 1) {
+      n >>= 1;
+      const bool upper = (lane & o) != 0;
+#pragma unroll
+      for (int i = 0; i < kCount / 2; ++i) {
+        if (i >= n) continue;
+        const uint32_t mine = upper ? v[i + n] : v[i], theirs = upper ? v[i] : v[i + n];
+        v[i] = max(mine, __shfl_xor_sync(0xffffffffu, theirs, o));
+      }
+    } else {
+      v[0] = max(v[0], __shfl_xor_sync(0xffffffffu, v[0], o));
+    }
   }
+  return v[0];
 }
 
 template <int kSrc, bool kTileScale, bool kTransposed>
-__global__ void __launch_bounds__(kQuantThreads) quantize_kernel(const QuantizeArgs a, const int vec_in,
-                                                                  const int vec_out) {
-  constexpr int kWidth = kSrc == 2 ? 4 : 8;          // elements of a 16-byte load
-  constexpr int kLanes = 128 / kWidth;               // threads along a row
-  constexpr int kRows = 128 / (kQuantThreads / kLanes);   // consecutive rows a thread holds: 8, or 16 (fp32)
-  __shared__ float s_scale[128];
-  __shared__ float s_max[kQuantThreads / 32][128];
+__global__ void __launch_bounds__(kQuantThreads, kSrc == 2 ? 2 : 4) quantize_kernel(const QuantizeArgs a, const int vec_in,
+                                                                                    const int vec_out) {
+  using S = Source<kSrc>;
+  constexpr int kWidth = S::kWidth, kLanes = S::kLanes, kRows = S::kRows, kWarps = kQuantThreads / 32;
+  __shared__ __align__(16) float s_scale[128];
+  __shared__ uint32_t s_max[kTransposed && !kTileScale ? kWarps : 1][128];
+  __shared__ uint32_t s_top[kWarps];
+  __shared__ uint32_t s_odd;   // some magnitude of the tile is infinite or NaN
   __shared__ __align__(16) uint8_t s_tile[kTransposed ? 128 * 128 : 16];
 
   const uint32_t tiles = static_cast<uint32_t>((a.cols + 127) / 128);
   const uint32_t tile_row = blockIdx.x / tiles, tile_col = blockIdx.x - tile_row * tiles;
   const int64_t row0 = static_cast<int64_t>(tile_row) * 128, col0 = static_cast<int64_t>(tile_col) * 128;
   const int lane = static_cast<int>(threadIdx.x) % kLanes, group = static_cast<int>(threadIdx.x) / kLanes;
-  const int64_t col = col0 + lane * kWidth;
   const int warp = static_cast<int>(threadIdx.x) >> 5;
+  const int64_t col = col0 + lane * kWidth, first = row0 + group * kRows;
+  if (threadIdx.x == 0) s_odd = 0;
   griddep_wait();
   griddep_launch_dependents();
 
-  float v[kRows][kWidth];
-  const bool whole = vec_in != 0 && col + kWidth <= a.cols;
-  if (whole) {
-    uint4 raw[kRows];
+  uint32_t w[kRows][4];
+  const uint8_t* from = static_cast<const uint8_t*>(a.x) + (first * a.ldx + col) * (16 / kWidth);
+  const int64_t pitch = a.ldx * (16 / kWidth);
+  if (vec_in != 0 && col + kWidth <= a.cols && first + kRows <= a.rows) {
 #pragma unroll
     for (int i = 0; i < kRows; ++i) {
-      const int64_t row = row0 + group * kRows + i;
-      raw[i] = make_uint4(0u, 0u, 0u, 0u);
-      if (row < a.rows)
-        raw[i] = __ldcs(reinterpret_cast<const uint4*>(static_cast<const uint8_t*>(a.x) +
-                                                       (row * a.ldx + col) * (kSrc == 2 ? 4 : 2)));
+      const uint4 v = __ldcs(reinterpret_cast<const uint4*>(from + i * pitch));
+      w[i][0] = v.x, w[i][1] = v.y, w[i][2] = v.z, w[i][3] = v.w;
     }
+  } else {
 #pragma unroll
     for (int i = 0; i < kRows; ++i) {
-      const uint32_t w[4] = {raw[i].x, raw[i].y, raw[i].z, raw[i].w};
+#pragma unroll
+      for (int j = 0; j < 4; ++j) w[i][j] = 0u;
+      if (first + i >= a.rows) continue;
+      const uint8_t* p = from + i * pitch;
+      if (vec_in != 0 && col + kWidth <= a.cols) {
+        const uint4 v = __ldcs(reinterpret_cast<const uint4*>(p));
+        w[i][0] = v.x, w[i][1] = v.y, w[i][2] = v.z, w[i][3] = v.w;
+        continue;
+      }
 #pragma unroll
       for (int j = 0; j < kWidth; ++j) {
+        if (col + j >= a.cols) continue;
         if constexpr (kSrc == 2) {
-          v[i][j] = __uint_as_float(w[j]);
+          w[i][j] = reinterpret_cast<const uint32_t*>(p)[j];
         } else {
-          v[i][j] = widen16<kSrc == 1>((j & 1) ? w[j >> 1] >> 16 : w[j >> 1] & 0xFFFFu);
+          w[i][j >> 1] |= static_cast<uint32_t>(reinterpret_cast<const uint16_t*>(p)[j]) << ((j & 1) * 16);
         }
       }
     }
-  } else {
-#pragma unroll
-    for (int i = 0; i < kRows; ++i) {
-      const int64_t row = row0 + group * kRows + i;
-#pragma unroll
-      for (int j = 0; j < kWidth; ++j)
-        v[i][j] = row < a.rows && col + j < a.cols ? element<kSrc>(a.x, row * a.ldx + col + j) : 0.0f;
-    }
   }
 
-  // scales: s_scale[line of q in this tile] (kTileScale: one for all, in s_scale[0])
+  // ---- the blocks' largest magnitudes and scales
+  bool odd = false;   // a block of this thread's holds infinities or NaN
   if constexpr (kTileScale) {
-    float top = 0.0f;
+    uint32_t most = 0;
 #pragma unroll
     for (int i = 0; i < kRows; ++i)
 #pragma unroll
-      for (int j = 0; j < kWidth; ++j) top = fmaxf(top, finite_magnitude(v[i][j]));
+      for (int j = 0; j < 4; ++j) most = S::larger(most, S::magnitudes(w[i][j]));
+    auto reduce = [&](uint32_t top) {
+      top = __reduce_max_sync(0xffffffffu, top);
+      if ((threadIdx.x & 31u) == 0) s_top[warp] = top;
+      __syncthreads();
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-    if ((threadIdx.x & 31u) == 0) s_max[warp][0] = top;
-    __syncthreads();
-    if (threadIdx.x == 0) {
-      for (int w = 1; w < kQuantThreads / 32; ++w) top = fmaxf(top, s_max[w][0]);
-      const float s = power_of_two(scale_exponent(top));
-      s_scale[0] = s;
-      const int64_t line = kTransposed ? tile_col : tile_row, blk = kTransposed ? tile_row : tile_col;
-      a.scale[line * a.s_line + blk * a.s_blk] = s;
+      for (int x = 0; x < kWarps; ++x) top = max(top, s_top[x]);
+      return top;
+    };
+    uint32_t top = reduce(S::largest(most));
+    odd = top > S::kLargest;   // of the whole CTA
+    if (odd) {
+      top = 0;
+#pragma unroll
+      for (int i = 0; i < kRows; ++i) top = S::largest_finite(top, w[i]);
+      __syncthreads();
+      top = reduce(top);
     }
+    const float s = power_of_two(scale_exponent(S::of_bits(top)));
+    if (threadIdx.x == 0)
+      a.scale[(kTransposed ? tile_col : tile_row) * a.s_line + (kTransposed ? tile_row : tile_col) * a.s_blk] = s;
+    if (threadIdx.x < 128) s_scale[threadIdx.x] = s;
     __syncthreads();
   } else if constexpr (!kTransposed) {
+    uint32_t top[kRows];
 #pragma unroll
     for (int i = 0; i < kRows; ++i) {
-      float top = 0.0f;
-#pragma unroll
-      for (int j = 0; j < kWidth; ++j) top = fmaxf(top, finite_magnitude(v[i][j]));
-#pragma unroll
-      for (int o = kLanes / 2; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-      if (lane == 0) s_scale[group * kRows + i] = power_of_two(scale_exponent(top));
+      const uint32_t lo = S::larger(S::magnitudes(w[i][0]), S::magnitudes(w[i][1]));
+      const uint32_t hi = S::larger(S::magnitudes(w[i][2]), S::magnitudes(w[i][3]));
+      top[i] = S::largest(S::larger(lo, hi));
     }
+    uint32_t mine = largest_of_lanes<kRows, kLanes>(top, lane);
+    odd = __any_sync(0xffffffffu, mine > S::kLargest);   // of the warp's rows
+    if (odd) {
+#pragma unroll
+      for (int i = 0; i < kRows; ++i) top[i] = S::largest_finite(0u, w[i]);
+      mine = largest_of_lanes<kRows, kLanes>(top, lane);
+    }
+    constexpr int kShare = kLanes / kRows;   // lanes that hold the same row's
+    if (lane % kShare == 0) s_scale[group * kRows + lane / kShare] = power_of_two(scale_exponent(S::of_bits(mine)));
     __syncthreads();
     const int64_t line = row0 + threadIdx.x;
-    if (threadIdx.x < 128 && line < a.rows)
-      a.scale[line * a.s_line + static_cast<int64_t>(tile_col) * a.s_blk] = s_scale[threadIdx.x];
+    if (threadIdx.x < 128 && line < a.rows) a.scale[line * a.s_line + tile_col * a.s_blk] = s_scale[threadIdx.x];
   } else {
+    auto reduce = [&](uint32_t (&most)[4]) {   // the columns' largest over the rows, then over the CTA's threads
 #pragma unroll
-    for (int j = 0; j < kWidth; ++j) {
-      float top = 0.0f;
+      for (int j = 0; j < 4; ++j) {
+        if constexpr (kLanes < 32) most[j] = S::larger(most[j], __shfl_xor_sync(0xffffffffu, most[j], kLanes));
+        if ((threadIdx.x & 31u) < static_cast<uint32_t>(kLanes)) s_max[warp][lane * 4 + j] = most[j];
+      }
+      __syncthreads();
+      uint32_t top = 0;
+      if (threadIdx.x < 128) {
+        // column x of the tile: word x * 4 / kWidth
+        const int at = static_cast<int>(threadIdx.x) * 4 / kWidth;
 #pragma unroll
-      for (int i = 0; i < kRows; ++i) top = fmaxf(top, finite_magnitude(v[i][j]));
-      if constexpr (kLanes < 32) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, kLanes));
-      if ((threadIdx.x & 31u) < static_cast<uint32_t>(kLanes)) s_max[warp][lane * kWidth + j] = top;
-    }
+        for (int x = 0; x < kWarps; ++x) top = S::larger(top, s_max[x][at]);
+        if constexpr (kSrc != 2) top = (top >> ((threadIdx.x & 1u) * 16u)) & 0xFFFFu;
+      }
+      return top;
+    };
+    uint32_t most[4] = {};
+#pragma unroll
+    for (int i = 0; i < kRows; ++i)
+#pragma unroll
+      for (int j = 0; j < 4; ++j) most[j] = S::larger(most[j], S::magnitudes(w[i][j]));
+    uint32_t top = reduce(most);
+    if (top > S::kLargest) s_odd = 1u;
     __syncthreads();
+    odd = s_odd != 0;   // of the whole CTA
+    if (odd) {
+#pragma unroll
+      for (int j = 0; j < 4; ++j) most[j] = 0u;
+#pragma unroll
+      for (int i = 0; i < kRows; ++i)
+#pragma unroll
+        for (int j = 0; j < kWidth; ++j) {
+          const uint32_t m = S::bits(w[i], j);
+          const uint32_t finite = m <= S::kLargest ? m : 0u;
+          const int word = kSrc == 2 ? j : j >> 1;
+          most[word] = S::larger(most[word], kSrc == 2 ? finite : finite << ((j & 1) * 16));
+        }
+      top = reduce(most);
+    }
     if (threadIdx.x < 128) {
-      float top = 0.0f;
-      for (int w = 0; w < kQuantThreads / 32; ++w) top = fmaxf(top, s_max[w][threadIdx.x]);
-      const float s = power_of_two(scale_exponent(top));
+      const float s = power_of_two(scale_exponent(S::of_bits(top)));
       s_scale[threadIdx.x] = s;
       const int64_t line = col0 + threadIdx.x;
-      if (line < a.cols) a.scale[line * a.s_line + static_cast<int64_t>(tile_row) * a.s_blk] = s;
+      if (line < a.cols) a.scale[line * a.s_line + tile_row * a.s_blk] = s;
     }
     __syncthreads();
   }
-  // the reciprocal of a power of two from its exponent field, exactly
-  auto inverse = [](float s) { return __uint_as_float((254u << 23) - __float_as_uint(s)); };
 
+  // ---- the quotients
   if constexpr (!kTransposed) {
 #pragma unroll
     for (int i = 0; i < kRows; ++i) {
-      const int64_t row = row0 + group * kRows + i;
-      const float inv = inverse(s_scale[kTileScale ? 0 : group * kRows + i]);
-      uint32_t w[kWidth / 4];
+      const int64_t row = first + i;
+      const float inv = inverse(s_scale[group * kRows + i]);
+      float v[kWidth];
 #pragma unroll
-      for (int j = 0; j < kWidth / 4; ++j)
-        w[j] = quantize4(v[i][4 * j], v[i][4 * j + 1], v[i][4 * j + 2], v[i][4 * j + 3], inv);
+      for (int j = 0; j < kWidth; ++j) v[j] = S::value(w[i], j) * inv;
+      if (odd) {
+#pragma unroll
+        for (int j = 0; j < kWidth; ++j) v[j] = nan_unless_finite(v[j]);
+      }
+      uint32_t out[kWidth / 4];
+#pragma unroll
+      for (int j = 0; j < kWidth / 4; ++j) out[j] = quantize4(v[4 * j], v[4 * j + 1], v[4 * j + 2], v[4 * j + 3]);
       if (row >= a.rows) continue;
       uint8_t* q = a.q + row * a.ldq + col;
       if (vec_out != 0 && col + kWidth <= a.cols) {
         if constexpr (kWidth == 8) {
-          *reinterpret_cast<uint2*>(q) = make_uint2(w[0], w[1]);
+          *reinterpret_cast<uint2*>(q) = make_uint2(out[0], out[1]);
         } else {
-          *reinterpret_cast<uint32_t*>(q) = w[0];
+          *reinterpret_cast<uint32_t*>(q) = out[0];
         }
       } else {
 #pragma unroll
         for (int j = 0; j < kWidth; ++j)
-          if (col + j < a.cols) q[j] = static_cast<uint8_t>(w[j >> 2] >> ((j & 3) * 8));
+          if (col + j < a.cols) q[j] = static_cast<uint8_t>(out[j >> 2] >> ((j & 3) * 8));
       }
     }
   } else {
@@ -296,13 +398,19 @@ __global__ void __launch_bounds__(kQuantThreads) quantize_kernel(const QuantizeA
 #pragma unroll
     for (int j = 0; j < kWidth; ++j) {
       const int c = lane * kWidth + j;
-      const float inv = inverse(s_scale[kTileScale ? 0 : c]);
+      const float inv = inverse(s_scale[c]);
 #pragma unroll
       for (int p = 0; p < kPieces; ++p) {
-        const uint32_t lo = quantize4(v[8 * p][j], v[8 * p + 1][j], v[8 * p + 2][j], v[8 * p + 3][j], inv);
-        const uint32_t hi = quantize4(v[8 * p + 4][j], v[8 * p + 5][j], v[8 * p + 6][j], v[8 * p + 7][j], inv);
+        float v[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) v[i] = S::value(w[8 * p + i], j) * inv;
+        if (odd) {
+#pragma unroll
+          for (int i = 0; i < 8; ++i) v[i] = nan_unless_finite(v[i]);
+        }
         const int piece = (group * kPieces + p) ^ (lane & 15);
-        *reinterpret_cast<uint2*>(s_tile + c * 128 + piece * 8) = make_uint2(lo, hi);
+        *reinterpret_cast<uint2*>(s_tile + c * 128 + piece * 8) =
+            make_uint2(quantize4(v[0], v[1], v[2], v[3]), quantize4(v[4], v[5], v[6], v[7]));
       }
     }
     __syncthreads();
@@ -314,14 +422,14 @@ __global__ void __launch_bounds__(kQuantThreads) quantize_kernel(const QuantizeA
       const int c = i * 16 + (static_cast<int>(threadIdx.x) >> 4);
       const int64_t line = col0 + c;
       if (line >= a.cols || along >= a.rows) continue;
-      const uint2 w = *reinterpret_cast<const uint2*>(s_tile + c * 128 + (piece ^ ((c / kWidth) & 15)) * 8);
+      const uint2 v = *reinterpret_cast<const uint2*>(s_tile + c * 128 + (piece ^ ((c / kWidth) & 15)) * 8);
       uint8_t* q = a.q + line * a.ldq + along;
       if (vec_out != 0 && along + 8 <= a.rows) {
-        *reinterpret_cast<uint2*>(q) = w;
+        *reinterpret_cast<uint2*>(q) = v;
       } else {
 #pragma unroll
         for (int j = 0; j < 8; ++j)
-          if (along + j < a.rows) q[j] = static_cast<uint8_t>((j < 4 ? w.x : w.y) >> ((j & 3) * 8));
+          if (along + j < a.rows) q[j] = static_cast<uint8_t>((j < 4 ? v.x : v.y) >> ((j & 3) * 8));
       }
     }
   }
@@ -350,13 +458,15 @@ cudaError_t launch_dependent(void (*kernel)(Args, Rest...), dim3 grid, int threa
   return cudaLaunchKernelEx(&cfg, kernel, args, rest...);
 }
 
-template <bool kBf16, bool kVec>
-cudaError_t launch_grad(const GatedGradArgs& a, dim3 grid, cudaStream_t stream) {
-  switch (a.activation) {
-    case ff::kSilu: return launch_dependent<GatedGradArgs>(ff::gated_grad_kernel<kBf16, ff::kSilu, kVec>, grid, ff::kGradThreads, stream, a);
-    case ff::kGelu: return launch_dependent<GatedGradArgs>(ff::gated_grad_kernel<kBf16, ff::kGelu, kVec>, grid, ff::kGradThreads, stream, a);
-    default: return launch_dependent<GatedGradArgs>(ff::gated_grad_kernel<kBf16, ff::kRelu, kVec>, grid, ff::kGradThreads, stream, a);
-  }
+template <bool kBf16, int kWidth>
+cudaError_t launch_grad(const GatedGradArgs& a, int num_sms, cudaStream_t stream) {
+  constexpr int64_t kPerBlock = ff::kGradThreads * ff::Piece<kWidth>::kPer;
+  const int64_t blocks = (a.m * (a.n / kWidth) + kPerBlock - 1) / kPerBlock, most = static_cast<int64_t>(num_sms) * 64;
+  const dim3 grid(static_cast<unsigned>(blocks < most ? blocks : most));
+  auto kernel = a.activation == ff::kSilu   ? ff::gated_grad_kernel<kBf16, ff::kSilu, kWidth>
+                : a.activation == ff::kGelu ? ff::gated_grad_kernel<kBf16, ff::kGelu, kWidth>
+                                            : ff::gated_grad_kernel<kBf16, ff::kRelu, kWidth>;
+  return launch_dependent<GatedGradArgs>(kernel, grid, ff::kGradThreads, stream, a);
 }
 
 template <int kSrc>
@@ -373,14 +483,15 @@ cudaError_t launch_quant(int block_rows, bool transpose, const QuantizeArgs& a, 
 }  // namespace
 
 cudaError_t launch_gated_grad(bool bf16, const GatedGradArgs& a, int num_sms, cudaStream_t stream) {
-  auto wide = [&](const void* p, int64_t ld) { return reinterpret_cast<uintptr_t>(p) % 16 == 0 && ld % 8 == 0; };
-  const bool vec = a.n % 8 == 0 && a.m * (a.n / 8) < (int64_t{1} << 31) && wide(a.grad, a.ldg) && wide(a.pre, a.ldp) && wide(a.out, a.ldo);
-  constexpr int64_t kPerBlock = ff::kGradThreads * ff::kGradPer;
-  const int64_t units = (a.m * (vec ? a.n / 8 : a.n) + kPerBlock - 1) / kPerBlock;
-  const int64_t most = static_cast<int64_t>(num_sms) * 64;
-  const dim3 grid(static_cast<unsigned>(units < most ? units : most));
-  if (bf16) return vec ? launch_grad<true, true>(a, grid, stream) : launch_grad<true, false>(a, grid, stream);
-  return vec ? launch_grad<false, true>(a, grid, stream) : launch_grad<false, false>(a, grid, stream);
+  // the widest pieces that n, the pitches and the pointers allow (and 32-bit counts)
+  auto allow = [&](int width) {
+    auto fits = [&](const void* p, int64_t ld) { return reinterpret_cast<uintptr_t>(p) % (2 * width) == 0 && ld % width == 0; };
+    return a.n % width == 0 && fits(a.grad, a.ldg) && fits(a.pre, a.ldp) && fits(a.out, a.ldo) &&
+           a.m * (a.n / width) < (int64_t{1} << 31);
+  };
+  if (allow(8)) return bf16 ? launch_grad<true, 8>(a, num_sms, stream) : launch_grad<false, 8>(a, num_sms, stream);
+  if (allow(4)) return bf16 ? launch_grad<true, 4>(a, num_sms, stream) : launch_grad<false, 4>(a, num_sms, stream);
+  return bf16 ? launch_grad<true, 1>(a, num_sms, stream) : launch_grad<false, 1>(a, num_sms, stream);
 }
 
 cudaError_t launch_pack_scales(const PackRequest (&req)[2], cudaStream_t stream) {

@@ -185,18 +185,43 @@ __device__ __forceinline__ uint64_t f32x2_mul(uint64_t a, uint64_t b) {
 // silu: g s with s = 1 / (1 + e^-g); slope s + g s (1 - s).
 // gelu: g P with P = erfc(-g / sqrt 2) / 2, the normal distribution's lower
 // tail taken directly so that it keeps its relative accuracy far below zero;
-// slope P + g e^(-g^2 / 2) / sqrt(2 pi).
+// slope P + g e^(-g^2 / 2) / sqrt(2 pi). erfc by the Chebyshev fit of Press,
+// Teukolsky, Vetterling and Flannery, Numerical Recipes, section 6.2 (erfcc):
+// erfc(z) = t e^(-z^2 + p(t)), t = 1 / (1 + z / 2), z >= 0, to 1.2e-7 of the
+// value; e^(-z^2) is the slope's too. (With CUDA's erfcf and expf the gradient of
+// 8192 x 8192 took 148 us instead of 99.)
 // relu: max(g, 0) (NaN stays NaN); slope 1 above zero, else 0.
 
 __device__ __forceinline__ float sigmoid(float g) { return __fdividef(1.0f, 1.0f + __expf(-g)); }
-__device__ __forceinline__ float normal_cdf(float g) { return 0.5f * erfcf(-0.70710678118654752f * g); }
+// P(g), and e^(-g^2 / 2) in `e`.
+__device__ __forceinline__ float normal_cdf(float g, float& e) {
+  // -g^2 / 2 in base 2 with what its roundings leave out
+  constexpr float kC = -0.72134752044448170f;   // -log2(e) / 2
+  const float sq = g * g, sq_low = fmaf(g, g, -sq);
+  const float x = kC * sq, x_low = fmaf(kC, sq, -x) + kC * sq_low;
+  e = ex2_approx(x);
+  if (sq < 1e4f) e = fmaf(e, x_low * 0.69314718055994531f, e);   // (past it e is zero)
+  const float t = __fdividef(1.0f, fmaf(0.35355339059327376f, fabsf(g), 1.0f));   // z / 2 = |g| / (2 sqrt 2)
+  float p = fmaf(t, 0.17087277f, -0.82215223f);
+  p = fmaf(t, p, 1.48851587f);
+  p = fmaf(t, p, -1.13520398f);
+  p = fmaf(t, p, 0.27886807f);
+  p = fmaf(t, p, -0.18628806f);
+  p = fmaf(t, p, 0.09678418f);
+  p = fmaf(t, p, 0.37409196f);
+  p = fmaf(t, p, 1.00002368f);
+  p = fmaf(t, p, -1.26551223f);
+  const float lower = 0.5f * t * e * ex2_approx(p * 1.44269504088896341f);   // P(-|g|)
+  return g < 0.0f ? lower : 1.0f - lower;
+}
 
 template <int kAct>
 __device__ __forceinline__ float act(float g) {
   if constexpr (kAct == kSilu) {
     return g * sigmoid(g);
   } else if constexpr (kAct == kGelu) {
-    return g * normal_cdf(g);
+    float e;
+    return g * normal_cdf(g, e);
   } else {
     return g < 0.0f ? 0.0f : g;
   }
@@ -209,8 +234,9 @@ __device__ __forceinline__ float2 act_slope(float g) {
     const float s = sigmoid(g);
     return make_float2(g * s, s * fmaf(g, 1.0f - s, 1.0f));
   } else if constexpr (kAct == kGelu) {
-    const float p = normal_cdf(g);
-    return make_float2(g * p, fmaf(g * 0.39894228040143268f, __expf(-0.5f * g * g), p));
+    float e;
+    const float p = normal_cdf(g, e);
+    return make_float2(g * p, fmaf(g * 0.39894228040143268f, e, p));
   } else {
     return make_float2(g < 0.0f ? 0.0f : g, g > 0.0f ? 1.0f : 0.0f);
   }
