@@ -99,9 +99,7 @@ bool scales_addressable(const float* p, int64_t rows, int64_t cols, int64_t s_i,
 constexpr double kTileTime[4][kNumFfTiles] = {
     {1.0, 0.71, 0.84}, {1.0, 0.60, 0.70}, {1.0, 0.56, 0.57}, {1.0, 0.48, 0.475}};
 
-// Rows of A up to which the skinny kernel runs whatever the number of tiles, and
-// up to which it can run.
-constexpr int64_t kFew = 32, kMostFew = 128;
+constexpr int64_t kMostFew = 128;   // rows of A that the skinny kernel can take
 
 struct Choice {
   int rows = 0, splits = 0;   // skinny (rows != 0)
@@ -109,15 +107,24 @@ struct Choice {
   int grid = 0;
 };
 
-int pairs_of(int sms) {
+// Clusters that run at once on the current device: of skinny CTAs by log2 of their number, and pairs of whole tiles.
+struct Resident {
+  bool known = false;
+  int splits[4] = {}, pairs = 0;
+};
+Resident resident_on(int sms) {
   static std::mutex mutex;
-  static int known[64] = {};
+  static Resident devices[64];
   int dev = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess) return 0;
+  if (cudaGetDevice(&dev) != cudaSuccess) return Resident{};
   std::lock_guard<std::mutex> lock(mutex);
-  int& pairs = known[dev & 63];
-  if (pairs == 0) pairs = ff_resident_pairs(sms);
-  return pairs;
+  Resident& r = devices[dev & 63];
+  if (!r.known) {
+    for (int i = 0; i < 4; ++i) r.splits[i] = ff_resident_clusters(1 << i, sms);
+    r.pairs = ff_resident_pairs(sms);
+    r.known = r.pairs > 0;
+  }
+  return r;
 }
 
 // GEMM_TN_FF_KERNEL (pair256, pair128, single128, skinny1, skinny2, skinny4 or
@@ -132,7 +139,8 @@ Forced forced() {
   const char* names[kNumFfTiles] = {"pair256", "pair128", "single128"};
   for (int t = 0; t < kNumFfTiles; ++t)
     if (std::strcmp(s, names[t]) == 0) f.tile = t;
-  if (std::strncmp(s, "skinny", 6) == 0) f.splits = std::atoi(s + 6);
+  for (int splits = 1; splits <= 8; splits *= 2)
+    if (std::strncmp(s, "skinny", 6) == 0 && std::atoi(s + 6) == splits) f.splits = splits;
   return f;
 }
 
@@ -140,23 +148,26 @@ Forced forced() {
 int choose(int kind, FfArgs& a, int sms, Choice* to) {
   const int64_t out_n = kind == kFfGated ? 2 : 1;   // columns of the product for one of C
   const Forced force = forced();
-  const bool force_skinny = a.m <= kMostFew && a.num_k_blocks >= force.splits &&
-                            (force.splits == 1 || force.splits == 2 || force.splits == 4 || force.splits == 8);
-  if (kind != kFfNt && (force_skinny || (force.tile < 0 && a.m <= kFew))) {
-    to->rows = a.m <= 16 ? 16 : a.m <= 32 ? 32 : a.m <= 64 ? 64 : 128;
+  const Resident at_once = resident_on(sms);
+  if (kind != kFfNt && a.m <= kMostFew && force.tile < 0) {
     const int64_t tiles = (static_cast<int64_t>(a.n) * out_n + 127) / 128;
+    // K is cut while all clusters run at once and every CTA has a few blocks of K
     int splits = 1;
-    // two CTAs run on an SM; each should have a few blocks of K
-    while (splits < 8 && tiles * splits * 2 < 3 * sms && a.num_k_blocks >= splits * 2 * 4) splits *= 2;
-    if (force_skinny) splits = force.splits;
-    if (tiles * splits > INT32_MAX) return api_fail(GEMM_TN_ERR_INVALID_VALUE, "too many output tiles");
-    to->splits = splits;
-    to->grid = static_cast<int>(tiles * splits);
-    a.num_m_tiles = 1;
-    a.num_n_tiles = a.num_tiles = static_cast<int32_t>(tiles);
-    return GEMM_TN_OK;
+    for (int i = 1; i < 4; ++i)
+      if (tiles <= at_once.splits[i] && a.num_k_blocks >= 4 << i) splits = 1 << i;
+    if (force.splits > 0 && a.num_k_blocks >= force.splits) splits = force.splits;
+    const int rows = a.m <= 16 ? 16 : a.m <= 32 ? 32 : a.m <= 64 ? 64 : 128;
+    if (ff_skinny_has(kind, rows, splits)) {
+      if (tiles * splits > INT32_MAX) return api_fail(GEMM_TN_ERR_INVALID_VALUE, "too many output tiles");
+      to->rows = rows;
+      to->splits = splits == 1 && tiles > sms ? 0 : splits;   // 0: two CTAs to an SM
+      to->grid = static_cast<int>(tiles * splits);
+      a.num_m_tiles = 1;
+      a.num_n_tiles = a.num_tiles = static_cast<int32_t>(tiles);
+      return GEMM_TN_OK;
+    }
   }
-  const int pairs = pairs_of(sms);
+  const int pairs = at_once.pairs;
   if (pairs <= 0) return api_fail(GEMM_TN_ERR_CUDA, "kernel cannot be resident on this device (occupancy query)");
   // the shape with the least time: waves times the time of one of its tiles
   const double* tile_time = kTileTime[kind];

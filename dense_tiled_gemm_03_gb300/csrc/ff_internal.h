@@ -76,7 +76,16 @@ cudaError_t launch_ff_e4m3(int tile, bool b_rows, const gemm_tn_dev::FfArgs& arg
 // a tile takes an SM's shared memory whole.
 int ff_resident_pairs(int sms);
 
-// Few rows of A: `rows` (16, 32, 64 or 128) of them against 128 rows of B a CTA, K split over clusters of `splits`.
+// Clusters of `splits` CTAs with an SM each that run at once on the current device (0 on error).
+int ff_resident_clusters(int splits, int sms);
+// Few rows of A: `rows` (16, 32, 64 or 128) of them against 128 rows of B a CTA, K split over clusters of `splits`
+// CTAs with an SM each (0: whole, two CTAs to an SM).
+// With more rows it pays only where K is cut: beside whole tiles, e4m3 products of
+// 64 rows with 8192 x 8192 took 20.7 and 18.3 us uncut or cut in two, with 1024 x
+// 8192 cut in eight 11.7 and 17.8.
+constexpr bool ff_skinny_has(int kind, int rows, int splits) {
+  return rows <= 32 || (rows <= 64 && splits > 1) || (kind == kFfGated && splits == 8);
+}
 cudaError_t launch_ff_skinny(int kind, bool bf16, int rows, int splits, const gemm_tn_dev::FfArgs& args, int grid,
                              cudaStream_t stream);
 

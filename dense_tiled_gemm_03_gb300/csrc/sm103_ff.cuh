@@ -181,6 +181,18 @@ __device__ __forceinline__ uint64_t f32x2_mul(uint64_t a, uint64_t b) {
   return d;
 }
 
+// ------------------------------------------------------------------ asynchronous copies of single values
+
+__device__ __forceinline__ void cp_async_4(void* to_shared, const void* from) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" :: "r"(smem_addr(to_shared)), "l"(from) : "memory");
+}
+__device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+// Waits until all but the newest N groups of this thread have landed.
+template <int N>
+__device__ __forceinline__ void cp_async_wait() {
+  asm volatile("cp.async.wait_group %0;" :: "n"(N) : "memory");
+}
+
 // ------------------------------------------------------------------ activations
 // silu: g s with s = 1 / (1 + e^-g); slope s + g s (1 - s).
 // gelu: g P with P = erfc(-g / sqrt 2) / 2, the normal distribution's lower

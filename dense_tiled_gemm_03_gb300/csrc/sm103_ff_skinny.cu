@@ -8,9 +8,10 @@
 // cluster of S CTAs, whose fp32 partials are added in CTA order through
 // distributed shared memory.
 //
-// A CTA takes half of an SM's shared memory, so that one's last loads and its
-// join overlap another's stream; S is the least that gives the device two CTAs
-// an SM (ff_api.cu).
+// S is the most for which all clusters run at once (ff_api.cu), a CTA to an SM:
+// what a CTA streams is bound by its loads in flight, so it takes all of the SM's
+// shared memory. With more tiles than SMs two CTAs share one, and the last
+// loads and the join of one overlap the other's stream.
 #include <atomic>
 
 #include "sm103_ff.cuh"
@@ -21,24 +22,29 @@ namespace skinny {
 
 constexpr int kThreads = 192;   // warp 0 loads, warp 1 multiplies, warps 2 to 5 are the epilogue
 constexpr uint32_t kStageB = 128 * 128;
-constexpr uint32_t kRingBudget = 100 * 1024;
 
-// kN: rows of A (MMA N); kGatedForm: gated 16-bit, else e4m3 with block scales.
-template <int kN_, int kSplits_, bool kGatedForm_, bool kBf16_>
+// kN: rows of A (MMA N); kGatedForm: gated 16-bit, else e4m3 with block scales;
+// kPerSm: CTAs that share an SM.
+template <int kN_, int kSplits_, int kPerSm_, bool kGatedForm_, bool kBf16_>
 struct Cfg {
+  static constexpr int kPerSm = kPerSm_;
+  static constexpr uint32_t kRingBudget = kPerSm == 2 ? 100 * 1024 : 200 * 1024;
   static constexpr int kN = kN_, kSplits = kSplits_;
   static constexpr bool kGatedForm = kGatedForm_, kBf16 = kBf16_, kScaled = !kGatedForm_;
   static constexpr int kBlockK = kScaled ? 128 : 64;
   static constexpr uint32_t kStageA = kN * 128;
   static constexpr int kStages = static_cast<int>(kRingBudget / (kStageB + kStageA));
-  static constexpr int kBuffers = kScaled ? 2 : 1;
+  static constexpr int kBuffers = kScaled ? 4 / kPerSm : 1;   // (of 512 columns to an SM)
   static constexpr uint32_t kTmemCols = kBuffers * kN < 32 ? 32 : kBuffers * kN;
   static constexpr int kPartStride = kN + 4;   // floats between the partial's rows (columns of C)
   static constexpr uint32_t kOffB = 0;
   static constexpr uint32_t kOffA = kOffB + kStages * kStageB;
   static constexpr uint32_t kRingEnd = kOffA + kStages * kStageA;
-  static constexpr uint32_t kOffScale = kRingEnd;   // e4m3: [4 warps][2][kN] scales of A's rows
-  static constexpr uint32_t kOffBar = kOffScale + (kScaled ? 4 * 2 * kN * 4 : 0);
+  // e4m3: each epilogue warp's ring of scales, of kAhead blocks: A's rows', then its own rows of B
+  static constexpr int kAhead = 8;
+  static constexpr int kScaleFloats = kN + 32;
+  static constexpr uint32_t kOffScale = kRingEnd;
+  static constexpr uint32_t kOffBar = kOffScale + (kScaled ? 4 * kAhead * kScaleFloats * 4 : 0);
   static constexpr int kNumBars = 2 * kStages + 2 * kBuffers + 1;
   static constexpr uint32_t kOffTmemSlot = kOffBar + kNumBars * 8;
   static constexpr uint32_t kOffAbort = kOffTmemSlot + 4;
@@ -48,17 +54,12 @@ struct Cfg {
   static_assert(kN == 16 || kN == 32 || kN == 64 || kN == 128, "rows of A");
   static_assert(kStageA % 1024 == 0, "swizzle atoms stay 1024-aligned");
   static_assert(128 * kPartStride * 4 <= kRingEnd, "the partial fits in the idle ring");
-  static_assert(2 * (kSmemBytes + 1024) <= 228 * 1024, "two CTAs to an SM");
+  static_assert(kStages <= 32, "issued phases fit a 32-bit mask");
+  static_assert(kPerSm * (kSmemBytes + 1024) <= 228 * 1024, "kPerSm CTAs to an SM");
 };
 
-__device__ __forceinline__ float ld_cluster_f32(uint32_t addr) {
-  float v;
-  asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(addr));
-  return v;
-}
-
 template <class C>
-__global__ void __launch_bounds__(kThreads, 2) ff_skinny_kernel(const __grid_constant__ FfArgs args) {
+__global__ void __launch_bounds__(kThreads, C::kPerSm) ff_skinny_kernel(const __grid_constant__ FfArgs args) {
   constexpr int S = C::kSplits;
   extern __shared__ uint8_t smem_raw[];
   const uint32_t raw = smem_addr(smem_raw);
@@ -178,33 +179,35 @@ __global__ void __launch_bounds__(kThreads, 2) ff_skinny_kernel(const __grid_con
     bool ok = true;
     if constexpr (C::kScaled) {
       const int col = tn * 128 + static_cast<int>(row);   // of C
-      const float* sb = args.b_scale + static_cast<int64_t>(min(col, args.n - 1) / (args.b_block_rows)) * args.bs_row;
-      float* vec = reinterpret_cast<float*>(smem + C::kOffScale) + quarter * (2 * C::kN);
-      constexpr int kPer = (C::kN + 31) / 32;
-      // the scales of a block are loaded a block ahead
-      float a_next[kPer], b_next = 0.0f;
-      auto load = [&](int kb) {
-        b_next = __ldg(sb + kb * args.bs_blk);
+      const float* sb = args.b_scale + static_cast<int64_t>(min(col, args.n - 1) / args.b_block_rows) * args.bs_row;
+      float* ring = reinterpret_cast<float*>(smem + C::kOffScale) + quarter * (C::kAhead * C::kScaleFloats);
+      // the scales' copies run kAhead - 1 blocks ahead: a block lasts less than a load
+      auto fetch = [&](int kb) {
+        if (kb < kb1) {
+          float* to = ring + (kb & (C::kAhead - 1)) * C::kScaleFloats;
 #pragma unroll
-        for (int i = 0; i < kPer; ++i)
-          a_next[i] = __ldg(args.a_scale + static_cast<int64_t>(min(i * 32 + static_cast<int>(lane), args.m - 1)) *
-                                               args.as_row + kb * args.as_blk);
+          for (int i = 0; i < C::kN; i += 32)
+            if (C::kN >= 32 || lane < static_cast<uint32_t>(C::kN))
+              cp_async_4(to + i + lane, args.a_scale + static_cast<int64_t>(min(i + static_cast<int>(lane), args.m - 1)) *
+                                                           args.as_row + kb * args.as_blk);
+          cp_async_4(to + C::kN + lane, sb + kb * args.bs_blk);
+        }
+        cp_async_commit();
       };
       uint64_t sum[C::kN / 2];
 #pragma unroll
       for (int j = 0; j < C::kN / 2; ++j) sum[j] = 0;
-      if (kb0 < kb1) load(kb0);
+      for (int i = 0; i < C::kAhead - 1; ++i) fetch(kb0 + i);
       int buf = 0;
       uint32_t buf_phase = 0;
       for (int kb = kb0; kb < kb1; ++kb) {
-        float* now = vec + (kb & 1) * C::kN;
-#pragma unroll
-        for (int i = 0; i < kPer; ++i)
-          if (C::kN >= 32 || lane < static_cast<uint32_t>(C::kN)) now[i * 32 + lane] = a_next[i];
+        __syncwarp();   // the slot's last readers are done with it
+        fetch(kb + C::kAhead - 1);
+        cp_async_wait<C::kAhead - 1>();
         __syncwarp();
-        const uint64_t b2 = f32x2_pack(b_next, b_next);
-        if (kb + 1 < kb1) load(kb + 1);
-        if (!__all_sync(0xffffffffu, wd.wait(sum_full(buf), buf_phase))) {
+        const float* now = ring + (kb & (C::kAhead - 1)) * C::kScaleFloats;
+        const uint64_t b2 = f32x2_pack(now[C::kN + lane], now[C::kN + lane]);
+        if (!wd.warp_wait(sum_full(buf), buf_phase)) {
           ok = false;
           break;
         }
@@ -220,10 +223,12 @@ __global__ void __launch_bounds__(kThreads, 2) ff_skinny_kernel(const __grid_con
             if (lane == 0) mbar_arrive(sum_empty(buf));
           }
 #pragma unroll
-          for (int j = 0; j < 8; ++j) {
-            const uint64_t a2 = *reinterpret_cast<const uint64_t*>(now + c * 16 + 2 * j);
-            const uint64_t p = f32x2_pack(__uint_as_float(v[2 * j]), __uint_as_float(v[2 * j + 1]));
-            sum[c * 8 + j] = f32x2_fma(f32x2_mul(p, a2), b2, sum[c * 8 + j]);
+          for (int j = 0; j < 8; j += 2) {
+            const ulonglong2 a2 = *reinterpret_cast<const ulonglong2*>(now + c * 16 + 2 * j);
+            const uint64_t p0 = f32x2_pack(__uint_as_float(v[2 * j]), __uint_as_float(v[2 * j + 1]));
+            const uint64_t p1 = f32x2_pack(__uint_as_float(v[2 * j + 2]), __uint_as_float(v[2 * j + 3]));
+            sum[c * 8 + j] = f32x2_fma(f32x2_mul(p0, a2.x), b2, sum[c * 8 + j]);
+            sum[c * 8 + j + 1] = f32x2_fma(f32x2_mul(p1, a2.y), b2, sum[c * 8 + j + 1]);
           }
         }
         if (++buf == C::kBuffers) {
@@ -272,46 +277,64 @@ __global__ void __launch_bounds__(kThreads, 2) ff_skinny_kernel(const __grid_con
   {
     constexpr int kCols = C::kOutN / S;   // columns of C that this CTA finishes
     const int c0 = static_cast<int>(rank) * kCols;
-    auto total = [&](int r, int i) {
-      const uint32_t off = base + static_cast<uint32_t>(r * C::kPartStride + i) * 4u;
-      float v[S];
+    auto total = [&](int r, int i) {      // of row r of the partials, rows i to i + 3 of A
+      const uint32_t off = static_cast<uint32_t>(r * C::kPartStride + i) * 4u;
+      float4 v[S];
 #pragma unroll
       for (int s = 0; s < S; ++s) {
         if constexpr (S > 1) {
-          v[s] = ld_cluster_f32(map_to_cta(off, static_cast<uint32_t>(s)));
+          v[s] = ld_cluster_f4(map_to_cta(base + off, static_cast<uint32_t>(s)));
         } else {
-          v[s] = *reinterpret_cast<const float*>(smem + (off - base));
+          v[s] = *reinterpret_cast<const float4*>(smem + off);
         }
       }
-      float t = v[0];
 #pragma unroll
-      for (int s = 1; s < S; ++s) t += v[s];
-      return t;
+      for (int s = 1; s < S; ++s) {
+        v[0].x += v[s].x;
+        v[0].y += v[s].y;
+        v[0].z += v[s].z;
+        v[0].w += v[s].w;
+      }
+      return v[0];
     };
     const int rows = min(args.m, C::kN);
-    for (int x = threadIdx.x; x < kCols * rows; x += kThreads) {   // consecutive threads: consecutive columns of C
-      const int r = c0 + x % kCols, i = x / kCols;
+    // consecutive threads: consecutive columns of C, four rows each
+    for (int x = threadIdx.x; x < kCols * ((rows + 3) / 4); x += kThreads) {
+      const int r = c0 + x % kCols, i0 = x / kCols * 4;
       const int col = tn * C::kOutN + r;
       if (col >= args.n) continue;
-      const int64_t at = static_cast<int64_t>(i) * args.ldc + col;
+      const float4 t = total(r, i0);
+      const float v[4] = {t.x, t.y, t.z, t.w};
       if constexpr (C::kGatedForm) {
-        const float g = total(r, i), u = total(r + 64, i);
-        const float h = (args.activation == kSilu ? act<kSilu>(g) : args.activation == kGelu ? act<kGelu>(g)
-                                                                                             : act<kRelu>(g)) * u;
-        static_cast<uint16_t*>(args.c)[at] = static_cast<uint16_t>(pack16<C::kBf16>(h, 0.0f));
-        if (args.pre != nullptr) {
-          uint16_t* pre = static_cast<uint16_t*>(args.pre) + static_cast<int64_t>(i) * args.ldp + col;
-          pre[0] = static_cast<uint16_t>(pack16<C::kBf16>(g, 0.0f));
-          pre[args.n] = static_cast<uint16_t>(pack16<C::kBf16>(u, 0.0f));
+        const float4 t2 = total(r + 64, i0);
+        const float u[4] = {t2.x, t2.y, t2.z, t2.w};
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          if (i0 + j >= rows) continue;
+          const float g = v[j];
+          const float h = (args.activation == kSilu ? act<kSilu>(g) : args.activation == kGelu ? act<kGelu>(g)
+                                                                                               : act<kRelu>(g)) * u[j];
+          static_cast<uint16_t*>(args.c)[static_cast<int64_t>(i0 + j) * args.ldc + col] =
+              static_cast<uint16_t>(pack16<C::kBf16>(h, 0.0f));
+          if (args.pre != nullptr) {
+            uint16_t* pre = static_cast<uint16_t*>(args.pre) + static_cast<int64_t>(i0 + j) * args.ldp + col;
+            const uint32_t both = pack16<C::kBf16>(g, u[j]);
+            pre[0] = static_cast<uint16_t>(both);
+            pre[args.n] = static_cast<uint16_t>(both >> 16);
+          }
         }
       } else {
-        const float v = total(r, i);
-        if (args.out_kind == kOutF32) {
-          float* c = static_cast<float*>(args.c) + at;
-          *c = args.accumulate ? *c + v : v;
-        } else {
-          static_cast<uint16_t*>(args.c)[at] = static_cast<uint16_t>(
-              args.out_kind == kOutBf16 ? pack16<true>(v, 0.0f) : pack16<false>(v, 0.0f));
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          if (i0 + j >= rows) continue;
+          const int64_t at = static_cast<int64_t>(i0 + j) * args.ldc + col;
+          if (args.out_kind == kOutF32) {
+            float* c = static_cast<float*>(args.c) + at;
+            *c = args.accumulate ? *c + v[j] : v[j];
+          } else {
+            static_cast<uint16_t*>(args.c)[at] = static_cast<uint16_t>(
+                args.out_kind == kOutBf16 ? pack16<true>(v[j], 0.0f) : pack16<false>(v[j], 0.0f));
+          }
         }
       }
     }
@@ -333,7 +356,7 @@ namespace {
 using namespace gemm_tn_dev::ff::skinny;
 
 template <class C>
-cudaError_t launch_one(const gemm_tn_dev::FfArgs& args, int grid, cudaStream_t stream) {
+cudaError_t fill(cudaLaunchConfig_t& cfg, cudaLaunchAttribute* attr, int grid, cudaStream_t stream) {
   static std::atomic<uint64_t> done_mask{0};
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
@@ -345,12 +368,11 @@ cudaError_t launch_one(const gemm_tn_dev::FfArgs& args, int grid, cudaStream_t s
     if (e != cudaSuccess) return e;
     done_mask.fetch_or(bit, std::memory_order_acq_rel);
   }
-  cudaLaunchConfig_t cfg{};
+  cfg = cudaLaunchConfig_t{};
   cfg.gridDim = dim3(static_cast<unsigned>(grid));
   cfg.blockDim = dim3(kThreads);
   cfg.dynamicSmemBytes = C::kSmemBytes;
   cfg.stream = stream;
-  cudaLaunchAttribute attr[2];
   cfg.attrs = attr;
   if (C::kSplits > 1) {
     attr[cfg.numAttrs].id = cudaLaunchAttributeClusterDimension;
@@ -358,6 +380,15 @@ cudaError_t launch_one(const gemm_tn_dev::FfArgs& args, int grid, cudaStream_t s
     attr[cfg.numAttrs].val.clusterDim.y = 1;
     attr[cfg.numAttrs++].val.clusterDim.z = 1;
   }
+  return cudaSuccess;
+}
+
+template <class C>
+cudaError_t launch_one(const gemm_tn_dev::FfArgs& args, int grid, cudaStream_t stream) {
+  cudaLaunchConfig_t cfg;
+  cudaLaunchAttribute attr[2];
+  const cudaError_t e = fill<C>(cfg, attr, grid, stream);
+  if (e != cudaSuccess) return e;
   if (dependent_launch_enabled()) {
     attr[cfg.numAttrs].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[cfg.numAttrs++].val.programmaticStreamSerializationAllowed = 1;
@@ -365,15 +396,35 @@ cudaError_t launch_one(const gemm_tn_dev::FfArgs& args, int grid, cudaStream_t s
   return cudaLaunchKernelEx(&cfg, ff_skinny_kernel<C>, args);
 }
 
+template <int kSplits>
+int resident(int sms) {
+  using C = Cfg<16, kSplits, 1, true, true>;
+  cudaLaunchConfig_t cfg;
+  cudaLaunchAttribute attr[2];
+  int clusters = 0;
+  if (fill<C>(cfg, attr, sms - sms % kSplits, nullptr) != cudaSuccess ||
+      cudaOccupancyMaxActiveClusters(&clusters, ff_skinny_kernel<C>, &cfg) != cudaSuccess) {
+    cudaGetLastError();
+    return 0;
+  }
+  return clusters;
+}
+
+// What ff_api.cu asks for (ff_skinny_has).
 template <int kN, bool kGatedForm, bool kBf16>
 cudaError_t launch_splits(int splits, const gemm_tn_dev::FfArgs& args, int grid, cudaStream_t stream) {
-  switch (splits) {
-    case 1: return launch_one<Cfg<kN, 1, kGatedForm, kBf16>>(args, grid, stream);
-    case 2: return launch_one<Cfg<kN, 2, kGatedForm, kBf16>>(args, grid, stream);
-    case 4: return launch_one<Cfg<kN, 4, kGatedForm, kBf16>>(args, grid, stream);
-    case 8: return launch_one<Cfg<kN, 8, kGatedForm, kBf16>>(args, grid, stream);
-    default: return cudaErrorInvalidValue;
+  if constexpr (kN <= 32) {
+    if (splits == 0) return launch_one<Cfg<kN, 1, 2, kGatedForm, kBf16>>(args, grid, stream);
+    if (splits == 1) return launch_one<Cfg<kN, 1, 1, kGatedForm, kBf16>>(args, grid, stream);
   }
+  if constexpr (kN <= 64) {
+    if (splits == 2) return launch_one<Cfg<kN, 2, 1, kGatedForm, kBf16>>(args, grid, stream);
+    if (splits == 4) return launch_one<Cfg<kN, 4, 1, kGatedForm, kBf16>>(args, grid, stream);
+  }
+  if constexpr (kN <= 64 || kGatedForm) {
+    if (splits == 8) return launch_one<Cfg<kN, 8, 1, kGatedForm, kBf16>>(args, grid, stream);
+  }
+  return cudaErrorInvalidValue;
 }
 
 template <bool kGatedForm, bool kBf16>
@@ -388,6 +439,10 @@ cudaError_t launch_rows(int rows, int splits, const gemm_tn_dev::FfArgs& args, i
 }
 
 }  // namespace
+
+int ff_resident_clusters(int splits, int sms) {
+  return splits == 2 ? resident<2>(sms) : splits == 4 ? resident<4>(sms) : splits == 8 ? resident<8>(sms) : sms;
+}
 
 cudaError_t launch_ff_skinny(int kind, bool bf16, int rows, int splits, const gemm_tn_dev::FfArgs& args, int grid,
                              cudaStream_t stream) {
