@@ -58,26 +58,18 @@ from ._native import (  # noqa: F401
 )
 from . import _cache
 from ._cache import tree_mask  # noqa: F401
-from ._feed_forward import (  # noqa: F401
-    GEMM_TN_ACT_SILU,
-    GEMM_TN_ELEM_BF16,
-    GEMM_TN_ELEM_F16,
-    GEMM_TN_ELEM_F32,
-    gated_grad,
-    mm_nt,
-    mm_tn_e4m3,
-    mm_tn_gated,
-    quantize_e4m3,
-)
+from . import _ff
+from ._ff import GEMM_TN_ACT_SILU, GEMM_TN_ELEM_BF16, GEMM_TN_ELEM_F16, GEMM_TN_ELEM_F32  # noqa: F401
 
 
 def __getattr__(name):
-    """The paged cache's names, which load its extension module at their first use."""
-    if name not in _cache.BOUND:
-        raise AttributeError(f"module {__name__!r} has no attribute {name!r}")
-    globals().update({n: getattr(_cache, n) for n in _cache.BOUND})
-    return globals()[name]
+    """The paged cache's and the feed-forward operators' names, which load their extension modules at their first use."""
+    for part in (_cache, _ff):
+        if name in part.BOUND:
+            globals().update({n: getattr(part, n) for n in part.BOUND})
+            return globals()[name]
+    raise AttributeError(f"module {__name__!r} has no attribute {name!r}")
 
 
 def __dir__():
-    return sorted({*globals(), *_cache.BOUND})
+    return sorted({*globals(), *_cache.BOUND, *_ff.BOUND})

@@ -157,7 +157,7 @@ int choose(int kind, FfArgs& a, int sms, Choice* to) {
       if (tiles <= at_once.splits[i] && a.num_k_blocks >= 4 << i) splits = 1 << i;
     if (force.splits > 0 && a.num_k_blocks >= force.splits) splits = force.splits;
     const int rows = a.m <= 16 ? 16 : a.m <= 32 ? 32 : a.m <= 64 ? 64 : 128;
-    if (ff_skinny_has(kind, rows, splits)) {
+    if (ff_skinny_has(kind, rows, splits) && (force.splits > 0 || ff_skinny_pays(rows, a.num_k_blocks))) {
       if (tiles * splits > INT32_MAX) return api_fail(GEMM_TN_ERR_INVALID_VALUE, "too many output tiles");
       to->rows = rows;
       to->splits = splits == 1 && tiles > sms ? 0 : splits;   // 0: two CTAs to an SM

@@ -80,12 +80,14 @@ int ff_resident_pairs(int sms);
 int ff_resident_clusters(int splits, int sms);
 // Few rows of A: `rows` (16, 32, 64 or 128) of them against 128 rows of B a CTA, K split over clusters of `splits`
 // CTAs with an SM each (0: whole, two CTAs to an SM).
-// With more rows it pays only where K is cut: beside whole tiles, e4m3 products of
-// 64 rows with 8192 x 8192 took 20.7 and 18.3 us uncut or cut in two, with 1024 x
-// 8192 cut in eight 11.7 and 17.8.
+// Up to 32 rows it runs whatever K; more pay where a long K is cut. Beside whole
+// tiles, us: e4m3, 64 rows, 4096 x 8192 11.7 and 18.2, x 1024 6.3 and 5.0; 128
+// rows, 4096 x 8192 17.0 and 18.4 cut in four, 8192 x 8192 23.4 and 18.6 cut in
+// two; gated, 128 rows, 4096 x 4096 14.9 and 17.8, x 1024 9.1 and 7.5.
 constexpr bool ff_skinny_has(int kind, int rows, int splits) {
-  return rows <= 32 || (rows <= 64 && splits > 1) || (kind == kFfGated && splits == 8);
+  return rows <= 32 || splits >= (rows == 128 && kind != kFfGated ? 4 : 2);
 }
+constexpr bool ff_skinny_pays(int rows, int64_t k_blocks) { return rows <= 32 || k_blocks >= rows / 4; }
 cudaError_t launch_ff_skinny(int kind, bool bf16, int rows, int splits, const gemm_tn_dev::FfArgs& args, int grid,
                              cudaStream_t stream);
 

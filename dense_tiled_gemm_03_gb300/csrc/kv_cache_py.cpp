@@ -21,80 +21,19 @@
 #include <c10/cuda/CUDAGuard.h>
 #include <c10/cuda/CUDAStream.h>
 #include <torch/csrc/Exceptions.h>
-#include <torch/csrc/autograd/python_variable.h>
-
-#include <cstring>
-#include <string>
 
 #include "kv_cache.h"
+#include "py_args.h"
 
 namespace {
 
-using at::Tensor;
+using namespace py_args;
 
 decltype(&tree_attn_fwd) g_attn = nullptr;
 decltype(&kv_cache_append) g_append = nullptr;
 decltype(&kv_cache_weigh) g_weigh = nullptr;
 decltype(&kv_cache_evict) g_evict = nullptr;
 PyObject* g_error = nullptr;   // GemmTnError(status, where)
-
-// ---------------------------------------------------------------- arguments
-
-// Places positional and keyword arguments (a vectorcall's) in `out`, None as
-// nullptr; the first `required` must be there.
-template <int kCount>
-bool place(const char* fn, const char* const (&names)[kCount], int required, PyObject* const* args, Py_ssize_t positional,
-           PyObject* kwnames, PyObject* (&out)[kCount]) {
-  for (PyObject*& o : out) o = nullptr;
-  if (positional > kCount) {
-    PyErr_Format(PyExc_TypeError, "%s() takes at most %d arguments (%zd given)", fn, kCount, positional);
-    return false;
-  }
-  bool given[kCount] = {};
-  for (Py_ssize_t i = 0; i < positional; ++i) {
-    given[i] = true;
-    out[i] = args[i] == Py_None ? nullptr : args[i];
-  }
-  const Py_ssize_t keywords = kwnames != nullptr ? PyTuple_GET_SIZE(kwnames) : 0;
-  for (Py_ssize_t x = 0; x < keywords; ++x) {
-    Py_ssize_t size = 0;
-    const char* name = PyUnicode_AsUTF8AndSize(PyTuple_GET_ITEM(kwnames, x), &size);
-    if (name == nullptr) return false;
-    int i = 0;
-    while (i < kCount && std::strcmp(names[i], name) != 0) ++i;
-    if (i == kCount) {
-      PyErr_Format(PyExc_TypeError, "%s() got an unexpected keyword argument '%s'", fn, name);
-      return false;
-    }
-    if (given[i]) {
-      PyErr_Format(PyExc_TypeError, "%s() got multiple values for argument '%s'", fn, name);
-      return false;
-    }
-    given[i] = true;
-    PyObject* value = args[positional + x];
-    out[i] = value == Py_None ? nullptr : value;
-  }
-  for (int i = 0; i < required; ++i)
-    if (!given[i]) {
-      PyErr_Format(PyExc_TypeError, "%s() missing required argument '%s'", fn, names[i]);
-      return false;
-    }
-  return true;
-}
-
-const Tensor* tensor(PyObject* o, const char* what) {
-  if (o != nullptr && THPVariable_Check(o)) return &THPVariable_Unpack(o);
-  PyErr_Format(PyExc_TypeError, "%s must be a tensor", what);
-  return nullptr;
-}
-
-int64_t cuda_index(const Tensor& t) { return t.is_cuda() ? t.get_device() : -1; }
-
-std::string shape_text(at::IntArrayRef shape) {
-  std::string s = "(";
-  for (size_t i = 0; i < shape.size(); ++i) s += (i > 0 ? ", " : "") + std::to_string(shape[i]);
-  return s + (shape.size() == 1 ? ",)" : ")");
-}
 
 // ---------------------------------------------------------------- KVCache
 
@@ -115,17 +54,6 @@ struct Cache {
   PyObject* dtype;
   Description made;   // as it was made; its pointers are not used again
 };
-
-// Whether the tensor's storage holds it (it may have been made smaller, or been freed).
-bool stored(const Tensor& t, const char* what) {
-  if (t.numel() == 0) return true;
-  int64_t extent = 1;
-  for (int64_t i = 0; i < t.dim(); ++i) extent += (t.size(i) - 1) * t.stride(i);
-  const uint64_t bytes = static_cast<uint64_t>(t.storage_offset() + extent) * t.element_size();
-  if (t.storage().nbytes() >= bytes) return true;
-  PyErr_Format(PyExc_ValueError, "the storage of %s is smaller than the tensor", what);
-  return false;
-}
 
 // The pointer of a contiguous tensor of 32-bit numbers of that shape, nullptr for no tensor; false with an exception set.
 bool numbers(PyObject* o, at::ScalarType type, int64_t index, const char* what, at::IntArrayRef shape, void** to) {
@@ -641,11 +569,6 @@ PyObject* bind(PyObject*, PyObject* const* args, Py_ssize_t nargs) {
   Py_RETURN_NONE;
 }
 
-template <class F>
-PyCFunction as_function(F f) {
-  return reinterpret_cast<PyCFunction>(reinterpret_cast<void*>(f));
-}
-
 PyMethodDef functions[] = {
     {"bind", as_function(bind), METH_FASTCALL, nullptr},
     {"tree_attn", as_function(tree_attn), METH_FASTCALL | METH_KEYWORDS,
@@ -703,7 +626,7 @@ PyMODINIT_FUNC PyInit__kv_cache() {
     return nullptr;
   }
   // the torch whose headers this was compiled with
-  if (PyModule_AddStringConstant(m, "built_against", KV_CACHE_TORCH) < 0) {
+  if (PyModule_AddStringConstant(m, "built_against", BUILT_AGAINST_TORCH) < 0) {
     Py_DECREF(m);
     return nullptr;
   }

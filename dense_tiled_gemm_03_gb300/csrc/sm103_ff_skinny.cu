@@ -417,13 +417,11 @@ cudaError_t launch_splits(int splits, const gemm_tn_dev::FfArgs& args, int grid,
     if (splits == 0) return launch_one<Cfg<kN, 1, 2, kGatedForm, kBf16>>(args, grid, stream);
     if (splits == 1) return launch_one<Cfg<kN, 1, 1, kGatedForm, kBf16>>(args, grid, stream);
   }
-  if constexpr (kN <= 64) {
-    if (splits == 2) return launch_one<Cfg<kN, 2, 1, kGatedForm, kBf16>>(args, grid, stream);
-    if (splits == 4) return launch_one<Cfg<kN, 4, 1, kGatedForm, kBf16>>(args, grid, stream);
-  }
   if constexpr (kN <= 64 || kGatedForm) {
-    if (splits == 8) return launch_one<Cfg<kN, 8, 1, kGatedForm, kBf16>>(args, grid, stream);
+    if (splits == 2) return launch_one<Cfg<kN, 2, 1, kGatedForm, kBf16>>(args, grid, stream);
   }
+  if (splits == 4) return launch_one<Cfg<kN, 4, 1, kGatedForm, kBf16>>(args, grid, stream);
+  if (splits == 8) return launch_one<Cfg<kN, 8, 1, kGatedForm, kBf16>>(args, grid, stream);
   return cudaErrorInvalidValue;
 }
 
