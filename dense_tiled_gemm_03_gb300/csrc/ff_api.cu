@@ -95,9 +95,9 @@ bool scales_addressable(const float* p, int64_t rows, int64_t cols, int64_t s_i,
 // Time of a tile of each shape, relative to the first's, where tiles abound
 // (smaller tiles read more from L2 for their work). Measured, us: gated 8192 x
 // 16384 x 4096 1061, 1512 and 1790; nt 16384 x 4096 x 8192 638, 771 and 900;
-// e4m3 8192^3 397, 446 and 450, with a scale for every row of B 588, 567 and 559.
+// e4m3 8192^3 383, 438 and 443, with a scale for every row of B 536, 580 and 560.
 constexpr double kTileTime[4][kNumFfTiles] = {
-    {1.0, 0.71, 0.84}, {1.0, 0.60, 0.70}, {1.0, 0.56, 0.57}, {1.0, 0.48, 0.475}};
+    {1.0, 0.71, 0.84}, {1.0, 0.60, 0.70}, {1.0, 0.57, 0.58}, {1.0, 0.54, 0.52}};
 
 constexpr int64_t kMostFew = 128;   // rows of A that the skinny kernel can take
 
@@ -200,6 +200,9 @@ struct Padded {
   explicit Padded(cudaStream_t s) : stream(s) {}
   int copy(const void** a, int64_t* lda, int64_t a_rows, int64_t a_cols, const void** b, int64_t* ldb, int64_t b_rows,
            int64_t b_cols, int sms) {
+    // (one row's pitch is never stepped over)
+    if (a_rows == 1) *lda = (a_cols + 7) / 8 * 8;
+    if (b_rows == 1) *ldb = (b_cols + 7) / 8 * 8;
     const bool pad_a = !addressable(*a, *lda), pad_b = !addressable(*b, *ldb);
     if (!pad_a && !pad_b) return GEMM_TN_OK;
     const int64_t la = (a_cols + 7) / 8 * 8, lb = (b_cols + 7) / 8 * 8;

@@ -336,35 +336,37 @@ __global__ void __launch_bounds__(kThreads, 1) ff_gemm_kernel(const __grid_const
           }
           tc_fence_after_sync();
           const uint32_t t = t_mine + static_cast<uint32_t>(buf * T::kBlockN);
+          uint32_t v[2][16];
+          tmem_load_32x16(t, v[0]);
           // (the block has been multiplied, so its scales have landed too)
           const float* scales = reinterpret_cast<const float*>(smem + T::kOffScale + static_cast<uint32_t>(slot) * T::kScaleStride);
           const float* cols = scales + T::kBlockM + half * kCols;
           if (++slot == T::kScaleSlots) slot = 0;
-          uint64_t scale2 = 0;
+          float scale = scales[quarter * 32u + lane];
+          if constexpr (T::kForm == kE4m3) scale *= scales[T::kBlockM + (half * kCols / 128) * 4 + (kb & 3)];
+          const uint64_t scale2 = f32x2_pack(scale, scale);
 #pragma unroll
           for (int c = 0; c < kCols / 16; ++c) {
-            uint32_t v[16];
-            tmem_load_32x16(t + 16u * c, v);
-            if (c == 0) {
-              float scale = scales[quarter * 32u + lane];
-              if constexpr (T::kForm == kE4m3) scale *= scales[T::kBlockM + (half * kCols / 128) * 4 + (kb & 3)];
-              scale2 = f32x2_pack(scale, scale);
-            }
-            tmem_loaded(v);
-            if (c == kCols / 16 - 1) hand_back();
+            uint64_t both[8];   // the columns' scales times the row's, while tensor memory answers
+            if constexpr (T::kForm == kE4m3Rows) {
 #pragma unroll
-            for (int j = 0; j < 8; j += 2) {
-              const uint64_t p0 = f32x2_pack(__uint_as_float(v[2 * j]), __uint_as_float(v[2 * j + 1]));
-              const uint64_t p1 = f32x2_pack(__uint_as_float(v[2 * j + 2]), __uint_as_float(v[2 * j + 3]));
-              uint64_t &s0 = sum[c * 8 + j], &s1 = sum[c * 8 + j + 1];
-              if constexpr (T::kForm == kE4m3) {
-                s0 = f32x2_fma(p0, scale2, s0);
-                s1 = f32x2_fma(p1, scale2, s1);
-              } else {
+              for (int j = 0; j < 8; j += 2) {
                 const ulonglong2 b = *reinterpret_cast<const ulonglong2*>(cols + c * 16 + 2 * j);
-                s0 = f32x2_fma(f32x2_mul(p0, scale2), b.x, s0);
-                s1 = f32x2_fma(f32x2_mul(p1, scale2), b.y, s1);
+                both[j] = f32x2_mul(b.x, scale2);
+                both[j + 1] = f32x2_mul(b.y, scale2);
               }
+            }
+            uint32_t(&x)[16] = v[c & 1];
+            tmem_loaded(x);
+            if (c + 1 < kCols / 16) {
+              tmem_load_32x16(t + 16u * (c + 1), v[(c + 1) & 1]);
+            } else {
+              hand_back();
+            }
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+              const uint64_t p = f32x2_pack(__uint_as_float(x[2 * j]), __uint_as_float(x[2 * j + 1]));
+              sum[c * 8 + j] = f32x2_fma(p, T::kForm == kE4m3 ? scale2 : both[j], sum[c * 8 + j]);
             }
           }
         }

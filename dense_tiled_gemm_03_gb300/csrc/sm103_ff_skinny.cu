@@ -236,6 +236,7 @@ __global__ void __launch_bounds__(kThreads, C::kPerSm) ff_skinny_kernel(const __
           buf_phase ^= 1u;
         }
       }
+      cp_async_wait<0>();
       // the ring is idle once the last block has been multiplied
       asm volatile("bar.sync 1, 128;" ::: "memory");
       if (ok) {

@@ -24,7 +24,7 @@ def oracle_lib():
 
 #: files whose tests hand the C ABI made-up addresses, some of them in calls that are
 #: valid but for the device: where a GPU is visible a kernel would follow them
-MADE_UP_ADDRESSES = ("test_abi_cpu.py", "test_kv_cache_cpu.py")
+MADE_UP_ADDRESSES = ("test_abi_cpu.py", "test_kv_cache_cpu.py", "test_feed_forward_cpu.py")
 
 
 def pytest_collection_modifyitems(items):

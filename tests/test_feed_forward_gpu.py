@@ -365,3 +365,310 @@ def test_e4m3_empty():
     assert bool((onto == 2).all())
     assert gt.mm_tn_e4m3(e(0, 16), f(0, 1), e(6, 16), f(6, 1)).shape == (0, 6)
     assert gt.mm_tn_e4m3(e(3, 16), f(3, 1), e(0, 16), f(0, 1)).shape == (3, 0)
+
+
+# ---------------------------------------------------------------- together, as they are used
+
+def rounded(x, dtype):
+    return x.to(dtype).double()
+
+
+@pytest.mark.parametrize("act", ["silu", "gelu"])
+@pytest.mark.parametrize("dtype", ["fp16", "bf16"])
+@pytest.mark.parametrize("tokens", [5, 200])
+def test_a_block_and_its_gradients(tokens, dtype, act):
+    """A feed-forward block, forward and backward: y = h Wd^T with h = act(x Wg^T) * (x Wu^T); from dy the gradients of
+    x and of all three weights. Every step is checked against 64 bits from the step's own inputs."""
+    gen = torch.Generator().manual_seed(tokens)
+    dt, k, n = DTYPES[dtype], 192, 328
+    x, w = normal(gen, tokens, k, dtype=dt).cuda(), normal(gen, 2 * n, k, scale=k ** -0.5, dtype=dt).cuda()
+    wd, dy = normal(gen, k, n, scale=n ** -0.5, dtype=dt).cuda(), normal(gen, tokens, k, dtype=dt).cuda()
+    pre = torch.empty((tokens, 2 * n), dtype=dt, device="cuda")
+    h = gt.mm_tn_gated(x, w, pre=pre, activation=act)
+    y = gt.mm_tn(h, wd)
+    dwd = gt.mm_nt(dy, h, out_dtype=torch.float32)          # [k, n], like wd
+    dh = gt.mm_nn(dy, wd)
+    d = gt.gated_grad(dh, pre, activation=act)
+    dx = gt.mm_nn(d, w)
+    dw = torch.zeros((2 * n, k), device="cuda")
+    for _ in range(2):
+        gt.mm_nt(d, x, out=dw, accumulate=True)             # two micro-batches' gradients, here the same
+    c = lambda t: t.cpu()
+    hr, ho, pr, po = ref.gated(c(x), c(w), act, dt)
+    ref.assert_close(h, hr, ho, "h")
+    ref.assert_close(pre, pr, po, "pre")
+    ref.assert_close(d, *ref.gated_grad(c(dh), c(pre), act), "d")
+    ref.assert_close(dwd, *ref.mm_nt(c(dy), c(h), torch.float32), "dwd")
+    once, off = ref.mm_nt(c(d), c(x), torch.float32)
+    ref.assert_close(dw, 2 * once, 2 * off + 2 * ref.ULP * (2 * once).abs(), "dw")
+    # the whole chain against 64 bits without any rounding between: each of the
+    # few roundings to 16 bits on the way is half a step of its value, and the
+    # products behind it carry it as a sum of signed terms, bounded by their magnitudes
+    eps = torch.finfo(dt).eps / 2
+    X, W, WD, DY = (c(t).double() for t in (x, w, wd, dy))
+    G, U = (X @ W.T).chunk(2, 1)
+    a, s = G * ref.share(G, act), ref.slope(G, act)
+    DH = DY @ WD
+    D = torch.cat([DH * U * s, DH * a], 1)
+    # d: dh's rounding, g's and u's (the slope's own slope is below 1.1) and d's own, and fp32 products' far smaller errors
+    size_h = DY.abs() @ WD.abs()
+    Doff = eps * (4 * D.abs() + torch.cat([1.2 * (DH * U * G).abs(), 1.2 * (DH * G).abs()], 1)) + \
+        400 * ref.ULP * torch.cat([size_h * (U * s).abs() + 2 * DH.abs() * (X.abs() @ W.abs().T).chunk(2, 1)[1] * 1.2
+                                   + 2 * DH.abs() * U.abs() * (X.abs() @ W.abs().T).chunk(2, 1)[0] * 1.2,
+                                   size_h * a.abs() + 2 * DH.abs() * (X.abs() @ W.abs().T).chunk(2, 1)[0] * 1.2], 1) + \
+        8 * ref.SMALLEST[dt]
+    DX = D @ W
+    ref.assert_close(dx, DX, Doff @ W.abs() + 700 * ref.ULP * (D.abs() @ W.abs()) + 2 * eps * DX.abs() + ref.SMALLEST[dt], "dx")
+    Y = (a * U) @ WD.T
+    Hoff = eps * 3 * (a * U).abs() + 200 * ref.ULP * 1.2 * ((X.abs() @ W.abs().T).chunk(2, 1)[0] * U.abs()
+                                                         + a.abs() * (X.abs() @ W.abs().T).chunk(2, 1)[1]) + ref.SMALLEST[dt]
+    ref.assert_close(y, Y, Hoff @ WD.abs().T + 400 * ref.ULP * ((a * U).abs() @ WD.abs().T) + 2 * eps * Y.abs() + ref.SMALLEST[dt], "y")
+
+
+@pytest.mark.parametrize("tokens", [3, 130, 300])
+def test_a_linear_layer_in_8_bits(tokens):
+    """y = x W^T with both quantised, and from dy the gradients: dx = dy W from the transposed weights, dW = dy^T x
+    summed over tokens, both sides quantised along them and added to an fp32 gradient."""
+    gen = torch.Generator().manual_seed(tokens)
+    k, n = 272, 400
+    x, w = normal(gen, tokens, k, dtype=torch.bfloat16).cuda(), normal(gen, n, k, scale=k ** -0.5).cuda()
+    dy = normal(gen, tokens, n, scale=1e-3, dtype=torch.bfloat16).cuda()
+
+    def both(t, rows=1, transpose=False):
+        q, s = gt.quantize_e4m3(t, block_rows=rows, transpose=transpose)
+        want_q, want_s = ref.quantized(t.cpu(), rows, transpose)
+        assert torch.equal(q.float().double().cpu(), want_q) and torch.equal(s.double().cpu(), want_s)
+        return q, s
+
+    def check(got, a, b, b_rows, dtype, onto=None):
+        ref.assert_close(got, *ref.mm_e4m3(a[0].float().cpu(), a[1].cpu(), b[0].float().cpu(), b[1].cpu(), b_rows, dtype, onto))
+
+    xq, wq, wt, dyq = both(x), both(w, 128), both(w, 128, True), both(dy)
+    check(gt.mm_tn_e4m3(*xq, *wq), xq, wq, 128, torch.bfloat16)
+    check(gt.mm_tn_e4m3(*dyq, *wt, out_dtype=torch.float16), dyq, wt, 128, torch.float16)
+    xt, dyt = both(x, 1, True), both(dy, 1, True)
+    grad = normal(gen, n, k, scale=1e-2)
+    out = grad.cuda()
+    assert gt.mm_tn_e4m3(*dyt, *xt, out=out, accumulate=True) is out
+    check(out, dyt, xt, 1, torch.float32, grad)
+    # how far 8 bits are from none: half a step of either side, as relative 2^-4 and
+    # for values below 2^-6 of their scale 2^-10 of it
+    Y = x.cpu().double() @ w.cpu().double().T
+    y = gt.mm_tn_e4m3(*xq, *wq, out_dtype=torch.float32).cpu().double()
+
+    def step(t, s, rows):
+        return t.abs() * 2.0 ** -4 + ref.spread(s.cpu(), rows, t.shape) * 2.0 ** -10
+
+    X, W = x.cpu().double(), w.cpu().double()
+    ex, ew = step(X, xq[1], 1), step(W, wq[1], 128)
+    off = ex @ W.abs().T + X.abs() @ ew.T + ex @ ew.T + 200 * ref.ULP * (X.abs() @ W.abs().T)
+    assert bool(((y - Y).abs() <= off).all())
+
+
+# ---------------------------------------------------------------- streams, captures, repeats, far offsets
+
+def calls(gen):
+    """One call of every operator and kind of kernel, some through workspaces: (name, call, outputs)."""
+    bf, out = torch.bfloat16, []
+    for m, odd in ((20, False), (300, False), (300, True), (20, True)):
+        k = 131 if odd else 136
+        a, b = normal(gen, m, k, dtype=bf).cuda(), normal(gen, 2 * 70, k, dtype=bf).cuda()
+        h, pre = torch.zeros((m, 70), dtype=bf, device="cuda"), torch.zeros((m, 140), dtype=bf, device="cuda")
+        out.append((lambda a=a, b=b, h=h, pre=pre: gt.mm_tn_gated(a, b, out=h, pre=pre), [h, pre]))
+        d, dh = torch.zeros((m, 140), dtype=bf, device="cuda"), normal(gen, m, 70, dtype=bf).cuda()
+        p = normal(gen, m, 140, dtype=bf).cuda()
+        out.append((lambda dh=dh, p=p, d=d: gt.gated_grad(dh, p, out=d), [d]))
+        c = torch.zeros((140, k), device="cuda")
+        out.append((lambda p=p, a=a, c=c: gt.mm_nt(p, a, out=c), [c]))
+        x = normal(gen, m, k).cuda()
+        for rows, transpose in ((1, False), (128, True)):
+            q, s = gt.quantize_e4m3(x, rows, transpose)
+            q.zero_()
+            s.zero_()
+            out.append((lambda x=x, r=rows, t=transpose, q=q, s=s: gt.quantize_e4m3(x, r, t, out=q, scale=s), [q, s]))
+        (qa, sa), (qb, sb) = gt.quantize_e4m3(x), gt.quantize_e4m3(normal(gen, 200, k).cuda())
+        if odd:
+            sa, sb = sa.contiguous(), sb.contiguous()      # strides that whole tiles copy first
+        y = torch.zeros((m, 200), dtype=torch.float16, device="cuda")
+        out.append((lambda qa=qa, sa=sa, qb=qb, sb=sb, y=y: gt.mm_tn_e4m3(qa, sa, qb, sb, out=y), [y]))
+    return out
+
+
+def bits(tensors):
+    return [t.clone().contiguous().view(torch.uint8).clone() for t in tensors]
+
+
+def test_repeats_streams_and_captures():
+    """The same bits again, on other streams at once, and from captures replayed in turn and over one another."""
+    work = calls(torch.Generator().manual_seed(17))
+    want = []
+    for call, outs in work:
+        call()
+        want.append(bits(outs))
+    torch.cuda.synchronize()
+
+    def check(what):
+        torch.cuda.synchronize()
+        for i, (_, outs) in enumerate(work):
+            for got, w in zip(bits(outs), want[i]):
+                assert torch.equal(got, w), (what, i)
+            for t in outs:
+                t.view(torch.uint8).zero_() if t.is_contiguous() else t.zero_()
+        torch.cuda.synchronize()
+
+    check("first")
+    for call, _ in work:
+        call()
+        call()
+    check("again")
+    streams = [torch.cuda.Stream() for _ in range(4)]
+    for s in streams:
+        s.wait_stream(torch.cuda.current_stream())
+    for i, (call, _) in enumerate(work):
+        with torch.cuda.stream(streams[i % 4]):
+            for _ in range(3):
+                call()
+    check("streams")
+    graphs = []
+    for part in range(2):
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g, stream=streams[part]):
+            for call, _ in work[part::2]:
+                call()
+        graphs.append(g)
+    check_zero = [bool((t.float() == 0).all()) for _, outs in work for t in outs]
+    assert all(check_zero), "a capture ran"
+    for _ in range(2):
+        for g, s in zip(graphs, streams):
+            with torch.cuda.stream(s):
+                g.replay()
+    check("replayed")
+
+
+def test_far_offsets():
+    """Rows more than 2^31 elements apart: offsets past 32 bits in outputs and inputs."""
+    pitch = (1 << 31) + 64
+    gen = torch.Generator().manual_seed(23)
+    bf = torch.bfloat16
+    whole = torch.empty((2 * pitch + 512,), dtype=bf, device="cuda")
+    far = whole.as_strided((3, 256), (pitch, 1))
+    a, b = normal(gen, 3, 64, dtype=bf), normal(gen, 512, 64, dtype=bf)
+    h, off, _, _ = ref.gated(a, b, "silu", bf)
+    for which in ("skinny1", "pair128"):
+        far.zero_()
+        with kernel(which):
+            gt.mm_tn_gated(a.cuda(), b.cuda(), out=far)
+        ref.assert_close(far, h, off, which)
+    # far rows as an operand: three tokens of a gradient's sum, and of a quantised matrix
+    x = normal(gen, 3, 40, dtype=bf)
+    ref.assert_close(gt.mm_nt(far, x.cuda(), out_dtype=torch.float32), *ref.mm_nt(far.cpu().contiguous(), x, torch.float32))
+    check_quantized_equal(far)
+    pre = whole.as_strided((3, 512), (pitch, 1))
+    pre.copy_(normal(gen, 3, 512, dtype=bf))
+    dh = normal(gen, 3, 256, dtype=bf)
+    d, off = ref.gated_grad(dh, pre.cpu(), "silu")
+    ref.assert_close(gt.gated_grad(dh.cuda(), pre, out=pre), d, off)
+    bytes8 = whole.view(torch.uint8).view(torch.float8_e4m3fn)
+    q8 = bytes8.as_strided((3, 256), (pitch, 1))           # (the third row past 2^32 bytes)
+    xq = normal(gen, 3, 256)
+    _, s = gt.quantize_e4m3(xq.cuda(), out=q8)
+    want_q, want_s = ref.quantized(xq, 1, False)
+    assert torch.equal(q8.float().double().cpu(), want_q) and torch.equal(s.double().cpu(), want_s)
+    bq, bs = gt.quantize_e4m3(normal(gen, 100, 256).cuda())
+    ref.assert_close(gt.mm_tn_e4m3(q8, s, bq, bs, out_dtype=torch.float32),
+                     *ref.mm_e4m3(q8.float().cpu(), s.cpu(), bq.float().cpu(), bs.cpu(), 1, torch.float32))
+
+
+def check_quantized_equal(x):
+    q, scale = gt.quantize_e4m3(x)
+    want_q, want_s = ref.quantized(x.cpu(), 1, False)
+    assert torch.equal(q.float().double().cpu(), want_q) and torch.equal(scale.double().cpu(), want_s)
+
+
+def test_the_watchdog():
+    """A load that never comes: the wait runs out, the status says so, and the next call is whole."""
+    import time
+    gen = torch.Generator().manual_seed(29)
+    bf = torch.bfloat16
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    runs = []
+    for which in TILES + ["skinny1", "skinny4"]:
+        m = 20 if which.startswith("skinny") else 300
+        a, b = normal(gen, m, 1024, dtype=bf).cuda(), normal(gen, 400, 1024, dtype=bf).cuda()
+        x = normal(gen, m, 1024).cuda()
+        q, qs = gt.quantize_e4m3(x)
+        w, ws = gt.quantize_e4m3(normal(gen, 300, 1024).cuda())
+        w2, ws2 = gt.quantize_e4m3(normal(gen, 300, 1024).cuda(), 128)
+        runs += [(which, lambda a=a, b=b: gt.mm_tn_gated(a, b, status=status)),
+                 (which, lambda q=q, qs=qs, w=w, ws=ws: gt.mm_tn_e4m3(q, qs, w, ws, status=status)),
+                 (which, lambda q=q, qs=qs, w=w2, ws=ws2: gt.mm_tn_e4m3(q, qs, w, ws, status=status))]
+        if which in TILES:
+            runs.append((which, lambda a=a: gt.mm_nt(a, a, status=status)))
+    for which, call in runs:
+        with kernel(which):
+            before = call().float().clone()
+            assert int(status.item()) == 0
+            t0 = time.perf_counter()
+            with env_var("GEMM_TN_WATCHDOG_MS", "100"), env_var("GEMM_TN_TEST_DROP_LOAD", "0"):
+                call()
+                torch.cuda.synchronize()
+            assert int(status.item()) == gt.GEMM_TN_ERR_TIMEOUT and time.perf_counter() - t0 < 5.0, which
+            status.zero_()
+            assert torch.equal(call().float(), before) and int(status.item()) == 0, which
+
+
+# ---------------------------------------------------------------- refusals
+
+def test_refusals():
+    bf, f8 = torch.bfloat16, torch.float8_e4m3fn
+    z = lambda *s, d=bf: torch.zeros(s, dtype=d, device="cuda")
+    a, b, x = z(4, 64), z(16, 64), z(6, 32, d=torch.float32)
+    q, s = gt.quantize_e4m3(z(6, 256))
+    w, ws = gt.quantize_e4m3(z(10, 256), 128)
+    shared = z(4, 80)
+    refused = [
+        (lambda: gt.mm_tn_gated(a, z(15, 64)), ValueError, "2N"), (lambda: gt.mm_tn_gated(a, z(16, 63)), ValueError, "2N"),
+        (lambda: gt.mm_tn_gated(a, z(16, 64, d=torch.float16)), TypeError, "same dtype"),
+        (lambda: gt.mm_tn_gated(a.float(), b.float()), TypeError, "unsupported dtype"),
+        (lambda: gt.mm_tn_gated(a.cpu(), b), ValueError, "CUDA"), (lambda: gt.mm_tn_gated(a, b.cpu()), ValueError, "CUDA"),
+        (lambda: gt.mm_tn_gated(a[0], b), ValueError, "2-D"), (lambda: gt.mm_tn_gated(z(64, 4).t(), b), ValueError, "unit stride"),
+        (lambda: gt.mm_tn_gated(a, b, out=z(4, 9)), ValueError, "out must be"),
+        (lambda: gt.mm_tn_gated(a, b, out=z(4, 8, d=torch.float32)), TypeError, "out must be"),
+        (lambda: gt.mm_tn_gated(a, b, pre=z(4, 8)), ValueError, "pre must be"),
+        (lambda: gt.mm_tn_gated(a, b, activation="none"), ValueError, "activation"),
+        (lambda: gt.mm_tn_gated(a, b, activation=3), ValueError, "activation"),
+        (lambda: gt.mm_tn_gated(a, b, status=z(1)), ValueError, "status"),
+        (lambda: gt.mm_tn_gated(shared[:, :64], b, out=shared[:, 56:64]), gt.GemmTnError, "overlaps"),
+        (lambda: gt.mm_tn_gated(a, b, out=shared[:, :8], pre=shared[:, 4:20]), gt.GemmTnError, "overlaps"),
+        (lambda: gt.mm_tn_gated(a, b, out=z(1, 8).expand(4, 8)), gt.GemmTnError, "ldh"),
+        (lambda: gt.gated_grad(z(4, 8), z(4, 15)), ValueError, "pre must be"),
+        (lambda: gt.gated_grad(z(4, 8), z(4, 16, d=torch.float16)), TypeError, "pre must be"),
+        (lambda: gt.gated_grad(x, z(6, 64, d=torch.float32)), TypeError, "unsupported dtype"),
+        (lambda: gt.gated_grad(shared[:, :8], shared[:, 8:24], out=shared[:, 7:23]), gt.GemmTnError, "overlaps"),
+        (lambda: gt.gated_grad(z(4, 8), shared[:, 8:24], out=shared[:, 9:25]), gt.GemmTnError, "overlaps"),
+        (lambda: gt.mm_nt(a, z(5, 8)), ValueError, "rows"), (lambda: gt.mm_nt(a, a, out_dtype=torch.float16), TypeError, "output dtype"),
+        (lambda: gt.mm_nt(a, a, out_dtype="float32"), TypeError, "torch.dtype"),
+        (lambda: gt.mm_nt(a, a, accumulate=True), ValueError, "accumulate"),
+        (lambda: gt.mm_nt(a, a, out=z(64, 64), accumulate=True), ValueError, "accumulate"),
+        (lambda: gt.quantize_e4m3(x, block_rows=64), ValueError, "block_rows"),
+        (lambda: gt.quantize_e4m3(x.double()), TypeError, "unsupported dtype"),
+        (lambda: gt.quantize_e4m3(x, out=z(6, 31, d=f8)), ValueError, "out must be"),
+        (lambda: gt.quantize_e4m3(x, out=z(6, 32)), TypeError, "out must be"),
+        (lambda: gt.quantize_e4m3(x, scale=z(6, 2, d=torch.float32)), ValueError, "scale must be"),
+        (lambda: gt.quantize_e4m3(z(6, 300, d=torch.float32), scale=z(1, 3, d=torch.float32).expand(6, 3)), gt.GemmTnError, "apart"),
+        (lambda: gt.mm_tn_e4m3(z(6, 256), s, w, ws), TypeError, "e4m3"), (lambda: gt.mm_tn_e4m3(q, s.to(bf), w, ws), TypeError, "float32"),
+        (lambda: gt.mm_tn_e4m3(q, s[:, :1], w, ws), ValueError, "a_scale"), (lambda: gt.mm_tn_e4m3(q, s, w, s), ValueError, "b_scale"),
+        (lambda: gt.mm_tn_e4m3(q, s, w[:, :128], ws[:, :1]), ValueError, "inner"),
+        (lambda: gt.mm_tn_e4m3(q, s, w, ws, out_dtype=f8), TypeError, "output dtype"),
+        (lambda: gt.mm_tn_e4m3(q, s, w, ws, accumulate=True), ValueError, "accumulate"),
+        (lambda: gt.mm_tn_e4m3(q[:, 1:129], s[:, :1], w[:, :128], ws[:, :1]), gt.GemmTnError, "16-byte"),
+        (lambda: gt.mm_tn_e4m3(z(6, 250, d=f8), s, z(10, 250, d=f8), ws), gt.GemmTnError, "16-byte"),
+    ]
+    for i, (call, kind, what) in enumerate(refused):
+        with pytest.raises(kind, match=what):
+            call()
+            raise AssertionError(f"call {i} was taken")
+    freed = z(4, 64)
+    freed.untyped_storage().resize_(0)
+    with pytest.raises(ValueError, match="storage"):
+        gt.mm_tn_gated(freed, b)
