@@ -199,7 +199,7 @@ struct Padded {
   cudaStream_t stream;
   explicit Padded(cudaStream_t s) : stream(s) {}
   int copy(const void** a, int64_t* lda, int64_t a_rows, int64_t a_cols, const void** b, int64_t* ldb, int64_t b_rows,
-           int64_t b_cols, int sms) {
+           int64_t b_cols) {
     // (one row's pitch is never stepped over)
     if (a_rows == 1) *lda = (a_cols + 7) / 8 * 8;
     if (b_rows == 1) *ldb = (b_cols + 7) / 8 * 8;
@@ -216,8 +216,8 @@ struct Padded {
     uint8_t* w = static_cast<uint8_t*>(workspace);
     const RepackRequest req[2] = {{*a, *lda, w, la, pad_a ? a_rows : 0, a_cols},
                                   {*b, *ldb, w + a_bytes, lb, pad_b ? b_rows : 0, b_cols}};
-    e = api_counted(launch_repack2(req, 2, sms, stream));
-    if (e != cudaSuccess) return api_fail_cuda(e, "repack launch");
+    e = api_counted(launch_pad_rows(req, stream));
+    if (e != cudaSuccess) return api_fail_cuda(e, "padding launch");
     if (pad_a) {
       *a = w;
       *lda = la;
@@ -298,7 +298,7 @@ int gemm_tn_gated(int dtype, int64_t m, int64_t n, int64_t k, const void* a, int
   st = choose(kFfGated, args, sms, &pick);
   if (st != GEMM_TN_OK) return st;
   Padded padded(stream);
-  st = padded.copy(&a, &lda, m, k, &b, &ldb, 2 * n, k, sms);
+  st = padded.copy(&a, &lda, m, k, &b, &ldb, 2 * n, k);
   if (st != GEMM_TN_OK) return st;
   st = encode16(&args.tmap_a, bf16, a, m, k, lda, pick.rows ? pick.rows : 128);
   if (st == GEMM_TN_OK) st = encode16(&args.tmap_b, bf16, b, 2 * n, k, ldb, pick.rows ? 64 : kFfTiles[pick.tile].block_n / 2);
@@ -371,7 +371,7 @@ int gemm_nt(int dtype, int64_t m, int64_t n, int64_t k, const void* a, int64_t l
   st = choose(kFfNt, args, sms, &pick);
   if (st != GEMM_TN_OK) return st;
   Padded padded(stream);
-  st = padded.copy(&a, &lda, k, m, &b, &ldb, k, n, sms);
+  st = padded.copy(&a, &lda, k, m, &b, &ldb, k, n);
   if (st == GEMM_TN_OK) st = encode16(&args.tmap_a, bf16, a, k, m, lda, 64);
   if (st == GEMM_TN_OK) st = encode16(&args.tmap_b, bf16, b, k, n, ldb, 64);
   if (st != GEMM_TN_OK) return st;

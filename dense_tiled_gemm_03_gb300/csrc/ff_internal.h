@@ -91,6 +91,10 @@ constexpr bool ff_skinny_pays(int rows, int64_t k_blocks) { return rows <= 32 ||
 cudaError_t launch_ff_skinny(int kind, bool bf16, int rows, int splits, const gemm_tn_dev::FfArgs& args, int grid,
                              cudaStream_t stream);
 
+// launch_repack2's copies of 16-bit rows, made by pieces through all rows (a
+// block to a row leaves most of it idle where rows are short).
+cudaError_t launch_pad_rows(const RepackRequest (&req)[2], cudaStream_t stream);
+
 // dst[i * pitch + j] = src[i * s_i + j * s_j] for i < rows, j < cols; up to two at once (rows 0: none).
 struct PackRequest {
   const float* src;

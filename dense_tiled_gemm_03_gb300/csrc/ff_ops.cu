@@ -87,6 +87,66 @@ __global__ void __launch_bounds__(kGradThreads) gated_grad_kernel(const GatedGra
   }
 }
 
+// ------------------------------------------------------------------ rows laid out for the TMA
+// A copy of 16-bit rows at any even address in rows of whole 16 bytes. A thread
+// makes kPadPer 16-byte pieces of the copies, counted through all rows, each from
+// the one or two aligned pieces of the source that hold it.
+struct PadArgs {
+  gemm_tn_impl::RepackRequest req[2];   // (rows 0: none)
+  uint32_t blocks0;                     // of the first
+};
+constexpr int kPadThreads = 256, kPadPer = 4;
+
+__global__ void __launch_bounds__(kPadThreads) pad_rows_kernel(const PadArgs a) {
+  griddep_wait();
+  griddep_launch_dependents();
+  const bool second = blockIdx.x >= a.blocks0;
+  const gemm_tn_impl::RepackRequest& q = second ? a.req[1] : a.req[0];
+  const uint32_t pieces = static_cast<uint32_t>(q.ld_dst / 8);
+  const int64_t total = q.rows * pieces;
+  const int64_t first = static_cast<int64_t>(blockIdx.x - (second ? a.blocks0 : 0u)) * (kPadThreads * kPadPer) + threadIdx.x;
+  uint4 lo[kPadPer], hi[kPadPer];
+  uint32_t shift[kPadPer];
+  int valid[kPadPer];   // elements of the piece inside the row
+#pragma unroll
+  for (int i = 0; i < kPadPer; ++i) {
+    const int64_t at = first + i * kPadThreads;
+    valid[i] = 0;
+    if (at >= total) continue;
+    // (rows and pieces of a row stay below 2^30)
+    const int64_t row = total < (int64_t{1} << 32) ? static_cast<int64_t>(static_cast<uint32_t>(at) / pieces) : at / pieces;
+    const int64_t col = (at - row * pieces) * 8;
+    valid[i] = static_cast<int>(min(q.cols - col, int64_t{8}));
+    const uintptr_t from = reinterpret_cast<uintptr_t>(q.src) + static_cast<uintptr_t>(row * q.ld_src + col) * 2;
+    const uintptr_t base = from & ~static_cast<uintptr_t>(15), end = from + static_cast<uintptr_t>(valid[i]) * 2;
+    shift[i] = static_cast<uint32_t>(from - base);
+    lo[i] = __ldg(reinterpret_cast<const uint4*>(base));
+    hi[i] = base + 16 < end ? __ldg(reinterpret_cast<const uint4*>(base + 16)) : make_uint4(0u, 0u, 0u, 0u);
+  }
+#pragma unroll
+  for (int i = 0; i < kPadPer; ++i) {
+    const int64_t at = first + i * kPadThreads;
+    if (at >= total) continue;
+    uint32_t w[8] = {lo[i].x, lo[i].y, lo[i].z, lo[i].w, hi[i].x, hi[i].y, hi[i].z, hi[i].w};
+    if (shift[i] & 8u) {
+#pragma unroll
+      for (int j = 0; j < 6; ++j) w[j] = w[j + 2];
+    }
+    if (shift[i] & 4u) {
+#pragma unroll
+      for (int j = 0; j < 5; ++j) w[j] = w[j + 1];
+    }
+    uint32_t out[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      out[j] = __funnelshift_r(w[j], w[j + 1], (shift[i] & 2u) * 8u);
+      const int left = valid[i] - 2 * j;
+      if (left < 2) out[j] = left < 1 ? 0u : out[j] & 0xFFFFu;
+    }
+    reinterpret_cast<uint4*>(q.dst)[at] = make_uint4(out[0], out[1], out[2], out[3]);
+  }
+}
+
 // ------------------------------------------------------------------ scales laid out for the product
 // 32 x 32 tiles through shared memory, lanes along the source's shorter stride.
 struct PackArgs {
@@ -492,6 +552,17 @@ cudaError_t launch_gated_grad(bool bf16, const GatedGradArgs& a, int num_sms, cu
   if (allow(8)) return bf16 ? launch_grad<true, 8>(a, num_sms, stream) : launch_grad<false, 8>(a, num_sms, stream);
   if (allow(4)) return bf16 ? launch_grad<true, 4>(a, num_sms, stream) : launch_grad<false, 4>(a, num_sms, stream);
   return bf16 ? launch_grad<true, 1>(a, num_sms, stream) : launch_grad<false, 1>(a, num_sms, stream);
+}
+
+cudaError_t launch_pad_rows(const RepackRequest (&req)[2], cudaStream_t stream) {
+  ff::PadArgs args{{req[0], req[1]}, 0};
+  constexpr int64_t kPerBlock = ff::kPadThreads * ff::kPadPer;
+  int64_t blocks[2];
+  for (int x = 0; x < 2; ++x) blocks[x] = (req[x].rows * (req[x].ld_dst / 8) + kPerBlock - 1) / kPerBlock;
+  if (blocks[0] + blocks[1] > INT32_MAX) return cudaErrorInvalidConfiguration;
+  args.blocks0 = static_cast<uint32_t>(blocks[0]);
+  return launch_dependent<ff::PadArgs>(ff::pad_rows_kernel, dim3(static_cast<unsigned>(blocks[0] + blocks[1])), ff::kPadThreads,
+                                       stream, args);
 }
 
 cudaError_t launch_pack_scales(const PackRequest (&req)[2], cudaStream_t stream) {
