@@ -99,7 +99,12 @@ bool scales_addressable(const float* p, int64_t rows, int64_t cols, int64_t s_i,
 constexpr double kTileTime[4][kNumFfTiles] = {
     {1.0, 0.71, 0.84}, {1.0, 0.60, 0.70}, {1.0, 0.57, 0.58}, {1.0, 0.54, 0.52}};
 
-constexpr int64_t kMostFew = 128;   // rows of A that the skinny kernel can take
+constexpr int64_t kMostFew = 1024;   // rows of A from which the skinny kernel, with 128 to a tile, is not looked at
+
+// Blocks of K that a product has at least to be cut, that a part has at least,
+// and the most parts. 512 x 512 over 8192 tokens 29.4 us whole and 12.3 cut, over
+// 4096 16.6 and 11.4; over 2048 cutting it would cost 0.7.
+constexpr int64_t kLeastCut = 64, kLeastPart = 16, kMostParts = 8;
 
 struct Choice {
   int rows = 0, splits = 0;   // skinny (rows != 0)
@@ -150,20 +155,22 @@ int choose(int kind, FfArgs& a, int sms, Choice* to) {
   const Forced force = forced();
   const Resident at_once = resident_on(sms);
   if (kind != kFfNt && a.m <= kMostFew && force.tile < 0) {
-    const int64_t tiles = (static_cast<int64_t>(a.n) * out_n + 127) / 128;
+    const int rows = a.m <= 16 ? 16 : a.m <= 32 ? 32 : a.m <= 64 ? 64 : 128;
+    const int64_t m_tiles = (a.m + rows - 1) / rows, n_tiles = (static_cast<int64_t>(a.n) * out_n + 127) / 128;
+    const int64_t tiles = m_tiles * n_tiles;
     // K is cut while all clusters run at once and every CTA has a few blocks of K
     int splits = 1;
     for (int i = 1; i < 4; ++i)
       if (tiles <= at_once.splits[i] && a.num_k_blocks >= 4 << i) splits = 1 << i;
     if (force.splits > 0 && a.num_k_blocks >= force.splits) splits = force.splits;
-    const int rows = a.m <= 16 ? 16 : a.m <= 32 ? 32 : a.m <= 64 ? 64 : 128;
-    if (ff_skinny_has(kind, rows, splits) && (force.splits > 0 || ff_skinny_pays(rows, a.num_k_blocks))) {
+    if (ff_skinny_has(kind, rows, splits) && (force.splits > 0 || ff_skinny_pays(kind, rows, splits, a.num_k_blocks))) {
       if (tiles * splits > INT32_MAX) return api_fail(GEMM_TN_ERR_INVALID_VALUE, "too many output tiles");
       to->rows = rows;
       to->splits = splits == 1 && tiles > sms ? 0 : splits;   // 0: two CTAs to an SM
       to->grid = static_cast<int>(tiles * splits);
-      a.num_m_tiles = 1;
-      a.num_n_tiles = a.num_tiles = static_cast<int32_t>(tiles);
+      a.num_m_tiles = static_cast<int32_t>(m_tiles);
+      a.num_n_tiles = static_cast<int32_t>(n_tiles);
+      a.num_tiles = static_cast<int32_t>(tiles);
       return GEMM_TN_OK;
     }
   }
@@ -190,6 +197,18 @@ int choose(int kind, FfArgs& a, int sms, Choice* to) {
     }
   }
   if (to->grid == 0) return api_fail(GEMM_TN_ERR_INVALID_VALUE, "too many output tiles");
+  a.splits = 1;
+  if (kind == kFfNt) {
+    // Few tiles and a long K (a small weight's gradient over many tokens): K is
+    // cut into parts that run at once, joined by a second kernel.
+    const int64_t slots = kFfTiles[to->tile].cta_group == 2 ? pairs : sms;
+    const int64_t parts = std::min<int64_t>({slots / a.num_tiles, a.num_k_blocks / kLeastPart, kMostParts});
+    if (parts > 1 && a.num_k_blocks >= kLeastCut) {
+      a.splits = static_cast<int32_t>(parts);
+      a.num_tiles *= a.splits;
+      to->grid *= a.splits;
+    }
+  }
   return GEMM_TN_OK;
 }
 
@@ -375,9 +394,26 @@ int gemm_nt(int dtype, int64_t m, int64_t n, int64_t k, const void* a, int64_t l
   if (st == GEMM_TN_OK) st = encode16(&args.tmap_a, bf16, a, k, m, lda, 64);
   if (st == GEMM_TN_OK) st = encode16(&args.tmap_b, bf16, b, k, n, ldb, 64);
   if (st != GEMM_TN_OK) return st;
-  const cudaError_t e = api_counted(launch_ff_nt(pick.tile, bf16, args, pick.grid, stream));
-  const cudaError_t freed = padded.free();
-  return finish(e == cudaSuccess ? freed : e);
+  Padded parts(stream);   // (workspace alone)
+  JoinRequest join{};
+  if (args.splits > 1) {
+    const int64_t pitch = (n + 3) / 4 * 4;
+    const cudaError_t e = api_workspace(static_cast<size_t>(args.splits * m * pitch * 4), stream, &parts.workspace);
+    if (e != cudaSuccess) {
+      parts.workspace = nullptr;
+      return api_fail_cuda(e, "workspace");
+    }
+    join = {static_cast<const float*>(parts.workspace), pitch, m * pitch, args.splits, c, ldc, m, n, args.out_kind, args.accumulate};
+    args.c = parts.workspace;
+    args.ldc = pitch;
+    args.part_stride = join.part_stride;
+    args.out_kind = GEMM_TN_ELEM_F32;
+    args.accumulate = 0;
+  }
+  cudaError_t e = api_counted(launch_ff_nt(pick.tile, bf16, args, pick.grid, stream));
+  if (e == cudaSuccess && args.splits > 1) e = api_counted(launch_join_parts(join, sms, stream));
+  const cudaError_t freed = padded.free(), freed_parts = parts.free();
+  return finish(e != cudaSuccess ? e : freed != cudaSuccess ? freed : freed_parts);
 }
 
 int quantize_e4m3(int src_type, int64_t rows, int64_t cols, const void* x, int64_t ldx, void* q, int64_t ldq,

@@ -33,6 +33,8 @@ struct FfArgs {
   int32_t activation;   // 1 relu, 2 gelu, 3 silu
   int32_t out_kind;     // 0 fp16, 1 bf16, 2 fp32
   int32_t accumulate;   // fp32: C's contents are added to
+  int32_t splits;       // nt: parts that K is cut into, each summed into an [m, n] array of its own (fp32, part_stride apart)
+  int64_t part_stride;
   int* status;
   uint64_t timeout_ns;
   int32_t drop_load_kb; // test hook: k-block of the first tile whose loads are skipped (-1: none)
@@ -81,15 +83,29 @@ int ff_resident_clusters(int splits, int sms);
 // Few rows of A: `rows` (16, 32, 64 or 128) of them against 128 rows of B a CTA, K split over clusters of `splits`
 // CTAs with an SM each (0: whole, two CTAs to an SM).
 // Up to 32 rows it runs whatever K; more pay where a long K is cut. Beside whole
-// tiles, us: e4m3, 64 rows, 4096 x 8192 11.7 and 18.2, x 1024 6.3 and 5.0; 128
-// rows, 4096 x 8192 17.0 and 18.4 cut in four, 8192 x 8192 23.4 and 18.6 cut in
-// two; gated, 128 rows, 4096 x 4096 14.9 and 17.8, x 1024 9.1 and 7.5.
+// tiles, us: e4m3, 64 rows, 4096 x 8192 11.7 and 18.2, x 1024 6.3 and 5.0; 256
+// rows cut in four, 1024 x 8192 15.9 and 18.4, x 4096 11.8 and 10.8; 200 rows cut
+// in eight, 512 x 4096 8.7 and 10.5; gated, 128 rows, 4096 x 4096 14.9 and 17.8, x
+// 1024 9.1 and 7.5; 256 rows, 512 x 4096 10.0 and 17.0.
 constexpr bool ff_skinny_has(int kind, int rows, int splits) {
   return rows <= 32 || splits >= (rows == 128 && kind != kFfGated ? 4 : 2);
 }
-constexpr bool ff_skinny_pays(int rows, int64_t k_blocks) { return rows <= 32 || k_blocks >= rows / 4; }
+constexpr bool ff_skinny_pays(int kind, int rows, int splits, int64_t k_blocks) {
+  return rows <= 32 || k_blocks >= (rows == 64 ? 16 : kind == kFfGated || splits == 8 ? 32 : 64);
+}
 cudaError_t launch_ff_skinny(int kind, bool bf16, int rows, int splits, const gemm_tn_dev::FfArgs& args, int grid,
                              cudaStream_t stream);
+
+// C [m, n] = the sum of `parts` fp32 arrays (pitch a multiple of 4), in order, as out_kind; or added to C.
+struct JoinRequest {
+  const float* parts;
+  int64_t pitch, part_stride;
+  int splits;
+  void* c;
+  int64_t ldc, m, n;
+  int out_kind, accumulate;
+};
+cudaError_t launch_join_parts(const JoinRequest& req, int num_sms, cudaStream_t stream);
 
 // launch_repack2's copies of 16-bit rows, made by pieces through all rows (a
 // block to a row leaves most of it idle where rows are short).

@@ -87,6 +87,40 @@ __global__ void __launch_bounds__(kGradThreads) gated_grad_kernel(const GatedGra
   }
 }
 
+// ------------------------------------------------------------------ a product's parts joined
+// Four columns a thread, the parts added in order (the same bits every time).
+constexpr int kJoinThreads = 256;
+
+__global__ void __launch_bounds__(kJoinThreads) join_parts_kernel(const gemm_tn_impl::JoinRequest q) {
+  griddep_wait();
+  griddep_launch_dependents();
+  const uint64_t pieces = static_cast<uint64_t>(q.pitch / 4), total = static_cast<uint64_t>(q.m) * pieces;
+  for (uint64_t x = blockIdx.x * static_cast<uint64_t>(kJoinThreads) + threadIdx.x; x < total;
+       x += static_cast<uint64_t>(gridDim.x) * kJoinThreads) {
+    const int64_t row = static_cast<int64_t>(total >> 32 == 0 ? static_cast<uint32_t>(x) / static_cast<uint32_t>(pieces) : x / pieces);
+    const int64_t col = static_cast<int64_t>(x - static_cast<uint64_t>(row) * pieces) * 4;
+    float4 t = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    const float* p = q.parts + row * q.pitch + col;
+    for (int s = 0; s < q.splits; ++s) {
+      const float4 v = __ldcg(reinterpret_cast<const float4*>(p + s * q.part_stride));
+      t = s == 0 ? v : make_float4(t.x + v.x, t.y + v.y, t.z + v.z, t.w + v.w);
+    }
+    const float v[4] = {t.x, t.y, t.z, t.w};
+    const int64_t at = row * q.ldc + col;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      if (col + j >= q.n) continue;
+      if (q.out_kind == kOutF32) {
+        float* c = static_cast<float*>(q.c) + at + j;
+        *c = q.accumulate ? *c + v[j] : v[j];
+      } else {
+        static_cast<uint16_t*>(q.c)[at + j] =
+            static_cast<uint16_t>(q.out_kind == kOutBf16 ? pack16<true>(v[j], 0.0f) : pack16<false>(v[j], 0.0f));
+      }
+    }
+  }
+}
+
 // ------------------------------------------------------------------ rows laid out for the TMA
 // A copy of 16-bit rows at any even address in rows of whole 16 bytes. A thread
 // makes kPadPer 16-byte pieces of the copies, counted through all rows, each from
@@ -552,6 +586,13 @@ cudaError_t launch_gated_grad(bool bf16, const GatedGradArgs& a, int num_sms, cu
   if (allow(8)) return bf16 ? launch_grad<true, 8>(a, num_sms, stream) : launch_grad<false, 8>(a, num_sms, stream);
   if (allow(4)) return bf16 ? launch_grad<true, 4>(a, num_sms, stream) : launch_grad<false, 4>(a, num_sms, stream);
   return bf16 ? launch_grad<true, 1>(a, num_sms, stream) : launch_grad<false, 1>(a, num_sms, stream);
+}
+
+cudaError_t launch_join_parts(const JoinRequest& req, int num_sms, cudaStream_t stream) {
+  const int64_t blocks = (req.m * (req.pitch / 4) + ff::kJoinThreads - 1) / ff::kJoinThreads;
+  const int64_t most = static_cast<int64_t>(num_sms) * 32;
+  return launch_dependent<JoinRequest>(ff::join_parts_kernel, dim3(static_cast<unsigned>(blocks < most ? blocks : most)),
+                                       ff::kJoinThreads, stream, req);
 }
 
 cudaError_t launch_pad_rows(const RepackRequest (&req)[2], cudaStream_t stream) {

@@ -340,8 +340,9 @@ __device__ __forceinline__ void store_rows(void* to, int64_t ldc, int rows, int 
 }
 
 // 32 fp32 values a lane, from column col0 of row row0 + lane, as C's element type.
-__device__ __forceinline__ void store_block(const FfArgs& a, int row0, int col0, const float (&v)[32], uint8_t* stage) {
-  const int64_t at = static_cast<int64_t>(row0) * a.ldc + col0;
+__device__ __forceinline__ void store_block(const FfArgs& a, int row0, int col0, const float (&v)[32], uint8_t* stage,
+                                            int64_t offset = 0) {
+  const int64_t at = static_cast<int64_t>(row0) * a.ldc + col0 + offset;
   uint32_t w[16];
   if (a.out_kind == kOutF32) {
 #pragma unroll

@@ -99,6 +99,27 @@ __device__ __forceinline__ void tile_at(const FfArgs& a, int tile, int& tm, int&
   tm = first + in - tn * rows;
 }
 
+// A CTA's units of work: tiles over all of K, or (nt) parts of K of a tile.
+struct Unit {
+  int tm, tn, kb0, kb1, part;
+};
+template <bool kCut>
+__device__ __forceinline__ Unit unit_at(const FfArgs& a, int unit) {
+  Unit u;
+  u.part = 0;
+  u.kb0 = 0;
+  u.kb1 = a.num_k_blocks;
+  if (kCut && a.splits > 1) {
+    const int tile = unit / a.splits;
+    u.part = unit - tile * a.splits;
+    u.kb0 = static_cast<int>(static_cast<int64_t>(u.part) * a.num_k_blocks / a.splits);
+    u.kb1 = static_cast<int>(static_cast<int64_t>(u.part + 1) * a.num_k_blocks / a.splits);
+    unit = tile;
+  }
+  tile_at(a, unit, u.tm, u.tn);
+  return u;
+}
+
 // H of a chunk of 32 columns from its two projections (32 fp32 values a lane).
 template <int kAct>
 __device__ __forceinline__ void gate(const uint32_t (&g)[32], const uint32_t (&u)[32], float (&h)[32]) {
@@ -176,11 +197,11 @@ __global__ void __launch_bounds__(kThreads, 1) ff_gemm_kernel(const __grid_const
       Issued issued;
       bool ok = true;
       for (int tile = first_tile; ok && tile < args.num_tiles; tile += tile_step) {
-        int tm, tn;
-        tile_at(args, tile, tm, tn);
-        const int a_row = tm * T::kTileM + static_cast<int>(rank) * T::kBlockM;
+        const Unit u = unit_at<T::kForm == kNt>(args, tile);
+        const int tn = u.tn;
+        const int a_row = u.tm * T::kTileM + static_cast<int>(rank) * T::kBlockM;
         const int b_row = tn * T::kOutN + static_cast<int>(rank) * T::kBRows;
-        for (int kb = 0; kb < args.num_k_blocks; ++kb) {
+        for (int kb = u.kb0; kb < u.kb1; ++kb) {
           if (!wd.warp_wait(empty_bar(stage), phase ^ 1u)) {
             ok = false;
             break;
@@ -246,9 +267,14 @@ __global__ void __launch_bounds__(kThreads, 1) ff_gemm_kernel(const __grid_const
       bool ok = true;
       int first_kb = stage;
       for (int tile = first_tile; ok && tile < args.num_tiles; tile += tile_step) {
-        int kb = first_kb;
-        for (; kb < args.num_k_blocks; kb += T::kMultiplyWarps) {
-          if ((T::kScaled || kb == 0) && !wd.warp_wait(sum_empty(buf), buf_phase ^ 1u)) ok = false;
+        int kb = first_kb, begin = 0, end = args.num_k_blocks;
+        if constexpr (T::kForm == kNt) {
+          const Unit u = unit_at<true>(args, tile);
+          kb = begin = u.kb0;
+          end = u.kb1;
+        }
+        for (; kb < end; kb += T::kMultiplyWarps) {
+          if ((T::kScaled || kb == begin) && !wd.warp_wait(sum_empty(buf), buf_phase ^ 1u)) ok = false;
           if (!ok || !wd.warp_wait(full_bar(stage), phase)) {
             ok = false;
             break;
@@ -264,14 +290,14 @@ __global__ void __launch_bounds__(kThreads, 1) ff_gemm_kernel(const __grid_const
 #pragma unroll
           for (int kk = 0; kk < 4; ++kk)
             mma_warp<T::kCtaGroup, T::kScaled>(elected, d, a_desc + kStep * kk, b_desc + kStep * kk, T::kIdesc,
-                                               kk > 0 || (!T::kScaled && kb > 0) ? 1u : 0u);
+                                               kk > 0 || (!T::kScaled && kb > begin) ? 1u : 0u);
           commit_warp<T::kCtaGroup>(elected, empty_bar(stage), 0x3);
           stage += T::kMultiplyWarps;
           if (stage >= T::kStages) {
             stage -= T::kStages;
             phase ^= 1u;
           }
-          if (T::kScaled || kb == args.num_k_blocks - 1) {
+          if (T::kScaled || kb == end - 1) {
             commit_warp<T::kCtaGroup>(elected, sum_full(buf), 0x3);
             buf += T::kMultiplyWarps;
             if (buf >= T::kBuffers) {
@@ -314,10 +340,9 @@ __global__ void __launch_bounds__(kThreads, 1) ff_gemm_kernel(const __grid_const
       }
     };
     for (int tile = first_tile; ok && tile < args.num_tiles; tile += tile_step) {
-      int tm, tn;
-      tile_at(args, tile, tm, tn);
-      const int row0 = tm * T::kTileM + static_cast<int>(rank) * T::kBlockM + static_cast<int>(quarter) * 32;
-      const int col0 = tn * T::kOutN;
+      const Unit unit = unit_at<T::kForm == kNt>(args, tile);
+      const int row0 = unit.tm * T::kTileM + static_cast<int>(rank) * T::kBlockM + static_cast<int>(quarter) * 32;
+      const int col0 = unit.tn * T::kOutN;
       const uint32_t t_quarter = tmem_base + ((quarter * 32u) << 16);
 
       if constexpr (T::kScaled) {
@@ -424,7 +449,7 @@ __global__ void __launch_bounds__(kThreads, 1) ff_gemm_kernel(const __grid_const
             float out[32];
 #pragma unroll
             for (int j = 0; j < 32; ++j) out[j] = __uint_as_float(v[j]);
-            store_block(args, row0, col, out, staging);
+            store_block(args, row0, col, out, staging, unit.part * args.part_stride);
           }
         }
       }

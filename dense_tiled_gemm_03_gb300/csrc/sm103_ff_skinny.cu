@@ -2,7 +2,7 @@
 // tokens): the gated projection and the e4m3 product, bound by reading B once.
 //
 // The roles swap: 128 rows of B are the MMA's M side and A's rows (zero-filled
-// past m) its N side, so that a CTA streams B through its ring and an
+// past m; 128 at most to a tile) its N side, so that a CTA streams B through its ring and an
 // accumulator lane holds one column of C. For the gated projection the 128 rows
 // are 64 of the gate and the same 64 of the other projection. K is cut over a
 // cluster of S CTAs, whose fp32 partials are added in CTA order through
@@ -67,7 +67,8 @@ __global__ void __launch_bounds__(kThreads, C::kPerSm) ff_skinny_kernel(const __
   const uint32_t base = smem_addr(smem);
   const uint32_t warp = threadIdx.x >> 5, lane = lane_id();
   const uint32_t rank = S > 1 ? cluster_ctarank() : 0u;
-  const int tn = static_cast<int>(blockIdx.x) / S;
+  const int tile = static_cast<int>(blockIdx.x) / S, tm = tile / args.num_n_tiles, tn = tile - tm * args.num_n_tiles;
+  const int row0 = tm * C::kN;   // of A and C
   const int kb0 = static_cast<int>(static_cast<int64_t>(rank) * args.num_k_blocks / S);
   const int kb1 = static_cast<int>(static_cast<int64_t>(rank + 1) * args.num_k_blocks / S);
 
@@ -130,7 +131,7 @@ __global__ void __launch_bounds__(kThreads, C::kPerSm) ff_skinny_kernel(const __
         } else {
           load_warp_hint(elected, &args.tmap_b, b_tile(stage), bar, k0, tn * 128, once);
         }
-        load_warp<1>(elected, &args.tmap_a, a_tile(stage), bar, k0, 0);
+        load_warp<1>(elected, &args.tmap_a, a_tile(stage), bar, k0, row0);
       }
       issued.record(stage, phase);
       if (++stage == C::kStages) {
@@ -188,7 +189,7 @@ __global__ void __launch_bounds__(kThreads, C::kPerSm) ff_skinny_kernel(const __
 #pragma unroll
           for (int i = 0; i < C::kN; i += 32)
             if (C::kN >= 32 || lane < static_cast<uint32_t>(C::kN))
-              cp_async_4(to + i + lane, args.a_scale + static_cast<int64_t>(min(i + static_cast<int>(lane), args.m - 1)) *
+              cp_async_4(to + i + lane, args.a_scale + static_cast<int64_t>(min(row0 + i + static_cast<int>(lane), args.m - 1)) *
                                                            args.as_row + kb * args.as_blk);
           cp_async_4(to + C::kN + lane, sb + kb * args.bs_blk);
         }
@@ -298,7 +299,7 @@ __global__ void __launch_bounds__(kThreads, C::kPerSm) ff_skinny_kernel(const __
       }
       return v[0];
     };
-    const int rows = min(args.m, C::kN);
+    const int rows = min(args.m - row0, C::kN);
     // consecutive threads: consecutive columns of C, four rows each
     for (int x = threadIdx.x; x < kCols * ((rows + 3) / 4); x += kThreads) {
       const int r = c0 + x % kCols, i0 = x / kCols * 4;
@@ -315,10 +316,10 @@ __global__ void __launch_bounds__(kThreads, C::kPerSm) ff_skinny_kernel(const __
           const float g = v[j];
           const float h = (args.activation == kSilu ? act<kSilu>(g) : args.activation == kGelu ? act<kGelu>(g)
                                                                                                : act<kRelu>(g)) * u[j];
-          static_cast<uint16_t*>(args.c)[static_cast<int64_t>(i0 + j) * args.ldc + col] =
+          static_cast<uint16_t*>(args.c)[static_cast<int64_t>(row0 + i0 + j) * args.ldc + col] =
               static_cast<uint16_t>(pack16<C::kBf16>(h, 0.0f));
           if (args.pre != nullptr) {
-            uint16_t* pre = static_cast<uint16_t*>(args.pre) + static_cast<int64_t>(i0 + j) * args.ldp + col;
+            uint16_t* pre = static_cast<uint16_t*>(args.pre) + static_cast<int64_t>(row0 + i0 + j) * args.ldp + col;
             const uint32_t both = pack16<C::kBf16>(g, u[j]);
             pre[0] = static_cast<uint16_t>(both);
             pre[args.n] = static_cast<uint16_t>(both >> 16);
@@ -328,7 +329,7 @@ __global__ void __launch_bounds__(kThreads, C::kPerSm) ff_skinny_kernel(const __
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
           if (i0 + j >= rows) continue;
-          const int64_t at = static_cast<int64_t>(i0 + j) * args.ldc + col;
+          const int64_t at = static_cast<int64_t>(row0 + i0 + j) * args.ldc + col;
           if (args.out_kind == kOutF32) {
             float* c = static_cast<float*>(args.c) + at;
             *c = args.accumulate ? *c + v[j] : v[j];

@@ -212,6 +212,37 @@ def test_mm_nt(mnk, dtype, out_dtype, which):
     assert_outside(out, whole)
 
 
+@pytest.mark.parametrize("which", ["auto"] + TILES)
+@pytest.mark.parametrize("out_dtype", ["bf16", "fp32", "added"])
+@pytest.mark.parametrize("mnk", [(1, 1, 4096), (70, 90, 4033), (300, 517, 5000), (1100, 513, 8190)], ids=str)
+def test_mm_nt_long(mnk, out_dtype, which):
+    """Few tiles and many tokens: K is cut into parts, joined in order."""
+    m, n, k = mnk
+    gen = torch.Generator().manual_seed(m + n + k)
+    a, b = normal(gen, k, m, dtype=torch.bfloat16), normal(gen, k, n, dtype=torch.bfloat16)
+    od = torch.bfloat16 if out_dtype == "bf16" else torch.float32
+    out, whole = padded((m, n), od, n + 9)
+    onto = None
+    if out_dtype == "added":
+        onto = normal(gen, m, n)
+        out.copy_(onto)
+    before = gt.gemm_tn_launch_count()
+    with kernel(which):
+        gt.mm_nt(a.cuda(), b.cuda(), out=out, accumulate=out_dtype == "added")
+    assert gt.gemm_tn_launch_count() - before >= 2
+    ref.assert_close(out, *ref.mm_nt(a, b, od, onto))
+    assert_outside(out, whole)
+
+
+@pytest.mark.parametrize("which", ["auto", "skinny2", "skinny4", "skinny8"])
+@pytest.mark.parametrize("mnk", [(129, 70, 2100), (300, 200, 4100), (700, 100, 2048)], ids=str)
+def test_several_tiles_of_few_rows(mnk, which):
+    """More rows than a skinny tile takes, few columns, a long K."""
+    check_gated(*mnk, "bf16", "silu", which)
+    for b_rows in (1, 128):
+        check_e4m3(mnk[0], mnk[1], 4 * mnk[2], b_rows, "fp32", which)
+
+
 @pytest.mark.parametrize("od", ["fp16", "fp32"])
 def test_mm_nt_odd_layouts(od):
     gen = torch.Generator().manual_seed(3)
@@ -480,6 +511,9 @@ def calls(gen):
         out.append((lambda dh=dh, p=p, d=d: gt.gated_grad(dh, p, out=d), [d]))
         c = torch.zeros((140, k), device="cuda")
         out.append((lambda p=p, a=a, c=c: gt.mm_nt(p, a, out=c), [c]))
+        if m == 300:
+            long, c2 = normal(gen, 5000, k, dtype=bf).cuda(), torch.zeros((k, k), dtype=bf, device="cuda")
+            out.append((lambda t=long, c=c2: gt.mm_nt(t, t, out=c), [c2]))
         x = normal(gen, m, k).cuda()
         for rows, transpose in ((1, False), (128, True)):
             q, s = gt.quantize_e4m3(x, rows, transpose)
