@@ -95,9 +95,9 @@ bool scales_addressable(const float* p, int64_t rows, int64_t cols, int64_t s_i,
 // Time of a tile of each shape, relative to the first's, where tiles abound
 // (smaller tiles read more from L2 for their work). Measured, us: gated 8192 x
 // 16384 x 4096 1061, 1512 and 1790; nt 16384 x 4096 x 8192 638, 771 and 900;
-// e4m3 8192^3 383, 438 and 443, with a scale for every row of B 536, 580 and 560.
+// e4m3 8192^3 374, 437 and 443, with a scale for every row of B 547, 580 and 560.
 constexpr double kTileTime[4][kNumFfTiles] = {
-    {1.0, 0.71, 0.84}, {1.0, 0.60, 0.70}, {1.0, 0.57, 0.58}, {1.0, 0.54, 0.52}};
+    {1.0, 0.71, 0.84}, {1.0, 0.60, 0.70}, {1.0, 0.585, 0.59}, {1.0, 0.53, 0.51}};
 
 constexpr int64_t kMostFew = 1024;   // rows of A from which the skinny kernel, with 128 to a tile, is not looked at
 

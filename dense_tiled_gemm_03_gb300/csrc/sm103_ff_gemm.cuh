@@ -58,6 +58,14 @@ struct Tile {
   static constexpr uint32_t kBoxBytes = 64 * 64 * 2;     // nt: 64 x 64 boxes
   static constexpr int kBuffers = kScaled ? 512 / kBlockN : 2;   // of tensor memory
   static constexpr uint32_t kTmemCols = kBuffers * kBlockN;
+  // kE4m3 pairs of 256 columns: a block is multiplied in two halves of N, each
+  // handed over and back by itself, so that the tensor core has three halves to
+  // go on with while one is being added (8192^3 391 us whole, 374 halved; with the
+  // columns' own scales, whose sums take longer than the products, no faster).
+  // A half is 64 of each CTA's rows of B: of the tile's columns the h-th 64 and
+  // the h-th 64 after 128.
+  static constexpr int kHalves = kForm == kE4m3 && kBlockN == 256 ? 2 : 1;
+  static constexpr int kMmaN = kBlockN / kHalves;
   // e4m3: warps 1 and 3 multiply, every other block each
   static constexpr int kMultiplyWarps = kScaled ? 2 : 1;
   // e4m3: a ring of the blocks' scales. A block's are loaded with its operands.
@@ -75,11 +83,11 @@ struct Tile {
   static constexpr uint32_t kOffStaging = kOffB + kStages * kStageB;
   static constexpr uint32_t kOffScale = kOffStaging + kEpilogueWarps * kStagingBytes;
   static constexpr uint32_t kOffBar = kOffScale + (kScaled ? kScaleSlots * kScaleStride : 0);
-  static constexpr int kNumBars = 2 * kStages + 2 * kBuffers + 1;   // full, empty, sum full, sum empty, drain
+  static constexpr int kNumBars = 2 * kStages + 2 * kBuffers * kHalves + 1;   // full, empty, sum full, sum empty, drain
   static constexpr uint32_t kOffTmemSlot = kOffBar + kNumBars * 8;
   static constexpr uint32_t kOffAbort = kOffTmemSlot + 4;
   static constexpr uint32_t kSmemBytes = kOffAbort + 4 + 1024;
-  static constexpr uint32_t kIdesc = mma_idesc_f16(!kScaled && kBf16, kTileM, kBlockN, kForm == kNt) |
+  static constexpr uint32_t kIdesc = mma_idesc_f16(!kScaled && kBf16, kTileM, kMmaN, kForm == kNt) |
                                      (kForm == kNt ? 1u << 15 : 0u);
   static_assert(kStages <= 32, "issued phases fit a 32-bit mask");
   static_assert(kTmemCols <= 512 && (kTmemCols & (kTmemCols - 1)) == 0, "TMEM columns");
@@ -143,8 +151,8 @@ __global__ void __launch_bounds__(kThreads, 1) ff_gemm_kernel(const __grid_const
   auto full_bar = [&](int s) { return base + T::kOffBar + 8u * s; };
   auto empty_bar = [&](int s) { return base + T::kOffBar + 8u * (T::kStages + s); };
   auto sum_full = [&](int b) { return base + T::kOffBar + 8u * (2 * T::kStages + b); };
-  auto sum_empty = [&](int b) { return base + T::kOffBar + 8u * (2 * T::kStages + T::kBuffers + b); };
-  const uint32_t drain_bar = base + T::kOffBar + 8u * (2 * T::kStages + 2 * T::kBuffers);
+  auto sum_empty = [&](int b) { return base + T::kOffBar + 8u * (2 * T::kStages + T::kBuffers * T::kHalves + b); };
+  const uint32_t drain_bar = base + T::kOffBar + 8u * (2 * T::kStages + 2 * T::kBuffers * T::kHalves);
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + T::kOffTmemSlot);
   volatile uint32_t* abort_flag = reinterpret_cast<volatile uint32_t*>(smem + T::kOffAbort);
 
@@ -153,9 +161,9 @@ __global__ void __launch_bounds__(kThreads, 1) ff_gemm_kernel(const __grid_const
       mbar_init(full_bar(s), 1);
       mbar_init(empty_bar(s), 1);
     }
-    for (int b = 0; b < T::kBuffers; ++b) {
+    for (int b = 0; b < T::kBuffers * T::kHalves; ++b) {
       mbar_init(sum_full(b), 1);
-      mbar_init(sum_empty(b), T::kCtaGroup * kEpilogueWarps);
+      mbar_init(sum_empty(b), T::kCtaGroup * kEpilogueWarps / T::kHalves);
     }
     mbar_init(drain_bar, T::kMultiplyWarps);
     *abort_flag = 0u;
@@ -274,13 +282,6 @@ __global__ void __launch_bounds__(kThreads, 1) ff_gemm_kernel(const __grid_const
           end = u.kb1;
         }
         for (; kb < end; kb += T::kMultiplyWarps) {
-          if ((T::kScaled || kb == begin) && !wd.warp_wait(sum_empty(buf), buf_phase ^ 1u)) ok = false;
-          if (!ok || !wd.warp_wait(full_bar(stage), phase)) {
-            ok = false;
-            break;
-          }
-          tc_fence_after_sync();
-          const uint32_t d = tmem_base + static_cast<uint32_t>(buf * T::kBlockN);
           // a step along K: 32 bytes of a K-major row, or two 8-row groups of an MN-major tile
           constexpr uint32_t kStep = T::kForm == kNt ? 2048u >> 4 : 2u;
           const uint64_t a_desc = T::kForm == kNt ? sw128_mnmajor_desc(a_tile(stage), T::kBoxBytes)
@@ -288,17 +289,28 @@ __global__ void __launch_bounds__(kThreads, 1) ff_gemm_kernel(const __grid_const
           const uint64_t b_desc = T::kForm == kNt ? sw128_mnmajor_desc(b_tile(stage), T::kBoxBytes)
                                                   : sw128_kmajor_desc(b_tile(stage));
 #pragma unroll
-          for (int kk = 0; kk < 4; ++kk)
-            mma_warp<T::kCtaGroup, T::kScaled>(elected, d, a_desc + kStep * kk, b_desc + kStep * kk, T::kIdesc,
-                                               kk > 0 || (!T::kScaled && kb > begin) ? 1u : 0u);
-          commit_warp<T::kCtaGroup>(elected, empty_bar(stage), 0x3);
+          for (int h = 0; h < T::kHalves; ++h) {
+            const int sum = buf * T::kHalves + h;
+            if (ok && (T::kScaled || kb == begin)) ok = wd.warp_wait(sum_empty(sum), buf_phase ^ 1u);
+            if (ok && h == 0) ok = wd.warp_wait(full_bar(stage), phase);
+            if (!ok) break;
+            tc_fence_after_sync();
+            const uint32_t d = tmem_base + static_cast<uint32_t>(sum * T::kMmaN);
+            constexpr uint32_t kHalfRows = T::kBRows / T::kHalves * 128u >> 4;   // of this CTA's rows of B
+#pragma unroll
+            for (int kk = 0; kk < 4; ++kk)
+              mma_warp<T::kCtaGroup, T::kScaled>(elected, d, a_desc + kStep * kk, b_desc + kHalfRows * h + kStep * kk, T::kIdesc,
+                                                 kk > 0 || (!T::kScaled && kb > begin) ? 1u : 0u);
+            if (h == T::kHalves - 1) commit_warp<T::kCtaGroup>(elected, empty_bar(stage), 0x3);
+            if (T::kScaled || kb == end - 1) commit_warp<T::kCtaGroup>(elected, sum_full(sum), 0x3);
+          }
+          if (!ok) break;
           stage += T::kMultiplyWarps;
           if (stage >= T::kStages) {
             stage -= T::kStages;
             phase ^= 1u;
           }
           if (T::kScaled || kb == end - 1) {
-            commit_warp<T::kCtaGroup>(elected, sum_full(buf), 0x3);
             buf += T::kMultiplyWarps;
             if (buf >= T::kBuffers) {
               buf -= T::kBuffers;
@@ -324,14 +336,16 @@ __global__ void __launch_bounds__(kThreads, 1) ff_gemm_kernel(const __grid_const
     int buf = 0, slot = 0;
     uint32_t buf_phase = 0;
     bool ok = true;
-    auto hand_back = [&]() {   // the buffer is in registers: the MMA warp may write it again
+    // this warp's sums: all of a buffer's, or the half that is its own
+    auto my_sum = [&]() { return T::kHalves == 2 ? 2 * buf + half : buf; };
+    auto hand_back = [&]() {   // they are in registers: the MMA warp may write them again
       tc_fence_before_sync();
       __syncwarp();
       if (lane == 0) {
         if constexpr (T::kCtaGroup == 2) {
-          arrive_remote(sum_empty0 + 8u * buf);
+          arrive_remote(sum_empty0 + 8u * my_sum());
         } else {
-          mbar_arrive(sum_empty(buf));
+          mbar_arrive(sum_empty(my_sum()));
         }
       }
       if (++buf == T::kBuffers) {
@@ -348,14 +362,18 @@ __global__ void __launch_bounds__(kThreads, 1) ff_gemm_kernel(const __grid_const
       if constexpr (T::kScaled) {
         // this warp's half of the columns; a thread's sums: its row's, two to a register pair
         constexpr int kCols = T::kBlockN / 2;
-        const int my_col = col0 + half * kCols;
+        // column of the tile of the thread's x-th sum
+        auto column = [&](int x) {
+          if constexpr (T::kHalves == 2) return half * 64 + (x < 64 ? x : x + 64);
+          return half * kCols + x;
+        };
         const uint32_t t_mine = t_quarter + static_cast<uint32_t>(half * kCols);
         uint64_t sum[kCols / 2];
 #pragma unroll
         for (int j = 0; j < kCols / 2; ++j) sum[j] = 0;
 #pragma unroll 1
         for (int kb = 0; kb < args.num_k_blocks; ++kb) {
-          if (!wd.warp_wait(sum_full(buf), buf_phase)) {
+          if (!wd.warp_wait(sum_full(my_sum()), buf_phase)) {
             ok = false;
             break;
           }
@@ -365,20 +383,24 @@ __global__ void __launch_bounds__(kThreads, 1) ff_gemm_kernel(const __grid_const
           tmem_load_32x16(t, v[0]);
           // (the block has been multiplied, so its scales have landed too)
           const float* scales = reinterpret_cast<const float*>(smem + T::kOffScale + static_cast<uint32_t>(slot) * T::kScaleStride);
-          const float* cols = scales + T::kBlockM + half * kCols;
+          const float* cols = scales + T::kBlockM;
           if (++slot == T::kScaleSlots) slot = 0;
-          float scale = scales[quarter * 32u + lane];
-          if constexpr (T::kForm == kE4m3) scale *= scales[T::kBlockM + (half * kCols / 128) * 4 + (kb & 3)];
-          const uint64_t scale2 = f32x2_pack(scale, scale);
+          const float row_scale = scales[quarter * 32u + lane];
+          uint64_t scale2[T::kHalves];   // kE4m3: by the columns' 128-row block of B
+#pragma unroll
+          for (int x = 0; x < T::kHalves; ++x) {
+            const float scale = T::kForm == kE4m3 ? row_scale * cols[x * 4 + (kb & 3)] : row_scale;
+            scale2[x] = f32x2_pack(scale, scale);
+          }
 #pragma unroll
           for (int c = 0; c < kCols / 16; ++c) {
             uint64_t both[8];   // the columns' scales times the row's, while tensor memory answers
             if constexpr (T::kForm == kE4m3Rows) {
 #pragma unroll
               for (int j = 0; j < 8; j += 2) {
-                const ulonglong2 b = *reinterpret_cast<const ulonglong2*>(cols + c * 16 + 2 * j);
-                both[j] = f32x2_mul(b.x, scale2);
-                both[j + 1] = f32x2_mul(b.y, scale2);
+                const ulonglong2 b = *reinterpret_cast<const ulonglong2*>(cols + column(c * 16) + 2 * j);
+                both[j] = f32x2_mul(b.x, scale2[0]);
+                both[j + 1] = f32x2_mul(b.y, scale2[0]);
               }
             }
             uint32_t(&x)[16] = v[c & 1];
@@ -391,7 +413,7 @@ __global__ void __launch_bounds__(kThreads, 1) ff_gemm_kernel(const __grid_const
 #pragma unroll
             for (int j = 0; j < 8; ++j) {
               const uint64_t p = f32x2_pack(__uint_as_float(x[2 * j]), __uint_as_float(x[2 * j + 1]));
-              sum[c * 8 + j] = f32x2_fma(p, T::kForm == kE4m3 ? scale2 : both[j], sum[c * 8 + j]);
+              sum[c * 8 + j] = f32x2_fma(p, T::kForm == kE4m3 ? scale2[c * 16 * T::kHalves / kCols] : both[j], sum[c * 8 + j]);
             }
           }
         }
@@ -401,7 +423,7 @@ __global__ void __launch_bounds__(kThreads, 1) ff_gemm_kernel(const __grid_const
           float out[32];
 #pragma unroll
           for (int j = 0; j < 16; ++j) f32x2_unpack(sum[c * 16 + j], out[2 * j], out[2 * j + 1]);
-          if (my_col + c * 32 < args.n) store_block(args, row0, my_col + c * 32, out, staging);
+          if (col0 + column(c * 32) < args.n) store_block(args, row0, col0 + column(c * 32), out, staging);
         }
       } else {
         // chunks of 32 columns of C, alternately this warp's and its partner's
