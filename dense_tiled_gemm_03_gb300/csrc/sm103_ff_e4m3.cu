@@ -1,4 +1,12 @@
-// sm103_ff_e4m3.cu -- instantiations.
+// sm103_ff_e4m3.cu -- the e4m3 product in whole tiles (sm103_ff_gemm.cuh).
+//
+// 8192^3 to bf16, a scale for 128 x 128 of B: 374 us (2940 TFLOP/s; 417 in a long
+// row of calls). The tensor core alone, nothing added up, takes 325: what is left
+// of the 16384 FLOP a clock is the hand-over of every block of 128 through a
+// barrier each way (870 clocks, of which two buffers in halves hide most). With a
+// scale for every row of B 547 us: the epilogue's two multiply-adds and a shared
+// load for each pair of elements, 297 instructions of a warp for a block against
+// 190, take longer than the product.
 #include "sm103_ff_gemm.cuh"
 
 namespace gemm_tn_impl {

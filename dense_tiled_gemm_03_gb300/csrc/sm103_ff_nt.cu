@@ -1,4 +1,9 @@
-// sm103_ff_nt.cu -- instantiations.
+// sm103_ff_nt.cu -- C = A^T B (sm103_ff_gemm.cuh), a weight's gradient.
+//
+// bf16, 16384 x 4096 over 8192 tokens: 564 us in a short graph (1950 TFLOP/s),
+// 638 at the power limit; the tensor pipe is active 91% of the kernel. What bounds
+// a small one (5000 x 1024 over 1000 tokens: 20 us) is the round of tiles begun for
+// the last few, and the start and end of the kernel.
 #include "sm103_ff_gemm.cuh"
 
 namespace gemm_tn_impl {

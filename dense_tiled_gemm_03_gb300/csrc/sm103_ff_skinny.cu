@@ -12,6 +12,10 @@
 // what a CTA streams is bound by its loads in flight, so it takes all of the SM's
 // shared memory. With more tiles than SMs two CTAs share one, and the last
 // loads and the join of one overlap the other's stream.
+//
+// Bound by memory: bf16, one token, 4096 to 2 x 16384: 40.3 us, 6.7 TB/s (whole
+// tiles 73); e4m3, 8 tokens, 8192 to 16384: 23.4 us, 5.7 TB/s, of which about 3 are
+// the start and the end. Small ones by latency: fp16, 24 tokens, 1000 to 2 x 2049: 5.4 us.
 #include <atomic>
 
 #include "sm103_ff.cuh"
