@@ -641,7 +641,8 @@ int stream_k_mode() {
 // launch counter in the low word. Each launch's flags start as whatever the
 // workspace held (no clearing pass): earlier launches wrote smaller counters,
 // and a contributor stores this launch's value only once its partial rows are
-// written.
+// written. (A launch that is captured, to be replayed with one value, is
+// preceded by a clearing of its flags.)
 std::atomic<uint64_t> g_flag_counter{0};
 uint64_t next_flag_epoch() {
   return (0x5EED5EEDull << 32) | ((g_flag_counter.fetch_add(1, std::memory_order_relaxed) + 1) & 0xFFFFFFFFull);
@@ -680,6 +681,16 @@ int group_rows(const ConfigInfo& cfg) {
     if (v > 0 && v < 65536) return static_cast<int>(v);
   }
   return cfg.cta_group == 2 ? 8 : 16;
+}
+
+// Whether the stream's work is being captured into a graph.
+bool capturing(cudaStream_t stream) {
+  cudaStreamCaptureStatus status = cudaStreamCaptureStatusNone;
+  if (cudaStreamIsCapturing(stream, &status) != cudaSuccess) {
+    cudaGetLastError();   // (the legacy stream while another captures: it cannot be captured itself)
+    return false;
+  }
+  return status != cudaStreamCaptureStatusNone;
 }
 
 int run_gemm(int dtype, int64_t m, int64_t n, int64_t k, const void* a, int64_t lda, const void* b, int64_t ldb,
@@ -823,6 +834,16 @@ int run_gemm(int dtype, int64_t m, int64_t n, int64_t k, const void* a, int64_t 
   }
   float* partials = partial_bytes ? reinterpret_cast<float*>(ws + a_bytes + b_bytes) : nullptr;
   uint64_t* flags = flag_bytes ? reinterpret_cast<uint64_t*>(ws + a_bytes + b_bytes + partial_bytes) : nullptr;
+  // A captured call's replays carry the capture's flag value and reuse its
+  // workspace, so they find the flags of the replay before: cleared first, or the
+  // finishing CTAs would take that replay's partial rows for this one's.
+  if (flags != nullptr && capturing(stream)) {
+    e = cudaMemsetAsync(flags, 0, flag_bytes, stream);
+    if (e != cudaSuccess) {
+      cudaFreeAsync(owned_workspace, stream);
+      return fail_cuda(e, "cudaMemsetAsync (stream-K flags)");
+    }
+  }
 
   alignas(64) gemm_tn_dev::GemmArgs args;
   std::memset(&args, 0, sizeof(args));
