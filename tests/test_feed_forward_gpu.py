@@ -579,6 +579,52 @@ def test_repeats_streams_and_captures():
     check("replayed")
 
 
+@pytest.mark.parametrize("tokens", [64, 2304])
+def test_a_captured_step_follows_its_inputs(tokens):
+    """A block's forward and backward pass captured once and replayed over new tokens, weights and gradients: the bits of
+    the same step called. Its products run on every kind of kernel, mm_nn's last tiles cut along K among them."""
+    gen = torch.Generator(device="cuda").manual_seed(tokens)
+    k, n, bf = 1000, 2176, torch.bfloat16
+    new = lambda *s: torch.randn(s, generator=gen, device="cuda").to(bf)
+    x, w, wd, dy = new(tokens, k), new(2 * n, k), new(k, n), new(tokens, k)
+    pre = torch.empty((tokens, 2 * n), dtype=bf, device="cuda")
+
+    def step():
+        h = gt.mm_tn_gated(x, w, pre=pre)
+        q, s = gt.quantize_e4m3(h)
+        y = gt.mm_tn_e4m3(q, s, *gt.quantize_e4m3(wd, block_rows=128))
+        dh = gt.mm_nn(dy, wd)
+        d = gt.gated_grad(dh, pre)
+        return [h, y, dh, gt.mm_nn(d, w), gt.mm_nt(d, x, out_dtype=torch.float32), gt.mm_nt(dy, h)]
+
+    step()
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g, stream=torch.cuda.Stream()):
+        captured = step()
+    for _ in range(4):
+        for t in (x, w, wd, dy):
+            t.copy_(new(*t.shape))
+        torch.cuda.synchronize()
+        g.replay()
+        torch.cuda.synchronize()
+        got = bits(captured)
+        want = bits(step())
+        assert all(torch.equal(a, b) for a, b in zip(got, want)), [torch.equal(a, b) for a, b in zip(got, want)]
+
+
+def test_one_scale_for_all():
+    """Scales broadcast with strides of zero: a scale for a whole matrix."""
+    gen = torch.Generator().manual_seed(31)
+    a, _, b, _ = operands(gen, 200, 150, 500, 1)
+    sa, sb = torch.full((1, 1), 0.37), torch.full((1, 1), 1.9)
+    for rows in (200, 9):
+        for lines, per in ((150, 1), (2, 128)):
+            got = gt.mm_tn_e4m3(on_gpu(a[:rows]), sa.cuda().expand(rows, 4), on_gpu(b), sb.cuda().expand(lines, 4),
+                                out_dtype=torch.float32)
+            ref.assert_close(got, *ref.mm_e4m3(a[:rows].float(), sa.expand(rows, 4), b.float(), sb.expand(lines, 4), per, torch.float32))
+
+
 def test_far_offsets():
     """Rows more than 2^31 elements apart: offsets past 32 bits in outputs and inputs."""
     pitch = (1 << 31) + 64
