@@ -227,9 +227,9 @@ PyObject* gated_grad_call(PyObject*, PyObject* const* args, Py_ssize_t nargs, Py
   if (!matrix(in[0], "grad", &index, &grad) || !half_type(grad, &code)) return nullptr;
   const int64_t m = grad.rows, n = grad.cols;
   Tensor keep;
-  // a new one's rows lie a multiple of 16 bytes apart: the products read them in place
+  // a new one's rows lie a multiple of 128 bytes apart: the products read them in place, in whole lines
   if (!matrix_of(in[1], "pre", index, m, 2 * n, grad.type(), &pre) ||
-      !(in[2] == nullptr ? made(at::empty_strided({m, 2 * n}, {round_up(2 * n, 8), 1}, grad.t->options()), &keep, &out)
+      !(in[2] == nullptr ? made(at::empty_strided({m, 2 * n}, {std::max<int64_t>(round_up(2 * n, 64), 1), 1}, grad.t->options()), &keep, &out)
                          : matrix_of(in[2], "out", index, m, 2 * n, grad.type(), &out)) ||
       !gate(in[3], &act))
     return nullptr;
@@ -298,7 +298,7 @@ PyObject* quantize(PyObject*, PyObject* const* args, Py_ssize_t nargs, PyObject*
   const int64_t lines = transpose ? x.cols : x.rows, along = transpose ? x.rows : x.cols;
   const int64_t s_lines = (lines + block - 1) / block, s_blocks = (along + 127) / 128;
   Tensor keep_q, keep_s;
-  if (!(in[3] == nullptr ? made(at::empty_strided({lines, along}, {std::max<int64_t>(round_up(along, 16), 1), 1},
+  if (!(in[3] == nullptr ? made(at::empty_strided({lines, along}, {std::max<int64_t>(round_up(along, 128), 1), 1},
                                                   x.t->options().dtype(at::kFloat8_e4m3fn)), &keep_q, &q)
                          : matrix_of(in[3], "out", index, lines, along, at::kFloat8_e4m3fn, &q)))
     return nullptr;
@@ -460,8 +460,8 @@ PyMethodDef functions[] = {
      "x [M, K] (CUDA fp16, bf16 or fp32, unit stride along K) as (q, scale)\n"
      "through quantize_e4m3: q float8_e4m3fn [M, K], or of x's transpose [K, M]; a\n"
      "power of two for each block of block_rows (1 or 128) rows and 128 columns of\n"
-     "q. Without out and scale, q's rows lie a multiple of 16 bytes apart, as\n"
-     "mm_tn_e4m3 takes them, and the scales of single rows (block_rows 1) side by\n"
+     "q. Without out and scale, q's rows lie a multiple of 128 bytes apart, which\n"
+     "suits mm_tn_e4m3 best, and the scales of single rows (block_rows 1) side by\n"
      "side (scale.stride(0) is 1)."},
     {"mm_tn_e4m3", as_function(mm_tn_e4m3), METH_FASTCALL | METH_KEYWORDS,
      "mm_tn_e4m3(a, a_scale, b, b_scale, out=None, out_dtype=None, accumulate=False, status=None)\n--\n\n"

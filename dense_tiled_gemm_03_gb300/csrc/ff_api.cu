@@ -212,7 +212,7 @@ int choose(int kind, FfArgs& a, int sms, Choice* to) {
   return GEMM_TN_OK;
 }
 
-// Copies of operands in rows a multiple of 16 bytes apart, where they need one; freed in stream order.
+// Copies of operands that the engine cannot address, where they need one; freed in stream order.
 struct Padded {
   void* workspace = nullptr;
   cudaStream_t stream;
@@ -224,7 +224,8 @@ struct Padded {
     if (b_rows == 1) *ldb = (b_cols + 7) / 8 * 8;
     const bool pad_a = !addressable(*a, *lda), pad_b = !addressable(*b, *ldb);
     if (!pad_a && !pad_b) return GEMM_TN_OK;
-    const int64_t la = (a_cols + 7) / 8 * 8, lb = (b_cols + 7) / 8 * 8;
+    // (rows of whole 128-byte lines: a box's row is one)
+    const int64_t la = (a_cols + 63) / 64 * 64, lb = (b_cols + 63) / 64 * 64;
     const size_t a_bytes = pad_a ? static_cast<size_t>((a_rows * la * 2 + 255) / 256 * 256) : 0;
     const size_t b_bytes = pad_b ? static_cast<size_t>(b_rows * lb * 2) : 0;
     cudaError_t e = api_workspace(a_bytes + b_bytes, stream, &workspace);
