@@ -99,7 +99,7 @@ bool scales_addressable(const float* p, int64_t rows, int64_t cols, int64_t s_i,
 constexpr double kTileTime[4][kNumFfTiles] = {
     {1.0, 0.71, 0.84}, {1.0, 0.60, 0.70}, {1.0, 0.585, 0.59}, {1.0, 0.53, 0.51}};
 
-constexpr int64_t kMostFew = 1024;   // rows of A from which the skinny kernel, with 128 to a tile, is not looked at
+constexpr int64_t kMostFew = 1024;   // rows of A up to which the skinny kernel (128 to a tile) is looked at
 
 // Blocks of K that a product has at least to be cut, that a part has at least,
 // and the most parts. 512 x 512 over 8192 tokens 29.4 us whole and 12.3 cut, over
@@ -149,7 +149,7 @@ Forced forced() {
   return f;
 }
 
-// Fills args' tile counts. False (with the error set) for too many tiles.
+// The kernel for args' sizes, and args' tile counts. A status.
 int choose(int kind, FfArgs& a, int sms, Choice* to) {
   const int64_t out_n = kind == kFfGated ? 2 : 1;   // columns of the product for one of C
   const Forced force = forced();

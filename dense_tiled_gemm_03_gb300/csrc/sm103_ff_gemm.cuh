@@ -45,7 +45,7 @@ template <int kForm_, int kCtaGroup_, int kBlockN_, int kStages_, bool kBf16_>
 struct Tile {
   static constexpr int kForm = kForm_;
   static constexpr int kCtaGroup = kCtaGroup_;
-  static constexpr int kBlockN = kBlockN_;               // MMA N
+  static constexpr int kBlockN = kBlockN_;               // columns of products to a tile
   static constexpr int kStages = kStages_;
   static constexpr bool kBf16 = kBf16_;
   static constexpr bool kScaled = kForm == kE4m3 || kForm == kE4m3Rows;
