@@ -165,7 +165,7 @@ ATTN_SOURCES = ("sm103_flash_attn.cu", "sm103_ptx.cuh", "gemm_tn_internal.h", "g
 NOT_GEMM_SOURCES = ("sm103_flash_attn.cu", "repack.cu", "kv_cache_api.cu", "kv_cache_internal.h", "kv_cache_ops.cu",
                     "sm103_cache.cuh", "sm103_cache_ptx.cuh", "sm103_cache_weigh.cu", "sm103_decode_attn.cu",
                     "sm103_tree_attn.cu", "sm103_tree_attn.cuh",
-                    "py_args.h", "ff_api.cu", "ff_internal.h", "ff_ops.cu", "sm103_ff.cuh", "sm103_ff_e4m3.cu", "sm103_ff_gated.cu",
+                    "py_args.h", "ff_api.cu", "ff_internal.h", "ff_ops.cu", "ff_pad.h", "sm103_ff.cuh", "sm103_ff_e4m3.cu", "sm103_ff_gated.cu",
                     "sm103_ff_gemm.cuh", "sm103_ff_nt.cu", "sm103_ff_skinny.cu")
 
 

@@ -10,6 +10,7 @@
 
 #include "feed_forward.h"
 #include "ff_internal.h"
+#include "ff_pad.h"
 
 namespace gemm_tn_impl {
 namespace {
@@ -224,8 +225,7 @@ struct Padded {
     if (b_rows == 1) *ldb = (b_cols + 7) / 8 * 8;
     const bool pad_a = !addressable(*a, *lda), pad_b = !addressable(*b, *ldb);
     if (!pad_a && !pad_b) return GEMM_TN_OK;
-    // (rows of whole 128-byte lines: a box's row is one)
-    const int64_t la = (a_cols + 63) / 64 * 64, lb = (b_cols + 63) / 64 * 64;
+    const int64_t la = gemm_tn_dev::ff::pad_pitch(a_cols), lb = gemm_tn_dev::ff::pad_pitch(b_cols);
     const size_t a_bytes = pad_a ? static_cast<size_t>((a_rows * la * 2 + 255) / 256 * 256) : 0;
     const size_t b_bytes = pad_b ? static_cast<size_t>(b_rows * lb * 2) : 0;
     cudaError_t e = api_workspace(a_bytes + b_bytes, stream, &workspace);

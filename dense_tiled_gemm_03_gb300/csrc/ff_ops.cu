@@ -3,6 +3,7 @@
 // Both are bound by memory: each element is read once and written once.
 #include <type_traits>
 
+#include "ff_pad.h"
 #include "sm103_ff.cuh"
 
 namespace gemm_tn_dev {
@@ -124,9 +125,10 @@ __global__ void __launch_bounds__(kJoinThreads) join_parts_kernel(const gemm_tn_
 }
 
 // ------------------------------------------------------------------ rows laid out for the TMA
-// A copy of 16-bit rows at any even address in rows of whole 16 bytes. A thread
-// makes kPadPer 16-byte pieces of the copies, counted through all rows, each from
-// the one or two aligned pieces of the source that hold it.
+// A copy of 16-bit rows at any even address in rows pad_pitch apart, zeros behind
+// the columns. A thread makes kPadPer 16-byte pieces of the copies, counted through
+// all rows, each from the aligned pieces of the source that hold it: one or two, or
+// none behind the row's last column, where the source may end and nothing is loaded.
 struct PadArgs {
   gemm_tn_impl::RepackRequest req[2];   // (rows 0: none)
   uint32_t blocks0;                     // of the first
@@ -152,12 +154,12 @@ __global__ void __launch_bounds__(kPadThreads) pad_rows_kernel(const PadArgs a) 
     // (rows and pieces of a row stay below 2^30)
     const int64_t row = total < (int64_t{1} << 32) ? static_cast<int64_t>(static_cast<uint32_t>(at) / pieces) : at / pieces;
     const int64_t col = (at - row * pieces) * 8;
-    valid[i] = static_cast<int>(min(q.cols - col, int64_t{8}));
-    const uintptr_t from = reinterpret_cast<uintptr_t>(q.src) + static_cast<uintptr_t>(row * q.ld_src + col) * 2;
-    const uintptr_t base = from & ~static_cast<uintptr_t>(15), end = from + static_cast<uintptr_t>(valid[i]) * 2;
-    shift[i] = static_cast<uint32_t>(from - base);
-    lo[i] = __ldg(reinterpret_cast<const uint4*>(base));
-    hi[i] = base + 16 < end ? __ldg(reinterpret_cast<const uint4*>(base + 16)) : make_uint4(0u, 0u, 0u, 0u);
+    const uintptr_t line = reinterpret_cast<uintptr_t>(q.src) + static_cast<uintptr_t>(row * q.ld_src) * 2;
+    const PadPiece piece = pad_piece(line, q.cols, col);
+    valid[i] = piece.valid;
+    shift[i] = piece.shift;
+    lo[i] = piece.lo != 0 ? __ldg(reinterpret_cast<const uint4*>(piece.lo)) : make_uint4(0u, 0u, 0u, 0u);
+    hi[i] = piece.hi != 0 ? __ldg(reinterpret_cast<const uint4*>(piece.hi)) : make_uint4(0u, 0u, 0u, 0u);
   }
 #pragma unroll
   for (int i = 0; i < kPadPer; ++i) {

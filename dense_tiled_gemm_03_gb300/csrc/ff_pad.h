@@ -1,0 +1,40 @@
+// ff_pad.h -- the layout of a copy of 16-bit rows (pad_rows_kernel), and which of
+// the source's memory each part of it reads; plain C++ for the host and the device.
+#pragma once
+
+#include <cstdint>
+
+#ifdef __CUDACC__
+#define FF_PAD_CALL __host__ __device__ __forceinline__
+#else
+#define FF_PAD_CALL inline
+#endif
+
+namespace gemm_tn_dev {
+namespace ff {
+
+// Elements between rows of the copy: whole 128-byte lines, since a box's row is one.
+FF_PAD_CALL int64_t pad_pitch(int64_t cols) { return (cols + 63) / 64 * 64; }
+
+// A 16-byte piece of the copy: 8 elements of a row, or those of them that the row has.
+struct PadPiece {
+  int valid;        // elements inside the row: 8, fewer at its end, 0 behind it
+  uint32_t shift;   // bytes from lo to the first of them
+  uintptr_t lo;     // the aligned 16 bytes of the source that hold the first of them (0: nothing to load),
+  uintptr_t hi;     // and the next 16, where they hold the last (0: they do not)
+};
+
+// The piece at column `col` of a row of `cols` elements that begins at address `row`.
+FF_PAD_CALL PadPiece pad_piece(uintptr_t row, int64_t cols, int64_t col) {
+  const int64_t left = cols - col;
+  if (left <= 0) return {0, 0, 0, 0};
+  const int valid = left < 8 ? static_cast<int>(left) : 8;
+  const uintptr_t from = row + static_cast<uintptr_t>(col) * 2, base = from & ~static_cast<uintptr_t>(15);
+  const uintptr_t end = from + static_cast<uintptr_t>(valid) * 2;
+  return {valid, static_cast<uint32_t>(from - base), base, base + 16 < end ? base + 16 : 0};
+}
+
+}  // namespace ff
+}  // namespace gemm_tn_dev
+
+#undef FF_PAD_CALL
