@@ -11,9 +11,9 @@ namespace ff {
 
 // ------------------------------------------------------------------ gated gradient
 // h = act(g) u: dg = dh u act'(g), du = dh act(g), in 32 bits from 16-bit
-// values, rounded once to 16. 8192 x 8192 bf16: 97 us with silu, 104 with gelu
-// (6.9 and 6.5 TB/s); by single elements, where n is odd, 1000 x 2501 takes 12.0 us
-// and by fours 1000 x 2500 6.4.
+// values, rounded once to 16. 8192 x 8192 bf16: 97 us with silu, 107 with gelu
+// (6.9 and 6.3 TB/s); by single elements, where n is odd, 1000 x 2501 with gelu takes
+// 12.5 us and by fours 1000 x 2500 7.0.
 constexpr int kGradThreads = 256;
 
 // A piece of kWidth 16-bit elements (8, 4 or 1), as a thread loads it.
