@@ -232,8 +232,9 @@ __global__ void __launch_bounds__(kThreads, C::kPerSm) ff_skinny_kernel(const __
             const ulonglong2 a2 = *reinterpret_cast<const ulonglong2*>(now + c * 16 + 2 * j);
             const uint64_t p0 = f32x2_pack(__uint_as_float(v[2 * j]), __uint_as_float(v[2 * j + 1]));
             const uint64_t p1 = f32x2_pack(__uint_as_float(v[2 * j + 2]), __uint_as_float(v[2 * j + 3]));
-            sum[c * 8 + j] = f32x2_fma(f32x2_mul(p0, a2.x), b2, sum[c * 8 + j]);
-            sum[c * 8 + j + 1] = f32x2_fma(f32x2_mul(p1, a2.y), b2, sum[c * 8 + j + 1]);
+            // (the scales' product first, as in whole tiles: a large one and a small one may meet)
+            sum[c * 8 + j] = f32x2_fma(p0, f32x2_mul(a2.x, b2), sum[c * 8 + j]);
+            sum[c * 8 + j + 1] = f32x2_fma(p1, f32x2_mul(a2.y, b2), sum[c * 8 + j + 1]);
           }
         }
         if (++buf == C::kBuffers) {

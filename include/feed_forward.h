@@ -91,11 +91,13 @@ GEMM_TN_API int quantize_e4m3(int src_type, int64_t rows, int64_t cols, const vo
  * gemm_tn_e4m3 -- C[i][j] = sum over blocks of 128 of K of
  * sa[i][block] * sb[j][block] * sum over the block of A[i][k] * B[j][k].
  * a: [m, k], b: [n, k] e4m3 with 16-byte-aligned bases and pitches (else
- * GEMM_TN_ERR_MISALIGNED). a_scale[i * as_row + block * as_blk]: fp32, any
- * values. b_scale likewise, for every row of b (b_block_rows 1) or for 128
+ * GEMM_TN_ERR_MISALIGNED). a_scale[i * as_row + block * as_blk]: fp32.
+ * b_scale likewise, for every row of b (b_block_rows 1) or for 128
  * rows together, b_scale[j / 128 * bs_row + block * bs_blk] (b_block_rows 128).
  * Fastest with as_row == 1 (and bs_row == 1 where b_block_rows is 1).
- * Products of a block are summed by the tensor core, the blocks in fp32.
+ * Products of a block are summed by the tensor core, the blocks in fp32: that sum
+ * times the two scales' product, which is taken first. Scales may have any values;
+ * where their product leaves fp32's range it is an infinity or zero, and so treated.
  * c: [m, n] of out_type (gemm_tn_element), aligned to its element; accumulate (fp32 only): added
  * to C. k == 0 as in gemm_nt.
  */
