@@ -13,8 +13,10 @@
 namespace gemm_tn_dev {
 namespace ff {
 
-// Elements between rows of the copy: whole 128-byte lines, since a box's row is one.
-FF_PAD_CALL int64_t pad_pitch(int64_t cols) { return (cols + 63) / 64 * 64; }
+// Elements between rows of the copy: whole 128-byte lines, since a box's row is one;
+// up to half a line whole 16-byte pieces, which take less memory and time (A^T B with A
+// 262144 x 20: 116 us, in lines 123; x 36 123 in lines, 128 in pieces).
+FF_PAD_CALL int64_t pad_pitch(int64_t cols) { return cols <= 32 ? (cols + 7) / 8 * 8 : (cols + 63) / 64 * 64; }
 
 // A 16-byte piece of the copy: 8 elements of a row, or those of them that the row has.
 struct PadPiece {

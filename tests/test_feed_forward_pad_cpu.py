@@ -77,3 +77,9 @@ def test_the_loads_hold_the_pieces_elements(pad, start):
             assert lo + shift == row + 2 * col and 0 <= shift < 16
             assert hi in (0, lo + 16)
             assert lo + (32 if hi else 16) >= row + 2 * (col + valid)
+
+
+def test_the_copy_of_narrow_rows_stays_small(pad):
+    """At most twice what rows of whole 16-byte pieces take, whatever the width."""
+    for cols in COLUMNS:
+        assert pad.pitch(cols) <= 2 * ((cols + 7) // 8 * 8), cols
