@@ -67,32 +67,32 @@ CSRC = ROOT / "dense_tiled_gemm_03_gb300" / "csrc"
 # are unchanged (a changed kernel makes it stale). Keyed by (workload, kernel
 # configuration) or, for the fused kernels, (workload, configuration, epilogue).
 NCU_TRAFFIC: dict[tuple, dict] = {
-    ("bf16_8192x8192x8192", "2cta_n256"): {  # 571.8 us
-        "bytes": 1162989824 + 136566016, "when": "2026-12-09", "source": "95450687c664",
+    ("bf16_8192x8192x8192", "2cta_n256"): {  # 543.0 us
+        "bytes": 1075120640 + 135926784, "when": "2026-12-09", "source": "ce039039d13d",
         "kernel": "gemm_tn_sm103_kernel<GemmConfig<2, 256, 6, 1, 1, 0, 0, 0, 0>>"},
-    ("fp16_4096x4096x4096", "2cta_n256_mc"): {  # 83.7 us
-        "bytes": 104703744 + 29661440, "when": "2026-12-09", "source": "95450687c664",
+    ("fp16_4096x4096x4096", "2cta_n256_mc"): {  # 81.0 us
+        "bytes": 106600448 + 30169344, "when": "2026-12-09", "source": "ce039039d13d",
         "kernel": "gemm_tn_sm103_kernel<GemmConfig<2, 256, 6, 0, 2, 0, 0, 0, 0>>"},
-    ("fp16_3001x5003x4097", "2cta_n256_mc"): {  # 88.4 us
-        "bytes": 96929536 + 21554432, "when": "2026-12-09", "source": "95450687c664",
+    ("fp16_3001x5003x4097", "2cta_n256_mc"): {  # 83.2 us
+        "bytes": 98186752 + 22677248, "when": "2026-12-09", "source": "ce039039d13d",
         "kernel": "gemm_tn_sm103_kernel<GemmConfig<2, 256, 6, 0, 2, 0, 0, 0, 0>>"},
-    ("bf16_128x16384x16384", "1cta_n128"): {  # 90.9 us
-        "bytes": 542156032 + 48128, "when": "2026-12-09", "source": "95450687c664",
+    ("bf16_128x16384x16384", "1cta_n128"): {  # 92.0 us
+        "bytes": 542157824 + 60416, "when": "2026-12-09", "source": "ce039039d13d",
         "kernel": "gemm_tn_sm103_kernel<GemmConfig<1, 128, 6, 1, 1, 0, 0, 0, 0>>"},
-    ("fp16_256x256x256", "1cta_n64"): {  # 6.8 us
-        "bytes": 305408 + 0, "when": "2026-12-09", "source": "95450687c664",
+    ("fp16_256x256x256", "1cta_n64"): {  # 6.7 us
+        "bytes": 305408 + 0, "when": "2026-12-09", "source": "ce039039d13d",
         "kernel": "gemm_tn_sm103_kernel<GemmConfig<1, 64, 4, 0, 1, 0, 0, 0, 1>>"},
-    ("bf16_8x4096x4096", "1cta_decode_splitk"): {  # 11.8 us
-        "bytes": 33643520 + 0, "when": "2026-12-09", "source": "95450687c664",
+    ("bf16_8x4096x4096", "1cta_decode_splitk"): {  # 11.6 us
+        "bytes": 33638144 + 0, "when": "2026-12-09", "source": "ce039039d13d",
         "kernel": "gemm_tn_decode_kernel<4, 16, 1, 2>"},
-    ("bf16_8192x8192x8192", "2cta_n256", "bias_gelu"): {  # 580.3 us
-        "bytes": 1113583104 + 132182272, "when": "2026-12-09", "source": "95450687c664",
+    ("bf16_8192x8192x8192", "2cta_n256", "bias_gelu"): {  # 558.0 us
+        "bytes": 1069615360 + 132244224, "when": "2026-12-09", "source": "ce039039d13d",
         "kernel": "gemm_tn_sm103_kernel<GemmConfig<2, 256, 6, 1, 1, 0, 1, 0, 0>>"},
 }
 # the same for the attention kernel, keyed by workload
 NCU_TRAFFIC_ATTN: dict[str, dict] = {
-    "attn_bf16_b2_s8192_h32_d128_causal": {  # 753.5 us
-        "bytes": 453142528 + 116584960, "when": "2026-12-09", "source": "90d77fa2c367",
+    "attn_bf16_b2_s8192_h32_d128_causal": {  # 752.0 us
+        "bytes": 453747712 + 113934336, "when": "2026-12-09", "source": "6067bbca1615",
         "kernel": "flash_attn_fwd_kernel<Cfg<128, 1>>"},
 }
 

@@ -488,12 +488,18 @@ cudaError_t workspace_pool(int dev, cudaMemPool_t* out) {
     props.location.type = cudaMemLocationTypeDevice;
     props.location.id = dev;
     cudaMemPool_t pool = nullptr;
+    // The first call that needs a workspace may be a captured one. Making the
+    // pool is no part of the capture, but would end it (and other threads'
+    // captures) in the mode that captures begin with.
+    cudaStreamCaptureMode mode = cudaStreamCaptureModeRelaxed;
+    const bool relaxed = cudaThreadExchangeStreamCaptureMode(&mode) == cudaSuccess;
     cudaError_t e = cudaMemPoolCreate(&pool, &props);
     if (e == cudaSuccess) {
       uint64_t keep = UINT64_MAX;
       e = cudaMemPoolSetAttribute(pool, cudaMemPoolAttrReleaseThreshold, &keep);
       if (e != cudaSuccess) cudaMemPoolDestroy(pool);
     }
+    if (relaxed) cudaThreadExchangeStreamCaptureMode(&mode);
     if (e != cudaSuccess) {
       cudaGetLastError();
       return e;
