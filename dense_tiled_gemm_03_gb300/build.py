@@ -75,7 +75,7 @@ def _binding_stamp() -> Path:
 
 
 def _ff_stamp() -> Path:
-    return FF_BINDING.with_name(f".{FF_BINDING.name}.torch.o")   # (ignored as what a build makes)
+    return BUILD_DIR / "ff_binding_torch.txt"
 
 
 def _is_stale(module: Path, source: Path, stamp: Path, torch_dir: Path) -> bool:
