@@ -158,8 +158,9 @@ __global__ void __launch_bounds__(kPadThreads) pad_rows_kernel(const PadArgs a) 
     const PadPiece piece = pad_piece(line, q.cols, col);
     valid[i] = piece.valid;
     shift[i] = piece.shift;
-    lo[i] = piece.lo != 0 ? __ldg(reinterpret_cast<const uint4*>(piece.lo)) : make_uint4(0u, 0u, 0u, 0u);
-    hi[i] = piece.hi != 0 ? __ldg(reinterpret_cast<const uint4*>(piece.hi)) : make_uint4(0u, 0u, 0u, 0u);
+    const uint4* from = reinterpret_cast<const uint4*>(piece.at);
+    lo[i] = piece.first ? __ldg(from) : make_uint4(0u, 0u, 0u, 0u);
+    hi[i] = piece.second ? __ldg(from + 1) : make_uint4(0u, 0u, 0u, 0u);
   }
 #pragma unroll
   for (int i = 0; i < kPadPer; ++i) {

@@ -18,22 +18,23 @@ namespace ff {
 // 262144 x 20: 116 us, in lines 123; x 36 123 in lines, 128 in pieces).
 FF_PAD_CALL int64_t pad_pitch(int64_t cols) { return cols <= 32 ? (cols + 7) / 8 * 8 : (cols + 63) / 64 * 64; }
 
-// A 16-byte piece of the copy: 8 elements of a row, or those of them that the row has.
+// A 16-byte piece of the copy: 8 elements of a row, or those of them that the row
+// has, from the one or two aligned 16-byte pieces of the source that hold them. Behind
+// the row's last column, where the source may end, there are none to load.
 struct PadPiece {
-  int valid;        // elements inside the row: 8, fewer at its end, 0 behind it
-  uint32_t shift;   // bytes from lo to the first of them
-  uintptr_t lo;     // the aligned 16 bytes of the source that hold the first of them (0: nothing to load),
-  uintptr_t hi;     // and the next 16, where they hold the last (0: they do not)
+  int valid;        // elements inside the row: 8, fewer at its end, none (<= 0) behind it
+  uint32_t shift;   // bytes from `at` to the first of them
+  uintptr_t at;     // the first aligned piece
+  bool first, second;   // whether it, and the one behind it, hold any of them
 };
 
 // The piece at column `col` of a row of `cols` elements that begins at address `row`.
 FF_PAD_CALL PadPiece pad_piece(uintptr_t row, int64_t cols, int64_t col) {
   const int64_t left = cols - col;
-  if (left <= 0) return {0, 0, 0, 0};
-  const int valid = left < 8 ? static_cast<int>(left) : 8;
-  const uintptr_t from = row + static_cast<uintptr_t>(col) * 2, base = from & ~static_cast<uintptr_t>(15);
-  const uintptr_t end = from + static_cast<uintptr_t>(valid) * 2;
-  return {valid, static_cast<uint32_t>(from - base), base, base + 16 < end ? base + 16 : 0};
+  const int valid = static_cast<int>(left < 8 ? left : 8);
+  const uintptr_t from = row + static_cast<uintptr_t>(col) * 2, at = from & ~static_cast<uintptr_t>(15);
+  const uintptr_t end = from + static_cast<uintptr_t>(static_cast<int64_t>(valid)) * 2;
+  return {valid, static_cast<uint32_t>(from - at), at, valid > 0, valid > 0 && at + 16 < end};
 }
 
 }  // namespace ff

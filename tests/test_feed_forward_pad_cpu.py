@@ -16,10 +16,10 @@ DRIVER = """
 extern "C" long long pitch(long long cols) { return gemm_tn_dev::ff::pad_pitch(cols); }
 extern "C" void piece(unsigned long long row, long long cols, long long col, long long* out) {
   const gemm_tn_dev::ff::PadPiece p = gemm_tn_dev::ff::pad_piece(row, cols, col);
-  out[0] = p.valid;
+  out[0] = p.valid > 0 ? p.valid : 0;
   out[1] = p.shift;
-  out[2] = static_cast<long long>(p.lo);
-  out[3] = static_cast<long long>(p.hi);
+  out[2] = p.first ? static_cast<long long>(p.at) : 0;
+  out[3] = p.second ? static_cast<long long>(p.at) + 16 : 0;
 }
 """
 
