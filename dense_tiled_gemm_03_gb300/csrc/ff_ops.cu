@@ -227,7 +227,7 @@ __global__ void __launch_bounds__(256) pack_scales_kernel(const PackArgs a) {
 // of these is looked through again without them.
 //
 // 16384 x 8192 bf16: 60.3 us (6.7 TB/s), transposed 64; 11001 x 4096 fp32 by
-// tiles, transposed: 36 us (6.2 TB/s); 16-bit rows at odd addresses, read element by
+// tiles, transposed: 39 us (5.8 TB/s; 36 with half of it in L2); 16-bit rows at odd addresses, read element by
 // element, take twice that. Each row reduced by itself, as floats (32 shuffles
 // a thread instead of 8), it took 129 us.
 
@@ -548,8 +548,8 @@ namespace {
 using namespace gemm_tn_dev;
 
 template <class Args, class... Rest>
-cudaError_t launch_dependent(void (*kernel)(Args, Rest...), dim3 grid, int threads, cudaStream_t stream, const Args& args,
-                             Rest... rest) {
+cudaError_t launch(void (*kernel)(Args, Rest...), dim3 grid, int threads, cudaStream_t stream, bool early, const Args& args,
+                   Rest... rest) {
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = grid;
   cfg.blockDim = dim3(static_cast<unsigned>(threads));
@@ -558,8 +558,23 @@ cudaError_t launch_dependent(void (*kernel)(Args, Rest...), dim3 grid, int threa
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
-  cfg.numAttrs = dependent_launch_enabled() ? 1 : 0;
+  cfg.numAttrs = early && dependent_launch_enabled() ? 1 : 0;
   return cudaLaunchKernelEx(&cfg, kernel, args, rest...);
+}
+// Its set-up may overlap the kernel before it in the stream.
+template <class Args, class... Rest>
+cudaError_t launch_dependent(void (*kernel)(Args, Rest...), dim3 grid, int threads, cudaStream_t stream, const Args& args,
+                             Rest... rest) {
+  return launch<Args, Rest...>(kernel, grid, threads, stream, true, args, rest...);
+}
+// It starts when all before it in the stream has ended. The copies into a
+// workspace are launched so: their workspace was freed and allocated anew behind the
+// product before. (In rows of 600 calls of A^T B, 16384 x 4095 over 8192 tokens,
+// whose copies could start early, the GPU came to a stop; captured rows, where
+// the memory's nodes lie between, and rows without copies never did.)
+template <class Args>
+cudaError_t launch_in_order(void (*kernel)(Args), dim3 grid, int threads, cudaStream_t stream, const Args& args) {
+  return launch<Args>(kernel, grid, threads, stream, false, args);
 }
 
 template <bool kBf16, int kWidth>
@@ -612,8 +627,8 @@ cudaError_t launch_pad_rows(const RepackRequest (&req)[2], cudaStream_t stream) 
   for (int x = 0; x < 2; ++x) blocks[x] = (req[x].rows * (req[x].ld_dst / 8) + kPerBlock - 1) / kPerBlock;
   if (blocks[0] + blocks[1] > INT32_MAX) return cudaErrorInvalidConfiguration;
   args.blocks0 = static_cast<uint32_t>(blocks[0]);
-  return launch_dependent<ff::PadArgs>(ff::pad_rows_kernel, dim3(static_cast<unsigned>(blocks[0] + blocks[1])), ff::kPadThreads,
-                                       stream, args);
+  return launch_in_order<ff::PadArgs>(ff::pad_rows_kernel, dim3(static_cast<unsigned>(blocks[0] + blocks[1])), ff::kPadThreads,
+                                      stream, args);
 }
 
 cudaError_t launch_pack_scales(const PackRequest (&req)[2], cudaStream_t stream) {
@@ -621,8 +636,8 @@ cudaError_t launch_pack_scales(const PackRequest (&req)[2], cudaStream_t stream)
   int64_t tiles[2];
   for (int x = 0; x < 2; ++x) tiles[x] = (req[x].rows + 31) / 32 * ((req[x].cols + 31) / 32);
   args.tiles0 = tiles[0];
-  return launch_dependent<ff::PackArgs>(ff::pack_scales_kernel, dim3(static_cast<unsigned>(tiles[0] + tiles[1])), 256, stream,
-                                        args);
+  return launch_in_order<ff::PackArgs>(ff::pack_scales_kernel, dim3(static_cast<unsigned>(tiles[0] + tiles[1])), 256, stream,
+                                       args);
 }
 
 cudaError_t launch_quantize(int src_kind, int block_rows, bool transpose, const QuantizeArgs& a, cudaStream_t stream) {
