@@ -63,10 +63,8 @@ __device__ __forceinline__ uint4 extract16(const uint4& lo, const uint4& hi, uin
 }
 
 __global__ void __launch_bounds__(256) repack_rows_kernel(const __grid_constant__ RepackArgs args) {
-  // launched as a programmatic dependent: read the sources only once the
-  // previous kernel in the stream has completed; the GEMM that follows may
-  // then be scheduled (it waits for this grid before reading the copies)
-  asm volatile("griddepcontrol.wait;" ::: "memory");
+  // the GEMM that follows may be scheduled (it waits for this grid before
+  // reading the copies)
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   uint64_t evict_first;
   asm volatile("createpolicy.fractional.L2::evict_first.b64 %0, 1.0;" : "=l"(evict_first));
@@ -145,11 +143,10 @@ cudaError_t launch_repack2(const RepackRequest* req, int num, int num_sms, cudaS
   cfg.blockDim = dim3(256, 1, 1);
   cfg.dynamicSmemBytes = 0;
   cfg.stream = stream;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = dependent_launch_enabled() ? 1 : 0;
+  // In stream order, not as a programmatic dependent: the workspace that it
+  // writes was freed and allocated anew behind the product before, and long rows
+  // of such copies that could start early have brought the GPU to a stop
+  // (launch_in_order, ff_ops.cu).
   return cudaLaunchKernelEx(&cfg, gemm_tn_dev::repack_rows_kernel, args);
 }
 

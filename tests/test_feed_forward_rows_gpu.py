@@ -58,3 +58,10 @@ def test_rows_of_e4m3_with_scales_copied():
     sa, sb = sa.contiguous(), sb.contiguous()      # strides that the TMA cannot address
     out = torch.empty((4096, 4095), device="cuda")
     row(lambda status: gt.mm_tn_e4m3(qa, sa, qb, sb, out=out, status=status), out, 600)
+
+
+@pytest.mark.parametrize("m,n,k,count", [(3001, 5003, 4097, 600), (8192, 8191, 4095, 300)])
+def test_rows_of_mm_tn(m, n, k, count):
+    gen = torch.Generator(device="cuda").manual_seed(k)
+    a, b, out = normal(gen, m, k), normal(gen, n, k), torch.empty((m, n), dtype=torch.bfloat16, device="cuda")
+    row(lambda status: gt.mm_tn(a, b, out=out, status=status), out, count)
