@@ -448,7 +448,8 @@ PyMethodDef functions[] = {
      "The gradient of act(G) * U through gated_grad. grad: [M, N], of the\n"
      "output; pre: [M, 2N], G and U side by side (mm_tn_gated's); out: optional\n"
      "[M, 2N], dG and dU side by side (may be pre itself). With mm_tn_gated's a\n"
-     "and b, the gradients are mm_nn(out, b) and mm_nt(out, a). Returns out."},
+     "and b, the gradients are mm_nn(out, b) and mm_nt(out, a). Without out, its\n"
+     "rows lie a multiple of 128 bytes apart, which suits both. Returns out."},
     {"mm_nt", as_function(mm_nt), METH_FASTCALL | METH_KEYWORDS,
      "mm_nt(a, b, out=None, out_dtype=None, accumulate=False, status=None)\n--\n\n"
      "C = A^T B through gemm_nt. a: [K, M], b: [K, N] CUDA tensors of one\n"

@@ -13,8 +13,9 @@
  * elements between rows, device pointers are the caller's, work is enqueued on
  * `stream` and the call returns; host-side errors are the return value and
  * nothing is enqueued then; a device watchdog's expiry goes to *d_status.
- * Outputs must not overlap inputs or one another, unless said otherwise. Every
- * sum is held in fp32, and repeated calls give the same bits. Workspaces
+ * Outputs must not overlap inputs or one another, unless said otherwise; a matrix
+ * is the stretch of memory from its first element to its last (so columns of one
+ * buffer, side by side, overlap). Every sum is held in fp32, and repeated calls give the same bits. Workspaces
  * (padded copies of operands that the tensor-memory-access engine cannot
  * address: base or pitch not a multiple of 16 bytes) come from
  * gemm_tn_workspace_pool() in stream order.
