@@ -1,7 +1,7 @@
 // sm103_ff_gated.cu -- the gated projection in whole tiles (sm103_ff_gemm.cuh).
 //
-// bf16, 8192 tokens, 4096 to 2 x 16384: 1118 us a call in a short replayed graph
-// with both projections written too (1967 TFLOP/s), 1280 in a long row of calls,
+// bf16, 8192 tokens, 4096 to 2 x 16384: 1108 to 1133 us a call in a short replayed graph
+// with both projections written too (1941 to 1985 TFLOP/s), 1300 in a long row of calls,
 // where the board's power limit holds the SM clock at 1.6 GHz; the tensor pipe is
 // active 96% of the kernel. fp16, 1111 tokens, 2048 to 2 x 5003: 32 us with the
 // operands in L2 and 37 from memory, 200 tiles in three rounds of 76 pairs.

@@ -37,7 +37,7 @@ def row(call, out, count):
     assert torch.equal(out, want)
 
 
-@pytest.mark.parametrize("k,m,n,count", [(8192, 16384, 4095, 600), (1000, 5001, 1023, 2000), (5000, 515, 67, 2000)])
+@pytest.mark.parametrize("k,m,n,count", [(8192, 16384, 4095, 600), (1000, 5001, 1023, 2000), (5000, 515, 67, 2000), (8192, 512, 512, 2000)])
 def test_rows_of_mm_nt(k, m, n, count):
     gen = torch.Generator(device="cuda").manual_seed(k)
     a, b, out = normal(gen, k, m), normal(gen, k, n), torch.empty((m, n), device="cuda")
