@@ -67,32 +67,32 @@ CSRC = ROOT / "dense_tiled_gemm_03_gb300" / "csrc"
 # are unchanged (a changed kernel makes it stale). Keyed by (workload, kernel
 # configuration) or, for the fused kernels, (workload, configuration, epilogue).
 NCU_TRAFFIC: dict[tuple, dict] = {
-    ("bf16_8192x8192x8192", "2cta_n256"): {  # 543.0 us
-        "bytes": 1075120640 + 135926784, "when": "2026-12-09", "source": "ce039039d13d",
+    ("bf16_8192x8192x8192", "2cta_n256"): {  # 550.0 us
+        "bytes": 1072354816 + 135396864, "when": "2026-12-09", "source": "6ed83ff0900f",
         "kernel": "gemm_tn_sm103_kernel<GemmConfig<2, 256, 6, 1, 1, 0, 0, 0, 0>>"},
-    ("fp16_4096x4096x4096", "2cta_n256_mc"): {  # 81.0 us
-        "bytes": 106600448 + 30169344, "when": "2026-12-09", "source": "ce039039d13d",
+    ("fp16_4096x4096x4096", "2cta_n256_mc"): {  # 81.6 us
+        "bytes": 105130496 + 29835520, "when": "2026-12-09", "source": "6ed83ff0900f",
         "kernel": "gemm_tn_sm103_kernel<GemmConfig<2, 256, 6, 0, 2, 0, 0, 0, 0>>"},
-    ("fp16_3001x5003x4097", "2cta_n256_mc"): {  # 83.2 us
-        "bytes": 98186752 + 22677248, "when": "2026-12-09", "source": "ce039039d13d",
+    ("fp16_3001x5003x4097", "2cta_n256_mc"): {  # 86.9 us
+        "bytes": 97273600 + 21588224, "when": "2026-12-09", "source": "6ed83ff0900f",
         "kernel": "gemm_tn_sm103_kernel<GemmConfig<2, 256, 6, 0, 2, 0, 0, 0, 0>>"},
-    ("bf16_128x16384x16384", "1cta_n128"): {  # 92.0 us
-        "bytes": 542157824 + 60416, "when": "2026-12-09", "source": "ce039039d13d",
+    ("bf16_128x16384x16384", "1cta_n128"): {  # 92.2 us
+        "bytes": 542158848 + 41216, "when": "2026-12-09", "source": "6ed83ff0900f",
         "kernel": "gemm_tn_sm103_kernel<GemmConfig<1, 128, 6, 1, 1, 0, 0, 0, 0>>"},
-    ("fp16_256x256x256", "1cta_n64"): {  # 6.7 us
-        "bytes": 305408 + 0, "when": "2026-12-09", "source": "ce039039d13d",
+    ("fp16_256x256x256", "1cta_n64"): {  # 6.5 us
+        "bytes": 305664 + 0, "when": "2026-12-09", "source": "6ed83ff0900f",
         "kernel": "gemm_tn_sm103_kernel<GemmConfig<1, 64, 4, 0, 1, 0, 0, 0, 1>>"},
     ("bf16_8x4096x4096", "1cta_decode_splitk"): {  # 11.6 us
-        "bytes": 33638144 + 0, "when": "2026-12-09", "source": "ce039039d13d",
+        "bytes": 33637888 + 0, "when": "2026-12-09", "source": "6ed83ff0900f",
         "kernel": "gemm_tn_decode_kernel<4, 16, 1, 2>"},
-    ("bf16_8192x8192x8192", "2cta_n256", "bias_gelu"): {  # 558.0 us
-        "bytes": 1069615360 + 132244224, "when": "2026-12-09", "source": "ce039039d13d",
+    ("bf16_8192x8192x8192", "2cta_n256", "bias_gelu"): {  # 562.1 us
+        "bytes": 1065826304 + 131899648, "when": "2026-12-09", "source": "6ed83ff0900f",
         "kernel": "gemm_tn_sm103_kernel<GemmConfig<2, 256, 6, 1, 1, 0, 1, 0, 0>>"},
 }
 # the same for the attention kernel, keyed by workload
 NCU_TRAFFIC_ATTN: dict[str, dict] = {
-    "attn_bf16_b2_s8192_h32_d128_causal": {  # 752.0 us
-        "bytes": 453747712 + 113934336, "when": "2026-12-09", "source": "6067bbca1615",
+    "attn_bf16_b2_s8192_h32_d128_causal": {  # 750.8 us
+        "bytes": 452813824 + 113785088, "when": "2026-12-09", "source": "f1a2ad69f9a8",
         "kernel": "flash_attn_fwd_kernel<Cfg<128, 1>>"},
 }
 

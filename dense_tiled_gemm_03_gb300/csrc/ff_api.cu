@@ -323,6 +323,7 @@ int gemm_tn_gated(int dtype, int64_t m, int64_t n, int64_t k, const void* a, int
   st = encode16(&args.tmap_a, bf16, a, m, k, lda, pick.rows ? pick.rows : 128);
   if (st == GEMM_TN_OK) st = encode16(&args.tmap_b, bf16, b, 2 * n, k, ldb, pick.rows ? 64 : kFfTiles[pick.tile].block_n / 2);
   if (st != GEMM_TN_OK) return st;
+  args.alone = padded.workspace != nullptr;
   cudaError_t e = api_counted(pick.rows ? launch_ff_skinny(kFfGated, bf16, pick.rows, pick.splits, args, pick.grid, stream)
                                         : launch_ff_gated(pick.tile, bf16, args, pick.grid, stream));
   const cudaError_t freed = padded.free();
@@ -395,6 +396,8 @@ int gemm_nt(int dtype, int64_t m, int64_t n, int64_t k, const void* a, int64_t l
   if (st == GEMM_TN_OK) st = encode16(&args.tmap_a, bf16, a, k, m, lda, 64);
   if (st == GEMM_TN_OK) st = encode16(&args.tmap_b, bf16, b, k, n, ldb, 64);
   if (st != GEMM_TN_OK) return st;
+  // (with parts to join it is followed by its own join, which no workspace's end precedes)
+  args.alone = padded.workspace != nullptr && args.splits == 1;
   Padded parts(stream);   // (workspace alone)
   JoinRequest join{};
   if (args.splits > 1) {
@@ -555,6 +558,7 @@ int gemm_tn_e4m3(int64_t m, int64_t n, int64_t k, const void* a, int64_t lda, co
              ? encode_scales(&args.tmap_bs, scales[1].p, blocks, n, pitch_of(scales[1]), tile.block_n, 1)
              : encode_scales(&args.tmap_bs, scales[1].p, b_lines, blocks, pitch_of(scales[1]), 4, tile.block_n / 128);
   if (st != GEMM_TN_OK) return st;
+  args.alone = copies.workspace != nullptr;
   const cudaError_t e = api_counted(launch_ff_e4m3(pick.tile, b_block_rows == 1, args, pick.grid, stream));
   const cudaError_t freed = copies.free();
   return finish(e == cudaSuccess ? freed : e);

@@ -35,6 +35,7 @@ struct FfArgs {
   int32_t accumulate;   // fp32: C's contents are added to
   int32_t splits;       // nt: parts that K is cut into, each summed into an [m, n] array of its own (fp32, part_stride apart)
   int64_t part_stride;
+  int32_t alone;        // nothing may start early while this runs (a workspace is freed behind it)
   int* status;
   uint64_t timeout_ns;
   int32_t drop_load_kb; // test hook: k-block of the first tile whose loads are skipped (-1: none)

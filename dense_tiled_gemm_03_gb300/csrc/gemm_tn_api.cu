@@ -918,6 +918,7 @@ int run_gemm(int dtype, int64_t m, int64_t n, int64_t k, const void* a, int64_t 
   args.partials = partials;
   args.flags = flags;
   args.flag_epoch = flags != nullptr ? next_flag_epoch() : 0;
+  args.alone = owned_workspace != nullptr ? 1 : 0;
   args.split = split;
   args.split_log2 = split == 4 ? 2 : (split == 2 ? 1 : 0);
   args.split_begin = static_cast<int32_t>(split_begin);

@@ -190,7 +190,7 @@ __global__ void __launch_bounds__(kThreads, 1) ff_gemm_kernel(const __grid_const
   const uint32_t tmem_base = *tmem_slot;
   // set-up may overlap the previous kernel in the stream; memory waits for it
   griddep_wait();
-  griddep_launch_dependents();
+  if (args.alone == 0) griddep_launch_dependents();
 
   const Waiter<T::kCtaGroup> wd{args.status, args.timeout_ns, abort_flag};
   const int first_tile = static_cast<int>(blockIdx.x) / T::kCtaGroup;

@@ -112,7 +112,7 @@ __global__ void __launch_bounds__(kThreads, C::kPerSm) ff_skinny_kernel(const __
   tc_fence_after_sync();
   const uint32_t tmem_base = *tmem_slot;
   griddep_wait();
-  griddep_launch_dependents();
+  if (args.alone == 0) griddep_launch_dependents();
   const Waiter<1> wd{args.status, args.timeout_ns, abort_flag};
 
   if (warp == 0) {

@@ -127,6 +127,7 @@ struct GemmArgs {
   // loads evict-first in L2.
   int32_t k_rotate;
   int32_t b_evict_first;
+  int32_t alone;          // nothing may start early while this runs (a workspace is freed behind it)
 };
 
 template <int kCtaGroup_, int kBlockN_, int kStages_, bool kBf16_, int kClusterPairs_ = 1, bool kBMnMajor_ = false,
@@ -486,7 +487,7 @@ __global__ void __launch_bounds__(kNumThreads, 1) gemm_tn_sm103_kernel(const __g
   const bool producer_thread = warp == kProducerWarp && lane == 0;
   if (!producer_thread) {
     griddep_wait();
-    griddep_launch_dependents();
+    if (args.alone == 0) griddep_launch_dependents();
   }
 
   const Watchdog<Cfg> wd{&args, abort_flag, smem_addr(const_cast<uint32_t*>(abort_flag))};
@@ -550,7 +551,7 @@ __global__ void __launch_bounds__(kNumThreads, 1) gemm_tn_sm103_kernel(const __g
           }
           if (!dep_waited) {
             griddep_wait();
-            griddep_launch_dependents();
+            if (args.alone == 0) griddep_launch_dependents();
             dep_waited = true;
           }
           const int kb = rotate_kb(kb_i, kstart, args.num_k_blocks);
@@ -602,7 +603,7 @@ __global__ void __launch_bounds__(kNumThreads, 1) gemm_tn_sm103_kernel(const __g
       }
       if (!dep_waited) {
         griddep_wait();
-        griddep_launch_dependents();
+        if (args.alone == 0) griddep_launch_dependents();
       }
       // Loads may still be landing if another role gave up: wait (bounded)
       // for the last phase issued into every stage before the CTA may exit.

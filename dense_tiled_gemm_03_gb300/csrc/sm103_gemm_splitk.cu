@@ -154,7 +154,7 @@ __global__ void __launch_bounds__(splitk::kThreads, 1) gemm_tn_splitk_kernel(con
   // it: the producer just before its first copy, every other thread here
   if (warp != 0 || lane != 0) {
     griddep_wait();
-    griddep_launch_dependents();
+    if (args.alone == 0) griddep_launch_dependents();
   }
   const Watchdog<ClusterOf<S>> wd{&args, abort_flag, smem_addr(const_cast<uint32_t*>(abort_flag))};
 
@@ -169,7 +169,7 @@ __global__ void __launch_bounds__(splitk::kThreads, 1) gemm_tn_splitk_kernel(con
         if (!wd.wait(empty_bar(stage), phase ^ 1u)) break;
         if (!dep_waited) {
           griddep_wait();
-          griddep_launch_dependents();
+          if (args.alone == 0) griddep_launch_dependents();
           dep_waited = true;
         }
         const uint32_t fb = full_bar(stage);
@@ -191,7 +191,7 @@ __global__ void __launch_bounds__(splitk::kThreads, 1) gemm_tn_splitk_kernel(con
       }
       if (!dep_waited) {
         griddep_wait();
-        griddep_launch_dependents();
+        if (args.alone == 0) griddep_launch_dependents();
       }
       // loads still landing after another role gave up finish before exit
       for (int s = 0; s < kRing; ++s)
@@ -428,7 +428,7 @@ __global__ void __launch_bounds__(decode::kThreads, 1) gemm_tn_decode_kernel(con
   // it: the producer just before its first copy, every other thread here
   if (warp != 0 || lane != 0) {
     griddep_wait();
-    griddep_launch_dependents();
+    if (args.alone == 0) griddep_launch_dependents();
   }
   const Watchdog<splitk::ClusterOf<S>> wd{&args, abort_flag, smem_addr(const_cast<uint32_t*>(abort_flag))};
 
@@ -443,7 +443,7 @@ __global__ void __launch_bounds__(decode::kThreads, 1) gemm_tn_decode_kernel(con
         if (!wd.wait(empty_bar(stage), phase ^ 1u)) break;
         if (!dep_waited) {
           griddep_wait();
-          griddep_launch_dependents();
+          if (args.alone == 0) griddep_launch_dependents();
           dep_waited = true;
         }
         const uint32_t fb = full_bar(stage);
@@ -465,7 +465,7 @@ __global__ void __launch_bounds__(decode::kThreads, 1) gemm_tn_decode_kernel(con
       }
       if (!dep_waited) {
         griddep_wait();
-        griddep_launch_dependents();
+        if (args.alone == 0) griddep_launch_dependents();
       }
       for (int s = 0; s < L::kStages; ++s)
         if (issued.any(s)) wd.drain(full_bar(s), issued.phase(s));

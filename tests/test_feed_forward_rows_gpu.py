@@ -65,3 +65,28 @@ def test_rows_of_mm_tn(m, n, k, count):
     gen = torch.Generator(device="cuda").manual_seed(k)
     a, b, out = normal(gen, m, k), normal(gen, n, k), torch.empty((m, n), dtype=torch.bfloat16, device="cuda")
     row(lambda status: gt.mm_tn(a, b, out=out, status=status), out, count)
+
+
+def test_rows_of_a_blocks_step():
+    """Products that use workspaces (a last wave cut along K, copied operands), with kernels of many blocks that may
+    start early right behind them: a block's backward pass and its output quantised, again and again."""
+    gen = torch.Generator(device="cuda").manual_seed(5)
+    m, n, k = 4100, 2303, 2047
+    x, w, wd, dy = normal(gen, m, k), normal(gen, 2 * n, k), normal(gen, k, n), normal(gen, m, k)
+    h, pre = torch.empty((m, n), dtype=x.dtype, device="cuda"), torch.empty((m, 2 * n), dtype=x.dtype, device="cuda")
+    q, s = gt.quantize_e4m3(h.zero_())
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+
+    def step():
+        gt.mm_tn_gated(x, w, out=h, pre=pre, status=status)
+        gt.quantize_e4m3(h, out=q, scale=s)
+        d = gt.gated_grad(gt.mm_nn(dy, wd), pre)
+        return [gt.mm_nn(d, w), gt.mm_nt(d, x, out_dtype=torch.float32, status=status), q.view(torch.uint8).clone()]
+
+    want = step()
+    torch.cuda.synchronize()
+    for _ in range(150):
+        got = step()
+    torch.cuda.synchronize()
+    assert int(status.item()) == 0
+    assert all(torch.equal(a, b) for a, b in zip(got, want))
